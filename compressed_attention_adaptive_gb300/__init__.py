@@ -6,7 +6,9 @@ entry points carry the names of the C ABI in ``include/mita.h``:
 ``mita_workspace_size``, ``mita_landmarks``, ``mita_select``,
 ``mita_forward``, ``mita_host_buffer_size``, ``mita_forward_host``,
 ``mita_forward_static``, ``mita_backward_workspace_size``, ``mita_backward``,
-``mita_device_status``, ``mita_uses_tensor_cores``.
+``mita_device_status``, ``mita_uses_tensor_cores``, and for the 4-bit
+key/value cache ``mita_cache_size``, ``mita_cache_workspace_size``,
+``mita_cache_write``, ``mita_cache_read``, ``mita_cache_attention``.
 
 The library must be built first (``python -c "import __graft_entry__ as g;
 g.build()"``); calling an entry point without it raises ``RuntimeError``.
@@ -65,6 +67,32 @@ class Params:
                         self.lm_h, self.lm_w, float(self.scale), int(self.flags), int(self.dtype))
 
 
+class _CCacheParams(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("H_kv", ctypes.c_int), ("T", ctypes.c_int),
+                ("d", ctypes.c_int), ("page", ctypes.c_int), ("n_pages", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("scale", ctypes.c_float), ("flags", ctypes.c_uint), ("dtype", ctypes.c_int)]
+
+
+@dataclasses.dataclass
+class CacheParams:
+    """Mirror of ``mita_cache_params`` (see include/mita.h)."""
+    B: int
+    H: int
+    H_kv: int
+    T: int
+    d: int
+    page: int
+    n_pages: int
+    max_pages: int
+    scale: float = 0.0
+    flags: int = 0
+    dtype: int = BF16
+
+    def c(self):
+        return _CCacheParams(self.B, self.H, self.H_kv, self.T, self.d, self.page, self.n_pages, self.max_pages,
+                             float(self.scale), int(self.flags), int(self.dtype))
+
+
 def lib():
     """The loaded libmita.so; raises if it has not been built."""
     global _lib
@@ -94,6 +122,15 @@ def lib():
         L.mita_backward.restype = ctypes.c_int
         L.mita_forward_static.argtypes = [P, vp, vp, vp, vp, ip, vp]
         L.mita_forward_static.restype = ctypes.c_int
+        C = ctypes.POINTER(_CCacheParams)
+        for f in ("mita_cache_size", "mita_cache_workspace_size"):
+            getattr(L, f).argtypes = [C]
+            getattr(L, f).restype = sz
+        L.mita_cache_write.argtypes = [C, vp, vp, vp, ip, ip, ip, ip, vp, sz, vp]
+        L.mita_cache_read.argtypes = [C, vp, ip, ip, ip, ip, vp, vp, vp, sz, vp]
+        L.mita_cache_attention.argtypes = [C, vp, vp, ip, ip, ip, ip, vp, fp, vp, sz, vp]
+        for f in ("mita_cache_write", "mita_cache_read", "mita_cache_attention"):
+            getattr(L, f).restype = ctypes.c_int
         L.mita_launch_count.argtypes = []
         L.mita_launch_count.restype = ctypes.c_longlong
         L.mita_profile_begin.argtypes = [ctypes.c_int]
@@ -255,3 +292,72 @@ def forward(Q, K, V, m, k, s, grid=None, lm=None, scale=0.0, flags=0, return_set
     Vt = torch.empty((B, H, m, d), dtype=torch.float32, device=Q.device)
     mita_forward(p, Q, K, V, O, ws, idx, route, Vt)
     return O, idx, route, Vt
+
+
+def mita_cache_size(p: CacheParams) -> int:
+    return int(lib().mita_cache_size(ctypes.byref(p.c())))
+
+
+def mita_cache_workspace_size(p: CacheParams) -> int:
+    return int(lib().mita_cache_workspace_size(ctypes.byref(p.c())))
+
+
+def cache_workspace(p: CacheParams, device="cuda"):
+    """A device workspace for the cache calls with ``p`` (torch uint8 tensor)."""
+    import torch
+    n = mita_cache_workspace_size(p)
+    if n == 0:
+        raise MitaError(1, lib().mita_last_error().decode() or "invalid parameters")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _check_cache(p: CacheParams, rows, cache, table, lens, counts, exps, ws, lse=None):
+    """The tensors of a cache call against ``p``: the C ABI sees only pointers."""
+    import torch
+    dt = {F32: torch.float32, BF16: torch.bfloat16}.get(p.dtype)
+    wanted = [(n, t, s, dt) for n, t, s in rows]
+    wanted += [("table", table, (p.B, p.max_pages), torch.int32), ("lens", lens, (p.B,), torch.int32)]
+    wanted += [(n, t, s, x) for n, t, s, x in (("counts", counts, (p.B,), torch.int32),
+                                               ("exps", exps, (2, p.H_kv), torch.int32),
+                                               ("lse_out", lse, (p.B, p.H, p.T), torch.float32)) if t is not None]
+    for name, t, shape, dtype in wanted:
+        if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
+            raise ValueError("%s must be a contiguous %s tensor of shape %s" % (name, dtype, shape))
+    for name, t in (("cache", cache), ("ws", ws)):
+        if t.dtype != torch.uint8 or not t.is_contiguous():
+            raise ValueError("%s must be a contiguous uint8 tensor" % name)
+    if cache.numel() < mita_cache_size(p):
+        raise ValueError("cache holds %d bytes, the pool needs %d" % (cache.numel(), mita_cache_size(p)))
+    for name, t in [(n, t) for n, t, _, _ in wanted] + [("cache", cache), ("ws", ws)]:
+        if not t.is_cuda or t.device != cache.device:
+            raise ValueError("%s must be on the cache's CUDA device" % name)
+    return cache.device
+
+
+def mita_cache_write(p: CacheParams, K, V, cache, table, lens, ws, counts=None, exps=None, stream=None):
+    """Stores the rows K, V [B, H_kv, T, d] in the pages that ``table`` names."""
+    import torch
+    s = (p.B, p.H_kv, p.T, p.d)
+    with torch.cuda.device(_check_cache(p, (("K", K, s), ("V", V, s)), cache, table, lens, counts, exps, ws)):
+        _check(lib().mita_cache_write(ctypes.byref(p.c()), _ptr(K), _ptr(V), _ptr(cache), _ptr(table), _ptr(lens),
+                                      _ptr(counts), _ptr(exps), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def mita_cache_read(p: CacheParams, cache, table, lens, K, V, ws, counts=None, exps=None, stream=None):
+    """Reads rows back into K, V [B, H_kv, T, d]; padding rows stay as they are."""
+    import torch
+    s = (p.B, p.H_kv, p.T, p.d)
+    with torch.cuda.device(_check_cache(p, (("K", K, s), ("V", V, s)), cache, table, lens, counts, exps, ws)):
+        _check(lib().mita_cache_read(ctypes.byref(p.c()), _ptr(cache), _ptr(table), _ptr(lens), _ptr(counts),
+                                     _ptr(exps), _ptr(K), _ptr(V), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def mita_cache_attention(p: CacheParams, Q, cache, table, lens, O, ws, counts=None, exps=None, lse_out=None,
+                         stream=None):
+    """Attention of the rows Q [B, H, T, d] over the cache, into O (and lse_out)."""
+    import torch
+    s = (p.B, p.H, p.T, p.d)
+    with torch.cuda.device(_check_cache(p, (("Q", Q, s), ("O", O, s)), cache, table, lens, counts, exps, ws, lse_out)):
+        _check(lib().mita_cache_attention(ctypes.byref(p.c()), _ptr(Q), _ptr(cache), _ptr(table), _ptr(lens),
+                                          _ptr(counts), _ptr(exps), _ptr(O), _ptr(lse_out), _ptr(ws), ws.numel(),
+                                          _stream(stream)))

@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "../../include/mita.h"
+#include "cache.cuh"
 #include "internal.h"
 
 namespace mita {
@@ -294,6 +295,75 @@ static BwdWork carve_bwd(const Dims& D, void* ws, size_t* bytes, int** status) {
     return w;
 }
 
+// ------------------------------------------------------------- 4-bit cache
+
+static mita_status resolve_cache(const mita_cache_params* p, CacheArgs* a) {
+    if (!p) return fail(MITA_ERR_INVALID_ARG, "params is NULL");
+    if (p->B < 1 || p->H < 1 || p->H_kv < 1 || p->T < 1) return fail(MITA_ERR_INVALID_ARG, "B, H, H_kv, T must be >= 1");
+    if (p->H % p->H_kv) return fail(MITA_ERR_INVALID_ARG, "H must be a multiple of H_kv");
+    if (p->d < 8 || p->d > 256 || p->d % 8) return fail(MITA_ERR_INVALID_ARG, "d must be a multiple of 8 in [8, 256]");
+    if (p->d != 64 && p->d != 128) return fail(MITA_ERR_UNSUPPORTED, "the cache supports d = 64 or 128");
+    if (p->page < kGroup || p->page > 4096 || p->page % kGroup)
+        return fail(MITA_ERR_INVALID_ARG, "page must be a multiple of %d in [%d, 4096]", kGroup, kGroup);
+    if (p->n_pages < 1 || p->max_pages < 1) return fail(MITA_ERR_INVALID_ARG, "n_pages, max_pages must be >= 1");
+    if (p->dtype != MITA_DTYPE_F32 && p->dtype != MITA_DTYPE_BF16) return fail(MITA_ERR_INVALID_ARG, "bad dtype");
+    if (p->flags & ~(unsigned)(MITA_FLAG_SIMT | MITA_FLAG_CAUSAL)) return fail(MITA_ERR_INVALID_ARG, "unknown flag");
+    if (!(p->scale >= 0.0f) || isinf(p->scale)) return fail(MITA_ERR_INVALID_ARG, "scale must be finite and >= 0");
+    if (p->B > 65535) return fail(MITA_ERR_UNSUPPORTED, "B must be <= 65535");
+    if ((long long)p->B * p->H >= (1LL << 31) || (long long)p->B * p->H * p->T >= (1LL << 31))
+        return fail(MITA_ERR_UNSUPPORTED, "B*H*T must be < 2^31");
+    if ((long long)p->max_pages * p->page > (1LL << 30))
+        return fail(MITA_ERR_UNSUPPORTED, "max_pages*page must be <= 2^30 tokens");
+    if ((double)p->n_pages * p->H_kv * (p->page / kGroup) >= 2147483648.0)
+        return fail(MITA_ERR_UNSUPPORTED, "n_pages*H_kv*page/%d must be < 2^31", kGroup);
+    *a = CacheArgs{};
+    a->B = p->B; a->H = p->H; a->Hkv = p->H_kv; a->T = p->T; a->G = p->H / p->H_kv;
+    a->page = p->page; a->pgroups = p->page / kGroup;
+    a->n_pages = p->n_pages; a->cols = p->max_pages;
+    a->causal = (p->flags & MITA_FLAG_CAUSAL) != 0;
+    a->scale = p->scale > 0.0f ? p->scale : 1.0f / sqrtf((float)p->d);
+    return MITA_OK;
+}
+
+// Workspace of the cache calls: the status word, then the attention's partial results.
+struct CacheWork {
+    int* status;
+    float* part;
+    float2* ml;
+};
+static CacheWork carve_cache(const mita_cache_params* p, const CachePlan& plan, void* ws, size_t* bytes) {
+    Carver c(ws);
+    CacheWork w{};
+    w.status = c.take<int>(64);
+    w.part = c.take<float>(plan.parts * p->d);
+    w.ml = c.take<float2>(plan.parts);
+    *bytes = align_up(c.off, 1024);
+    return w;
+}
+
+// Common part of the three calls; rows: the tensors in `dtype`.
+static mita_status cache_begin(const mita_cache_params* p, CacheArgs* a, CachePlan* plan, CacheWork* w,
+                               const void* r0, const void* r1, const void* cache, const int32_t* table,
+                               const int32_t* len, const int32_t* count, const int32_t* exps, void* ws,
+                               size_t ws_bytes) {
+    mita_status st = resolve_cache(p, a);
+    if (st) return st;
+    if (!r0 || !aligned16(r0) || !r1 || !aligned16(r1) || !cache || !aligned16(cache))
+        return fail(MITA_ERR_INVALID_ARG, "rows and cache must be 16-byte aligned device pointers");
+    if (!table || !len || ((uintptr_t)table | (uintptr_t)len | (uintptr_t)count | (uintptr_t)exps) % 4)
+        return fail(MITA_ERR_INVALID_ARG, "table and len must be device pointers, and all index arrays 4-byte aligned");
+    *plan = cache_attn_plan(*a, p->d, p->dtype, p->flags);
+    size_t need;
+    carve_cache(p, *plan, nullptr, &need);
+    if (!ws) return fail(MITA_ERR_WORKSPACE, "workspace is NULL");
+    if ((uintptr_t)ws % 256) return fail(MITA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    if (ws_bytes < need) return fail(MITA_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+    *w = carve_cache(p, *plan, ws, &need);
+    a->table = table; a->len = len; a->count = count; a->exps = exps;
+    a->status = w->status;
+    return MITA_OK;
+}
+
 }  // namespace mita
 
 using namespace mita;
@@ -548,6 +618,64 @@ int mita_uses_tensor_cores(const mita_params* p) {
     Dims D;
     if (resolve(p, &D)) return -1;
     return use_tc(D) ? 1 : 0;
+}
+
+size_t mita_cache_size(const mita_cache_params* p) {
+    CacheArgs a;
+    if (resolve_cache(p, &a)) return 0;
+    return (size_t)p->n_pages * p->H_kv * a.pgroups * (18 * (size_t)p->d);
+}
+
+size_t mita_cache_workspace_size(const mita_cache_params* p) {
+    CacheArgs a;
+    if (resolve_cache(p, &a)) return 0;
+    size_t bytes;
+    carve_cache(p, cache_attn_plan(a, p->d, p->dtype, p->flags), nullptr, &bytes);
+    return bytes;
+}
+
+mita_status mita_cache_write(const mita_cache_params* p, const void* K, const void* V, void* cache,
+                             const int32_t* table, const int32_t* len, const int32_t* count, const int32_t* exps,
+                             void* ws, size_t ws_bytes, void* stream) {
+    g_last_error.clear();
+    CacheArgs a;
+    CachePlan plan;
+    CacheWork w;
+    const mita_status st = cache_begin(p, &a, &plan, &w, K, V, cache, table, len, count, exps, ws, ws_bytes);
+    if (st) return st;
+    MITA_CUDA(launch_cache_rows(a, p->d, p->dtype, true, (void*)K, (void*)V, cache, (cudaStream_t)stream), "cache write");
+    prof_mark((cudaStream_t)stream, "");
+    return MITA_OK;
+}
+
+mita_status mita_cache_read(const mita_cache_params* p, const void* cache, const int32_t* table, const int32_t* len,
+                            const int32_t* count, const int32_t* exps, void* K, void* V, void* ws, size_t ws_bytes,
+                            void* stream) {
+    g_last_error.clear();
+    CacheArgs a;
+    CachePlan plan;
+    CacheWork w;
+    const mita_status st = cache_begin(p, &a, &plan, &w, K, V, cache, table, len, count, exps, ws, ws_bytes);
+    if (st) return st;
+    MITA_CUDA(launch_cache_rows(a, p->d, p->dtype, false, K, V, (void*)cache, (cudaStream_t)stream), "cache read");
+    prof_mark((cudaStream_t)stream, "");
+    return MITA_OK;
+}
+
+mita_status mita_cache_attention(const mita_cache_params* p, const void* Q, const void* cache, const int32_t* table,
+                                 const int32_t* len, const int32_t* count, const int32_t* exps, void* O,
+                                 float* lse_out, void* ws, size_t ws_bytes, void* stream) {
+    g_last_error.clear();
+    CacheArgs a;
+    CachePlan plan;
+    CacheWork w;
+    const mita_status st = cache_begin(p, &a, &plan, &w, Q, O, cache, table, len, count, exps, ws, ws_bytes);
+    if (st) return st;
+    if ((uintptr_t)lse_out % 4) return fail(MITA_ERR_INVALID_ARG, "lse_out must be 4-byte aligned");
+    MITA_CUDA(launch_cache_attn(a, plan, p->d, p->dtype, Q, cache, O, lse_out, w.part, w.ml, (cudaStream_t)stream),
+              "cache attention");
+    prof_mark((cudaStream_t)stream, "");
+    return MITA_OK;
 }
 
 }  // extern "C"

@@ -217,6 +217,88 @@ int mita_uses_tensor_cores(const mita_params* p);
 mita_status mita_forward_static(const mita_params* p, const void* Q, const void* K, const void* V, void* O,
                                 int32_t* status_out, void* stream);
 
+/* ---- 4-bit key/value cache --------------------------------------------------
+ * Not part of the method (the summaries have no counterpart): what a caller
+ * needs to generate with a model whose prompts went through mita_forward(). The
+ * keys and values of a sequence are kept in 4 bits in pages of one pool;
+ * mita_cache_write() stores rows, mita_cache_read() returns them (as contiguous
+ * K and V, for another mita_forward()), and mita_cache_attention() is dense
+ * softmax attention of a call's new rows over everything cached.
+ *
+ * Format. Each row of d channels is cut into blocks of 16. With e the exponent
+ * of the row's head and y = x * 2^-e:
+ *   s    = max |y| / 6, rounded to e4m3 (ties to even, at most 448);
+ *   code = y / s, rounded to e2m1: 0, 1/2, 1, 3/2, 2, 3, 4 or 6 with a sign
+ *          (ties to the even code, beyond 6 to 6);
+ *   the value read back is code * s * 2^e, exact in bf16 and float32.
+ * Both roundings are of the exact quotients. A block with s = 0 reads as zeros,
+ * one that holds a NaN reads as 16 NaN, an infinity as 6 * 448 * 2^e with its
+ * sign. 9/16 of a byte per channel in all. The exponent moves the
+ * range that scales cover (2^-9 .. 448, and their precision falls below 2^-6);
+ * it costs no accuracy, and 0 suits rows whose largest channels are between
+ * about 1/10 and 2688.
+ *
+ * Pages. `cache` is mita_cache_size() bytes, 16-byte aligned: n_pages pages of
+ * `page` tokens for all H_kv heads. Their inner order is the library's own.
+ * `table` int32 [B][max_pages] names the pages of each sequence in order;
+ * position i is place i % page of page table[b][i / page]. Sequences may share
+ * pages that they only read.
+ *
+ * Rows. len int32 [B] is the number of tokens that sequence b has, the call's
+ * own rows included; its rows are the last count[b] of them (count int32 [B], or
+ * NULL: T each): row t is position len[b] - count[b] + t. Rows t >= count[b] are
+ * padding: not read, and left as they were in outputs. exps int32 [2][H_kv]
+ * (first the keys' exponents, then the values'; |e| <= 60), or NULL: all zero.
+ * All four arrays are device memory and are read when the stream gets there, so
+ * a captured call follows them. The same arrays serve all three calls: write a
+ * step's rows, then attend.
+ *
+ * Out of range (a page outside [0, n_pages) among those that the call uses, a
+ * length outside [0, max_pages * page], a count outside [0, T], for write and
+ * read also count > len, an exponent outside +-60): the status word of `ws`
+ * becomes MITA_ERR_BOUNDS, the places concerned are neither read nor written,
+ * and what is computed from them is undefined. Every call writes the word. */
+typedef struct {
+    int B, H, H_kv;  /* sequences, query heads, cache heads (H % H_kv == 0)     */
+    int T, d;        /* rows per sequence and call; head dim: 64 or 128         */
+    int page;        /* tokens per page: a multiple of 16, 16 .. 4096           */
+    int n_pages;     /* pages in the pool                                       */
+    int max_pages;   /* columns of the page table                               */
+    float scale;     /* softmax scale; 0 means 1/sqrt(d)                        */
+    unsigned flags;  /* mita_cache_attention: MITA_FLAG_CAUSAL, MITA_FLAG_SIMT  */
+    int dtype;       /* mita_dtype of K, V, Q and O                             */
+} mita_cache_params;
+
+/* Bytes of the pool, and of device workspace that each of the three calls
+ * needs; 0 if `p` is invalid. The workspace does not depend on the lengths. */
+size_t mita_cache_size(const mita_cache_params* p);
+size_t mita_cache_workspace_size(const mita_cache_params* p);
+
+/* Stores rows K, V: [B, H_kv, T, d] in `dtype`. No place may be written twice
+ * in one call. */
+mita_status mita_cache_write(const mita_cache_params* p, const void* K, const void* V, void* cache,
+                             const int32_t* table, const int32_t* len, const int32_t* count, const int32_t* exps,
+                             void* ws, size_t ws_bytes, void* stream);
+
+/* Reads rows back into K, V: [B, H_kv, T, d] in `dtype`. With T the longest
+ * sequence and count = len it returns whole sequences. */
+mita_status mita_cache_read(const mita_cache_params* p, const void* cache, const int32_t* table, const int32_t* len,
+                            const int32_t* count, const int32_t* exps, void* K, void* V, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/* Attention of rows Q [B, H, T, d] over the cache; query head i uses cache head
+ * i / (H / H_kv). Row t sees the keys j < len[b], with MITA_FLAG_CAUSAL those up
+ * to its own position (j < len[b] - (count[b] - 1 - t)); a row that sees no key
+ * gets zeros. A key that a row does not see has no influence on it, whatever its
+ * bytes are. O: [B, H, T, d] in `dtype`. lse_out (float32 [B, H, T], or NULL):
+ * ln sum exp(scale q.k) over the seen keys, -infinity without any, with which the
+ * rows can be joined with attention over other keys (mita_forward's shared
+ * slots, say). count > len is allowed: rows before the first token see none.
+ * bf16 runs on tensor cores, float32 and MITA_FLAG_SIMT on CUDA cores in fp32. */
+mita_status mita_cache_attention(const mita_cache_params* p, const void* Q, const void* cache, const int32_t* table,
+                                 const int32_t* len, const int32_t* count, const int32_t* exps, void* O,
+                                 float* lse_out, void* ws, size_t ws_bytes, void* stream);
+
 /* ---- measurement hooks (not part of the method) ---------------------------
  * Number of kernels this library has launched in the process so far. */
 long long mita_launch_count(void);
@@ -225,7 +307,8 @@ long long mita_launch_count(void);
  * event on its stream at the start of each phase (landmark pooling, top-k
  * sample and threshold, landmark pass, top-k selection, shared-expert combine,
  * routing, bucketing, the shared slots' own pass when there are more than 128
- * landmarks, expert attention, merge) and at its end; up to max_marks events
+ * landmarks, expert attention, merge; the cache calls: write, read, attention,
+ * join) and at its end; up to max_marks events
  * in total (created here, kept for reuse). Process-wide; not for concurrent
  * calls. */
 mita_status mita_profile_begin(int max_marks);

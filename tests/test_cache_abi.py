@@ -1,0 +1,101 @@
+"""The cache calls' argument checks (no GPU: nothing here launches)."""
+import ctypes
+
+import pytest
+import torch
+
+import compressed_attention_adaptive_gb300 as mita
+from compressed_attention_adaptive_gb300 import build as mita_build
+
+
+@pytest.fixture(scope="module")
+def lib():
+    mita_build.build()
+    return mita.lib()
+
+
+def _p(**kw):
+    base = dict(B=2, H=8, H_kv=2, T=1, d=128, page=64, n_pages=10, max_pages=4)
+    base.update(kw)
+    return mita.CacheParams(**base)
+
+
+def test_sizes(lib):
+    assert mita.mita_cache_size(_p()) == 10 * 2 * 64 * (2 * (64 + 8))  # 9/16 byte per channel, keys and values
+    assert mita.mita_cache_size(_p(d=64, page=16)) == 10 * 2 * 16 * (2 * (32 + 4))
+    big = _p(n_pages=200000, H_kv=8)  # past 32 bits
+    assert mita.mita_cache_size(big) == 200000 * 8 * 64 * 144
+    assert mita.mita_cache_workspace_size(_p()) >= 1024
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(B=0), 1), (dict(H=0), 1), (dict(H_kv=0), 1), (dict(T=0), 1), (dict(H=7), 1), (dict(d=100), 1),
+    (dict(d=96), 2), (dict(d=256), 2), (dict(page=8), 1), (dict(page=40), 1), (dict(page=8192), 1),
+    (dict(n_pages=0), 1), (dict(max_pages=0), 1), (dict(dtype=5), 1), (dict(flags=1), 1), (dict(flags=8), 1),
+    (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(B=65536), 2),
+    (dict(T=1 << 29), 2), (dict(H=2 ** 31 - 2, H_kv=2), 2), (dict(max_pages=1 << 25), 2), (dict(n_pages=1 << 29), 2),
+])
+def test_invalid_parameters(lib, bad, status):
+    p = _p(**bad)
+    assert mita.mita_cache_size(p) == 0 and mita.mita_cache_workspace_size(p) == 0
+    f, c = ctypes.c_void_p(1 << 20), ctypes.byref(p.c())
+    big = 1 << 60
+    assert lib.mita_cache_write(c, f, f, f, f, f, None, None, f, big, None) == status
+    assert lib.mita_cache_read(c, f, f, f, None, None, f, f, f, big, None) == status
+    assert lib.mita_cache_attention(c, f, f, f, f, None, None, f, None, f, big, None) == status
+    assert lib.mita_last_error()
+
+
+def test_null_params(lib):
+    f = ctypes.c_void_p(1 << 20)
+    assert lib.mita_cache_size(None) == 0
+    assert lib.mita_cache_write(None, f, f, f, f, f, None, None, f, 1 << 60, None) == 1
+
+
+def test_pointers_and_workspace(lib):
+    p = _p()
+    c, need = ctypes.byref(p.c()), mita.mita_cache_workspace_size(p)
+    f, odd, no = ctypes.c_void_p(1 << 20), ctypes.c_void_p((1 << 20) + 8), ctypes.c_void_p((1 << 20) + 2)
+
+    def write(K=f, V=f, cache=f, table=f, lens=f, counts=None, exps=None, ws=f, n=need):
+        return lib.mita_cache_write(c, K, V, cache, table, lens, counts, exps, ws, n, None)
+
+    def attend(Q=f, cache=f, table=f, lens=f, O=f, lse=None, ws=f, n=need):
+        return lib.mita_cache_attention(c, Q, cache, table, lens, None, None, O, lse, ws, n, None)
+
+    for kw in (dict(K=None), dict(V=None), dict(cache=None), dict(table=None), dict(lens=None), dict(K=odd),
+               dict(cache=odd), dict(table=no), dict(lens=no), dict(counts=no), dict(exps=no)):
+        assert write(**kw) == 1, kw
+    for kw in (dict(Q=None), dict(O=None), dict(Q=odd), dict(O=odd), dict(lse=no)):
+        assert attend(**kw) == 1, kw
+    for fn in (write, attend):
+        assert fn(ws=None) == 3
+        assert fn(ws=odd) == 3
+        assert fn(n=need - 1) == 3
+
+
+def test_binding_checks_tensors(lib):
+    """The C side sees pointers only, so the binding checks shapes, types and devices."""
+    p = _p()
+    K = torch.zeros((2, 2, 1, 128), dtype=torch.bfloat16)
+    cache = torch.zeros(mita.mita_cache_size(p), dtype=torch.uint8)
+    table, lens = torch.zeros((2, 4), dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    ws = torch.zeros(mita.mita_cache_workspace_size(p), dtype=torch.uint8)
+    ok = dict(K=K, V=K, cache=cache, table=table, lens=lens, ws=ws)
+    for bad in (dict(K=K.float()), dict(V=K[:1]), dict(K=K.transpose(1, 2)[:, :, :1]), dict(table=table[:, :3]),
+                dict(table=table.long()), dict(lens=lens[:1]), dict(counts=lens.long()), dict(exps=table),
+                dict(cache=cache[:-1]), dict(cache=cache.view(torch.int8)), dict(ws=ws.view(torch.int8)),
+                dict(table=table.t().contiguous().t())):
+        with pytest.raises(ValueError):
+            mita.mita_cache_write(p, **{**ok, **bad})
+    with pytest.raises(ValueError, match="device"):  # host tensors of the right shapes
+        mita.mita_cache_write(p, **ok)
+    with pytest.raises(ValueError, match="device"):
+        mita.mita_cache_read(p, cache, table, lens, K, K, ws)
+    q = torch.zeros((2, 8, 1, 128), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="device"):
+        mita.mita_cache_attention(p, q, cache, table, lens, q, ws)
+    with pytest.raises(ValueError, match="lse_out"):
+        mita.mita_cache_attention(p, q, cache, table, lens, q, ws, lse_out=torch.zeros(2, 8, 1, 1))
+    with pytest.raises(mita.MitaError):
+        mita.cache_workspace(_p(d=96))

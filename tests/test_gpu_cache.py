@@ -1,0 +1,434 @@
+"""The 4-bit cache on the GPU against its fp64 oracle (oracle/cache.py).
+
+What is stored is compared for equality (the format's two roundings are of exact
+quotients); attention within bounds counted from its roundings
+(tests/cache_cases.py), the oracle attending over the values it says the cache
+holds.
+"""
+import math
+
+import numpy as np
+import pytest
+
+from oracle import cache as ocache
+from tests import parity
+from tests.cache_cases import Pool, attention_bound
+
+pytestmark = pytest.mark.gpu
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+# ------------------------------------------------------------ write and read
+
+
+@pytest.mark.parametrize("dtype,d,page,lens,counts,T,exps", [
+    ("bf16", 128, 16, [1], None, 1, False),
+    ("bf16", 128, 64, [5, 64, 65, 200], [5, 1, 2, 0], 7, True),
+    ("bf16", 64, 48, [31, 95, 1, 17], [31, 40, 1, 16], 40, False),
+    ("f32", 64, 16, [33, 16, 15], [33, 16, 0], 33, True),
+    ("f32", 128, 4096, [700, 3], [1, 3], 3, False),
+    ("bf16", 128, 112, [1000, 999], None, 999, True),
+])
+def test_rows_come_back_as_the_format_says(dtype, d, page, lens, counts, T, exps):
+    import torch
+    import compressed_attention_adaptive_gb300 as mita
+    Hkv = 3
+    rng = np.random.default_rng(T)
+    ex = rng.integers(-9, 10, (2, Hkv)).astype(np.int32) if exps else None
+    # every row written, some by the fill and the last ones again with other values
+    pool = Pool(lens, Hkv, d, page, dtype, seed=T, exps=ex, T=T)
+    cnt = counts or [T] * len(lens)
+    new = [rng.standard_normal((len(lens), Hkv, T, d)) * np.exp(rng.uniform(-3, 3, (len(lens), Hkv, T, 1)))
+           for _ in range(2)]
+    K, V = (torch.from_numpy(x).to(pool.td).cuda() for x in new)
+    cnt_t = None if counts is None else torch.tensor(counts, dtype=torch.int32).cuda()
+    mita.mita_cache_write(pool.p, K, V, pool.cache, pool.table, pool.len_t, pool.ws, counts=cnt_t, exps=pool.exps)
+    mita.mita_device_status(pool.ws)
+    longest = max(lens)
+    outs = [torch.full((len(lens), Hkv, longest, d), 7.0, dtype=pool.td, device="cuda") for _ in range(2)]
+    mita.mita_cache_read(pool.fill_p, pool.cache, pool.table, pool.len_t, outs[0], outs[1], pool.fill_ws,
+                         counts=pool.len_t, exps=pool.exps)
+    mita.mita_device_status(pool.fill_ws)
+    for which, (X, out) in enumerate(zip((K, V), outs)):
+        for b, n in enumerate(lens):
+            want = pool.held(b, which)
+            c = cnt[b]
+            if c:
+                e = 0 if ex is None else ex[which][:, None]
+                want[:, n - c:] = ocache.quantise(_np(X[b, :, :c]), e)
+            np.testing.assert_array_equal(_np(out[b, :, :n]), want)
+            assert torch.all(out[b, :, n:] == 7.0)  # padding rows left alone
+
+
+def test_special_rows():
+    import torch
+    import compressed_attention_adaptive_gb300 as mita
+
+    def make(rng, shape):
+        x = rng.standard_normal(shape)
+        x[0, 0, 0] = 0.0
+        x[0, 0, 1] = -0.0
+        x[0, 0, 2, 5] = np.nan
+        x[0, 0, 3, 40] = np.inf
+        x[0, 0, 4, 41] = -np.inf
+        x[0, 0, 5] *= 1e30
+        x[0, 0, 6] *= 1e-30
+        x[0, 0, 7] *= 2.0 ** -12  # scales below e4m3's normal range
+        x[0, 0, 8, :16] = np.r_[6.0, np.repeat([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], 2), 6.0]  # ties, scale 1
+        x[0, 0, 9, :16] = 2 * x[0, 0, 8, :16] * (-1.0) ** np.arange(16)
+        x[0, 0, 10] = rng.integers(-40, 41, shape[-1])
+        x[0, 0, 11, 2], x[0, 0, 11, 3] = np.nan, np.inf
+        x[0, 0, 12] = 3.0e38
+        return x, x[:, :, ::-1].copy()
+
+    for dtype in ("bf16", "f32"):
+        for ex in (None, [[0, 3], [-20, 1]]):
+            pool = Pool([40], 2, 128, 16, dtype, make=make, exps=ex)
+            K, V = (torch.empty_like(pool.K) for _ in range(2))
+            mita.mita_cache_read(pool.fill_p, pool.cache, pool.table, pool.len_t, K, V, pool.fill_ws,
+                                 counts=pool.len_t, exps=pool.exps)
+            for which, out in enumerate((K, V)):
+                np.testing.assert_array_equal(_np(out[0]), pool.held(0, which))
+
+
+def test_write_touches_only_its_places():
+    """Storing a row changes that token's bytes and no others: every other token
+    of the pool, of shared groups and of other pages too, reads as before."""
+    import torch
+    import compressed_attention_adaptive_gb300 as mita
+    pool = Pool([90, 70], 2, 64, 32, "bf16", T=1, seed=4)
+    before = pool.cache.clone()
+    K, V = (torch.randn((2, 2, 1, 64), device="cuda").to(torch.bfloat16) for _ in range(2))
+    counts = torch.tensor([1, 0], dtype=torch.int32).cuda()
+    mita.mita_cache_write(pool.p, K, V, pool.cache, pool.table, pool.len_t, pool.ws, counts=counts)
+    mita.mita_device_status(pool.ws)
+    changed = (pool.cache != before).view(-1)
+    assert 0 < int(changed.sum()) <= 2 * 2 * (32 + 4)
+    pages = torch.unique(changed.nonzero() // (changed.numel() // pool.n_pages))
+    assert pages.tolist() == [int(pool.table[0, 89 // 32])]
+
+
+# ---------------------------------------------------------------- attention
+
+
+def _attend(pool, H, T, causal, counts=None, simt=False, scale=0.0, seed=1, lse=True, q=None):
+    import torch
+    import compressed_attention_adaptive_gb300 as mita
+    B, d = len(pool.lens), pool.d
+    p = mita.CacheParams(B, H, pool.Hkv, T, d, pool.page, pool.n_pages, pool.cols, scale,
+                         (mita.FLAG_CAUSAL if causal else 0) | (mita.FLAG_SIMT if simt else 0), pool.p.dtype)
+    g = torch.Generator().manual_seed(seed)
+    Q = torch.randn((B, H, T, d), generator=g).to(pool.td).cuda() if q is None else q
+    O = torch.full_like(Q, 7.0)
+    L = torch.full((B, H, T), 7.0, dtype=torch.float32, device="cuda") if lse else None
+    ws = mita.cache_workspace(p)
+    ws.fill_(0xff)
+    cnt = None if counts is None else torch.tensor(counts, dtype=torch.int32).cuda()
+    mita.mita_cache_attention(p, Q, pool.cache, pool.table, pool.len_t, O, ws, counts=cnt, exps=pool.exps, lse_out=L)
+    mita.mita_device_status(ws)
+    return Q, O, L
+
+
+def _check(pool, H, T, causal, Q, O, L, counts=None, simt=False, scale=0.0, label=""):
+    G, worst = H // pool.Hkv, 0.0
+    sc = scale or 1.0 / math.sqrt(pool.d)
+    for b, n in enumerate(pool.lens):
+        c = T if counts is None else counts[b]
+        assert (O[b, :, c:] == 7.0).all() and (L[b, :, c:] == 7.0).all()  # padding rows left alone
+        if c == 0:
+            continue
+        K, V = pool.held(b, 0), pool.held(b, 1)
+        lim = [max(0, n - (c - 1 - t)) if causal else n for t in range(c)]
+        for h in range(H):
+            k, v, q = K[h // G], V[h // G], _np(Q[b, h, :c])
+            o, lse, spread = ocache.attention(q, k, v, lim, sc)
+            bound = attention_bound(pool.dtype, pool.dtype == "bf16" and not simt, o, spread, q, k, v, lim, sc)
+            diff = np.abs(_np(O[b, h, :c]) - o)
+            assert np.all(diff <= bound), (label, b, h, float((diff / bound).max()))
+            worst = max(worst, float((diff / bound).max()))
+            got = L[b, h, :c].double().cpu().numpy()
+            assert np.array_equal(got == -np.inf, lse == -np.inf)
+            some = lse > -np.inf
+            # the score's and the sum's relative errors become absolute ones
+            mag = sc * np.abs(q) @ np.abs(k).max(0) if n else np.zeros(c)
+            tol = (pool.d + 8) * 2.0 ** -23 * mag + (n / 16 + 64) * 2.0 ** -23 + 2.0 ** -20 + 2.0 ** -23 * np.abs(np.where(np.isinf(lse), 0, lse))
+            assert np.all(np.abs(got[some] - lse[some]) <= tol[some])
+    parity.REPORT.append(("cache attention " + label, worst, 0.0, O.numel()))
+
+
+CASES = [
+    # dtype, d, page, H, Hkv, T, causal, lens, counts, exps
+    ("bf16", 128, 16, 1, 1, 1, False, [1], None, False),
+    ("bf16", 128, 64, 4, 4, 1, True, [1, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 300], None, False),
+    ("bf16", 128, 64, 8, 2, 1, True, [5000, 0, 777], None, True),
+    ("bf16", 64, 48, 6, 2, 5, True, [40, 1000, 4, 129], [5, 3, 5, 0], False),
+    ("bf16", 128, 16, 16, 1, 1, False, [2049], None, False),
+    ("bf16", 128, 32, 16, 2, 3, True, [600, 2], [3, 2], True),       # 24 rows a head: more than one tile
+    ("bf16", 64, 64, 10, 1, 8, True, [900, 3, 64], None, False),     # 80 rows, rows without a key
+    ("bf16", 128, 128, 3, 3, 40, True, [40, 200], None, False),      # a chunk of a prompt, rows in several tiles
+    ("bf16", 64, 16, 5, 5, 2, False, [3000, 1, 257], [2, 2, 1], True),
+    ("f32", 128, 64, 2, 2, 1, False, [1, 127, 700], None, True),
+    ("f32", 64, 16, 6, 2, 3, True, [500, 2, 33], [3, 3, 1], False),
+    ("f32", 128, 32, 8, 1, 1, True, [4000, 0], None, False),
+]
+
+
+@pytest.mark.parametrize("simt", [False, True], ids=["", "simt"])
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "%s_d%d_p%d_H%d_%d_T%d" % c[:6])
+def test_attention_matches_oracle(case, simt):
+    dtype, d, page, H, Hkv, T, causal, lens, counts, exps = case
+    if simt and dtype == "f32":
+        pytest.skip("float32 runs on CUDA cores with and without the flag")
+    ex = np.random.default_rng(2).integers(-3, 4, (2, Hkv)) if exps else None
+    pool = Pool(lens, Hkv, d, page, dtype, seed=len(lens), exps=ex)
+    Q, O, L = _attend(pool, H, T, causal, counts, simt)
+    _check(pool, H, T, causal, Q, O, L, counts, simt, label="%s d%d H%d/%d T%d %s" % (dtype, d, H, Hkv, T, "simt" * simt))
+
+
+def test_scale_and_large_queries():
+    """Scores far apart (one key takes all the weight), an explicit scale, and
+    query rows of very unlike magnitude in one call."""
+    import torch
+    pool = Pool([333], 2, 128, 64, "bf16", seed=9)
+    Q = torch.randn((1, 4, 2, 128)).cuda() * torch.tensor([1e-30, 1e-3, 1.0, 40.0]).cuda().view(1, 4, 1, 1)
+    Q[0, 1, 0] = 0
+    Q = Q.to(torch.bfloat16)
+    _, O, L = _attend(pool, 4, 2, True, scale=0.5, q=Q)
+    _check(pool, 4, 2, True, Q, O, L, scale=0.5, label="scales")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_unseen_keys_have_no_influence(dtype):
+    """A later drafted token full of NaN, and whatever bytes lie behind the last
+    token: rows that do not see them are as without them, rows that do are NaN."""
+    import torch
+    T, H = 3, 4
+
+    def make(rng, shape):
+        K, V = Pool.rows(rng, shape)
+        K[0, :, 60], V[0, :, 60] = np.nan, np.nan     # the middle one of sequence 0's new tokens
+        V[1, 0, 39, 16:32] = np.nan                   # one block of one head of sequence 1's last token
+        K[2, 1, 5] = np.nan                           # a key that every row of sequence 2 sees
+        return K, V
+
+    pool = Pool([62, 40, 20], 2, 128, 16, dtype, make=make, seed=6)
+    Q, O, L = _attend(pool, H, T, True)
+    clean = Pool([62, 40, 20], 2, 128, 16, dtype, seed=6, fill=0)
+    Q2, O2, L2 = _attend(clean, H, T, True)
+    assert torch.equal(Q, Q2)
+    assert torch.equal(O[0, :, 0], O2[0, :, 0]) and torch.equal(L[0, :, 0], L2[0, :, 0])
+    assert O[0, :, 1:].isnan().all() and L[0, :, 1:].isnan().all()
+    assert torch.equal(O[1, :, :2], O2[1, :, :2]) and torch.equal(O[1, 2:, 2], O2[1, 2:, 2])
+    assert O[1, :2, 2, 16:32].isnan().all()
+    assert torch.equal(O[1, :2, 2, :16], O2[1, :2, 2, :16]) and torch.equal(O[1, :2, 2, 32:], O2[1, :2, 2, 32:])
+    assert O[2, 2:].isnan().all() and torch.equal(O[2, :2], O2[2, :2])
+
+
+def test_bad_rows_stay_in_their_rows():
+    """NaN and infinite queries make their own rows NaN and no others."""
+    import torch
+    pool = Pool([150], 1, 64, 16, "bf16", seed=3)
+    Q, O, L = _attend(pool, 8, 2, False)
+    bad = Q.clone()
+    bad[0, 2, 1, 5], bad[0, 7, 0, 60] = float("nan"), float("inf")
+    _, O2, _ = _attend(pool, 8, 2, False, q=bad)
+    hit = torch.zeros((8, 2), dtype=torch.bool)
+    hit[2, 1] = hit[7, 0] = True
+    assert O2[0][hit.cuda()].isnan().all()
+    assert torch.equal(O2[0][~hit.cuda()], O[0][~hit.cuda()])
+
+
+def test_repeated_calls_are_bit_equal_and_lse_is_optional():
+    import torch
+    pool = Pool([3000, 900], 2, 128, 64, "bf16", seed=12)
+    runs = [_attend(pool, 8, 2, True) for _ in range(3)]
+    for _, O, L in runs[1:]:
+        assert torch.equal(O, runs[0][1]) and torch.equal(L, runs[0][2])
+    assert torch.equal(_attend(pool, 8, 2, True, lse=False)[1], runs[0][1])
+
+
+# -------------------------------------------- out of range, and the status word
+
+
+@pytest.mark.parametrize("what", ["page", "negative page", "len", "negative len", "count", "exps"])
+def test_out_of_range_is_reported(what):
+    """Each call reports it, leaves the other sequence right, and the next call
+    on the same workspace is clean."""
+    import torch
+    import compressed_attention_adaptive_gb300 as mita
+    pool = Pool([100, 90], 2, 64, 32, "bf16", seed=8, T=2, H=4, exps=np.zeros((2, 2), int))
+    ref = _attend(pool, 4, 2, True)
+    table, lens = pool.table.clone(), pool.len_t.clone()
+    counts, exps = torch.tensor([2, 2], dtype=torch.int32).cuda(), pool.exps.clone()
+    if what == "page":
+        table[0, 3] = pool.n_pages
+    elif what == "negative page":
+        table[0, 3] = -1
+    elif what == "len":
+        lens[0] = pool.cols * 32 + 1
+    elif what == "negative len":
+        lens[0] = -5
+    elif what == "count":
+        counts[0] = 3
+    else:
+        exps[0, 0] = 61
+    K, V = (torch.randn((2, 2, 2, 64), device="cuda").to(torch.bfloat16) for _ in range(2))
+    cache = pool.cache.clone()
+    O = torch.zeros_like(ref[1])
+    p = mita.CacheParams(2, 4, 2, 2, 64, 32, pool.n_pages, pool.cols, 0.0, mita.FLAG_CAUSAL)
+    calls = [lambda t, n, c, e: mita.mita_cache_write(p, K, V, cache, t, n, pool.ws, counts=c, exps=e),
+             lambda t, n, c, e: mita.mita_cache_read(p, cache, t, n, K, V, pool.ws, counts=c, exps=e),
+             lambda t, n, c, e: mita.mita_cache_attention(p, ref[0], pool.cache, t, n, O, pool.ws, counts=c, exps=e)]
+    good = torch.tensor([2, 2], dtype=torch.int32).cuda()
+    for call in calls:
+        call(table, lens, counts, exps)
+        with pytest.raises(mita.MitaError) as err:
+            mita.mita_device_status(pool.ws)
+        assert err.value.status == 6
+    mine = slice(2, 4) if what == "exps" else slice(0, 4)  # an exponent belongs to a head, the rest to sequence 0
+    assert torch.equal(O[1, mine], ref[1][1, mine])
+    for call in calls:
+        call(pool.table, pool.len_t, good, pool.exps)
+        mita.mita_device_status(pool.ws)
+    assert torch.equal(O, ref[1])
+
+
+def test_more_rows_than_tokens():
+    """count > len: an error for the calls that store and read rows, rows without
+    keys for attention."""
+    import torch
+    import compressed_attention_adaptive_gb300 as mita
+    pool = Pool([2, 5], 1, 64, 16, "bf16", T=4)
+    K = torch.zeros((2, 1, 4, 64), dtype=torch.bfloat16, device="cuda")
+    before = pool.cache.view(pool.n_pages, -1).clone()
+    mita.mita_cache_write(pool.p, K, K, pool.cache, pool.table, pool.len_t, pool.ws,
+                          counts=torch.tensor([3, 0], dtype=torch.int32).cuda())
+    with pytest.raises(mita.MitaError):
+        mita.mita_device_status(pool.ws)
+    changed = (pool.cache.view(pool.n_pages, -1) != before).any(dim=1).nonzero().view(-1).tolist()
+    assert changed == [int(pool.table[0, 0])]  # the rows that have a place
+    pool = Pool([2, 5], 1, 64, 16, "bf16", T=4)
+    Q, O, L = _attend(pool, 1, 4, True)
+    _check(pool, 1, 4, True, Q, O, L, label="more rows than tokens")
+    assert torch.all(O[0, 0, :2] == 0) and torch.all(L[0, 0, :2] == -math.inf)
+
+
+# ------------------------------------------------------- streams and graphs
+
+
+def test_captured_calls_follow_lengths_and_tables():
+    """A captured step (write, then attend) replayed with other lengths, pages and
+    rows; two captured graphs with their own workspaces replayed at once."""
+    import torch
+    import compressed_attention_adaptive_gb300 as mita
+    pools = [Pool([224, 224], 2, 128, 32, "bf16", seed=s, T=1, H=4) for s in (1, 2)]
+    steps = []
+    for pool in pools:
+        st = dict(pool=pool, Q=torch.randn((2, 4, 1, 128)).cuda().to(torch.bfloat16),
+                  K=torch.randn((2, 2, 1, 128)).cuda().to(torch.bfloat16),
+                  V=torch.randn((2, 2, 1, 128)).cuda().to(torch.bfloat16))
+        st["O"] = torch.zeros_like(st["Q"])
+
+        def step(st=st, pool=pool):
+            mita.mita_cache_write(pool.p, st["K"], st["V"], pool.cache, pool.table, pool.len_t, pool.ws)
+            mita.mita_cache_attention(pool.p, st["Q"], pool.cache, pool.table, pool.len_t, st["O"], pool.ws)
+
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            step()
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        steps.append((st, step, graph, side))
+    torch.cuda.synchronize()
+    for lens in ([61, 201], [64, 17], [1, 224]):
+        for st, step, graph, side in steps:
+            st["pool"].len_t.copy_(torch.tensor(lens, dtype=torch.int32))
+            for x in ("Q", "K", "V"):
+                st[x].normal_()
+            st["pool"].table.copy_(st["pool"].table.flip(0))
+        torch.cuda.synchronize()
+        for st, step, graph, side in steps:
+            with torch.cuda.stream(side):
+                for _ in range(3):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for st, step, graph, side in steps:
+            got = st["O"].clone()
+            mita.mita_device_status(st["pool"].ws)
+            step()
+            mita.mita_device_status(st["pool"].ws)
+            assert got.isfinite().all() and torch.equal(got, st["O"])
+
+
+def test_another_stream():
+    import torch
+    import compressed_attention_adaptive_gb300 as mita
+    pool = Pool([500], 2, 64, 64, "bf16", H=2)
+    Q = torch.randn((1, 2, 1, 64)).cuda().to(torch.bfloat16)
+    a, b = torch.zeros_like(Q), torch.zeros_like(Q)
+    mita.mita_cache_attention(pool.p, Q, pool.cache, pool.table, pool.len_t, a, pool.ws)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    mita.mita_cache_attention(pool.p, Q, pool.cache, pool.table, pool.len_t, b, pool.ws, stream=s)
+    s.synchronize()
+    assert torch.equal(a, b)
+
+
+# --------------------------------------------------------- a run of them together
+
+
+def test_prompt_then_steps_then_another_pass():
+    """A prompt through mita_forward, its keys and values stored, steps of one and
+    of two tokens that store and attend, and at the end the whole sequences read
+    back for another forward pass."""
+    import torch
+    import compressed_attention_adaptive_gb300 as mita
+    B, H, Hkv, d, N, page, steps = 2, 4, 4, 128, 512, 64, [1, 1, 2, 1]
+    total = N + sum(steps)
+    g = torch.Generator().manual_seed(5)
+    allK, allV, allQ = (torch.randn((B, H, total, d), generator=g).to(torch.bfloat16).cuda() for _ in range(3))
+    cols = -(-total // page)
+    table = torch.randperm(B * cols, generator=g).to(torch.int32).view(B, cols).cuda()
+    mk = lambda T: mita.CacheParams(B, H, Hkv, T, d, page, B * cols, cols, flags=mita.FLAG_CAUSAL)
+    cache = torch.zeros(mita.mita_cache_size(mk(1)), dtype=torch.uint8, device="cuda")
+    ws = mita.cache_workspace(mk(N))
+    part = lambda x, lo, hi: x[:, :, lo:hi].contiguous()
+    O = mita.forward(part(allQ, 0, N), part(allK, 0, N), part(allV, 0, N), 16, 64, 2)
+    assert O.isfinite().all()
+    lens = torch.full((B,), N, dtype=torch.int32, device="cuda")
+    mita.mita_cache_write(mk(N), part(allK, 0, N), part(allV, 0, N), cache, table, lens, ws)
+    mita.mita_device_status(ws)
+    heldK, heldV = (ocache.quantise(_np(x)) for x in (allK, allV))
+    at = N
+    for T in steps:
+        p = mk(T)
+        lens += T
+        q, o = part(allQ, at, at + T), torch.zeros((B, H, T, d), dtype=torch.bfloat16, device="cuda")
+        w = mita.cache_workspace(p)
+        mita.mita_cache_write(p, part(allK, at, at + T), part(allV, at, at + T), cache, table, lens, w)
+        mita.mita_cache_attention(p, q, cache, table, lens, o, w)
+        mita.mita_device_status(w)
+        at += T
+        lim = [at - (T - 1 - t) for t in range(T)]
+        for b in range(B):
+            for h in range(H):
+                k, v, qq = heldK[b, h, :at], heldV[b, h, :at], _np(q[b, h])
+                ref, _, spread = ocache.attention(qq, k, v, lim, 1 / math.sqrt(d))
+                bound = attention_bound("bf16", True, ref, spread, qq, k, v, lim, 1 / math.sqrt(d))
+                assert np.all(np.abs(_np(o[b, h]) - ref) <= bound)
+    full = mk(total)
+    K, V = (torch.zeros((B, H, total, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    w = mita.cache_workspace(full)
+    mita.mita_cache_read(full, cache, table, lens, K, V, w)
+    mita.mita_device_status(w)
+    np.testing.assert_array_equal(_np(K), heldK)
+    np.testing.assert_array_equal(_np(V), heldV)
+    again = mita.forward(allQ, K, V, 16, 64, 2)
+    want = mita.forward(allQ, torch.from_numpy(heldK).to(torch.bfloat16).cuda(),
+                        torch.from_numpy(heldV).to(torch.bfloat16).cuda(), 16, 64, 2)
+    assert torch.equal(again, want)
