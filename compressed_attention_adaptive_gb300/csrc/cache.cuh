@@ -70,6 +70,7 @@ constexpr int kMaxExp = 60;
 // How the attention splits one call: rows of a tile, pieces of the line of
 // chunks, and the rows of partial results that the workspace holds.
 struct CachePlan {
+    bool tensor;  // tensor cores (bf16), else CUDA cores
     int rows, pieces;
     size_t parts;
 };

@@ -38,7 +38,7 @@ struct AttnOut {
     float* lse;    // or null
     float* part;   // [2 * pieces][rows][d]
     float2* ml;    // [2 * pieces][rows] (maximum in log2 units, sum)
-    int pieces;
+    int pieces, rows;  // pieces of the line, rows of a tile
 };
 
 // Chunks of sequence b: (row tiles) * Hkv * (chunks of its length).
@@ -394,13 +394,441 @@ k_cache_attn_simt(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restric
     }
 }
 
+// --------------------------------------------------------- tensor cores
+
+__device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+constexpr int mma_stages(int R) { return R == 1 ? 3 : 4; }
+
+template <int D, int R> constexpr int mma_smem() {
+    constexpr int ring = 4 * mma_stages(R) * 2 * Grp<D>::kBytes, merge = 4 * 16 * R * D * 4;
+    return (ring > merge ? ring : merge) + (R > 1 ? R * (D / 16) * 512 : 0);
+}
+
+// bf16 rows on the tensor cores' register form (m16n8k16, halves in, fp32 out).
+//
+// The codes come from shared memory into the registers of the lanes that feed
+// them to the step, are widened there and never go back to shared memory: one
+// conversion per two codes and one product by the scale, both exact. (The
+// tcgen05 form would need the widened operands in shared memory, 3.5 times the
+// cached bytes written and read again, for tiles of 128 rows of which decoding
+// fills 1 to 64.)
+//
+// A warp takes 32 tokens at a time, each warp its own, with its own maximum and
+// sums, so nothing but a segment's end joins the block. Per 32 tokens and 16 rows:
+//   S = Q K^T   4 token tiles x d/16 steps. Q's rows are scaled by a power of two that puts
+//               their largest entry in [2^14, 2^15), so that bf16 is exact as halves down to
+//               2^-31 of it; the power goes into the factor of the scores.
+//   p = 2^(S f - m) in fp32, rounded to halves for the product with V (2^-11 relative; the sum
+//               l takes the unrounded p). m is only moved when a row's maximum exceeds it by
+//               more than 8, so p <= 2^8 and the sums are rarely rescaled.
+//   O += P V    2 steps of 16 tokens x d/8 channel tiles. The layout of P in registers is that of S.
+template <int D, int R>
+__global__ void __launch_bounds__(kThreads, R == 1 ? 3 : 2)
+k_cache_attn_mma(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_t* __restrict__ cache, AttnOut out) {
+    using L = Grp<D>;
+    constexpr int KS = D / 16, NT = D / 8, W = D / 32, RT = 16 * R, ST = mma_stages(R);
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ long long tmp[8];
+    __shared__ float2 sml[4][RT];
+    __shared__ float szf[RT];
+    if (blockIdx.x == 0) {
+        cache_check_call(a, false);
+        return;
+    }
+    const int piece = blockIdx.x - 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, t4 = lane & 3;
+    long long total, before;
+    line_find(a, RT, -1, tmp, &total, nullptr, nullptr);
+    const Line line{total};
+    long long w = line.at(piece, out.pieces);
+    const long long w_begin = w, w_end = line.at(piece + 1, out.pieces);
+    if (w >= w_end) return;
+    int b;
+    line_find(a, RT, w, tmp, &total, &b, &before);
+    SeqWork sw = seq_work(a, b, RT);
+    uint8_t* ring = smem + warp * (ST * 2 * L::kBytes);
+    const uint32_t ring_addr = smem_addr(ring);
+    uint4* qs = reinterpret_cast<uint4*>(smem + mma_smem<D, R>() - (R > 1 ? R * KS * 512 : 0));
+
+    while (w < w_end) {
+        while (w >= before + sw.total) {  // next sequence with work
+            before += sw.total;
+            sw = seq_work(a, ++b, RT);
+        }
+        const Segment s = segment_at(a, RT, sw, b, before, w, w_end);
+        const int n = cache_len(a, b), count = cache_count(a, b);
+        // rows of a tile see more keys the later their token is
+        const int low = row_limit(a, n, count, s.row0 / a.G), top = row_limit(a, n, count, (s.row0 + s.rows - 1) / a.G);
+        const int steps = s.c1 - s.c0;
+        GroupRun gr;
+        gr.begin(a, s, top, warp, lane);
+#pragma unroll
+        for (int i = 0; i < ST - 1; ++i) {
+            const int g0 = gr.get(i, 0), g1 = gr.get(i, 1);
+            if (i < steps) stage_step<D>(cache, ring_addr + i * 2 * L::kBytes, g0, g1, lane); else copy_commit();
+        }
+        // Q: lane (g, t4) has rows g and g + 8 in channels [t4 d/4, (t4 + 1) d/4)
+        const float kf = a.scale * kLog2e * pow2(cache_exp(a, 0, s.h)), vscale = pow2(cache_exp(a, 1, s.h));
+        uint32_t qf[R == 1 ? KS : 1][4];
+        float zf[R][2];
+        int lim[R][2];
+#pragma unroll
+        for (int mt = 0; mt < R; ++mt) {
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int r = mt * 16 + hf * 8 + g;
+                int t = 0;
+                const long long at = row_offset(a, b, s.h, s.row0 + min(r, s.rows - 1), &t);
+                lim[mt][hf] = r < s.rows ? row_limit(a, n, count, t) : 0;
+                if (R > 1 && warp != mt) continue;
+                uint4 q4[D / 32];
+                uint32_t amax = 0;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    q4[i] = make_uint4(0, 0, 0, 0);
+                    if (r < s.rows) q4[i] = reinterpret_cast<const uint4*>(Q + at * D + t4 * (D / 4))[i];
+                    const uint32_t x[4] = {q4[i].x, q4[i].y, q4[i].z, q4[i].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) amax = max(amax, max(x[j] & 0x7fffu, (x[j] >> 16) & 0x7fffu));
+                }
+                amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                const int ex = (int)(amax >> 7);  // biased exponent of the row's largest entry
+                const int qe = ex == 255 ? 0 : min(141 - ex, 120);
+                const float up = pow2(qe);
+                // kept away from 0 and infinity: a masked score is -infinity times it
+                const float f = fminf(fmaxf(kf * pow2(-qe), 1.1754944e-38f), 3.4028235e38f);
+                if (R == 1) zf[mt][hf] = f;
+                else if (t4 == 0) szf[r] = f;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const uint32_t x[4] = {q4[i].x, q4[i].y, q4[i].z, q4[i].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t h = pack_half2(__uint_as_float(x[j] << 16) * up, __uint_as_float(x[j] & 0xffff0000u) * up);
+                        const int ks = 2 * i + (j >> 1), e = hf + 2 * (j & 1);
+                        if (R == 1) qf[ks][e] = h;
+                        else reinterpret_cast<uint32_t*>(qs + (mt * KS + ks) * 32 + lane)[e] = h;
+                    }
+                }
+            }
+        }
+        if (R > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int mt = 0; mt < R; ++mt)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) zf[mt][hf] = szf[mt * 16 + hf * 8 + g];
+        }
+        float o[R][NT][4], m[R][2], l[R][2];
+#pragma unroll
+        for (int mt = 0; mt < R; ++mt) {
+            m[mt][0] = m[mt][1] = -INFINITY;
+            l[mt][0] = l[mt][1] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[mt][i][e] = 0.0f;
+        }
+
+        for (int i = 0; i < steps; ++i) {
+            const int nx = i + ST - 1;
+            const int g0 = gr.get(nx, 0), g1 = gr.get(nx, 1);
+            __syncwarp();
+            if (nx < steps) stage_step<D>(cache, ring_addr + (nx % ST) * 2 * L::kBytes, g0, g1, lane); else copy_commit();
+            gr.advance(a, s, top, warp, lane, nx);
+            copy_wait<ST - 1>();
+            __syncwarp();
+            const int base = (s.c0 + i) * kChunk + warp * kStep;
+            if (base >= top) continue;
+            const uint8_t* st = ring + (i % ST) * 2 * L::kBytes;
+
+            float z[R][4][4];
+#pragma unroll
+            for (int mt = 0; mt < R; ++mt)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z[mt][x][e] = 0.0f;
+#pragma unroll
+            for (int gi = 0; gi < 2; ++gi) {
+                const uint8_t* kb = st + gi * L::kBytes;
+                uint32_t kw[2][W], sc[2][D / 64];  // codes; scales, each in both halves
+                if (D == 128) {
+                    const uint32_t sb = *reinterpret_cast<const uint32_t*>(kb + L::kKs + g * 16 + t4 * 4);
+                    const uint32_t s0 = e4m3x2_to_half2(sb & 0xffff), s1 = e4m3x2_to_half2(sb >> 16);
+                    sc[0][0] = __byte_perm(s0, s0, 0x1010);
+                    sc[0][D / 64 - 1] = __byte_perm(s0, s0, 0x3232);
+                    sc[1][0] = __byte_perm(s1, s1, 0x1010);
+                    sc[1][D / 64 - 1] = __byte_perm(s1, s1, 0x3232);
+                } else {
+                    const uint32_t s0 = e4m3x2_to_half2(*reinterpret_cast<const uint16_t*>(kb + L::kKs + g * 8 + t4 * 2));
+                    sc[0][0] = __byte_perm(s0, s0, 0x1010);
+                    sc[1][0] = __byte_perm(s0, s0, 0x3232);
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint8_t* kr = kb + (8 * x + g) * L::kRow + t4 * (D / 8);
+                    if (D == 128) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(kr);
+                        kw[x][0] = v.x; kw[x][1] = v.y; kw[x][W - 2] = v.z; kw[x][W - 1] = v.w;
+                    } else {
+                        const uint2 v = *reinterpret_cast<const uint2*>(kr);
+                        kw[x][0] = v.x; kw[x][1] = v.y;
+                    }
+                }
+#pragma unroll
+                for (int wi = 0; wi < W; ++wi) {
+                    uint32_t k8[2][4];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        e2m1x8_to_half2(kw[x][wi], k8[x]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) k8[x][j] = hmul2(k8[x][j], sc[x][wi >> 1]);
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < R; ++mt)
+#pragma unroll
+                        for (int ks = 0; ks < 2; ++ks) {
+                            uint32_t qa[4];
+                            if (R == 1) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) qa[e] = qf[2 * wi + ks][e];
+                            } else {
+                                const uint4 v = qs[(mt * KS + 2 * wi + ks) * 32 + lane];
+                                qa[0] = v.x; qa[1] = v.y; qa[2] = v.z; qa[3] = v.w;
+                            }
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
+                                mma_f16(z[mt][2 * gi + x], qa, k8[x][2 * ks], k8[x][2 * ks + 1]);
+                        }
+                }
+            }
+            const bool edge = base + kStep > low;  // some row does not see all 32 tokens
+            if (edge) {
+#pragma unroll
+                for (int mt = 0; mt < R; ++mt)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (base + 8 * x + 2 * t4 + (e & 1) >= lim[mt][e >> 1]) z[mt][x][e] = -INFINITY;
+            }
+            // maxima of the rows, and where they exceed the reference by more than 8
+            float mx[R][2];
+            bool move = false;
+#pragma unroll
+            for (int mt = 0; mt < R; ++mt)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    float v = -INFINITY;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) v = fmaxf(v, fmaxf(z[mt][x][2 * hf], z[mt][x][2 * hf + 1]));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                    mx[mt][hf] = v * zf[mt][hf];
+                    move |= mx[mt][hf] > m[mt][hf] + 8.0f;
+                }
+            if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                for (int mt = 0; mt < R; ++mt)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const float mn = fmaxf(m[mt][hf], mx[mt][hf]);
+                        const float f = mn == -INFINITY ? 1.0f : ex2(m[mt][hf] - mn);
+                        m[mt][hf] = mn;
+                        l[mt][hf] *= f;
+#pragma unroll
+                        for (int x = 0; x < NT; ++x) {
+                            o[mt][x][2 * hf] *= f;
+                            o[mt][x][2 * hf + 1] *= f;
+                        }
+                    }
+            }
+            uint32_t p[R][2][4];
+#pragma unroll
+            for (int mt = 0; mt < R; ++mt)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const float ref = m[mt][hf] == -INFINITY ? 0.0f : m[mt][hf];  // no key seen yet
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const float p0 = ex2(fmaf(z[mt][x][2 * hf], zf[mt][hf], -ref));
+                        const float p1 = ex2(fmaf(z[mt][x][2 * hf + 1], zf[mt][hf], -ref));
+                        l[mt][hf] += p0 + p1;
+                        p[mt][x >> 1][hf + 2 * (x & 1)] = pack_half2(p0, p1);
+                    }
+                }
+#pragma unroll
+            for (int gi = 0; gi < 2; ++gi) {
+                const uint8_t* vb = st + gi * L::kBytes;
+                uint32_t sb = *reinterpret_cast<const uint32_t*>(vb + L::kVs + (D == 128 ? g : g >> 1) * 16 + t4 * 4);
+                if (edge) {
+                    // Nothing of a token that a row does not see may reach it: bytes behind the
+                    // last token are made zero here; NaN of a token that only some rows see
+                    // is taken out of the product and put into the rows that see it.
+                    uint32_t nan = 0;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int tok = base + 16 * gi + 8 * (x >> 1) + 2 * t4 + (x & 1);
+                        const uint32_t byte = 0xffu << (8 * x);
+                        if (tok >= n) sb &= ~byte;
+                        if ((sb >> (8 * x) & 0x7f) == 0x7f) nan |= byte;
+                    }
+                    if (__any_sync(0xffffffffu, nan != 0)) {
+                        sb &= ~nan;
+                        const uint32_t one = 0x3c003c00u;  // (1, 1) in halves
+                        const uint32_t b0 = __byte_perm(nan, 0, 0x1100) & one, b1 = __byte_perm(nan, 0, 0x3322) & one;
+#pragma unroll
+                        for (int mt = 0; mt < R; ++mt) {
+                            uint32_t see[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int tok = base + 16 * gi + 8 * (e >> 1) + 2 * t4, lm = lim[mt][e & 1];
+                                see[e] = ((tok < lm ? 0x3c00u : 0) | (tok + 1 < lm ? 0x3c000000u : 0));
+                            }
+                            float hit[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                            mma_f16(hit, see, b0, b1);
+#pragma unroll
+                            for (int x = 0; x < NT; ++x)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (hit[e] > 0.0f) o[mt][x][e] = __int_as_float(0x7fc00000);
+                        }
+                    }
+                }
+                const uint32_t s0 = e4m3x2_to_half2(sb & 0xffff), s1 = e4m3x2_to_half2(sb >> 16);
+                uint32_t vw[4][D / 64];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const uint8_t* vr = vb + L::v_chunk(t4 + 4 * x, g);
+                    if (D == 128) {
+                        const uint2 v = *reinterpret_cast<const uint2*>(vr);
+                        vw[x][0] = v.x; vw[x][D / 64 - 1] = v.y;
+                    } else {
+                        vw[x][0] = *reinterpret_cast<const uint32_t*>(vr);
+                    }
+                }
+#pragma unroll
+                for (int wi = 0; wi < D / 64; ++wi) {
+                    // a byte of both tokens of a pair: even channels, then odd ones
+                    constexpr uint32_t lo = 0x0f0f0f0fu;
+                    uint32_t v8[2][2][4];  // [tokens 8 x + 2 t4 ..][parity of the channel]
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint32_t u0 = vw[2 * x][wi], u1 = vw[2 * x + 1][wi];
+                        e2m1x8_to_half2((u0 & lo) | ((u1 << 4) & ~lo), v8[x][0]);
+                        e2m1x8_to_half2(((u0 >> 4) & lo) | (u1 & ~lo), v8[x][1]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t b0 = hmul2(v8[0][j & 1][j >> 1], s0), b1 = hmul2(v8[1][j & 1][j >> 1], s1);
+#pragma unroll
+                        for (int mt = 0; mt < R; ++mt) mma_f16(o[mt][8 * wi + j], p[mt][gi], b0, b1);
+                    }
+                }
+            }
+        }
+        copy_wait<0>();
+        // the row sums of a quad's lanes
+#pragma unroll
+        for (int mt = 0; mt < R; ++mt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 1);
+                l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 2);
+            }
+        __syncthreads();  // every warp is done with its ring
+        // Join the warps: [warp][row][d] sums, 16 bytes (four channels) at a time. Lane
+        // (g, t4)'s chunks are 8 apart between the t4, so their low three bits take t4
+        // and the row's parity, which puts eight lanes on eight different bank groups.
+        float4* os = reinterpret_cast<float4*>(smem);
+        constexpr int C4 = D / 4;
+#pragma unroll
+        for (int mt = 0; mt < R; ++mt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int r = mt * 16 + hf * 8 + g;
+                if (t4 == 0) sml[warp][r] = make_float2(m[mt][hf], l[mt][hf]);
+                if (r >= s.rows) continue;
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int j = 0; j < NT / 4; ++j) {
+                        const int c = (2 * t4 + e) * (NT / 4) + j;
+                        os[(warp * RT + r) * C4 + (c ^ ((c / (NT / 2)) | (r & 1) << 2))] =
+                            make_float4(o[mt][4 * j][2 * hf + e], o[mt][4 * j + 1][2 * hf + e],
+                                        o[mt][4 * j + 2][2 * hf + e], o[mt][4 * j + 3][2 * hf + e]);
+                    }
+            }
+        __syncthreads();
+        const bool whole = s.c0 == 0 && s.c1 == s.chunks;
+        const int slot = 2 * piece + (w == w_begin ? 0 : 1);
+        for (int x = threadIdx.x; x < s.rows * C4; x += kThreads) {
+            const int r = x / C4, c = x - r * C4;
+            float2 v[4];
+            float mx = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] = sml[i][r];
+                mx = fmaxf(mx, v[i].x);
+            }
+            const float ref = mx == -INFINITY ? 0.0f : mx;
+            float sum = 0.0f;
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float f = ex2(v[i].x - ref);
+                const float4 u = os[(i * RT + r) * C4 + (c ^ ((c / (NT / 2)) | (r & 1) << 2))];
+                sum = fmaf(f, v[i].y, sum);
+                acc.x = fmaf(f, u.x, acc.x); acc.y = fmaf(f, u.y, acc.y);
+                acc.z = fmaf(f, u.z, acc.z); acc.w = fmaf(f, u.w, acc.w);
+            }
+            if (whole) {
+                int t;
+                const long long at = row_offset(a, b, s.h, s.row0 + r, &t);
+                const float inv = sum == 0.0f ? 0.0f : vscale / sum;
+                const __nv_bfloat162 h0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv),
+                                     h1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+                reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(out.O) + at * D)[c] =
+                    make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+                if (out.lse && c == 0) out.lse[at] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+            } else {
+                acc.x *= vscale; acc.y *= vscale; acc.z *= vscale; acc.w *= vscale;
+                reinterpret_cast<float4*>(out.part + ((long long)slot * RT + r) * D)[c] = acc;
+                if (c == 0) out.ml[(long long)slot * RT + r] = make_float2(mx, sum);
+            }
+        }
+        __syncthreads();
+        w = s.start + s.c1;
+    }
+}
+
 // ------------------------------------------------------------------ join
 
 // Block (c, y), c >= 1: if piece c's first chunk lies inside an item and is the
 // first such cut of it, joins that item's parts; each of the four warps takes a
 // row of the four rows from 4 y on. Piece c - 1 has the item's first chunk.
-template <typename T, int D, int R>
+template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) k_cache_join(CacheArgs a, AttnOut out) {
+    const int R = out.rows;
     __shared__ long long tmp[8];
     const int c = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long total, before;
@@ -442,9 +870,6 @@ __global__ void __launch_bounds__(kThreads) k_cache_join(CacheArgs a, AttnOut ou
 
 // ------------------------------------------------------------------ launch
 
-// Rows of a tile: one (a single row per cache head) or four.
-static int simt_rows(const CacheArgs& a) { return (long long)a.G * a.T == 1 ? 1 : 4; }
-
 static long long max_chunks(const CacheArgs& a, int rtile) {
     const long long tiles = ((long long)a.G * a.T + rtile - 1) / rtile;
     const long long len = ((long long)a.cols * a.page + kChunk - 1) / kChunk;
@@ -453,40 +878,65 @@ static long long max_chunks(const CacheArgs& a, int rtile) {
 
 CachePlan cache_attn_plan(const CacheArgs& a, int d, int dtype, unsigned flags) {
     CachePlan p;
-    p.rows = simt_rows(a);
-    // four blocks per SM, one of them the check of the call's indexes
-    p.pieces = (int)std::min<long long>(4LL * num_sms() - 1, max_chunks(a, p.rows));
+    const long long rows = (long long)a.G * a.T;
+    p.tensor = dtype == 1 && !(flags & MITA_FLAG_SIMT);
+    int blocks = 4;  // per SM
+    if (p.tensor) {
+        p.rows = rows <= 16 ? 16 : 32;
+        blocks = rows <= 16 ? 3 : 2;
+    } else {
+        p.rows = rows == 1 ? 1 : 4;
+    }
+    // one of the resident blocks checks the call's indexes
+    p.pieces = (int)std::min<long long>((long long)blocks * num_sms() - 1, max_chunks(a, p.rows));
     p.parts = (size_t)2 * p.pieces * p.rows;
     return p;
+}
+
+template <typename T, int D>
+static cudaError_t join_t(const CacheArgs& a, const AttnOut& o, cudaStream_t st) {
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || o.pieces == 1) return e;
+    prof_mark(st, "cache_join");
+    k_cache_join<T, D><<<dim3(o.pieces - 1, (o.rows + 3) / 4), kThreads, 0, st>>>(a, o);
+    count_launch();
+    return cudaGetLastError();
 }
 
 template <typename T, int D, int R>
 static cudaError_t simt_t(const CacheArgs& a, const void* Q, const uint8_t* cache, const AttnOut& o, cudaStream_t st) {
     constexpr int smem = simt_smem<D, R>();
-    cudaError_t e = cudaFuncSetAttribute(k_cache_attn_simt<T, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(k_cache_attn_simt<T, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     k_cache_attn_simt<T, D, R><<<o.pieces + 1, kThreads, smem, st>>>(a, (const T*)Q, cache, o);
     count_launch();
-    if ((e = cudaGetLastError()) != cudaSuccess || o.pieces == 1) return e;
-    prof_mark(st, "cache_join");
-    k_cache_join<T, D, R><<<dim3(o.pieces - 1, (R + 3) / 4), kThreads, 0, st>>>(a, o);
-    count_launch();
-    return cudaGetLastError();
+    return join_t<T, D>(a, o, st);
 }
 
-template <typename T, int D>
-static cudaError_t attn_t(const CacheArgs& a, const CachePlan& p, const void* Q, const uint8_t* cache,
+template <int D, int R>
+static cudaError_t mma_t(const CacheArgs& a, const void* Q, const uint8_t* cache, const AttnOut& o, cudaStream_t st) {
+    constexpr int smem = mma_smem<D, R>();
+    const cudaError_t e = cudaFuncSetAttribute(k_cache_attn_mma<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    k_cache_attn_mma<D, R><<<o.pieces + 1, kThreads, smem, st>>>(a, (const __nv_bfloat16*)Q, cache, o);
+    count_launch();
+    return join_t<__nv_bfloat16, D>(a, o, st);
+}
+
+template <int D>
+static cudaError_t attn_t(const CacheArgs& a, const CachePlan& p, int dtype, const void* Q, const uint8_t* cache,
                           const AttnOut& o, cudaStream_t st) {
-    return p.rows == 1 ? simt_t<T, D, 1>(a, Q, cache, o, st) : simt_t<T, D, 4>(a, Q, cache, o, st);
+    if (p.tensor) return p.rows == 16 ? mma_t<D, 1>(a, Q, cache, o, st) : mma_t<D, 2>(a, Q, cache, o, st);
+    if (dtype == 0) return p.rows == 1 ? simt_t<float, D, 1>(a, Q, cache, o, st) : simt_t<float, D, 4>(a, Q, cache, o, st);
+    return p.rows == 1 ? simt_t<__nv_bfloat16, D, 1>(a, Q, cache, o, st) : simt_t<__nv_bfloat16, D, 4>(a, Q, cache, o, st);
 }
 
 cudaError_t launch_cache_attn(const CacheArgs& a, const CachePlan& p, int d, int dtype, const void* Q,
                               const void* cache, void* O, float* lse, float* part, float2* ml, cudaStream_t st) {
-    const AttnOut o{O, lse, part, ml, p.pieces};
+    const AttnOut o{O, lse, part, ml, p.pieces, p.rows};
     const uint8_t* c = (const uint8_t*)cache;
     prof_mark(st, "cache_attention");
-    if (dtype == 0) return d == 64 ? attn_t<float, 64>(a, p, Q, c, o, st) : attn_t<float, 128>(a, p, Q, c, o, st);
-    return d == 64 ? attn_t<__nv_bfloat16, 64>(a, p, Q, c, o, st) : attn_t<__nv_bfloat16, 128>(a, p, Q, c, o, st);
+    return d == 64 ? attn_t<64>(a, p, dtype, Q, c, o, st) : attn_t<128>(a, p, dtype, Q, c, o, st);
 }
 
 }  // namespace mita
