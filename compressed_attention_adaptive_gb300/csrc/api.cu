@@ -328,15 +328,15 @@ static mita_status resolve_cache(const mita_cache_params* p, CacheArgs* a) {
 // Workspace of the cache calls: the status word, then the attention's partial results.
 struct CacheWork {
     int* status;
-    float* part;
-    float2* ml;
+    CacheParts parts;
 };
 static CacheWork carve_cache(const mita_cache_params* p, const CachePlan& plan, void* ws, size_t* bytes) {
     Carver c(ws);
     CacheWork w{};
     w.status = c.take<int>(64);
-    w.part = c.take<float>(plan.parts * p->d);
-    w.ml = c.take<float2>(plan.parts);
+    w.parts.part = c.take<float>(plan.parts * p->d);
+    w.parts.ml = c.take<float2>(plan.parts);
+    w.parts.cut = c.take<char>((size_t)plan.pieces * kCutBytes);
     *bytes = align_up(c.off, 1024);
     return w;
 }
@@ -672,7 +672,7 @@ mita_status mita_cache_attention(const mita_cache_params* p, const void* Q, cons
     const mita_status st = cache_begin(p, &a, &plan, &w, Q, O, cache, table, len, count, exps, ws, ws_bytes);
     if (st) return st;
     if ((uintptr_t)lse_out % 4) return fail(MITA_ERR_INVALID_ARG, "lse_out must be 4-byte aligned");
-    MITA_CUDA(launch_cache_attn(a, plan, p->d, p->dtype, Q, cache, O, lse_out, w.part, w.ml, (cudaStream_t)stream),
+    MITA_CUDA(launch_cache_attn(a, plan, p->d, p->dtype, Q, cache, O, lse_out, w.parts, (cudaStream_t)stream),
               "cache attention");
     prof_mark((cudaStream_t)stream, "");
     return MITA_OK;

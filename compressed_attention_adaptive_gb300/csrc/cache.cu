@@ -11,205 +11,222 @@
 
 namespace mita {
 
-// The 16 elements of a block as fp32.
-__device__ __forceinline__ void load16(const float* p, float* x) {
+// 32 bytes at a time where the caller's tensor allows it (`wide`: 32-byte
+// aligned), else 16.
+__device__ __forceinline__ void load32(const void* p, bool wide, uint32_t* r) {
+    if (wide) {
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "l"(p));
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 v = reinterpret_cast<const float4*>(p)[i];
-        x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
-    }
-}
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float* x) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint4 v = reinterpret_cast<const uint4*>(p)[i];
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-            x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        for (int i = 0; i < 2; ++i) {
+            const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+            r[4 * i] = v.x; r[4 * i + 1] = v.y; r[4 * i + 2] = v.z; r[4 * i + 3] = v.w;
         }
     }
 }
-__device__ __forceinline__ void store16(float* p, const float* x) {
+__device__ __forceinline__ void store32(void* p, bool wide, const uint32_t* r) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
+                     "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "l"(p)
+                     : "memory");
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        reinterpret_cast<float4*>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-}
-__device__ __forceinline__ void store16(__nv_bfloat16* p, const float* x) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(x[8 * i + 2 * j], x[8 * i + 2 * j + 1]);
-            w[j] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        reinterpret_cast<uint4*>(p)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int i = 0; i < 2; ++i)
+            reinterpret_cast<uint4*>(p)[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
     }
 }
 
-// y (16 values, already times 2^-e) -> 16 codes and the scale byte.
-//
-// s = RN_e4m3(amax / 6) and code = RN_e2m1(y / s), as if the quotients were
-// exact: a correctly rounded fp32 quotient equals a midpoint of the target
-// grid only if the exact one does. (A midpoint M has at most 5 significant
-// bits and the divisor at most 4, so M times the divisor is a float; the next
-// float is at least 2^-23 / f away relative to it, f in [1, 2) its
-// significand, which is more than half a step of the quotient, 2^-24 / h, h in
-// [1, 2) that of M. Below a power of two the float spacing halves, and so does
-// the quotient's if M is one too; the divisors' significands leave no other
-// case.)
-__device__ __forceinline__ void quantise16(const float* y, uint32_t* codes, uint32_t* scale) {
+// A block's 16 elements: as they are in memory, and as fp32.
+template <typename T> struct Raw {
+    static constexpr int kWords = 4 * sizeof(T);
+    uint32_t r[kWords];
+    __device__ __forceinline__ void load(const T* p, bool wide) {
+#pragma unroll
+        for (int i = 0; i < kWords; i += 8) load32(reinterpret_cast<const uint32_t*>(p) + i, wide, r + i);
+    }
+    __device__ __forceinline__ void store(T* p, bool wide) const {
+#pragma unroll
+        for (int i = 0; i < kWords; i += 8) store32(reinterpret_cast<uint32_t*>(p) + i, wide, r + i);
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if (sizeof(T) == 4) return __uint_as_float(r[i % kWords]);
+        return __uint_as_float(i & 1 ? r[i >> 1] & 0xffff0000u : r[i >> 1] << 16);
+    }
+    __device__ __forceinline__ void set2(int i, float x, float y) {  // elements i (even) and i + 1
+        if (sizeof(T) == 4) {
+            r[i] = __float_as_uint(x);
+            r[(i + 1) % kWords] = __float_as_uint(y);
+        } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+            r[i >> 1] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+    }
+};
+
+// y / s for the code grid, s an e4m3 number. Its rounding must not move a
+// quotient onto or off a midpoint M of the grid {1/4, 3/4, 5/4, 7/4, 5/2, 7/2, 5}.
+//   float32: the correctly rounded quotient. It equals M only if y = M s: M s is a float
+//   (3 and 4 significant bits), the next float is 2^-23 / f away relative to it, f in [1, 2)
+//   its significand, and half a step of the quotient is 2^-24 / h, h in [1, 2) that of M.
+//   (Below a power of two the spacing of floats halves; M s is one only where M is one
+//   too, and then half a step of the quotient halves as well.)
+//   bf16: y has 8 significant bits and M s has 7, so y is M s or at least 2^-8 of it
+//   away. y * (1 / s) is within 2^-23 of the quotient, relative: adding and
+//   subtracting 48 rounds it to a multiple of 2^-18, which is M itself in the
+//   first case and on the quotient's side of M in the second. Three operations
+//   per element instead of a division.
+template <typename T> __device__ __forceinline__ float code_quotient(float y, float s, float rs) {
+    if (sizeof(T) == 4) return __fdiv_rn(y, s);
+    return __fadd_rn(__fadd_rn(__fmul_rn(y, rs), 48.0f), -48.0f);
+}
+
+// A block (times 2^-e) -> 16 codes and the scale byte, s = RN_e4m3(amax / 6),
+// code = RN_e2m1(y / s). For s too the fp32 quotient is a midpoint of the grid
+// (5 significant bits, the divisor 2) only if the exact one is.
+template <typename T>
+__device__ __forceinline__ void quantise16(const Raw<T>& x, float up, uint32_t* codes, uint32_t* scale) {
     uint32_t amax = 0;  // as bits: NaN > infinity > every number
 #pragma unroll
-    for (int i = 0; i < 16; ++i) amax = max(amax, __float_as_uint(y[i]) & 0x7fffffffu);
+    for (int i = 0; i < 16; ++i) amax = max(amax, __float_as_uint(x.get(i)) & 0x7fffffffu);
     codes[0] = codes[1] = 0;
     if (amax > 0x7f800000u) {  // a NaN stays visible: the whole block reads as NaN
         *scale = 0x7f;
         return;
     }
-    const float raw = __fdiv_rn(__uint_as_float(amax), 6.0f);
+    const float raw = __fdiv_rn(__uint_as_float(amax) * up, 6.0f);
     uint16_t sb;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(sb) : "f"(0.0f), "f"(raw));
     *scale = sb & 0xff;
     if ((sb & 0xff) == 0) return;
-    const float s = half2_to_float2(e4m3x2_to_half2(sb)).x;
+    const float s = half2_to_float2(e4m3x2_to_half2(sb)).x, rs = __frcp_rn(s);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         uint32_t b;
         asm("{.reg .b8 t; .reg .b16 u; cvt.rn.satfinite.e2m1x2.f32 t, %1, %2; mov.b16 u, {t, 0}; cvt.u32.u16 %0, u;}"
             : "=r"(b)
-            : "f"(__fdiv_rn(y[2 * i + 1], s)), "f"(__fdiv_rn(y[2 * i], s)));
+            : "f"(code_quotient<T>(x.get(2 * i + 1) * up, s, rs)), "f"(code_quotient<T>(x.get(2 * i) * up, s, rs)));
         codes[i >> 2] |= b << (8 * (i & 3));
     }
 }
 
-// Place of a block: which group, and which bytes of it. Returns false for
-// padding rows and for places outside the sequence or the pool.
-struct BlockAt {
-    int which, b, h, t, blk;
-    long long row;  // of [B, Hkv, T]
+// Block blk of row `row` of [B, Hkv, T]: the thread has it for keys and values,
+// which share the sequence's place. found() loads the lengths, group() the
+// table, so that the rows can be loaded in between.
+template <int D> struct BlockAt {
+    int b, h, pos, blk;
+    uint32_t row;
+
+    // false: past the last row, padding, or before the sequence's first token
+    __device__ __forceinline__ bool found(const CacheArgs& a) {
+        constexpr int NB = Grp<D>::kBlocks;
+        const long long i = (long long)(blockIdx.x - 1) * blockDim.x + threadIdx.x;
+        blk = (int)(i % NB);
+        const long long r = i / NB;
+        if (r >= (long long)a.B * a.Hkv * a.T) return false;
+        row = (uint32_t)r;  // B * H * T < 2^31
+        const uint32_t bh = row / (uint32_t)a.T;
+        const int t = (int)(row - bh * a.T);
+        b = (int)(bh / (uint32_t)a.Hkv);
+        h = (int)(bh - (uint32_t)b * a.Hkv);
+        const int n = cache_len(a, b), c = cache_count(a, b);
+        pos = n - c + t;
+        return t < c && pos >= 0;
+    }
+    __device__ __forceinline__ int group(const CacheArgs& a) const { return cache_group(a, b, h, pos / kGroup); }
+    __device__ __forceinline__ int tok() const { return pos % kGroup; }
+    __device__ __forceinline__ long long element() const { return (long long)row * D + blk * 16; }
 };
-
-template <int D>
-__device__ __forceinline__ bool place(const CacheArgs& a, const BlockAt& x, long long* group, int* tok) {
-    const int n = cache_len(a, x.b), c = cache_count(a, x.b);
-    const int pos = n - c + x.t;
-    if (x.t >= c || pos < 0) return false;
-    const int g = cache_group(a, x.b, x.h, pos / kGroup);
-    *group = g;
-    *tok = pos % kGroup;
-    return g >= 0;
-}
-
-// Thread i: block i % (d/16) of row i / (d/16); blockIdx.y: keys or values.
-template <int D>
-__device__ __forceinline__ bool block_at(const CacheArgs& a, BlockAt* x) {
-    constexpr int NB = Grp<D>::kBlocks;
-    const long long i = (long long)(blockIdx.x - 1) * blockDim.x + threadIdx.x;
-    x->which = blockIdx.y;
-    x->blk = (int)(i % NB);
-    x->row = i / NB;
-    if (x->row >= (long long)a.B * a.Hkv * a.T) return false;
-    x->t = (int)(x->row % a.T);
-    const int bh = (int)(x->row / a.T);
-    x->b = bh / a.Hkv;
-    x->h = bh - x->b * a.Hkv;
-    return true;
-}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(256) k_cache_write(CacheArgs a, const T* __restrict__ K, const T* __restrict__ V,
-                                                     uint8_t* __restrict__ cache) {
+                                                     uint8_t* __restrict__ cache, bool wide) {
     using L = Grp<D>;
     if (blockIdx.x == 0) {
-        if (blockIdx.y == 0) cache_check_call(a, true);
+        cache_check_call(a, true);
         return;
     }
-    BlockAt x;
-    long long group;
-    int tok;
-    if (!block_at<D>(a, &x) || !place<D>(a, x, &group, &tok)) return;
-    float y[16];
-    load16((x.which ? V : K) + x.row * D + x.blk * 16, y);
-    const float up = pow2(-cache_exp(a, x.which, x.h));
-#pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] *= up;
+    BlockAt<D> x;
+    if (!x.found(a)) return;
+    Raw<T> k, v;
+    k.load(K + x.element(), wide);
+    v.load(V + x.element(), wide);
+    const int group = x.group(a), ke = cache_exp(a, 0, x.h), ve = cache_exp(a, 1, x.h), tok = x.tok();
+    if (group < 0) return;
+    uint8_t* g = cache + (long long)group * L::kBytes;
     uint32_t codes[2], scale;
-    quantise16(y, codes, &scale);
-    uint8_t* g = cache + group * L::kBytes;
-    if (x.which == 0) {
-        *reinterpret_cast<uint2*>(g + L::k_code(tok, x.blk)) = make_uint2(codes[0], codes[1]);
-        g[L::k_scale(tok, x.blk)] = (uint8_t)scale;
-    } else {
-        // a block is one chunk for d = 128, two for d = 64
-        const int row = L::v_row(tok);
-        if (D == 128) {
-            *reinterpret_cast<uint2*>(g + L::v_chunk(row, x.blk)) = make_uint2(codes[0], codes[1]);
-        } else {
-            *reinterpret_cast<uint32_t*>(g + L::v_chunk(row, 2 * x.blk)) = codes[0];
-            *reinterpret_cast<uint32_t*>(g + L::v_chunk(row, 2 * x.blk + 1)) = codes[1];
-        }
-        g[L::v_scale(tok, x.blk)] = (uint8_t)scale;
+    quantise16(k, pow2(-ke), codes, &scale);
+    *reinterpret_cast<uint2*>(g + L::k_code(tok, x.blk)) = make_uint2(codes[0], codes[1]);
+    g[L::k_scale(tok, x.blk)] = (uint8_t)scale;
+    quantise16(v, pow2(-ve), codes, &scale);
+    const int row = L::v_row(tok);
+    if (D == 128) {  // a block is one chunk
+        *reinterpret_cast<uint2*>(g + L::v_chunk(row, x.blk)) = make_uint2(codes[0], codes[1]);
+    } else {  // or two
+        *reinterpret_cast<uint32_t*>(g + L::v_chunk(row, 2 * x.blk)) = codes[0];
+        *reinterpret_cast<uint32_t*>(g + L::v_chunk(row, 2 * x.blk + 1)) = codes[1];
     }
+    g[L::v_scale(tok, x.blk)] = (uint8_t)scale;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(256) k_cache_read(CacheArgs a, const uint8_t* __restrict__ cache, T* __restrict__ K,
-                                                    T* __restrict__ V) {
-    using L = Grp<D>;
-    if (blockIdx.x == 0) {
-        if (blockIdx.y == 0) cache_check_call(a, true);
-        return;
-    }
-    BlockAt x;
-    long long group;
-    int tok;
-    if (!block_at<D>(a, &x) || !place<D>(a, x, &group, &tok)) return;
-    const uint8_t* g = cache + group * L::kBytes;
-    uint32_t codes[2];
-    uint32_t scale;
-    if (x.which == 0) {
-        const uint2 w = *reinterpret_cast<const uint2*>(g + L::k_code(tok, x.blk));
-        codes[0] = w.x; codes[1] = w.y;
-        scale = g[L::k_scale(tok, x.blk)];
-    } else {
-        const int row = L::v_row(tok);
-        if (D == 128) {
-            const uint2 w = *reinterpret_cast<const uint2*>(g + L::v_chunk(row, x.blk));
-            codes[0] = w.x; codes[1] = w.y;
-        } else {
-            codes[0] = *reinterpret_cast<const uint32_t*>(g + L::v_chunk(row, 2 * x.blk));
-            codes[1] = *reinterpret_cast<const uint32_t*>(g + L::v_chunk(row, 2 * x.blk + 1));
-        }
-        scale = g[L::v_scale(tok, x.blk)];
-    }
+// 16 codes and their scale byte -> the block.
+template <typename T>
+__device__ __forceinline__ void widen16(const uint32_t* codes, uint32_t scale, float down, Raw<T>* x) {
     const uint32_t s2 = e4m3x2_to_half2(scale | scale << 8);
-    const float down = pow2(cache_exp(a, x.which, x.h));
-    float y[16];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         uint32_t r[4];
         e2m1x8_to_half2(codes[i], r);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float2 v = half2_to_float2(hmul2(r[j], s2));
-            y[8 * i + 2 * j] = v.x * down;
-            y[8 * i + 2 * j + 1] = v.y * down;
+            const float2 y = half2_to_float2(hmul2(r[j], s2));
+            x->set2(8 * i + 2 * j, y.x * down, y.y * down);
         }
     }
-    store16((x.which ? V : K) + x.row * D + x.blk * 16, y);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(256) k_cache_read(CacheArgs a, const uint8_t* __restrict__ cache, T* __restrict__ K,
+                                                    T* __restrict__ V, bool wide) {
+    using L = Grp<D>;
+    if (blockIdx.x == 0) {
+        cache_check_call(a, true);
+        return;
+    }
+    BlockAt<D> x;
+    if (!x.found(a)) return;
+    const int group = x.group(a), ke = cache_exp(a, 0, x.h), ve = cache_exp(a, 1, x.h), tok = x.tok();
+    if (group < 0) return;
+    const uint8_t* g = cache + (long long)group * L::kBytes;
+    const int row = L::v_row(tok);
+    const uint2 kc = *reinterpret_cast<const uint2*>(g + L::k_code(tok, x.blk));
+    const uint32_t ks = g[L::k_scale(tok, x.blk)], vs = g[L::v_scale(tok, x.blk)];
+    uint32_t codes[2];
+    if (D == 128) {
+        const uint2 w = *reinterpret_cast<const uint2*>(g + L::v_chunk(row, x.blk));
+        codes[0] = w.x; codes[1] = w.y;
+    } else {
+        codes[0] = *reinterpret_cast<const uint32_t*>(g + L::v_chunk(row, 2 * x.blk));
+        codes[1] = *reinterpret_cast<const uint32_t*>(g + L::v_chunk(row, 2 * x.blk + 1));
+    }
+    Raw<T> y;
+    widen16(codes, vs, pow2(ve), &y);
+    y.store(V + x.element(), wide);
+    codes[0] = kc.x; codes[1] = kc.y;
+    widen16(codes, ks, pow2(ke), &y);
+    y.store(K + x.element(), wide);
 }
 
 template <typename T, int D>
 static cudaError_t rows_t(const CacheArgs& a, bool write, void* K, void* V, uint8_t* cache, cudaStream_t st) {
     const long long blocks = (long long)a.B * a.Hkv * a.T * (D / 16);
-    const dim3 grid((unsigned)((blocks + 255) / 256) + 1, 2);
+    const unsigned grid = (unsigned)((blocks + 255) / 256) + 1;
+    const bool wide = (((uintptr_t)K | (uintptr_t)V) & 31) == 0;
     if (write)
-        k_cache_write<T, D><<<grid, 256, 0, st>>>(a, (const T*)K, (const T*)V, cache);
+        k_cache_write<T, D><<<grid, 256, 0, st>>>(a, (const T*)K, (const T*)V, cache, wide);
     else
-        k_cache_read<T, D><<<grid, 256, 0, st>>>(a, cache, (T*)K, (T*)V);
+        k_cache_read<T, D><<<grid, 256, 0, st>>>(a, cache, (T*)K, (T*)V, wide);
     count_launch();
     return cudaGetLastError();
 }

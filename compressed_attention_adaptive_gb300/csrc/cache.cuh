@@ -75,13 +75,21 @@ struct CachePlan {
     size_t parts;
 };
 
+// Partial results of the attention, in the workspace.
+constexpr int kCutBytes = 24;  // one CutItem (cache_attn.cu)
+struct CacheParts {
+    float* part;  // [parts][d]
+    float2* ml;   // [parts]
+    void* cut;    // [pieces] of kCutBytes
+};
+
 // cache.cu
 cudaError_t launch_cache_rows(const CacheArgs& a, int d, int dtype, bool write, void* K, void* V, void* cache,
                               cudaStream_t st);
 // cache_attn.cu
 CachePlan cache_attn_plan(const CacheArgs& a, int d, int dtype, unsigned flags);
 cudaError_t launch_cache_attn(const CacheArgs& a, const CachePlan& p, int d, int dtype, const void* Q,
-                              const void* cache, void* O, float* lse, float* part, float2* ml, cudaStream_t st);
+                              const void* cache, void* O, float* lse, const CacheParts& parts, cudaStream_t st);
 
 __device__ __forceinline__ int cache_len(const CacheArgs& a, int b) {
     return min(max(a.len[b], 0), a.cols * a.page);

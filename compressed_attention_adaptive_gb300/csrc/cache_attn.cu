@@ -33,70 +33,106 @@ constexpr int kThreads = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// An item that is cut: the join's work. rows = 0: nothing to join here.
+struct CutItem {
+    int b, h, row0, rows;
+    int slot, parts;  // the first part's slot, and the pieces it goes over
+};
+
+static_assert(sizeof(CutItem) == kCutBytes, "the workspace holds CutItems");
+
 struct AttnOut {
     void* O;
     float* lse;    // or null
     float* part;   // [2 * pieces][rows][d]
     float2* ml;    // [2 * pieces][rows] (maximum in log2 units, sum)
+    CutItem* cut;  // [pieces]: the item that starts in a piece and ends behind it
     int pieces, rows;  // pieces of the line, rows of a tile
 };
 
-// Chunks of sequence b: (row tiles) * Hkv * (chunks of its length).
+// Division of numbers that nearly always fit 32 bits.
+__device__ __forceinline__ long long quot(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// One sequence's share of the line: (row tiles) * Hkv * (chunks of its length).
 struct SeqWork {
-    int rows, tiles, chunks;
+    int n, count, rows, chunks;
     long long total;
 };
 __device__ __forceinline__ SeqWork seq_work(const CacheArgs& a, int b, int rtile) {
     SeqWork s;
-    s.rows = cache_count(a, b) * a.G;
-    s.tiles = (s.rows + rtile - 1) / rtile;
-    s.chunks = max(1, (cache_len(a, b) + kChunk - 1) / kChunk);
-    s.total = (long long)s.tiles * a.Hkv * s.chunks;
+    s.n = cache_len(a, b);
+    s.count = cache_count(a, b);
+    s.rows = s.count * a.G;
+    s.chunks = max(1, (s.n + kChunk - 1) / kChunk);
+    s.total = (long long)((s.rows + rtile - 1) / rtile) * a.Hkv * s.chunks;
     return s;
 }
 
-// The line of chunks: piece c is [at(c), at(c + 1)).
+// The line of chunks, cut into `pieces` pieces that differ by one chunk at most.
 struct Line {
-    long long total;
-    __device__ __forceinline__ long long at(long long c, int pieces) const { return c * total / pieces; }
+    long long total, q, r;
+    int pieces;
+    __device__ __forceinline__ void set(long long t, int max_pieces) {
+        total = t;
+        pieces = (int)min((long long)max_pieces, t);
+        q = pieces ? quot(t, pieces) : 0;
+        r = t - q * pieces;
+    }
+    __device__ __forceinline__ long long at(int c) const { return c * q + min((long long)c, r); }
+    __device__ __forceinline__ int piece_of(long long x) const {
+        const long long head = r * (q + 1);
+        return (int)(x < head ? quot(x, q + 1) : r + quot(x - head, q));
+    }
 };
 
-// Block-wide: the sequence that holds chunk w of the line and the chunks before
-// that sequence. All threads call it and get the same answer; *total is set
-// when asked for (w < 0 asks for the total only).
-__device__ __forceinline__ void line_find(const CacheArgs& a, int rtile, long long w, long long* tmp, long long* total,
-                                          int* seq, long long* before) {
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    long long base = 0;
-    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-        const int b = b0 + tid;
-        const long long mine = b < a.B ? seq_work(a, b, rtile).total : 0;
-        long long x = mine;
+__device__ __forceinline__ long long warp_scan(long long x, int lane) {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        __syncthreads();  // the previous tile's tmp has been read
-        if (lane == 31) tmp[wid] = x;
-        __syncthreads();
-        long long off = base;
-        for (int i = 0; i < wid; ++i) off += tmp[i];
-        x += off;  // inclusive
-        if (w >= 0 && mine > 0 && w < x && w >= x - mine) {
-            tmp[5] = x - mine;
-            tmp[6] = b;
-        }
-        for (int i = 0; i < kThreads / 32; ++i) base += tmp[i];
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
     }
-    __syncthreads();
-    if (w < 0) {
-        *total = base;
-    } else {
-        *before = tmp[5];
-        *seq = (int)tmp[6];
+    return x;
+}
+
+// The line and, if `piece` has any of it, the sequence *b that piece starts in
+// and the chunks *before it. Each warp finds it by itself, from one load of 32
+// lengths at a time.
+__device__ __forceinline__ bool line_start(const CacheArgs& a, int rtile, int piece, int max_pieces, int lane,
+                                           Line* line, int* b, long long* before, SeqWork* sw) {
+    SeqWork mine{};
+    long long x = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+        mine.total = 0;
+        if (b0 + lane < a.B) mine = seq_work(a, b0 + lane, rtile);
+        x += mine.total;
     }
-    __syncthreads();
+    x = warp_scan(x, lane);
+    line->set(__shfl_sync(0xffffffffu, x, 31), max_pieces);
+    if (piece >= line->pieces) return false;
+    const long long w = line->at(piece);
+    long long base = 0;
+    for (int b0 = 0;; b0 += 32) {
+        if (a.B > 32) {
+            mine.total = 0;
+            if (b0 + lane < a.B) mine = seq_work(a, b0 + lane, rtile);
+            x = base + warp_scan(mine.total, lane);
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, w < x);
+        if (hit) {  // the first sequence whose share ends behind w
+            const int l = __ffs(hit) - 1;
+            *b = b0 + l;
+            *before = __shfl_sync(0xffffffffu, x - mine.total, l);
+            sw->n = __shfl_sync(0xffffffffu, mine.n, l);
+            sw->count = __shfl_sync(0xffffffffu, mine.count, l);
+            sw->rows = __shfl_sync(0xffffffffu, mine.rows, l);
+            sw->chunks = __shfl_sync(0xffffffffu, mine.chunks, l);
+            sw->total = __shfl_sync(0xffffffffu, mine.total, l);
+            return true;
+        }
+        base = __shfl_sync(0xffffffffu, x, 31);
+    }
 }
 
 // One block's part of an item.
@@ -106,15 +142,15 @@ struct Segment {
     long long start;       // the item's first chunk on the line
 };
 
-// Segment that begins at chunk w (in sequence b, `before` chunks before it) and ends
-// at w1 or at the item's end.
+// Segment that begins at chunk w (in sequence b, `before` chunks before it) and
+// ends at w1 or at the item's end.
 __device__ __forceinline__ Segment segment_at(const CacheArgs& a, int rtile, const SeqWork& s, int b, long long before,
                                               long long w, long long w1) {
     Segment g;
-    const long long rel = w - before, item = rel / s.chunks;
+    const long long rel = w - before, item = quot(rel, s.chunks);
     g.b = b;
     g.start = before + item * s.chunks;
-    const int tile = (int)(item / a.Hkv);
+    const int tile = (int)quot(item, a.Hkv);
     g.h = (int)(item - (long long)tile * a.Hkv);
     g.row0 = tile * rtile;
     g.rows = min(rtile, s.rows - g.row0);
@@ -123,6 +159,75 @@ __device__ __forceinline__ Segment segment_at(const CacheArgs& a, int rtile, con
     g.c1 = (int)min((long long)s.chunks, w1 - g.start);
     return g;
 }
+
+// A block's walk along its piece, in shared memory: registers are for the sums.
+// Thread 0 (at first its warp) moves it; begin() and next() are called by the
+// whole block and leave the next segment in `s`.
+struct Walk {
+    Line line;
+    long long w, w_begin, w_end, before;
+    SeqWork sw;
+    Segment s;
+    int b, slot;
+    bool more;
+
+    __device__ __forceinline__ void segment(const CacheArgs& a, const AttnOut& out, int piece) {
+        while (w >= before + sw.total) {  // next sequence with work
+            before += sw.total;
+            sw = seq_work(a, ++b, out.rows);
+        }
+        s = segment_at(a, out.rows, sw, b, before, w, w_end);
+        slot = 2 * piece + (w == w_begin ? 0 : 1);
+        w = s.start + s.c1;
+        if (w == w_end) note_cut(out, piece, s.c0 == 0 && s.c1 < s.chunks);
+    }
+    // The item that starts in this piece and ends behind it, if there is one.
+    __device__ __forceinline__ void note_cut(const AttnOut& out, int piece, bool cut) {
+        CutItem c{};
+        if (cut) {
+            c.b = s.b; c.h = s.h; c.row0 = s.row0; c.rows = s.rows;
+            c.slot = slot;
+            c.parts = line.piece_of(s.start + s.chunks - 1) - piece + 1;
+        }
+        out.cut[piece] = c;
+    }
+    __device__ __forceinline__ bool begin(const CacheArgs& a, const AttnOut& out, int piece) {
+        if (threadIdx.x < 32) {
+            Line l;
+            SeqWork q;
+            long long bf;
+            int sb;
+            const bool any = line_start(a, out.rows, piece, out.pieces, threadIdx.x, &l, &sb, &bf, &q);
+            if (threadIdx.x == 0) {
+                more = any;
+                if (any) {
+                    line = l; sw = q; before = bf; b = sb;
+                    w = w_begin = l.at(piece);
+                    w_end = l.at(piece + 1);
+                    segment(a, out, piece);
+                } else {
+                    note_cut(out, piece, false);
+                }
+            }
+        }
+        __syncthreads();
+        return more;
+    }
+    __device__ __forceinline__ bool next(const CacheArgs& a, const AttnOut& out, int piece) {
+        __syncthreads();  // the block is done with the segment and its shared memory
+        if (threadIdx.x == 0) {
+            more = w < w_end;
+            if (more) segment(a, out, piece);
+        }
+        __syncthreads();
+        return more;
+    }
+};
+
+// A kernel that this one's launch may be followed by can be set up meanwhile;
+// it waits for this one's end before it reads anything.
+__device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Row r of a sequence: token r / G of the call, query head h G + r % G.
 __device__ __forceinline__ long long row_offset(const CacheArgs& a, int b, int h, int r, int* t) {
@@ -206,32 +311,21 @@ k_cache_attn_simt(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restric
     using L = Grp<D>;
     constexpr int E = D / 8;  // channels of a lane
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long tmp[8];
+    allow_next();
     if (blockIdx.x == 0) {
         cache_check_call(a, false);
         return;
     }
     const int piece = blockIdx.x - 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sub = lane >> 3, ch = lane & 7;  // token of four, chunk
-    long long total, before;
-    line_find(a, R, -1, tmp, &total, nullptr, nullptr);
-    const Line line{total};
-    long long w = line.at(piece, out.pieces);
-    const long long w_begin = w, w_end = line.at(piece + 1, out.pieces);
-    if (w >= w_end) return;
-    int b;
-    line_find(a, R, w, tmp, &total, &b, &before);
-    SeqWork sw = seq_work(a, b, R);
+    __shared__ Walk walk;
+    if (!walk.begin(a, out, piece)) return;
     uint8_t* ring = smem + warp * (kSimtStages * 2 * L::kBytes);
     const uint32_t ring_addr = smem_addr(ring);
 
-    while (w < w_end) {
-        while (w >= before + sw.total) {  // next sequence with work
-            before += sw.total;
-            sw = seq_work(a, ++b, R);
-        }
-        const Segment s = segment_at(a, R, sw, b, before, w, w_end);
-        const int n = cache_len(a, b), count = cache_count(a, b);
+    do {
+        const Segment& s = walk.s;
+        const int n = walk.sw.n, count = walk.sw.count, b = s.b;
         const float kscale = a.scale * kLog2e * pow2(cache_exp(a, 0, s.h)), vscale = pow2(cache_exp(a, 1, s.h));
         float q[R][E], o[R][E], m[R], l[R];
         int lim[R];
@@ -366,7 +460,7 @@ k_cache_attn_simt(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restric
         }
         __syncthreads();
         const bool whole = s.c0 == 0 && s.c1 == s.chunks;
-        const int slot = 2 * piece + (w == w_begin ? 0 : 1);
+        const int slot = walk.slot;
         for (int x = threadIdx.x; x < s.rows * D; x += kThreads) {
             const int r = x / D, c = x - r * D;
             float mx = -INFINITY;
@@ -389,9 +483,7 @@ k_cache_attn_simt(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restric
                 if (c == 0) out.ml[(long long)slot * R + r] = make_float2(mx, sum);
             }
         }
-        __syncthreads();
-        w = s.start + s.c1;
-    }
+    } while (walk.next(a, out, piece));
 }
 
 // --------------------------------------------------------- tensor cores
@@ -445,35 +537,24 @@ k_cache_attn_mma(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_t
     using L = Grp<D>;
     constexpr int KS = D / 16, NT = D / 8, W = D / 32, RT = 16 * R, ST = mma_stages(R);
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long tmp[8];
     __shared__ float2 sml[4][RT];
     __shared__ float szf[RT];
+    allow_next();
     if (blockIdx.x == 0) {
         cache_check_call(a, false);
         return;
     }
     const int piece = blockIdx.x - 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t4 = lane & 3;
-    long long total, before;
-    line_find(a, RT, -1, tmp, &total, nullptr, nullptr);
-    const Line line{total};
-    long long w = line.at(piece, out.pieces);
-    const long long w_begin = w, w_end = line.at(piece + 1, out.pieces);
-    if (w >= w_end) return;
-    int b;
-    line_find(a, RT, w, tmp, &total, &b, &before);
-    SeqWork sw = seq_work(a, b, RT);
+    __shared__ Walk walk;
+    if (!walk.begin(a, out, piece)) return;
     uint8_t* ring = smem + warp * (ST * 2 * L::kBytes);
     const uint32_t ring_addr = smem_addr(ring);
     uint4* qs = reinterpret_cast<uint4*>(smem + mma_smem<D, R>() - (R > 1 ? R * KS * 512 : 0));
 
-    while (w < w_end) {
-        while (w >= before + sw.total) {  // next sequence with work
-            before += sw.total;
-            sw = seq_work(a, ++b, RT);
-        }
-        const Segment s = segment_at(a, RT, sw, b, before, w, w_end);
-        const int n = cache_len(a, b), count = cache_count(a, b);
+    do {
+        const Segment& s = walk.s;
+        const int n = walk.sw.n, count = walk.sw.count, b = s.b;
         // rows of a tile see more keys the later their token is
         const int low = row_limit(a, n, count, s.row0 / a.G), top = row_limit(a, n, count, (s.row0 + s.rows - 1) / a.G);
         const int steps = s.c1 - s.c0;
@@ -780,7 +861,7 @@ k_cache_attn_mma(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_t
             }
         __syncthreads();
         const bool whole = s.c0 == 0 && s.c1 == s.chunks;
-        const int slot = 2 * piece + (w == w_begin ? 0 : 1);
+        const int slot = walk.slot;
         for (int x = threadIdx.x; x < s.rows * C4; x += kThreads) {
             const int r = x / C4, c = x - r * C4;
             float2 v[4];
@@ -816,56 +897,65 @@ k_cache_attn_mma(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_t
                 if (c == 0) out.ml[(long long)slot * RT + r] = make_float2(mx, sum);
             }
         }
-        __syncthreads();
-        w = s.start + s.c1;
-    }
+    } while (walk.next(a, out, piece));
 }
 
 // ------------------------------------------------------------------ join
 
-// Block (c, y), c >= 1: if piece c's first chunk lies inside an item and is the
-// first such cut of it, joins that item's parts; each of the four warps takes a
-// row of the four rows from 4 y on. Piece c - 1 has the item's first chunk.
+// Block (c, y) joins the parts of the item that starts in piece c and ends
+// behind it, rows y, y + gridDim.y, ...: each warp adds every fourth part, a lane
+// d/32 channels of it, with several parts' loads in flight.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) k_cache_join(CacheArgs a, AttnOut out) {
-    const int R = out.rows;
-    __shared__ long long tmp[8];
-    const int c = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long total, before;
-    line_find(a, R, -1, tmp, &total, nullptr, nullptr);
-    const Line line{total};
-    const long long w = line.at(c, out.pieces), wp = line.at(c - 1, out.pieces);
-    if (w >= total) return;
-    int b;
-    line_find(a, R, w, tmp, &total, &b, &before);
-    const SeqWork sw = seq_work(a, b, R);
-    const Segment s = segment_at(a, R, sw, b, before, w, total);
-    if (s.c0 == 0 || wp > s.start) return;
-    const int r = blockIdx.y * 4 + warp;
-    if (r >= s.rows) return;
-    const long long end = s.start + s.chunks;
-    float mx = -INFINITY, sum = 0.0f, acc[D / 32];
+    constexpr int E = D / 32;
+    __shared__ float acc4[4][D];
+    wait_previous();
+    const CutItem c = out.cut[blockIdx.x];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, R = out.rows;
+    for (int r = blockIdx.y; r < c.rows; r += gridDim.y) {
+        // part p > 0 begins its piece
+        auto slot = [&](int p) { return (long long)(p == 0 ? c.slot : 2 * (blockIdx.x + p)) * R + r; };
+        float mx = -INFINITY;
+        for (int p = lane; p < c.parts; p += 32) mx = fmaxf(mx, out.ml[slot(p)].x);
+        mx = warp_max(mx);
+        const float ref = mx == -INFINITY ? 0.0f : mx;
+        float sum = 0.0f, acc[E];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) acc[i] = 0.0f;
-    for (int p = c - 1; p < out.pieces && line.at(p, out.pieces) < end; ++p) {
-        const long long wb = line.at(p, out.pieces);
-        if (wb == line.at(p + 1, out.pieces)) continue;  // an empty piece
-        const long long at = (2LL * p + (wb >= s.start ? 0 : 1)) * R + r;
-        const float2 ml = out.ml[at];
-        const float mn = fmaxf(mx, ml.x), ref = mn == -INFINITY ? 0.0f : mn;
-        const float f = exp2f(mx - ref), fp = exp2f(ml.x - ref);
-        mx = mn;
-        sum = sum * f + ml.y * fp;
+        for (int i = 0; i < E; ++i) acc[i] = 0.0f;
+#pragma unroll 8
+        for (int p = warp; p < c.parts; p += 4) {
+            const long long at = slot(p);
+            const float2 ml = out.ml[at];
+            const float f = exp2f(ml.x - ref);
+            sum = fmaf(f, ml.y, sum);
+            float v[E];
+            if (E == 4) {
+                const float4 u = reinterpret_cast<const float4*>(out.part + at * D)[lane];
+                v[0] = u.x; v[1] = u.y; v[E - 2] = u.z; v[E - 1] = u.w;
+            } else {
+                const float2 u = reinterpret_cast<const float2*>(out.part + at * D)[lane];
+                v[0] = u.x; v[1] = u.y;
+            }
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) acc[i] = acc[i] * f + out.part[at * D + lane * (D / 32) + i] * fp;
+            for (int i = 0; i < E; ++i) acc[i] = fmaf(f, v[i], acc[i]);
+        }
+        __shared__ float sum4[4];
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc4[warp][lane * E + i] = acc[i];
+        if (lane == 0) sum4[warp] = sum;
+        __syncthreads();
+        sum = (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
+        int t;
+        const long long at = row_offset(a, c.b, c.h, c.row0 + r, &t);
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        if (threadIdx.x < D) {
+            const int i = threadIdx.x;
+            const float v = (acc4[0][i] + acc4[1][i]) + (acc4[2][i] + acc4[3][i]);
+            reinterpret_cast<T*>(out.O)[at * D + i] = from_f<T>(sum == 0.0f ? 0.0f : v * inv);
+        }
+        if (out.lse && threadIdx.x == 0) out.lse[at] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+        __syncthreads();
     }
-    int t;
-    const long long at = row_offset(a, b, s.h, s.row0 + r, &t);
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-        reinterpret_cast<T*>(out.O)[at * D + lane * (D / 32) + i] = from_f<T>(sum == 0.0f ? 0.0f : acc[i] * inv);
-    if (out.lse && lane == 0) out.lse[at] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
 // ------------------------------------------------------------------ launch
@@ -898,9 +988,18 @@ static cudaError_t join_t(const CacheArgs& a, const AttnOut& o, cudaStream_t st)
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || o.pieces == 1) return e;
     prof_mark(st, "cache_join");
-    k_cache_join<T, D><<<dim3(o.pieces - 1, (o.rows + 3) / 4), kThreads, 0, st>>>(a, o);
-    count_launch();
-    return cudaGetLastError();
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(o.pieces, (o.rows + 3) / 4);
+    c.blockDim = dim3(kThreads);
+    c.stream = st;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    e = cudaLaunchKernelEx(&c, k_cache_join<T, D>, a, o);
+    if (e == cudaSuccess) count_launch();
+    return e;
 }
 
 template <typename T, int D, int R>
@@ -932,8 +1031,8 @@ static cudaError_t attn_t(const CacheArgs& a, const CachePlan& p, int dtype, con
 }
 
 cudaError_t launch_cache_attn(const CacheArgs& a, const CachePlan& p, int d, int dtype, const void* Q,
-                              const void* cache, void* O, float* lse, float* part, float2* ml, cudaStream_t st) {
-    const AttnOut o{O, lse, part, ml, p.pieces, p.rows};
+                              const void* cache, void* O, float* lse, const CacheParts& parts, cudaStream_t st) {
+    const AttnOut o{O, lse, parts.part, parts.ml, (CutItem*)parts.cut, p.pieces, p.rows};
     const uint8_t* c = (const uint8_t*)cache;
     prof_mark(st, "cache_attention");
     return d == 64 ? attn_t<64>(a, p, dtype, Q, c, o, st) : attn_t<128>(a, p, dtype, Q, c, o, st);
