@@ -311,53 +311,70 @@ def cache_workspace(p: CacheParams, device="cuda"):
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _check_cache(p: CacheParams, rows, cache, table, lens, counts, exps, ws, lse=None):
-    """The tensors of a cache call against ``p``: the C ABI sees only pointers."""
+def _need(name, t, shape, dtype, dev):
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s" % (name, dtype, shape))
+    if t.get_device() != dev:
+        raise ValueError("%s must be on the cache's CUDA device" % name)
+
+
+def _cache_call(fn, p: CacheParams, names, rows, heads, order, cache, table, lens, counts, exps, ws, lse, stream):
+    """One cache call. The C ABI sees only pointers, so the tensors are held to
+    ``p`` here. ``rows``: the call's two row tensors; ``order`` puts the arguments
+    in the C function's order. Kept short: a decoding step makes these calls for
+    every layer."""
     import torch
-    dt = {F32: torch.float32, BF16: torch.bfloat16}.get(p.dtype)
-    wanted = [(n, t, s, dt) for n, t, s in rows]
-    wanted += [("table", table, (p.B, p.max_pages), torch.int32), ("lens", lens, (p.B,), torch.int32)]
-    wanted += [(n, t, s, x) for n, t, s, x in (("counts", counts, (p.B,), torch.int32),
-                                               ("exps", exps, (2, p.H_kv), torch.int32),
-                                               ("lse_out", lse, (p.B, p.H, p.T), torch.float32)) if t is not None]
-    for name, t, shape, dtype in wanted:
-        if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
-            raise ValueError("%s must be a contiguous %s tensor of shape %s" % (name, dtype, shape))
-    for name, t in (("cache", cache), ("ws", ws)):
-        if t.dtype != torch.uint8 or not t.is_contiguous():
-            raise ValueError("%s must be a contiguous uint8 tensor" % name)
-    if cache.numel() < mita_cache_size(p):
-        raise ValueError("cache holds %d bytes, the pool needs %d" % (cache.numel(), mita_cache_size(p)))
-    for name, t in [(n, t) for n, t, _, _ in wanted] + [("cache", cache), ("ws", ws)]:
-        if not t.is_cuda or t.device != cache.device:
-            raise ValueError("%s must be on the cache's CUDA device" % name)
-    return cache.device
+    i32, u8, dev = torch.int32, torch.uint8, cache.get_device()
+    dt = torch.bfloat16 if p.dtype == BF16 else torch.float32
+    shape = (p.B, heads, p.T, p.d)
+    _need(names[0], rows[0], shape, dt, dev)
+    _need(names[1], rows[1], shape, dt, dev)
+    _need("table", table, (p.B, p.max_pages), i32, dev)
+    _need("lens", lens, (p.B,), i32, dev)
+    if counts is not None:
+        _need("counts", counts, (p.B,), i32, dev)
+    if exps is not None:
+        _need("exps", exps, (2, p.H_kv), i32, dev)
+    if lse is not None:
+        _need("lse_out", lse, (p.B, p.H, p.T), torch.float32, dev)
+    _need("cache", cache, (cache.numel(),), u8, dev)
+    _need("ws", ws, (ws.numel(),), u8, dev)
+    size = p.n_pages * p.H_kv * p.page * 9 * p.d // 8  # mita_cache_size
+    if cache.numel() < size:
+        raise ValueError("cache holds %d bytes, the pool needs %d" % (cache.numel(), size))
+    if dev < 0:
+        raise ValueError("cache must be on a CUDA device")
+    args = order(rows[0].data_ptr(), rows[1].data_ptr(), cache.data_ptr(),
+                 (table.data_ptr(), lens.data_ptr(), None if counts is None else counts.data_ptr(),
+                  None if exps is None else exps.data_ptr()))
+    if fn == "mita_cache_attention":
+        args += (None if lse is None else lse.data_ptr(),)
+    if stream is None:
+        st = torch.cuda.current_stream(dev).cuda_stream
+    else:
+        st = stream if isinstance(stream, int) else stream.cuda_stream
+    call = getattr(lib(), fn)
+    if torch.cuda.current_device() == dev:
+        _check(call(ctypes.byref(p.c()), *args, ws.data_ptr(), ws.numel(), st))
+    else:
+        with torch.cuda.device(dev):
+            _check(call(ctypes.byref(p.c()), *args, ws.data_ptr(), ws.numel(), st))
 
 
 def mita_cache_write(p: CacheParams, K, V, cache, table, lens, ws, counts=None, exps=None, stream=None):
     """Stores the rows K, V [B, H_kv, T, d] in the pages that ``table`` names."""
-    import torch
-    s = (p.B, p.H_kv, p.T, p.d)
-    with torch.cuda.device(_check_cache(p, (("K", K, s), ("V", V, s)), cache, table, lens, counts, exps, ws)):
-        _check(lib().mita_cache_write(ctypes.byref(p.c()), _ptr(K), _ptr(V), _ptr(cache), _ptr(table), _ptr(lens),
-                                      _ptr(counts), _ptr(exps), _ptr(ws), ws.numel(), _stream(stream)))
+    _cache_call("mita_cache_write", p, ("K", "V"), (K, V), p.H_kv, lambda k, v, c, idx: (k, v, c) + idx, cache, table,
+                lens, counts, exps, ws, None, stream)
 
 
 def mita_cache_read(p: CacheParams, cache, table, lens, K, V, ws, counts=None, exps=None, stream=None):
     """Reads rows back into K, V [B, H_kv, T, d]; padding rows stay as they are."""
-    import torch
-    s = (p.B, p.H_kv, p.T, p.d)
-    with torch.cuda.device(_check_cache(p, (("K", K, s), ("V", V, s)), cache, table, lens, counts, exps, ws)):
-        _check(lib().mita_cache_read(ctypes.byref(p.c()), _ptr(cache), _ptr(table), _ptr(lens), _ptr(counts),
-                                     _ptr(exps), _ptr(K), _ptr(V), _ptr(ws), ws.numel(), _stream(stream)))
+    _cache_call("mita_cache_read", p, ("K", "V"), (K, V), p.H_kv, lambda k, v, c, idx: (c,) + idx + (k, v), cache,
+                table, lens, counts, exps, ws, None, stream)
 
 
 def mita_cache_attention(p: CacheParams, Q, cache, table, lens, O, ws, counts=None, exps=None, lse_out=None,
                          stream=None):
     """Attention of the rows Q [B, H, T, d] over the cache, into O (and lse_out)."""
-    import torch
-    s = (p.B, p.H, p.T, p.d)
-    with torch.cuda.device(_check_cache(p, (("Q", Q, s), ("O", O, s)), cache, table, lens, counts, exps, ws, lse_out)):
-        _check(lib().mita_cache_attention(ctypes.byref(p.c()), _ptr(Q), _ptr(cache), _ptr(table), _ptr(lens),
-                                          _ptr(counts), _ptr(exps), _ptr(O), _ptr(lse_out), _ptr(ws), ws.numel(),
-                                          _stream(stream)))
+    _cache_call("mita_cache_attention", p, ("Q", "O"), (Q, O), p.H, lambda q, o, c, idx: (q, c) + idx + (o,), cache,
+                table, lens, counts, exps, ws, lse_out, stream)

@@ -65,49 +65,66 @@ template <typename T> struct Raw {
     }
 };
 
-// y / s for the code grid, s an e4m3 number. Its rounding must not move a
-// quotient onto or off a midpoint M of the grid {1/4, 3/4, 5/4, 7/4, 5/2, 7/2, 5}.
-//   float32: the correctly rounded quotient. It equals M only if y = M s: M s is a float
-//   (3 and 4 significant bits), the next float is 2^-23 / f away relative to it, f in [1, 2)
-//   its significand, and half a step of the quotient is 2^-24 / h, h in [1, 2) that of M.
-//   (Below a power of two the spacing of floats halves; M s is one only where M is one
-//   too, and then half a step of the quotient halves as well.)
-//   bf16: y has 8 significant bits and M s has 7, so y is M s or at least 2^-8 of it
-//   away. y * (1 / s) is within 2^-23 of the quotient, relative: adding and
-//   subtracting 48 rounds it to a multiple of 2^-18, which is M itself in the
-//   first case and on the quotient's side of M in the second. Three operations
-//   per element instead of a division.
-template <typename T> __device__ __forceinline__ float code_quotient(float y, float s, float rs) {
-    if (sizeof(T) == 4) return __fdiv_rn(y, s);
-    return __fadd_rn(__fadd_rn(__fmul_rn(y, rs), 48.0f), -48.0f);
+// Largest magnitude of a block, NaN if it has one.
+__device__ __forceinline__ float block_amax(const Raw<float>& x) {
+    uint32_t m = 0;  // as bits: NaN > infinity > every number
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = max(m, x.r[i] & 0x7fffffffu);
+    return __uint_as_float(m);
+}
+__device__ __forceinline__ float block_amax(const Raw<__nv_bfloat16>& x) {
+    uint32_t m = x.r[0] & 0x7fff7fffu;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(x.r[i] & 0x7fff7fffu));
+    uint16_t lo = (uint16_t)m, hi = (uint16_t)(m >> 16);
+    asm("max.NaN.bf16 %0, %0, %1;" : "+h"(lo) : "h"(hi));
+    return __uint_as_float((uint32_t)lo << 16);
 }
 
-// A block (times 2^-e) -> 16 codes and the scale byte, s = RN_e4m3(amax / 6),
+// x * up / s for the code grid: up a power of two, s an e4m3 number, rs = up / s
+// rounded. The rounding must not move a quotient onto or off a midpoint M of the
+// grid {1/4, 3/4, 5/4, 7/4, 5/2, 7/2, 5}.
+//   float32: the correctly rounded quotient. It equals M only if y = x up is M s: M s is a
+//   float (3 and 4 significant bits), the next float is 2^-23 / f away relative to it, f in
+//   [1, 2) its significand, and half a step of the quotient is 2^-24 / h, h in [1, 2) that
+//   of M. (Below a power of two the spacing of floats halves; M s is one only where M is
+//   one too, and then half a step of the quotient halves as well.)
+//   bf16: y has 8 significant bits and M s has 7, so y is M s or at least 2^-8 of it
+//   away. x rs is within 2^-24 of the quotient, relative: adding and subtracting
+//   48 rounds it to a multiple of 2^-18, which is M itself in the first case and
+//   on the quotient's side of M in the second. Two operations per element instead
+//   of a division.
+template <typename T> __device__ __forceinline__ float code_quotient(float x, float up, float s, float rs) {
+    if (sizeof(T) == 4) return __fdiv_rn(x * up, s);
+    return __fadd_rn(__fmaf_rn(x, rs, 48.0f), -48.0f);
+}
+
+// A block (times up = 2^-e) -> 16 codes and the scale byte, s = RN_e4m3(amax / 6),
 // code = RN_e2m1(y / s). For s too the fp32 quotient is a midpoint of the grid
 // (5 significant bits, the divisor 2) only if the exact one is.
 template <typename T>
 __device__ __forceinline__ void quantise16(const Raw<T>& x, float up, uint32_t* codes, uint32_t* scale) {
-    uint32_t amax = 0;  // as bits: NaN > infinity > every number
-#pragma unroll
-    for (int i = 0; i < 16; ++i) amax = max(amax, __float_as_uint(x.get(i)) & 0x7fffffffu);
+    const float amax = block_amax(x);
     codes[0] = codes[1] = 0;
-    if (amax > 0x7f800000u) {  // a NaN stays visible: the whole block reads as NaN
-        *scale = 0x7f;
-        return;
-    }
-    const float raw = __fdiv_rn(__uint_as_float(amax) * up, 6.0f);
+    *scale = 0x7f;
+    if (amax != amax) return;  // a NaN stays visible: the whole block reads as NaN
+    const float raw = __fdiv_rn(amax * up, 6.0f);
     uint16_t sb;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(sb) : "f"(0.0f), "f"(raw));
     *scale = sb & 0xff;
     if ((sb & 0xff) == 0) return;
-    const float s = half2_to_float2(e4m3x2_to_half2(sb)).x, rs = __frcp_rn(s);
+    const float s = half2_to_float2(e4m3x2_to_half2(sb)).x, rs = __frcp_rn(s) * up;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        uint32_t b;
-        asm("{.reg .b8 t; .reg .b16 u; cvt.rn.satfinite.e2m1x2.f32 t, %1, %2; mov.b16 u, {t, 0}; cvt.u32.u16 %0, u;}"
-            : "=r"(b)
-            : "f"(code_quotient<T>(x.get(2 * i + 1) * up, s, rs)), "f"(code_quotient<T>(x.get(2 * i) * up, s, rs)));
-        codes[i >> 2] |= b << (8 * (i & 3));
+    for (int w = 0; w < 2; ++w) {
+        float q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = code_quotient<T>(x.get(8 * w + i), up, s, rs);
+        asm("{.reg .b8 a, b, c, d;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1; cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5; cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+            "mov.b32 %0, {a, b, c, d};}"
+            : "=r"(codes[w])
+            : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
     }
 }
 

@@ -24,6 +24,7 @@
 #include <algorithm>
 
 #include "cache.cuh"
+#include "tc.cuh"
 
 namespace mita {
 
@@ -199,14 +200,13 @@ struct Walk {
             int sb;
             const bool any = line_start(a, out.rows, piece, out.pieces, threadIdx.x, &l, &sb, &bf, &q);
             if (threadIdx.x == 0) {
+                note_cut(out, piece, false);
                 more = any;
                 if (any) {
                     line = l; sw = q; before = bf; b = sb;
                     w = w_begin = l.at(piece);
                     w_end = l.at(piece + 1);
                     segment(a, out, piece);
-                } else {
-                    note_cut(out, piece, false);
                 }
             }
         }
@@ -488,32 +488,51 @@ k_cache_attn_simt(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restric
 
 // --------------------------------------------------------- tensor cores
 
-__device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+// 8 x 8 halves, lane (g, t) holding row g, columns 2 t and 2 t + 1: transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
-
-constexpr int mma_stages(int R) { return R == 1 ? 3 : 4; }
-
-template <int D, int R> constexpr int mma_smem() {
-    constexpr int ring = 4 * mma_stages(R) * 2 * Grp<D>::kBytes, merge = 4 * 16 * R * D * 4;
-    return (ring > merge ? ring : merge) + (R > 1 ? R * (D / 16) * 512 : 0);
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// One group of a step: a bulk copy that `bar` counts, or nothing.
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(smem_addr(bar))
+                 : "memory");
 }
 
-// bf16 rows on the tensor cores' register form (m16n8k16, halves in, fp32 out).
+constexpr float kNoKey = -1.7e38f;  // a row's maximum before it has seen a key: finite, so that differences are
+
+constexpr int kStages = 2;
+// Blocks per SM that the registers allow without spills. (16 rows of 128 channels: 3 blocks 48.6 us,
+// 4 at 128 registers 51.2; 16 rows of 64: 33.0 and 30.9.)
+constexpr int mma_blocks(int d, int NR) { return NR == 1 ? 4 : d == 64 ? (NR == 2 ? 4 : 3) : (NR == 2 ? 3 : 2); }
+
+template <int D, int NR> constexpr int mma_smem() {
+    constexpr int ring = 4 * kStages * 2 * Grp<D>::kBytes, merge = 4 * 8 * NR * D * 4;
+    return (ring > merge ? ring : merge) + NR * (D / 16) * 256;
+}
+
+// bf16 rows on the tensor cores' register form (m16n8k16, halves in, fp32 out),
+// tiles of 8 NR rows.
 //
 // The codes come from shared memory into the registers of the lanes that feed
 // them to the step, are widened there and never go back to shared memory: one
@@ -522,23 +541,32 @@ template <int D, int R> constexpr int mma_smem() {
 // cached bytes written and read again, for tiles of 128 rows of which decoding
 // fills 1 to 64.)
 //
+// Tokens and value channels are the 16 side of a step and query rows the 8 side
+// (S^T = K Q^T, O^T = V^T P^T): decoding has few rows, and with rows on the 16 side
+// half of the steps and exponentials would be for rows that are not there.
+//
 // A warp takes 32 tokens at a time, each warp its own, with its own maximum and
-// sums, so nothing but a segment's end joins the block. Per 32 tokens and 16 rows:
-//   S = Q K^T   4 token tiles x d/16 steps. Q's rows are scaled by a power of two that puts
-//               their largest entry in [2^14, 2^15), so that bf16 is exact as halves down to
-//               2^-31 of it; the power goes into the factor of the scores.
+// sums, so nothing but a segment's end joins the block:
+//   S^T   2 token tiles x d/16 steps. Q's rows are scaled by a power of two that puts their
+//         largest entry in [2^14, 2^15), so that bf16 is exact as halves down to 2^-31 of
+//         it; the power goes into the factor f of the scores.
 //   p = 2^(S f - m) in fp32, rounded to halves for the product with V (2^-11 relative; the sum
-//               l takes the unrounded p). m is only moved when a row's maximum exceeds it by
-//               more than 8, so p <= 2^8 and the sums are rarely rescaled.
-//   O += P V    2 steps of 16 tokens x d/8 channel tiles. The layout of P in registers is that of S.
-template <int D, int R>
-__global__ void __launch_bounds__(kThreads, R == 1 ? 3 : 2)
+//         l takes the unrounded p). m is only moved when a score exceeds it by more than 8,
+//         so p <= 2^8, and only then do lanes compare maxima and are the sums rescaled.
+//   O^T   P^T is S^T's register layout transposed 8 x 8; 2 steps of 16 tokens x d/16 channel tiles.
+template <int D, int NR>
+__global__ void __launch_bounds__(kThreads, mma_blocks(D, NR))
 k_cache_attn_mma(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_t* __restrict__ cache, AttnOut out) {
     using L = Grp<D>;
-    constexpr int KS = D / 16, NT = D / 8, W = D / 32, RT = 16 * R, ST = mma_stages(R);
+    constexpr int KS = D / 16, NT = D / 8, W = D / 32, RT = 8 * NR, ST = kStages;
+    constexpr int GP = NR == 1 ? 2 : 1;  // groups at a time: with more rows the registers hold one
+    constexpr int kStage = 2 * L::kBytes;
     extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ Walk walk;
     __shared__ float2 sml[4][RT];
     __shared__ float szf[RT];
+    __shared__ int slim[RT];
+    __shared__ uint64_t bars[4][ST];
     allow_next();
     if (blockIdx.x == 0) {
         cache_check_call(a, false);
@@ -546,11 +574,16 @@ k_cache_attn_mma(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_t
     }
     const int piece = blockIdx.x - 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t4 = lane & 3;
-    __shared__ Walk walk;
-    if (!walk.begin(a, out, piece)) return;
-    uint8_t* ring = smem + warp * (ST * 2 * L::kBytes);
+    uint8_t* ring = smem + warp * (ST * kStage);
     const uint32_t ring_addr = smem_addr(ring);
-    uint4* qs = reinterpret_cast<uint4*>(smem + mma_smem<D, R>() - (R > 1 ? R * KS * 512 : 0));
+    uint2* qs = reinterpret_cast<uint2*>(smem + mma_smem<D, NR>() - NR * KS * 256);
+    if (lane == 0) {
+        for (int i = 0; i < ST; ++i) tc::mbar_init(&bars[warp][i], 2);
+        tc::fence_mbar_init();
+    }
+    if (!walk.begin(a, out, piece)) return;
+    int put = 0, take = 0, phase = 0;  // stages of the ring, and the phase of `take`
+    bool dead = false;                 // a wait ran out
 
     do {
         const Segment& s = walk.s;
@@ -558,306 +591,327 @@ k_cache_attn_mma(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_t
         // rows of a tile see more keys the later their token is
         const int low = row_limit(a, n, count, s.row0 / a.G), top = row_limit(a, n, count, (s.row0 + s.rows - 1) / a.G);
         const int steps = s.c1 - s.c0;
-        GroupRun gr;
-        gr.begin(a, s, top, warp, lane);
-#pragma unroll
-        for (int i = 0; i < ST - 1; ++i) {
-            const int g0 = gr.get(i, 0), g1 = gr.get(i, 1);
-            if (i < steps) stage_step<D>(cache, ring_addr + i * 2 * L::kBytes, g0, g1, lane); else copy_commit();
-        }
-        // Q: lane (g, t4) has rows g and g + 8 in channels [t4 d/4, (t4 + 1) d/4)
-        const float kf = a.scale * kLog2e * pow2(cache_exp(a, 0, s.h)), vscale = pow2(cache_exp(a, 1, s.h));
-        uint32_t qf[R == 1 ? KS : 1][4];
-        float zf[R][2];
-        int lim[R][2];
-#pragma unroll
-        for (int mt = 0; mt < R; ++mt) {
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int r = mt * 16 + hf * 8 + g;
-                int t = 0;
-                const long long at = row_offset(a, b, s.h, s.row0 + min(r, s.rows - 1), &t);
-                lim[mt][hf] = r < s.rows ? row_limit(a, n, count, t) : 0;
-                if (R > 1 && warp != mt) continue;
-                uint4 q4[D / 32];
-                uint32_t amax = 0;
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    q4[i] = make_uint4(0, 0, 0, 0);
-                    if (r < s.rows) q4[i] = reinterpret_cast<const uint4*>(Q + at * D + t4 * (D / 4))[i];
-                    const uint32_t x[4] = {q4[i].x, q4[i].y, q4[i].z, q4[i].w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) amax = max(amax, max(x[j] & 0x7fffu, (x[j] >> 16) & 0x7fffu));
-                }
-                amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                const int ex = (int)(amax >> 7);  // biased exponent of the row's largest entry
-                const int qe = ex == 255 ? 0 : min(141 - ex, 120);
-                const float up = pow2(qe);
-                // kept away from 0 and infinity: a masked score is -infinity times it
-                const float f = fminf(fmaxf(kf * pow2(-qe), 1.1754944e-38f), 3.4028235e38f);
-                if (R == 1) zf[mt][hf] = f;
-                else if (t4 == 0) szf[r] = f;
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    const uint32_t x[4] = {q4[i].x, q4[i].y, q4[i].z, q4[i].w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t h = pack_half2(__uint_as_float(x[j] << 16) * up, __uint_as_float(x[j] & 0xffff0000u) * up);
-                        const int ks = 2 * i + (j >> 1), e = hf + 2 * (j & 1);
-                        if (R == 1) qf[ks][e] = h;
-                        else reinterpret_cast<uint32_t*>(qs + (mt * KS + ks) * 32 + lane)[e] = h;
-                    }
+        // Lane l has the group number of group l & 1 of step l >> 1 in the current run of 16
+        // steps, and issues that copy itself; the next run's table entries are loaded a run ahead.
+        auto groups = [&](int i0) -> const uint8_t* {
+            const int gi = GroupRun::load(a, s, top, warp, lane, i0);
+            return gi < 0 ? nullptr : cache + (long long)gi * L::kBytes;
+        };
+        const uint8_t *gcur = groups(0), *gnxt = groups(16);
+        auto issue = [&](int i) {
+            if (i < steps && (lane >> 1) == (i & 15)) {
+                uint64_t* bar = &bars[warp][put];
+                if (gcur) {
+                    tc::mbar_expect_tx(bar, L::kBytes);
+                    bulk_copy(ring_addr + put * kStage + (lane & 1) * L::kBytes, gcur, L::kBytes, bar);
+                } else {
+                    tc::mbar_arrive(bar);
                 }
             }
+            if (i < steps) put = put + 1 == ST ? 0 : put + 1;
+            if ((i & 15) == 15) {
+                gcur = gnxt;
+                gnxt = groups(i + 17);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < ST - 1; ++i) issue(i);
+
+        // Q: warp w has rows 8 w + g, lane (g, t4) channels [t4 d/4, (t4 + 1) d/4) of them
+        const float vscale = pow2(cache_exp(a, 1, s.h));
+        if (warp < NR) {
+            const int r = warp * 8 + g;
+            int t = 0;
+            const long long at = row_offset(a, b, s.h, s.row0 + min(r, s.rows - 1), &t);
+            uint32_t x[D / 8], amax = 0;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (r < s.rows) v = reinterpret_cast<const uint4*>(Q + at * D + t4 * (D / 4))[i];
+                x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+            }
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) amax = max(amax, max(x[i] & 0x7fffu, (x[i] >> 16) & 0x7fffu));
+            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            const int ex = (int)(amax >> 7);  // biased exponent of the row's largest entry
+            const int qe = ex == 255 ? 0 : min(141 - ex, 120);
+            const float up = pow2(qe), kf = a.scale * kLog2e * pow2(cache_exp(a, 0, s.h));
+            if (t4 == 0) {
+                // kept away from 0 and infinity: a masked score is -infinity times it
+                szf[r] = fminf(fmaxf(kf * pow2(-qe), 1.1754944e-38f), 3.4028235e38f);
+                slim[r] = r < s.rows ? row_limit(a, n, count, t) : 0;
+            }
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                uint32_t h[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t y = x[2 * ks + e];
+                    h[e] = pack_half2(__uint_as_float(y << 16) * up, __uint_as_float(y & 0xffff0000u) * up);
+                }
+                qs[(ks * NR + warp) * 32 + lane] = make_uint2(h[0], h[1]);
+            }
         }
-        if (R > 1) {
-            __syncthreads();
+        __syncthreads();
+        uint2 qf[NR == 1 ? KS : 1];
+        if (NR == 1) {
 #pragma unroll
-            for (int mt = 0; mt < R; ++mt)
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) zf[mt][hf] = szf[mt * 16 + hf * 8 + g];
+            for (int ks = 0; ks < KS; ++ks) qf[ks] = qs[ks * 32 + lane];
         }
-        float o[R][NT][4], m[R][2], l[R][2];
+        // of this lane's rows 8 i + 2 t4 and the next
+        float zf[NR][2], m[NR][2], l[NR][2], o[NR][NT / 2][4];
 #pragma unroll
-        for (int mt = 0; mt < R; ++mt) {
-            m[mt][0] = m[mt][1] = -INFINITY;
-            l[mt][0] = l[mt][1] = 0.0f;
+        for (int i = 0; i < NR; ++i) {
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
+            for (int e = 0; e < 2; ++e) {
+                zf[i][e] = szf[8 * i + 2 * t4 + e];
+                m[i][e] = kNoKey;
+                l[i][e] = 0.0f;
+            }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[mt][i][e] = 0.0f;
+            for (int j = 0; j < NT / 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][j][e] = 0.0f;
         }
 
         for (int i = 0; i < steps; ++i) {
-            const int nx = i + ST - 1;
-            const int g0 = gr.get(nx, 0), g1 = gr.get(nx, 1);
-            __syncwarp();
-            if (nx < steps) stage_step<D>(cache, ring_addr + (nx % ST) * 2 * L::kBytes, g0, g1, lane); else copy_commit();
-            gr.advance(a, s, top, warp, lane, nx);
-            copy_wait<ST - 1>();
-            __syncwarp();
-            const int base = (s.c0 + i) * kChunk + warp * kStep;
-            if (base >= top) continue;
-            const uint8_t* st = ring + (i % ST) * 2 * L::kBytes;
-
-            float z[R][4][4];
-#pragma unroll
-            for (int mt = 0; mt < R; ++mt)
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) z[mt][x][e] = 0.0f;
-#pragma unroll
-            for (int gi = 0; gi < 2; ++gi) {
-                const uint8_t* kb = st + gi * L::kBytes;
-                uint32_t kw[2][W], sc[2][D / 64];  // codes; scales, each in both halves
-                if (D == 128) {
-                    const uint32_t sb = *reinterpret_cast<const uint32_t*>(kb + L::kKs + g * 16 + t4 * 4);
-                    const uint32_t s0 = e4m3x2_to_half2(sb & 0xffff), s1 = e4m3x2_to_half2(sb >> 16);
-                    sc[0][0] = __byte_perm(s0, s0, 0x1010);
-                    sc[0][D / 64 - 1] = __byte_perm(s0, s0, 0x3232);
-                    sc[1][0] = __byte_perm(s1, s1, 0x1010);
-                    sc[1][D / 64 - 1] = __byte_perm(s1, s1, 0x3232);
-                } else {
-                    const uint32_t s0 = e4m3x2_to_half2(*reinterpret_cast<const uint16_t*>(kb + L::kKs + g * 8 + t4 * 2));
-                    sc[0][0] = __byte_perm(s0, s0, 0x1010);
-                    sc[1][0] = __byte_perm(s0, s0, 0x3232);
+            __syncwarp();  // the stage that the next copy goes to has been read
+            issue(i + ST - 1);
+            if (!tc::mbar_wait(&bars[warp][take], phase, a.status)) {
+                // give up, but not before the copies in flight have landed (or a second has passed for each)
+                for (int x = i + 1; x < steps && x < i + ST; ++x) {
+                    take = take + 1 == ST ? 0 : take + 1;
+                    phase ^= take == 0;
+                    tc::mbar_wait(&bars[warp][take], phase, a.status);
                 }
+                dead = true;
+                break;
+            }
+            const uint8_t* st = ring + take * kStage;
+            take = take + 1 == ST ? 0 : take + 1;
+            phase ^= take == 0;
+#pragma unroll 1
+            for (int h = 0; h < 2; h += GP) {
+                const int base = (s.c0 + i) * kChunk + warp * kStep + 16 * h;
+                if (base >= top) break;
+
+                // scores of 16 tokens each: [0], [1] token g, rows 2 t4 and the next; [2], [3] token g + 8
+                float z[NR][GP][4];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const uint8_t* kr = kb + (8 * x + g) * L::kRow + t4 * (D / 8);
+                for (int j = 0; j < NR; ++j)
+#pragma unroll
+                    for (int x = 0; x < GP; ++x)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) z[j][x][e] = 0.0f;
+                uint32_t kw[GP][2][W], sc[GP][2][D / 64];  // [group][token g, g + 8]: codes; scales, each in both halves
+#pragma unroll
+                for (int gi = 0; gi < GP; ++gi) {
+                    const uint8_t* kb = st + (h + gi) * L::kBytes;
                     if (D == 128) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(kr);
-                        kw[x][0] = v.x; kw[x][1] = v.y; kw[x][W - 2] = v.z; kw[x][W - 1] = v.w;
+                        const uint32_t sb = *reinterpret_cast<const uint32_t*>(kb + L::kKs + g * 16 + t4 * 4);
+                        const uint32_t s0 = e4m3x2_to_half2(sb & 0xffff), s1 = e4m3x2_to_half2(sb >> 16);
+                        sc[gi][0][0] = __byte_perm(s0, s0, 0x1010);
+                        sc[gi][0][D / 64 - 1] = __byte_perm(s0, s0, 0x3232);
+                        sc[gi][1][0] = __byte_perm(s1, s1, 0x1010);
+                        sc[gi][1][D / 64 - 1] = __byte_perm(s1, s1, 0x3232);
                     } else {
-                        const uint2 v = *reinterpret_cast<const uint2*>(kr);
-                        kw[x][0] = v.x; kw[x][1] = v.y;
+                        const uint32_t s0 = e4m3x2_to_half2(*reinterpret_cast<const uint16_t*>(kb + L::kKs + g * 8 + t4 * 2));
+                        sc[gi][0][0] = __byte_perm(s0, s0, 0x1010);
+                        sc[gi][1][0] = __byte_perm(s0, s0, 0x3232);
+                    }
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint8_t* kr = kb + (8 * x + g) * L::kRow + t4 * (D / 8);
+                        if (D == 128) {
+                            const uint4 v = *reinterpret_cast<const uint4*>(kr);
+                            kw[gi][x][0] = v.x; kw[gi][x][1] = v.y; kw[gi][x][W - 2] = v.z; kw[gi][x][W - 1] = v.w;
+                        } else {
+                            const uint2 v = *reinterpret_cast<const uint2*>(kr);
+                            kw[gi][x][0] = v.x; kw[gi][x][1] = v.y;
+                        }
                     }
                 }
 #pragma unroll
                 for (int wi = 0; wi < W; ++wi) {
-                    uint32_t k8[2][4];
+                    uint32_t k8[GP][2][4];
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        e2m1x8_to_half2(kw[x][wi], k8[x]);
+                    for (int gi = 0; gi < GP; ++gi)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) k8[x][j] = hmul2(k8[x][j], sc[x][wi >> 1]);
-                    }
+                        for (int x = 0; x < 2; ++x) {
+                            e2m1x8_to_half2(kw[gi][x][wi], k8[gi][x]);
 #pragma unroll
-                    for (int mt = 0; mt < R; ++mt)
+                            for (int j = 0; j < 4; ++j) k8[gi][x][j] = hmul2(k8[gi][x][j], sc[gi][x][wi >> 1]);
+                        }
 #pragma unroll
-                        for (int ks = 0; ks < 2; ++ks) {
-                            uint32_t qa[4];
-                            if (R == 1) {
+                    for (int k2 = 0; k2 < 2; ++k2)
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) qa[e] = qf[2 * wi + ks][e];
-                            } else {
-                                const uint4 v = qs[(mt * KS + 2 * wi + ks) * 32 + lane];
-                                qa[0] = v.x; qa[1] = v.y; qa[2] = v.z; qa[3] = v.w;
-                            }
+                        for (int j = 0; j < NR; ++j) {
+                            const uint2 q = NR == 1 ? qf[(2 * wi + k2) % (NR == 1 ? KS : 1)] : qs[((2 * wi + k2) * NR + j) * 32 + lane];
 #pragma unroll
-                            for (int x = 0; x < 2; ++x)
-                                mma_f16(z[mt][2 * gi + x], qa, k8[x][2 * ks], k8[x][2 * ks + 1]);
+                            for (int gi = 0; gi < GP; ++gi)
+                                mma_f16(z[j][gi], k8[gi][0][2 * k2], k8[gi][1][2 * k2], k8[gi][0][2 * k2 + 1],
+                                        k8[gi][1][2 * k2 + 1], q.x, q.y);
                         }
                 }
-            }
-            const bool edge = base + kStep > low;  // some row does not see all 32 tokens
-            if (edge) {
-#pragma unroll
-                for (int mt = 0; mt < R; ++mt)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (base + 8 * x + 2 * t4 + (e & 1) >= lim[mt][e >> 1]) z[mt][x][e] = -INFINITY;
-            }
-            // maxima of the rows, and where they exceed the reference by more than 8
-            float mx[R][2];
-            bool move = false;
-#pragma unroll
-            for (int mt = 0; mt < R; ++mt)
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    float v = -INFINITY;
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) v = fmaxf(v, fmaxf(z[mt][x][2 * hf], z[mt][x][2 * hf + 1]));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-                    mx[mt][hf] = v * zf[mt][hf];
-                    move |= mx[mt][hf] > m[mt][hf] + 8.0f;
-                }
-            if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-                for (int mt = 0; mt < R; ++mt)
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        const float mn = fmaxf(m[mt][hf], mx[mt][hf]);
-                        const float f = mn == -INFINITY ? 1.0f : ex2(m[mt][hf] - mn);
-                        m[mt][hf] = mn;
-                        l[mt][hf] *= f;
-#pragma unroll
-                        for (int x = 0; x < NT; ++x) {
-                            o[mt][x][2 * hf] *= f;
-                            o[mt][x][2 * hf + 1] *= f;
-                        }
-                    }
-            }
-            uint32_t p[R][2][4];
-#pragma unroll
-            for (int mt = 0; mt < R; ++mt)
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const float ref = m[mt][hf] == -INFINITY ? 0.0f : m[mt][hf];  // no key seen yet
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const float p0 = ex2(fmaf(z[mt][x][2 * hf], zf[mt][hf], -ref));
-                        const float p1 = ex2(fmaf(z[mt][x][2 * hf + 1], zf[mt][hf], -ref));
-                        l[mt][hf] += p0 + p1;
-                        p[mt][x >> 1][hf + 2 * (x & 1)] = pack_half2(p0, p1);
-                    }
-                }
-#pragma unroll
-            for (int gi = 0; gi < 2; ++gi) {
-                const uint8_t* vb = st + gi * L::kBytes;
-                uint32_t sb = *reinterpret_cast<const uint32_t*>(vb + L::kVs + (D == 128 ? g : g >> 1) * 16 + t4 * 4);
+                const bool edge = base + 16 * GP > low;  // some row does not see all of these tokens
                 if (edge) {
-                    // Nothing of a token that a row does not see may reach it: bytes behind the
-                    // last token are made zero here; NaN of a token that only some rows see
-                    // is taken out of the product and put into the rows that see it.
-                    uint32_t nan = 0;
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int tok = base + 16 * gi + 8 * (x >> 1) + 2 * t4 + (x & 1);
-                        const uint32_t byte = 0xffu << (8 * x);
-                        if (tok >= n) sb &= ~byte;
-                        if ((sb >> (8 * x) & 0x7f) == 0x7f) nan |= byte;
-                    }
-                    if (__any_sync(0xffffffffu, nan != 0)) {
-                        sb &= ~nan;
-                        const uint32_t one = 0x3c003c00u;  // (1, 1) in halves
-                        const uint32_t b0 = __byte_perm(nan, 0, 0x1100) & one, b1 = __byte_perm(nan, 0, 0x3322) & one;
+                    for (int j = 0; j < NR; ++j)
 #pragma unroll
-                        for (int mt = 0; mt < R; ++mt) {
-                            uint32_t see[4];
+                        for (int e = 0; e < 4; ++e) {
+                            const int lim = slim[8 * j + 2 * t4 + (e & 1)], tok = base + g + 8 * (e >> 1);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int tok = base + 16 * gi + 8 * (e >> 1) + 2 * t4, lm = lim[mt][e & 1];
-                                see[e] = ((tok < lm ? 0x3c00u : 0) | (tok + 1 < lm ? 0x3c000000u : 0));
+                            for (int x = 0; x < GP; ++x)
+                                if (tok + 16 * x >= lim) z[j][x][e] = -INFINITY;
+                        }
+                }
+                // against the reference, in log2 units
+                float y[NR][GP][4], big = kNoKey;
+#pragma unroll
+                for (int j = 0; j < NR; ++j)
+#pragma unroll
+                    for (int x = 0; x < GP; ++x)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            y[j][x][e] = fmaf(z[j][x][e], zf[j][e & 1], -m[j][e & 1]);
+                            big = fmaxf(big, y[j][x][e]);
+                        }
+                if (__any_sync(0xffffffffu, big > 8.0f)) {
+#pragma unroll
+                    for (int j = 0; j < NR; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float v = fmaxf(z[j][0][e], z[j][0][e + 2]);
+                            if (GP == 2) v = fmaxf(v, fmaxf(z[j][GP - 1][e], z[j][GP - 1][e + 2]));
+#pragma unroll
+                            for (int x = 4; x < 32; x <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
+                            const float mn = fmaxf(m[j][e], v * zf[j][e]), f = ex2(m[j][e] - mn);
+                            m[j][e] = mn;
+                            l[j][e] *= f;
+#pragma unroll
+                            for (int x = 0; x < NT / 2; ++x) {
+                                o[j][x][e] *= f;
+                                o[j][x][e + 2] *= f;
                             }
-                            float hit[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                            mma_f16(hit, see, b0, b1);
 #pragma unroll
-                            for (int x = 0; x < NT; ++x)
+                            for (int x = 0; x < GP; ++x) {
+                                y[j][x][e] = fmaf(z[j][x][e], zf[j][e], -mn);
+                                y[j][x][e + 2] = fmaf(z[j][x][e + 2], zf[j][e], -mn);
+                            }
+                        }
+                }
+                uint32_t p[NR][GP][2];  // P^T: [group][tokens 2 t4 and the next, 8 further], row g
 #pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (hit[e] > 0.0f) o[mt][x][e] = __int_as_float(0x7fc00000);
+                for (int j = 0; j < NR; ++j)
+#pragma unroll
+                    for (int x = 0; x < GP; ++x)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float p0 = ex2(y[j][x][2 * e]), p1 = ex2(y[j][x][2 * e + 1]);
+                            l[j][0] += p0;
+                            l[j][1] += p1;
+                            p[j][x][e] = transpose8(pack_half2(p0, p1));
+                        }
+#pragma unroll
+                for (int gi = 0; gi < GP; ++gi) {
+                    const uint8_t* vb = st + (h + gi) * L::kBytes;
+                    uint32_t sb = *reinterpret_cast<const uint32_t*>(vb + L::kVs + (D == 128 ? g : g >> 1) * 16 + t4 * 4);
+                    if (edge) {
+                        // Nothing of a token that a row does not see may reach it: bytes of tokens
+                        // that no row sees are made zero here; NaN of a token that only some rows
+                        // see is taken out of the product and put into the rows that see it.
+                        const int tok = base + 16 * gi + 2 * t4;
+                        uint32_t nan = 0;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const uint32_t byte = 0xffu << (8 * x);
+                            if (tok + 8 * (x >> 1) + (x & 1) >= top) sb &= ~byte;
+                            if ((sb >> (8 * x) & 0x7f) == 0x7f) nan |= byte;
+                        }
+                        if (__any_sync(0xffffffffu, nan != 0)) {
+                            sb &= ~nan;
+                            const uint32_t one = 0x3c003c00u;  // (1, 1) in halves
+                            const uint32_t a0 = __byte_perm(nan, 0, 0x1100) & one, a2 = __byte_perm(nan, 0, 0x3322) & one;
+#pragma unroll
+                            for (int j = 0; j < NR; ++j) {
+                                const int lim = slim[8 * j + g];
+                                uint32_t see[2];
+#pragma unroll
+                                for (int x = 0; x < 2; ++x)
+                                    see[x] = (tok + 8 * x < lim ? 0x3c00u : 0u) | (tok + 8 * x + 1 < lim ? 0x3c000000u : 0u);
+                                float hit[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                                mma_f16(hit, a0, a0, a2, a2, see[0], see[1]);
+#pragma unroll
+                                for (int x = 0; x < NT / 2; ++x)
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+                                        if (hit[e] > 0.0f) o[j][x][e] = __int_as_float(0x7fc00000);
+                            }
                         }
                     }
-                }
-                const uint32_t s0 = e4m3x2_to_half2(sb & 0xffff), s1 = e4m3x2_to_half2(sb >> 16);
-                uint32_t vw[4][D / 64];
+                    const uint32_t s0 = e4m3x2_to_half2(sb & 0xffff), s1 = e4m3x2_to_half2(sb >> 16);
+                    uint32_t vw[4][D / 64];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const uint8_t* vr = vb + L::v_chunk(t4 + 4 * x, g);
-                    if (D == 128) {
-                        const uint2 v = *reinterpret_cast<const uint2*>(vr);
-                        vw[x][0] = v.x; vw[x][D / 64 - 1] = v.y;
-                    } else {
-                        vw[x][0] = *reinterpret_cast<const uint32_t*>(vr);
-                    }
-                }
-#pragma unroll
-                for (int wi = 0; wi < D / 64; ++wi) {
-                    // a byte of both tokens of a pair: even channels, then odd ones
-                    constexpr uint32_t lo = 0x0f0f0f0fu;
-                    uint32_t v8[2][2][4];  // [tokens 8 x + 2 t4 ..][parity of the channel]
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const uint32_t u0 = vw[2 * x][wi], u1 = vw[2 * x + 1][wi];
-                        e2m1x8_to_half2((u0 & lo) | ((u1 << 4) & ~lo), v8[x][0]);
-                        e2m1x8_to_half2(((u0 >> 4) & lo) | (u1 & ~lo), v8[x][1]);
+                    for (int x = 0; x < 4; ++x) {
+                        const uint8_t* vr = vb + L::v_chunk(t4 + 4 * x, g);
+                        if (D == 128) {
+                            const uint2 v = *reinterpret_cast<const uint2*>(vr);
+                            vw[x][0] = v.x; vw[x][D / 64 - 1] = v.y;
+                        } else {
+                            vw[x][0] = *reinterpret_cast<const uint32_t*>(vr);
+                        }
                     }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint32_t b0 = hmul2(v8[0][j & 1][j >> 1], s0), b1 = hmul2(v8[1][j & 1][j >> 1], s1);
+                    for (int wi = 0; wi < D / 64; ++wi) {
+                        // a byte of both tokens of a pair: even channels, then odd ones
+                        constexpr uint32_t lo = 0x0f0f0f0fu;
+                        uint32_t v8[2][2][4];  // [tokens 8 x + 2 t4 ..][parity of the channel]
 #pragma unroll
-                        for (int mt = 0; mt < R; ++mt) mma_f16(o[mt][8 * wi + j], p[mt][gi], b0, b1);
+                        for (int x = 0; x < 2; ++x) {
+                            const uint32_t u0 = vw[2 * x][wi], u1 = vw[2 * x + 1][wi];
+                            e2m1x8_to_half2((u0 & lo) | ((u1 << 4) & ~lo), v8[x][0]);
+                            e2m1x8_to_half2(((u0 >> 4) & lo) | (u1 & ~lo), v8[x][1]);
+                        }
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const uint32_t a0 = hmul2(v8[0][0][x], s0), a1 = hmul2(v8[0][1][x], s0);
+                            const uint32_t a2 = hmul2(v8[1][0][x], s1), a3 = hmul2(v8[1][1][x], s1);
+#pragma unroll
+                            for (int j = 0; j < NR; ++j) mma_f16(o[j][4 * wi + x], a0, a1, a2, a3, p[j][gi][0], p[j][gi][1]);
+                        }
                     }
                 }
             }
         }
-        copy_wait<0>();
-        // the row sums of a quad's lanes
+        // the row sums over the lanes of a row
 #pragma unroll
-        for (int mt = 0; mt < R; ++mt)
+        for (int j = 0; j < NR; ++j)
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 1);
-                l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 2);
-            }
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], x);
         __syncthreads();  // every warp is done with its ring
-        // Join the warps: [warp][row][d] sums, 16 bytes (four channels) at a time. Lane
-        // (g, t4)'s chunks are 8 apart between the t4, so their low three bits take t4
-        // and the row's parity, which puts eight lanes on eight different bank groups.
+        // Join the warps: [warp][row][d] sums, 16 bytes (four channels) at a time. The
+        // lanes that store together have four rows and two chunks apart by d/32; the
+        // row's bits exchange chunks so that eight lanes meet eight bank groups.
         float4* os = reinterpret_cast<float4*>(smem);
         constexpr int C4 = D / 4;
+        auto at4 = [&](int wp, int r, int c) {
+            const int t = (r >> 1) & 3;
+            return (wp * RT + r) * C4 + (c ^ (D == 128 ? t : (t & 1) | (t & 2) << 1));
+        };
 #pragma unroll
-        for (int mt = 0; mt < R; ++mt)
+        for (int j = 0; j < NR; ++j)
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int r = mt * 16 + hf * 8 + g;
-                if (t4 == 0) sml[warp][r] = make_float2(m[mt][hf], l[mt][hf]);
+            for (int e = 0; e < 2; ++e) {
+                const int r = 8 * j + 2 * t4 + e;
+                if (g == 0) sml[warp][r] = make_float2(m[j][e], l[j][e]);
                 if (r >= s.rows) continue;
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int j = 0; j < NT / 4; ++j) {
-                        const int c = (2 * t4 + e) * (NT / 4) + j;
-                        os[(warp * RT + r) * C4 + (c ^ ((c / (NT / 2)) | (r & 1) << 2))] =
-                            make_float4(o[mt][4 * j][2 * hf + e], o[mt][4 * j + 1][2 * hf + e],
-                                        o[mt][4 * j + 2][2 * hf + e], o[mt][4 * j + 3][2 * hf + e]);
-                    }
+                for (int x = 0; x < NT / 4; ++x)
+                    os[at4(warp, r, g * (NT / 4) + x)] = make_float4(o[j][2 * x][e], o[j][2 * x][e + 2],
+                                                                     o[j][2 * x + 1][e], o[j][2 * x + 1][e + 2]);
             }
         __syncthreads();
         const bool whole = s.c0 == 0 && s.c1 == s.chunks;
@@ -865,19 +919,18 @@ k_cache_attn_mma(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_t
         for (int x = threadIdx.x; x < s.rows * C4; x += kThreads) {
             const int r = x / C4, c = x - r * C4;
             float2 v[4];
-            float mx = -INFINITY;
+            float mx = kNoKey;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 v[i] = sml[i][r];
                 mx = fmaxf(mx, v[i].x);
             }
-            const float ref = mx == -INFINITY ? 0.0f : mx;
             float sum = 0.0f;
             float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float f = ex2(v[i].x - ref);
-                const float4 u = os[(i * RT + r) * C4 + (c ^ ((c / (NT / 2)) | (r & 1) << 2))];
+                const float f = ex2(v[i].x - mx);
+                const float4 u = os[at4(i, r, c)];
                 sum = fmaf(f, v[i].y, sum);
                 acc.x = fmaf(f, u.x, acc.x); acc.y = fmaf(f, u.y, acc.y);
                 acc.z = fmaf(f, u.z, acc.z); acc.w = fmaf(f, u.w, acc.w);
@@ -897,64 +950,94 @@ k_cache_attn_mma(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_t
                 if (c == 0) out.ml[(long long)slot * RT + r] = make_float2(mx, sum);
             }
         }
-    } while (walk.next(a, out, piece));
+        tc::fence_proxy_async();  // the next segment's copies come after these accesses of the ring
+    } while (!__syncthreads_or(dead) && walk.next(a, out, piece));
 }
 
 // ------------------------------------------------------------------ join
 
+constexpr int kJoinRows = 4, kJoinWarps = 8;
+
 // Block (c, y) joins the parts of the item that starts in piece c and ends
-// behind it, rows y, y + gridDim.y, ...: each warp adds every fourth part, a lane
-// d/32 channels of it, with several parts' loads in flight.
+// behind it, rows 4 y to 4 y + 3 at once: each warp adds every eighth part, a lane
+// d/32 channels of each row. It is a chain of loads (the item, the maxima, the
+// sums), so the rows and parts are in flight together.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) k_cache_join(CacheArgs a, AttnOut out) {
+__global__ void __launch_bounds__(32 * kJoinWarps) k_cache_join(CacheArgs a, AttnOut out) {
     constexpr int E = D / 32;
-    __shared__ float acc4[4][D];
+    __shared__ float acc8[kJoinWarps][kJoinRows][D];
+    __shared__ float sum8[kJoinWarps][kJoinRows];
     wait_previous();
     const CutItem c = out.cut[blockIdx.x];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, R = out.rows;
-    for (int r = blockIdx.y; r < c.rows; r += gridDim.y) {
-        // part p > 0 begins its piece
-        auto slot = [&](int p) { return (long long)(p == 0 ? c.slot : 2 * (blockIdx.x + p)) * R + r; };
-        float mx = -INFINITY;
-        for (int p = lane; p < c.parts; p += 32) mx = fmaxf(mx, out.ml[slot(p)].x);
-        mx = warp_max(mx);
-        const float ref = mx == -INFINITY ? 0.0f : mx;
-        float sum = 0.0f, acc[E];
+    const int r0 = blockIdx.y * kJoinRows, rows = min(c.rows - r0, kJoinRows);
+    if (rows <= 0) return;
+    // part p > 0 begins its piece
+    auto slot = [&](int p) { return (long long)(p == 0 ? c.slot : 2 * (blockIdx.x + p)) * R + r0; };
+    float mx[kJoinRows], sum[kJoinRows], acc[kJoinRows][E];
 #pragma unroll
-        for (int i = 0; i < E; ++i) acc[i] = 0.0f;
-#pragma unroll 8
-        for (int p = warp; p < c.parts; p += 4) {
-            const long long at = slot(p);
-            const float2 ml = out.ml[at];
-            const float f = exp2f(ml.x - ref);
-            sum = fmaf(f, ml.y, sum);
+    for (int r = 0; r < kJoinRows; ++r) {
+        mx[r] = -INFINITY;
+        sum[r] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[r][i] = 0.0f;
+    }
+    for (int p = lane; p < c.parts; p += 32) {
+        const float2* ml = out.ml + slot(p);
+#pragma unroll
+        for (int r = 0; r < kJoinRows; ++r)
+            if (r < rows) mx[r] = fmaxf(mx[r], ml[r].x);
+    }
+#pragma unroll
+    for (int r = 0; r < kJoinRows; ++r) {
+        mx[r] = warp_max(mx[r]);
+        if (mx[r] == -INFINITY) mx[r] = 0.0f;  // no part has a key of this row
+    }
+#pragma unroll 2
+    for (int p = warp; p < c.parts; p += kJoinWarps) {
+        const long long at = slot(p);
+#pragma unroll
+        for (int r = 0; r < kJoinRows; ++r) {
+            if (r >= rows) continue;
+            const float2 ml = out.ml[at + r];
             float v[E];
             if (E == 4) {
-                const float4 u = reinterpret_cast<const float4*>(out.part + at * D)[lane];
+                const float4 u = reinterpret_cast<const float4*>(out.part + (at + r) * D)[lane];
                 v[0] = u.x; v[1] = u.y; v[E - 2] = u.z; v[E - 1] = u.w;
             } else {
-                const float2 u = reinterpret_cast<const float2*>(out.part + at * D)[lane];
+                const float2 u = reinterpret_cast<const float2*>(out.part + (at + r) * D)[lane];
                 v[0] = u.x; v[1] = u.y;
             }
+            const float f = exp2f(ml.x - mx[r]);
+            sum[r] = fmaf(f, ml.y, sum[r]);
 #pragma unroll
-            for (int i = 0; i < E; ++i) acc[i] = fmaf(f, v[i], acc[i]);
+            for (int i = 0; i < E; ++i) acc[r][i] = fmaf(f, v[i], acc[r][i]);
         }
-        __shared__ float sum4[4];
+    }
 #pragma unroll
-        for (int i = 0; i < E; ++i) acc4[warp][lane * E + i] = acc[i];
-        if (lane == 0) sum4[warp] = sum;
-        __syncthreads();
-        sum = (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
+    for (int r = 0; r < kJoinRows; ++r) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc8[warp][r][lane * E + i] = acc[r][i];
+        if (lane == 0) sum8[warp][r] = sum[r];
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < rows * D; x += 32 * kJoinWarps) {
+        const int r = x / D, i = x - r * D;
+        float s = 0.0f, v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            s += sum8[w][r];
+            v += acc8[w][r][i];
+        }
         int t;
-        const long long at = row_offset(a, c.b, c.h, c.row0 + r, &t);
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        if (threadIdx.x < D) {
-            const int i = threadIdx.x;
-            const float v = (acc4[0][i] + acc4[1][i]) + (acc4[2][i] + acc4[3][i]);
-            reinterpret_cast<T*>(out.O)[at * D + i] = from_f<T>(sum == 0.0f ? 0.0f : v * inv);
+        const long long at = row_offset(a, c.b, c.h, c.row0 + r0 + r, &t);
+        reinterpret_cast<T*>(out.O)[at * D + i] = from_f<T>(s == 0.0f ? 0.0f : v / s);
+        if (out.lse && i == 0) {
+            float top = mx[0];
+#pragma unroll
+            for (int q = 1; q < kJoinRows; ++q) top = q == r ? mx[q] : top;
+            out.lse[at] = s == 0.0f ? -INFINITY : (top + log2f(s)) * kLn2;
         }
-        if (out.lse && threadIdx.x == 0) out.lse[at] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * kLn2;
-        __syncthreads();
     }
 }
 
@@ -972,8 +1055,8 @@ CachePlan cache_attn_plan(const CacheArgs& a, int d, int dtype, unsigned flags) 
     p.tensor = dtype == 1 && !(flags & MITA_FLAG_SIMT);
     int blocks = 4;  // per SM
     if (p.tensor) {
-        p.rows = rows <= 16 ? 16 : 32;
-        blocks = rows <= 16 ? 3 : 2;
+        p.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+        blocks = mma_blocks(d, p.rows / 8);
     } else {
         p.rows = rows == 1 ? 1 : 4;
     }
@@ -992,8 +1075,8 @@ static cudaError_t join_t(const CacheArgs& a, const AttnOut& o, cudaStream_t st)
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t c{};
-    c.gridDim = dim3(o.pieces, (o.rows + 3) / 4);
-    c.blockDim = dim3(kThreads);
+    c.gridDim = dim3(o.pieces, (o.rows + kJoinRows - 1) / kJoinRows);
+    c.blockDim = dim3(32 * kJoinWarps);
     c.stream = st;
     c.attrs = &at;
     c.numAttrs = 1;
@@ -1012,12 +1095,13 @@ static cudaError_t simt_t(const CacheArgs& a, const void* Q, const uint8_t* cach
     return join_t<T, D>(a, o, st);
 }
 
-template <int D, int R>
+template <int D, int NR>
 static cudaError_t mma_t(const CacheArgs& a, const void* Q, const uint8_t* cache, const AttnOut& o, cudaStream_t st) {
-    constexpr int smem = mma_smem<D, R>();
-    const cudaError_t e = cudaFuncSetAttribute(k_cache_attn_mma<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    constexpr int smem = mma_smem<D, NR>();
+    static_assert(mma_blocks(D, NR) * (smem + 3 * 1024) <= 228 * 1024, "the blocks that a call counts on fit an SM");
+    const cudaError_t e = cudaFuncSetAttribute(k_cache_attn_mma<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    k_cache_attn_mma<D, R><<<o.pieces + 1, kThreads, smem, st>>>(a, (const __nv_bfloat16*)Q, cache, o);
+    k_cache_attn_mma<D, NR><<<o.pieces + 1, kThreads, smem, st>>>(a, (const __nv_bfloat16*)Q, cache, o);
     count_launch();
     return join_t<__nv_bfloat16, D>(a, o, st);
 }
@@ -1025,7 +1109,9 @@ static cudaError_t mma_t(const CacheArgs& a, const void* Q, const uint8_t* cache
 template <int D>
 static cudaError_t attn_t(const CacheArgs& a, const CachePlan& p, int dtype, const void* Q, const uint8_t* cache,
                           const AttnOut& o, cudaStream_t st) {
-    if (p.tensor) return p.rows == 16 ? mma_t<D, 1>(a, Q, cache, o, st) : mma_t<D, 2>(a, Q, cache, o, st);
+    if (p.tensor)
+        return p.rows == 8 ? mma_t<D, 1>(a, Q, cache, o, st)
+               : p.rows == 16 ? mma_t<D, 2>(a, Q, cache, o, st) : mma_t<D, 4>(a, Q, cache, o, st);
     if (dtype == 0) return p.rows == 1 ? simt_t<float, D, 1>(a, Q, cache, o, st) : simt_t<float, D, 4>(a, Q, cache, o, st);
     return p.rows == 1 ? simt_t<__nv_bfloat16, D, 1>(a, Q, cache, o, st) : simt_t<__nv_bfloat16, D, 4>(a, Q, cache, o, st);
 }
