@@ -311,70 +311,75 @@ def cache_workspace(p: CacheParams, device="cuda"):
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _need(name, t, shape, dtype, dev):
-    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s tensor of shape %s" % (name, dtype, shape))
-    if t.get_device() != dev:
-        raise ValueError("%s must be on the cache's CUDA device" % name)
-
-
-def _cache_call(fn, p: CacheParams, names, rows, heads, order, cache, table, lens, counts, exps, ws, lse, stream):
-    """One cache call. The C ABI sees only pointers, so the tensors are held to
-    ``p`` here. ``rows``: the call's two row tensors; ``order`` puts the arguments
-    in the C function's order. Kept short: a decoding step makes these calls for
-    every layer."""
+def _cache_args(p: CacheParams, tensors, shape, cache, table, lens, counts, exps, ws, lse, stream):
+    """Holds the tensors of a cache call to ``p`` (the C ABI sees only pointers) and
+    returns (device, stream, pointers of table, lens, counts and exps). Written out
+    and short: a decoding step makes these calls for every layer."""
     import torch
-    i32, u8, dev = torch.int32, torch.uint8, cache.get_device()
+    i32, dev = torch.int32, cache.get_device()
     dt = torch.bfloat16 if p.dtype == BF16 else torch.float32
-    shape = (p.B, heads, p.T, p.d)
-    _need(names[0], rows[0], shape, dt, dev)
-    _need(names[1], rows[1], shape, dt, dev)
-    _need("table", table, (p.B, p.max_pages), i32, dev)
-    _need("lens", lens, (p.B,), i32, dev)
-    if counts is not None:
-        _need("counts", counts, (p.B,), i32, dev)
-    if exps is not None:
-        _need("exps", exps, (2, p.H_kv), i32, dev)
-    if lse is not None:
-        _need("lse_out", lse, (p.B, p.H, p.T), torch.float32, dev)
-    _need("cache", cache, (cache.numel(),), u8, dev)
-    _need("ws", ws, (ws.numel(),), u8, dev)
-    size = p.n_pages * p.H_kv * p.page * 9 * p.d // 8  # mita_cache_size
-    if cache.numel() < size:
-        raise ValueError("cache holds %d bytes, the pool needs %d" % (cache.numel(), size))
+    for t in tensors:
+        if t.shape != shape or t.dtype is not dt or not t.is_contiguous() or t.get_device() != dev:
+            _refuse(t, shape, dt, dev)
+    for t, s in ((table, (p.B, p.max_pages)), (lens, (p.B,)), (counts, (p.B,)), (exps, (2, p.H_kv))):
+        if t is None:
+            if t is table or t is lens:
+                raise ValueError("table and lens are needed")
+        elif t.shape != s or t.dtype is not i32 or not t.is_contiguous() or t.get_device() != dev:
+            _refuse(t, s, i32, dev)
+    if lse is not None and (lse.shape != shape[:3] or lse.dtype is not torch.float32 or not lse.is_contiguous()
+                            or lse.get_device() != dev):
+        _refuse(lse, shape[:3], torch.float32, dev, "lse_out: ")
+    for t in (cache, ws):
+        if t.dtype is not torch.uint8 or not t.is_contiguous() or t.get_device() != dev:
+            _refuse(t, tuple(t.shape), torch.uint8, dev)
+    if cache.numel() < p.n_pages * p.H_kv * p.page * 9 * p.d // 8:  # mita_cache_size
+        raise ValueError("cache holds %d bytes, the pool needs %d" % (cache.numel(), mita_cache_size(p)))
     if dev < 0:
-        raise ValueError("cache must be on a CUDA device")
-    args = order(rows[0].data_ptr(), rows[1].data_ptr(), cache.data_ptr(),
-                 (table.data_ptr(), lens.data_ptr(), None if counts is None else counts.data_ptr(),
-                  None if exps is None else exps.data_ptr()))
-    if fn == "mita_cache_attention":
-        args += (None if lse is None else lse.data_ptr(),)
+        raise ValueError("the tensors must be on a CUDA device")
     if stream is None:
-        st = torch.cuda.current_stream(dev).cuda_stream
-    else:
-        st = stream if isinstance(stream, int) else stream.cuda_stream
-    call = getattr(lib(), fn)
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    return dev, stream, (table.data_ptr(), lens.data_ptr(), None if counts is None else counts.data_ptr(),
+                         None if exps is None else exps.data_ptr())
+
+
+def _refuse(t, shape, dtype, dev, what=""):
+    if t.get_device() != dev:
+        raise ValueError("%sall tensors of a call must be on the cache's CUDA device" % what)
+    raise ValueError("%sexpected a contiguous %s tensor of shape %s, got %s %s" % (what, dtype, tuple(shape), t.dtype,
+                                                                                tuple(t.shape)))
+
+
+def _on_device(dev, fn, *args):
+    import torch
     if torch.cuda.current_device() == dev:
-        _check(call(ctypes.byref(p.c()), *args, ws.data_ptr(), ws.numel(), st))
+        rc = fn(*args)
     else:
         with torch.cuda.device(dev):
-            _check(call(ctypes.byref(p.c()), *args, ws.data_ptr(), ws.numel(), st))
+            rc = fn(*args)
+    if rc:
+        _check(rc)
 
 
 def mita_cache_write(p: CacheParams, K, V, cache, table, lens, ws, counts=None, exps=None, stream=None):
     """Stores the rows K, V [B, H_kv, T, d] in the pages that ``table`` names."""
-    _cache_call("mita_cache_write", p, ("K", "V"), (K, V), p.H_kv, lambda k, v, c, idx: (k, v, c) + idx, cache, table,
-                lens, counts, exps, ws, None, stream)
+    dev, st, idx = _cache_args(p, (K, V), (p.B, p.H_kv, p.T, p.d), cache, table, lens, counts, exps, ws, None, stream)
+    _on_device(dev, lib().mita_cache_write, ctypes.byref(p.c()), K.data_ptr(), V.data_ptr(), cache.data_ptr(), *idx,
+               ws.data_ptr(), ws.numel(), st)
 
 
 def mita_cache_read(p: CacheParams, cache, table, lens, K, V, ws, counts=None, exps=None, stream=None):
     """Reads rows back into K, V [B, H_kv, T, d]; padding rows stay as they are."""
-    _cache_call("mita_cache_read", p, ("K", "V"), (K, V), p.H_kv, lambda k, v, c, idx: (c,) + idx + (k, v), cache,
-                table, lens, counts, exps, ws, None, stream)
+    dev, st, idx = _cache_args(p, (K, V), (p.B, p.H_kv, p.T, p.d), cache, table, lens, counts, exps, ws, None, stream)
+    _on_device(dev, lib().mita_cache_read, ctypes.byref(p.c()), cache.data_ptr(), *idx, K.data_ptr(), V.data_ptr(),
+               ws.data_ptr(), ws.numel(), st)
 
 
 def mita_cache_attention(p: CacheParams, Q, cache, table, lens, O, ws, counts=None, exps=None, lse_out=None,
                          stream=None):
     """Attention of the rows Q [B, H, T, d] over the cache, into O (and lse_out)."""
-    _cache_call("mita_cache_attention", p, ("Q", "O"), (Q, O), p.H, lambda q, o, c, idx: (q, c) + idx + (o,), cache,
-                table, lens, counts, exps, ws, lse_out, stream)
+    dev, st, idx = _cache_args(p, (Q, O), (p.B, p.H, p.T, p.d), cache, table, lens, counts, exps, ws, lse_out, stream)
+    _on_device(dev, lib().mita_cache_attention, ctypes.byref(p.c()), Q.data_ptr(), cache.data_ptr(), *idx,
+               O.data_ptr(), None if lse_out is None else lse_out.data_ptr(), ws.data_ptr(), ws.numel(), st)

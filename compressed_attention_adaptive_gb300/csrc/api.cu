@@ -322,6 +322,8 @@ static mita_status resolve_cache(const mita_cache_params* p, CacheArgs* a) {
     a->n_pages = p->n_pages; a->cols = p->max_pages;
     a->causal = (p->flags & MITA_FLAG_CAUSAL) != 0;
     a->scale = p->scale > 0.0f ? p->scale : 1.0f / sqrtf((float)p->d);
+    if (!cache_attn_plan(*a, p->d, p->dtype, p->flags).fits)
+        return fail(MITA_ERR_UNSUPPORTED, "too many rows and tokens for one call");
     return MITA_OK;
 }
 

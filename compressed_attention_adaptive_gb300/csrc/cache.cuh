@@ -70,7 +70,8 @@ constexpr int kMaxExp = 60;
 // How the attention splits one call: rows of a tile, pieces of the line of
 // chunks, and the rows of partial results that the workspace holds.
 struct CachePlan {
-    bool tensor;  // tensor cores (bf16), else CUDA cores
+    bool tensor;  // tensor cores, else CUDA cores
+    bool fits;    // the call's units of work can be counted in 32 bits
     int rows, pieces;
     size_t parts;
 };
@@ -80,7 +81,7 @@ constexpr int kCutBytes = 24;  // one CutItem (cache_attn.cu)
 struct CacheParts {
     float* part;  // [parts][d]
     float2* ml;   // [parts]
-    void* cut;    // [pieces] of kCutBytes
+    void* cut;    // [pieces] of kCutBytes (as many cut items there can be)
 };
 
 // cache.cu

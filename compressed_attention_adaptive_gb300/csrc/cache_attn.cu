@@ -37,7 +37,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // An item that is cut: the join's work. rows = 0: nothing to join here.
 struct CutItem {
     int b, h, row0, rows;
-    int slot, parts;  // the first part's slot, and the pieces it goes over
+    int piece, parts;  // the first part's piece, and the pieces it goes over
 };
 
 static_assert(sizeof(CutItem) == kCutBytes, "the workspace holds CutItems");
@@ -47,19 +47,19 @@ struct AttnOut {
     float* lse;    // or null
     float* part;   // [2 * pieces][rows][d]
     float2* ml;    // [2 * pieces][rows] (maximum in log2 units, sum)
-    CutItem* cut;  // [pieces]: the item that starts in a piece and ends behind it
+    CutItem* cut;      // [cuts]
     int pieces, rows;  // pieces of the line, rows of a tile
+    // The cut items, by their number (sequence, tile, head) when there are no more items
+    // than pieces, else by the piece that they start in.
+    int cuts, items, tiles;  // items: 0 in the second case; tiles of a sequence with T rows
 };
 
-// Division of numbers that nearly always fit 32 bits.
-__device__ __forceinline__ long long quot(long long a, long long b) {
-    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
-}
-
-// One sequence's share of the line: (row tiles) * Hkv * (chunks of its length).
+// One sequence's share of the line. Its items are cut into chunks, and each item
+// takes `extra` units more than its chunks: what starting and ending an item costs
+// a block (loading Q, the first copies' latency, joining the warps), so that
+// blocks with many short items get fewer chunks.
 struct SeqWork {
-    int n, count, rows, chunks;
-    long long total;
+    int n, count, rows, chunks, items;
 };
 __device__ __forceinline__ SeqWork seq_work(const CacheArgs& a, int b, int rtile) {
     SeqWork s;
@@ -67,162 +67,161 @@ __device__ __forceinline__ SeqWork seq_work(const CacheArgs& a, int b, int rtile
     s.count = cache_count(a, b);
     s.rows = s.count * a.G;
     s.chunks = max(1, (s.n + kChunk - 1) / kChunk);
-    s.total = (long long)((s.rows + rtile - 1) / rtile) * a.Hkv * s.chunks;
+    s.items = (s.rows + rtile - 1) / rtile * a.Hkv;
     return s;
 }
 
-// The line of chunks, cut into `pieces` pieces that differ by one chunk at most.
+// With less than kFew chunks per block an item's start is not counted: its blocks
+// run side by side then, and none has many. (64 sequences of 33 to 8191 tokens: the
+// slowest block at 69 us with the median at 49 without this, see the plan below.)
+constexpr int kExtra = 2, kFew = 8;
+
+// The line of units, cut into `pieces` pieces that differ by one unit at most.
 struct Line {
-    long long total, q, r;
-    int pieces;
-    __device__ __forceinline__ void set(long long t, int max_pieces) {
-        total = t;
-        pieces = (int)min((long long)max_pieces, t);
-        q = pieces ? quot(t, pieces) : 0;
-        r = t - q * pieces;
-    }
-    __device__ __forceinline__ long long at(int c) const { return c * q + min((long long)c, r); }
-    __device__ __forceinline__ int piece_of(long long x) const {
-        const long long head = r * (q + 1);
-        return (int)(x < head ? quot(x, q + 1) : r + quot(x - head, q));
+    int pieces, q, r, extra;
+    __device__ __forceinline__ int at(int c) const { return c * q + min(c, r); }
+    __device__ __forceinline__ int piece_of(int x) const {
+        const int head = r * (q + 1);
+        return x < head ? x / (q + 1) : r + (x - head) / q;
     }
 };
 
-__device__ __forceinline__ long long warp_scan(long long x, int lane) {
+__device__ __forceinline__ int warp_scan(int x, int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
     return x;
-}
-
-// The line and, if `piece` has any of it, the sequence *b that piece starts in
-// and the chunks *before it. Each warp finds it by itself, from one load of 32
-// lengths at a time.
-__device__ __forceinline__ bool line_start(const CacheArgs& a, int rtile, int piece, int max_pieces, int lane,
-                                           Line* line, int* b, long long* before, SeqWork* sw) {
-    SeqWork mine{};
-    long long x = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-        mine.total = 0;
-        if (b0 + lane < a.B) mine = seq_work(a, b0 + lane, rtile);
-        x += mine.total;
-    }
-    x = warp_scan(x, lane);
-    line->set(__shfl_sync(0xffffffffu, x, 31), max_pieces);
-    if (piece >= line->pieces) return false;
-    const long long w = line->at(piece);
-    long long base = 0;
-    for (int b0 = 0;; b0 += 32) {
-        if (a.B > 32) {
-            mine.total = 0;
-            if (b0 + lane < a.B) mine = seq_work(a, b0 + lane, rtile);
-            x = base + warp_scan(mine.total, lane);
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, w < x);
-        if (hit) {  // the first sequence whose share ends behind w
-            const int l = __ffs(hit) - 1;
-            *b = b0 + l;
-            *before = __shfl_sync(0xffffffffu, x - mine.total, l);
-            sw->n = __shfl_sync(0xffffffffu, mine.n, l);
-            sw->count = __shfl_sync(0xffffffffu, mine.count, l);
-            sw->rows = __shfl_sync(0xffffffffu, mine.rows, l);
-            sw->chunks = __shfl_sync(0xffffffffu, mine.chunks, l);
-            sw->total = __shfl_sync(0xffffffffu, mine.total, l);
-            return true;
-        }
-        base = __shfl_sync(0xffffffffu, x, 31);
-    }
 }
 
 // One block's part of an item.
 struct Segment {
     int b, h, row0, rows;  // sequence, cache head, first row and rows of the tile
     int c0, c1, chunks;    // chunks [c0, c1) of the item's `chunks`
-    long long start;       // the item's first chunk on the line
+    int first;             // the item's chunk 0 on the line
 };
 
-// Segment that begins at chunk w (in sequence b, `before` chunks before it) and
-// ends at w1 or at the item's end.
-__device__ __forceinline__ Segment segment_at(const CacheArgs& a, int rtile, const SeqWork& s, int b, long long before,
-                                              long long w, long long w1) {
-    Segment g;
-    const long long rel = w - before, item = quot(rel, s.chunks);
-    g.b = b;
-    g.start = before + item * s.chunks;
-    const int tile = (int)quot(item, a.Hkv);
-    g.h = (int)(item - (long long)tile * a.Hkv);
-    g.row0 = tile * rtile;
-    g.rows = min(rtile, s.rows - g.row0);
-    g.chunks = s.chunks;
-    g.c0 = (int)(rel - item * s.chunks);
-    g.c1 = (int)min((long long)s.chunks, w1 - g.start);
-    return g;
-}
-
 // A block's walk along its piece, in shared memory: registers are for the sums.
-// Thread 0 (at first its warp) moves it; begin() and next() are called by the
-// whole block and leave the next segment in `s`.
-struct Walk {
+// The first warp finds the start, thread 0 moves it; begin() and next() are called
+// by the whole block and leave the next segment in `s`. A piece holds at most one
+// segment of an item that began before it (the first) and one of an item that goes
+// on behind it (the last).
+template <int RT> struct Walk {
     Line line;
-    long long w, w_begin, w_end, before;
+    int w, w_end, before, b;  // position; units before sequence b
     SeqWork sw;
     Segment s;
-    int b, slot;
     bool more;
 
-    __device__ __forceinline__ void segment(const CacheArgs& a, const AttnOut& out, int piece) {
-        while (w >= before + sw.total) {  // next sequence with work
-            before += sw.total;
-            sw = seq_work(a, ++b, out.rows);
+    // The next segment from w on, if there is one.
+    __device__ __forceinline__ void segment(const CacheArgs& a) {
+        more = false;
+        while (w < w_end) {
+            const int len = sw.chunks + line.extra;
+            if (w - before >= sw.items * len) {  // next sequence with work
+                before += sw.items * len;
+                sw = seq_work(a, ++b, RT);
+                continue;
+            }
+            const int item = (w - before) / len, start = before + item * len;
+            const int tile = item / a.Hkv;
+            s.b = b;
+            s.h = item - tile * a.Hkv;
+            s.row0 = tile * RT;
+            s.rows = min(RT, sw.rows - s.row0);
+            s.chunks = sw.chunks;
+            s.first = start + line.extra;
+            s.c0 = max(w - s.first, 0);
+            s.c1 = min(s.chunks, w_end - s.first);
+            w = start + len;
+            if (s.c0 < s.c1) {
+                more = true;
+                return;
+            }
         }
-        s = segment_at(a, out.rows, sw, b, before, w, w_end);
-        slot = 2 * piece + (w == w_begin ? 0 : 1);
-        w = s.start + s.c1;
-        if (w == w_end) note_cut(out, piece, s.c0 == 0 && s.c1 < s.chunks);
     }
-    // The item that starts in this piece and ends behind it, if there is one.
-    __device__ __forceinline__ void note_cut(const AttnOut& out, int piece, bool cut) {
-        CutItem c{};
-        if (cut) {
-            c.b = s.b; c.h = s.h; c.row0 = s.row0; c.rows = s.rows;
-            c.slot = slot;
-            c.parts = line.piece_of(s.start + s.chunks - 1) - piece + 1;
-        }
-        out.cut[piece] = c;
-    }
-    __device__ __forceinline__ bool begin(const CacheArgs& a, const AttnOut& out, int piece) {
+    __device__ __forceinline__ bool begin(const CacheArgs& a, int piece, int max_pieces) {
         if (threadIdx.x < 32) {
+            const int lane = threadIdx.x;
+            SeqWork mine{};
+            unsigned items = 0, chunks = 0;
+            for (int b0 = 0; b0 < a.B; b0 += 32) {
+                mine.items = 0;
+                if (b0 + lane < a.B) mine = seq_work(a, b0 + lane, RT);
+                items += mine.items;
+                chunks += mine.items * mine.chunks;
+            }
+            items = __reduce_add_sync(0xffffffffu, items);
+            chunks = __reduce_add_sync(0xffffffffu, chunks);
             Line l;
-            SeqWork q;
-            long long bf;
-            int sb;
-            const bool any = line_start(a, out.rows, piece, out.pieces, threadIdx.x, &l, &sb, &bf, &q);
-            if (threadIdx.x == 0) {
-                note_cut(out, piece, false);
-                more = any;
-                if (any) {
-                    line = l; sw = q; before = bf; b = sb;
-                    w = w_begin = l.at(piece);
-                    w_end = l.at(piece + 1);
-                    segment(a, out, piece);
+            l.extra = chunks >= (unsigned)max_pieces * kFew ? kExtra : 0;
+            const int total = (int)(chunks + items * l.extra);
+            l.pieces = min(max_pieces, total);
+            l.q = l.pieces ? total / l.pieces : 0;
+            l.r = total - l.q * l.pieces;
+            if (piece >= l.pieces) {
+                if (lane == 0) more = false;
+            } else {
+                const int w0 = l.at(piece);
+                int base = 0, x = 0, share = 0;
+                unsigned hit = 0;
+                for (int b0 = 0; !hit; b0 += 32) {
+                    if (a.B > 32) {
+                        mine.items = 0;
+                        if (b0 + lane < a.B) mine = seq_work(a, b0 + lane, RT);
+                    }
+                    share = mine.items * (mine.chunks + l.extra);
+                    x = base + warp_scan(share, lane);
+                    hit = __ballot_sync(0xffffffffu, w0 < x);
+                    base = __shfl_sync(0xffffffffu, x, 31);
+                    if (hit && lane == __ffs(hit) - 1) {  // the first sequence whose share ends behind w0
+                        line = l;
+                        w = w0;
+                        w_end = l.at(piece + 1);
+                        before = x - share;
+                        b = b0 + lane;
+                        sw = mine;
+                        segment(a);
+                    }
                 }
             }
         }
         __syncthreads();
         return more;
     }
-    __device__ __forceinline__ bool next(const CacheArgs& a, const AttnOut& out, int piece) {
+    __device__ __forceinline__ bool next(const CacheArgs& a) {
         __syncthreads();  // the block is done with the segment and its shared memory
-        if (threadIdx.x == 0) {
-            more = w < w_end;
-            if (more) segment(a, out, piece);
-        }
+        if (threadIdx.x == 0) segment(a);
         __syncthreads();
         return more;
     }
+    __device__ __forceinline__ bool whole() const { return s.c0 == 0 && s.c1 == s.chunks; }
+    // Where the sums of a part of an item go: the part that starts the item, or another.
+    __device__ __forceinline__ int slot(int piece) const { return 2 * piece + (s.c0 == 0); }
+    // Notes for the join whether the item that starts here goes on behind the piece.
+    __device__ __forceinline__ void note(const CacheArgs& a, const AttnOut& out, int piece) const {
+        if (threadIdx.x != 0 || s.c0 != 0) return;
+        CutItem c{};
+        if (s.c1 < s.chunks) {
+            c.b = s.b; c.h = s.h; c.row0 = s.row0; c.rows = s.rows;
+            c.piece = piece;
+            c.parts = line.piece_of(s.first + s.chunks - 1) - piece + 1;
+        }
+        if (out.items)
+            out.cut[(s.b * out.tiles + s.row0 / RT) * a.Hkv + s.h] = c;
+        else if (c.rows)
+            out.cut[piece] = c;
+    }
 };
+
+// The entries of items that there are not: tiles of sequences with fewer rows.
+__device__ __forceinline__ void clear_cuts(const CacheArgs& a, const AttnOut& out) {
+    for (int i = threadIdx.x; i < out.items; i += blockDim.x) {
+        const int bt = i / a.Hkv, b = bt / out.tiles;
+        if ((bt - b * out.tiles) * out.rows >= cache_count(a, b) * a.G) out.cut[i] = CutItem{};
+    }
+}
 
 // A kernel that this one's launch may be followed by can be set up meanwhile;
 // it waits for this one's end before it reads anything.
@@ -313,13 +312,15 @@ k_cache_attn_simt(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restric
     extern __shared__ __align__(128) uint8_t smem[];
     allow_next();
     if (blockIdx.x == 0) {
+        clear_cuts(a, out);
         cache_check_call(a, false);
         return;
     }
     const int piece = blockIdx.x - 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sub = lane >> 3, ch = lane & 7;  // token of four, chunk
-    __shared__ Walk walk;
-    if (!walk.begin(a, out, piece)) return;
+    __shared__ Walk<R> walk;
+    if (!out.items && threadIdx.x == 0) out.cut[piece] = CutItem{};
+    if (!walk.begin(a, piece, out.pieces)) return;
     uint8_t* ring = smem + warp * (kSimtStages * 2 * L::kBytes);
     const uint32_t ring_addr = smem_addr(ring);
 
@@ -459,8 +460,9 @@ k_cache_attn_simt(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restric
             for (int i = 0; i < E; ++i) os[(set * R + r) * D + ch * E + i] = o[r][i];
         }
         __syncthreads();
-        const bool whole = s.c0 == 0 && s.c1 == s.chunks;
-        const int slot = walk.slot;
+        const bool whole = walk.whole();
+        const int slot = walk.slot(piece);
+        walk.note(a, out, piece);
         for (int x = threadIdx.x; x < s.rows * D; x += kThreads) {
             const int r = x / D, c = x - r * D;
             float mx = -INFINITY;
@@ -483,7 +485,7 @@ k_cache_attn_simt(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restric
                 if (c == 0) out.ml[(long long)slot * R + r] = make_float2(mx, sum);
             }
         }
-    } while (walk.next(a, out, piece));
+    } while (walk.next(a));
 }
 
 // --------------------------------------------------------- tensor cores
@@ -519,6 +521,14 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
+__device__ __forceinline__ void store4(float* p, float x, float y, float z, float w) {
+    *reinterpret_cast<float4*>(p) = make_float4(x, y, z, w);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float x, float y, float z, float w) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x, y), b = __floats2bfloat162_rn(z, w);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
 constexpr float kNoKey = -1.7e38f;  // a row's maximum before it has seen a key: finite, so that differences are
 
 constexpr int kStages = 2;
@@ -526,13 +536,15 @@ constexpr int kStages = 2;
 // 4 at 128 registers 51.2; 16 rows of 64: 33.0 and 30.9.)
 constexpr int mma_blocks(int d, int NR) { return NR == 1 ? 4 : d == 64 ? (NR == 2 ? 4 : 3) : (NR == 2 ? 3 : 2); }
 
-template <int D, int NR> constexpr int mma_smem() {
+// Q's halves: float rows are two of them
+template <typename T, int D, int NR> constexpr int mma_q_bytes() { return (sizeof(T) == 4 ? 2 : 1) * NR * (D / 16) * 256; }
+template <typename T, int D, int NR> constexpr int mma_smem() {
     constexpr int ring = 4 * kStages * 2 * Grp<D>::kBytes, merge = 4 * 8 * NR * D * 4;
-    return (ring > merge ? ring : merge) + NR * (D / 16) * 256;
+    return (ring > merge ? ring : merge) + mma_q_bytes<T, D, NR>();
 }
 
-// bf16 rows on the tensor cores' register form (m16n8k16, halves in, fp32 out),
-// tiles of 8 NR rows.
+// The tensor cores' register form (m16n8k16, halves in, fp32 out), tiles of 8 NR
+// rows.
 //
 // The codes come from shared memory into the registers of the lanes that feed
 // them to the step, are widened there and never go back to shared memory: one
@@ -551,24 +563,33 @@ template <int D, int NR> constexpr int mma_smem() {
 //         largest entry in [2^14, 2^15), so that bf16 is exact as halves down to 2^-31 of
 //         it; the power goes into the factor f of the scores.
 //   p = 2^(S f - m) in fp32, rounded to halves for the product with V (2^-11 relative; the sum
-//         l takes the unrounded p). m is only moved when a score exceeds it by more than 8,
-//         so p <= 2^8, and only then do lanes compare maxima and are the sums rescaled.
+//         l takes the unrounded p). m starts 7 below a row's first maximum and is moved, to 7
+//         below the maximum, when a score exceeds it by more than 15. So 2^7 <= max p <= 2^15,
+//         the halves' normal numbers reach 2^-21 of the maximum, and only a move makes lanes
+//         compare maxima and rescale sums.
 //   O^T   P^T is S^T's register layout transposed 8 x 8; 2 steps of 16 tokens x d/16 channel tiles.
-template <int D, int NR>
+//
+// float32 rows are each two halves, x = hi + lo with lo = x - hi rounded (22 bits and
+// a sign, 2^-23 of x), p likewise: two products where bf16 has one, with the same
+// exact keys and values. The products are summed in fp32 by steps of 16 tokens
+// and by ordinary additions from there.
+template <typename T, int D, int NR>
 __global__ void __launch_bounds__(kThreads, mma_blocks(D, NR))
-k_cache_attn_mma(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_t* __restrict__ cache, AttnOut out) {
+k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict__ cache, AttnOut out) {
     using L = Grp<D>;
+    constexpr bool F = sizeof(T) == 4;  // float rows
     constexpr int KS = D / 16, NT = D / 8, W = D / 32, RT = 8 * NR, ST = kStages;
     constexpr int GP = NR == 1 ? 2 : 1;  // groups at a time: with more rows the registers hold one
     constexpr int kStage = 2 * L::kBytes;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ Walk walk;
+    __shared__ Walk<RT> walk;
     __shared__ float2 sml[4][RT];
     __shared__ float szf[RT];
     __shared__ int slim[RT];
     __shared__ uint64_t bars[4][ST];
     allow_next();
     if (blockIdx.x == 0) {
+        clear_cuts(a, out);
         cache_check_call(a, false);
         return;
     }
@@ -576,21 +597,22 @@ k_cache_attn_mma(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_t
     const int g = lane >> 2, t4 = lane & 3;
     uint8_t* ring = smem + warp * (ST * kStage);
     const uint32_t ring_addr = smem_addr(ring);
-    uint2* qs = reinterpret_cast<uint2*>(smem + mma_smem<D, NR>() - NR * KS * 256);
+    uint2* qs = reinterpret_cast<uint2*>(smem + mma_smem<T, D, NR>() - mma_q_bytes<T, D, NR>());
     if (lane == 0) {
         for (int i = 0; i < ST; ++i) tc::mbar_init(&bars[warp][i], 2);
         tc::fence_mbar_init();
     }
-    if (!walk.begin(a, out, piece)) return;
+    if (!out.items && threadIdx.x == 0) out.cut[piece] = CutItem{};
+    if (!walk.begin(a, piece, out.pieces)) return;
     int put = 0, take = 0, phase = 0;  // stages of the ring, and the phase of `take`
-    bool dead = false;                 // a wait ran out
+    bool dead = false;                 // a wait ran out: the warp goes on without keys
 
     do {
         const Segment& s = walk.s;
         const int n = walk.sw.n, count = walk.sw.count, b = s.b;
         // rows of a tile see more keys the later their token is
         const int low = row_limit(a, n, count, s.row0 / a.G), top = row_limit(a, n, count, (s.row0 + s.rows - 1) / a.G);
-        const int steps = s.c1 - s.c0;
+        const int steps = dead ? 0 : s.c1 - s.c0;
         // Lane l has the group number of group l & 1 of step l >> 1 in the current run of 16
         // steps, and issues that copy itself; the next run's table entries are loaded a run ahead.
         auto groups = [&](int i0) -> const uint8_t* {
@@ -623,18 +645,20 @@ k_cache_attn_mma(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_t
             const int r = warp * 8 + g;
             int t = 0;
             const long long at = row_offset(a, b, s.h, s.row0 + min(r, s.rows - 1), &t);
-            uint32_t x[D / 8], amax = 0;
+            constexpr int QW = D / 16 * sizeof(T) / 4;  // 16-byte words of a lane's channels
+            uint32_t x[4 * QW], amax = 0;
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
+            for (int i = 0; i < QW; ++i) {
                 uint4 v = make_uint4(0, 0, 0, 0);
                 if (r < s.rows) v = reinterpret_cast<const uint4*>(Q + at * D + t4 * (D / 4))[i];
                 x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
             }
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) amax = max(amax, max(x[i] & 0x7fffu, (x[i] >> 16) & 0x7fffu));
+            for (int i = 0; i < 4 * QW; ++i)
+                amax = max(amax, F ? x[i] & 0x7fffffffu : max(x[i] << 16 & 0x7fff0000u, x[i] & 0x7fff0000u));
             amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            const int ex = (int)(amax >> 7);  // biased exponent of the row's largest entry
+            const int ex = (int)(amax >> 23);  // biased exponent of the row's largest entry
             const int qe = ex == 255 ? 0 : min(141 - ex, 120);
             const float up = pow2(qe), kf = a.scale * kLog2e * pow2(cache_exp(a, 0, s.h));
             if (t4 == 0) {
@@ -644,20 +668,25 @@ k_cache_attn_mma(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_t
             }
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                uint32_t h[2];
+                uint32_t hi[2], lo[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const uint32_t y = x[2 * ks + e];
-                    h[e] = pack_half2(__uint_as_float(y << 16) * up, __uint_as_float(y & 0xffff0000u) * up);
+                    const float y0 = __uint_as_float(F ? x[(4 * ks + 2 * e) % (4 * QW)] : x[2 * ks + e] << 16) * up;
+                    const float y1 = __uint_as_float(F ? x[(4 * ks + 2 * e + 1) % (4 * QW)] : x[2 * ks + e] & 0xffff0000u) * up;
+                    hi[e] = pack_half2(y0, y1);
+                    const float2 h = half2_to_float2(hi[e]);
+                    lo[e] = pack_half2(y0 - h.x, y1 - h.y);
                 }
-                qs[(ks * NR + warp) * 32 + lane] = make_uint2(h[0], h[1]);
+                qs[(ks * NR + warp) * 32 + lane] = make_uint2(hi[0], hi[1]);
+                if (F) qs[((KS + ks) * NR + warp) * 32 + lane] = make_uint2(lo[0], lo[1]);
             }
         }
         __syncthreads();
-        uint2 qf[NR == 1 ? KS : 1];
-        if (NR == 1) {
+        constexpr bool kQRegs = NR == 1 && !F;  // Q in registers, else in shared memory
+        uint2 qf[kQRegs ? KS : 1];
+        if (kQRegs) {
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) qf[ks] = qs[ks * 32 + lane];
+            for (int ks = 0; ks < KS; ++ks) qf[ks % (kQRegs ? KS : 1)] = qs[ks * 32 + lane];
         }
         // of this lane's rows 8 i + 2 t4 and the next
         float zf[NR][2], m[NR][2], l[NR][2], o[NR][NT / 2][4];
@@ -678,7 +707,7 @@ k_cache_attn_mma(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_t
         for (int i = 0; i < steps; ++i) {
             __syncwarp();  // the stage that the next copy goes to has been read
             issue(i + ST - 1);
-            if (!tc::mbar_wait(&bars[warp][take], phase, a.status)) {
+            if (!__all_sync(0xffffffffu, tc::mbar_wait(&bars[warp][take], phase, a.status))) {
                 // give up, but not before the copies in flight have landed (or a second has passed for each)
                 for (int x = i + 1; x < steps && x < i + ST; ++x) {
                     take = take + 1 == ST ? 0 : take + 1;
@@ -697,13 +726,14 @@ k_cache_attn_mma(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_t
                 if (base >= top) break;
 
                 // scores of 16 tokens each: [0], [1] token g, rows 2 t4 and the next; [2], [3] token g + 8
-                float z[NR][GP][4];
+                constexpr int NL = F ? NR : 1;
+                float z[NR][GP][4], zl[NL][GP][4];  // zl: the lower halves' part
 #pragma unroll
                 for (int j = 0; j < NR; ++j)
 #pragma unroll
                     for (int x = 0; x < GP; ++x)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) z[j][x][e] = 0.0f;
+                        for (int e = 0; e < 4; ++e) z[j][x][e] = zl[j % NL][x][e] = 0.0f;
                 uint32_t kw[GP][2][W], sc[GP][2][D / 64];  // [group][token g, g + 8]: codes; scales, each in both halves
 #pragma unroll
                 for (int gi = 0; gi < GP; ++gi) {
@@ -747,12 +777,28 @@ k_cache_attn_mma(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_t
                     for (int k2 = 0; k2 < 2; ++k2)
 #pragma unroll
                         for (int j = 0; j < NR; ++j) {
-                            const uint2 q = NR == 1 ? qf[(2 * wi + k2) % (NR == 1 ? KS : 1)] : qs[((2 * wi + k2) * NR + j) * 32 + lane];
+                            const int ks = 2 * wi + k2;
+                            const uint2 q = kQRegs ? qf[ks % (kQRegs ? KS : 1)] : qs[(ks * NR + j) * 32 + lane];
 #pragma unroll
                             for (int gi = 0; gi < GP; ++gi)
                                 mma_f16(z[j][gi], k8[gi][0][2 * k2], k8[gi][1][2 * k2], k8[gi][0][2 * k2 + 1],
                                         k8[gi][1][2 * k2 + 1], q.x, q.y);
+                            if (F) {
+                                const uint2 ql = qs[((KS + ks) * NR + j) * 32 + lane];
+#pragma unroll
+                                for (int gi = 0; gi < GP; ++gi)
+                                    mma_f16(zl[j % NL][gi], k8[gi][0][2 * k2], k8[gi][1][2 * k2], k8[gi][0][2 * k2 + 1],
+                                            k8[gi][1][2 * k2 + 1], ql.x, ql.y);
+                            }
                         }
+                }
+                if (F) {
+#pragma unroll
+                    for (int j = 0; j < NR; ++j)
+#pragma unroll
+                        for (int x = 0; x < GP; ++x)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) z[j][x][e] += zl[j % NL][x][e];
                 }
                 const bool edge = base + 16 * GP > low;  // some row does not see all of these tokens
                 if (edge) {
@@ -777,7 +823,7 @@ k_cache_attn_mma(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_t
                             y[j][x][e] = fmaf(z[j][x][e], zf[j][e & 1], -m[j][e & 1]);
                             big = fmaxf(big, y[j][x][e]);
                         }
-                if (__any_sync(0xffffffffu, big > 8.0f)) {
+                if (__any_sync(0xffffffffu, big > 15.0f)) {
 #pragma unroll
                     for (int j = 0; j < NR; ++j)
 #pragma unroll
@@ -786,7 +832,7 @@ k_cache_attn_mma(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_t
                             if (GP == 2) v = fmaxf(v, fmaxf(z[j][GP - 1][e], z[j][GP - 1][e + 2]));
 #pragma unroll
                             for (int x = 4; x < 32; x <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
-                            const float mn = fmaxf(m[j][e], v * zf[j][e]), f = ex2(m[j][e] - mn);
+                            const float mn = fmaxf(m[j][e], fmaf(v, zf[j][e], -7.0f)), f = ex2(m[j][e] - mn);
                             m[j][e] = mn;
                             l[j][e] *= f;
 #pragma unroll
@@ -801,7 +847,7 @@ k_cache_attn_mma(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_t
                             }
                         }
                 }
-                uint32_t p[NR][GP][2];  // P^T: [group][tokens 2 t4 and the next, 8 further], row g
+                uint32_t p[NR][GP][2], pl[NL][GP][2];  // P^T: [group][tokens 2 t4 and the next, 8 further], row g
 #pragma unroll
                 for (int j = 0; j < NR; ++j)
 #pragma unroll
@@ -811,7 +857,12 @@ k_cache_attn_mma(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_t
                             const float p0 = ex2(y[j][x][2 * e]), p1 = ex2(y[j][x][2 * e + 1]);
                             l[j][0] += p0;
                             l[j][1] += p1;
-                            p[j][x][e] = transpose8(pack_half2(p0, p1));
+                            const uint32_t h2 = pack_half2(p0, p1);
+                            p[j][x][e] = transpose8(h2);
+                            if (F) {
+                                const float2 hf = half2_to_float2(h2);
+                                pl[j % NL][x][e] = transpose8(pack_half2(p0 - hf.x, p1 - hf.y));
+                            }
                         }
 #pragma unroll
                 for (int gi = 0; gi < GP; ++gi) {
@@ -878,7 +929,17 @@ k_cache_attn_mma(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_t
                             const uint32_t a0 = hmul2(v8[0][0][x], s0), a1 = hmul2(v8[0][1][x], s0);
                             const uint32_t a2 = hmul2(v8[1][0][x], s1), a3 = hmul2(v8[1][1][x], s1);
 #pragma unroll
-                            for (int j = 0; j < NR; ++j) mma_f16(o[j][4 * wi + x], a0, a1, a2, a3, p[j][gi][0], p[j][gi][1]);
+                            for (int j = 0; j < NR; ++j) {
+                                if (!F) {
+                                    mma_f16(o[j][4 * wi + x], a0, a1, a2, a3, p[j][gi][0], p[j][gi][1]);
+                                    continue;
+                                }
+                                float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                                mma_f16(c, a0, a1, a2, a3, pl[j % NL][gi][0], pl[j % NL][gi][1]);
+                                mma_f16(c, a0, a1, a2, a3, p[j][gi][0], p[j][gi][1]);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) o[j][4 * wi + x][e] += c[e];
+                            }
                         }
                     }
                 }
@@ -914,8 +975,9 @@ k_cache_attn_mma(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_t
                                                                      o[j][2 * x + 1][e], o[j][2 * x + 1][e + 2]);
             }
         __syncthreads();
-        const bool whole = s.c0 == 0 && s.c1 == s.chunks;
-        const int slot = walk.slot;
+        const bool whole = walk.whole();
+        const int slot = walk.slot(piece);
+        walk.note(a, out, piece);
         for (int x = threadIdx.x; x < s.rows * C4; x += kThreads) {
             const int r = x / C4, c = x - r * C4;
             float2 v[4];
@@ -939,10 +1001,7 @@ k_cache_attn_mma(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_t
                 int t;
                 const long long at = row_offset(a, b, s.h, s.row0 + r, &t);
                 const float inv = sum == 0.0f ? 0.0f : vscale / sum;
-                const __nv_bfloat162 h0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv),
-                                     h1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-                reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(out.O) + at * D)[c] =
-                    make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+                store4(reinterpret_cast<T*>(out.O) + at * D + 4 * c, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
                 if (out.lse && c == 0) out.lse[at] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * kLn2;
             } else {
                 acc.x *= vscale; acc.y *= vscale; acc.z *= vscale; acc.w *= vscale;
@@ -951,117 +1010,108 @@ k_cache_attn_mma(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_t
             }
         }
         tc::fence_proxy_async();  // the next segment's copies come after these accesses of the ring
-    } while (!__syncthreads_or(dead) && walk.next(a, out, piece));
+    } while (walk.next(a));
 }
 
 // ------------------------------------------------------------------ join
 
-constexpr int kJoinRows = 4, kJoinWarps = 8;
+constexpr int kJoinRows = 2, kJoinWarps = 4;  // rows of a block, warps of a row
 
-// Block (c, y) joins the parts of the item that starts in piece c and ends
-// behind it, rows 4 y to 4 y + 3 at once: each warp adds every eighth part, a lane
-// d/32 channels of each row. It is a chain of loads (the item, the maxima, the
-// sums), so the rows and parts are in flight together.
+// Block (x, y) joins the parts of cut item x, rows 2 y and 2 y + 1: each of a row's
+// four warps adds every fourth part, a lane d/32 channels of it, several parts'
+// loads in flight. (It is a chain of loads, the item, then maxima and sums, then the
+// other warps' results, and takes 2 to 4 us.)
 template <typename T, int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) k_cache_join(CacheArgs a, AttnOut out) {
+__global__ void __launch_bounds__(32 * kJoinRows * kJoinWarps) k_cache_join(CacheArgs a, AttnOut out) {
     constexpr int E = D / 32;
-    __shared__ float acc8[kJoinWarps][kJoinRows][D];
-    __shared__ float sum8[kJoinWarps][kJoinRows];
+    __shared__ float acc8[kJoinRows][kJoinWarps][D];
+    __shared__ float2 ml8[kJoinRows][kJoinWarps];
     wait_previous();
     const CutItem c = out.cut[blockIdx.x];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, R = out.rows;
-    const int r0 = blockIdx.y * kJoinRows, rows = min(c.rows - r0, kJoinRows);
-    if (rows <= 0) return;
-    // part p > 0 begins its piece
-    auto slot = [&](int p) { return (long long)(p == 0 ? c.slot : 2 * (blockIdx.x + p)) * R + r0; };
-    float mx[kJoinRows], sum[kJoinRows], acc[kJoinRows][E];
+    if ((int)blockIdx.y * kJoinRows >= c.rows) return;
+    const int lane = threadIdx.x & 31, sub = threadIdx.x >> 5, mine = sub / kJoinWarps, warp = sub % kJoinWarps;
+    const int r = blockIdx.y * kJoinRows + mine;
+    if (r < c.rows) {
+        // part p > 0 begins its piece
+        auto slot = [&](int p) { return (long long)(2 * (c.piece + p) + (p == 0)) * out.rows + r; };
+        float mx = kNoKey, sum = 0.0f, acc[E];
 #pragma unroll
-    for (int r = 0; r < kJoinRows; ++r) {
-        mx[r] = -INFINITY;
-        sum[r] = 0.0f;
+        for (int i = 0; i < E; ++i) acc[i] = 0.0f;
+        // lane l has the maximum and sum of the l-th of 32 of the warp's parts
+        for (int p0 = warp; p0 < c.parts; p0 += 32 * kJoinWarps) {
+            const int pl = p0 + lane * kJoinWarps;
+            const float2 ml = pl < c.parts ? out.ml[slot(pl)] : make_float2(kNoKey, 0.0f);
+            const float m = fmaxf(ml.x, kNoKey), mn = fmaxf(mx, warp_max(m)), old = exp2f(mx - mn), f = exp2f(m - mn);
+            sum = sum * old + warp_sum(f * ml.y);
+            mx = mn;
 #pragma unroll
-        for (int i = 0; i < E; ++i) acc[r][i] = 0.0f;
-    }
-    for (int p = lane; p < c.parts; p += 32) {
-        const float2* ml = out.ml + slot(p);
+            for (int i = 0; i < E; ++i) acc[i] *= old;
+            const int n = min(32, (c.parts - p0 + kJoinWarps - 1) / kJoinWarps);
+#pragma unroll 8
+            for (int j = 0; j < n; ++j) {
+                const float fj = __shfl_sync(0xffffffffu, f, j);
+                const float* part = out.part + slot(p0 + j * kJoinWarps) * D;
+                float v[E];
+                if (E == 4) {
+                    const float4 u = reinterpret_cast<const float4*>(part)[lane];
+                    v[0] = u.x; v[1] = u.y; v[E - 2] = u.z; v[E - 1] = u.w;
+                } else {
+                    const float2 u = reinterpret_cast<const float2*>(part)[lane];
+                    v[0] = u.x; v[1] = u.y;
+                }
 #pragma unroll
-        for (int r = 0; r < kJoinRows; ++r)
-            if (r < rows) mx[r] = fmaxf(mx[r], ml[r].x);
-    }
-#pragma unroll
-    for (int r = 0; r < kJoinRows; ++r) {
-        mx[r] = warp_max(mx[r]);
-        if (mx[r] == -INFINITY) mx[r] = 0.0f;  // no part has a key of this row
-    }
-#pragma unroll 2
-    for (int p = warp; p < c.parts; p += kJoinWarps) {
-        const long long at = slot(p);
-#pragma unroll
-        for (int r = 0; r < kJoinRows; ++r) {
-            if (r >= rows) continue;
-            const float2 ml = out.ml[at + r];
-            float v[E];
-            if (E == 4) {
-                const float4 u = reinterpret_cast<const float4*>(out.part + (at + r) * D)[lane];
-                v[0] = u.x; v[1] = u.y; v[E - 2] = u.z; v[E - 1] = u.w;
-            } else {
-                const float2 u = reinterpret_cast<const float2*>(out.part + (at + r) * D)[lane];
-                v[0] = u.x; v[1] = u.y;
+                for (int i = 0; i < E; ++i) acc[i] = fmaf(fj, v[i], acc[i]);
             }
-            const float f = exp2f(ml.x - mx[r]);
-            sum[r] = fmaf(f, ml.y, sum[r]);
-#pragma unroll
-            for (int i = 0; i < E; ++i) acc[r][i] = fmaf(f, v[i], acc[r][i]);
         }
-    }
 #pragma unroll
-    for (int r = 0; r < kJoinRows; ++r) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) acc8[warp][r][lane * E + i] = acc[r][i];
-        if (lane == 0) sum8[warp][r] = sum[r];
+        for (int i = 0; i < E; ++i) acc8[mine][warp][lane * E + i] = acc[i];
+        if (lane == 0) ml8[mine][warp] = make_float2(mx, sum);
     }
     __syncthreads();
-    for (int x = threadIdx.x; x < rows * D; x += 32 * kJoinWarps) {
-        const int r = x / D, i = x - r * D;
-        float s = 0.0f, v = 0.0f;
+    if (r >= c.rows) return;
+    float top = kNoKey, s = 0.0f, f[kJoinWarps];
 #pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) {
-            s += sum8[w][r];
-            v += acc8[w][r][i];
-        }
-        int t;
-        const long long at = row_offset(a, c.b, c.h, c.row0 + r0 + r, &t);
-        reinterpret_cast<T*>(out.O)[at * D + i] = from_f<T>(s == 0.0f ? 0.0f : v / s);
-        if (out.lse && i == 0) {
-            float top = mx[0];
+    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, ml8[mine][w].x);
 #pragma unroll
-            for (int q = 1; q < kJoinRows; ++q) top = q == r ? mx[q] : top;
-            out.lse[at] = s == 0.0f ? -INFINITY : (top + log2f(s)) * kLn2;
-        }
+    for (int w = 0; w < kJoinWarps; ++w) {
+        f[w] = exp2f(ml8[mine][w].x - top);
+        s = fmaf(f[w], ml8[mine][w].y, s);
     }
+    int t;
+    const long long at = row_offset(a, c.b, c.h, c.row0 + r, &t);
+    const int i0 = warp * 32 + lane;
+    if (i0 < D) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) v = fmaf(f[w], acc8[mine][w][i0], v);
+        reinterpret_cast<T*>(out.O)[at * D + i0] = from_f<T>(s == 0.0f ? 0.0f : v / s);
+    }
+    if (out.lse && i0 == 0) out.lse[at] = s == 0.0f ? -INFINITY : (top + log2f(s)) * kLn2;
 }
 
 // ------------------------------------------------------------------ launch
 
-static long long max_chunks(const CacheArgs& a, int rtile) {
+// Units of the line, at most (cache_attn.cu's Line counts them in 32 bits).
+static long long cache_attn_units(const CacheArgs& a, int rtile, int extra) {
     const long long tiles = ((long long)a.G * a.T + rtile - 1) / rtile;
     const long long len = ((long long)a.cols * a.page + kChunk - 1) / kChunk;
-    return (long long)a.B * a.Hkv * tiles * len;
+    return (long long)a.B * a.Hkv * tiles * (len + extra);
 }
 
 CachePlan cache_attn_plan(const CacheArgs& a, int d, int dtype, unsigned flags) {
     CachePlan p;
     const long long rows = (long long)a.G * a.T;
-    p.tensor = dtype == 1 && !(flags & MITA_FLAG_SIMT);
+    p.tensor = !(flags & MITA_FLAG_SIMT);
     int blocks = 4;  // per SM
     if (p.tensor) {
-        p.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+        p.rows = rows <= 8 ? 8 : rows <= 16 || dtype == 0 ? 16 : 32;
         blocks = mma_blocks(d, p.rows / 8);
     } else {
         p.rows = rows == 1 ? 1 : 4;
     }
     // one of the resident blocks checks the call's indexes
-    p.pieces = (int)std::min<long long>((long long)blocks * num_sms() - 1, max_chunks(a, p.rows));
+    p.pieces = (int)std::min<long long>((long long)blocks * num_sms() - 1, cache_attn_units(a, p.rows, 0));
+    p.fits = cache_attn_units(a, p.rows, kExtra) < (1LL << 31);
     p.parts = (size_t)2 * p.pieces * p.rows;
     return p;
 }
@@ -1075,8 +1125,8 @@ static cudaError_t join_t(const CacheArgs& a, const AttnOut& o, cudaStream_t st)
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t c{};
-    c.gridDim = dim3(o.pieces, (o.rows + kJoinRows - 1) / kJoinRows);
-    c.blockDim = dim3(32 * kJoinWarps);
+    c.gridDim = dim3(o.cuts, (o.rows + kJoinRows - 1) / kJoinRows);
+    c.blockDim = dim3(32 * kJoinRows * kJoinWarps);
     c.stream = st;
     c.attrs = &at;
     c.numAttrs = 1;
@@ -1095,30 +1145,39 @@ static cudaError_t simt_t(const CacheArgs& a, const void* Q, const uint8_t* cach
     return join_t<T, D>(a, o, st);
 }
 
-template <int D, int NR>
+template <typename T, int D, int NR>
 static cudaError_t mma_t(const CacheArgs& a, const void* Q, const uint8_t* cache, const AttnOut& o, cudaStream_t st) {
-    constexpr int smem = mma_smem<D, NR>();
+    constexpr int smem = mma_smem<T, D, NR>();
     static_assert(mma_blocks(D, NR) * (smem + 3 * 1024) <= 228 * 1024, "the blocks that a call counts on fit an SM");
-    const cudaError_t e = cudaFuncSetAttribute(k_cache_attn_mma<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(k_cache_attn_mma<T, D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    k_cache_attn_mma<D, NR><<<o.pieces + 1, kThreads, smem, st>>>(a, (const __nv_bfloat16*)Q, cache, o);
+    k_cache_attn_mma<T, D, NR><<<o.pieces + 1, kThreads, smem, st>>>(a, (const T*)Q, cache, o);
     count_launch();
-    return join_t<__nv_bfloat16, D>(a, o, st);
+    return join_t<T, D>(a, o, st);
 }
 
 template <int D>
 static cudaError_t attn_t(const CacheArgs& a, const CachePlan& p, int dtype, const void* Q, const uint8_t* cache,
                           const AttnOut& o, cudaStream_t st) {
+    using bf16 = __nv_bfloat16;
+    if (dtype == 0) {
+        if (p.tensor) return p.rows == 8 ? mma_t<float, D, 1>(a, Q, cache, o, st) : mma_t<float, D, 2>(a, Q, cache, o, st);
+        return p.rows == 1 ? simt_t<float, D, 1>(a, Q, cache, o, st) : simt_t<float, D, 4>(a, Q, cache, o, st);
+    }
     if (p.tensor)
-        return p.rows == 8 ? mma_t<D, 1>(a, Q, cache, o, st)
-               : p.rows == 16 ? mma_t<D, 2>(a, Q, cache, o, st) : mma_t<D, 4>(a, Q, cache, o, st);
-    if (dtype == 0) return p.rows == 1 ? simt_t<float, D, 1>(a, Q, cache, o, st) : simt_t<float, D, 4>(a, Q, cache, o, st);
-    return p.rows == 1 ? simt_t<__nv_bfloat16, D, 1>(a, Q, cache, o, st) : simt_t<__nv_bfloat16, D, 4>(a, Q, cache, o, st);
+        return p.rows == 8    ? mma_t<bf16, D, 1>(a, Q, cache, o, st)
+               : p.rows == 16 ? mma_t<bf16, D, 2>(a, Q, cache, o, st)
+                              : mma_t<bf16, D, 4>(a, Q, cache, o, st);
+    return p.rows == 1 ? simt_t<bf16, D, 1>(a, Q, cache, o, st) : simt_t<bf16, D, 4>(a, Q, cache, o, st);
 }
 
 cudaError_t launch_cache_attn(const CacheArgs& a, const CachePlan& p, int d, int dtype, const void* Q,
                               const void* cache, void* O, float* lse, const CacheParts& parts, cudaStream_t st) {
-    const AttnOut o{O, lse, parts.part, parts.ml, (CutItem*)parts.cut, p.pieces, p.rows};
+    const int tiles = (int)(((long long)a.G * a.T + p.rows - 1) / p.rows);
+    const long long items = (long long)a.B * tiles * a.Hkv;
+    const bool by_item = items <= p.pieces;
+    const AttnOut o{O, lse, parts.part, parts.ml, (CutItem*)parts.cut, p.pieces, p.rows,
+                    by_item ? (int)items : p.pieces, by_item ? (int)items : 0, tiles};
     const uint8_t* c = (const uint8_t*)cache;
     prof_mark(st, "cache_attention");
     return d == 64 ? attn_t<64>(a, p, dtype, Q, c, o, st) : attn_t<128>(a, p, dtype, Q, c, o, st);

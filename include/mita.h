@@ -294,7 +294,8 @@ mita_status mita_cache_read(const mita_cache_params* p, const void* cache, const
  * ln sum exp(scale q.k) over the seen keys, -infinity without any, with which the
  * rows can be joined with attention over other keys (mita_forward's shared
  * slots, say). count > len is allowed: rows before the first token see none.
- * bf16 runs on tensor cores, float32 and MITA_FLAG_SIMT on CUDA cores in fp32. */
+ * Runs on tensor cores, float32 with each number as the sum of two halves (22
+ * bits), and with MITA_FLAG_SIMT on CUDA cores in fp32. */
 mita_status mita_cache_attention(const mita_cache_params* p, const void* Q, const void* cache, const int32_t* table,
                                  const int32_t* len, const int32_t* count, const int32_t* exps, void* O,
                                  float* lse_out, void* ws, size_t ws_bytes, void* stream);

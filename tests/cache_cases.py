@@ -73,8 +73,10 @@ def attention_bound(dtype, tensor_cores, o, spread, q, k, v, limits, scale):
         much relative, the weights' sum likewise; the difference z - max and the
         exponential itself: 2^-21 (1 + |z - max|), with |z - max| at most twice
         the magnitude above and at most 64 where the weight is not nothing;
-      - weights as halves on tensor cores: 2^-11 each, or 2^-25 of the largest
-        below 2^-14 of it, against a sum of at least the largest;
+      - bf16 on tensor cores rounds the weights to halves: 2^-11 each, or 2^-25 of
+        the largest below 2^-14 of it, against a sum of at least the largest;
+        float32 makes two halves of a query's entry and of a weight: 2^-23 each,
+        which the next two lines' chains and the scores' d additions have room for;
       - sums over keys in fp32: 2^-23 for every addition in a chain, of which
         there are at most one per 16 keys and 64 more for the joins."""
     u = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
