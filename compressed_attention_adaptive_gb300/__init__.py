@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -73,9 +74,9 @@ class _CCacheParams(ctypes.Structure):
                 ("scale", ctypes.c_float), ("flags", ctypes.c_uint), ("dtype", ctypes.c_int)]
 
 
-@dataclasses.dataclass
+@dataclasses.dataclass(frozen=True)
 class CacheParams:
-    """Mirror of ``mita_cache_params`` (see include/mita.h)."""
+    """Mirror of ``mita_cache_params`` (see include/mita.h); its C form is made once."""
     B: int
     H: int
     H_kv: int
@@ -88,9 +89,13 @@ class CacheParams:
     flags: int = 0
     dtype: int = BF16
 
-    def c(self):
+    @functools.cached_property
+    def _c(self):
         return _CCacheParams(self.B, self.H, self.H_kv, self.T, self.d, self.page, self.n_pages, self.max_pages,
                              float(self.scale), int(self.flags), int(self.dtype))
+
+    def c(self):
+        return self._c
 
 
 def lib():

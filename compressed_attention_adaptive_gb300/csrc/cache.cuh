@@ -82,6 +82,7 @@ struct CacheParts {
     float* part;  // [parts][d]
     float2* ml;   // [parts]
     void* cut;    // [pieces] of kCutBytes (as many cut items there can be)
+    int* found;   // [pieces]
 };
 
 // cache.cu
@@ -113,32 +114,16 @@ __device__ __forceinline__ int cache_group(const CacheArgs& a, int b, int h, int
     return (pg * a.Hkv + h) * a.pgroups + (gi - col * a.pgroups);
 }
 
-// Run by one whole block of a call: checks every index the call uses and
-// stores the call's status word. One block can do it for all, since a page's
-// entry is 4 bytes against at least 1152 bytes of codes for each head; the
-// other blocks only leave out what is out of range.
-__device__ inline void cache_check_call(const CacheArgs& a, bool rows_only) {
-    int bad = 0;
-    const int w = threadIdx.x >> 5, l = threadIdx.x & 31, nw = blockDim.x >> 5;
+__device__ __forceinline__ bool bad_len(const CacheArgs& a, int b) {
+    return a.len[b] != cache_len(a, b) || (a.count && a.count[b] != cache_count(a, b));
+}
+// Run by the threads of one block.
+__device__ __forceinline__ bool bad_exps(const CacheArgs& a) {
+    bool bad = false;
     if (a.exps)
-        for (int i = threadIdx.x; i < 2 * a.Hkv; i += blockDim.x) bad |= abs(a.exps[i]) > kMaxExp || a.exps[i] == INT_MIN;
-    for (int b = w; b < a.B; b += nw) {
-        const int n = cache_len(a, b), c = cache_count(a, b);
-        bad |= a.len[b] != n || (a.count && a.count[b] != c);
-        if (c == 0) continue;
-        if (rows_only) bad |= c > n;
-        const int first = rows_only ? max(n - c, 0) / a.page : 0, last = (n + a.page - 1) / a.page;
-        const int* tb = a.table + (long long)b * a.cols;
-        int i = first + l;
-        for (; i + 96 < last; i += 128) {  // four loads in flight
-            const int p0 = tb[i], p1 = tb[i + 32], p2 = tb[i + 64], p3 = tb[i + 96];
-            bad |= (unsigned)p0 >= (unsigned)a.n_pages || (unsigned)p1 >= (unsigned)a.n_pages ||
-                   (unsigned)p2 >= (unsigned)a.n_pages || (unsigned)p3 >= (unsigned)a.n_pages;
-        }
-        for (; i < last; i += 32) bad |= (unsigned)tb[i] >= (unsigned)a.n_pages;
-    }
-    bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) *a.status = bad ? kStBounds : kStOk;
+        for (int i = threadIdx.x; i < 2 * a.Hkv; i += blockDim.x)
+            bad |= (unsigned)(a.exps[i] + kMaxExp) > (unsigned)(2 * kMaxExp);
+    return bad;
 }
 
 // ------------------------------------------------------------- conversions

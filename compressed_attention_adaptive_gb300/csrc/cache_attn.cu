@@ -22,6 +22,7 @@
 #include <limits.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "cache.cuh"
 #include "tc.cuh"
@@ -48,6 +49,7 @@ struct AttnOut {
     float* part;   // [2 * pieces][rows][d]
     float2* ml;    // [2 * pieces][rows] (maximum in log2 units, sum)
     CutItem* cut;      // [cuts]
+    int* found;        // [pieces]: what a piece found wrong, for the call's status word
     int pieces, rows;  // pieces of the line, rows of a tile
     // The cut items, by their number (sequence, tile, head) when there are no more items
     // than pieces, else by the piece that they start in.
@@ -215,12 +217,25 @@ template <int RT> struct Walk {
     }
 };
 
-// The entries of items that there are not: tiles of sequences with fewer rows.
-__device__ __forceinline__ void clear_cuts(const CacheArgs& a, const AttnOut& out) {
+// What a piece finds wrong; the join makes the call's status word of it. Between
+// them the pieces read every table entry that the call uses; the first also
+// checks the lengths, counts and exponents, and notes the items that there are
+// not (tiles of sequences with fewer rows) as not cut.
+enum : int { kFoundBounds = 1, kFoundTimeout = 2 };
+__device__ __forceinline__ int first_piece(const CacheArgs& a, const AttnOut& out) {
+    bool bad = bad_exps(a);
+    for (int b = threadIdx.x; b < a.B; b += blockDim.x) bad |= bad_len(a, b);
     for (int i = threadIdx.x; i < out.items; i += blockDim.x) {
         const int bt = i / a.Hkv, b = bt / out.tiles;
         if ((bt - b * out.tiles) * out.rows >= cache_count(a, b) * a.G) out.cut[i] = CutItem{};
     }
+    return bad ? kFoundBounds : 0;
+}
+// The end of a piece, by the whole block.
+__device__ __forceinline__ void end_piece(const CacheArgs& a, const AttnOut& out, int piece, int found) {
+    if (piece == 0) found |= first_piece(a, out);
+    const int bounds = __syncthreads_or(found & kFoundBounds), timeout = __syncthreads_or(found & kFoundTimeout);
+    if (threadIdx.x == 0) out.found[piece] = (bounds ? kFoundBounds : 0) | (timeout ? kFoundTimeout : 0);
 }
 
 // A kernel that this one's launch may be followed by can be set up meanwhile;
@@ -253,21 +268,27 @@ template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.
 // table entries are loaded a run ahead.
 struct GroupRun {
     int cur, nxt;
-    __device__ __forceinline__ static int load(const CacheArgs& a, const Segment& s, int n, int warp, int lane, int i0) {
+    // -1: behind the segment or the last key that a row sees (n), or no page of the pool
+    __device__ __forceinline__ static int load(const CacheArgs& a, const Segment& s, int n, int warp, int lane, int i0,
+                                               int* found) {
         const int step = i0 + (lane >> 1);
         const int gi = ((s.c0 + step) * kChunk + warp * kStep) / kGroup + (lane & 1);
-        return s.c0 + step < s.c1 && gi * kGroup < n ? cache_group(a, s.b, s.h, gi) : -1;
+        if (s.c0 + step >= s.c1 || gi * kGroup >= n) return -1;
+        const int g = cache_group(a, s.b, s.h, gi);
+        if (g < 0) *found |= kFoundBounds;
+        return g;
     }
-    __device__ __forceinline__ void begin(const CacheArgs& a, const Segment& s, int n, int warp, int lane) {
-        cur = load(a, s, n, warp, lane, 0);
-        nxt = load(a, s, n, warp, lane, 16);
+    __device__ __forceinline__ void begin(const CacheArgs& a, const Segment& s, int n, int warp, int lane, int* found) {
+        cur = load(a, s, n, warp, lane, 0, found);
+        nxt = load(a, s, n, warp, lane, 16, found);
     }
     // group g of step i; called once per step, in order
     __device__ __forceinline__ int get(int i, int g) const { return __shfl_sync(0xffffffffu, cur, 2 * (i & 15) + g); }
-    __device__ __forceinline__ void advance(const CacheArgs& a, const Segment& s, int n, int warp, int lane, int i) {
+    __device__ __forceinline__ void advance(const CacheArgs& a, const Segment& s, int n, int warp, int lane, int i,
+                                            int* found) {
         if ((i & 15) == 15) {
             cur = nxt;
-            nxt = load(a, s, n, warp, lane, i + 17);
+            nxt = load(a, s, n, warp, lane, i + 17, found);
         }
     }
 };
@@ -311,16 +332,15 @@ k_cache_attn_simt(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restric
     constexpr int E = D / 8;  // channels of a lane
     extern __shared__ __align__(128) uint8_t smem[];
     allow_next();
-    if (blockIdx.x == 0) {
-        clear_cuts(a, out);
-        cache_check_call(a, false);
-        return;
-    }
-    const int piece = blockIdx.x - 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int found = 0;
+    const int piece = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sub = lane >> 3, ch = lane & 7;  // token of four, chunk
     __shared__ Walk<R> walk;
     if (!out.items && threadIdx.x == 0) out.cut[piece] = CutItem{};
-    if (!walk.begin(a, piece, out.pieces)) return;
+    if (!walk.begin(a, piece, out.pieces)) {
+        end_piece(a, out, piece, 0);
+        return;
+    }
     uint8_t* ring = smem + warp * (kSimtStages * 2 * L::kBytes);
     const uint32_t ring_addr = smem_addr(ring);
 
@@ -347,19 +367,19 @@ k_cache_attn_simt(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restric
         }
         const int steps = s.c1 - s.c0;
         GroupRun gr;
-        gr.begin(a, s, min(n, top), warp, lane);
+        gr.begin(a, s, min(n, top), warp, lane, &found);
         int issued = 0;
         for (; issued < kSimtStages - 1; ++issued) {
             const int g0 = gr.get(issued, 0), g1 = gr.get(issued, 1);
             if (issued < steps) stage_step<D>(cache, ring_addr + issued * 2 * L::kBytes, g0, g1, lane); else copy_commit();
-            gr.advance(a, s, min(n, top), warp, lane, issued);
+            gr.advance(a, s, min(n, top), warp, lane, issued, &found);
         }
         for (int i = 0; i < steps; ++i) {
             const int nx = i + kSimtStages - 1;
             const int g0 = gr.get(nx, 0), g1 = gr.get(nx, 1);
             __syncwarp();
             if (nx < steps) stage_step<D>(cache, ring_addr + (nx % kSimtStages) * 2 * L::kBytes, g0, g1, lane); else copy_commit();
-            gr.advance(a, s, min(n, top), warp, lane, nx);
+            gr.advance(a, s, min(n, top), warp, lane, nx, &found);
             copy_wait<kSimtStages - 1>();
             __syncwarp();
             const int base = (s.c0 + i) * kChunk + warp * kStep;
@@ -486,6 +506,7 @@ k_cache_attn_simt(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restric
             }
         }
     } while (walk.next(a));
+    end_piece(a, out, piece, found);
 }
 
 // --------------------------------------------------------- tensor cores
@@ -588,12 +609,8 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
     __shared__ int slim[RT];
     __shared__ uint64_t bars[4][ST];
     allow_next();
-    if (blockIdx.x == 0) {
-        clear_cuts(a, out);
-        cache_check_call(a, false);
-        return;
-    }
-    const int piece = blockIdx.x - 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int found = 0;
+    const int piece = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t4 = lane & 3;
     uint8_t* ring = smem + warp * (ST * kStage);
     const uint32_t ring_addr = smem_addr(ring);
@@ -603,7 +620,10 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
         tc::fence_mbar_init();
     }
     if (!out.items && threadIdx.x == 0) out.cut[piece] = CutItem{};
-    if (!walk.begin(a, piece, out.pieces)) return;
+    if (!walk.begin(a, piece, out.pieces)) {
+        end_piece(a, out, piece, 0);
+        return;
+    }
     int put = 0, take = 0, phase = 0;  // stages of the ring, and the phase of `take`
     bool dead = false;                 // a wait ran out: the warp goes on without keys
 
@@ -616,7 +636,7 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
         // Lane l has the group number of group l & 1 of step l >> 1 in the current run of 16
         // steps, and issues that copy itself; the next run's table entries are loaded a run ahead.
         auto groups = [&](int i0) -> const uint8_t* {
-            const int gi = GroupRun::load(a, s, top, warp, lane, i0);
+            const int gi = GroupRun::load(a, s, top, warp, lane, i0, &found);
             return gi < 0 ? nullptr : cache + (long long)gi * L::kBytes;
         };
         const uint8_t *gcur = groups(0), *gnxt = groups(16);
@@ -715,6 +735,7 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
                     tc::mbar_wait(&bars[warp][take], phase, a.status);
                 }
                 dead = true;
+                found |= kFoundTimeout;
                 break;
             }
             const uint8_t* st = ring + take * kStage;
@@ -1011,6 +1032,7 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
         }
         tc::fence_proxy_async();  // the next segment's copies come after these accesses of the ring
     } while (walk.next(a));
+    end_piece(a, out, piece, found);
 }
 
 // ------------------------------------------------------------------ join
@@ -1027,6 +1049,14 @@ __global__ void __launch_bounds__(32 * kJoinRows * kJoinWarps) k_cache_join(Cach
     __shared__ float acc8[kJoinRows][kJoinWarps][D];
     __shared__ float2 ml8[kJoinRows][kJoinWarps];
     wait_previous();
+    if (blockIdx.x == gridDim.x - 1) {
+        if (blockIdx.y) return;
+        int found = 0;
+        for (int i = threadIdx.x; i < out.pieces; i += blockDim.x) found |= out.found[i];
+        const int bounds = __syncthreads_or(found & kFoundBounds), timeout = __syncthreads_or(found & kFoundTimeout);
+        if (threadIdx.x == 0) *a.status = timeout ? kStTimeout : bounds ? kStBounds : kStOk;
+        return;
+    }
     const CutItem c = out.cut[blockIdx.x];
     if ((int)blockIdx.y * kJoinRows >= c.rows) return;
     const int lane = threadIdx.x & 31, sub = threadIdx.x >> 5, mine = sub / kJoinWarps, warp = sub % kJoinWarps;
@@ -1109,8 +1139,7 @@ CachePlan cache_attn_plan(const CacheArgs& a, int d, int dtype, unsigned flags) 
     } else {
         p.rows = rows == 1 ? 1 : 4;
     }
-    // one of the resident blocks checks the call's indexes
-    p.pieces = (int)std::min<long long>((long long)blocks * num_sms() - 1, cache_attn_units(a, p.rows, 0));
+    p.pieces = (int)std::min<long long>((long long)blocks * num_sms(), cache_attn_units(a, p.rows, 0));
     p.fits = cache_attn_units(a, p.rows, kExtra) < (1LL << 31);
     p.parts = (size_t)2 * p.pieces * p.rows;
     return p;
@@ -1119,13 +1148,13 @@ CachePlan cache_attn_plan(const CacheArgs& a, int d, int dtype, unsigned flags) 
 template <typename T, int D>
 static cudaError_t join_t(const CacheArgs& a, const AttnOut& o, cudaStream_t st) {
     cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || o.pieces == 1) return e;
+    if (e != cudaSuccess) return e;
     prof_mark(st, "cache_join");
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t c{};
-    c.gridDim = dim3(o.cuts, (o.rows + kJoinRows - 1) / kJoinRows);
+    c.gridDim = dim3(o.cuts + 1, (o.rows + kJoinRows - 1) / kJoinRows);
     c.blockDim = dim3(32 * kJoinRows * kJoinWarps);
     c.stream = st;
     c.attrs = &at;
@@ -1135,12 +1164,26 @@ static cudaError_t join_t(const CacheArgs& a, const AttnOut& o, cudaStream_t st)
     return e;
 }
 
+// Sets a kernel's shared memory limit, once per device (`done`: a bit for each of
+// the first 64; above those every time).
+static cudaError_t set_smem_once(const void* f, int bytes, std::atomic<unsigned long long>* done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ULL << dev : 0;
+    if (done->load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
 template <typename T, int D, int R>
 static cudaError_t simt_t(const CacheArgs& a, const void* Q, const uint8_t* cache, const AttnOut& o, cudaStream_t st) {
     constexpr int smem = simt_smem<D, R>();
-    const cudaError_t e = cudaFuncSetAttribute(k_cache_attn_simt<T, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e = set_smem_once((const void*)k_cache_attn_simt<T, D, R>, smem, &done);
     if (e != cudaSuccess) return e;
-    k_cache_attn_simt<T, D, R><<<o.pieces + 1, kThreads, smem, st>>>(a, (const T*)Q, cache, o);
+    k_cache_attn_simt<T, D, R><<<o.pieces, kThreads, smem, st>>>(a, (const T*)Q, cache, o);
     count_launch();
     return join_t<T, D>(a, o, st);
 }
@@ -1149,9 +1192,10 @@ template <typename T, int D, int NR>
 static cudaError_t mma_t(const CacheArgs& a, const void* Q, const uint8_t* cache, const AttnOut& o, cudaStream_t st) {
     constexpr int smem = mma_smem<T, D, NR>();
     static_assert(mma_blocks(D, NR) * (smem + 3 * 1024) <= 228 * 1024, "the blocks that a call counts on fit an SM");
-    const cudaError_t e = cudaFuncSetAttribute(k_cache_attn_mma<T, D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e = set_smem_once((const void*)k_cache_attn_mma<T, D, NR>, smem, &done);
     if (e != cudaSuccess) return e;
-    k_cache_attn_mma<T, D, NR><<<o.pieces + 1, kThreads, smem, st>>>(a, (const T*)Q, cache, o);
+    k_cache_attn_mma<T, D, NR><<<o.pieces, kThreads, smem, st>>>(a, (const T*)Q, cache, o);
     count_launch();
     return join_t<T, D>(a, o, st);
 }
@@ -1176,7 +1220,7 @@ cudaError_t launch_cache_attn(const CacheArgs& a, const CachePlan& p, int d, int
     const int tiles = (int)(((long long)a.G * a.T + p.rows - 1) / p.rows);
     const long long items = (long long)a.B * tiles * a.Hkv;
     const bool by_item = items <= p.pieces;
-    const AttnOut o{O, lse, parts.part, parts.ml, (CutItem*)parts.cut, p.pieces, p.rows,
+    const AttnOut o{O, lse, parts.part, parts.ml, (CutItem*)parts.cut, parts.found, p.pieces, p.rows,
                     by_item ? (int)items : p.pieces, by_item ? (int)items : 0, tiles};
     const uint8_t* c = (const uint8_t*)cache;
     prof_mark(st, "cache_attention");
