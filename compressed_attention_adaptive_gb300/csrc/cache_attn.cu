@@ -19,243 +19,18 @@
 // one that has a part writes the unnormalized sums, and k_cache_join adds the
 // parts. Everything is derived from the lengths on the device, so a captured
 // call follows them when it is replayed.
-#include <limits.h>
-
 #include <algorithm>
 #include <atomic>
 
-#include "cache.cuh"
-#include "tc.cuh"
+#include "cache_walk.cuh"
 
 namespace mita {
 
-constexpr int kChunk = 128;    // tokens of a block's step
-constexpr int kStep = 32;      // tokens of a warp's step (4 warps)
+constexpr int kStep = 32;  // tokens of a warp's step (4 warps)
 constexpr int kThreads = 128;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
-// An item that is cut: the join's work. rows = 0: nothing to join here.
-struct CutItem {
-    int b, h, row0, rows;
-    int piece, parts;  // the first part's piece, and the pieces it goes over
-};
-
-static_assert(sizeof(CutItem) == kCutBytes, "the workspace holds CutItems");
-
-struct AttnOut {
-    void* O;
-    float* lse;    // or null
-    float* part;   // [2 * pieces][rows][d]
-    float2* ml;    // [2 * pieces][rows] (maximum in log2 units, sum)
-    CutItem* cut;      // [cuts]
-    int* found;        // [pieces]: what a piece found wrong, for the call's status word
-    int pieces, rows;  // pieces of the line, rows of a tile
-    // The cut items, by their number (sequence, tile, head) when there are no more items
-    // than pieces, else by the piece that they start in.
-    int cuts, items, tiles;  // items: 0 in the second case; tiles of a sequence with T rows
-};
-
-// One sequence's share of the line. Its items are cut into chunks, and each item
-// takes `extra` units more than its chunks: what starting and ending an item costs
-// a block (loading Q, the first copies' latency, joining the warps), so that
-// blocks with many short items get fewer chunks.
-struct SeqWork {
-    int n, count, rows, chunks, items;
-};
-__device__ __forceinline__ SeqWork seq_work(const CacheArgs& a, int b, int rtile) {
-    SeqWork s;
-    s.n = cache_len(a, b);
-    s.count = cache_count(a, b);
-    s.rows = s.count * a.G;
-    s.chunks = max(1, (s.n + kChunk - 1) / kChunk);
-    s.items = (s.rows + rtile - 1) / rtile * a.Hkv;
-    return s;
-}
-
-// With less than kFew chunks per block an item's start is not counted: its blocks
-// run side by side then, and none has many. (64 sequences of 33 to 8191 tokens: the
-// slowest block at 69 us with the median at 49 without this, see the plan below.)
-constexpr int kExtra = 2, kFew = 8;
-
-// The line of units, cut into `pieces` pieces that differ by one unit at most.
-struct Line {
-    int pieces, q, r, extra;
-    __device__ __forceinline__ int at(int c) const { return c * q + min(c, r); }
-    __device__ __forceinline__ int piece_of(int x) const {
-        const int head = r * (q + 1);
-        return x < head ? x / (q + 1) : r + (x - head) / q;
-    }
-};
-
-__device__ __forceinline__ int warp_scan(int x, int lane) {
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    return x;
-}
-
-// One block's part of an item.
-struct Segment {
-    int b, h, row0, rows;  // sequence, cache head, first row and rows of the tile
-    int c0, c1, chunks;    // chunks [c0, c1) of the item's `chunks`
-    int first;             // the item's chunk 0 on the line
-};
-
-// A block's walk along its piece, in shared memory: registers are for the sums.
-// The first warp finds the start, thread 0 moves it; begin() and next() are called
-// by the whole block and leave the next segment in `s`. A piece holds at most one
-// segment of an item that began before it (the first) and one of an item that goes
-// on behind it (the last).
-template <int RT> struct Walk {
-    Line line;
-    int w, w_end, before, b;  // position; units before sequence b
-    SeqWork sw;
-    Segment s;
-    bool more;
-
-    // The next segment from w on, if there is one.
-    __device__ __forceinline__ void segment(const CacheArgs& a) {
-        more = false;
-        while (w < w_end) {
-            const int len = sw.chunks + line.extra;
-            if (w - before >= sw.items * len) {  // next sequence with work
-                before += sw.items * len;
-                sw = seq_work(a, ++b, RT);
-                continue;
-            }
-            const int item = (w - before) / len, start = before + item * len;
-            const int tile = item / a.Hkv;
-            s.b = b;
-            s.h = item - tile * a.Hkv;
-            s.row0 = tile * RT;
-            s.rows = min(RT, sw.rows - s.row0);
-            s.chunks = sw.chunks;
-            s.first = start + line.extra;
-            s.c0 = max(w - s.first, 0);
-            s.c1 = min(s.chunks, w_end - s.first);
-            w = start + len;
-            if (s.c0 < s.c1) {
-                more = true;
-                return;
-            }
-        }
-    }
-    __device__ __forceinline__ bool begin(const CacheArgs& a, int piece, int max_pieces) {
-        if (threadIdx.x < 32) {
-            const int lane = threadIdx.x;
-            SeqWork mine{};
-            unsigned items = 0, chunks = 0;
-            for (int b0 = 0; b0 < a.B; b0 += 32) {
-                mine.items = 0;
-                if (b0 + lane < a.B) mine = seq_work(a, b0 + lane, RT);
-                items += mine.items;
-                chunks += mine.items * mine.chunks;
-            }
-            items = __reduce_add_sync(0xffffffffu, items);
-            chunks = __reduce_add_sync(0xffffffffu, chunks);
-            Line l;
-            l.extra = chunks >= (unsigned)max_pieces * kFew ? kExtra : 0;
-            const int total = (int)(chunks + items * l.extra);
-            l.pieces = min(max_pieces, total);
-            l.q = l.pieces ? total / l.pieces : 0;
-            l.r = total - l.q * l.pieces;
-            if (piece >= l.pieces) {
-                if (lane == 0) more = false;
-            } else {
-                const int w0 = l.at(piece);
-                int base = 0, x = 0, share = 0;
-                unsigned hit = 0;
-                for (int b0 = 0; !hit; b0 += 32) {
-                    if (a.B > 32) {
-                        mine.items = 0;
-                        if (b0 + lane < a.B) mine = seq_work(a, b0 + lane, RT);
-                    }
-                    share = mine.items * (mine.chunks + l.extra);
-                    x = base + warp_scan(share, lane);
-                    hit = __ballot_sync(0xffffffffu, w0 < x);
-                    base = __shfl_sync(0xffffffffu, x, 31);
-                    if (hit && lane == __ffs(hit) - 1) {  // the first sequence whose share ends behind w0
-                        line = l;
-                        w = w0;
-                        w_end = l.at(piece + 1);
-                        before = x - share;
-                        b = b0 + lane;
-                        sw = mine;
-                        segment(a);
-                    }
-                }
-            }
-        }
-        __syncthreads();
-        return more;
-    }
-    __device__ __forceinline__ bool next(const CacheArgs& a) {
-        __syncthreads();  // the block is done with the segment and its shared memory
-        if (threadIdx.x == 0) segment(a);
-        __syncthreads();
-        return more;
-    }
-    __device__ __forceinline__ bool whole() const { return s.c0 == 0 && s.c1 == s.chunks; }
-    // Where the sums of a part of an item go: the part that starts the item, or another.
-    __device__ __forceinline__ int slot(int piece) const { return 2 * piece + (s.c0 == 0); }
-    // Notes for the join whether the item that starts here goes on behind the piece.
-    __device__ __forceinline__ void note(const CacheArgs& a, const AttnOut& out, int piece) const {
-        if (threadIdx.x != 0 || s.c0 != 0) return;
-        CutItem c{};
-        if (s.c1 < s.chunks) {
-            c.b = s.b; c.h = s.h; c.row0 = s.row0; c.rows = s.rows;
-            c.piece = piece;
-            c.parts = line.piece_of(s.first + s.chunks - 1) - piece + 1;
-        }
-        if (out.items)
-            out.cut[(s.b * out.tiles + s.row0 / RT) * a.Hkv + s.h] = c;
-        else if (c.rows)
-            out.cut[piece] = c;
-    }
-};
-
-// What a piece finds wrong; the join makes the call's status word of it. Between
-// them the pieces read every table entry that the call uses; the first also
-// checks the lengths, counts and exponents, and notes the items that there are
-// not (tiles of sequences with fewer rows) as not cut.
-enum : int { kFoundBounds = 1, kFoundTimeout = 2 };
-__device__ __forceinline__ int first_piece(const CacheArgs& a, const AttnOut& out) {
-    bool bad = bad_exps(a);
-    for (int b = threadIdx.x; b < a.B; b += blockDim.x) bad |= bad_len(a, b);
-    for (int i = threadIdx.x; i < out.items; i += blockDim.x) {
-        const int bt = i / a.Hkv, b = bt / out.tiles;
-        if ((bt - b * out.tiles) * out.rows >= cache_count(a, b) * a.G) out.cut[i] = CutItem{};
-    }
-    return bad ? kFoundBounds : 0;
-}
-// The end of a piece, by the whole block.
-__device__ __forceinline__ void end_piece(const CacheArgs& a, const AttnOut& out, int piece, int found) {
-    if (piece == 0) found |= first_piece(a, out);
-    const int bounds = __syncthreads_or(found & kFoundBounds), timeout = __syncthreads_or(found & kFoundTimeout);
-    if (threadIdx.x == 0) out.found[piece] = (bounds ? kFoundBounds : 0) | (timeout ? kFoundTimeout : 0);
-}
-
-// A kernel that this one's launch may be followed by can be set up meanwhile;
-// it waits for this one's end before it reads anything.
-__device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-// Row r of a sequence: token r / G of the call, query head h G + r % G.
-__device__ __forceinline__ long long row_offset(const CacheArgs& a, int b, int h, int r, int* t) {
-    *t = r / a.G;
-    return ((long long)(b * a.H + h * a.G + (r - *t * a.G)) * a.T + *t);
-}
-// Keys that token t of the call sees.
-__device__ __forceinline__ int row_limit(const CacheArgs& a, int n, int count, int t) {
-    return a.causal ? max(n - (count - 1 - t), 0) : n;
-}
 
 // ------------------------------------------------------ staging of groups
 
-__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
@@ -519,29 +294,12 @@ __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 // 8 x 8 halves, lane (g, t) holding row g, columns 2 t and 2 t + 1: transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-// One group of a step: a bulk copy that `bar` counts, or nothing.
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(smem_addr(bar))
-                 : "memory");
-}
-
 __device__ __forceinline__ void store4(float* p, float x, float y, float z, float w) {
     *reinterpret_cast<float4*>(p) = make_float4(x, y, z, w);
 }
@@ -549,8 +307,6 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float x, float y, float
     const __nv_bfloat162 a = __floats2bfloat162_rn(x, y), b = __floats2bfloat162_rn(z, w);
     *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
-
-constexpr float kNoKey = -1.7e38f;  // a row's maximum before it has seen a key: finite, so that differences are
 
 constexpr int kStages = 2;
 // Blocks per SM that the registers allow without spills. (16 rows of 128 channels: 3 blocks 48.6 us,
@@ -1129,18 +885,19 @@ static long long cache_attn_units(const CacheArgs& a, int rtile, int extra) {
 }
 
 CachePlan cache_attn_plan(const CacheArgs& a, int d, int dtype, unsigned flags) {
-    CachePlan p;
+    CachePlan p{};
     const long long rows = (long long)a.G * a.T;
     p.tensor = !(flags & MITA_FLAG_SIMT);
     int blocks = 4;  // per SM
     if (p.tensor) {
-        p.rows = rows <= 8 ? 8 : rows <= 16 || dtype == 0 ? 16 : 32;
-        blocks = mma_blocks(d, p.rows / 8);
+        p.rows = rows <= 8 ? 8 : rows <= 16 || dtype == 0 ? 16 : rows <= 32 || d == 64 ? 32 : 64;
+        p.tile = p.rows == 64;
+        blocks = p.tile ? 1 : mma_blocks(d, p.rows / 8);
     } else {
         p.rows = rows == 1 ? 1 : 4;
     }
     p.pieces = (int)std::min<long long>((long long)blocks * num_sms(), cache_attn_units(a, p.rows, 0));
-    p.fits = cache_attn_units(a, p.rows, kExtra) < (1LL << 31);
+    p.fits = cache_attn_units(a, p.rows, kTileExtra) < (1LL << 31);
     p.parts = (size_t)2 * p.pieces * p.rows;
     return p;
 }
@@ -1166,7 +923,7 @@ static cudaError_t join_t(const CacheArgs& a, const AttnOut& o, cudaStream_t st)
 
 // Sets a kernel's shared memory limit, once per device (`done`: a bit for each of
 // the first 64; above those every time).
-static cudaError_t set_smem_once(const void* f, int bytes, std::atomic<unsigned long long>* done) {
+cudaError_t set_smem_once(const void* f, int bytes, std::atomic<unsigned long long>* done) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -1207,6 +964,10 @@ static cudaError_t attn_t(const CacheArgs& a, const CachePlan& p, int dtype, con
     if (dtype == 0) {
         if (p.tensor) return p.rows == 8 ? mma_t<float, D, 1>(a, Q, cache, o, st) : mma_t<float, D, 2>(a, Q, cache, o, st);
         return p.rows == 1 ? simt_t<float, D, 1>(a, Q, cache, o, st) : simt_t<float, D, 4>(a, Q, cache, o, st);
+    }
+    if (p.tile) {
+        const cudaError_t e = launch_cache_tile(a, Q, cache, o, st);
+        return e != cudaSuccess ? e : join_t<bf16, D>(a, o, st);
     }
     if (p.tensor)
         return p.rows == 8    ? mma_t<bf16, D, 1>(a, Q, cache, o, st)

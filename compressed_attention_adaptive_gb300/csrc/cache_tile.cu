@@ -1,0 +1,617 @@
+// Attention over the 4-bit cache for many rows per cache head (drafted tokens of
+// grouped queries, parts of prompts): tiles of 64 bf16 rows of 128 channels on tcgen05. (cache_attn.cu has the work split and the form for few rows.)
+//
+// With 64 rows a cached token costs 64 times 4 d = 32,768 flops against 144 bytes,
+// so the products bound it, and the register form of cache_attn.cu (17.6 clocks of
+// an SM per token at its full rate, twice the widening of the codes for two tiles
+// of 32) does not reach HBM. Here a chunk of 128 tokens is widened once, to halves in
+// shared memory, for all rows:
+//
+//   S^T = K Q^T    128 tokens x N rows, K and Q K-major tiles, fp32 in tensor memory
+//   P^T = 2^(f S^T - m) as halves, in shared memory (MN-major: a token's N rows are contiguous)
+//   O^T += V^T P^T  128 channels x N rows, V as it was widened (MN-major), fp32 in tensor memory
+//
+// Tokens and channels are the 128 side: rows would fill only half of it. A softmax
+// thread has a token of S^T with all its rows, so a row's maximum would go across
+// 128 threads; as in cache_attn.cu the reference m is only moved when a score
+// exceeds it by more than 15, and each thread keeps its own part of the rows' sums
+// until a segment ends.
+//
+// Warps: N / 4 for the softmax and the epilogue, each warpgroup 16 of the rows; one
+// copies (eight lanes, a group of 16 tokens each); one issues the products; eight
+// widen. Raw codes, K, V and P have two stages each; S two
+// accumulators. Every wait is bounded; a block that gives up raises its abort
+// flag, lets its copies and products land and frees its tensor memory.
+#include <atomic>
+#include <type_traits>
+
+#include "cache_walk.cuh"
+
+namespace mita {
+
+namespace {
+
+constexpr int kD = 128, N = 64;  // channels; rows of a tile
+constexpr int HN = 16;           // rows of a softmax thread
+constexpr int kRaw = 8 * Grp<kD>::kBytes;  // a chunk's codes and scales
+constexpr int kTile = 128 * kD * 2;        // a chunk's keys or values as halves
+constexpr int kEdge = 64;                  // tokens that only some rows of a tile see, at most
+constexpr long long kSpin = 2LL << 30;     // about a second
+
+struct TileSmem {
+    static constexpr int kSoft = N / 4, kCopy = kSoft, kIssue = kSoft + 1, kWiden = kSoft + 2;  // warps
+    static constexpr int kThreads = 32 * (kSoft + 10);
+    static constexpr int kP = 128 * 128;  // a token's rows, padded to 128 bytes
+    static constexpr int kQ = 0, kK = kQ + 64 * kD * 2, kV = kK + 2 * kTile, kPo = kV + 2 * kTile, kRawO = kPo + 2 * kP,
+                         kBytes = kRawO + 2 * kRaw + 1024;
+};
+
+// Instruction descriptor of kind::f16 with half A and B and fp32 accumulate.
+constexpr uint32_t idesc_half(int M, int N, int a_mn, int b_mn) {
+    return (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
+}
+
+// Bounded wait that also ends when another role has given up.
+__device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!tc::mbar_try_wait(bar, parity)) {
+        if (*abort_flag) return false;
+        if (clock64() - t0 > kSpin) {
+            *abort_flag = 1;
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    return __all_sync(0xffffffffu, tile_wait(bar, parity, abort_flag));
+}
+// For what this block has issued to the asynchronous units, whatever the abort flag says.
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, int* status) { (void)tc::mbar_wait(bar, parity, status); }
+
+// The W softmax warps meet here, all of them the same number of times whatever
+// happened to the waits before.
+template <int W> __device__ __forceinline__ void softmax_sync() {
+    __syncwarp();
+    asm volatile("barrier.sync 1, %0;" ::"n"(32 * W) : "memory");
+}
+template <int W> __device__ __forceinline__ bool softmax_any(bool x) {
+    uint32_t r;
+    __syncwarp();
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.red.or.pred q, 1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x), "n"(32 * W)
+        : "memory");
+    return r != 0;
+}
+
+// (No memory clobber: loads may move across. fence_proxy_async() orders it.)
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d));
+}
+
+// Joins v[0..16) over the 32 lanes: each step a lane keeps half of the values and
+// gives the other half away. Lane l ends with value l / 2, in v[0].
+template <typename Op> __device__ __forceinline__ void reduce_lanes(float* v, int lane, Op op) {
+#pragma unroll
+    for (int s = 16, n = HN / 2; s; s >>= 1, n >>= 1) {
+        if (n == 0) {
+            v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], s));
+            continue;
+        }
+        const bool up = lane & s;
+#pragma unroll
+        for (int i = 0; i < HN / 2; ++i) {
+            if (i >= n) break;
+            const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+            v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, s));
+        }
+    }
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
+    const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void load_cols(uint32_t taddr, float* v) {  // HN columns
+    tmem_ld16(taddr, v);
+    tc::tmem_wait_ld();
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+// v, or NaN if a token from `low` on that the row sees (up to `end`) has NaN in this block of its values
+__device__ __noinline__ float seen_nan(float v, const uint8_t* nanv, int low, int end, int blk) {
+    for (int x = low; x < end; ++x)
+        if (nanv[x - low] >> blk & 1) v = __int_as_float(0x7fc00000);
+    return v;
+}
+// One lane of a whole warp. (Behind a branch on this the compiler keeps the products'
+// operands in uniform registers; behind one on the lane's number it moves each there.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
+struct TileBars {
+    uint64_t raw_full[2], raw_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2];
+    uint64_t q_full, pv_done, o_full, drain;
+};
+
+}  // namespace
+
+__global__ void __launch_bounds__(TileSmem::kThreads, 1)
+k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_t* __restrict__ cache, AttnOut out) {
+    using L = Grp<kD>;
+    using S = TileSmem;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t sm = (smem_addr(smem_raw) + 1023) & ~1023u;
+    uint8_t* smp = smem_raw + (sm - smem_addr(smem_raw));
+    __shared__ Walk<N, kTileExtra> walk;
+    __shared__ TileBars bar;
+    __shared__ __align__(16) float mref[N];  // the rows' references
+    __shared__ uint32_t qmax[S::kSoft];
+    __shared__ float fac[N], lsum[N], linv[N], part4[4][N];
+    __shared__ int lim[N], nan_flag;
+    __shared__ long long row_at[N];
+    __shared__ __align__(16) uint8_t nanv[kEdge];  // blocks of a token's values that are NaN, tokens from `low` on
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    volatile int* abort_v = &abort_flag;
+    allow_next();
+    const int piece = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int found = 0;
+    if (!out.items && tid == 0) out.cut[piece] = CutItem{};
+    if (warp == S::kIssue) tc::tmem_alloc(&tmem_slot, 256);
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&bar.raw_full[i], 8);
+            tc::mbar_init(&bar.raw_empty[i], 8);
+            tc::mbar_init(&bar.k_full[i], 4);
+            tc::mbar_init(&bar.k_empty[i], 1);
+            tc::mbar_init(&bar.v_full[i], 4);
+            tc::mbar_init(&bar.v_empty[i], 1);
+            tc::mbar_init(&bar.s_full[i], 1);
+            tc::mbar_init(&bar.p_full[i], S::kSoft);
+        }
+        tc::mbar_init(&bar.q_full, S::kSoft);
+        tc::mbar_init(&bar.pv_done, 1);
+        tc::mbar_init(&bar.o_full, 1);
+        tc::mbar_init(&bar.drain, 1);
+        tc::fence_mbar_init();
+        abort_flag = nan_flag = 0;
+    }
+    if (tid < kEdge) nanv[tid] = 0;
+    tc::fence_before_sync();
+    bool more = walk.begin(a, piece, out.pieces);
+    tc::fence_after_sync();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
+    constexpr uint32_t kO = 128;  // columns: two S of 64, O
+
+    int done = 0, seg = 0;  // chunks and segments before this one: the barriers' phases go on
+    int issued = 0;         // chunks that the copying warp has issued
+    for (; more; ++seg) {
+        const Segment s = walk.s;
+        const int n = walk.sw.n, count = walk.sw.count;
+        const int low = row_limit(a, n, count, s.row0 / a.G), top = row_limit(a, n, count, (s.row0 + s.rows - 1) / a.G);
+        // chunks that some row of the tile sees, at least one
+        const int nc = max(1, min(s.c1, (top + kChunk - 1) / kChunk) - s.c0);
+        if (abort_flag) {
+            // only the items' ends are still noted
+        } else if (warp == S::kCopy) {
+            // ---------------------------------------------------- copies
+            if (lane < 8) {
+                auto group = [&](int c) {
+                    const int gi = (s.c0 + c) * 8 + lane;
+                    if (c >= nc || gi * kGroup >= top) return -1;
+                    const int g = cache_group(a, s.b, s.h, gi);
+                    if (g < 0) found |= kFoundBounds;
+                    return g;
+                };
+                int g = group(0);
+                for (int c = 0; c < nc; ++c) {
+                    const int t = done + c, st = t & 1, gn = group(c + 1);
+                    if (!tile_wait(&bar.raw_empty[st], ((t >> 1) & 1) ^ 1, abort_v)) break;
+                    if (g >= 0) {
+                        tc::mbar_expect_tx(&bar.raw_full[st], L::kBytes);
+                        bulk_copy(sm + S::kRawO + st * kRaw + lane * L::kBytes, cache + (long long)g * L::kBytes, L::kBytes,
+                                  &bar.raw_full[st]);
+                    } else {
+                        tc::mbar_arrive(&bar.raw_full[st]);
+                    }
+                    issued = t + 1;
+                    g = gn;
+                }
+            }
+            __syncwarp();
+        } else if (warp == S::kIssue) {
+            // -------------------------------------------------- products
+            // The whole warp goes through the loop and one lane's instructions are predicated: the
+            // descriptors are then uniform and stay in uniform registers.
+            constexpr uint32_t idS = idesc_half(128, N, 0, 0), idO = idesc_half(128, N, 1, 1);
+            bool ok = warp_wait(&bar.q_full, seg & 1, abort_v);
+            // (the stage is a constant in each copy of these, and so are the descriptors' offsets)
+            auto issue_s = [&](auto stage) {
+                constexpr int st = decltype(stage)::value;
+                tc::fence_after_sync();
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)  // 16 channels each
+                        tc::mma_bf16(tmem + st * 64,
+                                     tc::sdesc(sm + S::kK + st * kTile + (k >> 2) * (kTile / 2) + (k & 3) * 32, 16, 1024),
+                                     tc::sdesc(sm + S::kQ + (k >> 2) * (64 * 128) + (k & 3) * 32, 16, 1024), idS, k > 0);
+                    tc::mma_commit(&bar.s_full[st]);
+                    tc::mma_commit(&bar.k_empty[st]);
+                }
+                __syncwarp();
+            };
+            auto issue_o = [&](auto stage, bool more_o, bool last) {
+                constexpr int st = decltype(stage)::value;
+                tc::fence_after_sync();
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)  // 16 tokens each
+                        tc::mma_bf16(tmem + kO, tc::sdesc(sm + S::kV + st * kTile + k * 2048, kTile / 2, 1024),
+                                     tc::sdesc(sm + S::kPo + st * S::kP + k * 2048, S::kP, 1024), idO, k > 0 || more_o);
+                    tc::mma_commit(&bar.pv_done);
+                    tc::mma_commit(&bar.v_empty[st]);
+                    if (last) tc::mma_commit(&bar.o_full);
+                }
+                __syncwarp();
+            };
+            auto flush_o = [&](int c) {
+                const int t = done + c, st = t & 1;
+                if (!warp_wait(&bar.v_full[st], (t >> 1) & 1, abort_v)) return false;
+                if (!warp_wait(&bar.p_full[st], (t >> 1) & 1, abort_v)) return false;
+                if (st)
+                    issue_o(std::integral_constant<int, 1>{}, c > 0, c == nc - 1);
+                else
+                    issue_o(std::integral_constant<int, 0>{}, c > 0, c == nc - 1);
+                return true;
+            };
+            for (int c = 0; c < nc && ok; ++c) {
+                const int t = done + c, st = t & 1;
+                if (!(ok = warp_wait(&bar.k_full[st], (t >> 1) & 1, abort_v))) break;
+                if (st)
+                    issue_s(std::integral_constant<int, 1>{});
+                else
+                    issue_s(std::integral_constant<int, 0>{});
+                if (c > 0) ok = flush_o(c - 1);
+            }
+            if (ok) flush_o(nc - 1);
+            __syncwarp();
+        } else if (warp >= S::kWiden) {
+            // -------------------------------------------------- widening
+            // Four warps have the keys and four the values, two groups each, so that neither waits
+            // for the other's stage.
+            const int wj = (warp - S::kWiden) & 3;
+            const bool keys = warp - S::kWiden < 4;
+            // keys: lane (tt, q) has channels 32 q to 32 q + 31 of token tt, then of tt + 8; lanes with
+            // q >= 2 take their words in the order 2, 3, 0, 1
+            const int tt = lane >> 2, q = lane & 3, swap = q & 2;
+            // values: lane bits 0, 1, 3: channel block gb; bit 2: the low bit of t; bit 4: c; pass: the rest
+            // of the token 8 a + 2 t + c; odd t take their words in the order 1, 0
+            const int gb = (lane & 3) | (lane >> 1 & 4), t0 = lane >> 2 & 1, cc = lane >> 4;
+            // (Both ways a load meets every bank once and eight lanes store to eight bank groups.)
+            for (int c = 0; c < nc; ++c) {
+                const int t = done + c, st = t & 1;
+                if (!warp_wait(&bar.raw_full[st], (t >> 1) & 1, abort_v)) break;
+                const uint8_t* raw = smp + S::kRawO + st * kRaw + 2 * wj * L::kBytes;
+                const int tok0 = (s.c0 + c) * kChunk + 32 * wj;
+                if (keys) {
+                    uint4 kw[4];
+                    uint32_t ks[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const uint8_t* g = raw + (x >> 1) * L::kBytes;
+                        kw[x] = *reinterpret_cast<const uint4*>(g + (8 * (x & 1) + tt) * L::kRow + q * 16);
+                        ks[x] = *reinterpret_cast<const uint16_t*>(g + L::kKs + tt * 16 + q * 4 + (x & 1) * 2);
+                    }
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&bar.raw_empty[st]);
+                    if (!warp_wait(&bar.k_empty[st], ((t >> 1) & 1) ^ 1, abort_v)) break;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const uint32_t w[4] = {swap ? kw[x].z : kw[x].x, swap ? kw[x].w : kw[x].y,
+                                               swap ? kw[x].x : kw[x].z, swap ? kw[x].y : kw[x].w};
+                        const uint32_t s2 = e4m3x2_to_half2(ks[x]);
+                        const uint32_t sc[2] = {__byte_perm(s2, s2, swap ? 0x3232 : 0x1010),
+                                                __byte_perm(s2, s2, swap ? 0x1010 : 0x3232)};
+                        const int row = 32 * wj + 8 * x + tt;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t r[4];
+                            e2m1x8_to_half2(w[i], r);
+                            st_shared16(sm + S::kK + st * kTile + tc::sw_off(row, q * 4 + (i ^ swap), 128),
+                                        hmul2(r[0], sc[i >> 1]), hmul2(r[1], sc[i >> 1]), hmul2(r[2], sc[i >> 1]),
+                                        hmul2(r[3], sc[i >> 1]));
+                        }
+                    }
+                    tc::fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&bar.k_full[st]);
+                } else {
+                    uint2 vw[8];
+                    uint32_t vs[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        const int tk = t0 + 2 * (x & 1), aa = x >> 1 & 1;
+                        const uint8_t* g = raw + (x >> 2) * L::kBytes;
+                        vw[x] = *reinterpret_cast<const uint2*>(g + L::v_chunk(tk + 4 * (2 * aa + cc), gb));
+                        vs[x] = g[L::kVs + gb * 16 + tk * 4 + 2 * aa + cc];
+                    }
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&bar.raw_empty[st]);
+                    if (tok0 + 32 > low) {
+                        // Nothing of a token that a row does not see may reach it: tokens that no row sees
+                        // are zero; NaN of one that some see is zero here and put into those rows' results.
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            const int tok = tok0 + 8 * (x >> 1) + 2 * (t0 + 2 * (x & 1)) + cc;
+                            if (tok >= top) {
+                                vs[x] = 0;
+                            } else if (tok >= low && (vs[x] & 0x7f) == 0x7f) {
+                                vs[x] = 0;
+                                // the byte's other bits belong to other lanes
+                                atomicOr(reinterpret_cast<uint32_t*>(nanv) + ((tok - low) >> 2),
+                                         1u << (((tok - low) & 3) * 8 + gb));
+                                nan_flag = 1;
+                            }
+                        }
+                    }
+                    if (!warp_wait(&bar.v_empty[st], ((t >> 1) & 1) ^ 1, abort_v)) break;
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        const uint32_t sc = e4m3x2_to_half2(vs[x] | vs[x] << 8);
+                        const int row = 32 * wj + 8 * (x >> 1) + 2 * (t0 + 2 * (x & 1)) + cc;
+                        const uint32_t ws[2] = {t0 ? vw[x].y : vw[x].x, t0 ? vw[x].x : vw[x].y};
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t r[4];
+                            e2m1x8_to_half2(ws[i], r);
+                            st_shared16(sm + S::kV + st * kTile + tc::sw_off(row, gb * 2 + (i ^ t0), 128), hmul2(r[0], sc),
+                                        hmul2(r[1], sc), hmul2(r[2], sc), hmul2(r[3], sc));
+                        }
+                    }
+                    tc::fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&bar.v_full[st]);
+                }
+            }
+        } else {
+            // --------------------------------------------------- softmax
+            const float vscale = pow2(cache_exp(a, 1, s.h));
+            // Q: thread (r, part) has 16 channels of row r. All rows of the tile are scaled by the power
+            // of two that puts the largest finite entry in [2^14, 2^15): bf16 is exact as halves down
+            // to 2^-31 of it, and what is lost below is 2^-40 of the largest scores.
+            float f;  // factor of the scores, in log2 units
+            {
+                const int r = tid >> 3, part = tid & 7;
+                int t = 0;
+                const long long at = row_offset(a, s.b, s.h, s.row0 + min(r, s.rows - 1), &t);
+                uint32_t x[8], amax = 0;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (r < s.rows) v = reinterpret_cast<const uint4*>(Q + at * kD + part * 16)[i];
+                    x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t lo = x[i] & 0x7fffu, hi = x[i] >> 16 & 0x7fffu;
+                    amax = max(amax, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+                }
+                amax = __reduce_max_sync(0xffffffffu, amax);
+                if (lane == 0) qmax[warp] = amax;
+                if (part == 0) {
+                    mref[r] = kNoKey;
+                    lim[r] = r < s.rows ? row_limit(a, n, count, t) : 0;
+                    row_at[r] = at;
+                }
+                softmax_sync<S::kSoft>();
+#pragma unroll
+                for (int i = 0; i < S::kSoft; ++i) amax = max(amax, qmax[i]);
+                const int qe = min(141 - (int)(amax >> 7), 120);
+                const float up = pow2(qe);
+                // kept away from 0 and infinity: a masked score is -infinity times it
+                f = fminf(fmaxf(a.scale * kLog2e * pow2(cache_exp(a, 0, s.h)) * pow2(-qe), 1.1754944e-38f), 3.4028235e38f);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t h[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        h[j] = pack_half2(__uint_as_float(x[4 * i + j] << 16) * up,
+                                          __uint_as_float(x[4 * i + j] & 0xffff0000u) * up);
+                    st_shared16(sm + S::kQ + tc::sw_off(r, part * 2 + i, 64), h[0], h[1], h[2], h[3]);
+                }
+                tc::fence_proxy_async();
+                softmax_sync<S::kSoft>();
+                if (lane == 0) tc::mbar_arrive(&bar.q_full);
+            }
+            // thread: token (then channel) tl, rows r0 to r0 + HN - 1
+            const int tl = tid & 127, r0 = (warp >> 2) * HN, quarter = warp & 3;
+            const uint32_t cols = tmem + ((uint32_t)(tid & 96) << 16) + r0;
+            float l[HN];
+#pragma unroll
+            for (int r = 0; r < HN; ++r) l[r] = 0.0f;
+            bool ok = true;
+            for (int c = 0; c < nc; ++c) {
+                const int t = done + c, st = t & 1, tok = (s.c0 + c) * kChunk + tl;
+                // after a wait that gave up the warp goes on without waiting, for the others' sake
+                ok &= warp_wait(&bar.s_full[st], (t >> 1) & 1, abort_v);
+                tc::fence_after_sync();
+                const bool edge = (s.c0 + c + 1) * kChunk > low;  // some row does not see all of the chunk
+                float y[HN], big = kNoKey;
+                // again after the reference has moved, which happens once: no score is more than 7 above it then
+#pragma unroll 1
+                for (int again = 0;; ++again) {
+                    load_cols(cols + st * 64, y);
+#pragma unroll
+                    for (int r = 0; r < HN; r += 4) {
+                        const float4 m = *reinterpret_cast<const float4*>(mref + r0 + r);
+                        y[r] = fmaf(y[r], f, -m.x);
+                        y[r + 1] = fmaf(y[r + 1], f, -m.y);
+                        y[r + 2] = fmaf(y[r + 2], f, -m.z);
+                        y[r + 3] = fmaf(y[r + 3], f, -m.w);
+                    }
+                    if (edge) {
+#pragma unroll
+                        for (int r = 0; r < HN; ++r)
+                            if (tok >= lim[r0 + r]) y[r] = -INFINITY;
+                    }
+                    if (again) break;
+#pragma unroll
+                    for (int r = 0; r < HN; ++r) big = fmaxf(big, y[r]);
+                    if (!softmax_any<S::kSoft>(big > 15.0f)) break;
+                    load_cols(cols + st * 64, y);
+#pragma unroll
+                    for (int r = 0; r < HN; ++r) y[r] = edge && tok >= lim[r0 + r] ? -INFINITY : y[r] * f;
+                    reduce_lanes(y, lane, [](float p, float q) { return fmaxf(p, q); });
+                    part4[quarter][r0 + HN * lane / 32] = y[0];
+                    softmax_sync<S::kSoft>();
+                    if (tid < N) {
+                        const float mx = fmaxf(fmaxf(part4[0][tid], part4[1][tid]), fmaxf(part4[2][tid], part4[3][tid]));
+                        const float old = mref[tid], mn = fmaxf(old, mx - 7.0f);
+                        fac[tid] = tc::ex2(old - mn);
+                        mref[tid] = mn;
+                    }
+                    softmax_sync<S::kSoft>();
+#pragma unroll
+                    for (int r = 0; r < HN; ++r) l[r] *= fac[r0 + r];
+                    if (c > 0) {
+                        // S of this chunk is done, so the products with V up to the one before the last are;
+                        // this wait can only be for the last
+                        ok &= warp_wait(&bar.pv_done, (t - 1) & 1, abort_v);
+                        tc::fence_after_sync();
+                        load_cols(cols + kO, y);
+#pragma unroll
+                        for (int r = 0; r < HN; ++r) y[r] *= fac[r0 + r];
+                        tmem_st16(cols + kO, y);
+                        tc::tmem_wait_st();
+                    }
+                }
+                const uint32_t pd = sm + S::kPo + st * S::kP;
+#pragma unroll
+                for (int j = 0; j < HN / 8; ++j) {
+                    uint32_t h[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 8 * j + 2 * i;
+                        const float p0 = tc::ex2(y[r]), p1 = tc::ex2(y[r + 1]);
+                        l[r] += p0;
+                        l[r + 1] += p1;
+                        h[i] = pack_half2(p0, p1);
+                    }
+                    st_shared16(pd + tc::sw_off(tl, r0 / 8 + j, 128), h[0], h[1], h[2], h[3]);
+                }
+                tc::fence_proxy_async();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bar.p_full[st]);
+            }
+            ok &= warp_wait(&bar.o_full, seg & 1, abort_v);
+            tc::fence_after_sync();
+            if (!softmax_any<S::kSoft>(!ok)) {
+                reduce_lanes(l, lane, [](float p, float q) { return p + q; });
+                part4[quarter][r0 + HN * lane / 32] = l[0];
+                softmax_sync<S::kSoft>();
+                if (tid < N) {
+                    const float sum = (part4[0][tid] + part4[1][tid]) + (part4[2][tid] + part4[3][tid]);
+                    lsum[tid] = sum;
+                    linv[tid] = sum == 0.0f ? 0.0f : 1.0f / sum;
+                }
+                softmax_sync<S::kSoft>();
+                const bool whole = walk.whole(), nans = nan_flag;
+                const long long slot = (long long)walk.slot(piece) * N;
+                // channel tl of the thread's rows, eight at a time (little code: it runs once a segment)
+#pragma unroll 1
+                for (int i0 = 0; i0 < HN && r0 + i0 < s.rows; i0 += 8) {
+                    float o[8];
+                    tmem_ld8(cols + kO + i0, o);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = r0 + i0 + i;
+                        float v = o[i] * vscale;
+                        if (r < s.rows) {
+                            if (nans) v = seen_nan(v, nanv, low, min(top, lim[r]), tl >> 4);
+                            if (whole)
+                                reinterpret_cast<__nv_bfloat16*>(out.O)[row_at[r] * kD + tl] = __float2bfloat16_rn(v * linv[r]);
+                            else
+                                out.part[(slot + r) * kD + tl] = v;
+                        }
+                    }
+                }
+                if (tid < s.rows) {
+                    const float sum = lsum[tid], m = mref[tid];
+                    if (!whole)
+                        out.ml[slot + tid] = make_float2(m, sum);
+                    else if (out.lse)
+                        out.lse[row_at[tid]] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
+                }
+                if (nans) {
+                    softmax_sync<S::kSoft>();
+                    if (tid < kEdge) nanv[tid] = 0;
+                    if (tid == 0) nan_flag = 0;
+                }
+            }
+            tc::fence_before_sync();
+        }
+        walk.note(a, out, piece);
+        done += nc;
+        more = walk.next(a);
+        tc::fence_after_sync();
+    }
+    // what is in flight lands before the block frees its tensor memory and ends
+    if (warp == S::kCopy && lane == 0)
+        for (int t = max(0, issued - 2); t < issued; ++t) drain(&bar.raw_full[t & 1], (t >> 1) & 1, a.status);
+    if (warp == S::kIssue && lane == 0) {
+        tc::mma_commit(&bar.drain);
+        drain(&bar.drain, 0, a.status);
+    }
+    tc::fence_before_sync();
+    if (abort_flag) found |= kFoundTimeout;
+    end_piece(a, out, piece, found);
+    tc::fence_after_sync();
+    if (warp == S::kIssue) tc::tmem_dealloc(tmem, 256);
+}
+
+cudaError_t launch_cache_tile(const CacheArgs& a, const void* Q, const uint8_t* cache, const AttnOut& o, cudaStream_t st) {
+    constexpr int smem = TileSmem::kBytes;
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e = set_smem_once((const void*)k_cache_attn_tile, smem, &done);
+    if (e != cudaSuccess) return e;
+    k_cache_attn_tile<<<o.pieces, TileSmem::kThreads, smem, st>>>(a, (const __nv_bfloat16*)Q, cache, o);
+    count_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace mita

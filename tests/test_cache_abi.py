@@ -34,6 +34,7 @@ def test_sizes(lib):
     (dict(n_pages=0), 1), (dict(max_pages=0), 1), (dict(dtype=5), 1), (dict(flags=1), 1), (dict(flags=8), 1),
     (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(B=65536), 2),
     (dict(T=1 << 29), 2), (dict(H=2 ** 31 - 2, H_kv=2), 2), (dict(max_pages=1 << 25), 2), (dict(n_pages=1 << 29), 2),
+    (dict(B=1, H=1, H_kv=1, T=1 << 24, max_pages=1 << 14), 2),  # more work than 32 bits count
 ])
 def test_invalid_parameters(lib, bad, status):
     p = _p(**bad)

@@ -170,6 +170,11 @@ CASES = [
     ("bf16", 64, 64, 10, 1, 8, True, [900, 3, 64], None, False),     # 80 rows, rows without a key
     ("bf16", 128, 128, 3, 3, 40, True, [40, 200], None, False),      # a chunk of a prompt, rows in several tiles
     ("bf16", 64, 16, 5, 5, 2, False, [3000, 1, 257], [2, 2, 1], True),
+    # more than 32 rows a head: tiles of 64
+    ("bf16", 128, 64, 48, 1, 1, False, [5000, 0, 130, 128], None, False),
+    ("bf16", 128, 16, 64, 2, 3, True, [2500, 2, 100], [3, 3, 1], True),
+    ("bf16", 128, 32, 2, 2, 70, True, [300, 69, 71], [70, 70, 3], False),
+    ("bf16", 128, 48, 33, 1, 2, True, [1, 700], None, True),
     ("f32", 128, 64, 2, 2, 1, False, [1, 127, 700], None, True),
     ("f32", 64, 16, 6, 2, 3, True, [500, 2, 33], [3, 3, 1], False),
     ("f32", 128, 32, 8, 1, 1, True, [4000, 0], None, False),
@@ -186,24 +191,27 @@ def test_attention_matches_oracle(case, simt):
     _check(pool, H, T, causal, Q, O, L, counts, simt, label="%s d%d H%d/%d T%d %s" % (dtype, d, H, Hkv, T, "simt" * simt))
 
 
-def test_scale_and_large_queries():
+@pytest.mark.parametrize("dtype,H", [("bf16", 4), ("bf16", 64), ("f32", 4)])
+def test_scale_and_large_queries(dtype, H):
     """Scores far apart (one key takes all the weight), an explicit scale, and
     query rows of very unlike magnitude in one call."""
     import torch
-    pool = Pool([333], 2, 128, 64, "bf16", seed=9)
-    Q = torch.randn((1, 4, 2, 128)).cuda() * torch.tensor([1e-30, 1e-3, 1.0, 40.0]).cuda().view(1, 4, 1, 1)
+    pool = Pool([333], 2, 128, 64, dtype, seed=9)
+    mag = torch.tensor([1e-30, 1e-3, 1.0, 40.0]).cuda().repeat(H // 4).view(1, H, 1, 1)
+    Q = torch.randn((1, H, 2, 128), generator=torch.Generator().manual_seed(2)).cuda() * mag
     Q[0, 1, 0] = 0
-    Q = Q.to(torch.bfloat16)
-    _, O, L = _attend(pool, 4, 2, True, scale=0.5, q=Q)
-    _check(pool, 4, 2, True, Q, O, L, scale=0.5, label="scales")
+    Q = Q.to(pool.td)
+    _, O, L = _attend(pool, H, 2, True, scale=0.5, q=Q)
+    _check(pool, H, 2, True, Q, O, L, scale=0.5, label="scales %s H%d" % (dtype, H))
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_unseen_keys_have_no_influence(dtype):
+@pytest.mark.parametrize("dtype,H,d,simt", [("bf16", 4, 128, False), ("bf16", 12, 64, False), ("bf16", 64, 128, False),
+                                            ("f32", 4, 128, False), ("f32", 4, 128, True)])
+def test_unseen_keys_have_no_influence(dtype, H, d, simt):
     """A later drafted token full of NaN, and whatever bytes lie behind the last
     token: rows that do not see them are as without them, rows that do are NaN."""
     import torch
-    T, H = 3, 4
+    T = 3
 
     def make(rng, shape):
         K, V = Pool.rows(rng, shape)
@@ -212,40 +220,44 @@ def test_unseen_keys_have_no_influence(dtype):
         K[2, 1, 5] = np.nan                           # a key that every row of sequence 2 sees
         return K, V
 
-    pool = Pool([62, 40, 20], 2, 128, 16, dtype, make=make, seed=6)
-    Q, O, L = _attend(pool, H, T, True)
-    clean = Pool([62, 40, 20], 2, 128, 16, dtype, seed=6, fill=0)
-    Q2, O2, L2 = _attend(clean, H, T, True)
+    pool = Pool([62, 40, 20], 2, d, 16, dtype, make=make, seed=6)
+    Q, O, L = _attend(pool, H, T, True, simt=simt)
+    clean = Pool([62, 40, 20], 2, d, 16, dtype, seed=6, fill=0)
+    Q2, O2, L2 = _attend(clean, H, T, True, simt=simt)
+    half = H // 2
     assert torch.equal(Q, Q2)
     assert torch.equal(O[0, :, 0], O2[0, :, 0]) and torch.equal(L[0, :, 0], L2[0, :, 0])
     assert O[0, :, 1:].isnan().all() and L[0, :, 1:].isnan().all()
-    assert torch.equal(O[1, :, :2], O2[1, :, :2]) and torch.equal(O[1, 2:, 2], O2[1, 2:, 2])
-    assert O[1, :2, 2, 16:32].isnan().all()
-    assert torch.equal(O[1, :2, 2, :16], O2[1, :2, 2, :16]) and torch.equal(O[1, :2, 2, 32:], O2[1, :2, 2, 32:])
-    assert O[2, 2:].isnan().all() and torch.equal(O[2, :2], O2[2, :2])
+    assert torch.equal(O[1, :, :2], O2[1, :, :2]) and torch.equal(O[1, half:, 2], O2[1, half:, 2])
+    assert O[1, :half, 2, 16:32].isnan().all()
+    assert torch.equal(O[1, :half, 2, :16], O2[1, :half, 2, :16])
+    assert torch.equal(O[1, :half, 2, 32:], O2[1, :half, 2, 32:])
+    assert O[2, half:].isnan().all() and torch.equal(O[2, :half], O2[2, :half])
 
 
-def test_bad_rows_stay_in_their_rows():
+@pytest.mark.parametrize("dtype,H,d", [("bf16", 8, 64), ("bf16", 40, 128), ("f32", 8, 128)])
+def test_bad_rows_stay_in_their_rows(dtype, H, d):
     """NaN and infinite queries make their own rows NaN and no others."""
     import torch
-    pool = Pool([150], 1, 64, 16, "bf16", seed=3)
-    Q, O, L = _attend(pool, 8, 2, False)
+    pool = Pool([150], 1, d, 16, dtype, seed=3)
+    Q, O, L = _attend(pool, H, 2, False)
     bad = Q.clone()
     bad[0, 2, 1, 5], bad[0, 7, 0, 60] = float("nan"), float("inf")
-    _, O2, _ = _attend(pool, 8, 2, False, q=bad)
-    hit = torch.zeros((8, 2), dtype=torch.bool)
+    _, O2, _ = _attend(pool, H, 2, False, q=bad)
+    hit = torch.zeros((H, 2), dtype=torch.bool)
     hit[2, 1] = hit[7, 0] = True
     assert O2[0][hit.cuda()].isnan().all()
     assert torch.equal(O2[0][~hit.cuda()], O[0][~hit.cuda()])
 
 
-def test_repeated_calls_are_bit_equal_and_lse_is_optional():
+@pytest.mark.parametrize("H", [8, 64])
+def test_repeated_calls_are_bit_equal_and_lse_is_optional(H):
     import torch
     pool = Pool([3000, 900], 2, 128, 64, "bf16", seed=12)
-    runs = [_attend(pool, 8, 2, True) for _ in range(3)]
+    runs = [_attend(pool, H, 2, True) for _ in range(3)]
     for _, O, L in runs[1:]:
         assert torch.equal(O, runs[0][1]) and torch.equal(L, runs[0][2])
-    assert torch.equal(_attend(pool, 8, 2, True, lse=False)[1], runs[0][1])
+    assert torch.equal(_attend(pool, H, 2, True, lse=False)[1], runs[0][1])
 
 
 # -------------------------------------------- out of range, and the status word
