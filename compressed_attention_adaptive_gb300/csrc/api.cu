@@ -310,8 +310,8 @@ static mita_status resolve_cache(const mita_cache_params* p, CacheArgs* a) {
     if (p->flags & ~(unsigned)(MITA_FLAG_SIMT | MITA_FLAG_CAUSAL)) return fail(MITA_ERR_INVALID_ARG, "unknown flag");
     if (!(p->scale >= 0.0f) || isinf(p->scale)) return fail(MITA_ERR_INVALID_ARG, "scale must be finite and >= 0");
     if (p->B > 65535) return fail(MITA_ERR_UNSUPPORTED, "B must be <= 65535");
-    if ((long long)p->B * p->H >= (1LL << 31) || (long long)p->B * p->H * p->T >= (1LL << 31))
-        return fail(MITA_ERR_UNSUPPORTED, "B*H*T must be < 2^31");
+    if ((long long)p->B * p->H > (1LL << 30) || (long long)p->B * p->H * p->T > (1LL << 30))
+        return fail(MITA_ERR_UNSUPPORTED, "B*H*T must be <= 2^30");
     if ((long long)p->max_pages * p->page > (1LL << 30))
         return fail(MITA_ERR_UNSUPPORTED, "max_pages*page must be <= 2^30 tokens");
     if ((double)p->n_pages * p->H_kv * (p->page / kGroup) >= 2147483648.0)

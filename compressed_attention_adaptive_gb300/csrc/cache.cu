@@ -142,7 +142,7 @@ template <int D> struct BlockAt {
         blk = (int)(i % NB);
         const long long r = i / NB;
         if (r >= (long long)a.B * a.Hkv * a.T) return false;
-        row = (uint32_t)r;  // B * H * T < 2^31
+        row = (uint32_t)r;  // B * H * T <= 2^30
         const uint32_t bh = row / (uint32_t)a.T;
         const int t = (int)(row - bh * a.T);
         b = (int)(bh / (uint32_t)a.Hkv);

@@ -288,16 +288,25 @@ k_cache_attn_simt(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restric
 
 __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same onto zeros.
+__device__ __forceinline__ void mma_f16_first(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 // 8 x 8 halves, lane (g, t) holding row g, columns 2 t and 2 t + 1: transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
 __device__ __forceinline__ void store4(float* p, float x, float y, float z, float w) {
@@ -505,12 +514,6 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
                 // scores of 16 tokens each: [0], [1] token g, rows 2 t4 and the next; [2], [3] token g + 8
                 constexpr int NL = F ? NR : 1;
                 float z[NR][GP][4], zl[NL][GP][4];  // zl: the lower halves' part
-#pragma unroll
-                for (int j = 0; j < NR; ++j)
-#pragma unroll
-                    for (int x = 0; x < GP; ++x)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) z[j][x][e] = zl[j % NL][x][e] = 0.0f;
                 uint32_t kw[GP][2][W], sc[GP][2][D / 64];  // [group][token g, g + 8]: codes; scales, each in both halves
 #pragma unroll
                 for (int gi = 0; gi < GP; ++gi) {
@@ -557,15 +560,24 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
                             const int ks = 2 * wi + k2;
                             const uint2 q = kQRegs ? qf[ks % (kQRegs ? KS : 1)] : qs[(ks * NR + j) * 32 + lane];
 #pragma unroll
-                            for (int gi = 0; gi < GP; ++gi)
-                                mma_f16(z[j][gi], k8[gi][0][2 * k2], k8[gi][1][2 * k2], k8[gi][0][2 * k2 + 1],
-                                        k8[gi][1][2 * k2 + 1], q.x, q.y);
+                            for (int gi = 0; gi < GP; ++gi) {
+                                if (ks == 0)
+                                    mma_f16_first(z[j][gi], k8[gi][0][0], k8[gi][1][0], k8[gi][0][1], k8[gi][1][1], q.x, q.y);
+                                else
+                                    mma_f16(z[j][gi], k8[gi][0][2 * k2], k8[gi][1][2 * k2], k8[gi][0][2 * k2 + 1],
+                                            k8[gi][1][2 * k2 + 1], q.x, q.y);
+                            }
                             if (F) {
                                 const uint2 ql = qs[((KS + ks) * NR + j) * 32 + lane];
 #pragma unroll
-                                for (int gi = 0; gi < GP; ++gi)
-                                    mma_f16(zl[j % NL][gi], k8[gi][0][2 * k2], k8[gi][1][2 * k2], k8[gi][0][2 * k2 + 1],
-                                            k8[gi][1][2 * k2 + 1], ql.x, ql.y);
+                                for (int gi = 0; gi < GP; ++gi) {
+                                    if (ks == 0)
+                                        mma_f16_first(zl[j % NL][gi], k8[gi][0][0], k8[gi][1][0], k8[gi][0][1], k8[gi][1][1],
+                                                      ql.x, ql.y);
+                                    else
+                                        mma_f16(zl[j % NL][gi], k8[gi][0][2 * k2], k8[gi][1][2 * k2], k8[gi][0][2 * k2 + 1],
+                                                k8[gi][1][2 * k2 + 1], ql.x, ql.y);
+                                }
                             }
                         }
                 }
@@ -668,8 +680,8 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
 #pragma unroll
                                 for (int x = 0; x < 2; ++x)
                                     see[x] = (tok + 8 * x < lim ? 0x3c00u : 0u) | (tok + 8 * x + 1 < lim ? 0x3c000000u : 0u);
-                                float hit[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                                mma_f16(hit, a0, a0, a2, a2, see[0], see[1]);
+                                float hit[4];
+                                mma_f16_first(hit, a0, a0, a2, a2, see[0], see[1]);
 #pragma unroll
                                 for (int x = 0; x < NT / 2; ++x)
 #pragma unroll
@@ -711,8 +723,8 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
                                     mma_f16(o[j][4 * wi + x], a0, a1, a2, a3, p[j][gi][0], p[j][gi][1]);
                                     continue;
                                 }
-                                float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                                mma_f16(c, a0, a1, a2, a3, pl[j % NL][gi][0], pl[j % NL][gi][1]);
+                                float c[4];
+                                mma_f16_first(c, a0, a1, a2, a3, pl[j % NL][gi][0], pl[j % NL][gi][1]);
                                 mma_f16(c, a0, a1, a2, a3, p[j][gi][0], p[j][gi][1]);
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) o[j][4 * wi + x][e] += c[e];

@@ -127,6 +127,7 @@ template <int RT, int EXTRA = kExtra> struct Walk {
             const int lane = threadIdx.x;
             SeqWork mine{};
             unsigned items = 0, chunks = 0;
+#pragma unroll 8
             for (int b0 = 0; b0 < a.B; b0 += 32) {
                 mine.items = 0;
                 if (b0 + lane < a.B) mine = seq_work(a, b0 + lane, RT);

@@ -294,6 +294,8 @@ mita_status mita_cache_read(const mita_cache_params* p, const void* cache, const
  * ln sum exp(scale q.k) over the seen keys, -infinity without any, with which the
  * rows can be joined with attention over other keys (mita_forward's shared
  * slots, say). count > len is allowed: rows before the first token see none.
+ * O must not overlap Q. The same call gives the same bits; how a sequence's keys
+ * are divided, and so the last bits, depends on all the call's lengths.
  * Runs on tensor cores, float32 with each number as the sum of two halves (22
  * bits), and with MITA_FLAG_SIMT on CUDA cores in fp32. */
 mita_status mita_cache_attention(const mita_cache_params* p, const void* Q, const void* cache, const int32_t* table,

@@ -260,6 +260,57 @@ def test_repeated_calls_are_bit_equal_and_lse_is_optional(H):
     assert torch.equal(_attend(pool, H, 2, True, lse=False)[1], runs[0][1])
 
 
+def test_pool_past_32_bits():
+    """Pages more than 2^32 bytes into the pool."""
+    import torch
+    import compressed_attention_adaptive_gb300 as mita
+    small = Pool([700, 90], 8, 128, 64, "bf16", seed=21, H=16)
+    n_pages = 70000
+    p = mita.CacheParams(2, 16, 8, 1, 128, 64, n_pages, small.cols)
+    assert mita.mita_cache_size(p) > 2 ** 32 + 2 ** 29
+    cache = torch.empty(mita.mita_cache_size(p), dtype=torch.uint8, device="cuda")
+    table = torch.where(small.table < small.n_pages, n_pages - 1 - 3 * small.table, small.table)
+    f = mita.CacheParams(2, 8, 8, 700, 128, 64, n_pages, small.cols)
+    ws = mita.cache_workspace(f)
+    mita.mita_cache_write(f, small.K, small.V, cache, table, small.len_t, ws, counts=small.len_t)
+    mita.mita_device_status(ws)
+    K, V = torch.zeros_like(small.K), torch.zeros_like(small.V)
+    mita.mita_cache_read(f, cache, table, small.len_t, K, V, ws, counts=small.len_t)
+    mita.mita_device_status(ws)
+    for b, n in enumerate(small.lens):
+        np.testing.assert_array_equal(_np(K[b, :, :n]), small.held(b, 0))
+        np.testing.assert_array_equal(_np(V[b, :, :n]), small.held(b, 1))
+    Q, O, L = _attend(small, 16, 1, False)
+    for q in (p, mita.CacheParams(2, 16, 8, 1, 128, 64, n_pages, small.cols, flags=mita.FLAG_SIMT)):
+        O2, w = torch.zeros_like(O), mita.cache_workspace(q)
+        mita.mita_cache_attention(q, Q, cache, table, small.len_t, O2, w)
+        mita.mita_device_status(w)
+        if not q.flags:
+            assert torch.equal(O, O2)
+        else:
+            assert torch.allclose(O.float(), O2.float(), rtol=2 ** -6, atol=2 ** -8)
+
+
+def test_many_short_sequences_and_shared_pages():
+    """A thousand sequences, most of a few tokens, some without a row; then every
+    second one with the pages of its neighbour (a shared prefix)."""
+    import torch
+    rng = np.random.default_rng(31)
+    lens = [int(n) for n in np.where(rng.random(1000) < 0.9, rng.integers(0, 40, 1000), rng.integers(100, 900, 1000))]
+    counts = [int(c) for c in rng.integers(0, 3, 1000)]
+    pool = Pool(lens, 1, 64, 16, "bf16", seed=31)
+    Q, O, L = _attend(pool, 2, 2, True, counts)
+    _check(pool, 2, 2, True, Q, O, L, counts, label="1000 sequences")
+    pool.table[1::2] = pool.table[0::2]
+    pool.len_t[1::2] = pool.len_t[0::2]
+    Q[1::2] = Q[0::2]
+    _, O2, _ = _attend(pool, 2, 2, True, [c for c in counts[0::2] for _ in range(2)], q=Q)
+    # equal sequences are cut at different places: two roundings to bf16 (2^-8 |o| each) and of
+    # the weights to halves (2^-11 of at most max |v| < 4, each)
+    a, b = O2[0::2].float(), O2[1::2].float()
+    assert torch.all((a - b).abs() <= 2 * (2.0 ** -8 * a.abs().maximum(b.abs()) + 2.0 ** -11 * 4))
+
+
 # -------------------------------------------- out of range, and the status word
 
 
