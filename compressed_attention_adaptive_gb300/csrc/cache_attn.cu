@@ -9,7 +9,14 @@
 //
 // in one pass over the cache with a running maximum and sum. It reads
 // len 2 (d/2 + d/16) bytes per sequence and cache head and does 4 d flops per
-// row and key, so with few rows per cache head it is bound by HBM.
+// row and key, so with few rows per cache head it is bound by HBM: at the
+// measured copy rate an SM has 6.3 clocks per token of 128 channels, 3.1 of 64.
+//
+// Measured (one row per cache head, d = 128, 32 heads): 8.3 us for 1024 tokens, 34 for
+// 32,768 (4.5 TB/s), 104 for 131,072 (5.8), 198 for 262,144 (6.1); each further
+// token costs 1.02 times what it does at the copy rate. The other 11 us are the same for
+// every length: 2 to launch, 1.4 to find a block's place on the line, 1.5 until
+// the first codes arrive, an SM's last blocks alone, 3 to 4 for the join.
 //
 // Work split. An item is one (sequence, tile of query rows, cache head); it is
 // cut into chunks of 128 tokens. The chunks of all items form one line, and the
@@ -146,14 +153,20 @@ k_cache_attn_simt(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restric
         int issued = 0;
         for (; issued < kSimtStages - 1; ++issued) {
             const int g0 = gr.get(issued, 0), g1 = gr.get(issued, 1);
-            if (issued < steps) stage_step<D>(cache, ring_addr + issued * 2 * L::kBytes, g0, g1, lane); else copy_commit();
+            if (issued < steps)
+                stage_step<D>(cache, ring_addr + issued * 2 * L::kBytes, g0, g1, lane);
+            else
+                copy_commit();
             gr.advance(a, s, min(n, top), warp, lane, issued, &found);
         }
         for (int i = 0; i < steps; ++i) {
             const int nx = i + kSimtStages - 1;
             const int g0 = gr.get(nx, 0), g1 = gr.get(nx, 1);
             __syncwarp();
-            if (nx < steps) stage_step<D>(cache, ring_addr + (nx % kSimtStages) * 2 * L::kBytes, g0, g1, lane); else copy_commit();
+            if (nx < steps)
+                stage_step<D>(cache, ring_addr + (nx % kSimtStages) * 2 * L::kBytes, g0, g1, lane);
+            else
+                copy_commit();
             gr.advance(a, s, min(n, top), warp, lane, nx, &found);
             copy_wait<kSimtStages - 1>();
             __syncwarp();
@@ -334,10 +347,9 @@ template <typename T, int D, int NR> constexpr int mma_smem() {
 //
 // The codes come from shared memory into the registers of the lanes that feed
 // them to the step, are widened there and never go back to shared memory: one
-// conversion per two codes and one product by the scale, both exact. (The
-// tcgen05 form would need the widened operands in shared memory, 3.5 times the
-// cached bytes written and read again, for tiles of 128 rows of which decoding
-// fills 1 to 64.)
+// conversion per two codes and one product by the scale, both exact. (tcgen05
+// needs the widened operands in shared memory, 3.5 times the cached bytes written
+// and read again, which pays with more than 32 rows: cache_tile.cu.)
 //
 // Tokens and value channels are the 16 side of a step and query rows the 8 side
 // (S^T = K Q^T, O^T = V^T P^T): decoding has few rows, and with rows on the 16 side
@@ -358,7 +370,19 @@ template <typename T, int D, int NR> constexpr int mma_smem() {
 // float32 rows are each two halves, x = hi + lo with lo = x - hi rounded (22 bits and
 // a sign, 2^-23 of x), p likewise: two products where bf16 has one, with the same
 // exact keys and values. The products are summed in fp32 by steps of 16 tokens
-// and by ordinary additions from there.
+// and by ordinary additions from there. (8 x 12 heads of 16384 tokens, d = 64: 39 us, on
+// CUDA cores 52.)
+//
+// A warp has about 570 instructions per 32 tokens of 128 channels and 8 rows, 128 of
+// them conversions of codes and 128 products by scales (half rate each). Over the
+// whole of a 32 us launch (two 32k prompts, 32 heads) the arithmetic pipe is at
+// 51 %, the issue slots at 56 %, DRAM at 61 %; in the middle of it DRAM is near the
+// copy rate. Other forms, measured on that case, this one at 33 us, 36.7 with the join: rows
+// on the 16 side 42.7; with the join, 5 blocks per SM at 96 registers 39.8 against
+// 39.0 then, three copy stages 37.1, twice as many pieces of half the size 41.1, smaller
+// pieces for an SM's later blocks (which run behind the first) 37.2 to 38.6. Steps
+// of 64 tokens for d = 64: 131,072 tokens 68.1 to 64.8 us, but 26.8 to 27.9 for the
+// ragged drafts of 15 rows.
 template <typename T, int D, int NR>
 __global__ void __launch_bounds__(kThreads, mma_blocks(D, NR))
 k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict__ cache, AttnOut out) {
@@ -899,6 +923,11 @@ static long long cache_attn_units(const CacheArgs& a, int rtile, int extra) {
 CachePlan cache_attn_plan(const CacheArgs& a, int d, int dtype, unsigned flags) {
     CachePlan p{};
     const long long rows = (long long)a.G * a.T;
+    // Rows of a tile: the fewest that hold the cache head's rows. Up to 32 rows a tile is
+    // in registers; above, 64 rows of 128 channels go to tcgen05. (32 rows over 2 x 16 heads
+    // of 32768 tokens: 65 us in registers, 73 on tcgen05; 64 rows over 4 x 8 heads of 9000
+    // to 16384 tokens: 57.5 as two tiles in registers, 43.4 on tcgen05.) float32 takes
+    // twice the registers, so 16 rows at most.
     p.tensor = !(flags & MITA_FLAG_SIMT);
     int blocks = 4;  // per SM
     if (p.tensor) {

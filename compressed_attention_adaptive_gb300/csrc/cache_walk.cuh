@@ -10,7 +10,7 @@
 
 namespace mita {
 
-constexpr int kChunk = 128;    // tokens of a block's step
+constexpr int kChunk = 128;  // tokens of a block's step
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -52,9 +52,12 @@ __device__ __forceinline__ SeqWork seq_work(const CacheArgs& a, int b, int rtile
     return s;
 }
 
-// With less than kFew chunks per block an item's start is not counted: its blocks
-// run side by side then, and none has many. (64 sequences of 33 to 8191 tokens: the
-// slowest block at 69 us with the median at 49 without this, see the plan below.)
+// With fewer than kFew chunks per block an item's start is not counted: chunks run
+// side by side then, and what counts is that no block has one more of them.
+// Measured with 64 sequences of 33 to 8191 tokens (16,400 chunks, 512 items): the
+// slowest block ended at 69 us without `extra` and at 56 with it, the median at 49.
+// cache_tile.cu's items cost more to start and end (kTileExtra 2, 4, 6, 9: 45.2,
+// 43.2, 45.3, 45.3 us for 32 items of 64 rows over 9000 to 16384 tokens).
 constexpr int kExtra = 2, kTileExtra = 4, kFew = 8;
 
 // The line of units, cut into `pieces` pieces that differ by one unit at most.
@@ -102,7 +105,8 @@ template <int RT, int EXTRA = kExtra> struct Walk {
             const int len = sw.chunks + line.extra;
             if (w - before >= sw.items * len) {  // next sequence with work
                 before += sw.items * len;
-                sw = seq_work(a, ++b, RT);
+                if (++b >= a.B) return;
+                sw = seq_work(a, b, RT);
                 continue;
             }
             const int item = (w - before) / len, start = before + item * len;
@@ -142,13 +146,13 @@ template <int RT, int EXTRA = kExtra> struct Walk {
             l.pieces = min(max_pieces, total);
             l.q = l.pieces ? total / l.pieces : 0;
             l.r = total - l.q * l.pieces;
-            if (piece >= l.pieces) {
-                if (lane == 0) more = false;
-            } else {
+            if (lane == 0) more = false;
+            __syncwarp();
+            if (piece < l.pieces) {
                 const int w0 = l.at(piece);
                 int base = 0, x = 0, share = 0;
                 unsigned hit = 0;
-                for (int b0 = 0; !hit; b0 += 32) {
+                for (int b0 = 0; b0 < a.B && !hit; b0 += 32) {
                     if (a.B > 32) {
                         mine.items = 0;
                         if (b0 + lane < a.B) mine = seq_work(a, b0 + lane, RT);
