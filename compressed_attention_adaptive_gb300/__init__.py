@@ -94,6 +94,14 @@ class CacheParams:
         return _CCacheParams(self.B, self.H, self.H_kv, self.T, self.d, self.page, self.n_pages, self.max_pages,
                              float(self.scale), int(self.flags), int(self.dtype))
 
+    @functools.cached_property
+    def ref(self):
+        return ctypes.byref(self._c)
+
+    @functools.cached_property
+    def pool_bytes(self):  # mita_cache_size
+        return self.n_pages * self.H_kv * self.page * 9 * self.d // 8
+
     def c(self):
         return self._c
 
@@ -316,38 +324,46 @@ def cache_workspace(p: CacheParams, device="cuda"):
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _cache_args(p: CacheParams, tensors, shape, cache, table, lens, counts, exps, ws, lse, stream):
+def _cache_index(p: CacheParams, X, Y, heads, cache, table, lens, ws, counts, exps, stream):
     """Holds the tensors of a cache call to ``p`` (the C ABI sees only pointers) and
-    returns (device, stream, pointers of table, lens, counts and exps). Written out
-    and short: a decoding step makes these calls for every layer."""
+    returns the pointers of table, lens, counts and exps, and the stream. Written
+    out, not in loops: a decoding step makes these calls for every layer."""
     import torch
-    i32, dev = torch.int32, cache.get_device()
+    i32, u8, dev = torch.int32, torch.uint8, cache.get_device()
     dt = torch.bfloat16 if p.dtype == BF16 else torch.float32
-    for t in tensors:
-        if t.shape != shape or t.dtype is not dt or not t.is_contiguous() or t.get_device() != dev:
-            _refuse(t, shape, dt, dev)
-    for t, s in ((table, (p.B, p.max_pages)), (lens, (p.B,)), (counts, (p.B,)), (exps, (2, p.H_kv))):
-        if t is None:
-            if t is table or t is lens:
-                raise ValueError("table and lens are needed")
-        elif t.shape != s or t.dtype is not i32 or not t.is_contiguous() or t.get_device() != dev:
-            _refuse(t, s, i32, dev)
-    if lse is not None and (lse.shape != shape[:3] or lse.dtype is not torch.float32 or not lse.is_contiguous()
-                            or lse.get_device() != dev):
-        _refuse(lse, shape[:3], torch.float32, dev, "lse_out: ")
-    for t in (cache, ws):
-        if t.dtype is not torch.uint8 or not t.is_contiguous() or t.get_device() != dev:
-            _refuse(t, tuple(t.shape), torch.uint8, dev)
-    if cache.numel() < p.n_pages * p.H_kv * p.page * 9 * p.d // 8:  # mita_cache_size
-        raise ValueError("cache holds %d bytes, the pool needs %d" % (cache.numel(), mita_cache_size(p)))
+    s = (p.B, heads, p.T, p.d)
+    if X.dtype is not dt or X.get_device() != dev or X.shape != s or not X.is_contiguous():
+        _refuse(X, s, dt, dev)
+    if Y.dtype is not dt or Y.get_device() != dev or Y.shape != s or not Y.is_contiguous():
+        _refuse(Y, s, dt, dev)
+    s = (p.B, p.max_pages)
+    if table.dtype is not i32 or table.get_device() != dev or table.shape != s or not table.is_contiguous():
+        _refuse(table, s, i32, dev)
+    s = (p.B,)
+    if lens.dtype is not i32 or lens.get_device() != dev or lens.shape != s or not lens.is_contiguous():
+        _refuse(lens, s, i32, dev)
+    if counts is not None:
+        if counts.dtype is not i32 or counts.get_device() != dev or counts.shape != s or not counts.is_contiguous():
+            _refuse(counts, s, i32, dev)
+        counts = counts.data_ptr()
+    if exps is not None:
+        s = (2, p.H_kv)
+        if exps.dtype is not i32 or exps.get_device() != dev or exps.shape != s or not exps.is_contiguous():
+            _refuse(exps, s, i32, dev)
+        exps = exps.data_ptr()
+    if cache.dtype is not u8 or not cache.is_contiguous():
+        _refuse(cache, cache.shape, u8, dev)
+    if ws.dtype is not u8 or ws.get_device() != dev or not ws.is_contiguous():
+        _refuse(ws, ws.shape, u8, dev)
+    if cache.numel() < p.pool_bytes:
+        raise ValueError("cache holds %d bytes, the pool needs %d" % (cache.numel(), p.pool_bytes))
     if dev < 0:
         raise ValueError("the tensors must be on a CUDA device")
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(dev)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    return dev, stream, (table.data_ptr(), lens.data_ptr(), None if counts is None else counts.data_ptr(),
-                         None if exps is None else exps.data_ptr())
+    return table.data_ptr(), lens.data_ptr(), counts, exps, stream
 
 
 def _refuse(t, shape, dtype, dev, what=""):
@@ -357,8 +373,10 @@ def _refuse(t, shape, dtype, dev, what=""):
                                                                                 tuple(t.shape)))
 
 
-def _on_device(dev, fn, *args):
+def _on_device(t, fn, args):
+    """The C call with t's device current."""
     import torch
+    dev = t.get_device()
     if torch.cuda.current_device() == dev:
         rc = fn(*args)
     else:
@@ -370,21 +388,29 @@ def _on_device(dev, fn, *args):
 
 def mita_cache_write(p: CacheParams, K, V, cache, table, lens, ws, counts=None, exps=None, stream=None):
     """Stores the rows K, V [B, H_kv, T, d] in the pages that ``table`` names."""
-    dev, st, idx = _cache_args(p, (K, V), (p.B, p.H_kv, p.T, p.d), cache, table, lens, counts, exps, ws, None, stream)
-    _on_device(dev, lib().mita_cache_write, ctypes.byref(p.c()), K.data_ptr(), V.data_ptr(), cache.data_ptr(), *idx,
-               ws.data_ptr(), ws.numel(), st)
+    tp, lp, cp, ep, st = _cache_index(p, K, V, p.H_kv, cache, table, lens, ws, counts, exps, stream)
+    _on_device(cache, (_lib or lib()).mita_cache_write,
+               (p.ref, K.data_ptr(), V.data_ptr(), cache.data_ptr(), tp, lp, cp, ep, ws.data_ptr(), ws.numel(), st))
 
 
 def mita_cache_read(p: CacheParams, cache, table, lens, K, V, ws, counts=None, exps=None, stream=None):
     """Reads rows back into K, V [B, H_kv, T, d]; padding rows stay as they are."""
-    dev, st, idx = _cache_args(p, (K, V), (p.B, p.H_kv, p.T, p.d), cache, table, lens, counts, exps, ws, None, stream)
-    _on_device(dev, lib().mita_cache_read, ctypes.byref(p.c()), cache.data_ptr(), *idx, K.data_ptr(), V.data_ptr(),
-               ws.data_ptr(), ws.numel(), st)
+    tp, lp, cp, ep, st = _cache_index(p, K, V, p.H_kv, cache, table, lens, ws, counts, exps, stream)
+    _on_device(cache, (_lib or lib()).mita_cache_read,
+               (p.ref, cache.data_ptr(), tp, lp, cp, ep, K.data_ptr(), V.data_ptr(), ws.data_ptr(), ws.numel(), st))
 
 
 def mita_cache_attention(p: CacheParams, Q, cache, table, lens, O, ws, counts=None, exps=None, lse_out=None,
                          stream=None):
     """Attention of the rows Q [B, H, T, d] over the cache, into O (and lse_out)."""
-    dev, st, idx = _cache_args(p, (Q, O), (p.B, p.H, p.T, p.d), cache, table, lens, counts, exps, ws, lse_out, stream)
-    _on_device(dev, lib().mita_cache_attention, ctypes.byref(p.c()), Q.data_ptr(), cache.data_ptr(), *idx,
-               O.data_ptr(), None if lse_out is None else lse_out.data_ptr(), ws.data_ptr(), ws.numel(), st)
+    tp, lp, cp, ep, st = _cache_index(p, Q, O, p.H, cache, table, lens, ws, counts, exps, stream)
+    if lse_out is not None:
+        import torch
+        s = (p.B, p.H, p.T)
+        if (lse_out.dtype is not torch.float32 or lse_out.get_device() != cache.get_device() or lse_out.shape != s
+                or not lse_out.is_contiguous()):
+            _refuse(lse_out, s, torch.float32, cache.get_device(), "lse_out: ")
+        lse_out = lse_out.data_ptr()
+    _on_device(cache, (_lib or lib()).mita_cache_attention,
+               (p.ref, Q.data_ptr(), cache.data_ptr(), tp, lp, cp, ep, O.data_ptr(), lse_out, ws.data_ptr(), ws.numel(),
+                st))

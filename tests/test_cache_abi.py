@@ -96,7 +96,5 @@ def test_binding_checks_tensors(lib):
     q = torch.zeros((2, 8, 1, 128), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="device"):
         mita.mita_cache_attention(p, q, cache, table, lens, q, ws)
-    with pytest.raises(ValueError, match="lse_out"):
-        mita.mita_cache_attention(p, q, cache, table, lens, q, ws, lse_out=torch.zeros(2, 8, 1, 1))
     with pytest.raises(mita.MitaError):
         mita.cache_workspace(_p(d=96))

@@ -377,6 +377,27 @@ def test_more_rows_than_tokens():
     assert torch.all(O[0, 0, :2] == 0) and torch.all(L[0, 0, :2] == -math.inf)
 
 
+def test_binding_refuses():
+    """Shapes, types and devices that the pointers of the C side cannot show."""
+    import torch
+    import compressed_attention_adaptive_gb300 as mita
+    pool = Pool([20, 5], 2, 64, 16, "bf16", H=4)
+    Q = torch.zeros((2, 4, 1, 64), dtype=torch.bfloat16, device="cuda")
+    ok = dict(Q=Q, cache=pool.cache, table=pool.table, lens=pool.len_t, O=torch.zeros_like(Q), ws=pool.ws)
+    for bad in (dict(Q=Q.float()), dict(O=Q[:, :2]), dict(Q=Q.cpu()), dict(lens=pool.len_t.cpu()),
+                dict(table=pool.table.long()), dict(cache=pool.cache[:-1]), dict(ws=pool.ws.cpu()),
+                dict(counts=pool.len_t[:1]), dict(exps=pool.table[:1]), dict(lse_out=torch.zeros(2, 4, 1)),
+                dict(lse_out=torch.zeros((2, 4, 1), dtype=torch.float64, device="cuda")),
+                dict(lse_out=torch.zeros((2, 1, 4), device="cuda"))):
+        with pytest.raises(ValueError):
+            mita.mita_cache_attention(pool.p, **{**ok, **bad})
+    with pytest.raises(mita.MitaError) as err:
+        mita.mita_cache_attention(pool.p, **{**ok, "ws": pool.ws[:512]})
+    assert err.value.status == 3
+    mita.mita_cache_attention(pool.p, **ok)
+    mita.mita_device_status(pool.ws)
+
+
 # ------------------------------------------------------- streams and graphs
 
 
