@@ -78,7 +78,7 @@ struct CachePlan {
 };
 
 // Partial results of the attention, in the workspace.
-constexpr int kCutBytes = 24;  // one CutItem (cache_attn.cu)
+constexpr int kCutBytes = 24;  // one CutItem (cache_walk.cuh)
 struct CacheParts {
     float* part;  // [parts][d]
     float2* ml;   // [parts]
@@ -107,7 +107,7 @@ __device__ __forceinline__ int cache_exp(const CacheArgs& a, int which, int h) {
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }
 
 // Group number of sequence b's 16 tokens from 16 * gi on in head h, or -1 when
-// the table names no page of the pool (recorded by cache_check_call).
+// the table names no page of the pool (the kernels record it).
 __device__ __forceinline__ int cache_group(const CacheArgs& a, int b, int h, int gi) {
     const int col = gi / a.pgroups;
     const int pg = a.table[(long long)b * a.cols + col];
@@ -123,7 +123,7 @@ __device__ __forceinline__ bool bad_exps(const CacheArgs& a) {
     bool bad = false;
     if (a.exps)
         for (int i = threadIdx.x; i < 2 * a.Hkv; i += blockDim.x)
-            bad |= (unsigned)(a.exps[i] + kMaxExp) > (unsigned)(2 * kMaxExp);
+            bad |= (unsigned)a.exps[i] + kMaxExp > 2u * kMaxExp;
     return bad;
 }
 

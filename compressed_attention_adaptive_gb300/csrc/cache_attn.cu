@@ -376,8 +376,8 @@ template <typename T, int D, int NR> constexpr int mma_smem() {
 // A warp has about 570 instructions per 32 tokens of 128 channels and 8 rows, 128 of
 // them conversions of codes and 128 products by scales (half rate each). Over the
 // whole of a 32 us launch (two 32k prompts, 32 heads) the arithmetic pipe is at
-// 51 %, the issue slots at 56 %, DRAM at 61 %; in the middle of it DRAM is near the
-// copy rate. Other forms, measured on that case, this one at 33 us, 36.7 with the join: rows
+// 51 %, the issue slots at 56 %, DRAM at 0.72 of the copy rate; in the middle of it
+// DRAM is near that rate. Other forms, measured on that case, this one at 33 us, 36.7 with the join: rows
 // on the 16 side 42.7; with the join, 5 blocks per SM at 96 registers 39.8 against
 // 39.0 then, three copy stages 37.1, twice as many pieces of half the size 41.1, smaller
 // pieces for an SM's later blocks (which run behind the first) 37.2 to 38.6. Steps
