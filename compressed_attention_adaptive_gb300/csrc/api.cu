@@ -344,6 +344,13 @@ static CacheWork carve_cache(const mita_cache_params* p, const CachePlan& plan, 
     return w;
 }
 
+// Whether two tensors of `heads` heads share bytes.
+static bool cache_overlap(const mita_cache_params* p, int heads, const void* x, const void* y) {
+    const uintptr_t bytes = (uintptr_t)p->B * heads * p->T * p->d * (p->dtype == MITA_DTYPE_F32 ? 4 : 2);
+    const uintptr_t a = (uintptr_t)x, b = (uintptr_t)y;
+    return (a < b ? b - a : a - b) < bytes;
+}
+
 // Common part of the three calls; rows: the tensors in `dtype`.
 static mita_status cache_begin(const mita_cache_params* p, CacheArgs* a, CachePlan* plan, CacheWork* w,
                                const void* r0, const void* r1, const void* cache, const int32_t* table,
@@ -660,6 +667,7 @@ mita_status mita_cache_read(const mita_cache_params* p, const void* cache, const
     CacheWork w;
     const mita_status st = cache_begin(p, &a, &plan, &w, K, V, cache, table, len, count, exps, ws, ws_bytes);
     if (st) return st;
+    if (cache_overlap(p, p->H_kv, K, V)) return fail(MITA_ERR_INVALID_ARG, "K and V must not overlap");
     MITA_CUDA(launch_cache_rows(a, p->d, p->dtype, false, K, V, (void*)cache, (cudaStream_t)stream), "cache read");
     prof_mark((cudaStream_t)stream, "");
     return MITA_OK;
@@ -674,6 +682,7 @@ mita_status mita_cache_attention(const mita_cache_params* p, const void* Q, cons
     CacheWork w;
     const mita_status st = cache_begin(p, &a, &plan, &w, Q, O, cache, table, len, count, exps, ws, ws_bytes);
     if (st) return st;
+    if (cache_overlap(p, p->H, Q, O)) return fail(MITA_ERR_INVALID_ARG, "O must not overlap Q");
     if ((uintptr_t)lse_out % 4) return fail(MITA_ERR_INVALID_ARG, "lse_out must be 4-byte aligned");
     MITA_CUDA(launch_cache_attn(a, plan, p->d, p->dtype, Q, cache, O, lse_out, w.parts, (cudaStream_t)stream),
               "cache attention");

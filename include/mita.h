@@ -281,7 +281,7 @@ mita_status mita_cache_write(const mita_cache_params* p, const void* K, const vo
                              void* ws, size_t ws_bytes, void* stream);
 
 /* Reads rows back into K, V: [B, H_kv, T, d] in `dtype`. With T the longest
- * sequence and count = len it returns whole sequences. */
+ * sequence and count = len it returns whole sequences. K and V must not overlap. */
 mita_status mita_cache_read(const mita_cache_params* p, const void* cache, const int32_t* table, const int32_t* len,
                             const int32_t* count, const int32_t* exps, void* K, void* V, void* ws, size_t ws_bytes,
                             void* stream);
@@ -290,7 +290,8 @@ mita_status mita_cache_read(const mita_cache_params* p, const void* cache, const
  * i / (H / H_kv). Row t sees the keys j < len[b], with MITA_FLAG_CAUSAL those up
  * to its own position (j < len[b] - (count[b] - 1 - t)); a row that sees no key
  * gets zeros. A key that a row does not see has no influence on it, whatever its
- * bytes are. O: [B, H, T, d] in `dtype`. lse_out (float32 [B, H, T], or NULL):
+ * bytes are, and neither have the call's other rows; a row with a NaN or an
+ * infinity that sees a key gets NaN. O: [B, H, T, d] in `dtype`. lse_out (float32 [B, H, T], or NULL):
  * ln sum exp(scale q.k) over the seen keys, -infinity without any, with which the
  * rows can be joined with attention over other keys (mita_forward's shared
  * slots, say). count > len is allowed: rows before the first token see none.

@@ -98,3 +98,16 @@ def test_binding_checks_tensors(lib):
         mita.mita_cache_attention(p, q, cache, table, lens, q, ws)
     with pytest.raises(mita.MitaError):
         mita.cache_workspace(_p(d=96))
+
+
+def test_overlapping_rows_are_refused(lib):
+    """A part of O over Q would be read after it was written, and K over V written twice."""
+    p = _p()
+    c, need, at = ctypes.byref(p.c()), mita.mita_cache_workspace_size(p), 1 << 20
+    f, q_bytes, k_bytes = ctypes.c_void_p(at), 2 * 8 * 128 * 2, 2 * 2 * 128 * 2
+    for off in (0, 16, q_bytes - 16, -16, 16 - q_bytes):
+        assert lib.mita_cache_attention(c, f, f, f, f, None, None, ctypes.c_void_p(at + off), None, f, need, None) == 1
+        assert b"overlap" in lib.mita_last_error()
+    for off in (0, k_bytes - 16, 16 - k_bytes):
+        assert lib.mita_cache_read(c, f, f, f, None, None, f, ctypes.c_void_p(at + off), f, need, None) == 1
+        assert b"overlap" in lib.mita_last_error()
