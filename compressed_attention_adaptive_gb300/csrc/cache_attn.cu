@@ -143,7 +143,8 @@ k_cache_attn_simt(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restric
             l[r] = 0.0f;
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                q[r][i] = to_float(Q[at + i]);
+                const float x = to_float(Q[at + i]);
+                q[r][i] = isfinite(x) ? x : __int_as_float(0x7fc00000);  // the row becomes NaN, as its softmax is
                 o[r][i] = 0.0f;
             }
         }
@@ -331,7 +332,8 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float x, float y, float
 }
 
 constexpr int kStages = 2;
-// Blocks per SM that the registers allow without spills. (16 rows of 128 channels: 3 blocks 48.6 us,
+// Blocks per SM that the registers allow without spills (but 4 to 8 registers of float32
+// rows of 128 channels, at a segment's start). (16 rows of 128 channels: 3 blocks 48.6 us,
 // 4 at 128 registers 51.2; 16 rows of 64: 33.0 and 30.9.)
 constexpr int mma_blocks(int d, int NR) { return NR == 1 ? 4 : d == 64 ? (NR == 2 ? 4 : 3) : (NR == 2 ? 3 : 2); }
 
@@ -467,12 +469,10 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
                 amax = max(amax, F ? x[i] & 0x7fffffffu : max(x[i] << 16 & 0x7fff0000u, x[i] & 0x7fff0000u));
             amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            const int ex = (int)(amax >> 23);  // biased exponent of the row's largest entry
-            const int qe = ex == 255 ? 0 : min(141 - ex, 120);
-            const float up = pow2(qe), kf = a.scale * kLog2e * pow2(cache_exp(a, 0, s.h));
+            float up, f;
+            query_scale(a, s.h, amax >> 23, &up, &f);
             if (t4 == 0) {
-                // kept away from 0 and infinity: a masked score is -infinity times it
-                szf[r] = fminf(fmaxf(kf * pow2(-qe), 1.1754944e-38f), 3.4028235e38f);
+                szf[r] = f;
                 slim[r] = r < s.rows ? row_limit(a, n, count, t) : 0;
             }
 #pragma unroll
@@ -633,7 +633,7 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
                     for (int x = 0; x < GP; ++x)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            y[j][x][e] = fmaf(z[j][x][e], zf[j][e & 1], -m[j][e & 1]);
+                            y[j][x][e] = score_diff(z[j][x][e], zf[j][e & 1], m[j][e & 1]);
                             big = fmaxf(big, y[j][x][e]);
                         }
                 if (__any_sync(0xffffffffu, big > 15.0f)) {
@@ -645,7 +645,9 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
                             if (GP == 2) v = fmaxf(v, fmaxf(z[j][GP - 1][e], z[j][GP - 1][e + 2]));
 #pragma unroll
                             for (int x = 4; x < 32; x <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
-                            const float mn = fmaxf(m[j][e], fmaf(v, zf[j][e], -7.0f)), f = ex2(m[j][e] - mn);
+                            // (a row's own scores move it, not another's)
+                            const float mn = score_diff(v, zf[j][e], m[j][e]) > 15.0f ? score_diff(v, zf[j][e], 7.0f) : m[j][e];
+                            const float f = ex2(m[j][e] - mn);
                             m[j][e] = mn;
                             l[j][e] *= f;
 #pragma unroll
@@ -655,8 +657,8 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
                             }
 #pragma unroll
                             for (int x = 0; x < GP; ++x) {
-                                y[j][x][e] = fmaf(z[j][x][e], zf[j][e], -mn);
-                                y[j][x][e + 2] = fmaf(z[j][x][e + 2], zf[j][e], -mn);
+                                y[j][x][e] = score_diff(z[j][x][e], zf[j][e], mn);
+                                y[j][x][e + 2] = score_diff(z[j][x][e + 2], zf[j][e], mn);
                             }
                         }
                 }
@@ -913,7 +915,7 @@ __global__ void __launch_bounds__(32 * kJoinRows * kJoinWarps) k_cache_join(Cach
 
 // ------------------------------------------------------------------ launch
 
-// Units of the line, at most (cache_attn.cu's Line counts them in 32 bits).
+// Units of the line, at most (cache_walk.cuh's Line counts them in 32 bits).
 static long long cache_attn_units(const CacheArgs& a, int rtile, int extra) {
     const long long tiles = ((long long)a.G * a.T + rtile - 1) / rtile;
     const long long len = ((long long)a.cols * a.page + kChunk - 1) / kChunk;

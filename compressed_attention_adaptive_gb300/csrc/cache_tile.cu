@@ -23,8 +23,7 @@
 // accumulators. Every wait is bounded; a block that gives up raises its abort
 // flag, lets its copies and products land and frees its tensor memory.
 //
-// Measured: 64 rows over 2 x 16 heads of 131,072 tokens 281 us (490 TFLOP/s; the
-// register form about 480 us), 4 x 8 heads of 9000 to 16384 tokens 43 us (57.5). A
+// Measured: 64 rows over 2 x 16 heads of 131,072 tokens 281 us (490 TFLOP/s), 4 x 8 heads of 9000 to 16384 tokens 43 us (57.5). A
 // chunk takes about 2300 clocks, and no unit is full: the products alone would take
 // 800 (51 each in a kernel of nothing else), shared memory is at 46 %, the issue
 // slots at 53 %. It waits for instructions of 26 warps with four different loops:
@@ -186,8 +185,7 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
     uint8_t* smp = smem_raw + (sm - smem_addr(smem_raw));
     __shared__ Walk<N, kTileExtra> walk;
     __shared__ TileBars bar;
-    __shared__ __align__(16) float mref[N];  // the rows' references
-    __shared__ uint32_t qmax[S::kSoft];
+    __shared__ __align__(16) float2 ref[N];  // the rows' factors of scores, in log2 units, and references
     __shared__ float fac[N], lsum[N], linv[N], part4[4][N];
     __shared__ int lim[N], nan_flag;
     __shared__ long long row_at[N];
@@ -227,13 +225,14 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
 
     int done = 0, seg = 0;  // chunks and segments before this one: the barriers' phases go on
     int issued = 0;         // chunks that the copying warp has issued
+    bool stop = false;      // a wait of an earlier segment gave up
     for (; more; ++seg) {
         const Segment s = walk.s;
         const int n = walk.sw.n, count = walk.sw.count;
         const int low = row_limit(a, n, count, s.row0 / a.G), top = row_limit(a, n, count, (s.row0 + s.rows - 1) / a.G);
         // chunks that some row of the tile sees, at least one
         const int nc = max(1, min(s.c1, (top + kChunk - 1) / kChunk) - s.c0);
-        if (abort_flag) {
+        if (stop) {
             // only the items' ends are still noted
         } else if (warp == S::kCopy) {
             // ---------------------------------------------------- copies
@@ -418,10 +417,7 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
         } else {
             // --------------------------------------------------- softmax
             const float vscale = pow2(cache_exp(a, 1, s.h));
-            // Q: thread (r, part) has 16 channels of row r. All rows of the tile are scaled by the power
-            // of two that puts the largest finite entry in [2^14, 2^15): bf16 is exact as halves down
-            // to 2^-31 of it, and what is lost below is 2^-40 of the largest scores.
-            float f;  // factor of the scores, in log2 units
+            // Q: thread (r, part) has 16 channels of row r, scaled as in cache_attn.cu.
             {
                 const int r = tid >> 3, part = tid & 7;
                 int t = 0;
@@ -434,24 +430,16 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
                     x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t lo = x[i] & 0x7fffu, hi = x[i] >> 16 & 0x7fffu;
-                    amax = max(amax, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-                }
-                amax = __reduce_max_sync(0xffffffffu, amax);
-                if (lane == 0) qmax[warp] = amax;
+                for (int i = 0; i < 8; ++i) amax = max(amax, max(x[i] & 0x7fffu, x[i] >> 16 & 0x7fffu));
+#pragma unroll
+                for (int i = 1; i < 8; i <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, i));
+                float up, f;
+                query_scale(a, s.h, amax >> 7, &up, &f);
                 if (part == 0) {
-                    mref[r] = kNoKey;
+                    ref[r] = make_float2(f, kNoKey);
                     lim[r] = r < s.rows ? row_limit(a, n, count, t) : 0;
                     row_at[r] = at;
                 }
-                softmax_sync<S::kSoft>();
-#pragma unroll
-                for (int i = 0; i < S::kSoft; ++i) amax = max(amax, qmax[i]);
-                const int qe = min(141 - (int)(amax >> 7), 120);
-                const float up = pow2(qe);
-                // kept away from 0 and infinity: a masked score is -infinity times it
-                f = fminf(fmaxf(a.scale * kLog2e * pow2(cache_exp(a, 0, s.h)) * pow2(-qe), 1.1754944e-38f), 3.4028235e38f);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     uint32_t h[4];
@@ -479,17 +467,15 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
                 tc::fence_after_sync();
                 const bool edge = (s.c0 + c + 1) * kChunk > low;  // some row does not see all of the chunk
                 float y[HN], big = kNoKey;
-                // again after the reference has moved, which happens once: no score is more than 7 above it then
+                // again after references have moved, which happens once
 #pragma unroll 1
                 for (int again = 0;; ++again) {
                     load_cols(cols + st * 64, y);
 #pragma unroll
-                    for (int r = 0; r < HN; r += 4) {
-                        const float4 m = *reinterpret_cast<const float4*>(mref + r0 + r);
-                        y[r] = fmaf(y[r], f, -m.x);
-                        y[r + 1] = fmaf(y[r + 1], f, -m.y);
-                        y[r + 2] = fmaf(y[r + 2], f, -m.z);
-                        y[r + 3] = fmaf(y[r + 3], f, -m.w);
+                    for (int r = 0; r < HN; r += 2) {
+                        const float4 m = *reinterpret_cast<const float4*>(ref + r0 + r);
+                        y[r] = score_diff(y[r], m.x, m.y);
+                        y[r + 1] = score_diff(y[r + 1], m.z, m.w);
                     }
                     if (edge) {
 #pragma unroll
@@ -502,15 +488,16 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
                     if (!softmax_any<S::kSoft>(big > 15.0f)) break;
                     load_cols(cols + st * 64, y);
 #pragma unroll
-                    for (int r = 0; r < HN; ++r) y[r] = edge && tok >= lim[r0 + r] ? -INFINITY : y[r] * f;
+                    for (int r = 0; r < HN; ++r) y[r] = edge && tok >= lim[r0 + r] ? -INFINITY : __fmul_rn(y[r], ref[r0 + r].x);
                     reduce_lanes(y, lane, [](float p, float q) { return fmaxf(p, q); });
                     part4[quarter][r0 + HN * lane / 32] = y[0];
                     softmax_sync<S::kSoft>();
                     if (tid < N) {
                         const float mx = fmaxf(fmaxf(part4[0][tid], part4[1][tid]), fmaxf(part4[2][tid], part4[3][tid]));
-                        const float old = mref[tid], mn = fmaxf(old, mx - 7.0f);
-                        fac[tid] = tc::ex2(old - mn);
-                        mref[tid] = mn;
+                        // (a row's own scores move it, not another's)
+                        const float old = ref[tid].y, mn = mx - old > 15.0f ? mx - 7.0f : old;
+                        fac[tid] = ex2(old - mn);
+                        ref[tid].y = mn;
                     }
                     softmax_sync<S::kSoft>();
 #pragma unroll
@@ -534,7 +521,7 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int r = 8 * j + 2 * i;
-                        const float p0 = tc::ex2(y[r]), p1 = tc::ex2(y[r + 1]);
+                        const float p0 = ex2(y[r]), p1 = ex2(y[r + 1]);
                         l[r] += p0;
                         l[r + 1] += p1;
                         h[i] = pack_half2(p0, p1);
@@ -580,7 +567,7 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
                     }
                 }
                 if (tid < s.rows) {
-                    const float sum = lsum[tid], m = mref[tid];
+                    const float sum = lsum[tid], m = ref[tid].y;
                     if (!whole)
                         out.ml[slot + tid] = make_float2(m, sum);
                     else if (out.lse)
@@ -596,6 +583,8 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
         }
         walk.note(a, out, piece);
         done += nc;
+        // every warp is through the segment, so that all see the same and meet at the same barriers
+        stop = __syncthreads_or(abort_flag);
         more = walk.next(a);
         tc::fence_after_sync();
     }

@@ -257,6 +257,22 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     return r;
 }
 
+// Query rows go to halves scaled by a power of two (`up`) that puts the row's
+// largest entry, of biased exponent ex, in [2^14, 2^15); f: the factor of the
+// scores for it, in log2 units. A row with an infinity or a NaN becomes NaN
+// altogether, as its softmax is (infinite scores have no differences).
+__device__ __forceinline__ void query_scale(const CacheArgs& a, int h, int ex, float* up, float* f) {
+    const int qe = min(141 - ex, 120);
+    *up = ex == 255 ? __int_as_float(0x7fc00000) : pow2(qe);
+    // kept away from 0 and infinity: a masked score is -infinity times it
+    *f = fminf(fmaxf(a.scale * kLog2e * pow2(cache_exp(a, 0, h)) * pow2(-qe), 1.1754944e-38f), 3.4028235e38f);
+}
+
+// z f - m, with the product rounded: the reference m was made of a rounded product
+// too, so that the difference to its own score stays 7 (or less) when scores are so
+// large that 7 is lost in them. One rounding would leave up to 2^-24 of m.
+__device__ __forceinline__ float score_diff(float z, float f, float m) { return __fadd_rn(__fmul_rn(z, f), -m); }
+
 constexpr float kNoKey = -1.7e38f;  // a row's maximum before it has seen a key: finite, so that differences are
 
 // cache_attn.cu

@@ -250,6 +250,49 @@ def test_bad_rows_stay_in_their_rows(dtype, H, d):
     assert torch.equal(O2[0][~hit.cuda()], O[0][~hit.cuda()])
 
 
+@pytest.mark.parametrize("dtype,H,d,simt", [("bf16", 8, 128, False), ("bf16", 24, 64, False), ("bf16", 64, 128, False),
+                                            ("f32", 8, 128, False), ("f32", 16, 64, False), ("bf16", 8, 128, True)])
+def test_rows_do_not_influence_each_other(dtype, H, d, simt):
+    """Rows next to huge, tiny, infinite and NaN ones are the same bits as without them;
+    a row with an infinity is NaN also where all of its scores are -infinity."""
+    import torch
+
+    def make(rng, shape):
+        K, V = Pool.rows(rng, shape)
+        K[..., 3] = 4 + np.abs(K[..., 3])
+        return K, V
+
+    pool = Pool([700, 33], 2, d, 16, dtype, make=make, seed=13)
+    Q, O, L = _attend(pool, H, 2, True, simt=simt)
+    bad = Q.clone()
+    bad[:, 0::4, 0] *= 1e30
+    bad[:, 1::4, 0] *= 1e-30
+    bad[:, 2::4, 0, 3] = -math.inf
+    bad[:, 3::4, 0, 3] = math.inf
+    bad[:, 3::8, 0, 5] = math.nan
+    _, O2, L2 = _attend(pool, H, 2, True, q=bad, simt=simt)
+    assert torch.equal(O2[:, :, 1], O[:, :, 1]) and torch.equal(L2[:, :, 1], L[:, :, 1])
+    for h in (2, 3):
+        assert O2[:, h::4, 0].isnan().all() and L2[:, h::4, 0].isnan().all()
+    u = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    # the huge rows have the values of their largest score, up to scores that fp32 sums cannot tell from it
+    for b, n in enumerate(pool.lens):
+        for h in range(0, H, 4):
+            k, v = (pool.held(b, w)[h // (H // 2), :n - 1] for w in (0, 1))
+            q = _np(bad[b, h, 0])
+            z, err = k @ q, (d + 8) * 2.0 ** -23 * (np.abs(k) @ np.abs(q)).max()
+            top, got = v[z >= z.max() - 2 * err], _np(O2[b, h, 0])
+            slack = (u + 100 * 2.0 ** -23) * np.abs(top).max(0)
+            assert np.all(got >= top.min(0) - slack) and np.all(got <= top.max(0) + slack)
+    # the tiny rows weigh all keys alike
+    for b, n in enumerate(pool.lens):
+        mean = np.stack([pool.held(b, 1)[h, :n - 1].mean(0) for h in range(2)]).repeat(H // 2, 0)
+        spread = np.stack([np.abs(pool.held(b, 1)[h, :n - 1]).mean(0) for h in range(2)]).repeat(H // 2, 0)
+        # the output's rounding; equal weights round alike; chains of fp32 additions and one quotient
+        tol = u * np.abs(mean) + (n / 16 + 70) * 2.0 ** -23 * spread
+        assert np.all(np.abs(_np(O2[b, :, 0]) - mean)[1::4] <= tol[1::4])
+
+
 @pytest.mark.parametrize("H", [8, 64])
 def test_repeated_calls_are_bit_equal_and_lse_is_optional(H):
     import torch
