@@ -350,8 +350,8 @@ template <typename T, int D, int NR> constexpr int mma_smem() {
 // The codes come from shared memory into the registers of the lanes that feed
 // them to the step, are widened there and never go back to shared memory: one
 // conversion per two codes and one product by the scale, both exact. (tcgen05
-// needs the widened operands in shared memory, 3.5 times the cached bytes written
-// and read again, which pays with more than 32 rows: cache_tile.cu.)
+// needs the widened operands written first, to shared or tensor memory, 3.5 times the
+// cached bytes, which pays with more than 32 rows: cache_tile.cu.)
 //
 // Tokens and value channels are the 16 side of a step and query rows the 8 side
 // (S^T = K Q^T, O^T = V^T P^T): decoding has few rows, and with rows on the 16 side
@@ -927,8 +927,8 @@ CachePlan cache_attn_plan(const CacheArgs& a, int d, int dtype, unsigned flags) 
     const long long rows = (long long)a.G * a.T;
     // Rows of a tile: the fewest that hold the cache head's rows. Up to 32 rows a tile is
     // in registers; above, 64 rows of 128 channels go to tcgen05. (32 rows over 2 x 16 heads
-    // of 32768 tokens: 65 us in registers, 73 on tcgen05; 64 rows over 4 x 8 heads of 9000
-    // to 16384 tokens: 57.5 as two tiles in registers, 43.4 on tcgen05.) float32 takes
+    // of 32768 tokens: 66 us in registers, 78 on tcgen05; 64 rows over 4 x 8 heads of 9000
+    // to 16384 tokens: 57.5 as two tiles in registers, 45.2 on tcgen05.) float32 takes
     // twice the registers, so 16 rows at most.
     p.tensor = !(flags & MITA_FLAG_SIMT);
     int blocks = 4;  // per SM

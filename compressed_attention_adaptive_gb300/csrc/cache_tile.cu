@@ -5,33 +5,40 @@
 // With 64 rows a cached token costs 64 times 4 d = 32,768 flops against 144 bytes.
 // The register form of cache_attn.cu needs 17.6 clocks of an SM per token for that
 // at its full rate, and widens the codes for each 32 rows anew. Here a chunk of
-// 128 tokens is widened once, to halves in shared memory, for all rows:
+// 128 tokens is widened once, to halves in tensor memory, for all rows:
 //
-//   S^T = K Q^T    128 tokens x N rows, K and Q K-major tiles, fp32 in tensor memory
+//   S^T = K Q^T    128 tokens x N rows: K from tensor memory, Q a K-major tile, fp32 in tensor memory
 //   P^T = 2^(f S^T - m) as halves, in shared memory (MN-major: a token's N rows are contiguous)
-//   O^T += V^T P^T  128 channels x N rows, V as it was widened (MN-major), fp32 in tensor memory
+//   O^T += V^T P^T  128 channels x N rows: V^T from tensor memory, O^T fp32 in tensor memory
 //
 // Tokens and channels are the 128 side: rows would fill only half of it. A softmax
-// thread has a token of S^T with all its rows, so a row's maximum would go across
+// thread has a token of S^T with 16 of its rows, so a row's maximum would go across
 // 128 threads; as in cache_attn.cu the reference m is only moved when a score
 // exceeds it by more than 15, and each thread keeps its own part of the rows' sums
 // until a segment ends.
 //
-// Warps: N / 4 for the softmax and the epilogue, each warpgroup 16 of the rows; one
-// copies (eight lanes, a group of 16 tokens each); one issues the products; eight
-// widen. Raw codes, K, V and P have two stages each; S two
-// accumulators. Every wait is bounded; a block that gives up raises its abort
-// flag, lets its copies and products land and frees its tensor memory.
+// Widened operands go to tensor memory, 512 columns in all: keys as rows of 64
+// columns, a lane a token; values in the register order of m16n8k16's A, which is
+// that of a 16 x 128 bit store and needs no transposition. Lane 32 w + 16 i + 8 o + g
+// has channel 16 g + 4 w + 2 i + o. (As tiles in shared memory they were written and
+// read there, 160 KB a chunk: 288 us against 269 for the long case below.)
 //
-// Measured: 64 rows over 2 x 16 heads of 131,072 tokens 281 us (490 TFLOP/s), 4 x 8 heads of 9000 to 16384 tokens 43 us (57.5). A
-// chunk takes about 2300 clocks, and no unit is full: the products alone would take
-// 800 (51 each in a kernel of nothing else), shared memory is at 46 %, the issue
-// slots at 53 %. It waits for instructions of 26 warps with four different loops:
-// the issuing warp's operands in uniform registers took 323 us to 288, 16 rows per
-// softmax thread instead of 32 a softmax chunk from 2200 clocks to 1450, an
-// epilogue of little code 13 us off every item (cold instructions).
+// Warps: N / 4 for the softmax and the epilogue, each warpgroup 16 of the rows; one
+// copies; one issues the products; four widen keys and four values. Codes have four
+// stages, scores and weights three, keys and values two. Every wait is bounded; a
+// block that gives up raises its abort flag, lets its copies and products land and
+// frees its tensor memory.
+//
+// Measured: 64 rows over 2 x 16 heads of 131,072 tokens 269 us (510 TFLOP/s), of 32,768
+// 81 us; 4 x 8 heads of 9000 to 16384 tokens 45 us (the register form 57.5). A chunk
+// takes about 2400 clocks, and no role is busy all of it: softmax 1900, values 1500,
+// issuing 1000 (a product of 128 x 64 x 16 takes 51 to 60), copies 1000, keys 800. They
+// share the issue slots (56 %, 6500 instructions a chunk) and wait for each other's
+// stages. What it took: operands in uniform registers (323 us to 288), 16 rows per softmax
+// thread instead of 32 (a softmax chunk 2200 clocks to 1450), an epilogue of little
+// code (13 us off every item: cold instructions), fewer and longer copies (each takes 180
+// clocks to issue).
 #include <atomic>
-#include <type_traits>
 
 #include "cache_walk.cuh"
 
@@ -42,7 +49,7 @@ namespace {
 constexpr int kD = 128, N = 64;  // channels; rows of a tile
 constexpr int HN = 16;           // rows of a softmax thread
 constexpr int kRaw = 8 * Grp<kD>::kBytes;  // a chunk's codes and scales
-constexpr int kTile = 128 * kD * 2;        // a chunk's keys or values as halves
+constexpr int kRawStages = 4, kSoftStages = 3;  // of codes; of scores and weights
 constexpr int kEdge = 64;                  // tokens that only some rows of a tile see, at most
 constexpr long long kSpin = 2LL << 30;     // about a second
 
@@ -50,8 +57,8 @@ struct TileSmem {
     static constexpr int kSoft = N / 4, kCopy = kSoft, kIssue = kSoft + 1, kWiden = kSoft + 2;  // warps
     static constexpr int kThreads = 32 * (kSoft + 10);
     static constexpr int kP = 128 * 128;  // a token's rows, padded to 128 bytes
-    static constexpr int kQ = 0, kK = kQ + 64 * kD * 2, kV = kK + 2 * kTile, kPo = kV + 2 * kTile, kRawO = kPo + 2 * kP,
-                         kBytes = kRawO + 2 * kRaw + 1024;
+    static constexpr int kQ = 0, kPo = kQ + 64 * kD * 2, kRawO = kPo + kSoftStages * kP,
+                         kBytes = kRawO + kRawStages * kRaw + 1024;
 };
 
 // Instruction descriptor of kind::f16 with half A and B and fp32 accumulate.
@@ -77,24 +84,26 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
     return __all_sync(0xffffffffu, tile_wait(bar, parity, abort_flag));
 }
 // For what this block has issued to the asynchronous units, whatever the abort flag says.
-__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, int* status) { (void)tc::mbar_wait(bar, parity, status); }
-
-// The W softmax warps meet here, all of them the same number of times whatever
-// happened to the waits before.
-template <int W> __device__ __forceinline__ void softmax_sync() {
-    __syncwarp();
-    asm volatile("barrier.sync 1, %0;" ::"n"(32 * W) : "memory");
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, int* status) {
+    (void)tc::mbar_wait(bar, parity, status);
 }
-template <int W> __device__ __forceinline__ bool softmax_any(bool x) {
+
+// The four softmax warps with the same rows meet here (barrier 1 + wg), all of them the
+// same number of times whatever happened to the waits before.
+__device__ __forceinline__ void softmax_sync(int wg) {
+    __syncwarp();
+    asm volatile("barrier.sync %0, 128;" ::"r"(1 + wg) : "memory");
+}
+__device__ __forceinline__ bool softmax_any(int wg, bool x) {
     uint32_t r;
     __syncwarp();
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.red.or.pred q, 1, %2, p;\n\t"
+        "barrier.red.or.pred q, %2, 128, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)x), "n"(32 * W)
+        : "r"((uint32_t)x), "r"(1 + wg)
         : "memory");
     return r != 0;
 }
@@ -141,6 +150,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
         "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+// Registers {a0, a1, a2, a3} of an m16n8k16 step's A, twice (two steps): 16 lanes, 16 columns.
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 __device__ __forceinline__ void load_cols(uint32_t taddr, float* v) {  // HN columns
     tmem_ld16(taddr, v);
     tc::tmem_wait_ld();
@@ -170,8 +185,8 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 struct TileBars {
-    uint64_t raw_full[2], raw_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2];
-    uint64_t q_full, pv_done, o_full, drain;
+    uint64_t raw_full[kRawStages], raw_empty[kRawStages], k_full[2], v_full[2], v_empty[2];
+    uint64_t s_full[kSoftStages], p_full[kSoftStages], q_full, o_full, drain;
 };
 
 }  // namespace
@@ -197,20 +212,22 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
     const int piece = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int found = 0;
     if (!out.items && tid == 0) out.cut[piece] = CutItem{};
-    if (warp == S::kIssue) tc::tmem_alloc(&tmem_slot, 256);
+    if (warp == S::kIssue) tc::tmem_alloc(&tmem_slot, 512);
     if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&bar.raw_full[i], 8);
+        for (int i = 0; i < kRawStages; ++i) {
+            tc::mbar_init(&bar.raw_full[i], 1);
             tc::mbar_init(&bar.raw_empty[i], 8);
+        }
+        for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&bar.k_full[i], 4);
-            tc::mbar_init(&bar.k_empty[i], 1);
             tc::mbar_init(&bar.v_full[i], 4);
             tc::mbar_init(&bar.v_empty[i], 1);
+        }
+        for (int i = 0; i < kSoftStages; ++i) {
             tc::mbar_init(&bar.s_full[i], 1);
             tc::mbar_init(&bar.p_full[i], S::kSoft);
         }
         tc::mbar_init(&bar.q_full, S::kSoft);
-        tc::mbar_init(&bar.pv_done, 1);
         tc::mbar_init(&bar.o_full, 1);
         tc::mbar_init(&bar.drain, 1);
         tc::fence_mbar_init();
@@ -221,7 +238,7 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
     bool more = walk.begin(a, piece, out.pieces);
     tc::fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
-    constexpr uint32_t kO = 128;  // columns: two S of 64, O
+    constexpr uint32_t kO = 192, kK = 256, kV = 384;  // columns: three S of 64, O, two chunks' keys, two chunks' values
 
     int done = 0, seg = 0;  // chunks and segments before this one: the barriers' phases go on
     int issued = 0;         // chunks that the copying warp has issued
@@ -236,182 +253,190 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
             // only the items' ends are still noted
         } else if (warp == S::kCopy) {
             // ---------------------------------------------------- copies
-            if (lane < 8) {
-                auto group = [&](int c) {
-                    const int gi = (s.c0 + c) * 8 + lane;
-                    if (c >= nc || gi * kGroup >= top) return -1;
-                    const int g = cache_group(a, s.b, s.h, gi);
-                    if (g < 0) found |= kFoundBounds;
-                    return g;
-                };
-                int g = group(0);
-                for (int c = 0; c < nc; ++c) {
-                    const int t = done + c, st = t & 1, gn = group(c + 1);
-                    if (!tile_wait(&bar.raw_empty[st], ((t >> 1) & 1) ^ 1, abort_v)) break;
-                    if (g >= 0) {
-                        tc::mbar_expect_tx(&bar.raw_full[st], L::kBytes);
-                        bulk_copy(sm + S::kRawO + st * kRaw + lane * L::kBytes, cache + (long long)g * L::kBytes, L::kBytes,
-                                  &bar.raw_full[st]);
-                    } else {
-                        tc::mbar_arrive(&bar.raw_full[st]);
-                    }
-                    issued = t + 1;
-                    g = gn;
+            // Lane l looks after group l % 8 of chunk l / 8 in the current run of four chunks; the next
+            // run's table entries are loaded a run ahead. A copy takes the groups that a page and a
+            // chunk have together (issuing one takes 180 clocks), and the first one's lane issues it.
+            struct Copy {
+                const uint8_t* src;
+                uint32_t bytes;
+            };
+            auto copies = [&](int c0) {
+                const int c = c0 + (lane >> 3), first = lane & 7, gi = (s.c0 + c) * 8 + first, rem = gi % a.pgroups;
+                const int last = (top + kGroup - 1) / kGroup;
+                if (c >= nc || gi >= last || (first && rem)) return Copy{nullptr, 0};
+                const int g = cache_group(a, s.b, s.h, gi);
+                if (g < 0) {
+                    found |= kFoundBounds;
+                    return Copy{nullptr, 0};
+                }
+                const int groups = min(min(8 - first, a.pgroups - rem), last - gi);
+                return Copy{cache + (long long)g * L::kBytes, (uint32_t)(groups * L::kBytes)};
+            };
+            Copy cur = copies(0), nxt = copies(4);
+            for (int c = 0; c < nc; ++c) {
+                const int t = done + c, st = t % kRawStages;
+                if (!warp_wait(&bar.raw_empty[st], ((t / kRawStages) & 1) ^ 1, abort_v)) break;
+                const bool mine = (lane >> 3) == (c & 3);
+                const uint32_t bytes = __reduce_add_sync(0xffffffffu, mine ? cur.bytes : 0u);
+                if (elect_one()) tc::mbar_expect_tx(&bar.raw_full[st], bytes);
+                __syncwarp();
+                if (mine && cur.bytes)
+                    bulk_copy(sm + S::kRawO + st * kRaw + (lane & 7) * L::kBytes, cur.src, cur.bytes, &bar.raw_full[st]);
+                issued = t + 1;
+                if ((c & 3) == 3) {
+                    cur = nxt;
+                    nxt = copies(c + 5);
                 }
             }
             __syncwarp();
         } else if (warp == S::kIssue) {
             // -------------------------------------------------- products
-            // The whole warp goes through the loop and one lane's instructions are predicated: the
-            // descriptors are then uniform and stay in uniform registers.
-            constexpr uint32_t idS = idesc_half(128, N, 0, 0), idO = idesc_half(128, N, 1, 1);
+            // Scores are issued two chunks ahead of the values, so that the way from one chunk's
+            // weights over the next scores to their weights, which is several waits long, is gone
+            // over once for three chunks.
+            constexpr uint32_t idS = idesc_half(128, N, 0, 0), idO = idesc_half(128, N, 0, 1);
             bool ok = warp_wait(&bar.q_full, seg & 1, abort_v);
-            // (the stage is a constant in each copy of these, and so are the descriptors' offsets)
-            auto issue_s = [&](auto stage) {
-                constexpr int st = decltype(stage)::value;
+            auto issue_s = [&](int c) {
+                const int t = done + c, st = t & 1, ss = t % kSoftStages;
+                if (!warp_wait(&bar.k_full[st], (t >> 1) & 1, abort_v)) return false;
                 tc::fence_after_sync();
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)  // 16 channels each
-                        tc::mma_bf16(tmem + st * 64,
-                                     tc::sdesc(sm + S::kK + st * kTile + (k >> 2) * (kTile / 2) + (k & 3) * 32, 16, 1024),
-                                     tc::sdesc(sm + S::kQ + (k >> 2) * (64 * 128) + (k & 3) * 32, 16, 1024), idS, k > 0);
-                    tc::mma_commit(&bar.s_full[st]);
-                    tc::mma_commit(&bar.k_empty[st]);
+                        tc::mma_bf16_ts(tmem + ss * 64, tmem + kK + st * 64 + k * 8,
+                                        tc::sdesc(sm + S::kQ + (k >> 2) * (64 * 128) + (k & 3) * 32, 16, 1024), idS, k > 0);
+                    tc::mma_commit(&bar.s_full[ss]);
                 }
                 __syncwarp();
+                return true;
             };
-            auto issue_o = [&](auto stage, bool more_o, bool last) {
-                constexpr int st = decltype(stage)::value;
+            for (int c = 0; c < min(2, nc) && ok; ++c) ok = issue_s(c);
+            for (int c = 0; c < nc && ok; ++c) {
+                // (into the scores of chunk c - 1, whose weights are there)
+                if (c + 2 < nc && !(ok = issue_s(c + 2))) break;
+                const int t = done + c, st = t & 1, ss = t % kSoftStages;
+                if (!(ok = warp_wait(&bar.v_full[st], (t >> 1) & 1, abort_v))) break;
+                if (!(ok = warp_wait(&bar.p_full[ss], (t / kSoftStages) & 1, abort_v))) break;
                 tc::fence_after_sync();
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)  // 16 tokens each
-                        tc::mma_bf16(tmem + kO, tc::sdesc(sm + S::kV + st * kTile + k * 2048, kTile / 2, 1024),
-                                     tc::sdesc(sm + S::kPo + st * S::kP + k * 2048, S::kP, 1024), idO, k > 0 || more_o);
-                    tc::mma_commit(&bar.pv_done);
+                        tc::mma_bf16_ts(tmem + kO, tmem + kV + st * 64 + k * 8,
+                                        tc::sdesc(sm + S::kPo + ss * S::kP + k * 2048, S::kP, 1024), idO, k > 0 || c > 0);
                     tc::mma_commit(&bar.v_empty[st]);
-                    if (last) tc::mma_commit(&bar.o_full);
+                    if (c == nc - 1) tc::mma_commit(&bar.o_full);
                 }
                 __syncwarp();
-            };
-            auto flush_o = [&](int c) {
-                const int t = done + c, st = t & 1;
-                if (!warp_wait(&bar.v_full[st], (t >> 1) & 1, abort_v)) return false;
-                if (!warp_wait(&bar.p_full[st], (t >> 1) & 1, abort_v)) return false;
-                if (st)
-                    issue_o(std::integral_constant<int, 1>{}, c > 0, c == nc - 1);
-                else
-                    issue_o(std::integral_constant<int, 0>{}, c > 0, c == nc - 1);
-                return true;
-            };
-            for (int c = 0; c < nc && ok; ++c) {
-                const int t = done + c, st = t & 1;
-                if (!(ok = warp_wait(&bar.k_full[st], (t >> 1) & 1, abort_v))) break;
-                if (st)
-                    issue_s(std::integral_constant<int, 1>{});
-                else
-                    issue_s(std::integral_constant<int, 0>{});
-                if (c > 0) ok = flush_o(c - 1);
             }
-            if (ok) flush_o(nc - 1);
-            __syncwarp();
         } else if (warp >= S::kWiden) {
             // -------------------------------------------------- widening
-            // Four warps have the keys and four the values, two groups each, so that neither waits
-            // for the other's stage.
-            const int wj = (warp - S::kWiden) & 3;
+            // Four warps have the keys and four the values, each the quarter of the lanes of tensor
+            // memory that it can reach.
+            const int quarter = warp & 3;
             const bool keys = warp - S::kWiden < 4;
-            // keys: lane (tt, q) has channels 32 q to 32 q + 31 of token tt, then of tt + 8; lanes with
-            // q >= 2 take their words in the order 2, 3, 0, 1
-            const int tt = lane >> 2, q = lane & 3, swap = q & 2;
-            // values: lane bits 0, 1, 3: channel block gb; bit 2: the low bit of t; bit 4: c; pass: the rest
-            // of the token 8 a + 2 t + c; odd t take their words in the order 1, 0
-            const int gb = (lane & 3) | (lane >> 1 & 4), t0 = lane >> 2 & 1, cc = lane >> 4;
-            // (Both ways a load meets every bank once and eight lanes store to eight bank groups.)
+            const uint32_t lanes = tmem + ((uint32_t)quarter << 21);
+            // keys: the lane's token, its four 16-byte words read in an order that meets every bank once
+            const int kt = lane & 15, rot = (lane >> 1) & 3;
+            // values: lane (g, t) as in cache_attn.cu; of each 16 channels the warp has bytes 2 quarter and the next
+            const int g = lane >> 2, t4 = lane & 3;
             for (int c = 0; c < nc; ++c) {
-                const int t = done + c, st = t & 1;
-                if (!warp_wait(&bar.raw_full[st], (t >> 1) & 1, abort_v)) break;
-                const uint8_t* raw = smp + S::kRawO + st * kRaw + 2 * wj * L::kBytes;
-                const int tok0 = (s.c0 + c) * kChunk + 32 * wj;
+                const int t = done + c, st = t & 1, rs = t % kRawStages;
+                if (!warp_wait(&bar.raw_full[rs], (t / kRawStages) & 1, abort_v)) break;
+                const uint8_t* raw = smp + S::kRawO + rs * kRaw;
                 if (keys) {
-                    uint4 kw[4];
-                    uint32_t ks[4];
+                    const uint8_t* gr = raw + (2 * quarter + (lane >> 4)) * L::kBytes;
+                    uint4 v[4], w[4];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const uint8_t* g = raw + (x >> 1) * L::kBytes;
-                        kw[x] = *reinterpret_cast<const uint4*>(g + (8 * (x & 1) + tt) * L::kRow + q * 16);
-                        ks[x] = *reinterpret_cast<const uint16_t*>(g + L::kKs + tt * 16 + q * 4 + (x & 1) * 2);
-                    }
+                    for (int i = 0; i < 4; ++i) v[i] = reinterpret_cast<const uint4*>(gr + kt * L::kRow)[(i + rot) & 3];
+                    const uint4 sw = *reinterpret_cast<const uint4*>(gr + L::kKs + (kt & 7) * 16);
                     __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&bar.raw_empty[st]);
-                    if (!warp_wait(&bar.k_empty[st], ((t >> 1) & 1) ^ 1, abort_v)) break;
+                    if (lane == 0) tc::mbar_arrive(&bar.raw_empty[rs]);
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const uint32_t w[4] = {swap ? kw[x].z : kw[x].x, swap ? kw[x].w : kw[x].y,
-                                               swap ? kw[x].x : kw[x].z, swap ? kw[x].y : kw[x].w};
-                        const uint32_t s2 = e4m3x2_to_half2(ks[x]);
-                        const uint32_t sc[2] = {__byte_perm(s2, s2, swap ? 0x3232 : 0x1010),
-                                                __byte_perm(s2, s2, swap ? 0x1010 : 0x3232)};
-                        const int row = 32 * wj + 8 * x + tt;
+                    for (int i = 0; i < 4; ++i) w[i] = rot & 1 ? v[(i + 3) & 3] : v[i];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t r[4];
-                            e2m1x8_to_half2(w[i], r);
-                            st_shared16(sm + S::kK + st * kTile + tc::sw_off(row, q * 4 + (i ^ swap), 128),
-                                        hmul2(r[0], sc[i >> 1]), hmul2(r[1], sc[i >> 1]), hmul2(r[2], sc[i >> 1]),
-                                        hmul2(r[3], sc[i >> 1]));
+                    for (int i = 0; i < 4; ++i) v[i] = rot & 2 ? w[(i + 2) & 3] : w[i];
+                    // the products that read this stage: scores of chunk t - 2
+                    const int ts = t - 2;
+                    if (ts >= 0 && !warp_wait(&bar.s_full[ts % kSoftStages], (ts / kSoftStages) & 1, abort_v)) break;
+                    tc::fence_after_sync();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {  // 32 channels, 16 columns
+                        const uint32_t s8 = i == 0 ? sw.x : i == 1 ? sw.y : i == 2 ? sw.z : sw.w;
+                        const uint32_t s2 = e4m3x2_to_half2(kt < 8 ? s8 & 0xffff : s8 >> 16);
+                        const uint32_t cw[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                        uint32_t h[16];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t sc = __byte_perm(s2, s2, j < 2 ? 0x1010 : 0x3232);
+                            e2m1x8_to_half2(cw[j], h + 4 * j);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) h[4 * j + x] = hmul2(h[4 * j + x], sc);
                         }
+                        tmem_st16(lanes + kK + st * 64 + 16 * i, reinterpret_cast<const float*>(h));
                     }
-                    tc::fence_proxy_async();
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&bar.k_full[st]);
                 } else {
-                    uint2 vw[8];
-                    uint32_t vs[8];
+                    const int tok0 = (s.c0 + c) * kChunk;
+                    const bool edge = tok0 + kChunk > low;
+                    if (!warp_wait(&bar.v_empty[st], ((t >> 1) & 1) ^ 1, abort_v)) break;
+                    tc::fence_after_sync();
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        const int tk = t0 + 2 * (x & 1), aa = x >> 1 & 1;
-                        const uint8_t* g = raw + (x >> 2) * L::kBytes;
-                        vw[x] = *reinterpret_cast<const uint2*>(g + L::v_chunk(tk + 4 * (2 * aa + cc), gb));
-                        vs[x] = g[L::kVs + gb * 16 + tk * 4 + 2 * aa + cc];
-                    }
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&bar.raw_empty[st]);
-                    if (tok0 + 32 > low) {
-                        // Nothing of a token that a row does not see may reach it: tokens that no row sees
-                        // are zero; NaN of one that some see is zero here and put into those rows' results.
+                    for (int gi = 0; gi < 8; gi += 2) {
+                        uint32_t h[2][8];  // [lanes 0 .. 15, 16 .. 31]
 #pragma unroll
-                        for (int x = 0; x < 8; ++x) {
-                            const int tok = tok0 + 8 * (x >> 1) + 2 * (t0 + 2 * (x & 1)) + cc;
-                            if (tok >= top) {
-                                vs[x] = 0;
-                            } else if (tok >= low && (vs[x] & 0x7f) == 0x7f) {
-                                vs[x] = 0;
-                                // the byte's other bits belong to other lanes
-                                atomicOr(reinterpret_cast<uint32_t*>(nanv) + ((tok - low) >> 2),
-                                         1u << (((tok - low) & 3) * 8 + gb));
-                                nan_flag = 1;
+                        for (int y = 0; y < 2; ++y) {
+                            const uint8_t* gr = raw + (gi + y) * L::kBytes;
+                            uint32_t sb = *reinterpret_cast<const uint32_t*>(gr + L::kVs + g * 16 + t4 * 4);
+                            uint32_t u[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                u[x] = *reinterpret_cast<const uint16_t*>(gr + L::v_chunk(t4 + 4 * x, g) + 2 * quarter);
+                            if (edge) {
+                                // Nothing of a token that a row does not see may reach it: tokens that no row sees
+                                // are zero; NaN of one that some see is zero here and put into those rows' results.
+                                const int tok = tok0 + 16 * (gi + y) + 2 * t4;
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) {
+                                    const int at = tok + 8 * (x >> 1) + (x & 1);
+                                    if (at >= top) {
+                                        sb &= ~(0xffu << (8 * x));
+                                    } else if (at >= low && (sb >> (8 * x) & 0x7f) == 0x7f) {
+                                        sb &= ~(0xffu << (8 * x));
+                                        // the byte's other bits belong to other lanes
+                                        atomicOr(reinterpret_cast<uint32_t*>(nanv) + ((at - low) >> 2),
+                                                 1u << (((at - low) & 3) * 8 + g));
+                                        nan_flag = 1;
+                                    }
+                                }
+                            }
+                            const uint32_t s0 = e4m3x2_to_half2(sb & 0xffff), s1 = e4m3x2_to_half2(sb >> 16);
+                            // a byte of both tokens of a pair: even channels, then odd ones
+                            constexpr uint32_t lo = 0x0f0f0f0fu;
+                            const uint32_t u0 = __byte_perm(u[0], u[2], 0x5410), u1 = __byte_perm(u[1], u[3], 0x5410);
+                            uint32_t e[4], o[4];
+                            e2m1x8_to_half2((u0 & lo) | ((u1 << 4) & ~lo), e);
+                            e2m1x8_to_half2(((u0 >> 4) & lo) | (u1 & ~lo), o);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                h[i][4 * y] = hmul2(e[i], s0);
+                                h[i][4 * y + 1] = hmul2(o[i], s0);
+                                h[i][4 * y + 2] = hmul2(e[2 + i], s1);
+                                h[i][4 * y + 3] = hmul2(o[2 + i], s1);
                             }
                         }
+                        tmem_st_frag(lanes + kV + st * 64 + 8 * gi, h[0]);
+                        tmem_st_frag(lanes + (16u << 16) + kV + st * 64 + 8 * gi, h[1]);
                     }
-                    if (!warp_wait(&bar.v_empty[st], ((t >> 1) & 1) ^ 1, abort_v)) break;
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        const uint32_t sc = e4m3x2_to_half2(vs[x] | vs[x] << 8);
-                        const int row = 32 * wj + 8 * (x >> 1) + 2 * (t0 + 2 * (x & 1)) + cc;
-                        const uint32_t ws[2] = {t0 ? vw[x].y : vw[x].x, t0 ? vw[x].x : vw[x].y};
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            uint32_t r[4];
-                            e2m1x8_to_half2(ws[i], r);
-                            st_shared16(sm + S::kV + st * kTile + tc::sw_off(row, gb * 2 + (i ^ t0), 128), hmul2(r[0], sc),
-                                        hmul2(r[1], sc), hmul2(r[2], sc), hmul2(r[3], sc));
-                        }
-                    }
-                    tc::fence_proxy_async();
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
                     __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&bar.v_full[st]);
+                    if (lane == 0) {
+                        tc::mbar_arrive(&bar.raw_empty[rs]);
+                        tc::mbar_arrive(&bar.v_full[st]);
+                    }
                 }
             }
         } else {
@@ -450,20 +475,20 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
                     st_shared16(sm + S::kQ + tc::sw_off(r, part * 2 + i, 64), h[0], h[1], h[2], h[3]);
                 }
                 tc::fence_proxy_async();
-                softmax_sync<S::kSoft>();
+                softmax_sync(warp >> 2);
                 if (lane == 0) tc::mbar_arrive(&bar.q_full);
             }
             // thread: token (then channel) tl, rows r0 to r0 + HN - 1
-            const int tl = tid & 127, r0 = (warp >> 2) * HN, quarter = warp & 3;
+            const int tl = tid & 127, wg = warp >> 2, r0 = wg * HN, quarter = warp & 3;
             const uint32_t cols = tmem + ((uint32_t)(tid & 96) << 16) + r0;
             float l[HN];
 #pragma unroll
             for (int r = 0; r < HN; ++r) l[r] = 0.0f;
             bool ok = true;
             for (int c = 0; c < nc; ++c) {
-                const int t = done + c, st = t & 1, tok = (s.c0 + c) * kChunk + tl;
+                const int t = done + c, st = t % kSoftStages, tok = (s.c0 + c) * kChunk + tl;
                 // after a wait that gave up the warp goes on without waiting, for the others' sake
-                ok &= warp_wait(&bar.s_full[st], (t >> 1) & 1, abort_v);
+                ok &= warp_wait(&bar.s_full[st], (t / kSoftStages) & 1, abort_v);
                 tc::fence_after_sync();
                 const bool edge = (s.c0 + c + 1) * kChunk > low;  // some row does not see all of the chunk
                 float y[HN], big = kNoKey;
@@ -485,27 +510,28 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
                     if (again) break;
 #pragma unroll
                     for (int r = 0; r < HN; ++r) big = fmaxf(big, y[r]);
-                    if (!softmax_any<S::kSoft>(big > 15.0f)) break;
+                    if (!softmax_any(wg, big > 15.0f)) break;
                     load_cols(cols + st * 64, y);
 #pragma unroll
-                    for (int r = 0; r < HN; ++r) y[r] = edge && tok >= lim[r0 + r] ? -INFINITY : __fmul_rn(y[r], ref[r0 + r].x);
+                    for (int r = 0; r < HN; ++r)
+                        y[r] = edge && tok >= lim[r0 + r] ? -INFINITY : __fmul_rn(y[r], ref[r0 + r].x);
                     reduce_lanes(y, lane, [](float p, float q) { return fmaxf(p, q); });
                     part4[quarter][r0 + HN * lane / 32] = y[0];
-                    softmax_sync<S::kSoft>();
-                    if (tid < N) {
-                        const float mx = fmaxf(fmaxf(part4[0][tid], part4[1][tid]), fmaxf(part4[2][tid], part4[3][tid]));
+                    softmax_sync(wg);
+                    if (tl < HN) {
+                        const int r = r0 + tl;
+                        const float mx = fmaxf(fmaxf(part4[0][r], part4[1][r]), fmaxf(part4[2][r], part4[3][r]));
                         // (a row's own scores move it, not another's)
-                        const float old = ref[tid].y, mn = mx - old > 15.0f ? mx - 7.0f : old;
-                        fac[tid] = ex2(old - mn);
-                        ref[tid].y = mn;
+                        const float old = ref[r].y, mn = mx - old > 15.0f ? mx - 7.0f : old;
+                        fac[r] = ex2(old - mn);
+                        ref[r].y = mn;
                     }
-                    softmax_sync<S::kSoft>();
+                    softmax_sync(wg);
 #pragma unroll
                     for (int r = 0; r < HN; ++r) l[r] *= fac[r0 + r];
                     if (c > 0) {
-                        // S of this chunk is done, so the products with V up to the one before the last are;
-                        // this wait can only be for the last
-                        ok &= warp_wait(&bar.pv_done, (t - 1) & 1, abort_v);
+                        // the last products with V (those up to chunk c - 3 were issued before S of this one)
+                        ok &= warp_wait(&bar.v_empty[(t - 1) & 1], ((t - 1) >> 1) & 1, abort_v);
                         tc::fence_after_sync();
                         load_cols(cols + kO, y);
 #pragma unroll
@@ -535,19 +561,21 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
             }
             ok &= warp_wait(&bar.o_full, seg & 1, abort_v);
             tc::fence_after_sync();
-            if (!softmax_any<S::kSoft>(!ok)) {
+            if (!softmax_any(wg, !ok)) {
                 reduce_lanes(l, lane, [](float p, float q) { return p + q; });
                 part4[quarter][r0 + HN * lane / 32] = l[0];
-                softmax_sync<S::kSoft>();
-                if (tid < N) {
-                    const float sum = (part4[0][tid] + part4[1][tid]) + (part4[2][tid] + part4[3][tid]);
-                    lsum[tid] = sum;
-                    linv[tid] = sum == 0.0f ? 0.0f : 1.0f / sum;
+                softmax_sync(wg);
+                if (tl < HN) {
+                    const int r = r0 + tl;
+                    const float sum = (part4[0][r] + part4[1][r]) + (part4[2][r] + part4[3][r]);
+                    lsum[r] = sum;
+                    linv[r] = sum == 0.0f ? 0.0f : 1.0f / sum;
                 }
-                softmax_sync<S::kSoft>();
+                softmax_sync(wg);
                 const bool whole = walk.whole(), nans = nan_flag;
                 const long long slot = (long long)walk.slot(piece) * N;
-                // channel tl of the thread's rows, eight at a time (little code: it runs once a segment)
+                // lane tl of the thread's rows, eight at a time (little code: it runs once a segment)
+                const int ch = 16 * (tl & 7) + 4 * (tl >> 5) + ((tl >> 3) & 2) + ((tl >> 3) & 1);
 #pragma unroll 1
                 for (int i0 = 0; i0 < HN && r0 + i0 < s.rows; i0 += 8) {
                     float o[8];
@@ -558,25 +586,21 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
                         const int r = r0 + i0 + i;
                         float v = o[i] * vscale;
                         if (r < s.rows) {
-                            if (nans) v = seen_nan(v, nanv, low, min(top, lim[r]), tl >> 4);
+                            if (nans) v = seen_nan(v, nanv, low, min(top, lim[r]), ch >> 4);
                             if (whole)
-                                reinterpret_cast<__nv_bfloat16*>(out.O)[row_at[r] * kD + tl] = __float2bfloat16_rn(v * linv[r]);
+                                reinterpret_cast<__nv_bfloat16*>(out.O)[row_at[r] * kD + ch] = __float2bfloat16_rn(v * linv[r]);
                             else
-                                out.part[(slot + r) * kD + tl] = v;
+                                out.part[(slot + r) * kD + ch] = v;
                         }
                     }
                 }
-                if (tid < s.rows) {
-                    const float sum = lsum[tid], m = ref[tid].y;
+                if (tl < HN && r0 + tl < s.rows) {
+                    const int r = r0 + tl;
+                    const float sum = lsum[r], m = ref[r].y;
                     if (!whole)
-                        out.ml[slot + tid] = make_float2(m, sum);
+                        out.ml[slot + r] = make_float2(m, sum);
                     else if (out.lse)
-                        out.lse[row_at[tid]] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
-                }
-                if (nans) {
-                    softmax_sync<S::kSoft>();
-                    if (tid < kEdge) nanv[tid] = 0;
-                    if (tid == 0) nan_flag = 0;
+                        out.lse[row_at[r]] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
                 }
             }
             tc::fence_before_sync();
@@ -585,12 +609,15 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
         done += nc;
         // every warp is through the segment, so that all see the same and meet at the same barriers
         stop = __syncthreads_or(abort_flag);
+        if (tid < kEdge) nanv[tid] = 0;
+        if (tid == 0) nan_flag = 0;
         more = walk.next(a);
         tc::fence_after_sync();
     }
     // what is in flight lands before the block frees its tensor memory and ends
     if (warp == S::kCopy && lane == 0)
-        for (int t = max(0, issued - 2); t < issued; ++t) drain(&bar.raw_full[t & 1], (t >> 1) & 1, a.status);
+        for (int t = max(0, issued - kRawStages); t < issued; ++t)
+            drain(&bar.raw_full[t % kRawStages], (t / kRawStages) & 1, a.status);
     if (warp == S::kIssue && lane == 0) {
         tc::mma_commit(&bar.drain);
         drain(&bar.drain, 0, a.status);
@@ -599,7 +626,7 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
     if (abort_flag) found |= kFoundTimeout;
     end_piece(a, out, piece, found);
     tc::fence_after_sync();
-    if (warp == S::kIssue) tc::tmem_dealloc(tmem, 256);
+    if (warp == S::kIssue) tc::tmem_dealloc(tmem, 512);
 }
 
 cudaError_t launch_cache_tile(const CacheArgs& a, const void* Q, const uint8_t* cache, const AttnOut& o, cudaStream_t st) {

@@ -56,8 +56,8 @@ __device__ __forceinline__ SeqWork seq_work(const CacheArgs& a, int b, int rtile
 // side by side then, and what counts is that no block has one more of them.
 // Measured with 64 sequences of 33 to 8191 tokens (16,400 chunks, 512 items): the
 // slowest block ended at 69 us without `extra` and at 56 with it, the median at 49.
-// cache_tile.cu's items cost more to start and end (kTileExtra 2, 4, 6, 9: 45.2,
-// 43.2, 45.3, 45.3 us for 32 items of 64 rows over 9000 to 16384 tokens).
+// cache_tile.cu's items cost more to start and end (kTileExtra 2, 4, 6, 9, 14:
+// 47.3, 45.2, 45.2, 45.3, 46.2 us for 32 items of 64 rows over 9000 to 16384 tokens).
 constexpr int kExtra = 2, kTileExtra = 4, kFew = 8;
 
 // The line of units, cut into `pieces` pieces that differ by one unit at most.
