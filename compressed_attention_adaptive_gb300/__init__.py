@@ -105,6 +105,9 @@ class CacheParams:
     def c(self):
         return self._c
 
+    def __reduce__(self):  # copies and pickles hold the fields, not the C form
+        return CacheParams, dataclasses.astuple(self)
+
 
 def lib():
     """The loaded libmita.so; raises if it has not been built."""

@@ -1,5 +1,7 @@
 """The cache calls' argument checks (no GPU: nothing here launches)."""
+import copy
 import ctypes
+import pickle
 
 import pytest
 import torch
@@ -111,3 +113,11 @@ def test_overlapping_rows_are_refused(lib):
     for off in (0, k_bytes - 16, 16 - k_bytes):
         assert lib.mita_cache_read(c, f, f, f, None, None, f, ctypes.c_void_p(at + off), f, need, None) == 1
         assert b"overlap" in lib.mita_last_error()
+
+
+def test_params_copy_and_pickle_after_use(lib):
+    p = _p(scale=0.25)
+    mita.mita_cache_size(p)
+    p.ref, p.pool_bytes
+    for q in (copy.deepcopy(p), copy.copy(p), pickle.loads(pickle.dumps(p))):
+        assert q == p and mita.mita_cache_size(q) == mita.mita_cache_size(p) == q.pool_bytes
