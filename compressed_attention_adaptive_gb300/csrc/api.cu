@@ -338,7 +338,6 @@ static CacheWork carve_cache(const mita_cache_params* p, const CachePlan& plan, 
     w.status = c.take<int>(64);
     w.parts.part = c.take<float>(plan.parts * p->d);
     w.parts.ml = c.take<float2>(plan.parts);
-    w.parts.cut = c.take<char>((size_t)plan.pieces * kCutBytes);
     w.parts.found = c.take<int>(plan.pieces);
     *bytes = align_up(c.off, 1024);
     return w;

@@ -78,11 +78,9 @@ struct CachePlan {
 };
 
 // Partial results of the attention, in the workspace.
-constexpr int kCutBytes = 24;  // one CutItem (cache_walk.cuh)
 struct CacheParts {
     float* part;  // [parts][d]
     float2* ml;   // [parts]
-    void* cut;    // [pieces] of kCutBytes (as many cut items there can be)
     int* found;   // [pieces]
 };
 

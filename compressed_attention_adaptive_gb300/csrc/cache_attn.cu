@@ -118,7 +118,6 @@ k_cache_attn_simt(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restric
     const int piece = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sub = lane >> 3, ch = lane & 7;  // token of four, chunk
     __shared__ Walk<R> walk;
-    if (!out.items && threadIdx.x == 0) out.cut[piece] = CutItem{};
     if (!walk.begin(a, piece, out.pieces)) {
         end_piece(a, out, piece, 0);
         return;
@@ -271,7 +270,6 @@ k_cache_attn_simt(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restric
         __syncthreads();
         const bool whole = walk.whole();
         const int slot = walk.slot(piece);
-        walk.note(a, out, piece);
         for (int x = threadIdx.x; x < s.rows * D; x += kThreads) {
             const int r = x / D, c = x - r * D;
             float mx = -INFINITY;
@@ -410,7 +408,6 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
         for (int i = 0; i < ST; ++i) tc::mbar_init(&bars[warp][i], 2);
         tc::fence_mbar_init();
     }
-    if (!out.items && threadIdx.x == 0) out.cut[piece] = CutItem{};
     if (!walk.begin(a, piece, out.pieces)) {
         end_piece(a, out, piece, 0);
         return;
@@ -792,7 +789,6 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
         __syncthreads();
         const bool whole = walk.whole();
         const int slot = walk.slot(piece);
-        walk.note(a, out, piece);
         for (int x = threadIdx.x; x < s.rows * C4; x += kThreads) {
             const int r = x / C4, c = x - r * C4;
             float2 v[4];
@@ -831,58 +827,95 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
 
 // ------------------------------------------------------------------ join
 
-constexpr int kJoinRows = 2, kJoinWarps = 4;  // rows of a block, warps of a row
+// Rows of a block that has W warps for each row.
+constexpr int join_rows(int W) { return W >= 8 ? 1 : 8 / W; }
+constexpr int kJoinAhead = 4;
 
-// Block (x, y) joins the parts of cut item x, rows 2 y and 2 y + 1: each of a row's
-// four warps adds every fourth part, a lane d/32 channels of it, several parts'
-// loads in flight. (It is a chain of loads, the item, then maxima and sums, then the
-// other warps' results, and takes 2 to 4 us.)
-template <typename T, int D>
-__global__ void __launch_bounds__(32 * kJoinRows * kJoinWarps) k_cache_join(CacheArgs a, AttnOut out) {
-    constexpr int E = D / 32;
-    __shared__ float acc8[kJoinRows][kJoinWarps][D];
-    __shared__ float2 ml8[kJoinRows][kJoinWarps];
-    wait_previous();
+// Block (x, y) joins the parts of one cut item, the y-th join_rows(W) rows: item x of
+// the call when there are no more items than pieces, else the one that begins in piece x
+// and goes on behind it. It finds that from the lengths while the attention runs (loading
+// a description of it that the attention left made a call 1.5 us longer). Each of a row's
+// W warps adds every W-th part, a lane d/32 channels of it; the first kJoinAhead are
+// loaded together with the maxima and sums.
+template <typename T, int D, int W>
+__global__ void __launch_bounds__(32 * W * join_rows(W)) k_cache_join(CacheArgs a, AttnOut out, bool by_item) {
+    constexpr int E = D / 32, R = join_rows(W);
+    __shared__ float acc8[R][W][D];
+    __shared__ float2 ml8[R][W];
+    __shared__ CutItem cut;
+    const int lane = threadIdx.x & 31, sub = threadIdx.x >> 5, mine = sub / W, warp = sub % W;
     if (blockIdx.x == gridDim.x - 1) {
         if (blockIdx.y) return;
+        wait_previous();
         int found = 0;
         for (int i = threadIdx.x; i < out.pieces; i += blockDim.x) found |= out.found[i];
         const int bounds = __syncthreads_or(found & kFoundBounds), timeout = __syncthreads_or(found & kFoundTimeout);
         if (threadIdx.x == 0) *a.status = timeout ? kStTimeout : bounds ? kStBounds : kStOk;
         return;
     }
-    const CutItem c = out.cut[blockIdx.x];
-    if ((int)blockIdx.y * kJoinRows >= c.rows) return;
-    const int lane = threadIdx.x & 31, sub = threadIdx.x >> 5, mine = sub / kJoinWarps, warp = sub % kJoinWarps;
-    const int r = blockIdx.y * kJoinRows + mine;
+    if (sub == 0) {
+        CutItem x{};
+        if (by_item) {
+            x = cut_item(a, out, blockIdx.x, lane);
+            if (lane == 0) cut = x;
+        } else {
+            if (lane == 0) cut.rows = 0;
+            __syncwarp();
+            if (cut_item_of_piece(a, out, blockIdx.x, lane, &x)) cut = x;
+        }
+    }
+    __syncthreads();
+    const CutItem c = cut;
+    if ((int)blockIdx.y * R >= c.rows) return;
+    wait_previous();
+    const int r = blockIdx.y * R + mine;
     if (r < c.rows) {
         // part p > 0 begins its piece
         auto slot = [&](int p) { return (long long)(2 * (c.piece + p) + (p == 0)) * out.rows + r; };
-        float mx = kNoKey, sum = 0.0f, acc[E];
+        auto load = [&](int p, float* v) {
+            const float* part = out.part + slot(p) * D;
+            if (E == 4) {
+                const float4 u = reinterpret_cast<const float4*>(part)[lane];
+                v[0] = u.x; v[1] = u.y; v[E - 2] = u.z; v[E - 1] = u.w;
+            } else {
+                const float2 u = reinterpret_cast<const float2*>(part)[lane];
+                v[0] = u.x; v[1] = u.y;
+            }
+        };
+        float mx = kNoKey, sum = 0.0f, acc[E], ahead[kJoinAhead][E];
+#pragma unroll
+        for (int j = 0; j < kJoinAhead; ++j) {
+#pragma unroll
+            for (int i = 0; i < E; ++i) ahead[j][i] = 0.0f;
+            if (warp + j * W < c.parts) load(warp + j * W, ahead[j]);
+        }
 #pragma unroll
         for (int i = 0; i < E; ++i) acc[i] = 0.0f;
         // lane l has the maximum and sum of the l-th of 32 of the warp's parts
-        for (int p0 = warp; p0 < c.parts; p0 += 32 * kJoinWarps) {
-            const int pl = p0 + lane * kJoinWarps;
+        for (int p0 = warp; p0 < c.parts; p0 += 32 * W) {
+            const int pl = p0 + lane * W;
             const float2 ml = pl < c.parts ? out.ml[slot(pl)] : make_float2(kNoKey, 0.0f);
             const float m = fmaxf(ml.x, kNoKey), mn = fmaxf(mx, warp_max(m)), old = exp2f(mx - mn), f = exp2f(m - mn);
             sum = sum * old + warp_sum(f * ml.y);
             mx = mn;
 #pragma unroll
             for (int i = 0; i < E; ++i) acc[i] *= old;
-            const int n = min(32, (c.parts - p0 + kJoinWarps - 1) / kJoinWarps);
-#pragma unroll 8
-            for (int j = 0; j < n; ++j) {
-                const float fj = __shfl_sync(0xffffffffu, f, j);
-                const float* part = out.part + slot(p0 + j * kJoinWarps) * D;
-                float v[E];
-                if (E == 4) {
-                    const float4 u = reinterpret_cast<const float4*>(part)[lane];
-                    v[0] = u.x; v[1] = u.y; v[E - 2] = u.z; v[E - 1] = u.w;
-                } else {
-                    const float2 u = reinterpret_cast<const float2*>(part)[lane];
-                    v[0] = u.x; v[1] = u.y;
+            const int n = min(32, (c.parts - p0 + W - 1) / W);
+            int j = 0;
+            if (p0 == warp) {
+#pragma unroll
+                for (; j < kJoinAhead; ++j) {
+                    const float fj = __shfl_sync(0xffffffffu, f, j);
+#pragma unroll
+                    for (int i = 0; i < E; ++i)
+                        if (j < n) acc[i] = fmaf(fj, ahead[j][i], acc[i]);
                 }
+            }
+#pragma unroll 8
+            for (; j < n; ++j) {
+                const float fj = __shfl_sync(0xffffffffu, f, j);
+                float v[E];
+                load(p0 + j * W, v);
 #pragma unroll
                 for (int i = 0; i < E; ++i) acc[i] = fmaf(fj, v[i], acc[i]);
             }
@@ -893,22 +926,22 @@ __global__ void __launch_bounds__(32 * kJoinRows * kJoinWarps) k_cache_join(Cach
     }
     __syncthreads();
     if (r >= c.rows) return;
-    float top = kNoKey, s = 0.0f, f[kJoinWarps];
+    float top = kNoKey, s = 0.0f, f[W];
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, ml8[mine][w].x);
+    for (int w = 0; w < W; ++w) top = fmaxf(top, ml8[mine][w].x);
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
+    for (int w = 0; w < W; ++w) {
         f[w] = exp2f(ml8[mine][w].x - top);
         s = fmaf(f[w], ml8[mine][w].y, s);
     }
     int t;
     const long long at = row_offset(a, c.b, c.h, c.row0 + r, &t);
     const int i0 = warp * 32 + lane;
-    if (i0 < D) {
+    for (int i = i0; i < D; i += 32 * W) {
         float v = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) v = fmaf(f[w], acc8[mine][w][i0], v);
-        reinterpret_cast<T*>(out.O)[at * D + i0] = from_f<T>(s == 0.0f ? 0.0f : v / s);
+        for (int w = 0; w < W; ++w) v = fmaf(f[w], acc8[mine][w][i], v);
+        reinterpret_cast<T*>(out.O)[at * D + i] = from_f<T>(s == 0.0f ? 0.0f : v / s);
     }
     if (out.lse && i0 == 0) out.lse[at] = s == 0.0f ? -INFINITY : (top + log2f(s)) * kLn2;
 }
@@ -945,23 +978,36 @@ CachePlan cache_attn_plan(const CacheArgs& a, int d, int dtype, unsigned flags) 
     return p;
 }
 
-template <typename T, int D>
-static cudaError_t join_t(const CacheArgs& a, const AttnOut& o, cudaStream_t st) {
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    prof_mark(st, "cache_join");
+template <typename T, int D, int W>
+static cudaError_t join_w(const CacheArgs& a, const AttnOut& o, long long items, cudaStream_t st) {
+    const bool by_item = items <= o.pieces;
+    const int rows = (int)std::min<long long>(o.rows, (long long)a.G * a.T);
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t c{};
-    c.gridDim = dim3(o.cuts + 1, (o.rows + kJoinRows - 1) / kJoinRows);
-    c.blockDim = dim3(32 * kJoinRows * kJoinWarps);
+    c.gridDim = dim3((by_item ? (int)items : o.pieces) + 1, (rows + join_rows(W) - 1) / join_rows(W));
+    c.blockDim = dim3(32 * W * join_rows(W));
     c.stream = st;
     c.attrs = &at;
     c.numAttrs = 1;
-    e = cudaLaunchKernelEx(&c, k_cache_join<T, D>, a, o);
+    const cudaError_t e = cudaLaunchKernelEx(&c, k_cache_join<T, D, W>, a, o, by_item);
     if (e == cudaSuccess) count_launch();
     return e;
+}
+
+template <typename T, int D>
+static cudaError_t join_t(const CacheArgs& a, const AttnOut& o, cudaStream_t st) {
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    prof_mark(st, "cache_join");
+    // Warps of a row by the pieces that there are for an item: with 76 of them (8 items) 4, 8
+    // and 16 warps 39.1, 37.1 and 35.8 us; with 9.5 (64 items) 2, 4 and 8 warps 37.1, 35.0
+    // and 35.0; with 5 (32 items of 64 rows) 41.6, 44.0 and 49.4; with 1.2 (512 items) 63.9,
+    // 66.3 and 70.6; with 38 (16 items) 4 and 16 warps 33.6 and 32.3, with 19 both 32.3.
+    const long long items = (long long)a.B * o.tiles * a.Hkv;
+    if (o.pieces >= 24 * items) return join_w<T, D, 16>(a, o, items, st);
+    return o.pieces >= 6 * items ? join_w<T, D, 4>(a, o, items, st) : join_w<T, D, 2>(a, o, items, st);
 }
 
 // Sets a kernel's shared memory limit, once per device (`done`: a bit for each of
@@ -1022,10 +1068,7 @@ static cudaError_t attn_t(const CacheArgs& a, const CachePlan& p, int dtype, con
 cudaError_t launch_cache_attn(const CacheArgs& a, const CachePlan& p, int d, int dtype, const void* Q,
                               const void* cache, void* O, float* lse, const CacheParts& parts, cudaStream_t st) {
     const int tiles = (int)(((long long)a.G * a.T + p.rows - 1) / p.rows);
-    const long long items = (long long)a.B * tiles * a.Hkv;
-    const bool by_item = items <= p.pieces;
-    const AttnOut o{O, lse, parts.part, parts.ml, (CutItem*)parts.cut, parts.found, p.pieces, p.rows,
-                    by_item ? (int)items : p.pieces, by_item ? (int)items : 0, tiles};
+    const AttnOut o{O, lse, parts.part, parts.ml, parts.found, p.pieces, p.rows, p.tile ? kTileExtra : kExtra, tiles};
     const uint8_t* c = (const uint8_t*)cache;
     prof_mark(st, "cache_attention");
     return d == 64 ? attn_t<64>(a, p, dtype, Q, c, o, st) : attn_t<128>(a, p, dtype, Q, c, o, st);

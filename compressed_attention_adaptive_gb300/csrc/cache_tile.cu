@@ -211,7 +211,6 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
     allow_next();
     const int piece = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int found = 0;
-    if (!out.items && tid == 0) out.cut[piece] = CutItem{};
     if (warp == S::kIssue) tc::tmem_alloc(&tmem_slot, 512);
     if (tid == 0) {
         for (int i = 0; i < kRawStages; ++i) {
@@ -250,7 +249,7 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
         // chunks that some row of the tile sees, at least one
         const int nc = max(1, min(s.c1, (top + kChunk - 1) / kChunk) - s.c0);
         if (stop) {
-            // only the items' ends are still noted
+            // what is left of the piece is not computed, and the status word says so
         } else if (warp == S::kCopy) {
             // ---------------------------------------------------- copies
             // Lane l looks after group l % 8 of chunk l / 8 in the current run of four chunks; the next
@@ -605,7 +604,6 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
             }
             tc::fence_before_sync();
         }
-        walk.note(a, out, piece);
         done += nc;
         // every warp is through the segment, so that all see the same and meet at the same barriers
         stop = __syncthreads_or(abort_flag);

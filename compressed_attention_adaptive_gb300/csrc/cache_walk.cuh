@@ -14,25 +14,14 @@ constexpr int kChunk = 128;  // tokens of a block's step
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// An item that is cut: the join's work. rows = 0: nothing to join here.
-struct CutItem {
-    int b, h, row0, rows;
-    int piece, parts;  // the first part's piece, and the pieces it goes over
-};
-
-static_assert(sizeof(CutItem) == kCutBytes, "the workspace holds CutItems");
-
 struct AttnOut {
     void* O;
     float* lse;    // or null
     float* part;   // [2 * pieces][rows][d]
     float2* ml;    // [2 * pieces][rows] (maximum in log2 units, sum)
-    CutItem* cut;      // [cuts]
     int* found;        // [pieces]: what a piece found wrong, for the call's status word
     int pieces, rows;  // pieces of the line, rows of a tile
-    // The cut items, by their number (sequence, tile, head) when there are no more items
-    // than pieces, else by the piece that they start in.
-    int cuts, items, tiles;  // items: 0 in the second case; tiles of a sequence with T rows
+    int extra, tiles;  // Walk's EXTRA; tiles of a sequence with T rows
 };
 
 // One sequence's share of the line. Its items are cut into chunks, and each item
@@ -62,7 +51,7 @@ constexpr int kExtra = 2, kTileExtra = 4, kFew = 8;
 
 // The line of units, cut into `pieces` pieces that differ by one unit at most.
 struct Line {
-    int pieces, q, r, extra;
+    int pieces, q, r, extra, total;
     __device__ __forceinline__ int at(int c) const { return c * q + min(c, r); }
     __device__ __forceinline__ int piece_of(int x) const {
         const int head = r * (q + 1);
@@ -77,6 +66,48 @@ __device__ __forceinline__ int warp_scan(int x, int lane) {
         if (lane >= o) x += y;
     }
     return x;
+}
+
+// The line of a call, by a whole warp. `mine` is left with the lane's sequence of the last 32.
+__device__ __forceinline__ Line call_line(const CacheArgs& a, int rtile, int extra, int max_pieces, int lane, SeqWork* mine) {
+    unsigned items = 0, chunks = 0;
+#pragma unroll 8
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+        mine->items = 0;
+        if (b0 + lane < a.B) *mine = seq_work(a, b0 + lane, rtile);
+        items += mine->items;
+        chunks += mine->items * mine->chunks;
+    }
+    items = __reduce_add_sync(0xffffffffu, items);
+    chunks = __reduce_add_sync(0xffffffffu, chunks);
+    Line l;
+    l.extra = chunks >= (unsigned)max_pieces * kFew ? extra : 0;
+    l.total = (int)(chunks + items * l.extra);
+    l.pieces = min(max_pieces, l.total);
+    l.q = l.pieces ? l.total / l.pieces : 0;
+    l.r = l.total - l.q * l.pieces;
+    return l;
+}
+// The sequence whose share holds unit w, by the same warp after call_line(): one lane
+// returns true, with the sequence, its work and the units before it.
+__device__ __forceinline__ bool find_unit(const CacheArgs& a, const Line& l, int rtile, int w, int lane, SeqWork* mine,
+                                          int* b, int* before) {
+    int base = 0, x = 0, share = 0;
+    unsigned hit = 0;
+    int b0 = 0;
+    for (; b0 < a.B && !hit; b0 += 32) {
+        if (a.B > 32) {
+            mine->items = 0;
+            if (b0 + lane < a.B) *mine = seq_work(a, b0 + lane, rtile);
+        }
+        share = mine->items * (mine->chunks + l.extra);
+        x = base + warp_scan(share, lane);
+        hit = __ballot_sync(0xffffffffu, w < x);  // the first whose share ends behind w
+        base = __shfl_sync(0xffffffffu, x, 31);
+    }
+    *before = x - share;
+    *b = b0 - 32 + lane;
+    return hit && lane == __ffs(hit) - 1;
 }
 
 // One block's part of an item.
@@ -130,47 +161,18 @@ template <int RT, int EXTRA = kExtra> struct Walk {
         if (threadIdx.x < 32) {
             const int lane = threadIdx.x;
             SeqWork mine{};
-            unsigned items = 0, chunks = 0;
-#pragma unroll 8
-            for (int b0 = 0; b0 < a.B; b0 += 32) {
-                mine.items = 0;
-                if (b0 + lane < a.B) mine = seq_work(a, b0 + lane, RT);
-                items += mine.items;
-                chunks += mine.items * mine.chunks;
-            }
-            items = __reduce_add_sync(0xffffffffu, items);
-            chunks = __reduce_add_sync(0xffffffffu, chunks);
-            Line l;
-            l.extra = chunks >= (unsigned)max_pieces * kFew ? EXTRA : 0;
-            const int total = (int)(chunks + items * l.extra);
-            l.pieces = min(max_pieces, total);
-            l.q = l.pieces ? total / l.pieces : 0;
-            l.r = total - l.q * l.pieces;
+            const Line l = call_line(a, RT, EXTRA, max_pieces, lane, &mine);
             if (lane == 0) more = false;
             __syncwarp();
-            if (piece < l.pieces) {
-                const int w0 = l.at(piece);
-                int base = 0, x = 0, share = 0;
-                unsigned hit = 0;
-                for (int b0 = 0; b0 < a.B && !hit; b0 += 32) {
-                    if (a.B > 32) {
-                        mine.items = 0;
-                        if (b0 + lane < a.B) mine = seq_work(a, b0 + lane, RT);
-                    }
-                    share = mine.items * (mine.chunks + l.extra);
-                    x = base + warp_scan(share, lane);
-                    hit = __ballot_sync(0xffffffffu, w0 < x);
-                    base = __shfl_sync(0xffffffffu, x, 31);
-                    if (hit && lane == __ffs(hit) - 1) {  // the first sequence whose share ends behind w0
-                        line = l;
-                        w = w0;
-                        w_end = l.at(piece + 1);
-                        before = x - share;
-                        b = b0 + lane;
-                        sw = mine;
-                        segment(a);
-                    }
-                }
+            int b1, before1;
+            if (piece < l.pieces && find_unit(a, l, RT, l.at(piece), lane, &mine, &b1, &before1)) {
+                line = l;
+                w = l.at(piece);
+                w_end = l.at(piece + 1);
+                before = before1;
+                b = b1;
+                sw = mine;
+                segment(a);
             }
         }
         __syncthreads();
@@ -185,41 +187,71 @@ template <int RT, int EXTRA = kExtra> struct Walk {
     __device__ __forceinline__ bool whole() const { return s.c0 == 0 && s.c1 == s.chunks; }
     // Where the sums of a part of an item go: the part that starts the item, or another.
     __device__ __forceinline__ int slot(int piece) const { return 2 * piece + (s.c0 == 0); }
-    // Notes for the join whether the item that starts here goes on behind the piece.
-    __device__ __forceinline__ void note(const CacheArgs& a, const AttnOut& out, int piece) const {
-        if (threadIdx.x != 0 || s.c0 != 0) return;
-        CutItem c{};
-        if (s.c1 < s.chunks) {
-            c.b = s.b; c.h = s.h; c.row0 = s.row0; c.rows = s.rows;
-            c.piece = piece;
-            c.parts = line.piece_of(s.first + s.chunks - 1) - piece + 1;
-        }
-        if (out.items)
-            out.cut[(s.b * out.tiles + s.row0 / RT) * a.Hkv + s.h] = c;
-        else if (c.rows)
-            out.cut[piece] = c;
-    }
 };
 
 // What a piece finds wrong; the join makes the call's status word of it. Between
 // them the pieces read every table entry that the call uses; the first also
-// checks the lengths, counts and exponents, and notes the items that there are
-// not (tiles of sequences with fewer rows) as not cut.
+// checks the lengths, counts and exponents.
 enum : int { kFoundBounds = 1, kFoundTimeout = 2 };
-__device__ __forceinline__ int first_piece(const CacheArgs& a, const AttnOut& out) {
+__device__ __forceinline__ int first_piece(const CacheArgs& a) {
     bool bad = bad_exps(a);
     for (int b = threadIdx.x; b < a.B; b += blockDim.x) bad |= bad_len(a, b);
-    for (int i = threadIdx.x; i < out.items; i += blockDim.x) {
-        const int bt = i / a.Hkv, b = bt / out.tiles;
-        if ((bt - b * out.tiles) * out.rows >= cache_count(a, b) * a.G) out.cut[i] = CutItem{};
-    }
     return bad ? kFoundBounds : 0;
 }
 // The end of a piece, by the whole block.
 __device__ __forceinline__ void end_piece(const CacheArgs& a, const AttnOut& out, int piece, int found) {
-    if (piece == 0) found |= first_piece(a, out);
+    if (piece == 0) found |= first_piece(a);
     const int bounds = __syncthreads_or(found & kFoundBounds), timeout = __syncthreads_or(found & kFoundTimeout);
     if (threadIdx.x == 0) out.found[piece] = (bounds ? kFoundBounds : 0) | (timeout ? kFoundTimeout : 0);
+}
+
+// An item that is cut, for the join.
+struct CutItem {
+    int b, h, row0, rows;  // rows = 0: not cut
+    int piece, parts;      // the first part's piece, and the pieces it goes over
+};
+// Item i of the call (of all tiles of T rows), by a whole warp.
+__device__ __forceinline__ CutItem cut_item(const CacheArgs& a, const AttnOut& out, int i, int lane) {
+    SeqWork sw{};
+    const Line l = call_line(a, out.rows, out.extra, out.pieces, lane, &sw);
+    CutItem c{};
+    c.b = i / (out.tiles * a.Hkv);
+    const int j = i - c.b * (out.tiles * a.Hkv), tile = j / a.Hkv;
+    int before = 0;  // units before the sequence
+    for (int b0 = 0; b0 < c.b; b0 += 32)
+        if (b0 + lane < c.b) {
+            const SeqWork x = seq_work(a, b0 + lane, out.rows);
+            before += x.items * (x.chunks + l.extra);
+        }
+    before = __reduce_add_sync(0xffffffffu, before);
+    sw = seq_work(a, c.b, out.rows);
+    if (j >= sw.items) return c;
+    const int first = before + j * (sw.chunks + l.extra) + l.extra;
+    c.piece = l.piece_of(first);
+    c.parts = l.piece_of(first + sw.chunks - 1) - c.piece + 1;
+    c.h = j - tile * a.Hkv;
+    c.row0 = tile * out.rows;
+    if (c.parts > 1) c.rows = min(out.rows, sw.rows - c.row0);
+    return c;
+}
+// The item that begins in piece p and goes on behind it (there is at most one), by a
+// whole warp; the lane that returns true has it.
+__device__ __forceinline__ bool cut_item_of_piece(const CacheArgs& a, const AttnOut& out, int p, int lane, CutItem* c) {
+    SeqWork sw{};
+    const Line l = call_line(a, out.rows, out.extra, out.pieces, lane, &sw);
+    if (p + 1 >= l.pieces) return false;
+    const int w = l.at(p + 1);  // the first unit behind the piece
+    int before;
+    if (!find_unit(a, l, out.rows, w, lane, &sw, &c->b, &before)) return false;
+    const int len = sw.chunks + l.extra, j = (w - before) / len, first = before + j * len + l.extra;
+    if (first >= w || first < l.at(p)) return false;
+    const int tile = j / a.Hkv;
+    c->h = j - tile * a.Hkv;
+    c->row0 = tile * out.rows;
+    c->rows = min(out.rows, sw.rows - c->row0);
+    c->piece = p;
+    c->parts = l.piece_of(first + sw.chunks - 1) - p + 1;
+    return true;
 }
 
 // A kernel that this one's launch may be followed by can be set up meanwhile;

@@ -191,6 +191,16 @@ def test_attention_matches_oracle(case, simt):
     _check(pool, H, T, causal, Q, O, L, counts, simt, label="%s d%d H%d/%d T%d %s" % (dtype, d, H, Hkv, T, "simt" * simt))
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("f32", 128), ("f32", 64)])
+@pytest.mark.parametrize("lens,Hkv", [([380, 380], 3), ([1275], 1), ([1275, 500, 3], 2), ([5115], 1), ([5115, 0], 2),
+                                      ([9000] * 2, 2)])
+def test_few_and_many_parts(dtype, d, lens, Hkv):
+    """Items that are cut into few parts, some and many: the join has a form for each."""
+    pool = Pool(lens, Hkv, d, 48, dtype, seed=41)
+    Q, O, L = _attend(pool, 3 * Hkv, 2, True)
+    _check(pool, 3 * Hkv, 2, True, Q, O, L, label="parts %s d%d %s" % (dtype, d, lens))
+
+
 @pytest.mark.parametrize("dtype,H", [("bf16", 4), ("bf16", 64), ("f32", 4)])
 def test_scale_and_large_queries(dtype, H):
     """Scores far apart (one key takes all the weight), an explicit scale, and
