@@ -12,11 +12,11 @@
 // row and key, so with few rows per cache head it is bound by HBM: at the
 // measured copy rate an SM has 6.3 clocks per token of 128 channels, 3.1 of 64.
 //
-// Measured (one row per cache head, d = 128, 32 heads): 8.3 us for 1024 tokens, 34 for
-// 32,768 (4.5 TB/s), 104 for 131,072 (5.8), 198 for 262,144 (6.1); each further
-// token costs 1.02 times what it does at the copy rate. The other 11 us are the same for
+// Measured (one row per cache head, d = 128, 32 heads): 7.4 us for 1024 tokens, 32 for
+// 32,768 (4.7 TB/s), 103 for 131,072 (5.9), 196 for 262,144 (6.2); each further
+// token costs 1.03 times what it does at the copy rate. The other 9 us are the same for
 // every length: 2 to launch, 1.4 to find a block's place on the line, 1.5 until
-// the first codes arrive, an SM's last blocks alone, 3 to 4 for the join.
+// the first codes arrive, an SM's last blocks alone, 2 for the join.
 //
 // Work split. An item is one (sequence, tile of query rows, cache head); it is
 // cut into chunks of 128 tokens. The chunks of all items form one line, and the
@@ -960,8 +960,8 @@ CachePlan cache_attn_plan(const CacheArgs& a, int d, int dtype, unsigned flags) 
     const long long rows = (long long)a.G * a.T;
     // Rows of a tile: the fewest that hold the cache head's rows. Up to 32 rows a tile is
     // in registers; above, 64 rows of 128 channels go to tcgen05. (32 rows over 2 x 16 heads
-    // of 32768 tokens: 66 us in registers, 78 on tcgen05; 64 rows over 4 x 8 heads of 9000
-    // to 16384 tokens: 57.5 as two tiles in registers, 45.2 on tcgen05.) float32 takes
+    // of 32768 tokens: 65 us in registers, 78 on tcgen05; 64 rows over 4 x 8 heads of 9000
+    // to 16384 tokens: 57.5 as two tiles in registers, 41.6 on tcgen05.) float32 takes
     // twice the registers, so 16 rows at most.
     p.tensor = !(flags & MITA_FLAG_SIMT);
     int blocks = 4;  // per SM

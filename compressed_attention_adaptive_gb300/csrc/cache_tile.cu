@@ -29,8 +29,8 @@
 // block that gives up raises its abort flag, lets its copies and products land and
 // frees its tensor memory.
 //
-// Measured: 64 rows over 2 x 16 heads of 131,072 tokens 269 us (510 TFLOP/s), of 32,768
-// 81 us; 4 x 8 heads of 9000 to 16384 tokens 45 us (the register form 57.5). A chunk
+// Measured: 64 rows over 2 x 16 heads of 131,072 tokens 265 us (519 TFLOP/s), of 32,768
+// 79 us; 4 x 8 heads of 9000 to 16384 tokens 41.6 us (the register form 57.5). A chunk
 // takes about 2400 clocks, and no role is busy all of it: softmax 1900, values 1500,
 // issuing 1000 (a product of 128 x 64 x 16 takes 51 to 60), copies 1000, keys 800. They
 // share the issue slots (56 %, 6500 instructions a chunk) and wait for each other's
