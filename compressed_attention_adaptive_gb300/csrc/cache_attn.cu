@@ -118,7 +118,8 @@ k_cache_attn_simt(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restric
     const int piece = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sub = lane >> 3, ch = lane & 7;  // token of four, chunk
     __shared__ Walk<R> walk;
-    if (!walk.begin(a, piece, out.pieces)) {
+    __shared__ LineScan sums;
+    if (!walk.begin(a, piece, out.pieces, sums)) {
         end_piece(a, out, piece, 0);
         return;
     }
@@ -408,7 +409,8 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
         for (int i = 0; i < ST; ++i) tc::mbar_init(&bars[warp][i], 2);
         tc::fence_mbar_init();
     }
-    if (!walk.begin(a, piece, out.pieces)) {
+    __shared__ LineScan sums;
+    if (!walk.begin(a, piece, out.pieces, sums)) {
         end_piece(a, out, piece, 0);
         return;
     }
@@ -843,6 +845,7 @@ __global__ void __launch_bounds__(32 * W * join_rows(W)) k_cache_join(CacheArgs 
     __shared__ float acc8[R][W][D];
     __shared__ float2 ml8[R][W];
     __shared__ CutItem cut;
+    __shared__ LineScan sums;
     const int lane = threadIdx.x & 31, sub = threadIdx.x >> 5, mine = sub / W, warp = sub % W;
     if (blockIdx.x == gridDim.x - 1) {
         if (blockIdx.y) return;
@@ -853,17 +856,8 @@ __global__ void __launch_bounds__(32 * W * join_rows(W)) k_cache_join(CacheArgs 
         if (threadIdx.x == 0) *a.status = timeout ? kStTimeout : bounds ? kStBounds : kStOk;
         return;
     }
-    if (sub == 0) {
-        CutItem x{};
-        if (by_item) {
-            x = cut_item(a, out, blockIdx.x, lane);
-            if (lane == 0) cut = x;
-        } else {
-            if (lane == 0) cut.rows = 0;
-            __syncwarp();
-            if (cut_item_of_piece(a, out, blockIdx.x, lane, &x)) cut = x;
-        }
-    }
+    if (threadIdx.x == 0) cut.rows = 0;
+    find_cut(a, out, blockIdx.x, by_item, sums, cut);
     __syncthreads();
     const CutItem c = cut;
     if ((int)blockIdx.y * R >= c.rows) return;

@@ -234,7 +234,8 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
     }
     if (tid < kEdge) nanv[tid] = 0;
     tc::fence_before_sync();
-    bool more = walk.begin(a, piece, out.pieces);
+    __shared__ LineScan sums;
+    bool more = walk.begin(a, piece, out.pieces, sums);
     tc::fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
     constexpr uint32_t kO = 192, kK = 256, kV = 384;  // columns: three S of 64, O, two chunks' keys, two chunks' values

@@ -68,46 +68,71 @@ __device__ __forceinline__ int warp_scan(int x, int lane) {
     return x;
 }
 
-// The line of a call, by a whole warp. `mine` is left with the lane's sequence of the last 32.
-__device__ __forceinline__ Line call_line(const CacheArgs& a, int rtile, int extra, int max_pieces, int lane, SeqWork* mine) {
-    unsigned items = 0, chunks = 0;
-#pragma unroll 8
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-        mine->items = 0;
-        if (b0 + lane < a.B) *mine = seq_work(a, b0 + lane, rtile);
-        items += mine->items;
-        chunks += mine->items * mine->chunks;
+// Finds the line of a call, by a whole block: a thread takes B / blockDim sequences, its
+// own few or one. `at(line, s0, s1, first, before, share)` is then called by each thread
+// that has sequences [s0, s1), with the work of s0, the units before them and theirs. (One warp that went over
+// the sequences 32 at a time, twice, made a call of 1024 sequences 46 us longer.)
+struct LineScan {
+    unsigned items[32], chunks[32];  // of each warp
+};
+template <typename At>
+__device__ __forceinline__ void scan_line(const CacheArgs& a, int rtile, int extra, int max_pieces, LineScan& sums, At at) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = a.B <= blockDim.x ? 1 : (a.B + blockDim.x - 1) / blockDim.x;
+    const int warps = per == 1 ? (a.B + 31) / 32 : (a.B + 32 * per - 1) / (32 * per);
+    const int s0 = threadIdx.x * per, s1 = min(s0 + per, a.B);
+    unsigned items = 0, chunks = 0, items0 = 0, chunks0 = 0;  // the thread's; of the warps before
+    SeqWork first{};
+    if (warp < warps && s0 < s1) {
+        first = seq_work(a, s0, rtile);
+        items = first.items;
+        chunks = first.items * first.chunks;
+#pragma unroll 4
+        for (int b = s0 + 1; b < s1; ++b) {
+            const SeqWork w = seq_work(a, b, rtile);
+            items += w.items;
+            chunks += w.items * w.chunks;
+        }
     }
-    items = __reduce_add_sync(0xffffffffu, items);
-    chunks = __reduce_add_sync(0xffffffffu, chunks);
+    unsigned all_items = __reduce_add_sync(0xffffffffu, items), all_chunks = __reduce_add_sync(0xffffffffu, chunks);
+    if (warps > 1) {
+        if (lane == 0) {
+            sums.items[warp] = all_items;
+            sums.chunks[warp] = all_chunks;
+        }
+        __syncthreads();
+        all_items = all_chunks = 0;
+        for (int w = 0; w < warps; ++w) {
+            if (w == warp) {
+                items0 = all_items;
+                chunks0 = all_chunks;
+            }
+            all_items += sums.items[w];
+            all_chunks += sums.chunks[w];
+        }
+    } else {
+        __syncwarp();
+    }
+    if (warp >= warps) return;
     Line l;
-    l.extra = chunks >= (unsigned)max_pieces * kFew ? extra : 0;
-    l.total = (int)(chunks + items * l.extra);
+    l.extra = all_chunks >= (unsigned)max_pieces * kFew ? extra : 0;
+    l.total = (int)(all_chunks + all_items * l.extra);
     l.pieces = min(max_pieces, l.total);
     l.q = l.pieces ? l.total / l.pieces : 0;
     l.r = l.total - l.q * l.pieces;
-    return l;
+    const int share = (int)(chunks + items * l.extra);
+    const int before = (int)(chunks0 + items0 * l.extra) + warp_scan(share, lane) - share;
+    if (s0 < s1) at(l, s0, s1, first, before, share);
 }
-// The sequence whose share holds unit w, by the same warp after call_line(): one lane
-// returns true, with the sequence, its work and the units before it.
-__device__ __forceinline__ bool find_unit(const CacheArgs& a, const Line& l, int rtile, int w, int lane, SeqWork* mine,
-                                          int* b, int* before) {
-    int base = 0, x = 0, share = 0;
-    unsigned hit = 0;
-    int b0 = 0;
-    for (; b0 < a.B && !hit; b0 += 32) {
-        if (a.B > 32) {
-            mine->items = 0;
-            if (b0 + lane < a.B) *mine = seq_work(a, b0 + lane, rtile);
-        }
-        share = mine->items * (mine->chunks + l.extra);
-        x = base + warp_scan(share, lane);
-        hit = __ballot_sync(0xffffffffu, w < x);  // the first whose share ends behind w
-        base = __shfl_sync(0xffffffffu, x, 31);
+// The sequence of [s0, ..) whose share holds unit w, with its work (first that of s0) and
+// the units before it.
+__device__ __forceinline__ int find_unit(const CacheArgs& a, const Line& l, int rtile, int w, int s0, int* before, SeqWork* sw) {
+    for (;;) {
+        const int share = sw->items * (sw->chunks + l.extra);
+        if (w < *before + share) return s0;
+        *before += share;
+        *sw = seq_work(a, ++s0, rtile);
     }
-    *before = x - share;
-    *b = b0 - 32 + lane;
-    return hit && lane == __ffs(hit) - 1;
 }
 
 // One block's part of an item.
@@ -118,7 +143,7 @@ struct Segment {
 };
 
 // A block's walk along its piece, in shared memory: registers are for the sums.
-// The first warp finds the start, thread 0 moves it; begin() and next() are called
+// The thread with the first sequence finds the start, thread 0 moves it; begin() and next() are called
 // by the whole block and leave the next segment in `s`. A piece holds at most one
 // segment of an item that began before it (the first) and one of an item that goes
 // on behind it (the last).
@@ -157,24 +182,20 @@ template <int RT, int EXTRA = kExtra> struct Walk {
             }
         }
     }
-    __device__ __forceinline__ bool begin(const CacheArgs& a, int piece, int max_pieces) {
-        if (threadIdx.x < 32) {
-            const int lane = threadIdx.x;
-            SeqWork mine{};
-            const Line l = call_line(a, RT, EXTRA, max_pieces, lane, &mine);
-            if (lane == 0) more = false;
-            __syncwarp();
-            int b1, before1;
-            if (piece < l.pieces && find_unit(a, l, RT, l.at(piece), lane, &mine, &b1, &before1)) {
-                line = l;
-                w = l.at(piece);
-                w_end = l.at(piece + 1);
-                before = before1;
-                b = b1;
-                sw = mine;
-                segment(a);
-            }
-        }
+    __device__ __forceinline__ bool begin(const CacheArgs& a, int piece, int max_pieces, LineScan& sums) {
+        if (threadIdx.x == 0) more = false;
+        scan_line(a, RT, EXTRA, max_pieces, sums, [&](const Line& l, int s0, int, SeqWork first, int before0, int share) {
+            if (piece >= l.pieces) return;
+            const int w0 = l.at(piece);
+            if (w0 < before0 || w0 >= before0 + share) return;
+            b = find_unit(a, l, RT, w0, s0, &before0, &first);
+            line = l;
+            w = w0;
+            w_end = l.at(piece + 1);
+            before = before0;
+            sw = first;
+            segment(a);
+        });
         __syncthreads();
         return more;
     }
@@ -210,48 +231,36 @@ struct CutItem {
     int b, h, row0, rows;  // rows = 0: not cut
     int piece, parts;      // the first part's piece, and the pieces it goes over
 };
-// Item i of the call (of all tiles of T rows), by a whole warp.
-__device__ __forceinline__ CutItem cut_item(const CacheArgs& a, const AttnOut& out, int i, int lane) {
-    SeqWork sw{};
-    const Line l = call_line(a, out.rows, out.extra, out.pieces, lane, &sw);
-    CutItem c{};
-    c.b = i / (out.tiles * a.Hkv);
-    const int j = i - c.b * (out.tiles * a.Hkv), tile = j / a.Hkv;
-    int before = 0;  // units before the sequence
-    for (int b0 = 0; b0 < c.b; b0 += 32)
-        if (b0 + lane < c.b) {
-            const SeqWork x = seq_work(a, b0 + lane, out.rows);
-            before += x.items * (x.chunks + l.extra);
+// Fills in `c` (rows = 0 so far) for item i of the call (of all tiles of T rows) or, with
+// by_item false, for the item that begins in piece i and goes on behind it (there is at
+// most one). By a whole block; visible after its next barrier.
+__device__ __forceinline__ void find_cut(const CacheArgs& a, const AttnOut& out, int i, bool by_item, LineScan& sums,
+                                         CutItem& c) {
+    scan_line(a, out.rows, out.extra, out.pieces, sums, [&](const Line& l, int s0, int s1, SeqWork sw, int before, int share) {
+        int b, j;  // the sequence, and the item's number in it
+        if (by_item) {
+            b = i / (out.tiles * a.Hkv);
+            if (b < s0 || b >= s1) return;
+            j = i - b * (out.tiles * a.Hkv);
+            for (int x = s0; x < b; sw = seq_work(a, ++x, out.rows)) before += sw.items * (sw.chunks + l.extra);
+            if (j >= sw.items) return;
+        } else {
+            if (i + 1 >= l.pieces) return;
+            const int w = l.at(i + 1);  // the first unit behind the piece
+            if (w < before || w >= before + share) return;
+            b = find_unit(a, l, out.rows, w, s0, &before, &sw);
+            j = (w - before) / (sw.chunks + l.extra);
         }
-    before = __reduce_add_sync(0xffffffffu, before);
-    sw = seq_work(a, c.b, out.rows);
-    if (j >= sw.items) return c;
-    const int first = before + j * (sw.chunks + l.extra) + l.extra;
-    c.piece = l.piece_of(first);
-    c.parts = l.piece_of(first + sw.chunks - 1) - c.piece + 1;
-    c.h = j - tile * a.Hkv;
-    c.row0 = tile * out.rows;
-    if (c.parts > 1) c.rows = min(out.rows, sw.rows - c.row0);
-    return c;
-}
-// The item that begins in piece p and goes on behind it (there is at most one), by a
-// whole warp; the lane that returns true has it.
-__device__ __forceinline__ bool cut_item_of_piece(const CacheArgs& a, const AttnOut& out, int p, int lane, CutItem* c) {
-    SeqWork sw{};
-    const Line l = call_line(a, out.rows, out.extra, out.pieces, lane, &sw);
-    if (p + 1 >= l.pieces) return false;
-    const int w = l.at(p + 1);  // the first unit behind the piece
-    int before;
-    if (!find_unit(a, l, out.rows, w, lane, &sw, &c->b, &before)) return false;
-    const int len = sw.chunks + l.extra, j = (w - before) / len, first = before + j * len + l.extra;
-    if (first >= w || first < l.at(p)) return false;
-    const int tile = j / a.Hkv;
-    c->h = j - tile * a.Hkv;
-    c->row0 = tile * out.rows;
-    c->rows = min(out.rows, sw.rows - c->row0);
-    c->piece = p;
-    c->parts = l.piece_of(first + sw.chunks - 1) - p + 1;
-    return true;
+        const int first = before + j * (sw.chunks + l.extra) + l.extra, last = first + sw.chunks - 1, tile = j / a.Hkv;
+        const int piece = l.piece_of(first), parts = l.piece_of(last) - piece + 1;
+        if (parts < 2 || (!by_item && piece != i)) return;
+        c.b = b;
+        c.h = j - tile * a.Hkv;
+        c.row0 = tile * out.rows;
+        c.rows = min(out.rows, sw.rows - c.row0);
+        c.piece = piece;
+        c.parts = parts;
+    });
 }
 
 // A kernel that this one's launch may be followed by can be set up meanwhile;
