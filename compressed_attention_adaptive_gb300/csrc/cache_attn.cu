@@ -127,8 +127,8 @@ k_cache_attn_simt(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restric
     const uint32_t ring_addr = smem_addr(ring);
 
     do {
-        const Segment& s = walk.s;
-        const int n = walk.sw.n, count = walk.sw.count, b = s.b;
+        const Segment& s = walk.s();
+        const int n = s.n, count = s.count, b = s.b;
         const float kscale = a.scale * kLog2e * pow2(cache_exp(a, 0, s.h)), vscale = pow2(cache_exp(a, 1, s.h));
         float q[R][E], o[R][E], m[R], l[R];
         int lim[R];
@@ -269,8 +269,8 @@ k_cache_attn_simt(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restric
             for (int i = 0; i < E; ++i) os[(set * R + r) * D + ch * E + i] = o[r][i];
         }
         __syncthreads();
-        const bool whole = walk.whole();
-        const int slot = walk.slot(piece);
+        const bool whole = s.whole();
+        const int slot = s.slot(piece);
         for (int x = threadIdx.x; x < s.rows * D; x += kThreads) {
             const int r = x / D, c = x - r * D;
             float mx = -INFINITY;
@@ -371,8 +371,12 @@ template <typename T, int D, int NR> constexpr int mma_smem() {
 // float32 rows are each two halves, x = hi + lo with lo = x - hi rounded (22 bits and
 // a sign, 2^-23 of x), p likewise: two products where bf16 has one, with the same
 // exact keys and values. The products are summed in fp32 by steps of 16 tokens
-// and by ordinary additions from there. (8 x 12 heads of 16384 tokens, d = 64: 39 us, on
+// and by ordinary additions from there. (8 x 12 heads of 16384 tokens, d = 64: 38 us, on
 // CUDA cores 52.)
+//
+// The next segment is found while a segment's first codes are on their way, and its own
+// first copies are issued before the warps' sums are joined (8 x 12 heads of 16384 tokens in
+// float32 39.1 to 37.8 us, 32 x 32 of 2048 77 to 75, bf16 batches of short sequences 1 to 2 %).
 //
 // A warp has about 570 instructions per 32 tokens of 128 channels and 8 rows, 128 of
 // them conversions of codes and 128 products by scales (half rate each). Over the
@@ -416,39 +420,46 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
     }
     int put = 0, take = 0, phase = 0;  // stages of the ring, and the phase of `take`
     bool dead = false;                 // a wait ran out: the warp goes on without keys
-
-    do {
-        const Segment& s = walk.s;
-        const int n = walk.sw.n, count = walk.sw.count, b = s.b;
+    // A segment's copies. Lane l has the group number of group l & 1 of step l >> 1 in the
+    // current run of 16 steps, and issues that copy itself; the next run's table entries are
+    // loaded a run ahead.
+    const uint8_t *gcur, *gnxt;
+    int low, top, steps;  // keys that the first and the last row of the tile see
+    auto groups = [&](const Segment& s, int i0) -> const uint8_t* {
+        const int gi = GroupRun::load(a, s, top, warp, lane, i0, &found);
+        return gi < 0 ? nullptr : cache + (long long)gi * L::kBytes;
+    };
+    auto enter = [&](const Segment& s) {
         // rows of a tile see more keys the later their token is
-        const int low = row_limit(a, n, count, s.row0 / a.G), top = row_limit(a, n, count, (s.row0 + s.rows - 1) / a.G);
-        const int steps = dead ? 0 : s.c1 - s.c0;
-        // Lane l has the group number of group l & 1 of step l >> 1 in the current run of 16
-        // steps, and issues that copy itself; the next run's table entries are loaded a run ahead.
-        auto groups = [&](int i0) -> const uint8_t* {
-            const int gi = GroupRun::load(a, s, top, warp, lane, i0, &found);
-            return gi < 0 ? nullptr : cache + (long long)gi * L::kBytes;
-        };
-        const uint8_t *gcur = groups(0), *gnxt = groups(16);
-        auto issue = [&](int i) {
-            if (i < steps && (lane >> 1) == (i & 15)) {
-                uint64_t* bar = &bars[warp][put];
-                if (gcur) {
-                    tc::mbar_expect_tx(bar, L::kBytes);
-                    bulk_copy(ring_addr + put * kStage + (lane & 1) * L::kBytes, gcur, L::kBytes, bar);
-                } else {
-                    tc::mbar_arrive(bar);
-                }
+        low = row_limit(a, s.n, s.count, s.row0 / a.G);
+        top = row_limit(a, s.n, s.count, (s.row0 + s.rows - 1) / a.G);
+        steps = dead ? 0 : s.c1 - s.c0;
+        gcur = groups(s, 0);
+        gnxt = groups(s, 16);
+    };
+    auto issue = [&](const Segment& s, int i) {
+        if (i < steps && (lane >> 1) == (i & 15)) {
+            uint64_t* bar = &bars[warp][put];
+            if (gcur) {
+                tc::mbar_expect_tx(bar, L::kBytes);
+                bulk_copy(ring_addr + put * kStage + (lane & 1) * L::kBytes, gcur, L::kBytes, bar);
+            } else {
+                tc::mbar_arrive(bar);
             }
-            if (i < steps) put = put + 1 == ST ? 0 : put + 1;
-            if ((i & 15) == 15) {
-                gcur = gnxt;
-                gnxt = groups(i + 17);
-            }
-        };
-#pragma unroll
-        for (int i = 0; i < ST - 1; ++i) issue(i);
+        }
+        if (i < steps) put = put + 1 == ST ? 0 : put + 1;
+        if ((i & 15) == 15) {
+            gcur = gnxt;
+            gnxt = groups(s, i + 17);
+        }
+    };
+    int k = walk.cur;  // the current segment
+    enter(walk.segs[k]);
+    issue(walk.segs[k], 0);
 
+    for (bool more = true; more; k ^= 1) {
+        const Segment& s = walk.segs[k];
+        const int n = s.n, count = s.count, b = s.b;
         // Q: warp w has rows 8 w + g, lane (g, t4) channels [t4 d/4, (t4 + 1) d/4) of them
         const float vscale = pow2(cache_exp(a, 1, s.h));
         if (warp < NR) {
@@ -490,6 +501,7 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
             }
         }
         __syncthreads();
+        if (threadIdx.x == 0) walk.segment(a);  // the next one, while the first codes are on their way
         constexpr bool kQRegs = NR == 1 && !F;  // Q in registers, else in shared memory
         uint2 qf[kQRegs ? KS : 1];
         if (kQRegs) {
@@ -514,7 +526,7 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
 
         for (int i = 0; i < steps; ++i) {
             __syncwarp();  // the stage that the next copy goes to has been read
-            issue(i + ST - 1);
+            issue(s, i + ST - 1);
             if (!__all_sync(0xffffffffu, tc::mbar_wait(&bars[warp][take], phase, a.status))) {
                 // give up, but not before the copies in flight have landed (or a second has passed for each)
                 for (int x = i + 1; x < steps && x < i + ST; ++x) {
@@ -766,15 +778,20 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
             for (int e = 0; e < 2; ++e)
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], x);
-        __syncthreads();  // every warp is done with its ring
-        // Join the warps: [warp][row][d] sums, 16 bytes (four channels) at a time. The
-        // lanes that store together have four rows and two chunks apart by d/32; the
-        // row's bits exchange chunks so that eight lanes meet eight bank groups.
-        float4* os = reinterpret_cast<float4*>(smem);
-        constexpr int C4 = D / 4;
+        // Join the warps: [warp][row][d] sums, 16 bytes (four channels) at a time. With 8 rows
+        // they are in the stage of the warp's ring that the next segment's first copy does not
+        // go to, else over all the rings. The lanes that store together have four rows and two
+        // chunks apart by d/32; the row's bits exchange chunks so that eight lanes meet eight bank
+        // groups.
+        constexpr bool kOwn = NR == 1;
+        static_assert(!kOwn || (ST == 2 && kStage >= 8 * D * 4 && kStage % 128 == 0), "a stage holds a warp's sums");
+        if (!kOwn) __syncthreads();  // every warp is done with its ring
+        float4* os = reinterpret_cast<float4*>(smem + (kOwn ? (put ^ 1) * kStage : 0));
+        constexpr int C4 = D / 4, kWarpRows = kOwn ? ST * kStage / (D * 4) : RT;  // rows from one warp's to the next's
+        static_assert(!kOwn || ST * kStage % (D * 4) == 0, "whole rows");
         auto at4 = [&](int wp, int r, int c) {
             const int t = (r >> 1) & 3;
-            return (wp * RT + r) * C4 + (c ^ (D == 128 ? t : (t & 1) | (t & 2) << 1));
+            return (wp * kWarpRows + r) * C4 + (c ^ (D == 128 ? t : (t & 1) | (t & 2) << 1));
         };
 #pragma unroll
         for (int j = 0; j < NR; ++j)
@@ -789,8 +806,14 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
                                                                      o[j][2 * x + 1][e], o[j][2 * x + 1][e + 2]);
             }
         __syncthreads();
-        const bool whole = walk.whole();
-        const int slot = walk.slot(piece);
+        const Segment& next = walk.segs[k ^ 1];
+        more = walk.more;
+        if (more) {
+            enter(next);
+            if (kOwn) issue(next, 0);
+        }
+        const bool whole = s.whole();
+        const int slot = s.slot(piece);
         for (int x = threadIdx.x; x < s.rows * C4; x += kThreads) {
             const int r = x / C4, c = x - r * C4;
             float2 v[4];
@@ -823,7 +846,9 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
             }
         }
         tc::fence_proxy_async();  // the next segment's copies come after these accesses of the ring
-    } while (walk.next(a));
+        __syncthreads();
+        if (!kOwn && more) issue(next, 0);
+    }
     end_piece(a, out, piece, found);
 }
 

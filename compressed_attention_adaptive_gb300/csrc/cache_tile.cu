@@ -244,8 +244,8 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
     int issued = 0;         // chunks that the copying warp has issued
     bool stop = false;      // a wait of an earlier segment gave up
     for (; more; ++seg) {
-        const Segment s = walk.s;
-        const int n = walk.sw.n, count = walk.sw.count;
+        const Segment s = walk.s();
+        const int n = s.n, count = s.count;
         const int low = row_limit(a, n, count, s.row0 / a.G), top = row_limit(a, n, count, (s.row0 + s.rows - 1) / a.G);
         // chunks that some row of the tile sees, at least one
         const int nc = max(1, min(s.c1, (top + kChunk - 1) / kChunk) - s.c0);
@@ -572,8 +572,8 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
                     linv[r] = sum == 0.0f ? 0.0f : 1.0f / sum;
                 }
                 softmax_sync(wg);
-                const bool whole = walk.whole(), nans = nan_flag;
-                const long long slot = (long long)walk.slot(piece) * N;
+                const bool whole = s.whole(), nans = nan_flag;
+                const long long slot = (long long)s.slot(piece) * N;
                 // lane tl of the thread's rows, eight at a time (little code: it runs once a segment)
                 const int ch = 16 * (tl & 7) + 4 * (tl >> 5) + ((tl >> 3) & 2) + ((tl >> 3) & 1);
 #pragma unroll 1

@@ -140,23 +140,32 @@ struct Segment {
     int b, h, row0, rows;  // sequence, cache head, first row and rows of the tile
     int c0, c1, chunks;    // chunks [c0, c1) of the item's `chunks`
     int first;             // the item's chunk 0 on the line
+    int n, count;          // the sequence's
+    __device__ __forceinline__ bool whole() const { return c0 == 0 && c1 == chunks; }
+    // Where the sums of a part of an item go: the part that starts the item, or another.
+    __device__ __forceinline__ int slot(int piece) const { return 2 * piece + (c0 == 0); }
 };
 
 // A block's walk along its piece, in shared memory: registers are for the sums.
-// The thread with the first sequence finds the start, thread 0 moves it; begin() and next() are called
-// by the whole block and leave the next segment in `s`. A piece holds at most one
-// segment of an item that began before it (the first) and one of an item that goes
-// on behind it (the last).
+// The thread with the first sequence finds the start, thread 0 moves it; begin() and
+// next() are called by the whole block and leave the next segment in s(). (A kernel may
+// call segment() ahead instead, by thread 0: the segment before stays as it was.) A
+// piece holds at most one segment of an item that began before it (the first) and
+// one of an item that goes on behind it (the last).
 template <int RT, int EXTRA = kExtra> struct Walk {
     Line line;
     int w, w_end, before, b;  // position; units before sequence b
     SeqWork sw;
-    Segment s;
+    Segment segs[2];  // the current one and another
+    int cur;
     bool more;
 
+    __device__ __forceinline__ const Segment& s() const { return segs[cur]; }
     // The next segment from w on, if there is one.
     __device__ __forceinline__ void segment(const CacheArgs& a) {
         more = false;
+        cur ^= 1;
+        Segment& s = segs[cur];
         while (w < w_end) {
             const int len = sw.chunks + line.extra;
             if (w - before >= sw.items * len) {  // next sequence with work
@@ -172,6 +181,8 @@ template <int RT, int EXTRA = kExtra> struct Walk {
             s.row0 = tile * RT;
             s.rows = min(RT, sw.rows - s.row0);
             s.chunks = sw.chunks;
+            s.n = sw.n;
+            s.count = sw.count;
             s.first = start + line.extra;
             s.c0 = max(w - s.first, 0);
             s.c1 = min(s.chunks, w_end - s.first);
@@ -194,6 +205,7 @@ template <int RT, int EXTRA = kExtra> struct Walk {
             w_end = l.at(piece + 1);
             before = before0;
             sw = first;
+            cur = 0;
             segment(a);
         });
         __syncthreads();
@@ -205,9 +217,6 @@ template <int RT, int EXTRA = kExtra> struct Walk {
         __syncthreads();
         return more;
     }
-    __device__ __forceinline__ bool whole() const { return s.c0 == 0 && s.c1 == s.chunks; }
-    // Where the sums of a part of an item go: the part that starts the item, or another.
-    __device__ __forceinline__ int slot(int piece) const { return 2 * piece + (s.c0 == 0); }
 };
 
 // What a piece finds wrong; the join makes the call's status word of it. Between
