@@ -364,6 +364,21 @@ def test_many_short_sequences_and_shared_pages():
     assert torch.all((a - b).abs() <= 2 * (2.0 ** -8 * a.abs().maximum(b.abs()) + 2.0 ** -11 * 4))
 
 
+@pytest.mark.parametrize("dtype,d,H,T,B,simt", [("bf16", 128, 64, 1, 200, False), ("bf16", 128, 3, 5, 700, False),
+                                                ("bf16", 64, 10, 2, 150, False), ("f32", 128, 1, 3, 300, False),
+                                                ("f32", 64, 2, 1, 1400, False), ("bf16", 128, 2, 2, 150, True)])
+def test_many_sequences_in_every_form(dtype, d, H, T, B, simt):
+    """More sequences than a block's warps or threads, more items than pieces, empty ones among them."""
+    rng = np.random.default_rng(B)
+    lens = [int(n) for n in rng.integers(0, 400 if B < 500 else 90, B) * rng.integers(0, 2, B)]
+    lens[0], lens[-1] = 0, 700
+    counts = [int(c) for c in rng.integers(0, T + 1, B)]
+    counts[-1] = T
+    pool = Pool(lens, 1, d, 16, dtype, seed=B)
+    Q, O, L = _attend(pool, H, T, True, counts, simt)
+    _check(pool, H, T, True, Q, O, L, counts, simt, label="%d sequences %s d%d%s" % (B, dtype, d, " simt" * simt))
+
+
 # -------------------------------------------- out of range, and the status word
 
 
