@@ -211,6 +211,7 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
     allow_next();
     const int piece = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int found = 0;
+    // (waits for another kernel's blocks on this SM, which end whatever this one does)
     if (warp == S::kIssue) tc::tmem_alloc(&tmem_slot, 512);
     if (tid == 0) {
         for (int i = 0; i < kRawStages; ++i) {

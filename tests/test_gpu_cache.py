@@ -344,6 +344,25 @@ def test_pool_past_32_bits():
             assert torch.allclose(O.float(), O2.float(), rtol=2 ** -6, atol=2 ** -8)
 
 
+def test_tiles_past_32_bits():
+    """The same for tiles of 64 rows, whose copies take several groups of a page."""
+    import torch
+    import compressed_attention_adaptive_gb300 as mita
+    small = Pool([700, 90], 2, 128, 256, "bf16", seed=22, H=128)
+    n_pages = 70000
+    p = mita.CacheParams(2, 128, 2, 1, 128, 256, n_pages, small.cols)
+    assert mita.mita_cache_size(p) > 2 ** 32 + 2 ** 29
+    cache = torch.empty(mita.mita_cache_size(p), dtype=torch.uint8, device="cuda")
+    table = torch.where(small.table < small.n_pages, n_pages - 1 - 3 * small.table, small.table)
+    f = mita.CacheParams(2, 2, 2, 700, 128, 256, n_pages, small.cols)
+    mita.mita_cache_write(f, small.K, small.V, cache, table, small.len_t, mita.cache_workspace(f), counts=small.len_t)
+    Q, O, L = _attend(small, 128, 1, False)
+    O2, ws = torch.zeros_like(O), mita.cache_workspace(p)
+    mita.mita_cache_attention(p, Q, cache, table, small.len_t, O2, ws)
+    mita.mita_device_status(ws)
+    assert torch.equal(O, O2)
+
+
 def test_many_short_sequences_and_shared_pages():
     """A thousand sequences, most of a few tokens, some without a row; then every
     second one with the pages of its neighbour (a shared prefix)."""
@@ -530,6 +549,37 @@ def test_another_stream():
 
 
 # --------------------------------------------------------- a run of them together
+
+
+def test_beside_a_forward_pass_on_another_stream():
+    """Attention of each form beside mita_forward on another stream is the same bits as alone."""
+    import torch
+    import compressed_attention_adaptive_gb300 as mita
+    g = torch.Generator(device="cuda").manual_seed(5)
+    X = [torch.randn((1, 4, 8192, 128), generator=g, device="cuda").to(torch.bfloat16) for _ in range(3)]
+    fp = mita.Params(1, 4, 8192, 128, m=128, k=256, s=2)
+    fws, FO = mita.workspace(fp), torch.empty_like(X[0])
+    mita.mita_forward(fp, *X, FO, fws)
+    want = FO.clone()
+    calls = []
+    for H, T, lens in ((2, 1, [3000, 500]), (16, 8, [2000, 900]), (128, 1, [4000, 700])):
+        pool = Pool(lens, 2, 128, 64, "bf16", seed=H)
+        Q, O, _ = _attend(pool, H, T, True)
+        p = mita.CacheParams(2, H, 2, T, 128, 64, pool.n_pages, pool.cols, 0.0, mita.FLAG_CAUSAL)
+        calls.append((pool, p, Q, O, torch.zeros_like(O), mita.cache_workspace(p)))
+    torch.cuda.synchronize()
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(20):
+        mita.mita_forward(fp, *X, FO, fws, stream=one)
+        for pool, p, Q, O, O2, ws in calls:
+            mita.mita_cache_attention(p, Q, pool.cache, pool.table, pool.len_t, O2, ws, stream=two)
+    torch.cuda.synchronize()
+    mita.mita_device_status(fws)
+    # (its buckets fill in any order, so it is held to its own tolerance)
+    assert torch.allclose(FO.float(), want.float(), rtol=2e-2, atol=2e-2)
+    for _, _, _, O, O2, ws in calls:
+        mita.mita_device_status(ws)
+        assert torch.equal(O, O2)
 
 
 def test_prompt_then_steps_then_another_pass():
