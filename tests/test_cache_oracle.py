@@ -42,6 +42,19 @@ def test_fp32_quotients_round_to_the_same_codes(dtype):
     np.testing.assert_array_equal(oc.nearest((y / s).astype(np.float64), oc.E2M1), exact)
 
 
+def test_fp32_scales_round_as_the_exact_quotient():
+    """The correctly rounded fp32 quotient max / 6 is on a midpoint of the scales only
+    where the exact quotient is: every midpoint and the floats next to 6 times it. A
+    product by the rounded 1 / 6 is not enough: it moves some of them onto a midpoint."""
+    mid = (oc.E4M3[1:] + oc.E4M3[:-1]) / 2
+    a = (6 * mid).astype(np.float32)  # exact: 5 and 2 significant bits
+    a = (a.view(np.int32)[:, None] + np.arange(-4, 5, dtype=np.int32)).view(np.float32).ravel()
+    want = oc.nearest(a.astype(np.float64) / 6, oc.E4M3)
+    np.testing.assert_array_equal(oc.nearest((a / np.float32(6)).astype(np.float64), oc.E4M3), want)
+    product = oc.nearest((a * (np.float32(1) / np.float32(6))).astype(np.float64), oc.E4M3)
+    assert 0 < int((product != want).sum()) < 40
+
+
 def test_special_blocks():
     x = np.zeros((6, 16))
     x[1, 3], x[2, 4], x[3, 0] = np.nan, -np.inf, 1e30

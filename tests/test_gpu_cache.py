@@ -94,6 +94,33 @@ def test_special_rows():
                 np.testing.assert_array_equal(_np(out[0]), pool.held(0, which))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scales_next_to_midpoints(dtype, d):
+    """Blocks whose largest channel is 6 times a midpoint between two scales, or one of
+    the numbers next to it: the scale is that of the exact quotient, ties to even."""
+    import torch
+    import compressed_attention_adaptive_gb300 as mita
+    big = (3 * (ocache.E4M3[1:] + ocache.E4M3[:-1])).astype(np.float32)
+    step = 1 << 16 if dtype == "bf16" else 1
+    big = (big.view(np.int32)[:, None] + step * np.arange(-2, 3, dtype=np.int32)).view(np.float32).ravel()
+    n = -(-big.size // (d // 16))
+
+    def make(rng, shape):
+        x = rng.uniform(-1, 1, (n * (d // 16), 16)).astype(np.float32)
+        x[:big.size] *= 0.99 * big[:, None]
+        x[np.arange(big.size), rng.integers(0, 16, big.size)] = big * rng.choice(np.float32([-1, 1]), big.size)
+        x = x.reshape(1, 1, n, d)
+        return x, -x
+
+    pool = Pool([n], 1, d, 16, dtype, make=make, seed=d)
+    K, V = (torch.empty_like(pool.K) for _ in range(2))
+    mita.mita_cache_read(pool.fill_p, pool.cache, pool.table, pool.len_t, K, V, pool.fill_ws)
+    mita.mita_device_status(pool.fill_ws)
+    for which, out in enumerate((K, V)):
+        np.testing.assert_array_equal(_np(out[0]), pool.held(0, which))
+
+
 def test_write_touches_only_its_places():
     """Storing a row changes that token's bytes and no others: every other token
     of the pool, of shared groups and of other pages too, reads as before."""
