@@ -297,7 +297,7 @@ static BwdWork carve_bwd(const Dims& D, void* ws, size_t* bytes, int** status) {
 
 // ------------------------------------------------------------- 4-bit cache
 
-static mita_status resolve_cache(const mita_cache_params* p, CacheArgs* a) {
+static mita_status resolve_cache(const mita_cache_params* p, bool attention, CacheArgs* a, CachePlan* plan) {
     if (!p) return fail(MITA_ERR_INVALID_ARG, "params is NULL");
     if (p->B < 1 || p->H < 1 || p->H_kv < 1 || p->T < 1) return fail(MITA_ERR_INVALID_ARG, "B, H, H_kv, T must be >= 1");
     if (p->H % p->H_kv) return fail(MITA_ERR_INVALID_ARG, "H must be a multiple of H_kv");
@@ -322,12 +322,17 @@ static mita_status resolve_cache(const mita_cache_params* p, CacheArgs* a) {
     a->n_pages = p->n_pages; a->cols = p->max_pages;
     a->causal = (p->flags & MITA_FLAG_CAUSAL) != 0;
     a->scale = p->scale > 0.0f ? p->scale : 1.0f / sqrtf((float)p->d);
-    if (!cache_attn_plan(*a, p->d, p->dtype, p->flags).fits)
-        return fail(MITA_ERR_UNSUPPORTED, "too many rows and tokens for one call");
+    // Only the attention counts rows times tokens. Rows that no sequence has room for are
+    // padding, and are taken as long as it can count those too.
+    *plan = cache_attn_plan(*a, p->d, p->dtype, p->flags);
+    if (!plan->fits && (attention || p->T > p->max_pages * p->page))
+        return fail(MITA_ERR_UNSUPPORTED, "too many rows and tokens for one %s", attention ? "attention call" : "call");
+    if (!plan->fits) plan->parts = plan->pieces = 0;
     return MITA_OK;
 }
 
-// Workspace of the cache calls: the status word, then the attention's partial results.
+// Workspace of the cache calls: the status word, then the attention's partial results
+// (none where it does not take the parameters).
 struct CacheWork {
     int* status;
     CacheParts parts;
@@ -350,18 +355,17 @@ static bool cache_overlap(const mita_cache_params* p, int heads, const void* x, 
     return (a < b ? b - a : a - b) < bytes;
 }
 
-// Common part of the three calls; rows: the tensors in `dtype`.
-static mita_status cache_begin(const mita_cache_params* p, CacheArgs* a, CachePlan* plan, CacheWork* w,
+// Common part of the three calls; r0, r1: the tensors in `dtype`.
+static mita_status cache_begin(const mita_cache_params* p, bool attention, CacheArgs* a, CachePlan* plan, CacheWork* w,
                                const void* r0, const void* r1, const void* cache, const int32_t* table,
                                const int32_t* len, const int32_t* count, const int32_t* exps, void* ws,
                                size_t ws_bytes) {
-    mita_status st = resolve_cache(p, a);
+    mita_status st = resolve_cache(p, attention, a, plan);
     if (st) return st;
     if (!r0 || !aligned16(r0) || !r1 || !aligned16(r1) || !cache || !aligned16(cache))
         return fail(MITA_ERR_INVALID_ARG, "rows and cache must be 16-byte aligned device pointers");
     if (!table || !len || ((uintptr_t)table | (uintptr_t)len | (uintptr_t)count | (uintptr_t)exps) % 4)
         return fail(MITA_ERR_INVALID_ARG, "table and len must be device pointers, and all index arrays 4-byte aligned");
-    *plan = cache_attn_plan(*a, p->d, p->dtype, p->flags);
     size_t need;
     carve_cache(p, *plan, nullptr, &need);
     if (!ws) return fail(MITA_ERR_WORKSPACE, "workspace is NULL");
@@ -631,15 +635,17 @@ int mita_uses_tensor_cores(const mita_params* p) {
 
 size_t mita_cache_size(const mita_cache_params* p) {
     CacheArgs a;
-    if (resolve_cache(p, &a)) return 0;
+    CachePlan plan;
+    if (resolve_cache(p, false, &a, &plan)) return 0;
     return (size_t)p->n_pages * p->H_kv * a.pgroups * (18 * (size_t)p->d);
 }
 
 size_t mita_cache_workspace_size(const mita_cache_params* p) {
     CacheArgs a;
-    if (resolve_cache(p, &a)) return 0;
+    CachePlan plan;
+    if (resolve_cache(p, false, &a, &plan)) return 0;
     size_t bytes;
-    carve_cache(p, cache_attn_plan(a, p->d, p->dtype, p->flags), nullptr, &bytes);
+    carve_cache(p, plan, nullptr, &bytes);
     return bytes;
 }
 
@@ -650,7 +656,7 @@ mita_status mita_cache_write(const mita_cache_params* p, const void* K, const vo
     CacheArgs a;
     CachePlan plan;
     CacheWork w;
-    const mita_status st = cache_begin(p, &a, &plan, &w, K, V, cache, table, len, count, exps, ws, ws_bytes);
+    const mita_status st = cache_begin(p, false, &a, &plan, &w, K, V, cache, table, len, count, exps, ws, ws_bytes);
     if (st) return st;
     MITA_CUDA(launch_cache_rows(a, p->d, p->dtype, true, (void*)K, (void*)V, cache, (cudaStream_t)stream), "cache write");
     prof_mark((cudaStream_t)stream, "");
@@ -664,7 +670,7 @@ mita_status mita_cache_read(const mita_cache_params* p, const void* cache, const
     CacheArgs a;
     CachePlan plan;
     CacheWork w;
-    const mita_status st = cache_begin(p, &a, &plan, &w, K, V, cache, table, len, count, exps, ws, ws_bytes);
+    const mita_status st = cache_begin(p, false, &a, &plan, &w, K, V, cache, table, len, count, exps, ws, ws_bytes);
     if (st) return st;
     if (cache_overlap(p, p->H_kv, K, V)) return fail(MITA_ERR_INVALID_ARG, "K and V must not overlap");
     MITA_CUDA(launch_cache_rows(a, p->d, p->dtype, false, K, V, (void*)cache, (cudaStream_t)stream), "cache read");
@@ -679,7 +685,7 @@ mita_status mita_cache_attention(const mita_cache_params* p, const void* Q, cons
     CacheArgs a;
     CachePlan plan;
     CacheWork w;
-    const mita_status st = cache_begin(p, &a, &plan, &w, Q, O, cache, table, len, count, exps, ws, ws_bytes);
+    const mita_status st = cache_begin(p, true, &a, &plan, &w, Q, O, cache, table, len, count, exps, ws, ws_bytes);
     if (st) return st;
     if (cache_overlap(p, p->H, Q, O)) return fail(MITA_ERR_INVALID_ARG, "O must not overlap Q");
     if ((uintptr_t)lse_out % 4) return fail(MITA_ERR_INVALID_ARG, "lse_out must be 4-byte aligned");

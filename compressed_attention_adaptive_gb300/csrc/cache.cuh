@@ -72,7 +72,7 @@ constexpr int kMaxExp = 60;
 struct CachePlan {
     bool tensor;  // tensor cores, else CUDA cores
     bool tile;    // tcgen05 tiles (cache_tile.cu)
-    bool fits;    // the call's units of work can be counted in 32 bits
+    bool fits;    // the attention's units of work can be counted in 32 bits
     int rows, pieces;
     size_t parts;
 };

@@ -270,7 +270,15 @@ typedef struct {
 } mita_cache_params;
 
 /* Bytes of the pool, and of device workspace that each of the three calls
- * needs; 0 if `p` is invalid. The workspace does not depend on the lengths. */
+ * needs; 0 if `p` is invalid. The workspace does not depend on the lengths.
+ *
+ * Attention counts its work in 32 bits: with R rows to a tile (8, 16, 32 or 64,
+ * the fewest that hold T * H / H_kv or else the most: 16 for float32, 32 for
+ * bf16 with d = 64, 64 with d = 128; with MITA_FLAG_SIMT 1 or 4),
+ *   B * H_kv * ceil(T * H / H_kv / R) * (ceil(max_pages * page / 128) + 4) < 2^31,
+ * else it is MITA_ERR_UNSUPPORTED (a prompt is attended in parts then). Storing and reading
+ * have no such limit for T <= max_pages * page; for parameters that only they take
+ * the workspace is what they need. */
 size_t mita_cache_size(const mita_cache_params* p);
 size_t mita_cache_workspace_size(const mita_cache_params* p);
 

@@ -49,6 +49,26 @@ def test_invalid_parameters(lib, bad, status):
     assert lib.mita_last_error()
 
 
+@pytest.mark.parametrize("kw", [
+    dict(B=1, H=8, H_kv=8, T=1 << 20, d=64, n_pages=16384, max_pages=16384),
+    dict(B=1, H=16, H_kv=16, T=1 << 20, n_pages=16384, max_pages=16384),
+    dict(B=1, H=4, H_kv=4, T=1 << 20, n_pages=16384, max_pages=16384, dtype=mita.F32),
+    dict(B=32, H=8, H_kv=8, T=131072, d=64, n_pages=65536, max_pages=2048, dtype=mita.F32),
+])
+def test_long_prompts_are_stored_whole(lib, kw):
+    """The attention counts rows times tokens, storing and reading do not."""
+    p = _p(**kw)
+    c, f, odd = ctypes.byref(p.c()), ctypes.c_void_p(1 << 20), ctypes.c_void_p((1 << 20) + 8)
+    assert mita.mita_cache_size(p) == p.pool_bytes
+    need = mita.mita_cache_workspace_size(p)
+    assert 0 < need <= 4096  # no partial results
+    for n, k, status in ((need - 1, f, 3), (need, odd, 1)):  # past the parameters, to the checks behind them
+        assert lib.mita_cache_write(c, k, f, f, f, f, None, None, f, n, None) == status
+        assert lib.mita_cache_read(c, f, f, f, None, None, k, f, f, n, None) == status
+    assert lib.mita_cache_attention(c, f, f, f, f, None, None, f, None, f, 1 << 60, None) == 2
+    assert b"attention" in lib.mita_last_error()
+
+
 def test_null_params(lib):
     f = ctypes.c_void_p(1 << 20)
     assert lib.mita_cache_size(None) == 0

@@ -371,6 +371,41 @@ def test_pool_past_32_bits():
             assert torch.allclose(O.float(), O2.float(), rtol=2 ** -6, atol=2 ** -8)
 
 
+def test_a_prompt_too_long_for_one_attention_call():
+    """A million tokens stored and read back in one call each; attention takes as many
+    tokens, but not as many rows at once."""
+    import torch
+    import compressed_attention_adaptive_gb300 as mita
+    n, H, d, page = 1 << 20, 8, 64, 64
+    p = mita.CacheParams(1, H, H, n, d, page, n // page, n // page)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    K, V = (torch.randn((1, H, n, d), generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    cache = torch.zeros(mita.mita_cache_size(p), dtype=torch.uint8, device="cuda")
+    table = torch.randperm(n // page, generator=g, device="cuda").to(torch.int32).view(1, -1)
+    lens, ws = torch.tensor([n], dtype=torch.int32, device="cuda"), mita.cache_workspace(p)
+    mita.mita_cache_write(p, K, V, cache, table, lens, ws)
+    mita.mita_device_status(ws)
+    outs = [torch.zeros_like(K) for _ in range(2)]
+    mita.mita_cache_read(p, cache, table, lens, *outs, ws)
+    mita.mita_device_status(ws)
+    at = torch.cat([torch.arange(40), torch.randint(0, n, (2000,), generator=torch.Generator().manual_seed(1)),
+                    torch.arange(n - 40, n)]).cuda()
+    for X, out in zip((K, V), outs):
+        np.testing.assert_array_equal(_np(out[0, :, at]), ocache.quantise(_np(X[0, :, at])))
+    with pytest.raises(mita.MitaError) as err:
+        mita.mita_cache_attention(p, K, cache, table, lens, torch.empty_like(K), ws)
+    assert err.value.status == 2
+    one = mita.CacheParams(1, H, H, 1, d, page, n // page, n // page)
+    q, o = K[:, :, -1:].contiguous(), torch.zeros((1, H, 1, d), dtype=torch.bfloat16, device="cuda")
+    w = mita.cache_workspace(one)
+    mita.mita_cache_attention(one, q, cache, table, lens, o, w)
+    mita.mita_device_status(w)
+    for h in (0, H - 1):
+        k, v, qq = _np(outs[0][0, h]), _np(outs[1][0, h]), _np(q[0, h])
+        ref, _, spread = ocache.attention(qq, k, v, [n], 1 / math.sqrt(d))
+        assert np.all(np.abs(_np(o[0, h]) - ref) <= attention_bound("bf16", True, ref, spread, qq, k, v, [n], 1 / math.sqrt(d)))
+
+
 def test_tiles_past_32_bits():
     """The same for tiles of 64 rows, whose copies take several groups of a page."""
     import torch
