@@ -323,7 +323,10 @@ __device__ __forceinline__ void query_scale(const CacheArgs& a, int h, int ex, f
 // large that 7 is lost in them. One rounding would leave up to 2^-24 of m.
 __device__ __forceinline__ float score_diff(float z, float f, float m) { return __fadd_rn(__fmul_rn(z, f), -m); }
 
-constexpr float kNoKey = -1.7e38f;  // a row's maximum before it has seen a key: finite, so that differences are
+// A row's maximum before it has seen a key: finite, so that differences to it are not
+// NaN, and no finite score is below it (one that is far above gives an infinite difference,
+// which moves the maximum like any other).
+constexpr float kNoKey = -3.402823466e38f;
 
 // cache_attn.cu
 cudaError_t set_smem_once(const void* f, int bytes, std::atomic<unsigned long long>* done);

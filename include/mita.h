@@ -299,7 +299,8 @@ mita_status mita_cache_read(const mita_cache_params* p, const void* cache, const
  * to its own position (j < len[b] - (count[b] - 1 - t)); a row that sees no key
  * gets zeros. A key that a row does not see has no influence on it, whatever its
  * bytes are, and neither have the call's other rows; a row with a NaN or an
- * infinity that sees a key gets NaN. O: [B, H, T, d] in `dtype`. lse_out (float32 [B, H, T], or NULL):
+ * infinity that sees a key gets NaN. Scores times log2(e) have to be within float32's
+ * range. O: [B, H, T, d] in `dtype`. lse_out (float32 [B, H, T], or NULL):
  * ln sum exp(scale q.k) over the seen keys, -infinity without any, with which the
  * rows can be joined with attention over other keys (mita_forward's shared
  * slots, say). count > len is allowed: rows before the first token see none.

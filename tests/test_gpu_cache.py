@@ -330,6 +330,44 @@ def test_rows_do_not_influence_each_other(dtype, H, d, simt):
         assert np.all(np.abs(_np(O2[b, :, 0]) - mean)[1::4] <= tol[1::4])
 
 
+@pytest.mark.parametrize("dtype,H,d,simt", [("bf16", 4, 128, False), ("bf16", 24, 64, False), ("bf16", 64, 128, False),
+                                            ("f32", 4, 128, False), ("f32", 24, 64, False), ("bf16", 4, 128, True),
+                                            ("f32", 4, 64, True)])
+def test_scores_near_the_lowest_float(dtype, H, d, simt):
+    """Rows all of whose scores lie between the lowest float and half of it see their keys
+    like any other: the keys with the largest score share the weight."""
+    import torch
+
+    def make(rng, shape):
+        K, V = Pool.rows(rng, shape)
+        K[..., :16] = 0
+        K[..., 3] = rng.choice([4.0, 6.0], shape[:-1])
+        K[0, 1, :, 3] = 6.0
+        return K, V
+
+    pool = Pool([700, 33, 1], 2, d, 16, dtype, make=make, seed=17)
+    g = torch.Generator().manual_seed(4)
+    Q = torch.randn((3, H, 2, d), generator=g).to(pool.td).cuda()
+    _, O, L = _attend(pool, H, 2, True, simt=simt, scale=1.0, q=Q)
+    low = Q.clone()
+    low[:, 0::2, 1] = 0
+    low[:, 0::2, 1, 3] = -3.7e37  # -2.1e38 and -3.2e38 in log2 units
+    _, O2, L2 = _attend(pool, H, 2, True, simt=simt, scale=1.0, q=low)
+    assert torch.equal(O2[:, 1::2], O[:, 1::2]) and torch.equal(O2[:, :, 0], O[:, :, 0])
+    assert torch.equal(L2[:, 1::2], L[:, 1::2]) and torch.equal(L2[:, :, 0], L[:, :, 0])
+    u = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    for b, n in enumerate(pool.lens):
+        for h in range(0, H, 2):
+            k, v = (pool.held(b, w)[h // (H // 2)] for w in (0, 1))
+            z = k[:, 3] * float(low[b, h, 1, 3])
+            best = z == z.max()
+            mean, spread = v[best].mean(0), np.abs(v[best]).mean(0)
+            # equal weights round alike; chains of fp32 additions and one quotient
+            assert np.all(np.abs(_np(O2[b, h, 1]) - mean) <= u * np.abs(mean) + (n / 16 + 70) * 2.0 ** -23 * spread)
+            # scale, log2(e) and ln(2) rounded, and the products
+            assert abs(float(L2[b, h, 1]) / (z.max() + math.log(best.sum())) - 1) <= 8 * 2.0 ** -24
+
+
 @pytest.mark.parametrize("H", [8, 64])
 def test_repeated_calls_are_bit_equal_and_lse_is_optional(H):
     import torch
