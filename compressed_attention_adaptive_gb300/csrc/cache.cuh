@@ -92,10 +92,10 @@ CachePlan cache_attn_plan(const CacheArgs& a, int d, int dtype, unsigned flags);
 cudaError_t launch_cache_attn(const CacheArgs& a, const CachePlan& p, int d, int dtype, const void* Q,
                               const void* cache, void* O, float* lse, const CacheParts& parts, cudaStream_t st);
 
-__device__ __forceinline__ int cache_len(const CacheArgs& a, int b) {
+__host__ __device__ __forceinline__ int cache_len(const CacheArgs& a, int b) {
     return min(max(a.len[b], 0), a.cols * a.page);
 }
-__device__ __forceinline__ int cache_count(const CacheArgs& a, int b) {
+__host__ __device__ __forceinline__ int cache_count(const CacheArgs& a, int b) {
     return a.count ? min(max(a.count[b], 0), a.T) : a.T;
 }
 __device__ __forceinline__ int cache_exp(const CacheArgs& a, int which, int h) {

@@ -31,7 +31,7 @@ struct AttnOut {
 struct SeqWork {
     int n, count, rows, chunks, items;
 };
-__device__ __forceinline__ SeqWork seq_work(const CacheArgs& a, int b, int rtile) {
+__host__ __device__ __forceinline__ SeqWork seq_work(const CacheArgs& a, int b, int rtile) {
     SeqWork s;
     s.n = cache_len(a, b);
     s.count = cache_count(a, b);
@@ -52,8 +52,8 @@ constexpr int kExtra = 2, kTileExtra = 4, kFew = 8;
 // The line of units, cut into `pieces` pieces that differ by one unit at most.
 struct Line {
     int pieces, q, r, extra, total;
-    __device__ __forceinline__ int at(int c) const { return c * q + min(c, r); }
-    __device__ __forceinline__ int piece_of(int x) const {
+    __host__ __device__ __forceinline__ int at(int c) const { return c * q + min(c, r); }
+    __host__ __device__ __forceinline__ int piece_of(int x) const {
         const int head = r * (q + 1);
         return x < head ? x / (q + 1) : r + (x - head) / q;
     }
@@ -124,15 +124,28 @@ __device__ __forceinline__ void scan_line(const CacheArgs& a, int rtile, int ext
     const int before = (int)(chunks0 + items0 * l.extra) + warp_scan(share, lane) - share;
     if (s0 < s1) at(l, s0, s1, first, before, share);
 }
-// The sequence of [s0, ..) whose share holds unit w, with its work (first that of s0) and
-// the units before it.
-__device__ __forceinline__ int find_unit(const CacheArgs& a, const Line& l, int rtile, int w, int s0, int* before, SeqWork* sw) {
+// A sequence may be read more than once in a call. Lengths that change meanwhile leave the
+// results undefined, but no search goes past the sequences and no part past the pieces.
+//
+// The sequence of [s0, s1) whose share holds unit w, with its work (first that of s0) and
+// the units before it; -1 if it is none of them.
+__host__ __device__ __forceinline__ int find_unit(const CacheArgs& a, const Line& l, int rtile, int w, int s0, int s1,
+                                                  int* before, SeqWork* sw) {
     for (;;) {
         const int share = sw->items * (sw->chunks + l.extra);
         if (w < *before + share) return s0;
         *before += share;
-        *sw = seq_work(a, ++s0, rtile);
+        if (++s0 >= s1) return -1;
+        *sw = seq_work(a, s0, rtile);
     }
+}
+// The pieces of item j of a sequence with `before` units before it: the first and their
+// number, 0 if the item is not on the line.
+__host__ __device__ __forceinline__ int item_pieces(const Line& l, const SeqWork& sw, int before, int j, int* piece) {
+    const int first = before + j * (sw.chunks + l.extra) + l.extra, last = first + sw.chunks - 1;
+    if (last >= l.total) return 0;
+    *piece = l.piece_of(first);
+    return l.piece_of(last) - *piece + 1;
 }
 
 // One block's part of an item.
@@ -195,11 +208,12 @@ template <int RT, int EXTRA = kExtra> struct Walk {
     }
     __device__ __forceinline__ bool begin(const CacheArgs& a, int piece, int max_pieces, LineScan& sums) {
         if (threadIdx.x == 0) more = false;
-        scan_line(a, RT, EXTRA, max_pieces, sums, [&](const Line& l, int s0, int, SeqWork first, int before0, int share) {
+        scan_line(a, RT, EXTRA, max_pieces, sums, [&](const Line& l, int s0, int s1, SeqWork first, int before0, int share) {
             if (piece >= l.pieces) return;
             const int w0 = l.at(piece);
             if (w0 < before0 || w0 >= before0 + share) return;
-            b = find_unit(a, l, RT, w0, s0, &before0, &first);
+            b = find_unit(a, l, RT, w0, s0, s1, &before0, &first);
+            if (b < 0) return;
             line = l;
             w = w0;
             w_end = l.at(piece + 1);
@@ -257,11 +271,13 @@ __device__ __forceinline__ void find_cut(const CacheArgs& a, const AttnOut& out,
             if (i + 1 >= l.pieces) return;
             const int w = l.at(i + 1);  // the first unit behind the piece
             if (w < before || w >= before + share) return;
-            b = find_unit(a, l, out.rows, w, s0, &before, &sw);
+            b = find_unit(a, l, out.rows, w, s0, s1, &before, &sw);
+            if (b < 0) return;
             j = (w - before) / (sw.chunks + l.extra);
         }
-        const int first = before + j * (sw.chunks + l.extra) + l.extra, last = first + sw.chunks - 1, tile = j / a.Hkv;
-        const int piece = l.piece_of(first), parts = l.piece_of(last) - piece + 1;
+        const int tile = j / a.Hkv;
+        int piece;
+        const int parts = item_pieces(l, sw, before, j, &piece);
         if (parts < 2 || (!by_item && piece != i)) return;
         c.b = b;
         c.h = j - tile * a.Hkv;

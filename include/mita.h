@@ -250,7 +250,8 @@ mita_status mita_forward_static(const mita_params* p, const void* Q, const void*
  * padding: not read, and left as they were in outputs. exps int32 [2][H_kv]
  * (first the keys' exponents, then the values'; |e| <= 60), or NULL: all zero.
  * All four arrays are device memory and are read when the stream gets there, so
- * a captured call follows them. The same arrays serve all three calls: write a
+ * a captured call follows them; they stay as they are until it has ended (the results are
+ * undefined otherwise). The same arrays serve all three calls: write a
  * step's rows, then attend.
  *
  * Out of range (a page outside [0, n_pages) among those that the call uses, a
