@@ -304,7 +304,8 @@ mita_status mita_cache_read(const mita_cache_params* p, const void* cache, const
  * range. O: [B, H, T, d] in `dtype`. lse_out (float32 [B, H, T], or NULL):
  * ln sum exp(scale q.k) over the seen keys, -infinity without any, with which the
  * rows can be joined with attention over other keys (mita_forward's shared
- * slots, say). count > len is allowed: rows before the first token see none.
+ * slots, say). count > len is allowed: with MITA_FLAG_CAUSAL rows before the first
+ * token see none, without it every row sees all keys.
  * O must not overlap Q. The same call gives the same bits; how a sequence's keys
  * are divided, and so the last bits, depends on all the call's lengths.
  * Runs on tensor cores, float32 with each number as the sum of two halves (22

@@ -564,6 +564,16 @@ def test_more_rows_than_tokens():
     assert torch.all(O[0, 0, :2] == 0) and torch.all(L[0, 0, :2] == -math.inf)
 
 
+@pytest.mark.parametrize("dtype,H,simt", [("bf16", 1, False), ("bf16", 12, False), ("f32", 1, False), ("bf16", 1, True)])
+def test_more_rows_than_tokens_that_see_all(dtype, H, simt):
+    """Without the causal flag rows have no position: each sees all keys, however many rows there are."""
+    pool = Pool([2, 5, 0], 1, 128, 16, dtype)
+    Q, O, L = _attend(pool, H, 4, False, simt=simt)
+    _check(pool, H, 4, False, Q, O, L, simt=simt, label="more rows than tokens, all seen")
+    assert (O[0] != 0).any(-1).all() and L[0].isfinite().all()
+    assert (O[2] == 0).all() and (L[2] == -math.inf).all()
+
+
 def test_binding_refuses():
     """Shapes, types and devices that the pointers of the C side cannot show."""
     import torch
