@@ -258,7 +258,11 @@ mita_status mita_forward_static(const mita_params* p, const void* Q, const void*
  * length outside [0, max_pages * page], a count outside [0, T], for write and
  * read also count > len, an exponent outside +-60): the status word of `ws`
  * becomes MITA_ERR_BOUNDS, the places concerned are neither read nor written,
- * and what is computed from them is undefined. Every call writes the word. */
+ * and what is computed from them is undefined. Every call writes the word, which
+ * so holds the last call's verdict: a write's is lost if another call on the same
+ * workspace follows before mita_device_status(). (Attention finds a bad page, length, count
+ * or exponent again; count > len is no error there, so the rows that the write left out for
+ * it then go unreported.) To read both, give the two calls a workspace each. */
 typedef struct {
     int B, H, H_kv;  /* sequences, query heads, cache heads (H % H_kv == 0)     */
     int T, d;        /* rows per sequence and call; head dim: 64 or 128         */

@@ -564,6 +564,28 @@ def test_more_rows_than_tokens():
     assert torch.all(O[0, 0, :2] == 0) and torch.all(L[0, 0, :2] == -math.inf)
 
 
+def test_the_status_word_is_the_last_calls():
+    """A write's verdict is there until another call on its workspace: a workspace for each
+    call keeps it, one for both has the attention's."""
+    import torch
+    import compressed_attention_adaptive_gb300 as mita
+    pool = Pool([2, 5], 1, 64, 16, "bf16", T=4)
+    K = torch.zeros((2, 1, 4, 64), dtype=torch.bfloat16, device="cuda")
+    O, other = torch.zeros_like(K), mita.cache_workspace(pool.p)
+
+    def step(ws):  # stores four rows of a sequence of two, which the attention may have
+        mita.mita_cache_write(pool.p, K, K, pool.cache, pool.table, pool.len_t, pool.ws)
+        mita.mita_cache_attention(pool.p, K, pool.cache, pool.table, pool.len_t, O, ws)
+
+    step(other)
+    mita.mita_device_status(other)
+    with pytest.raises(mita.MitaError) as err:
+        mita.mita_device_status(pool.ws)
+    assert err.value.status == 6
+    step(pool.ws)
+    mita.mita_device_status(pool.ws)
+
+
 @pytest.mark.parametrize("dtype,H,simt", [("bf16", 1, False), ("bf16", 12, False), ("f32", 1, False), ("bf16", 1, True)])
 def test_more_rows_than_tokens_that_see_all(dtype, H, simt):
     """Without the causal flag rows have no position: each sees all keys, however many rows there are."""
