@@ -331,6 +331,7 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float x, float y, float
 }
 
 constexpr int kStages = 2;
+constexpr float kLow = 4096.0f;  // lo is at most 8 where its number is below 2^15
 // Blocks per SM that the registers allow without spills (but 4 to 8 registers of float32
 // rows of 128 channels, at a segment's start). (16 rows of 128 channels: 3 blocks 48.6 us,
 // 4 at 128 registers 51.2; 16 rows of 64: 33.0 and 30.9.)
@@ -370,9 +371,14 @@ template <typename T, int D, int NR> constexpr int mma_smem() {
 //
 // float32 rows are each two halves, x = hi + lo with lo = x - hi rounded (22 bits and
 // a sign, 2^-23 of x), p likewise: two products where bf16 has one, with the same
-// exact keys and values. The products are summed in fp32 by steps of 16 tokens
-// and by ordinary additions from there. (8 x 12 heads of 16384 tokens, d = 64: 38 us, on
-// CUDA cores 52.)
+// exact keys and values. The products are summed in fp32 by steps of 16 or 32 tokens
+// and by ordinary additions from there. The lower halves are held kLow times as large, and m
+// starts 11 below a maximum, so that p keeps its 22 bits down to 2^-26 of the maximum and is
+// off by 2^-48 of it below. (Unscaled, weights 2^-24 of the largest had 8 bits and those below
+// 2^-32 none: 1e-4 of the result where a key of that weight has no value. The scale takes a
+// second sum: over lengths around 16384, 8 x 12 heads, d = 64, 37.0 us against 35.7; 2 x 16 heads
+// of about 30,000, d = 128, 40.6 against 40.3; with 12 rows 26.0 against 25.0. On CUDA cores the first
+// case takes 52.)
 //
 // The next segment is found while a segment's first codes are on their way, and its own
 // first copies are issued before the warps' sums are joined (8 x 12 heads of 16384 tokens in
@@ -494,7 +500,7 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
                     const float y1 = __uint_as_float(F ? x[(4 * ks + 2 * e + 1) % (4 * QW)] : x[2 * ks + e] & 0xffff0000u) * up;
                     hi[e] = pack_half2(y0, y1);
                     const float2 h = half2_to_float2(hi[e]);
-                    lo[e] = pack_half2(y0 - h.x, y1 - h.y);
+                    lo[e] = pack_half2((y0 - h.x) * kLow, (y1 - h.y) * kLow);
                 }
                 qs[(ks * NR + warp) * 32 + lane] = make_uint2(hi[0], hi[1]);
                 if (F) qs[((KS + ks) * NR + warp) * 32 + lane] = make_uint2(lo[0], lo[1]);
@@ -622,7 +628,7 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
 #pragma unroll
                         for (int x = 0; x < GP; ++x)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) z[j][x][e] += zl[j % NL][x][e];
+                            for (int e = 0; e < 4; ++e) z[j][x][e] = fmaf(zl[j % NL][x][e], 1 / kLow, z[j][x][e]);
                 }
                 const bool edge = base + 16 * GP > low;  // some row does not see all of these tokens
                 if (edge) {
@@ -657,7 +663,7 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
 #pragma unroll
                             for (int x = 4; x < 32; x <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
                             // (a row's own scores move it, not another's)
-                            const float mn = score_diff(v, zf[j][e], m[j][e]) > 15.0f ? score_diff(v, zf[j][e], 7.0f) : m[j][e];
+                            const float mn = score_diff(v, zf[j][e], m[j][e]) > 15.0f ? score_diff(v, zf[j][e], F ? 11.0f : 7.0f) : m[j][e];
                             const float f = ex2(m[j][e] - mn);
                             m[j][e] = mn;
                             l[j][e] *= f;
@@ -687,84 +693,102 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
                             p[j][x][e] = transpose8(h2);
                             if (F) {
                                 const float2 hf = half2_to_float2(h2);
-                                pl[j % NL][x][e] = transpose8(pack_half2(p0 - hf.x, p1 - hf.y));
+                                pl[j % NL][x][e] = transpose8(pack_half2(fmaf(hf.x, -kLow, p0 * kLow), fmaf(hf.y, -kLow, p1 * kLow)));
                             }
                         }
+                // groups whose products with V are summed before they go to a float row's o
+                constexpr int GS = F ? GP : 1;
 #pragma unroll
-                for (int gi = 0; gi < GP; ++gi) {
-                    const uint8_t* vb = st + (h + gi) * L::kBytes;
-                    uint32_t sb = *reinterpret_cast<const uint32_t*>(vb + L::kVs + (D == 128 ? g : g >> 1) * 16 + t4 * 4);
-                    if (edge) {
-                        // Nothing of a token that a row does not see may reach it: bytes of tokens
-                        // that no row sees are made zero here; NaN of a token that only some rows
-                        // see is taken out of the product and put into the rows that see it.
-                        const int tok = base + 16 * gi + 2 * t4;
-                        uint32_t nan = 0;
+                for (int g0 = 0; g0 < GP; g0 += GS) {
+                    uint32_t s0[GS], s1[GS], vw[GS][4][D / 64];
+#pragma unroll
+                    for (int gs = 0; gs < GS; ++gs) {
+                        const int gi = g0 + gs;
+                        const uint8_t* vb = st + (h + gi) * L::kBytes;
+                        uint32_t sb = *reinterpret_cast<const uint32_t*>(vb + L::kVs + (D == 128 ? g : g >> 1) * 16 + t4 * 4);
+                        if (edge) {
+                            // Nothing of a token that a row does not see may reach it: bytes of tokens
+                            // that no row sees are made zero here; NaN of a token that only some rows
+                            // see is taken out of the product and put into the rows that see it.
+                            const int tok = base + 16 * gi + 2 * t4;
+                            uint32_t nan = 0;
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const uint32_t byte = 0xffu << (8 * x);
+                                if (tok + 8 * (x >> 1) + (x & 1) >= top) sb &= ~byte;
+                                if ((sb >> (8 * x) & 0x7f) == 0x7f) nan |= byte;
+                            }
+                            if (__any_sync(0xffffffffu, nan != 0)) {
+                                sb &= ~nan;
+                                const uint32_t one = 0x3c003c00u;  // (1, 1) in halves
+                                const uint32_t a0 = __byte_perm(nan, 0, 0x1100) & one, a2 = __byte_perm(nan, 0, 0x3322) & one;
+#pragma unroll
+                                for (int j = 0; j < NR; ++j) {
+                                    const int lim = slim[8 * j + g];
+                                    uint32_t see[2];
+#pragma unroll
+                                    for (int x = 0; x < 2; ++x)
+                                        see[x] = (tok + 8 * x < lim ? 0x3c00u : 0u) | (tok + 8 * x + 1 < lim ? 0x3c000000u : 0u);
+                                    float hit[4];
+                                    mma_f16_first(hit, a0, a0, a2, a2, see[0], see[1]);
+#pragma unroll
+                                    for (int x = 0; x < NT / 2; ++x)
+#pragma unroll
+                                        for (int e = 0; e < 4; ++e)
+                                            if (hit[e] > 0.0f) o[j][x][e] = __int_as_float(0x7fc00000);
+                                }
+                            }
+                        }
+                        s0[gs] = e4m3x2_to_half2(sb & 0xffff);
+                        s1[gs] = e4m3x2_to_half2(sb >> 16);
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            const uint32_t byte = 0xffu << (8 * x);
-                            if (tok + 8 * (x >> 1) + (x & 1) >= top) sb &= ~byte;
-                            if ((sb >> (8 * x) & 0x7f) == 0x7f) nan |= byte;
-                        }
-                        if (__any_sync(0xffffffffu, nan != 0)) {
-                            sb &= ~nan;
-                            const uint32_t one = 0x3c003c00u;  // (1, 1) in halves
-                            const uint32_t a0 = __byte_perm(nan, 0, 0x1100) & one, a2 = __byte_perm(nan, 0, 0x3322) & one;
-#pragma unroll
-                            for (int j = 0; j < NR; ++j) {
-                                const int lim = slim[8 * j + g];
-                                uint32_t see[2];
-#pragma unroll
-                                for (int x = 0; x < 2; ++x)
-                                    see[x] = (tok + 8 * x < lim ? 0x3c00u : 0u) | (tok + 8 * x + 1 < lim ? 0x3c000000u : 0u);
-                                float hit[4];
-                                mma_f16_first(hit, a0, a0, a2, a2, see[0], see[1]);
-#pragma unroll
-                                for (int x = 0; x < NT / 2; ++x)
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e)
-                                        if (hit[e] > 0.0f) o[j][x][e] = __int_as_float(0x7fc00000);
+                            const uint8_t* vr = vb + L::v_chunk(t4 + 4 * x, g);
+                            if (D == 128) {
+                                const uint2 v = *reinterpret_cast<const uint2*>(vr);
+                                vw[gs][x][0] = v.x; vw[gs][x][D / 64 - 1] = v.y;
+                            } else {
+                                vw[gs][x][0] = *reinterpret_cast<const uint32_t*>(vr);
                             }
-                        }
-                    }
-                    const uint32_t s0 = e4m3x2_to_half2(sb & 0xffff), s1 = e4m3x2_to_half2(sb >> 16);
-                    uint32_t vw[4][D / 64];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const uint8_t* vr = vb + L::v_chunk(t4 + 4 * x, g);
-                        if (D == 128) {
-                            const uint2 v = *reinterpret_cast<const uint2*>(vr);
-                            vw[x][0] = v.x; vw[x][D / 64 - 1] = v.y;
-                        } else {
-                            vw[x][0] = *reinterpret_cast<const uint32_t*>(vr);
                         }
                     }
 #pragma unroll
                     for (int wi = 0; wi < D / 64; ++wi) {
                         // a byte of both tokens of a pair: even channels, then odd ones
                         constexpr uint32_t lo = 0x0f0f0f0fu;
-                        uint32_t v8[2][2][4];  // [tokens 8 x + 2 t4 ..][parity of the channel]
+                        uint32_t v8[GS][2][2][4];  // [group][tokens 8 x + 2 t4 ..][parity of the channel]
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const uint32_t u0 = vw[2 * x][wi], u1 = vw[2 * x + 1][wi];
-                            e2m1x8_to_half2((u0 & lo) | ((u1 << 4) & ~lo), v8[x][0]);
-                            e2m1x8_to_half2(((u0 >> 4) & lo) | (u1 & ~lo), v8[x][1]);
-                        }
+                        for (int gs = 0; gs < GS; ++gs)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const uint32_t u0 = vw[gs][2 * x][wi], u1 = vw[gs][2 * x + 1][wi];
+                                e2m1x8_to_half2((u0 & lo) | ((u1 << 4) & ~lo), v8[gs][x][0]);
+                                e2m1x8_to_half2(((u0 >> 4) & lo) | (u1 & ~lo), v8[gs][x][1]);
+                            }
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            const uint32_t a0 = hmul2(v8[0][0][x], s0), a1 = hmul2(v8[0][1][x], s0);
-                            const uint32_t a2 = hmul2(v8[1][0][x], s1), a3 = hmul2(v8[1][1][x], s1);
+                            uint32_t av[GS][4];
+#pragma unroll
+                            for (int gs = 0; gs < GS; ++gs)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    av[gs][e] = hmul2(v8[gs][e >> 1][e & 1][x], e < 2 ? s0[gs] : s1[gs]);
 #pragma unroll
                             for (int j = 0; j < NR; ++j) {
                                 if (!F) {
-                                    mma_f16(o[j][4 * wi + x], a0, a1, a2, a3, p[j][gi][0], p[j][gi][1]);
+                                    mma_f16(o[j][4 * wi + x], av[0][0], av[0][1], av[0][2], av[0][3], p[j][g0][0], p[j][g0][1]);
                                     continue;
                                 }
-                                float c[4];
-                                mma_f16_first(c, a0, a1, a2, a3, pl[j % NL][gi][0], pl[j % NL][gi][1]);
-                                mma_f16(c, a0, a1, a2, a3, p[j][gi][0], p[j][gi][1]);
+                                float c[4], cl[4];
+                                mma_f16_first(cl, av[0][0], av[0][1], av[0][2], av[0][3], pl[j % NL][g0][0], pl[j % NL][g0][1]);
+                                mma_f16_first(c, av[0][0], av[0][1], av[0][2], av[0][3], p[j][g0][0], p[j][g0][1]);
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) o[j][4 * wi + x][e] += c[e];
+                                for (int gs = 1; gs < GS; ++gs) {
+                                    mma_f16(cl, av[gs][0], av[gs][1], av[gs][2], av[gs][3], pl[j % NL][gs][0], pl[j % NL][gs][1]);
+                                    mma_f16(c, av[gs][0], av[gs][1], av[gs][2], av[gs][3], p[j][gs][0], p[j][gs][1]);
+                                }
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) o[j][4 * wi + x][e] += fmaf(cl[e], 1 / kLow, c[e]);
                             }
                         }
                     }

@@ -368,6 +368,35 @@ def test_scores_near_the_lowest_float(dtype, H, d, simt):
             assert abs(float(L2[b, h, 1]) / (z.max() + math.log(best.sum())) - 1) <= 8 * 2.0 ** -24
 
 
+@pytest.mark.parametrize("simt", [False, True], ids=["", "simt"])
+@pytest.mark.parametrize("d,T", [(64, 1), (128, 1), (64, 9), (128, 12)])
+@pytest.mark.parametrize("gap", [24, 30, 36])
+def test_float32_weights_far_below_the_largest(d, T, gap, simt):
+    """A first key with 2^gap times the weight of the others and no values, as models have
+    it: the result is what the others give, to float32."""
+
+    def make(rng, shape):
+        K, V = Pool.rows(rng, shape)
+        K[..., :16] = 0
+        K[:, :, 0, 0] = 6
+        V[:, :, 0] = 0
+        return K, V
+
+    import torch
+    pool = Pool([100, 4096, 700], 2, d, 64, "f32", make=make, seed=gap)
+    Q = 0.1 * torch.randn((3, 2, T, d), generator=torch.Generator().manual_seed(gap))
+    Q[..., 0] = gap * math.log(2) / 6
+    Q = Q.cuda()
+    _, O, L = _attend(pool, 2, T, False, simt=simt, scale=1.0, q=Q)
+    for b, n in enumerate(pool.lens):
+        for h in range(2):
+            k, v, q = pool.held(b, 0)[h], pool.held(b, 1)[h], _np(Q[b, h])
+            ref, lse, spread = ocache.attention(q, k, v, [n] * T, 1.0)
+            # and 2^-48 of the largest weight where lower halves end
+            bound = attention_bound("f32", False, ref, spread, q, k, v, [n] * T, 1.0) + 2.0 ** -48 * np.abs(v).sum(0)
+            assert np.all(np.abs(_np(O[b, h]) - ref) <= bound), float((np.abs(_np(O[b, h]) - ref) / bound).max())
+
+
 @pytest.mark.parametrize("H", [8, 64])
 def test_repeated_calls_are_bit_equal_and_lse_is_optional(H):
     import torch
