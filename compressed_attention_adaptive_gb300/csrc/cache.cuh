@@ -106,7 +106,7 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) <
 
 // Group number of sequence b's 16 tokens from 16 * gi on in head h, or -1 when
 // the table names no page of the pool (the kernels record it).
-__device__ __forceinline__ int cache_group(const CacheArgs& a, int b, int h, int gi) {
+__host__ __device__ __forceinline__ int cache_group(const CacheArgs& a, int b, int h, int gi) {
     const int col = gi / a.pgroups;
     const int pg = a.table[(long long)b * a.cols + col];
     if ((unsigned)pg >= (unsigned)a.n_pages) return -1;

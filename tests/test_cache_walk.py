@@ -102,7 +102,41 @@ static void changed() {
     CHECK(item_pieces(none, seq_work(a, 0, 8), 0, 0, &piece) == 0);
 }
 
+// Whatever the arrays hold: lengths and counts end in range, and a group is one of the pool's or none.
+static void any_numbers() {
+    const int odd[] = {0, 1, -1, 4, 5, 63, 64, 65, 1 << 30, 2147483647, -2147483647 - 1, 127, 128, 200};
+    const int k = sizeof odd / sizeof odd[0];
+    for (int page = 16; page <= 48; page += 16) {
+        CacheArgs a{};
+        a.B = k;
+        a.Hkv = 3;
+        a.T = 5;
+        a.page = page;
+        a.pgroups = page / 16;
+        a.n_pages = 5;
+        a.cols = 4;
+        std::vector<int> table;
+        for (int i = 0; i < k * a.cols; ++i) table.push_back(odd[i * 5 % k]);
+        a.table = table.data();
+        a.len = a.count = odd;
+        for (int b = 0; b < k; ++b) {
+            const int n = cache_len(a, b), c = cache_count(a, b);
+            CHECK(n >= 0 && n <= a.cols * page && (n == odd[b]) == (odd[b] >= 0 && odd[b] <= a.cols * page));
+            CHECK(c >= 0 && c <= a.T && (c == odd[b]) == (odd[b] >= 0 && odd[b] <= a.T));
+            for (int gi = 0; gi * 16 < a.cols * page; ++gi)
+                for (int h = 0; h < a.Hkv; ++h) {
+                    const int pg = table[b * a.cols + gi / a.pgroups], g = cache_group(a, b, h, gi);
+                    if (pg < 0 || pg >= a.n_pages)
+                        CHECK(g == -1);
+                    else
+                        CHECK(g == (pg * a.Hkv + h) * a.pgroups + gi % a.pgroups);
+                }
+        }
+    }
+}
+
 int main() {
+    any_numbers();
     for (int i = 0; i < 300; ++i) counted(i);
     changed();
     if (!failed) printf("ok\n");

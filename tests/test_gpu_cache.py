@@ -573,6 +573,67 @@ def test_out_of_range_is_reported(what):
     assert torch.equal(O, ref[1])
 
 
+FORMS = [("bf16", 128, 1, 1), ("bf16", 64, 1, 5), ("bf16", 128, 6, 2), ("bf16", 64, 3, 10), ("bf16", 128, 32, 2),
+         ("bf16", 128, 5, 40), ("f32", 128, 1, 1), ("f32", 64, 6, 3)]  # dtype, d, query heads a cache head, T
+
+
+@pytest.mark.parametrize("simt", [False, True], ids=["", "simt"])
+@pytest.mark.parametrize("form", FORMS, ids=lambda f: "%s_d%d_G%d_T%d" % f)
+def test_out_of_range_in_every_form(form, simt):
+    """Each form of the attention reports each kind of number that is out of range, leaves
+    the sequences and heads that have none right, and is clean afterwards."""
+    import torch
+    import compressed_attention_adaptive_gb300 as mita
+    dtype, d, G, T = form
+    lens, Hkv, page = [700, 333, 450], 2, 48
+    H = G * Hkv
+    pool = Pool(lens, Hkv, d, page, dtype, seed=9, T=T, H=H, exps=np.array([[1, -2], [0, 3]]))
+    flags = mita.FLAG_CAUSAL | (mita.FLAG_SIMT if simt else 0)
+    p = mita.CacheParams(3, H, Hkv, T, d, page, pool.n_pages, pool.cols, 0.0, flags, pool.p.dtype)
+    Q, O, L = _attend(pool, H, T, True, simt=simt)
+    _check(pool, H, T, True, Q, O, L, simt=simt, label="in range, %s d%d G%d T%d" % form)
+    counts = torch.full((3,), T, dtype=torch.int32, device="cuda")
+    ws = mita.cache_workspace(p)
+    sc = 1.0 / math.sqrt(d)
+
+    def call(table=pool.table, lens=pool.len_t, counts=counts, exps=pool.exps):
+        out, lse = torch.full_like(O, 7.0), torch.full_like(L, 7.0)
+        mita.mita_cache_attention(p, Q, pool.cache, table, lens, out, ws, counts=counts, exps=exps, lse_out=lse)
+        return out, lse
+
+    def with_(t, at, v):
+        t = t.clone()
+        t[at] = v
+        return t
+
+    def bounds(b, h):
+        n, lim = lens[b], [max(0, lens[b] - (T - 1 - t)) for t in range(T)]
+        k, v, q = pool.held(b, 0)[h // G], pool.held(b, 1)[h // G], _np(Q[b, h])
+        ref, _, spread = ocache.attention(q, k, v, lim, sc)
+        off = attention_bound(dtype, dtype == "bf16" and not simt, ref, spread, q, k, v, lim, sc)
+        return ref - off, ref + off
+
+    # the first and the last query head of each cache head
+    right = {(b, h): bounds(b, h) for b in range(3) for h in {0, G - 1, G, H - 1}}
+    # the entry of a page in the middle, of the first and of the last one of sequence 1
+    bad = [("page", dict(table=with_(pool.table, (1, i), v))) for i, v in ((3, pool.n_pages), (0, -1), (6, 2 ** 31 - 1))]
+    bad += [("len", dict(lens=with_(pool.len_t, 1, v))) for v in (pool.cols * page + 1, -1, 2 ** 31 - 1)]
+    bad += [("count", dict(counts=with_(counts, 1, v))) for v in (T + 1, -3)]
+    bad += [("exps", dict(exps=with_(pool.exps, (w, 1), v))) for w, v in ((0, 61), (1, -61))]
+    for what, kw in bad:
+        out, _ = call(**kw)
+        with pytest.raises(mita.MitaError) as err:
+            mita.mita_device_status(ws)
+        assert err.value.status == 6, what
+        for (b, h), (lo, hi) in right.items():
+            if h < G if what == "exps" else b != 1:  # an exponent belongs to a cache head, the rest to sequence 1
+                got = _np(out[b, h])
+                assert np.all((lo <= got) & (got <= hi)), (what, b, h)
+    out, lse = call()
+    mita.mita_device_status(ws)
+    assert torch.equal(out, O) and torch.equal(lse, L)
+
+
 def test_more_rows_than_tokens():
     """count > len: an error for the calls that store and read rows, rows without
     keys for attention."""
