@@ -307,7 +307,8 @@ static mita_status resolve_cache(const mita_cache_params* p, bool attention, Cac
         return fail(MITA_ERR_INVALID_ARG, "page must be a multiple of %d in [%d, 4096]", kGroup, kGroup);
     if (p->n_pages < 1 || p->max_pages < 1) return fail(MITA_ERR_INVALID_ARG, "n_pages, max_pages must be >= 1");
     if (p->dtype != MITA_DTYPE_F32 && p->dtype != MITA_DTYPE_BF16) return fail(MITA_ERR_INVALID_ARG, "bad dtype");
-    if (p->flags & ~(unsigned)(MITA_FLAG_SIMT | MITA_FLAG_CAUSAL)) return fail(MITA_ERR_INVALID_ARG, "unknown flag");
+    if (p->flags & ~(unsigned)(MITA_FLAG_SIMT | MITA_FLAG_CAUSAL | MITA_TESTFLAG_STALL_PRODUCER))
+        return fail(MITA_ERR_INVALID_ARG, "unknown flag");
     if (!(p->scale >= 0.0f) || isinf(p->scale)) return fail(MITA_ERR_INVALID_ARG, "scale must be finite and >= 0");
     if (p->B > 65535) return fail(MITA_ERR_UNSUPPORTED, "B must be <= 65535");
     if ((long long)p->B * p->H > (1LL << 30) || (long long)p->B * p->H * p->T > (1LL << 30))
@@ -321,6 +322,8 @@ static mita_status resolve_cache(const mita_cache_params* p, bool attention, Cac
     a->page = p->page; a->pgroups = p->page / kGroup;
     a->n_pages = p->n_pages; a->cols = p->max_pages;
     a->causal = (p->flags & MITA_FLAG_CAUSAL) != 0;
+    a->stall = (p->flags & MITA_TESTFLAG_STALL_PRODUCER) != 0;
+    a->spin = cache_spin(a->stall);
     a->scale = p->scale > 0.0f ? p->scale : 1.0f / sqrtf((float)p->d);
     // Only the attention counts rows times tokens. Rows that no sequence has room for are
     // padding, and are taken as long as it can count those too.

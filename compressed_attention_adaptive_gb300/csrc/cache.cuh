@@ -60,9 +60,11 @@ struct CacheArgs {
     int page, pgroups;      // tokens and groups per page
     int n_pages, cols;      // pages in the pool, columns of the page table
     int causal;
+    int stall;       // fault test: a signal is left out
     float scale;
     const int *table, *len, *count, *exps;
     int* status;
+    long long spin;  // cycles that a wait takes at most
 };
 
 constexpr int kMaxExp = 60;
@@ -89,6 +91,7 @@ cudaError_t launch_cache_rows(const CacheArgs& a, int d, int dtype, bool write, 
                               cudaStream_t st);
 // cache_attn.cu
 CachePlan cache_attn_plan(const CacheArgs& a, int d, int dtype, unsigned flags);
+long long cache_spin(bool stall);
 cudaError_t launch_cache_attn(const CacheArgs& a, const CachePlan& p, int d, int dtype, const void* Q,
                               const void* cache, void* O, float* lse, const CacheParts& parts, cudaStream_t st);
 

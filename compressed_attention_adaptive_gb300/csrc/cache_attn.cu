@@ -416,7 +416,8 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
     const uint32_t ring_addr = smem_addr(ring);
     uint2* qs = reinterpret_cast<uint2*>(smem + mma_smem<T, D, NR>() - mma_q_bytes<T, D, NR>());
     if (lane == 0) {
-        for (int i = 0; i < ST; ++i) tc::mbar_init(&bars[warp][i], 2);
+        // (fault test: one more signal for the first step of one warp of the call than come)
+        for (int i = 0; i < ST; ++i) tc::mbar_init(&bars[warp][i], a.stall && i + warp + piece == 0 ? 3 : 2);
         tc::fence_mbar_init();
     }
     __shared__ LineScan sums;
@@ -533,12 +534,14 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
         for (int i = 0; i < steps; ++i) {
             __syncwarp();  // the stage that the next copy goes to has been read
             issue(s, i + ST - 1);
-            if (!__all_sync(0xffffffffu, tc::mbar_wait(&bars[warp][take], phase, a.status))) {
-                // give up, but not before the copies in flight have landed (or a second has passed for each)
+            if (!__all_sync(0xffffffffu, tc::mbar_wait(&bars[warp][take], phase, a.status, a.spin))) {
+                // Give up, but not before the copies in flight have landed (or the wait's time has passed
+                // for each). The warp takes part in what the block still does, with sums that mean
+                // nothing, as the status word will say.
                 for (int x = i + 1; x < steps && x < i + ST; ++x) {
                     take = take + 1 == ST ? 0 : take + 1;
                     phase ^= take == 0;
-                    tc::mbar_wait(&bars[warp][take], phase, a.status);
+                    tc::mbar_wait(&bars[warp][take], phase, a.status, a.spin);
                 }
                 dead = true;
                 found |= kFoundTimeout;
@@ -1020,6 +1023,8 @@ CachePlan cache_attn_plan(const CacheArgs& a, int d, int dtype, unsigned flags) 
     p.parts = (size_t)2 * p.pieces * p.rows;
     return p;
 }
+
+long long cache_spin(bool stall) { return stall ? tc::kSpinTest : tc::kSpin; }
 
 template <typename T, int D, int W>
 static cudaError_t join_w(const CacheArgs& a, const AttnOut& o, long long items, cudaStream_t st) {

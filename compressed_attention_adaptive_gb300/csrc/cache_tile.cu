@@ -51,7 +51,6 @@ constexpr int HN = 16;           // rows of a softmax thread
 constexpr int kRaw = 8 * Grp<kD>::kBytes;  // a chunk's codes and scales
 constexpr int kRawStages = 4, kSoftStages = 3;  // of codes; of scores and weights
 constexpr int kEdge = 64;                  // tokens that only some rows of a tile see, at most
-constexpr long long kSpin = 2LL << 30;     // about a second
 
 struct TileSmem {
     static constexpr int kSoft = N / 4, kCopy = kSoft, kIssue = kSoft + 1, kWiden = kSoft + 2;  // warps
@@ -68,24 +67,24 @@ constexpr uint32_t idesc_half(int M, int N, int a_mn, int b_mn) {
 }
 
 // Bounded wait that also ends when another role has given up.
-__device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+__device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, long long lim) {
     if (tc::mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
     while (!tc::mbar_try_wait(bar, parity)) {
         if (*abort_flag) return false;
-        if (clock64() - t0 > kSpin) {
+        if (clock64() - t0 > lim) {
             *abort_flag = 1;
             return false;
         }
     }
     return true;
 }
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-    return __all_sync(0xffffffffu, tile_wait(bar, parity, abort_flag));
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, long long lim) {
+    return __all_sync(0xffffffffu, tile_wait(bar, parity, abort_flag, lim));
 }
 // For what this block has issued to the asynchronous units, whatever the abort flag says.
-__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, int* status) {
-    (void)tc::mbar_wait(bar, parity, status);
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, int* status, long long lim) {
+    (void)tc::mbar_wait(bar, parity, status, lim);
 }
 
 // The four softmax warps with the same rows meet here (barrier 1 + wg), all of them the
@@ -215,7 +214,8 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
     if (warp == S::kIssue) tc::tmem_alloc(&tmem_slot, 512);
     if (tid == 0) {
         for (int i = 0; i < kRawStages; ++i) {
-            tc::mbar_init(&bar.raw_full[i], 1);
+            // (fault test: one more signal for the first chunk of one block than comes)
+            tc::mbar_init(&bar.raw_full[i], a.stall && i + piece == 0 ? 2 : 1);
             tc::mbar_init(&bar.raw_empty[i], 8);
         }
         for (int i = 0; i < 2; ++i) {
@@ -276,7 +276,7 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
             Copy cur = copies(0), nxt = copies(4);
             for (int c = 0; c < nc; ++c) {
                 const int t = done + c, st = t % kRawStages;
-                if (!warp_wait(&bar.raw_empty[st], ((t / kRawStages) & 1) ^ 1, abort_v)) break;
+                if (!warp_wait(&bar.raw_empty[st], ((t / kRawStages) & 1) ^ 1, abort_v, a.spin)) break;
                 const bool mine = (lane >> 3) == (c & 3);
                 const uint32_t bytes = __reduce_add_sync(0xffffffffu, mine ? cur.bytes : 0u);
                 if (elect_one()) tc::mbar_expect_tx(&bar.raw_full[st], bytes);
@@ -296,10 +296,10 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
             // weights over the next scores to their weights, which is several waits long, is gone
             // over once for three chunks.
             constexpr uint32_t idS = idesc_half(128, N, 0, 0), idO = idesc_half(128, N, 0, 1);
-            bool ok = warp_wait(&bar.q_full, seg & 1, abort_v);
+            bool ok = warp_wait(&bar.q_full, seg & 1, abort_v, a.spin);
             auto issue_s = [&](int c) {
                 const int t = done + c, st = t & 1, ss = t % kSoftStages;
-                if (!warp_wait(&bar.k_full[st], (t >> 1) & 1, abort_v)) return false;
+                if (!warp_wait(&bar.k_full[st], (t >> 1) & 1, abort_v, a.spin)) return false;
                 tc::fence_after_sync();
                 if (elect_one()) {
 #pragma unroll
@@ -316,8 +316,8 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
                 // (into the scores of chunk c - 1, whose weights are there)
                 if (c + 2 < nc && !(ok = issue_s(c + 2))) break;
                 const int t = done + c, st = t & 1, ss = t % kSoftStages;
-                if (!(ok = warp_wait(&bar.v_full[st], (t >> 1) & 1, abort_v))) break;
-                if (!(ok = warp_wait(&bar.p_full[ss], (t / kSoftStages) & 1, abort_v))) break;
+                if (!(ok = warp_wait(&bar.v_full[st], (t >> 1) & 1, abort_v, a.spin))) break;
+                if (!(ok = warp_wait(&bar.p_full[ss], (t / kSoftStages) & 1, abort_v, a.spin))) break;
                 tc::fence_after_sync();
                 if (elect_one()) {
 #pragma unroll
@@ -342,7 +342,7 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
             const int g = lane >> 2, t4 = lane & 3;
             for (int c = 0; c < nc; ++c) {
                 const int t = done + c, st = t & 1, rs = t % kRawStages;
-                if (!warp_wait(&bar.raw_full[rs], (t / kRawStages) & 1, abort_v)) break;
+                if (!warp_wait(&bar.raw_full[rs], (t / kRawStages) & 1, abort_v, a.spin)) break;
                 const uint8_t* raw = smp + S::kRawO + rs * kRaw;
                 if (keys) {
                     const uint8_t* gr = raw + (2 * quarter + (lane >> 4)) * L::kBytes;
@@ -358,7 +358,7 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
                     for (int i = 0; i < 4; ++i) v[i] = rot & 2 ? w[(i + 2) & 3] : w[i];
                     // the products that read this stage: scores of chunk t - 2
                     const int ts = t - 2;
-                    if (ts >= 0 && !warp_wait(&bar.s_full[ts % kSoftStages], (ts / kSoftStages) & 1, abort_v)) break;
+                    if (ts >= 0 && !warp_wait(&bar.s_full[ts % kSoftStages], (ts / kSoftStages) & 1, abort_v, a.spin)) break;
                     tc::fence_after_sync();
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {  // 32 channels, 16 columns
@@ -382,7 +382,7 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
                 } else {
                     const int tok0 = (s.c0 + c) * kChunk;
                     const bool edge = tok0 + kChunk > low;
-                    if (!warp_wait(&bar.v_empty[st], ((t >> 1) & 1) ^ 1, abort_v)) break;
+                    if (!warp_wait(&bar.v_empty[st], ((t >> 1) & 1) ^ 1, abort_v, a.spin)) break;
                     tc::fence_after_sync();
 #pragma unroll
                     for (int gi = 0; gi < 8; gi += 2) {
@@ -489,7 +489,7 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
             for (int c = 0; c < nc; ++c) {
                 const int t = done + c, st = t % kSoftStages, tok = (s.c0 + c) * kChunk + tl;
                 // after a wait that gave up the warp goes on without waiting, for the others' sake
-                ok &= warp_wait(&bar.s_full[st], (t / kSoftStages) & 1, abort_v);
+                ok &= warp_wait(&bar.s_full[st], (t / kSoftStages) & 1, abort_v, a.spin);
                 tc::fence_after_sync();
                 const bool edge = (s.c0 + c + 1) * kChunk > low;  // some row does not see all of the chunk
                 float y[HN], big = kNoKey;
@@ -532,7 +532,7 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
                     for (int r = 0; r < HN; ++r) l[r] *= fac[r0 + r];
                     if (c > 0) {
                         // the last products with V (those up to chunk c - 3 were issued before S of this one)
-                        ok &= warp_wait(&bar.v_empty[(t - 1) & 1], ((t - 1) >> 1) & 1, abort_v);
+                        ok &= warp_wait(&bar.v_empty[(t - 1) & 1], ((t - 1) >> 1) & 1, abort_v, a.spin);
                         tc::fence_after_sync();
                         load_cols(cols + kO, y);
 #pragma unroll
@@ -560,7 +560,7 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&bar.p_full[st]);
             }
-            ok &= warp_wait(&bar.o_full, seg & 1, abort_v);
+            ok &= warp_wait(&bar.o_full, seg & 1, abort_v, a.spin);
             tc::fence_after_sync();
             if (!softmax_any(wg, !ok)) {
                 reduce_lanes(l, lane, [](float p, float q) { return p + q; });
@@ -617,10 +617,10 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
     // what is in flight lands before the block frees its tensor memory and ends
     if (warp == S::kCopy && lane == 0)
         for (int t = max(0, issued - kRawStages); t < issued; ++t)
-            drain(&bar.raw_full[t % kRawStages], (t / kRawStages) & 1, a.status);
+            drain(&bar.raw_full[t % kRawStages], (t / kRawStages) & 1, a.status, a.spin);
     if (warp == S::kIssue && lane == 0) {
         tc::mma_commit(&bar.drain);
-        drain(&bar.drain, 0, a.status);
+        drain(&bar.drain, 0, a.status, a.spin);
     }
     tc::fence_before_sync();
     if (abort_flag) found |= kFoundTimeout;

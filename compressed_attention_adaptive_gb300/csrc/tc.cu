@@ -54,10 +54,6 @@ __device__ __forceinline__ bool sync_on_mma(uint64_t* bar, uint32_t& phase, int*
     return !bad;
 }
 
-// Wait budgets in SM clock cycles: about one second normally; about one
-// millisecond for a launch that injects a stall (the fault tests).
-constexpr long long kSpin = 2LL << 30, kSpinTest = 1LL << 21;
-
 // Bounded wait used by the warp-specialized kernels: gives up when another
 // role has set the abort flag, or after `lim` cycles (then sets the device
 // status and the abort flag itself).

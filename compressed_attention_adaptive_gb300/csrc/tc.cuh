@@ -47,14 +47,18 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Waits for the phase with `parity` to complete, for about one second of SM
+// Wait budgets in SM clock cycles: about one second normally; about one
+// millisecond for a launch that injects a stall (the fault tests).
+constexpr long long kSpin = 2LL << 30, kSpinTest = 1LL << 21;
+
+// Waits for the phase with `parity` to complete, for `lim` cycles of SM
 // clock at most; on timeout records kStTimeout in the status word and
 // returns false.
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* status) {
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* status, long long lim = kSpin) {
     if (mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
     while (!mbar_try_wait(bar, parity)) {
-        if (clock64() - t0 > (2LL << 30)) {
+        if (clock64() - t0 > lim) {
             set_status(status, kStTimeout);
             return false;
         }
