@@ -314,8 +314,11 @@ mita_status mita_cache_read(const mita_cache_params* p, const void* cache, const
  * token see none, without it every row sees all keys.
  * O must not overlap Q. The same call gives the same bits; how a sequence's keys
  * are divided, and so the last bits, depends on all the call's lengths.
- * Runs on tensor cores, float32 with each number as the sum of two halves (22
- * bits), and with MITA_FLAG_SIMT on CUDA cores in fp32. */
+ * Runs on tensor cores with fp32 scores, softmax statistics and sums. The weights of
+ * bf16 rows are rounded to halves before they meet the values: 2^-11 each, and
+ * 2^-32 of the row's largest for those below 2^-21 of it. Numbers of float32 rows
+ * are the sum of two halves: 22 bits, and 2^-48 of the largest for weights below
+ * 2^-26 of it. With MITA_FLAG_SIMT on CUDA cores, in fp32 throughout. */
 mita_status mita_cache_attention(const mita_cache_params* p, const void* Q, const void* cache, const int32_t* table,
                                  const int32_t* len, const int32_t* count, const int32_t* exps, void* O,
                                  float* lse_out, void* ws, size_t ws_bytes, void* stream);
