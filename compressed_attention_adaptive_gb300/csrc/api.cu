@@ -351,11 +351,14 @@ static CacheWork carve_cache(const mita_cache_params* p, const CachePlan& plan, 
     return w;
 }
 
-// Whether two tensors of `heads` heads share bytes.
-static bool cache_overlap(const mita_cache_params* p, int heads, const void* x, const void* y) {
-    const uintptr_t bytes = (uintptr_t)p->B * heads * p->T * p->d * (p->dtype == MITA_DTYPE_F32 ? 4 : 2);
+// Whether two ranges share bytes.
+static bool overlap(const void* x, size_t nx, const void* y, size_t ny) {
     const uintptr_t a = (uintptr_t)x, b = (uintptr_t)y;
-    return (a < b ? b - a : a - b) < bytes;
+    return a < b ? b - a < nx : a - b < ny;
+}
+// Bytes of a call's rows in `dtype`.
+static size_t cache_bytes(const mita_cache_params* p, int heads) {
+    return (size_t)p->B * heads * p->T * p->d * (p->dtype == MITA_DTYPE_F32 ? 4 : 2);
 }
 
 // Common part of the three calls; r0, r1: the tensors in `dtype`.
@@ -675,7 +678,8 @@ mita_status mita_cache_read(const mita_cache_params* p, const void* cache, const
     CacheWork w;
     const mita_status st = cache_begin(p, false, &a, &plan, &w, K, V, cache, table, len, count, exps, ws, ws_bytes);
     if (st) return st;
-    if (cache_overlap(p, p->H_kv, K, V)) return fail(MITA_ERR_INVALID_ARG, "K and V must not overlap");
+    const size_t n = cache_bytes(p, p->H_kv);
+    if (overlap(K, n, V, n)) return fail(MITA_ERR_INVALID_ARG, "K and V must not overlap");
     MITA_CUDA(launch_cache_rows(a, p->d, p->dtype, false, K, V, (void*)cache, (cudaStream_t)stream), "cache read");
     prof_mark((cudaStream_t)stream, "");
     return MITA_OK;
@@ -690,8 +694,11 @@ mita_status mita_cache_attention(const mita_cache_params* p, const void* Q, cons
     CacheWork w;
     const mita_status st = cache_begin(p, true, &a, &plan, &w, Q, O, cache, table, len, count, exps, ws, ws_bytes);
     if (st) return st;
-    if (cache_overlap(p, p->H, Q, O)) return fail(MITA_ERR_INVALID_ARG, "O must not overlap Q");
+    const size_t n = cache_bytes(p, p->H), nl = (size_t)p->B * p->H * p->T * sizeof(float);
+    if (overlap(Q, n, O, n)) return fail(MITA_ERR_INVALID_ARG, "O must not overlap Q");
     if ((uintptr_t)lse_out % 4) return fail(MITA_ERR_INVALID_ARG, "lse_out must be 4-byte aligned");
+    if (lse_out && (overlap(lse_out, nl, Q, n) || overlap(lse_out, nl, O, n)))
+        return fail(MITA_ERR_INVALID_ARG, "lse_out must not overlap Q or O");
     MITA_CUDA(launch_cache_attn(a, plan, p->d, p->dtype, Q, cache, O, lse_out, w.parts, (cudaStream_t)stream),
               "cache attention");
     prof_mark((cudaStream_t)stream, "");

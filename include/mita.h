@@ -312,7 +312,7 @@ mita_status mita_cache_read(const mita_cache_params* p, const void* cache, const
  * rows can be joined with attention over other keys (mita_forward's shared
  * slots, say). count > len is allowed: with MITA_FLAG_CAUSAL rows before the first
  * token see none, without it every row sees all keys.
- * O must not overlap Q. The same call gives the same bits; how a sequence's keys
+ * O must not overlap Q, nor lse_out either of them. The same call gives the same bits; how a sequence's keys
  * are divided, and so the last bits, depends on all the call's lengths.
  * Runs on tensor cores with fp32 scores, softmax statistics and sums. The weights of
  * bf16 rows are rounded to halves before they meet the values: 2^-11 each, and

@@ -135,6 +135,19 @@ def test_overlapping_rows_are_refused(lib):
         assert b"overlap" in lib.mita_last_error()
 
 
+def test_overlapping_log_sums_are_refused(lib):
+    """A log sum over Q would be read as a query by blocks that come later, one over O be lost."""
+    p = _p()
+    c, need = ctypes.byref(p.c()), mita.mita_cache_workspace_size(p)
+    Q, O, q_bytes, l_bytes = 1 << 20, (1 << 20) + (1 << 16), 2 * 8 * 128 * 2, 2 * 8 * 4
+    f = ctypes.c_void_p(Q)
+    for x in (Q, O):
+        for lse in (x, x + q_bytes - 4, x + 4 - l_bytes):
+            assert lib.mita_cache_attention(c, f, f, f, f, None, None, ctypes.c_void_p(O), ctypes.c_void_p(lse), f, need,
+                                            None) == 1
+            assert b"lse_out must not overlap" in lib.mita_last_error()
+
+
 def test_params_copy_and_pickle_after_use(lib):
     p = _p(scale=0.25)
     mita.mita_cache_size(p)
