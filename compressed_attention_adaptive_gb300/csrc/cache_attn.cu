@@ -38,9 +38,6 @@ constexpr int kThreads = 128;
 
 // ------------------------------------------------------ staging of groups
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
-}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
@@ -85,16 +82,13 @@ __device__ __forceinline__ void stage_step(const uint8_t* cache, uint32_t dst, i
         const int k = lane + 32 * j;
         if (2 * N % 32 == 0 || k < 2 * N) {
             const int g = k < N ? g0 : g1;
-            copy16(dst + k * 16, cache + (long long)max(g, 0) * Grp<D>::kBytes + (k < N ? k : k - N) * 16, g >= 0);
+            tc::cp_async16(dst + k * 16, cache + (long long)max(g, 0) * Grp<D>::kBytes + (k < N ? k : k - N) * 16, g >= 0);
         }
     }
     copy_commit();
 }
 
 // ------------------------------------------------------------ CUDA cores
-
-__device__ __forceinline__ float to_float(float x) { return x; }
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
 constexpr int kSimtStages = 2;
 
@@ -124,7 +118,7 @@ k_cache_attn_simt(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restric
         return;
     }
     uint8_t* ring = smem + warp * (kSimtStages * 2 * L::kBytes);
-    const uint32_t ring_addr = smem_addr(ring);
+    const uint32_t ring_addr = tc::smem_u32(ring);
 
     do {
         const Segment& s = walk.s();
@@ -143,7 +137,7 @@ k_cache_attn_simt(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restric
             l[r] = 0.0f;
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                const float x = to_float(Q[at + i]);
+                const float x = to_f(Q[at + i]);
                 q[r][i] = isfinite(x) ? x : __int_as_float(0x7fc00000);  // the row becomes NaN, as its softmax is
                 o[r][i] = 0.0f;
             }
@@ -413,7 +407,7 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
     const int piece = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t4 = lane & 3;
     uint8_t* ring = smem + warp * (ST * kStage);
-    const uint32_t ring_addr = smem_addr(ring);
+    const uint32_t ring_addr = tc::smem_u32(ring);
     uint2* qs = reinterpret_cast<uint2*>(smem + mma_smem<T, D, NR>() - mma_q_bytes<T, D, NR>());
     if (lane == 0) {
         // (fault test: one more signal for the first step of one warp of the call than come)
@@ -667,7 +661,7 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
                             for (int x = 4; x < 32; x <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
                             // (a row's own scores move it, not another's)
                             const float mn = score_diff(v, zf[j][e], m[j][e]) > 15.0f ? score_diff(v, zf[j][e], F ? 11.0f : 7.0f) : m[j][e];
-                            const float f = ex2(m[j][e] - mn);
+                            const float f = tc::ex2(m[j][e] - mn);
                             m[j][e] = mn;
                             l[j][e] *= f;
 #pragma unroll
@@ -689,7 +683,7 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
                     for (int x = 0; x < GP; ++x)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const float p0 = ex2(y[j][x][2 * e]), p1 = ex2(y[j][x][2 * e + 1]);
+                            const float p0 = tc::ex2(y[j][x][2 * e]), p1 = tc::ex2(y[j][x][2 * e + 1]);
                             l[j][0] += p0;
                             l[j][1] += p1;
                             const uint32_t h2 = pack_half2(p0, p1);
@@ -854,7 +848,7 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
             float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float f = ex2(v[i].x - mx);
+                const float f = tc::ex2(v[i].x - mx);
                 const float4 u = os[at4(i, r, c)];
                 sum = fmaf(f, v[i].y, sum);
                 acc.x = fmaf(f, u.x, acc.x); acc.y = fmaf(f, u.y, acc.y);

@@ -195,8 +195,8 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
     using L = Grp<kD>;
     using S = TileSmem;
     extern __shared__ uint8_t smem_raw[];
-    const uint32_t sm = (smem_addr(smem_raw) + 1023) & ~1023u;
-    uint8_t* smp = smem_raw + (sm - smem_addr(smem_raw));
+    const uint32_t sm = (tc::smem_u32(smem_raw) + 1023) & ~1023u;
+    uint8_t* smp = smem_raw + (sm - tc::smem_u32(smem_raw));
     __shared__ Walk<N, kTileExtra> walk;
     __shared__ TileBars bar;
     __shared__ __align__(16) float2 ref[N];  // the rows' factors of scores, in log2 units, and references
@@ -524,7 +524,7 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
                         const float mx = fmaxf(fmaxf(part4[0][r], part4[1][r]), fmaxf(part4[2][r], part4[3][r]));
                         // (a row's own scores move it, not another's)
                         const float old = ref[r].y, mn = mx - old > 15.0f ? mx - 7.0f : old;
-                        fac[r] = ex2(old - mn);
+                        fac[r] = tc::ex2(old - mn);
                         ref[r].y = mn;
                     }
                     softmax_sync(wg);
@@ -548,7 +548,7 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int r = 8 * j + 2 * i;
-                        const float p0 = ex2(y[r]), p1 = ex2(y[r + 1]);
+                        const float p0 = tc::ex2(y[r]), p1 = tc::ex2(y[r + 1]);
                         l[r] += p0;
                         l[r + 1] += p1;
                         h[i] = pack_half2(p0, p1);

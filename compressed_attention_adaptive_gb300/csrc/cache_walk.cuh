@@ -305,17 +305,11 @@ __device__ __forceinline__ int row_limit(const CacheArgs& a, int n, int count, i
 
 // --------------------------------------------------------------- helpers
 
-__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 // One group of a step: a bulk copy that `bar` counts, or nothing.
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(smem_addr(bar))
+                 "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
                  : "memory");
-}
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
 }
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     uint32_t r;
