@@ -527,6 +527,117 @@ def test_many_sequences_in_every_form(dtype, d, H, T, B, simt):
     _check(pool, H, T, True, Q, O, L, counts, simt, label="%d sequences %s d%d%s" % (B, dtype, d, " simt" * simt))
 
 
+@pytest.mark.parametrize("dtype,d,H,T", [("bf16", 128, 2, 1), ("bf16", 64, 6, 2), ("bf16", 128, 64, 2), ("f32", 64, 2, 3),
+                                         ("f32", 128, 8, 4)])
+def test_tensors_at_the_least_alignment(dtype, d, H, T):
+    """Rows and pool 16 bytes past, index arrays and log sums 4 bytes past a larger boundary:
+    the same bits, and nothing outside of the outputs is written."""
+    import torch
+    import compressed_attention_adaptive_gb300 as mita
+
+    def shifted(t, by):
+        n = t.numel() * t.element_size()
+        buf = torch.full((n + 256,), 0x55, dtype=torch.uint8, device="cuda")
+        x = buf[by:by + n].view(t.dtype).view(t.shape)
+        x.copy_(t)
+        assert x.data_ptr() % 256 == by
+        return x, buf
+
+    def kept(buf, x):
+        n = x.numel() * x.element_size()
+        at = x.data_ptr() - buf.data_ptr()
+        return bool((buf[:at] == 0x55).all()) and bool((buf[at + n:] == 0x55).all())
+
+    pool = Pool([300, 77], 2, d, 32, dtype, seed=2, exps=[[1, 2], [-1, 0]])
+    Q, O, L = _attend(pool, H, T, True)
+    K2, V2, Q2 = (shifted(x, 16)[0] for x in (pool.K, pool.V, Q))
+    (cache, cb), (O2, ob), (L2, lb) = shifted(torch.zeros_like(pool.cache), 16), shifted(O, 16), shifted(L, 4)
+    table, lens, exps = (shifted(x, 4)[0] for x in (pool.table, pool.len_t, pool.exps))
+    O2.zero_(), L2.zero_()
+    mita.mita_cache_write(pool.fill_p, K2, V2, cache, table, lens, pool.fill_ws, counts=lens, exps=exps)
+    mita.mita_device_status(pool.fill_ws)
+    outs = [shifted(torch.zeros_like(pool.K), 16) for _ in range(2)]
+    mita.mita_cache_read(pool.fill_p, cache, table, lens, outs[0][0], outs[1][0], pool.fill_ws, counts=lens, exps=exps)
+    mita.mita_device_status(pool.fill_ws)
+    for which, (x, buf) in enumerate(outs):
+        for b, n in enumerate(pool.lens):
+            np.testing.assert_array_equal(_np(x[b, :, :n]), pool.held(b, which))
+            assert (x[b, :, n:] == 0).all()
+        assert kept(buf, x)
+    p = mita.CacheParams(2, H, 2, T, d, 32, pool.n_pages, pool.cols, 0.0, mita.FLAG_CAUSAL, pool.p.dtype)
+    ws = mita.cache_workspace(p)
+    mita.mita_cache_attention(p, Q2, cache, table, lens, O2, ws, exps=exps, lse_out=L2)
+    mita.mita_device_status(ws)
+    assert torch.equal(O, O2) and torch.equal(L, L2)
+    assert kept(cb, cache) and kept(ob, O2) and kept(lb, L2)
+
+
+@pytest.mark.parametrize("dtype,d,H,simt", [("bf16", 128, 1, False), ("bf16", 128, 40, False), ("f32", 64, 1, False),
+                                            ("bf16", 64, 1, True)])
+def test_calls_without_rows(dtype, d, H, simt):
+    """No sequence has a row, or a token: nothing is written, and the status word says so."""
+    pool = Pool([50, 3, 0], 1, d, 16, dtype)
+    Q, O, L = _attend(pool, H, 2, True, counts=[0, 0, 0], simt=simt)
+    assert (O == 7).all() and (L == 7).all()
+    empty = Pool([0, 0], 1, d, 16, dtype)
+    for causal in (False, True):
+        Q, O, L = _attend(empty, H, 2, causal, simt=simt)
+        assert (O == 0).all() and (L == -math.inf).all()
+
+
+@pytest.mark.parametrize("dtype,G,simt", [("bf16", 1, False), ("bf16", 40, False), ("f32", 2, False), ("bf16", 1, True)])
+def test_as_many_sequences_as_a_call_takes(dtype, G, simt):
+    """65535 sequences, most of a token or two: rows of some of them, and all of them
+    against a call for the second half."""
+    import torch
+    import compressed_attention_adaptive_gb300 as mita
+    B, d, page = 65535, 128 if G > 8 else 64, 16
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 4, B)
+    lens[rng.integers(0, B, 300)] = rng.integers(1, 200, 300)
+    lens[-1] = 130
+    cols = -(-int(lens.max()) // page)
+    need = -(-lens // page)
+    table = np.full((B, cols), -1, np.int32)
+    at = np.concatenate([[0], np.cumsum(need)])
+    for b in np.flatnonzero(need):
+        table[b, :need[b]] = at[b] + np.arange(need[b])
+    dt, td = (mita.F32, torch.float32) if dtype == "f32" else (mita.BF16, torch.bfloat16)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    longest = int(lens.max())
+    K, V = (torch.randn((B, 1, longest, d), generator=g, device="cuda").to(td) for _ in range(2))
+    Q = torch.randn((B, G, 1, d), generator=g, device="cuda").to(td)
+    table_t, len_t = torch.from_numpy(table).cuda(), torch.from_numpy(lens.astype(np.int32)).cuda()
+    f = mita.CacheParams(B, 1, 1, longest, d, page, int(at[-1]), cols, dtype=dt)
+    cache, ws = torch.zeros(mita.mita_cache_size(f), dtype=torch.uint8, device="cuda"), mita.cache_workspace(f)
+    mita.mita_cache_write(f, K, V, cache, table_t, len_t, ws, counts=len_t)
+    mita.mita_device_status(ws)
+
+    def attend(lo, hi):
+        p = mita.CacheParams(hi - lo, G, 1, 1, d, page, int(at[-1]), cols, 0.0, mita.FLAG_SIMT * simt, dt)
+        O, w = torch.full_like(Q[lo:hi], 7.0), mita.cache_workspace(p)
+        mita.mita_cache_attention(p, Q[lo:hi].contiguous(), cache, table_t[lo:hi].contiguous(),
+                                  len_t[lo:hi].contiguous(), O, w)
+        mita.mita_device_status(w)
+        return O
+
+    O = attend(0, B)
+    assert (O[torch.from_numpy(lens == 0).cuda()] == 0).all()
+    # a sequence is cut at other places in the other call: the bound of _check, twice, with weights of at most 1
+    half = attend(B // 2, B).float()
+    tol = 2 * (2.0 ** -8 * half.abs() + 2.0 ** -11 * 6) if dtype == "bf16" else 2.0 ** -15
+    assert torch.all((O[B // 2:].float() - half).abs() <= tol)
+    for b in np.concatenate([[0, 1, B - 2, B - 1], rng.integers(0, B, 40), np.flatnonzero(lens > 100)[:20]]):
+        n = int(lens[b])
+        if n == 0:
+            continue
+        k, v = (ocache.quantise(_np(X[b, 0, :n])) for X in (K, V))
+        q = _np(Q[b, :, 0])
+        ref, _, spread = ocache.attention(q, k, v, [n] * G, 1 / math.sqrt(d))
+        bound = attention_bound(dtype, dtype == "bf16" and not simt, ref, spread, q, k, v, [n] * G, 1 / math.sqrt(d))
+        assert np.all(np.abs(_np(O[b, :, 0]) - ref) <= bound), b
+
+
 # -------------------------------------------- out of range, and the status word
 
 
