@@ -66,21 +66,26 @@ constexpr uint32_t idesc_half(int M, int N, int a_mn, int b_mn) {
            ((uint32_t)(M >> 4) << 24);
 }
 
+struct Abort {
+    int flag;   // a role has given up
+    int limit;  // what a wait takes at most, in kSpinTest (from shared memory: as the kernel's
+                // parameter it took operands out of the uniform registers, 263.8 us against 261.4)
+};
 // Bounded wait that also ends when another role has given up.
-__device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, long long lim) {
+__device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t parity, volatile Abort* abort) {
     if (tc::mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
     while (!tc::mbar_try_wait(bar, parity)) {
-        if (*abort_flag) return false;
-        if (clock64() - t0 > lim) {
-            *abort_flag = 1;
+        if (abort->flag) return false;
+        if (clock64() - t0 > abort->limit * tc::kSpinTest) {
+            abort->flag = 1;
             return false;
         }
     }
     return true;
 }
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, long long lim) {
-    return __all_sync(0xffffffffu, tile_wait(bar, parity, abort_flag, lim));
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile Abort* abort) {
+    return __all_sync(0xffffffffu, tile_wait(bar, parity, abort));
 }
 // For what this block has issued to the asynchronous units, whatever the abort flag says.
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, int* status, long long lim) {
@@ -205,8 +210,8 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
     __shared__ long long row_at[N];
     __shared__ __align__(16) uint8_t nanv[kEdge];  // blocks of a token's values that are NaN, tokens from `low` on
     __shared__ uint32_t tmem_slot;
-    __shared__ int abort_flag;
-    volatile int* abort_v = &abort_flag;
+    __shared__ Abort abort;
+    volatile Abort* abort_v = &abort;
     allow_next();
     const int piece = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int found = 0;
@@ -231,7 +236,8 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
         tc::mbar_init(&bar.o_full, 1);
         tc::mbar_init(&bar.drain, 1);
         tc::fence_mbar_init();
-        abort_flag = nan_flag = 0;
+        abort.flag = nan_flag = 0;
+        abort.limit = (int)(a.spin / tc::kSpinTest);
     }
     if (tid < kEdge) nanv[tid] = 0;
     tc::fence_before_sync();
@@ -276,7 +282,7 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
             Copy cur = copies(0), nxt = copies(4);
             for (int c = 0; c < nc; ++c) {
                 const int t = done + c, st = t % kRawStages;
-                if (!warp_wait(&bar.raw_empty[st], ((t / kRawStages) & 1) ^ 1, abort_v, a.spin)) break;
+                if (!warp_wait(&bar.raw_empty[st], ((t / kRawStages) & 1) ^ 1, abort_v)) break;
                 const bool mine = (lane >> 3) == (c & 3);
                 const uint32_t bytes = __reduce_add_sync(0xffffffffu, mine ? cur.bytes : 0u);
                 if (elect_one()) tc::mbar_expect_tx(&bar.raw_full[st], bytes);
@@ -296,10 +302,10 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
             // weights over the next scores to their weights, which is several waits long, is gone
             // over once for three chunks.
             constexpr uint32_t idS = idesc_half(128, N, 0, 0), idO = idesc_half(128, N, 0, 1);
-            bool ok = warp_wait(&bar.q_full, seg & 1, abort_v, a.spin);
+            bool ok = warp_wait(&bar.q_full, seg & 1, abort_v);
             auto issue_s = [&](int c) {
                 const int t = done + c, st = t & 1, ss = t % kSoftStages;
-                if (!warp_wait(&bar.k_full[st], (t >> 1) & 1, abort_v, a.spin)) return false;
+                if (!warp_wait(&bar.k_full[st], (t >> 1) & 1, abort_v)) return false;
                 tc::fence_after_sync();
                 if (elect_one()) {
 #pragma unroll
@@ -316,8 +322,8 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
                 // (into the scores of chunk c - 1, whose weights are there)
                 if (c + 2 < nc && !(ok = issue_s(c + 2))) break;
                 const int t = done + c, st = t & 1, ss = t % kSoftStages;
-                if (!(ok = warp_wait(&bar.v_full[st], (t >> 1) & 1, abort_v, a.spin))) break;
-                if (!(ok = warp_wait(&bar.p_full[ss], (t / kSoftStages) & 1, abort_v, a.spin))) break;
+                if (!(ok = warp_wait(&bar.v_full[st], (t >> 1) & 1, abort_v))) break;
+                if (!(ok = warp_wait(&bar.p_full[ss], (t / kSoftStages) & 1, abort_v))) break;
                 tc::fence_after_sync();
                 if (elect_one()) {
 #pragma unroll
@@ -342,7 +348,7 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
             const int g = lane >> 2, t4 = lane & 3;
             for (int c = 0; c < nc; ++c) {
                 const int t = done + c, st = t & 1, rs = t % kRawStages;
-                if (!warp_wait(&bar.raw_full[rs], (t / kRawStages) & 1, abort_v, a.spin)) break;
+                if (!warp_wait(&bar.raw_full[rs], (t / kRawStages) & 1, abort_v)) break;
                 const uint8_t* raw = smp + S::kRawO + rs * kRaw;
                 if (keys) {
                     const uint8_t* gr = raw + (2 * quarter + (lane >> 4)) * L::kBytes;
@@ -358,7 +364,7 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
                     for (int i = 0; i < 4; ++i) v[i] = rot & 2 ? w[(i + 2) & 3] : w[i];
                     // the products that read this stage: scores of chunk t - 2
                     const int ts = t - 2;
-                    if (ts >= 0 && !warp_wait(&bar.s_full[ts % kSoftStages], (ts / kSoftStages) & 1, abort_v, a.spin)) break;
+                    if (ts >= 0 && !warp_wait(&bar.s_full[ts % kSoftStages], (ts / kSoftStages) & 1, abort_v)) break;
                     tc::fence_after_sync();
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {  // 32 channels, 16 columns
@@ -382,7 +388,7 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
                 } else {
                     const int tok0 = (s.c0 + c) * kChunk;
                     const bool edge = tok0 + kChunk > low;
-                    if (!warp_wait(&bar.v_empty[st], ((t >> 1) & 1) ^ 1, abort_v, a.spin)) break;
+                    if (!warp_wait(&bar.v_empty[st], ((t >> 1) & 1) ^ 1, abort_v)) break;
                     tc::fence_after_sync();
 #pragma unroll
                     for (int gi = 0; gi < 8; gi += 2) {
@@ -489,7 +495,7 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
             for (int c = 0; c < nc; ++c) {
                 const int t = done + c, st = t % kSoftStages, tok = (s.c0 + c) * kChunk + tl;
                 // after a wait that gave up the warp goes on without waiting, for the others' sake
-                ok &= warp_wait(&bar.s_full[st], (t / kSoftStages) & 1, abort_v, a.spin);
+                ok &= warp_wait(&bar.s_full[st], (t / kSoftStages) & 1, abort_v);
                 tc::fence_after_sync();
                 const bool edge = (s.c0 + c + 1) * kChunk > low;  // some row does not see all of the chunk
                 float y[HN], big = kNoKey;
@@ -532,7 +538,7 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
                     for (int r = 0; r < HN; ++r) l[r] *= fac[r0 + r];
                     if (c > 0) {
                         // the last products with V (those up to chunk c - 3 were issued before S of this one)
-                        ok &= warp_wait(&bar.v_empty[(t - 1) & 1], ((t - 1) >> 1) & 1, abort_v, a.spin);
+                        ok &= warp_wait(&bar.v_empty[(t - 1) & 1], ((t - 1) >> 1) & 1, abort_v);
                         tc::fence_after_sync();
                         load_cols(cols + kO, y);
 #pragma unroll
@@ -560,7 +566,7 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&bar.p_full[st]);
             }
-            ok &= warp_wait(&bar.o_full, seg & 1, abort_v, a.spin);
+            ok &= warp_wait(&bar.o_full, seg & 1, abort_v);
             tc::fence_after_sync();
             if (!softmax_any(wg, !ok)) {
                 reduce_lanes(l, lane, [](float p, float q) { return p + q; });
@@ -608,7 +614,7 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
         }
         done += nc;
         // every warp is through the segment, so that all see the same and meet at the same barriers
-        stop = __syncthreads_or(abort_flag);
+        stop = __syncthreads_or(abort.flag);
         if (tid < kEdge) nanv[tid] = 0;
         if (tid == 0) nan_flag = 0;
         more = walk.next(a);
@@ -623,7 +629,7 @@ k_cache_attn_tile(CacheArgs a, const __nv_bfloat16* __restrict__ Q, const uint8_
         drain(&bar.drain, 0, a.status, a.spin);
     }
     tc::fence_before_sync();
-    if (abort_flag) found |= kFoundTimeout;
+    if (abort.flag) found |= kFoundTimeout;
     end_piece(a, out, piece, found);
     tc::fence_after_sync();
     if (warp == S::kIssue) tc::tmem_dealloc(tmem, 512);
