@@ -6,13 +6,14 @@
 // owns one block of 16 channels of a row's keys and values: its maximum, its scale
 // and its codes need nothing from another thread.
 //
-// Measured, two prompts of 32768, 16 heads, d = 128, bf16 (688 MB): writing 108 us
-// (6.4 TB/s, 0.95 of the copy rate; issue slots 83 %), reading 103 us (0.99). One new
+// Measured, calls back to back, two prompts of 32768, 16 heads, d = 128: bf16 (688 MB)
+// written in 109 us (6.3 TB/s, 0.94 of the copy rate; issue slots 83 %) and read back in 106
+// (0.97), float32 (1225 MB) in 199 (0.92) and 183 (1.00). One new
 // token of 48 sequences: 3.2 us each, the latency of a length, a table entry and
 // a row one after the other.
 //   - A true division per element made writing 228 us (issue-bound), three operations instead of it
 //     136, packed maxima and packing four code pairs at a time 108 (bf16; float32 divides).
-//   - 32-byte accesses, and keys and values in one thread, took reading from 140 us to 103.
+//   - 32-byte accesses, and keys and values in one thread, took reading from 140 us to 106.
 #include "cache.cuh"
 
 namespace mita {

@@ -12,11 +12,12 @@
 // row and key, so with few rows per cache head it is bound by HBM: at the
 // measured copy rate an SM has 6.3 clocks per token of 128 channels, 3.1 of 64.
 //
-// Measured (one row per cache head, d = 128, 32 heads): 7.4 us for 1024 tokens, 32 for
-// 32,768 (4.7 TB/s), 103 for 131,072 (5.9), 196 for 262,144 (6.2); each further
+// Measured (one row per cache head, d = 128, 32 heads, calls in a graph): 7.5 us for 1024
+// tokens, 32 for 32,768 (4.7 TB/s), 102 for 131,072 (5.9), 195 for 262,144 (6.2); each further
 // token costs 1.03 times what it does at the copy rate. The other 9 us are the same for
 // every length: 2 to launch, 1.4 to find a block's place on the line, 1.5 until
-// the first codes arrive, an SM's last blocks alone, 2 for the join.
+// the first codes arrive, an SM's last blocks alone, 2 for the join. Calls launched one by
+// one take about 3 us more (35 for 32,768 tokens).
 //
 // Work split. An item is one (sequence, tile of query rows, cache head); it is
 // cut into chunks of 128 tokens. The chunks of all items form one line, and the
@@ -372,18 +373,20 @@ template <typename T, int D, int NR> constexpr int mma_smem() {
 // 2^-32 none: 1e-4 of the result where a key of that weight has no value. The scale takes a
 // second sum: over lengths around 16384, 8 x 12 heads, d = 64, 37.0 us against 35.7; 2 x 16 heads
 // of about 30,000, d = 128, 40.6 against 40.3; with 12 rows 26.0 against 25.0. On CUDA cores the first
-// case takes 52.)
+// case takes 49.)
 //
 // The next segment is found while a segment's first codes are on their way, and its own
-// first copies are issued before the warps' sums are joined (8 x 12 heads of 16384 tokens in
-// float32 39.1 to 37.8 us, 32 x 32 of 2048 77 to 75, bf16 batches of short sequences 1 to 2 %).
+// first copies are issued before the warps' sums are joined (3 % of 8 x 12 heads of 16384 tokens
+// in float32 and of 32 x 32 of 2048, bf16 batches of short sequences 1 to 2 %).
 //
 // A warp has about 570 instructions per 32 tokens of 128 channels and 8 rows, 128 of
 // them conversions of codes and 128 products by scales (half rate each). Over the
-// whole of a 32 us launch (two 32k prompts, 32 heads) the arithmetic pipe is at
-// 51 %, the issue slots at 56 %, DRAM at 0.72 of the copy rate; in the middle of it
-// DRAM is near that rate. Other forms, measured on that case, this one at 33 us, 36.7 with the join: rows
-// on the 16 side 42.7; with the join, 5 blocks per SM at 96 registers 39.8 against
+// whole of a 32 us launch under ncu (two 32k prompts, 32 heads) the arithmetic pipe is at
+// 52 %, the issue slots at 57 %, DRAM at 0.72 of the copy rate; in the middle of it
+// DRAM is near that rate. float32 with d = 64 (8 x 12 heads of 16384 tokens) is at 41 %, 60 % and
+// 0.47 and 15 rows of d = 64 at 39 %, 55 % and 0.34: no unit is full there, a warp's steps wait for
+// each other's results. Other forms, measured on the first case when this one was at 33 us, 36.7
+// with the join: rows on the 16 side 42.7; with the join, 5 blocks per SM at 96 registers 39.8 against
 // 39.0 then, three copy stages 37.1, twice as many pieces of half the size 41.1, smaller
 // pieces for an SM's later blocks (which run behind the first) 37.2 to 38.6. Steps
 // of 64 tokens for d = 64: 131,072 tokens 68.1 to 64.8 us, but 26.8 to 27.9 for the
@@ -660,7 +663,9 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
 #pragma unroll
                             for (int x = 4; x < 32; x <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
                             // (a row's own scores move it, not another's)
-                            const float mn = score_diff(v, zf[j][e], m[j][e]) > 15.0f ? score_diff(v, zf[j][e], F ? 11.0f : 7.0f) : m[j][e];
+                            const float mn = score_diff(v, zf[j][e], m[j][e]) > 15.0f
+                                                 ? score_diff(v, zf[j][e], F ? 11.0f : 7.0f)
+                                                 : m[j][e];
                             const float f = tc::ex2(m[j][e] - mn);
                             m[j][e] = mn;
                             l[j][e] *= f;
@@ -690,7 +695,8 @@ k_cache_attn_mma(CacheArgs a, const T* __restrict__ Q, const uint8_t* __restrict
                             p[j][x][e] = transpose8(h2);
                             if (F) {
                                 const float2 hf = half2_to_float2(h2);
-                                pl[j % NL][x][e] = transpose8(pack_half2(fmaf(hf.x, -kLow, p0 * kLow), fmaf(hf.y, -kLow, p1 * kLow)));
+                                pl[j % NL][x][e] =
+                                    transpose8(pack_half2(fmaf(hf.x, -kLow, p0 * kLow), fmaf(hf.y, -kLow, p1 * kLow)));
                             }
                         }
                 // groups whose products with V are summed before they go to a float row's o

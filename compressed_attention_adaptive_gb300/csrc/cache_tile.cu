@@ -29,15 +29,15 @@
 // block that gives up raises its abort flag, lets its copies and products land and
 // frees its tensor memory.
 //
-// Measured: 64 rows over 2 x 16 heads of 131,072 tokens 265 us (519 TFLOP/s), of 32,768
-// 79 us; 4 x 8 heads of 9000 to 16384 tokens 41.6 us (the register form 57.5). A chunk
+// Measured, calls in a graph: 64 rows over 2 x 16 heads of 131,072 tokens 261 us (526 TFLOP/s),
+// of 32,768 77 us; 4 x 8 heads of 9000 to 16384 tokens 41.6 us (the register form 57.5). A chunk
 // takes about 2400 clocks, and no role is busy all of it: softmax 1900, values 1500,
-// issuing 1000 (a product of 128 x 64 x 16 takes 51 to 60), copies 1000, keys 800. They
-// share the issue slots (56 %, 6500 instructions a chunk) and wait for each other's
-// stages. What it took: operands in uniform registers (323 us to 288), 16 rows per softmax
-// thread instead of 32 (a softmax chunk 2200 clocks to 1450), an epilogue of little
-// code (13 us off every item: cold instructions), fewer and longer copies (each takes 180
-// clocks to issue).
+// issuing 1000 (a product of 128 x 64 x 16 takes 51 to 60), copies 1000, keys 800. No unit
+// is full (issue slots 58 %, the tensor pipe 16 %): the roles wait for each other's stages.
+// The values' 16-bit reads are two-way bank conflicts, all of them. What it took: operands in
+// uniform registers (323 us to 288), 16 rows per softmax thread instead of 32 (a softmax chunk
+// 2200 clocks to 1450), an epilogue of little code (13 us off every item: cold instructions),
+// fewer and longer copies (each takes 180 clocks to issue).
 #include <atomic>
 
 #include "cache_walk.cuh"
