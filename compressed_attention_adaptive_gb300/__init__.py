@@ -8,7 +8,10 @@ entry points carry the names of the C ABI in ``include/mita.h``:
 ``mita_forward_static``, ``mita_backward_workspace_size``, ``mita_backward``,
 ``mita_device_status``, ``mita_uses_tensor_cores``, and for the 4-bit
 key/value cache ``mita_cache_size``, ``mita_cache_workspace_size``,
-``mita_cache_write``, ``mita_cache_read``, ``mita_cache_attention``.
+``mita_cache_write``, ``mita_cache_read``, ``mita_cache_attention``,
+``mita_cache_weights``, ``mita_cache_evict_workspace_size``,
+``mita_cache_evict``, and for rotary positions ``mita_rope_frequencies``,
+``mita_rope``, ``mita_rope_backward``.
 
 The library must be built first (``python -c "import __graft_entry__ as g;
 g.build()"``); calling an entry point without it raises ``RuntimeError``.
@@ -25,7 +28,9 @@ LIB_PATH = os.path.join(_PKG, "libmita.so")
 _lib = None
 
 F32, BF16 = 0, 1
-FLAG_NO_SHARED, FLAG_SIMT, FLAG_CAUSAL = 1, 2, 4
+FLAG_NO_SHARED, FLAG_SIMT, FLAG_CAUSAL, FLAG_INTERLEAVED = 1, 2, 4, 8
+ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_PARTS = 0, 1, 2, 3
+ROPE_PAIRS = 128
 TESTFLAG_STALL_PRODUCER = 1 << 31  # fault test only (see include/mita.h)
 STATUS = {0: "MITA_OK", 1: "MITA_ERR_INVALID_ARG", 2: "MITA_ERR_UNSUPPORTED", 3: "MITA_ERR_WORKSPACE",
           4: "MITA_ERR_CUDA", 5: "MITA_ERR_TIMEOUT", 6: "MITA_ERR_BOUNDS"}
@@ -109,6 +114,47 @@ class CacheParams:
         return CacheParams, dataclasses.astuple(self)
 
 
+class _CRopeParams(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("H_kv", ctypes.c_int), ("T", ctypes.c_int),
+                ("d", ctypes.c_int), ("rot", ctypes.c_int), ("gain", ctypes.c_float), ("flags", ctypes.c_uint),
+                ("dtype", ctypes.c_int), ("freqs", ctypes.c_double * ROPE_PAIRS)]
+
+
+@dataclasses.dataclass(frozen=True)
+class RopeParams:
+    """Mirror of ``mita_rope_params`` (see include/mita.h); its C form is made once.
+    ``freqs``: radians per position of the rot / 2 pairs (``mita_rope_frequencies``
+    makes them), or None for base 10000."""
+    B: int
+    H: int
+    H_kv: int
+    T: int
+    d: int
+    rot: int
+    freqs: tuple = None
+    gain: float = 0.0
+    flags: int = 0
+    dtype: int = BF16
+
+    @functools.cached_property
+    def _c(self):
+        f = mita_rope_frequencies(self.rot) if self.freqs is None else tuple(float(x) for x in self.freqs)
+        if len(f) > ROPE_PAIRS or len(f) != self.rot // 2:
+            raise ValueError("freqs must have rot / 2 = %d numbers, got %d" % (self.rot // 2, len(f)))
+        return _CRopeParams(self.B, self.H, self.H_kv, self.T, self.d, self.rot, float(self.gain), int(self.flags),
+                            int(self.dtype), (ctypes.c_double * ROPE_PAIRS)(*f))
+
+    @functools.cached_property
+    def ref(self):
+        return ctypes.byref(self._c)
+
+    def c(self):
+        return self._c
+
+    def __reduce__(self):  # copies and pickles hold the fields, not the C form
+        return RopeParams, dataclasses.astuple(self)
+
+
 def lib():
     """The loaded libmita.so; raises if it has not been built."""
     global _lib
@@ -146,6 +192,17 @@ def lib():
         L.mita_cache_read.argtypes = [C, vp, ip, ip, ip, ip, vp, vp, vp, sz, vp]
         L.mita_cache_attention.argtypes = [C, vp, vp, ip, ip, ip, ip, vp, fp, vp, sz, vp]
         for f in ("mita_cache_write", "mita_cache_read", "mita_cache_attention"):
+            getattr(L, f).restype = ctypes.c_int
+        L.mita_cache_weights.argtypes = [C, vp, vp, ip, ip, ip, ip, fp, ctypes.c_float, fp, fp, vp, sz, vp]
+        L.mita_cache_evict_workspace_size.argtypes = [C]
+        L.mita_cache_evict_workspace_size.restype = sz
+        L.mita_cache_evict.argtypes = [C, vp, ip, ip, ip, ctypes.c_int, ctypes.c_int, fp, ip, fp, ip, vp, sz, vp]
+        R, dbl = ctypes.POINTER(_CRopeParams), ctypes.c_double
+        L.mita_rope_frequencies.argtypes = [R, dbl, ctypes.c_int, dbl, dbl, dbl, dbl]
+        for f in ("mita_rope", "mita_rope_backward"):
+            getattr(L, f).argtypes = [R, vp, vp, vp, vp, vp, ip, ctypes.c_int64, vp]
+        for f in ("mita_cache_weights", "mita_cache_evict", "mita_rope_frequencies", "mita_rope",
+                  "mita_rope_backward"):
             getattr(L, f).restype = ctypes.c_int
         L.mita_launch_count.argtypes = []
         L.mita_launch_count.restype = ctypes.c_longlong
@@ -417,3 +474,155 @@ def mita_cache_attention(p: CacheParams, Q, cache, table, lens, O, ws, counts=No
     _on_device(cache, (_lib or lib()).mita_cache_attention,
                (p.ref, Q.data_ptr(), cache.data_ptr(), tp, lp, cp, ep, O.data_ptr(), lse_out, ws.data_ptr(), ws.numel(),
                 st))
+
+
+def _float_sums(p: CacheParams, t, what, dev):
+    import torch
+    s = (p.B, p.H_kv, p.max_pages * p.page)
+    if t.dtype is not torch.float32 or t.get_device() != dev or t.shape != s or not t.is_contiguous():
+        _refuse(t, s, torch.float32, dev, what)
+    return t.data_ptr()
+
+
+def mita_cache_weights(p: CacheParams, Q, cache, table, lens, lse, acc, ws, counts=None, exps=None, decay=1.0,
+                       acc_out=None, stream=None):
+    """Adds the attention weight that each cached token gets from the rows Q [B, H, T, d],
+    whose log sums are lse [B, H, T], to decay times its sum in acc [B, H_kv, max_pages *
+    page], into acc_out (acc itself if None). acc may be None with decay = 0."""
+    import torch
+    tp, lp, cp, ep, st = _cache_index(p, Q, Q, p.H, cache, table, lens, ws, counts, exps, stream)
+    dev, s = cache.get_device(), (p.B, p.H, p.T)
+    if lse.dtype is not torch.float32 or lse.get_device() != dev or lse.shape != s or not lse.is_contiguous():
+        _refuse(lse, s, torch.float32, dev, "lse: ")
+    ap = None if acc is None else _float_sums(p, acc, "acc: ", dev)
+    if acc_out is None and acc is None:
+        raise ValueError("without acc the sums need acc_out")
+    op = ap if acc_out is None else _float_sums(p, acc_out, "acc_out: ", dev)
+    _on_device(cache, (_lib or lib()).mita_cache_weights,
+               (p.ref, Q.data_ptr(), cache.data_ptr(), tp, lp, cp, ep, lse.data_ptr(), decay, ap, op, ws.data_ptr(),
+                ws.numel(), st))
+
+
+def mita_cache_evict_workspace_size(p: CacheParams) -> int:
+    return int(lib().mita_cache_evict_workspace_size(ctypes.byref(p.c())))
+
+
+def cache_evict_workspace(p: CacheParams, device="cuda"):
+    """A device workspace for ``mita_cache_evict`` with ``p`` (torch uint8 tensor)."""
+    import torch
+    n = mita_cache_evict_workspace_size(p)
+    if n == 0:
+        raise MitaError(1, lib().mita_last_error().decode() or "invalid parameters")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def mita_cache_evict(p: CacheParams, cache, table, lens, keep, acc, ws, first=0, recent=0, len_out=None, acc_out=None,
+                     src_out=None, stream=None):
+    """Keeps keep[b] tokens of each sequence that has more, in each cache head the first
+    ``first``, the last ``recent`` and those with the largest sums in acc [B, H_kv, max_pages *
+    page]. The new lengths go to len_out (lens itself if None), the sums to acc_out (acc
+    itself if None), the place that each row had to src_out (int32 like acc, optional)."""
+    import torch
+    i32, u8, dev = torch.int32, torch.uint8, cache.get_device()
+    if cache.dtype is not u8 or not cache.is_contiguous():
+        _refuse(cache, cache.shape, u8, dev)
+    if cache.numel() < p.pool_bytes:
+        raise ValueError("cache holds %d bytes, the pool needs %d" % (cache.numel(), p.pool_bytes))
+    if ws.dtype is not u8 or ws.get_device() != dev or not ws.is_contiguous():
+        _refuse(ws, ws.shape, u8, dev)
+    s = (p.B, p.max_pages)
+    if table.dtype is not i32 or table.get_device() != dev or table.shape != s or not table.is_contiguous():
+        _refuse(table, s, i32, dev)
+    if len_out is None:
+        len_out = lens
+    s = (p.B,)
+    for t in (lens, keep, len_out):
+        if t.dtype is not i32 or t.get_device() != dev or t.shape != s or not t.is_contiguous():
+            _refuse(t, s, i32, dev)
+    if dev < 0:
+        raise ValueError("the tensors must be on a CUDA device")
+    ap = _float_sums(p, acc, "acc: ", dev)
+    op = ap if acc_out is None else _float_sums(p, acc_out, "acc_out: ", dev)
+    sp = None
+    if src_out is not None:
+        s = (p.B, p.H_kv, p.max_pages * p.page)
+        if src_out.dtype is not i32 or src_out.get_device() != dev or src_out.shape != s or not src_out.is_contiguous():
+            _refuse(src_out, s, i32, dev, "src_out: ")
+        sp = src_out.data_ptr()
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    _on_device(cache, (_lib or lib()).mita_cache_evict,
+               (p.ref, cache.data_ptr(), table.data_ptr(), lens.data_ptr(), keep.data_ptr(), first, recent, ap,
+                len_out.data_ptr(), op, sp, ws.data_ptr(), ws.numel(), stream))
+
+
+def mita_rope_frequencies(rot, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, original=0.0, low=1.0, high=4.0) -> tuple:
+    """Radians per position of the rot / 2 pairs (see include/mita.h for the scaled forms)."""
+    c = _CRopeParams(rot=rot)
+    _check(lib().mita_rope_frequencies(ctypes.byref(c), base, scaling, factor, original, low, high))
+    return tuple(c.freqs[:rot // 2])
+
+
+def _rope(p, fn, Q, K, Qo, Ko, pos, stream):
+    """Written out, like _cache_index. The rows are [B, heads, T, d] with any strides but the last."""
+    import torch
+    dt, dev = torch.bfloat16 if p.dtype == BF16 else torch.float32, Q.get_device()
+    s = (p.B, p.H, p.T, p.d)
+    for t in (Q, Qo):
+        if t.dtype is not dt or t.get_device() != dev or t.shape != s:
+            _refuse_rows(t, s, dt, dev)
+    q0, q1, q2, q3 = Q.stride()
+    o0, o1, o2, o3 = Qo.stride()
+    if K is None and Ko is None:
+        kp = kop = None
+        k0 = k1 = k2 = r0 = r1 = r2 = 0
+    elif K is None or Ko is None:
+        raise ValueError("K and its output come together")
+    else:
+        s = (p.B, p.H_kv, p.T, p.d)
+        for t in (K, Ko):
+            if t.dtype is not dt or t.get_device() != dev or t.shape != s:
+                _refuse_rows(t, s, dt, dev)
+        k0, k1, k2, k3 = K.stride()
+        r0, r1, r2, r3 = Ko.stride()
+        q3, o3, kp, kop = max(q3, k3), max(o3, r3), K.data_ptr(), Ko.data_ptr()
+    if q3 != 1 or o3 != 1:
+        raise ValueError("the channels of a row must be contiguous")
+    if dev < 0:
+        raise ValueError("the tensors must be on a CUDA device")
+    pp, ps = None, 0
+    if pos is not None:
+        if pos.dtype is not torch.int32 or pos.get_device() != dev or pos.shape not in ((p.T,), (p.B, p.T)):
+            _refuse_rows(pos, (p.B, p.T), torch.int32, dev)
+        if p.T > 1 and pos.stride(-1) != 1:
+            raise ValueError("a sequence's positions must be contiguous")
+        pp, ps = pos.data_ptr(), pos.stride(0) if pos.dim() == 2 else 0
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    _on_device(Q, fn, (p.ref, Q.data_ptr(), kp, Qo.data_ptr(), kop,
+                       _Strides(q0, q1, q2, k0, k1, k2, o0, o1, o2, r0, r1, r2), pp, ps, stream))
+
+
+_Strides = ctypes.c_int64 * 12
+
+
+def _refuse_rows(t, shape, dtype, dev):
+    if t.get_device() != dev:
+        raise ValueError("all tensors of a call must be on one CUDA device")
+    raise ValueError("expected a %s tensor of shape %s, got %s %s" % (dtype, tuple(shape), t.dtype, tuple(t.shape)))
+
+
+def mita_rope(p: RopeParams, Q, K, Qo, Ko, pos=None, stream=None):
+    """Rotates the rows Q [B, H, T, d] into Qo and K [B, H_kv, T, d] into Ko by the positions
+    pos [B, T] or [T] (int32; None: 0 .. T - 1). Any strides over contiguous channels; Qo may
+    be Q and Ko K. K = Ko = None with p.H_kv = 0."""
+    _rope(p, (_lib or lib()).mita_rope, Q, K, Qo, Ko, pos, stream)
+
+
+def mita_rope_backward(p: RopeParams, dQo, dKo, dQ, dK, pos=None, stream=None):
+    """The transposed map: gradients with respect to the rotated rows into those of the rows."""
+    _rope(p, (_lib or lib()).mita_rope_backward, dQo, dKo, dQ, dK, pos, stream)

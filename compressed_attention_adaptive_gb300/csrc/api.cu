@@ -14,6 +14,7 @@
 #include "../../include/mita.h"
 #include "cache.cuh"
 #include "internal.h"
+#include "rope.cuh"
 
 namespace mita {
 
@@ -383,6 +384,126 @@ static mita_status cache_begin(const mita_cache_params* p, bool attention, Cache
     return MITA_OK;
 }
 
+// Workspace of an eviction: the status word and the moves of each (sequence, head).
+static int* carve_evict(const mita_cache_params* p, void* ws, int** moves, size_t* bytes) {
+    Carver c(ws);
+    int* status = c.take<int>(64);
+    *moves = c.take<int>((size_t)p->B * p->H_kv * 2 * (((size_t)p->max_pages * p->page + 1) / 2));
+    *bytes = align_up(c.off, 1024);
+    return status;
+}
+
+// ----------------------------------------------------------------- rotation
+
+static mita_status check_rope(const mita_rope_params* p) {
+    if (!p) return fail(MITA_ERR_INVALID_ARG, "params is NULL");
+    if (p->B < 1 || p->H < 1 || p->H_kv < 0 || p->T < 1)
+        return fail(MITA_ERR_INVALID_ARG, "B, H, T must be >= 1 and H_kv >= 0");
+    if (p->d < 2 || p->d > 2 * MITA_ROPE_PAIRS || p->d % 2)
+        return fail(MITA_ERR_INVALID_ARG, "d must be even, in [2, %d]", 2 * MITA_ROPE_PAIRS);
+    if (p->rot < 2 || p->rot > p->d || p->rot % 2) return fail(MITA_ERR_INVALID_ARG, "rot must be even, in [2, d]");
+    if (!isfinite(p->gain)) return fail(MITA_ERR_INVALID_ARG, "gain must be finite");
+    if (p->flags & ~(unsigned)MITA_FLAG_INTERLEAVED) return fail(MITA_ERR_INVALID_ARG, "unknown flag");
+    if (p->dtype != MITA_DTYPE_F32 && p->dtype != MITA_DTYPE_BF16) return fail(MITA_ERR_INVALID_ARG, "bad dtype");
+    for (int i = 0; i < p->rot / 2; ++i)
+        if (!isfinite(p->freqs[i])) return fail(MITA_ERR_INVALID_ARG, "freqs must be finite");
+    if ((long long)p->H + p->H_kv > 65535) return fail(MITA_ERR_UNSUPPORTED, "H + H_kv must be <= 65535");
+    if ((long long)p->B * p->T > (1LL << 30)) return fail(MITA_ERR_UNSUPPORTED, "B*T must be <= 2^30");
+    return MITA_OK;
+}
+
+// Rows [B, H, T, d] in memory.
+struct Rows {
+    const void* p;
+    int B, H, T, d, elem;
+    const long long* s;  // batch, head and row stride in elements
+
+    long long reach() const { return (B - 1LL) * s[0] + (H - 1LL) * s[1] + (T - 1LL) * s[2] + d; }  // elements
+    bool counts() const {  // in 64 bits
+        return (double)(B - 1) * s[0] + (double)(H - 1) * s[1] + (double)(T - 1) * s[2] + d < 1e17;
+    }
+    // Whether no two rows share an element (or so it seems: strides that nest).
+    bool apart() const {
+        std::pair<long long, int> dims[3] = {{s[0], B}, {s[1], H}, {s[2], T}};
+        std::sort(dims, dims + 3);
+        long long inner = d;
+        for (const auto& x : dims) {
+            if (x.second == 1) continue;
+            if (x.first < inner) return false;
+            inner += x.first * (x.second - 1);
+        }
+        return true;
+    }
+    bool same(const Rows& o) const {
+        return p == o.p && (B == 1 || s[0] == o.s[0]) && (H == 1 || s[1] == o.s[1]) && (T == 1 || s[2] == o.s[2]);
+    }
+};
+
+// Whether x and y (of the same B and T) share no element: their ranges do not meet, or
+// both have their rows at multiples of one distance and places of their own between them.
+static bool disjoint(const Rows& x, const Rows& y) {
+    if (!overlap(x.p, (size_t)x.reach() * x.elem, y.p, (size_t)y.reach() * y.elem)) return true;
+    if ((x.B > 1 && x.s[0] != y.s[0]) || (x.T > 1 && x.s[2] != y.s[2]) || (x.B == 1 && x.T == 1)) return false;
+    const long long bs = x.B > 1 ? x.s[0] : x.s[2], ts = x.T > 1 ? x.s[2] : x.s[0], step = std::min(bs, ts);
+    if (step < 1 || std::max(bs, ts) % step) return false;
+    const long long fx = (x.H - 1) * x.s[1] + x.d, fy = (y.H - 1) * y.s[1] + y.d;
+    const long long by = (long long)((intptr_t)y.p - (intptr_t)x.p);
+    if (by % x.elem) return false;
+    const long long at = ((by / x.elem) % step + step) % step;
+    return at >= fx && at + fy <= step;
+}
+
+static mita_status run_rope(const mita_rope_params* p, bool back, const void* Q, const void* K, void* Qo, void* Ko,
+                            const int64_t* strides, const int32_t* pos, int64_t pos_stride, void* stream) {
+    const mita_status st = check_rope(p);
+    if (st) return st;
+    const int elem = p->dtype == MITA_DTYPE_F32 ? 4 : 2, n = p->H_kv ? 2 : 1;
+    if (!Q || !Qo || (p->H_kv && (!K || !Ko))) return fail(MITA_ERR_INVALID_ARG, "rows must be device pointers");
+    if (!p->H_kv && (K || Ko)) return fail(MITA_ERR_INVALID_ARG, "K and Ko must be NULL with H_kv = 0");
+    if (((uintptr_t)Q | (uintptr_t)K | (uintptr_t)Qo | (uintptr_t)Ko) % elem || (uintptr_t)pos % 4)
+        return fail(MITA_ERR_INVALID_ARG, "pointers must be aligned to their elements");
+    RopeArgs a{};
+    a.B = p->B; a.H = p->H; a.Hkv = p->H_kv; a.T = p->T; a.d = p->d; a.rot = p->rot;
+    a.back = back;
+    a.gain = p->gain == 0.0f ? 1.0f : p->gain;
+    a.in[0] = Q; a.in[1] = K; a.out[0] = Qo; a.out[1] = Ko;
+    a.pos = pos; a.pos_stride = pos_stride;
+    Rows in[2], out[2];
+    for (int w = 0; w < n; ++w) {
+        const int H = w ? p->H_kv : p->H;
+        for (int i = 0; i < 3; ++i) {
+            const long long whole = i == 0 ? (long long)H * p->T * p->d : i == 1 ? (long long)p->T * p->d : p->d;
+            a.is[w][i] = strides ? strides[3 * w + i] : whole;
+            a.os[w][i] = strides ? strides[6 + 3 * w + i] : whole;
+            if (a.is[w][i] < 0 || a.os[w][i] < 0) return fail(MITA_ERR_INVALID_ARG, "strides must be >= 0");
+            if ((i == 0 ? p->B : i == 1 ? H : p->T) == 1) a.is[w][i] = a.os[w][i] = 0;  // not used
+        }
+        in[w] = Rows{a.in[w], p->B, H, p->T, p->d, elem, a.is[w]};
+        out[w] = Rows{a.out[w], p->B, H, p->T, p->d, elem, a.os[w]};
+        if (!in[w].counts() || !out[w].counts()) return fail(MITA_ERR_UNSUPPORTED, "strides too large");
+        if (!out[w].apart()) return fail(MITA_ERR_INVALID_ARG, "rows of an output must not overlap");
+        a.same[w] = in[w].same(out[w]);
+    }
+    if (pos_stride < 0 || (double)(p->B - 1) * pos_stride > 1e17)
+        return fail(MITA_ERR_INVALID_ARG, "pos_stride must be >= 0 and not too large");
+    for (int w = 0; w < n; ++w) {
+        for (int x = 0; x < n; ++x)
+            if (!(x == w && a.same[w]) && !disjoint(in[x], out[w]))
+                return fail(MITA_ERR_INVALID_ARG, "an output must not overlap an input other than its own in place");
+        if (pos && overlap(pos, 4 * (size_t)((p->B - 1) * pos_stride + p->T), out[w].p, (size_t)out[w].reach() * elem))
+            return fail(MITA_ERR_INVALID_ARG, "an output must not overlap pos");
+    }
+    if (n == 2 && !disjoint(out[0], out[1])) return fail(MITA_ERR_INVALID_ARG, "outputs must not overlap");
+    for (int i = 0; i < p->rot / 2; ++i) {
+        const double turns = p->freqs[i] * 0.15915494309189535;  // 1 / (2 pi)
+        const double part = turns - floor(turns);
+        a.turns[i] = part < 1.0 ? (unsigned long long)ldexp(part, 64) : 0;
+    }
+    MITA_CUDA(launch_rope(a, p->dtype, p->flags & MITA_FLAG_INTERLEAVED, (cudaStream_t)stream), "rope");
+    prof_mark((cudaStream_t)stream, "");
+    return MITA_OK;
+}
+
 }  // namespace mita
 
 using namespace mita;
@@ -703,6 +824,124 @@ mita_status mita_cache_attention(const mita_cache_params* p, const void* Q, cons
               "cache attention");
     prof_mark((cudaStream_t)stream, "");
     return MITA_OK;
+}
+
+mita_status mita_cache_weights(const mita_cache_params* p, const void* Q, const void* cache, const int32_t* table,
+                               const int32_t* len, const int32_t* count, const int32_t* exps, const float* lse,
+                               float decay, const float* acc, float* acc_out, void* ws, size_t ws_bytes,
+                               void* stream) {
+    g_last_error.clear();
+    CacheArgs a;
+    CachePlan plan;
+    CacheWork w;
+    const mita_status st = cache_begin(p, false, &a, &plan, &w, Q, Q, cache, table, len, count, exps, ws, ws_bytes);
+    if (st) return st;
+    if (!(decay >= 0.0f) || isinf(decay)) return fail(MITA_ERR_INVALID_ARG, "decay must be finite and >= 0");
+    if (!lse || !acc_out || (decay != 0.0f && !acc) || ((uintptr_t)lse | (uintptr_t)acc | (uintptr_t)acc_out) % 4)
+        return fail(MITA_ERR_INVALID_ARG, "lse, acc and acc_out must be 4-byte aligned device pointers");
+    const size_t n = (size_t)p->B * p->H_kv * p->max_pages * p->page * sizeof(float);
+    if ((acc && acc != acc_out && overlap(acc, n, acc_out, n)) || overlap(Q, cache_bytes(p, p->H), acc_out, n) ||
+        overlap(lse, (size_t)p->B * p->H * p->T * sizeof(float), acc_out, n))
+        return fail(MITA_ERR_INVALID_ARG, "acc_out must not overlap Q, lse or acc (but may be acc)");
+    MITA_CUDA(launch_cache_weigh(a, p->d, p->dtype, p->flags, Q, cache, lse, decay, acc, acc_out, (cudaStream_t)stream),
+              "cache weights");
+    prof_mark((cudaStream_t)stream, "");
+    return MITA_OK;
+}
+
+size_t mita_cache_evict_workspace_size(const mita_cache_params* p) {
+    CacheArgs a;
+    CachePlan plan;
+    if (resolve_cache(p, false, &a, &plan)) return 0;
+    size_t bytes;
+    int* moves;
+    carve_evict(p, nullptr, &moves, &bytes);
+    return bytes;
+}
+
+mita_status mita_cache_evict(const mita_cache_params* p, void* cache, const int32_t* table, const int32_t* len,
+                             const int32_t* keep, int first, int recent, const float* acc, int32_t* len_out,
+                             float* acc_out, int32_t* src_out, void* ws, size_t ws_bytes, void* stream) {
+    g_last_error.clear();
+    CacheArgs a;
+    CachePlan plan;
+    const mita_status st = resolve_cache(p, false, &a, &plan);
+    if (st) return st;
+    if (!cache || !aligned16(cache)) return fail(MITA_ERR_INVALID_ARG, "cache must be a 16-byte aligned device pointer");
+    if (!table || !len || !keep || !acc || !len_out || !acc_out ||
+        ((uintptr_t)table | (uintptr_t)len | (uintptr_t)keep | (uintptr_t)acc | (uintptr_t)len_out | (uintptr_t)acc_out |
+         (uintptr_t)src_out) % 4)
+        return fail(MITA_ERR_INVALID_ARG, "table, len, keep, acc, len_out and acc_out must be 4-byte aligned device pointers");
+    if (first < 0 || recent < 0) return fail(MITA_ERR_INVALID_ARG, "first and recent must be >= 0");
+    const size_t places = (size_t)p->max_pages * p->page, n = (size_t)p->B * p->H_kv * places * 4, nb = (size_t)p->B * 4;
+    const size_t pool = (size_t)p->n_pages * p->H_kv * a.pgroups * (18 * (size_t)p->d);
+    struct Range {
+        const void* p;
+        size_t n;
+    };
+    const Range ins[] = {{table, nb * p->max_pages}, {len, nb}, {keep, nb}, {acc, n}};
+    const Range outs[] = {{len_out, nb}, {acc_out, n}, {src_out, src_out ? n : 0}, {cache, pool}};
+    for (int i = 0; i < 4; ++i) {
+        if (!outs[i].p) continue;
+        for (const Range& x : ins)
+            if (!(i < 2 && x.p == outs[i].p && x.n == outs[i].n && (i == 0 ? x.p == len : x.p == acc)) &&
+                overlap(x.p, x.n, outs[i].p, outs[i].n))
+                return fail(MITA_ERR_INVALID_ARG, "outputs must not overlap inputs (but len_out may be len, and acc_out acc)");
+        for (int j = 0; j < i; ++j)
+            if (outs[j].p && overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n))
+                return fail(MITA_ERR_INVALID_ARG, "outputs must not overlap each other or the cache");
+    }
+    size_t need;
+    EvictArgs e{keep, first, recent, acc, acc_out, src_out, len_out, nullptr, (long long)places};
+    carve_evict(p, nullptr, &e.moves, &need);
+    if (!ws) return fail(MITA_ERR_WORKSPACE, "workspace is NULL");
+    if ((uintptr_t)ws % 256) return fail(MITA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    if (ws_bytes < need) return fail(MITA_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+    a.table = table; a.len = len;
+    a.status = carve_evict(p, ws, &e.moves, &need);
+    MITA_CUDA(launch_cache_evict(a, e, p->d, cache, (cudaStream_t)stream), "cache evict");
+    prof_mark((cudaStream_t)stream, "");
+    return MITA_OK;
+}
+
+mita_status mita_rope_frequencies(mita_rope_params* p, double base, int scaling, double factor, double original,
+                                  double low, double high) {
+    g_last_error.clear();
+    if (!p) return fail(MITA_ERR_INVALID_ARG, "params is NULL");
+    if (p->rot < 2 || p->rot > 2 * MITA_ROPE_PAIRS || p->rot % 2)
+        return fail(MITA_ERR_INVALID_ARG, "rot must be even, in [2, %d]", 2 * MITA_ROPE_PAIRS);
+    if (!(base > 1.0) || !isfinite(base)) return fail(MITA_ERR_INVALID_ARG, "base must be finite and > 1");
+    if (scaling < MITA_ROPE_PLAIN || scaling > MITA_ROPE_PARTS) return fail(MITA_ERR_INVALID_ARG, "unknown scaling");
+    if (scaling != MITA_ROPE_PLAIN && (!(factor >= 1.0) || !isfinite(factor)))
+        return fail(MITA_ERR_INVALID_ARG, "factor must be finite and >= 1");
+    if (scaling == MITA_ROPE_PARTS &&
+        (!(original > 0.0) || !isfinite(original) || !isfinite(low) || !isfinite(high) || !(low < high)))
+        return fail(MITA_ERR_INVALID_ARG, "original must be > 0 and low < high, all finite");
+    const int rot = p->rot;
+    if (scaling == MITA_ROPE_NTK && rot > 2) base *= pow(factor, rot / (rot - 2.0));
+    if (!isfinite(base)) return fail(MITA_ERR_INVALID_ARG, "base and factor too large");
+    for (int i = 0; i < rot / 2; ++i) {
+        double f = pow(base, -2.0 * i / rot);
+        if (scaling == MITA_ROPE_LINEAR) f /= factor;
+        if (scaling == MITA_ROPE_PARTS) {
+            const double g = std::min(1.0, std::max(0.0, (original * f / 6.283185307179586 - low) / (high - low)));
+            f *= g + (1.0 - g) / factor;
+        }
+        p->freqs[i] = f;
+    }
+    return MITA_OK;
+}
+
+mita_status mita_rope(const mita_rope_params* p, const void* Q, const void* K, void* Qo, void* Ko,
+                      const int64_t* strides, const int32_t* pos, int64_t pos_stride, void* stream) {
+    g_last_error.clear();
+    return run_rope(p, false, Q, K, Qo, Ko, strides, pos, pos_stride, stream);
+}
+
+mita_status mita_rope_backward(const mita_rope_params* p, const void* dQo, const void* dKo, void* dQ, void* dK,
+                               const int64_t* strides, const int32_t* pos, int64_t pos_stride, void* stream) {
+    g_last_error.clear();
+    return run_rope(p, true, dQo, dKo, dQ, dK, strides, pos, pos_stride, stream);
 }
 
 }  // extern "C"

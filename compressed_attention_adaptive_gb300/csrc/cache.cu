@@ -163,42 +163,10 @@ template <int D> struct BlockAt {
     __device__ __forceinline__ long long element() const { return (long long)row * D + blk * 16; }
 };
 
-// Run by one whole block of a call: checks every index that the call uses and
-// stores the call's status word; the other blocks only leave out what is out of
-// range. One block can do it for all: a page's entry is 4 bytes, its rows at least
-// 1152 bytes for each head. A thread takes a sequence, with its pages if they are
-// few; the block takes the others' pages together.
+// Run by one whole block of a call: checks every index that the call uses and stores the
+// call's status word; the other blocks only leave out what is out of range.
 __device__ __forceinline__ void check_call(const CacheArgs& a) {
-    constexpr int kFewPages = 4;
-    bool bad = bad_exps(a);
-    for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
-        const int b = b0 + threadIdx.x;
-        int first = 0, last = 0;
-        if (b < a.B) {
-            const int n = cache_len(a, b), c = cache_count(a, b);
-            bad |= bad_len(a, b) || c > n;
-            if (c > 0) {
-                first = max(n - c, 0) / a.page;
-                last = (n + a.page - 1) / a.page;
-            }
-        }
-        const bool few = last - first <= kFewPages;
-        if (few)
-            for (int i = first; i < last; ++i)
-                bad |= (unsigned)a.table[(long long)b * a.cols + i] >= (unsigned)a.n_pages;
-        if (!__syncthreads_or(!few)) continue;
-        __shared__ int2 range[256];
-        range[threadIdx.x] = few ? make_int2(0, 0) : make_int2(first, last);
-        __syncthreads();
-        const int lane = threadIdx.x & 31;
-        for (int s = threadIdx.x >> 5; s < 256 && b0 + s < a.B; s += 8) {  // a warp a sequence
-            const int* tb = a.table + (long long)(b0 + s) * a.cols;
-#pragma unroll 8
-            for (int i = range[s].x + lane; i < range[s].y; i += 32) bad |= (unsigned)tb[i] >= (unsigned)a.n_pages;
-        }
-        __syncthreads();
-    }
-    bad = __syncthreads_or(bad);
+    const bool bad = __syncthreads_or(bad_call<false>(a));
     if (threadIdx.x == 0) *a.status = bad ? kStBounds : kStOk;
 }
 

@@ -89,6 +89,20 @@ struct CacheParts {
 // cache.cu
 cudaError_t launch_cache_rows(const CacheArgs& a, int d, int dtype, bool write, void* K, void* V, void* cache,
                               cudaStream_t st);
+// cache_weigh.cu
+cudaError_t launch_cache_weigh(const CacheArgs& a, int d, int dtype, unsigned flags, const void* Q, const void* cache,
+                               const float* lse, float decay, const float* acc, float* acc_out, cudaStream_t st);
+// cache_evict.cu
+struct EvictArgs {
+    const int* keep;
+    int first, recent;
+    const float* acc;
+    float* acc_out;  // may be acc
+    int *src, *len_out;
+    int* moves;     // [B * Hkv][2][half]: places that are freed, places that move there
+    long long cap;  // places of a sequence
+};
+cudaError_t launch_cache_evict(const CacheArgs& a, const EvictArgs& e, int d, void* cache, cudaStream_t st);
 // cache_attn.cu
 CachePlan cache_attn_plan(const CacheArgs& a, int d, int dtype, unsigned flags);
 long long cache_spin(bool stall);
@@ -125,6 +139,44 @@ __device__ __forceinline__ bool bad_exps(const CacheArgs& a) {
     if (a.exps)
         for (int i = threadIdx.x; i < 2 * a.Hkv; i += blockDim.x)
             bad |= (unsigned)a.exps[i] + kMaxExp > 2u * kMaxExp;
+    return bad;
+}
+
+// Whether an index that a call uses is out of range, as far as the calling thread has looked;
+// run by one whole block of 256 threads. One block can do it for all: a page's entry is 4 bytes, its
+// rows at least 1152 bytes for each head. A thread takes a sequence, with its pages if they are
+// few; the block takes the others' pages together. WHOLE: the call uses all places of a sequence, else its
+// own rows, which then have to be among them.
+template <bool WHOLE> __device__ __forceinline__ bool bad_call(const CacheArgs& a) {
+    constexpr int kFewPages = 4;
+    bool bad = bad_exps(a);
+    for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
+        const int b = b0 + threadIdx.x;
+        int first = 0, last = 0;
+        if (b < a.B) {
+            const int n = cache_len(a, b), c = WHOLE ? n : cache_count(a, b);
+            bad |= bad_len(a, b) || c > n;
+            if (c > 0) {
+                first = max(n - c, 0) / a.page;
+                last = (n + a.page - 1) / a.page;
+            }
+        }
+        const bool few = last - first <= kFewPages;
+        if (few)
+            for (int i = first; i < last; ++i)
+                bad |= (unsigned)a.table[(long long)b * a.cols + i] >= (unsigned)a.n_pages;
+        if (!__syncthreads_or(!few)) continue;
+        __shared__ int2 range[256];
+        range[threadIdx.x] = few ? make_int2(0, 0) : make_int2(first, last);
+        __syncthreads();
+        const int lane = threadIdx.x & 31;
+        for (int s = threadIdx.x >> 5; s < 256 && b0 + s < a.B; s += 8) {  // a warp a sequence
+            const int* tb = a.table + (long long)(b0 + s) * a.cols;
+#pragma unroll 8
+            for (int i = range[s].x + lane; i < range[s].y; i += 32) bad |= (unsigned)tb[i] >= (unsigned)a.n_pages;
+        }
+        __syncthreads();
+    }
     return bad;
 }
 

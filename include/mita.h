@@ -81,7 +81,9 @@ enum {
      * slots are on, and on the CUDA-core path (float32, or MITA_FLAG_SIMT);
      * other shapes return MITA_ERR_UNSUPPORTED. With 2-D pooling it is
      * MITA_ERR_INVALID_ARG. */
-    MITA_FLAG_CAUSAL = 1u << 2
+    MITA_FLAG_CAUSAL = 1u << 2,
+    /* mita_rope only: pairs are neighbouring channels. */
+    MITA_FLAG_INTERLEAVED = 1u << 3
 };
 
 /* Fault test of the device-side failure detection, not for production: in
@@ -323,6 +325,112 @@ mita_status mita_cache_attention(const mita_cache_params* p, const void* Q, cons
                                  const int32_t* len, const int32_t* count, const int32_t* exps, void* O,
                                  float* lse_out, void* ws, size_t ws_bytes, void* stream);
 
+/* ---- what cached tokens are worth, and eviction ------------------------------
+ * Not part of the method (the summaries have no counterpart): keeps the cache of a
+ * long generation within a budget. After a call's rows have attended,
+ * mita_cache_weights() adds the attention weight that each cached token got from
+ * them to its sum; mita_cache_evict() keeps the tokens of each cache head with the
+ * largest sums. Sums are float32 [B][H_kv][max_pages * page], by place.
+ *
+ * Weights. For each token j < len[b] and cache head h
+ *   acc_out[b][h][j] = decay * acc[b][h][j]  (0 for the call's own tokens, j >= len[b] - count[b])
+ *                      + sum over the rows t < count[b] and the query heads of h that see j
+ *                        of exp(scale q.k_j - lse[b][head][t])
+ * with the keys that a row sees, Q, table, len, count and exps as in
+ * mita_cache_attention(), and lse what that call returned (any float32 [B, H, T]
+ * with the rows' log sums). A token that a row does not see gets nothing of it, so a
+ * row that sees no key is harmless; no weight is above 1 (a rounded lse may be below a score);
+ * a row with a NaN or an infinity in Q, or whose lse
+ * is NaN, makes the sums of the tokens that it sees NaN. Places j >= len[b] are left
+ * as they were. acc_out may be acc; otherwise they must not overlap, and Q and lse must not
+ * overlap acc_out. decay is finite, >= 0; with 0 acc is not read and may be NULL. The sum
+ * of an own token starts at 0 whatever its place held before, so sums need no initial value.
+ * A sequence with count[b] = 0 has its sums decayed. The same call gives the same bits.
+ * Scores, weights and sums are fp32; float32 rows enter as two halves (22 bits), bf16
+ * rows exactly. With MITA_FLAG_SIMT fp32 throughout, on CUDA cores. The workspace is that of
+ * mita_cache_workspace_size(). */
+mita_status mita_cache_weights(const mita_cache_params* p, const void* Q, const void* cache, const int32_t* table,
+                               const int32_t* len, const int32_t* count, const int32_t* exps, const float* lse,
+                               float decay, const float* acc, float* acc_out, void* ws, size_t ws_bytes,
+                               void* stream);
+
+/* Eviction. keep int32 [B] (device): the tokens that sequence b keeps. A sequence with
+ * len[b] <= keep[b] stays as it is. Of the others each cache head keeps its first `first` and
+ * its last `recent` tokens and, of those between, the keep[b] - first - recent with the largest
+ * acc (ties to the lower place; NaN counts as the largest, -0 as 0). The kept rows at places
+ * j >= keep[b] move, in ascending order, to the places that were freed below keep[b], in
+ * ascending order; the other kept rows stay where they are. Keys and values move as they are
+ * held, without another rounding. (Places are not positions, then: a caller that rotates by
+ * position counts positions itself. Heads of one sequence keep different tokens.)
+ *   len_out  int32 [B]: min(len[b], keep[b]). May be len.
+ *   acc_out  float32 like acc: the sums of the rows now at j < len_out[b]. May be acc.
+ *   src_out  int32 [B][H_kv][max_pages * page] or NULL: the place that the row now at
+ *            j < len_out[b] had, to carry anything else along.
+ * Places from len_out[b] on keep what they held in acc_out and src_out, and in the cache. Other
+ * overlaps of outputs with anything are refused. Pages that the call writes (those of places below
+ * keep[b] of a sequence that is cut) must not be shared with another sequence.
+ * Uses B, H_kv, d, page, n_pages and max_pages of p. first, recent >= 0. Out of range: as
+ * above, and a budget keep[b] below first + recent; a sequence whose length or budget is out of
+ * range is left as it was, with len_out[b] = len[b]. */
+size_t mita_cache_evict_workspace_size(const mita_cache_params* p);
+mita_status mita_cache_evict(const mita_cache_params* p, void* cache, const int32_t* table, const int32_t* len,
+                             const int32_t* keep, int first, int recent, const float* acc, int32_t* len_out,
+                             float* acc_out, int32_t* src_out, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- rotary positions ----------------------------------------------------------
+ * Not part of the method (the summaries have no counterpart): turns the rows of Q and K by
+ * their positions before mita_forward(), mita_cache_write() and mita_cache_attention().
+ * Pair i of the first `rot` channels of a row at position t is turned by the angle
+ * a = t * freqs[i] and scaled:
+ *   y0 = gain (x0 cos a - x1 sin a),  y1 = gain (x0 sin a + x1 cos a);
+ * the other channels are copied. Pair i is channels i and i + rot / 2, or with
+ * MITA_FLAG_INTERLEAVED 2 i and 2 i + 1. Angles are reduced exactly in 64-bit integers (a
+ * position times a frequency in turns), so far positions lose nothing: cos and sin are off by
+ * about 2^-23. Products and sums are fp32, rounded once to `dtype`. */
+#define MITA_ROPE_PAIRS 128
+typedef struct {
+    int B, H, H_kv;   /* sequences, query heads, key heads (H_kv = 0: Q alone)     */
+    int T, d;         /* rows per sequence; head dim: even, 2 .. 256               */
+    int rot;          /* channels that are rotated: even, 2 .. d                   */
+    float gain;       /* 0 means 1                                                 */
+    unsigned flags;   /* MITA_FLAG_INTERLEAVED                                     */
+    int dtype;        /* mita_dtype of all rows                                    */
+    double freqs[MITA_ROPE_PAIRS]; /* radians per position of pair i < rot / 2     */
+} mita_rope_params;
+
+enum {
+    MITA_ROPE_PLAIN = 0,  /* base^(-2 i / rot)                                                     */
+    MITA_ROPE_LINEAR = 1, /* that / factor: positions of a longer context squeezed into the first  */
+    MITA_ROPE_NTK = 2,    /* base * factor^(rot / (rot - 2)) in place of base: the slowest pair
+                             is slowed by factor, the fastest not (rot = 2: plain)                 */
+    MITA_ROPE_PARTS = 3   /* by the turns r = original f / (2 pi) that a pair makes over the
+                             original length: f (g + (1 - g) / factor) with
+                             g = clamp((r - low) / (high - low), 0, 1)                             */
+};
+
+/* Fills p->freqs[0 .. rot / 2) (of p only rot is read). base > 1; factor >= 1 for the scaled
+ * forms; original > 0 and low < high for MITA_ROPE_PARTS (ignored otherwise). */
+mita_status mita_rope_frequencies(mita_rope_params* p, double base, int scaling, double factor, double original,
+                                  double low, double high);
+
+/* Rotates Q [B, H, T, d] into Qo and K [B, H_kv, T, d] into Ko (K and Ko NULL with H_kv = 0).
+ * strides: 12 numbers of elements (host memory): batch, head and row stride of Q, K, Qo and Ko in turn;
+ * NULL: all contiguous. So a projection's [B, T, heads, d] can be read where it is and written as
+ * the other calls want it. Channels are contiguous. Inputs may repeat rows (stride 0), an
+ * output's rows must not overlap. Qo may be Q with the same strides (in place), Ko likewise K;
+ * an output must not share elements with anything else: what cannot be told apart by its range, or
+ * row by row with equal batch and row strides, is refused. pos int32 (device): row t of
+ * sequence b is at position pos[b * pos_stride + t] (any int32; pos_stride >= 0, 0 for positions
+ * that all sequences share); NULL: at t. Pointers are aligned to their elements; 16-byte aligned
+ * rows are faster. No workspace, no device status. */
+mita_status mita_rope(const mita_rope_params* p, const void* Q, const void* K, void* Qo, void* Ko,
+                      const int64_t* strides, const int32_t* pos, int64_t pos_stride, void* stream);
+
+/* The backward pass: the transposed map (angles negated, the same gain) of gradients dQo, dKo with
+ * respect to the rotated rows into dQ, dK. Its arguments are those of mita_rope. */
+mita_status mita_rope_backward(const mita_rope_params* p, const void* dQo, const void* dKo, void* dQ, void* dK,
+                               const int64_t* strides, const int32_t* pos, int64_t pos_stride, void* stream);
+
 /* ---- measurement hooks (not part of the method) ---------------------------
  * Number of kernels this library has launched in the process so far. */
 long long mita_launch_count(void);
@@ -332,7 +440,7 @@ long long mita_launch_count(void);
  * sample and threshold, landmark pass, top-k selection, shared-expert combine,
  * routing, bucketing, the shared slots' own pass when there are more than 128
  * landmarks, expert attention, merge; the cache calls: write, read, attention,
- * join) and at its end; up to max_marks events
+ * join, weights, evict; rope) and at its end; up to max_marks events
  * in total (created here, kept for reuse). Process-wide; not for concurrent
  * calls. */
 mita_status mita_profile_begin(int max_marks);

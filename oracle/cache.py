@@ -53,3 +53,30 @@ def attention(q, k, v, limits, scale):
         o[r], spread[r] = (p @ v[:m]) / p.sum(), (p @ np.abs(v[:m])) / p.sum()
         lse[r] = z.max() + np.log(p.sum())
     return o, lse, spread
+
+
+def weights(q, k, limits, lse, scale):
+    """w [rows, n]: exp(scale q.k_j - lse_r), at most 1, of the keys j < limits[r] that
+    row r sees, 0 of the others (q [rows, d], k [n, d], lse [rows], all fp64)."""
+    w = np.zeros((len(q), len(k)))
+    for r, m in enumerate(limits):
+        if m > 0:
+            w[r, :m] = np.exp(np.minimum((k[:m] @ q[r]) * scale - lse[r], 0.0))
+    return w
+
+
+def evict(acc, keep, first, recent):
+    """src: the place that the row at each place j < min(len, keep) had, for one head's
+    sums acc [len]. Straight from the definition in include/mita.h, with Python's sort."""
+    n = len(acc)
+    if n <= keep:
+        return np.arange(n)
+    between = list(range(first, n - recent))
+    value = lambda j: np.inf if np.isnan(acc[j]) else float(acc[j]) + 0.0
+    between.sort(key=lambda j: (not np.isnan(acc[j]), -value(j), j))
+    stay = set(range(first)) | set(range(n - recent, n)) | set(between[:keep - first - recent])
+    free = [j for j in range(keep) if j not in stay]
+    move = sorted(j for j in stay if j >= keep)
+    src = np.arange(keep)
+    src[free] = move
+    return src
