@@ -143,7 +143,7 @@ __device__ __forceinline__ bool bad_exps(const CacheArgs& a) {
 }
 
 // Whether an index that a call uses is out of range, as far as the calling thread has looked;
-// run by one whole block of 256 threads. One block can do it for all: a page's entry is 4 bytes, its
+// run by one whole block of at most 256 threads. One block can do it for all: a page's entry is 4 bytes, its
 // rows at least 1152 bytes for each head. A thread takes a sequence, with its pages if they are
 // few; the block takes the others' pages together. WHOLE: the call uses all places of a sequence, else its
 // own rows, which then have to be among them.
@@ -170,7 +170,7 @@ template <bool WHOLE> __device__ __forceinline__ bool bad_call(const CacheArgs& 
         range[threadIdx.x] = few ? make_int2(0, 0) : make_int2(first, last);
         __syncthreads();
         const int lane = threadIdx.x & 31;
-        for (int s = threadIdx.x >> 5; s < 256 && b0 + s < a.B; s += 8) {  // a warp a sequence
+        for (int s = threadIdx.x >> 5; s < blockDim.x && b0 + s < a.B; s += blockDim.x >> 5) {  // a warp a sequence
             const int* tb = a.table + (long long)(b0 + s) * a.cols;
 #pragma unroll 8
             for (int i = range[s].x + lane; i < range[s].y; i += 32) bad |= (unsigned)tb[i] >= (unsigned)a.n_pages;

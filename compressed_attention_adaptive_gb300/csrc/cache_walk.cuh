@@ -311,6 +311,24 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
                  "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
                  : "memory");
 }
+// An m16n8k16 step of the tensor cores, halves in and fp32 sums.
+__device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same onto zeros.
+__device__ __forceinline__ void mma_f16_first(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -321,9 +339,13 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 // largest entry, of biased exponent ex, in [2^14, 2^15); f: the factor of the
 // scores for it, in log2 units. A row with an infinity or a NaN becomes NaN
 // altogether, as its softmax is (infinite scores have no differences).
-__device__ __forceinline__ void query_scale(const CacheArgs& a, int h, int ex, float* up, float* f) {
+__device__ __forceinline__ int query_exp(int ex, float* up) {
     const int qe = min(141 - ex, 120);
     *up = ex == 255 ? __int_as_float(0x7fc00000) : pow2(qe);
+    return qe;
+}
+__device__ __forceinline__ void query_scale(const CacheArgs& a, int h, int ex, float* up, float* f) {
+    const int qe = query_exp(ex, up);
     // kept away from 0 and infinity: a masked score is -infinity times it
     *f = fminf(fmaxf(a.scale * kLog2e * pow2(cache_exp(a, 0, h)) * pow2(-qe), 1.1754944e-38f), 3.4028235e38f);
 }

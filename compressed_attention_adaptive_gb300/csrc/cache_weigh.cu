@@ -13,15 +13,14 @@
 // added in an order of its own, whatever the cut, so the same call gives the same bits.
 #include <algorithm>
 
-#include "cache.cuh"
-#include "tc.cuh"
+#include "cache_walk.cuh"
 
 namespace mita {
 
 namespace {
 
-constexpr int kThreads = 128;  // of a block
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kThreads = 256, kWarps = kThreads / 32;  // of a block
+constexpr int kAhead = 4;                              // groups that a warp's loads are ahead
 
 struct WeighArgs {
     const float* lse;
@@ -33,7 +32,7 @@ struct WeighArgs {
 
 // Where a warp is on the line. begin() is called by the whole block.
 struct LineStart {
-    unsigned long long before[kThreads], warps[kThreads / 32];
+    unsigned long long before[kThreads], warps[kWarps];
 };
 struct Place {
     int b, h, g, groups, n, count;  // sequence, cache head, group of it; the sequence's
@@ -65,7 +64,7 @@ struct Place {
         __syncthreads();
         unsigned long long total = 0, base = 0;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
             if (w == warp) base = total;
             total += s.warps[w];
         }
@@ -113,16 +112,6 @@ struct Place {
     }
 };
 
-__device__ __forceinline__ int rows_of(const CacheArgs& a, int count) { return count * a.G; }
-// Row r of a sequence: token r / G of the call, query head h G + r % G.
-__device__ __forceinline__ long long row_offset(const CacheArgs& a, int b, int h, int r, int* t) {
-    *t = r / a.G;
-    return ((long long)(b * a.H + h * a.G + (r - *t * a.G)) * a.T + *t);
-}
-// Keys that token t of the call sees.
-__device__ __forceinline__ int row_limit(const CacheArgs& a, int n, int count, int t) {
-    return a.causal ? max(n - (count - 1 - t), 0) : n;
-}
 // exp(z - lse), at most 1, for a score z = dot f: one rounding of the difference, so that the weights that
 // matter, whose scores are near lse, keep their bits. (Scores of 2^28 and more are further from
 // a rounded lse than exponents reach; a sum that became infinite would stay so.) NaN stays NaN.
@@ -134,6 +123,12 @@ __device__ __forceinline__ float weight(float dot, float f, float lse) {
 
 }  // namespace
 
+// The call's first block: its status word.
+__device__ __forceinline__ void check(const CacheArgs& a) {
+    const bool bad = __syncthreads_or(bad_call<true>(a));
+    if (threadIdx.x == 0) *a.status = bad ? kStBounds : kStOk;
+}
+
 // ------------------------------------------------------------ CUDA cores
 
 // fp32 throughout: eight lanes share a token, each with the d/8 channels of two blocks' halves or of one
@@ -144,9 +139,13 @@ k_cache_weigh_simt(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint
     using L = Grp<D>;
     constexpr int E = D / 8;  // channels of a lane
     __shared__ LineStart start;
+    if (blockIdx.x == 0) {
+        check(a);
+        return;
+    }
     const int lane = threadIdx.x & 31, sub = lane >> 3, ch = lane & 7, blk = D == 128 ? ch : ch >> 1;
     Place at;
-    at.begin(a, start, (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), (long long)gridDim.x * (kThreads / 32));
+    at.begin(a, start, (long long)(blockIdx.x - 1) * kWarps + (threadIdx.x >> 5), (long long)(gridDim.x - 1) * kWarps);
     if (at.left == 0) return;
     do {
         const int group = cache_group(a, at.b, at.h, at.g);
@@ -171,7 +170,7 @@ k_cache_weigh_simt(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint
                 }
             }
         }
-        const int rows = rows_of(a, at.count);
+        const int rows = at.count * a.G;
         for (int r = 0; r < rows; ++r) {
             int t;
             const long long row = row_offset(a, at.b, at.h, r, &t);
@@ -205,22 +204,248 @@ k_cache_weigh_simt(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint
     } while (at.next(a, 1));
 }
 
-// Block behind the others' work: the call's status word.
-__global__ void __launch_bounds__(256) k_cache_weigh_check(CacheArgs a) {
-    const bool bad = __syncthreads_or(bad_call<true>(a));
-    if (threadIdx.x == 0) *a.status = bad ? kStBounds : kStOk;
+// --------------------------------------------------------- tensor cores
+
+// Q's halves of a warp in shared memory: float rows are two of them; eight bf16 rows are in registers
+template <typename T, int D, int NR> constexpr int q_bytes() {
+    return NR == 1 && sizeof(T) == 2 ? 0 : (sizeof(T) == 4 ? 2 : 1) * NR * (D / 16) * 256;
+}
+
+// Scores on m16n8k16 steps (halves in, fp32 out), tokens on the 16 side and 8 NR query rows on the 8 side.
+//
+// The lanes of a warp load the codes of a group in the order in which they feed the steps, 16
+// bytes each for d = 128 and neighbours next to each other, so codes go from memory to registers
+// and nothing passes through shared memory; kAhead groups are on their way. Widening is exact
+// (cache.cuh). Rows are scaled by a power of two that puts the largest entry in [2^14, 2^15): bf16 rows are exact
+// as halves down to 2^-31 of it; float32 rows are two halves, hi + lo, both in one sum.
+// A lane ends with two tokens and two rows for each eight; four lanes share a token.
+template <typename T, int D, int NR>
+__global__ void __launch_bounds__(kThreads, 2)
+k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* __restrict__ cache) {
+    using L = Grp<D>;
+    constexpr bool F = sizeof(T) == 4;  // float rows
+    constexpr bool kQRegs = NR == 1 && !F;
+    constexpr int KS = D / 16, W = D / 32, RT = 8 * NR, KW = D / 64;  // KW: 8-byte words of a lane's codes of a token
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ LineStart start;
+    if (blockIdx.x == 0) {
+        check(a);
+        return;
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
+    uint2* qs = reinterpret_cast<uint2*>(smem + warp * q_bytes<T, D, NR>());
+    Place at;
+    at.begin(a, start, (long long)(blockIdx.x - 1) * kWarps + warp, (long long)(gridDim.x - 1) * kWarps);
+    if (at.left == 0) return;
+    for (bool more = true; more;) {
+        const int cnt = (int)min(at.left, (long long)(at.groups - at.g)), n = at.n, g0 = at.g;
+        const int rows = at.count * a.G;
+        const long long sums = ((long long)at.b * a.Hkv + at.h) * w.cap;
+        auto groups = [&](int i) { return i + lane < cnt ? cache_group(a, at.b, at.h, g0 + i + lane) : -1; };
+        // Rows in tiles: the first starts from what the tokens had, the others add to what is there
+        // (a lane reads what it wrote itself).
+        for (int row0 = 0; row0 < max(rows, 1); row0 += RT) {
+            const float* had = row0 ? w.acc_out : w.acc;
+            const float decay = row0 ? 1.0f : w.decay;
+            const int olds = row0 ? n : w.decay != 0.0f ? n - at.count : 0;  // places with a sum
+            int gcur = groups(0), gnxt = groups(32);
+            uint2 kc[kAhead][2][KW];
+            uint32_t sc[kAhead], ok = 0;
+            float base[kAhead];
+            auto load = [&](int u, int i) {  // called for every i in turn
+                const int grp = __shfl_sync(0xffffffffu, gcur, i & 31);
+                const int place = (g0 + i) * kGroup + g + 8 * t4;
+                ok = grp >= 0 ? ok | 1u << u : ok & ~(1u << u);
+                base[u] = 0.0f;
+                if (grp >= 0) {
+                    const uint8_t* p = cache + (long long)grp * L::kBytes;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint8_t* r = p + (8 * x + g) * L::kRow + t4 * (D / 8);
+                        if (D == 128) {
+                            const uint4 v = *reinterpret_cast<const uint4*>(r);
+                            kc[u][x][0] = make_uint2(v.x, v.y);
+                            kc[u][x][KW - 1] = make_uint2(v.z, v.w);
+                        } else {
+                            kc[u][x][0] = *reinterpret_cast<const uint2*>(r);
+                        }
+                    }
+                    sc[u] = D == 128 ? *reinterpret_cast<const uint32_t*>(p + L::kKs + g * 16 + t4 * 4)
+                                     : *reinterpret_cast<const uint16_t*>(p + L::kKs + g * 8 + t4 * 2);
+                    if (t4 < 2 && place < olds) base[u] = had[sums + place];
+                }
+                if ((i & 31) == 31) {
+                    gcur = gnxt;
+                    gnxt = groups(i + 33);
+                }
+            };
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) load(u, u);
+
+            // Q: lane (g, t4) has channels [t4 d/4, (t4 + 1) d/4) of rows g, and what it needs of
+            // rows 2 t4 and the next: factor of the scores, lse, keys that they see
+            uint2 qf[kQRegs ? KS : 1];
+            float zf[NR][2], lse[NR][2];
+            int lim[NR][2], low = 0, top = 0;
+            __syncwarp();  // all have read the tile before
+#pragma unroll
+            for (int j = 0; j < NR; ++j) {
+                const int r = row0 + 8 * j + g;
+                int t = 0;
+                const long long row = row_offset(a, at.b, at.h, min(r, max(rows - 1, 0)), &t);
+                constexpr int QW = D / 16 * sizeof(T) / 4;  // 16-byte words of a lane's channels
+                uint32_t x[4 * QW], amax = 0;
+#pragma unroll
+                for (int i = 0; i < QW; ++i) {
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (r < rows) v = reinterpret_cast<const uint4*>(Q + row * D + t4 * (D / 4))[i];
+                    x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+                }
+                // (a row that is not there: weights of 0)
+                const float l = r < rows ? w.lse[row] : INFINITY;
+                const int m = r < rows ? row_limit(a, n, at.count, t) : 0;
+#pragma unroll
+                for (int i = 0; i < 4 * QW; ++i)
+                    amax = max(amax, F ? x[i] & 0x7fffffffu : max(x[i] << 16 & 0x7fff0000u, x[i] & 0x7fff0000u));
+                amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                float up;
+                const int qe = query_exp(amax >> 23, &up);
+                const float f = fminf(a.scale * pow2(cache_exp(a, 0, at.h)) * pow2(-qe), 3.4028235e38f);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    uint32_t hi[2], lo[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float y0 = __uint_as_float(F ? x[(4 * ks + 2 * e) % (4 * QW)] : x[2 * ks + e] << 16) * up;
+                        const float y1 = __uint_as_float(F ? x[(4 * ks + 2 * e + 1) % (4 * QW)] : x[2 * ks + e] & 0xffff0000u) * up;
+                        hi[e] = pack_half2(y0, y1);
+                        const float2 h = half2_to_float2(hi[e]);
+                        lo[e] = pack_half2(y0 - h.x, y1 - h.y);
+                    }
+                    if (kQRegs)
+                        qf[ks % (kQRegs ? KS : 1)] = make_uint2(hi[0], hi[1]);
+                    else
+                        qs[(ks * NR + j) * 32 + lane] = make_uint2(hi[0], hi[1]);
+                    if (F) qs[((KS + ks) * NR + j) * 32 + lane] = make_uint2(lo[0], lo[1]);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int from = (2 * t4 + e) * 4;
+                    zf[j][e] = __shfl_sync(0xffffffffu, f, from);
+                    lse[j][e] = __shfl_sync(0xffffffffu, l, from);
+                    lim[j][e] = __shfl_sync(0xffffffffu, m, from);
+                }
+            }
+            if (rows) {  // keys that the tile's first and last row see: later tokens see more
+                low = row_limit(a, n, at.count, row0 / a.G);
+                top = row_limit(a, n, at.count, min(row0 + RT - 1, rows - 1) / a.G);
+            }
+            __syncwarp();
+
+            for (int i0 = 0; i0 < cnt; i0 += kAhead) {
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int i = i0 + u, tok = (g0 + i) * kGroup;
+                    float sum = 0.0f;
+                    if (i < cnt && tok < top) {
+                        uint32_t s2[2][KW];  // [token g, g + 8]: scales, each in both halves
+                        if (D == 128) {
+                            const uint32_t a0 = e4m3x2_to_half2(sc[u] & 0xffff), a1 = e4m3x2_to_half2(sc[u] >> 16);
+                            s2[0][0] = __byte_perm(a0, a0, 0x1010);
+                            s2[0][KW - 1] = __byte_perm(a0, a0, 0x3232);
+                            s2[1][0] = __byte_perm(a1, a1, 0x1010);
+                            s2[1][KW - 1] = __byte_perm(a1, a1, 0x3232);
+                        } else {
+                            const uint32_t a0 = e4m3x2_to_half2(sc[u]);
+                            s2[0][0] = __byte_perm(a0, a0, 0x1010);
+                            s2[1][0] = __byte_perm(a0, a0, 0x3232);
+                        }
+                        float z[NR][4];
+#pragma unroll
+                        for (int wi = 0; wi < W; ++wi) {
+                            uint32_t k8[2][4];
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                e2m1x8_to_half2(wi & 1 ? kc[u][x][wi / 2].y : kc[u][x][wi / 2].x, k8[x]);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) k8[x][j] = hmul2(k8[x][j], s2[x][wi / 2]);
+                            }
+#pragma unroll
+                            for (int k2 = 0; k2 < 2; ++k2)
+#pragma unroll
+                                for (int j = 0; j < NR; ++j) {
+                                    const int ks = 2 * wi + k2;
+                                    const uint2 q = kQRegs ? qf[ks % (kQRegs ? KS : 1)] : qs[(ks * NR + j) * 32 + lane];
+                                    if (ks == 0)
+                                        mma_f16_first(z[j], k8[0][0], k8[1][0], k8[0][1], k8[1][1], q.x, q.y);
+                                    else
+                                        mma_f16(z[j], k8[0][2 * k2], k8[1][2 * k2], k8[0][2 * k2 + 1], k8[1][2 * k2 + 1], q.x, q.y);
+                                    if (F) {
+                                        const uint2 ql = qs[((KS + ks) * NR + j) * 32 + lane];
+                                        mma_f16(z[j], k8[0][2 * k2], k8[1][2 * k2], k8[0][2 * k2 + 1], k8[1][2 * k2 + 1], ql.x, ql.y);
+                                    }
+                                }
+                        }
+                        const bool edge = tok + kGroup > low;  // some row does not see all of these tokens
+                        float s0 = 0.0f, s1 = 0.0f;  // tokens g and g + 8
+#pragma unroll
+                        for (int j = 0; j < NR; ++j)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                float p = weight(z[j][e], zf[j][e & 1], lse[j][e & 1]);
+                                if (edge && tok + g + 8 * (e >> 1) >= lim[j][e & 1]) p = 0.0f;
+                                (e < 2 ? s0 : s1) += p;
+                            }
+                        // over the four lanes of a token: even lanes end with token g, odd ones with g + 8
+                        const float give = t4 & 1 ? s0 : s1;
+                        sum = t4 & 1 ? s1 : s0;
+                        sum += __shfl_xor_sync(0xffffffffu, give, 1);
+                        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                    }
+                    const int place = tok + g + 8 * t4;
+                    if (i < cnt && t4 < 2 && place < n && (ok >> u & 1)) w.acc_out[sums + place] = fmaf(decay, base[u], sum);
+                    load(u, i + kAhead);
+                }
+            }
+        }
+        more = at.next(a, cnt);
+    }
 }
 
 // ------------------------------------------------------------------ launch
 
-template <typename T, int D>
-static cudaError_t weigh_t(const CacheArgs& a, const WeighArgs& w, const void* Q, const uint8_t* cache, cudaStream_t st) {
+// Parts of the line for `blocks` blocks on each SM, and the block that checks.
+static unsigned weigh_grid(const CacheArgs& a, const WeighArgs& w, int blocks) {
     const long long groups = (long long)a.B * a.Hkv * ((w.cap + kGroup - 1) / kGroup);
-    const int blocks = (int)std::min<long long>((groups + kThreads / 32 - 1) / (kThreads / 32), 8LL * num_sms());
-    k_cache_weigh_simt<T, D><<<blocks, kThreads, 0, st>>>(a, w, (const T*)Q, cache);
-    k_cache_weigh_check<<<1, 256, 0, st>>>(a);
-    count_launch(2);
+    return (unsigned)std::min<long long>((groups + kWarps - 1) / kWarps, (long long)blocks * num_sms()) + 1;
+}
+
+template <typename T, int D, int NR>
+static cudaError_t mma_t(const CacheArgs& a, const WeighArgs& w, const void* Q, const uint8_t* cache, cudaStream_t st) {
+    constexpr int smem = kWarps * q_bytes<T, D, NR>();
+    static std::atomic<unsigned long long> done{0};
+    if (smem > 40 * 1024) {
+        const cudaError_t e = set_smem_once((const void*)k_cache_weigh<T, D, NR>, smem, &done);
+        if (e != cudaSuccess) return e;
+    }
+    k_cache_weigh<T, D, NR><<<weigh_grid(a, w, 2), kThreads, smem, st>>>(a, w, (const T*)Q, cache);
+    count_launch();
     return cudaGetLastError();
+}
+
+template <typename T, int D>
+static cudaError_t weigh_t(const CacheArgs& a, const WeighArgs& w, unsigned flags, const void* Q, const uint8_t* cache,
+                           cudaStream_t st) {
+    if (flags & MITA_FLAG_SIMT) {
+        k_cache_weigh_simt<T, D><<<weigh_grid(a, w, 4), kThreads, 0, st>>>(a, w, (const T*)Q, cache);
+        count_launch();
+        return cudaGetLastError();
+    }
+    const long long rows = (long long)a.G * a.T;
+    if (rows <= 8) return mma_t<T, D, 1>(a, w, Q, cache, st);
+    if (rows <= 16 || sizeof(T) == 4) return mma_t<T, D, 2>(a, w, Q, cache, st);
+    return mma_t<T, D, sizeof(T) == 4 ? 2 : 4>(a, w, Q, cache, st);
 }
 
 cudaError_t launch_cache_weigh(const CacheArgs& a, int d, int dtype, unsigned flags, const void* Q, const void* cache,
@@ -228,8 +453,9 @@ cudaError_t launch_cache_weigh(const CacheArgs& a, int d, int dtype, unsigned fl
     const WeighArgs w{lse, acc, acc_out, decay, (long long)a.cols * a.page};
     const uint8_t* c = (const uint8_t*)cache;
     prof_mark(st, "cache_weights");
-    if (dtype == 0) return d == 64 ? weigh_t<float, 64>(a, w, Q, c, st) : weigh_t<float, 128>(a, w, Q, c, st);
-    return d == 64 ? weigh_t<__nv_bfloat16, 64>(a, w, Q, c, st) : weigh_t<__nv_bfloat16, 128>(a, w, Q, c, st);
+    if (dtype == 0) return d == 64 ? weigh_t<float, 64>(a, w, flags, Q, c, st) : weigh_t<float, 128>(a, w, flags, Q, c, st);
+    return d == 64 ? weigh_t<__nv_bfloat16, 64>(a, w, flags, Q, c, st)
+                   : weigh_t<__nv_bfloat16, 128>(a, w, flags, Q, c, st);
 }
 
 }  // namespace mita
