@@ -285,6 +285,8 @@ EVICT = [
     (128, 128, 1, [70000, 3], [20001, 600], 4, 512, "any", False),
     (64, 64, 2, [40000, 33000], [39999, 1], 0, 1, "ties", False),
     (128, 16, 3, [5, 0, 17], [0, 0, 0], 0, 0, "any", False),
+    (64, 128, 1, [400001, 50], [100000, 60], 3, 20, "ties", False),  # more than the blocks hold
+    (64, 4096, 100, [30, 9000], [20, 4500], 2, 2, "any", False),     # many heads
 ]
 
 
@@ -333,6 +335,29 @@ def test_eviction_matches_oracle(case, dtype, in_place):
                 np.testing.assert_array_equal(bits(a_out[b, h, now[b]:]), sums[b, h, now[b]:].view(np.int32))
             else:
                 assert (a_out[b, h, now[b]:] == 7.0).all()
+
+
+@pytest.mark.parametrize("kind", ["any", "near"])
+def test_eviction_of_unaligned_sums(kind):
+    """Sums that are aligned to their elements only."""
+    import torch
+    import compressed_attention_adaptive_gb300 as mita
+    lens, keep = [5000, 33, 4997], [1234, 20, 4000]
+    pool = Pool(lens, 2, 64, 16, "bf16", seed=3)
+    cap = pool.cols * 16
+    sums = _sums(np.random.default_rng(5), (3, 2, cap), kind)
+    odd = lambda dt: torch.full((6 * cap + 1,), 7, dtype=dt, device="cuda")[1:].view(3, 2, cap)
+    acc, out, src = odd(torch.float32), odd(torch.float32), odd(torch.int32)
+    acc.copy_(torch.from_numpy(sums))
+    ws = mita.cache_evict_workspace(pool.p)
+    mita.mita_cache_evict(pool.p, pool.cache, pool.table, pool.len_t, torch.tensor(keep, dtype=torch.int32).cuda(), acc, ws,
+                          recent=5, acc_out=out, src_out=src)
+    mita.mita_device_status(ws)
+    for b in range(3):
+        for h in range(2):
+            want = ocache.evict(sums[b, h, :lens[b]], keep[b], 0, 5)
+            assert src[b, h, :keep[b]].tolist() == want.tolist()
+            np.testing.assert_array_equal(out[b, h, :keep[b]].cpu().numpy(), sums[b, h][want])
 
 
 def test_eviction_out_of_range():
