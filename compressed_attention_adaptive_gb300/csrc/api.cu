@@ -496,8 +496,8 @@ static mita_status run_rope(const mita_rope_params* p, bool back, const void* Q,
     if (n == 2 && !disjoint(out[0], out[1])) return fail(MITA_ERR_INVALID_ARG, "outputs must not overlap");
     for (int i = 0; i < p->rot / 2; ++i) {
         const double turns = p->freqs[i] * 0.15915494309189535;  // 1 / (2 pi)
-        const double part = turns - floor(turns);
-        a.turns[i] = part < 1.0 ? (unsigned long long)ldexp(part, 64) : 0;
+        const double part = turns - floor(turns);  // (1 for a tiny negative one)
+        a.turns[i] = part < 1.0 ? (unsigned long long)(part * 18446744073709551616.0) : 0;
     }
     MITA_CUDA(launch_rope(a, p->dtype, p->flags & MITA_FLAG_INTERLEAVED, (cudaStream_t)stream), "rope");
     prof_mark((cudaStream_t)stream, "");

@@ -9,6 +9,12 @@
 // Angles. A frequency is held in turns per position as a 64-bit fraction (host: double, 2^-53
 // of it); position * fraction in integers wraps at whole turns, which is the reduction, exactly. The
 // signed fraction goes to sincospi as a float: 2^-24 of the angle in (-pi, pi].
+//
+// Measured: queries and keys of two prompts of 32768, 16 heads each, d = 128, out of a projection's order
+// (1074 MB) 167 us (6.4 TB/s, 0.95 of the copy rate), 131,072 rows of 10 heads in place of
+// order 99 us (0.99). One token of 64 sequences, 40 heads: 3.2 us, a launch and three memory latencies.
+//   - 16-byte accesses, four heads' loads and then their stores: 253 and 155 us; 16 bytes with the next
+//     heads' loads ahead: 235 and 145; 32 bytes with them ahead: 167 and 99.
 #include <math.h>
 
 #include "rope.cuh"
@@ -17,18 +23,39 @@ namespace mita {
 
 constexpr int kRopeThreads = 256;
 
-// V elements of a row, one access.
+// V elements of a row, one access of up to 32 bytes.
 template <typename T, int V> struct alignas(sizeof(T) * V) Elems {
     T x[V];
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (sizeof(T) * V == 32) {
+            uint32_t* r = reinterpret_cast<uint32_t*>(x);
+            asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                         : "l"(p));
+        } else {
+            *this = *reinterpret_cast<const Elems*>(p);
+        }
+    }
+    __device__ __forceinline__ void store(T* p) const {
+        if constexpr (sizeof(T) * V == 32) {
+            const uint32_t* r = reinterpret_cast<const uint32_t*>(x);
+            asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
+                         "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "l"(p)
+                         : "memory");
+        } else {
+            *reinterpret_cast<Elems*>(p) = *this;
+        }
+    }
 };
 
 // T: element; IL: interleaved pairs; V: elements of an access. A unit of a rotated place is V pairs (two accesses),
 // or one access of V / 2 interleaved pairs.
 template <typename T, bool IL, int V>
 __global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ RopeArgs a) {
-    constexpr bool kOne = IL && V > 1;       // one access holds whole pairs
-    constexpr int P = kOne ? V / 2 : V;      // pairs of a unit
-    constexpr int kHeads = V * sizeof(T) == 16 ? 4 : 2;  // heads whose loads are in flight together
+    constexpr bool kOne = IL && V > 1;    // one access holds whole pairs
+    constexpr int P = kOne ? V / 2 : V;   // pairs of a unit
+    constexpr int N = kOne ? 1 : 2;       // accesses of a unit
+    constexpr int kHeads = std::max(1, 64 / (N * V * (int)sizeof(T)));  // heads loaded together, twice over
     using E = Elems<T, V>;
     const int units = a.rot / 2 / P, slots = units + (a.d - a.rot) / V;
     const int mine = threadIdx.x / slots, slot = threadIdx.x - mine * slots, rows = kRopeThreads / slots;
@@ -39,46 +66,67 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ R
     // channels of the unit's accesses
     const int c0 = !turn ? a.rot + (slot - units) * V : IL ? slot * 2 * P : slot * V;
     const int c1 = IL ? c0 + 1 : c0 + a.rot / 2;
+    struct Heads {
+        E x[kHeads][N];
+    };
+    Heads v[2];
     float cs[P], sn[P];
-    if (turn) {
-        const long long at = a.pos ? a.pos[b * a.pos_stride + t] : t;
+    bool known = false;
+    // heads of Q, then of K (numbered from H on)
+    const int h0 = blockIdx.y * a.heads, h1 = min(a.H + a.Hkv, h0 + a.heads);
+#pragma unroll 1
+    for (int w = h0 >= a.H; w < 2; ++w) {
+        const int lo = w ? max(h0 - a.H, 0) : h0, n = (w ? h1 - a.H : min(h1, a.H)) - lo;
+        if (n <= 0 || (!turn && a.same[w])) continue;
+        const long long is = a.is[w][1], os = a.os[w][1];
+        const T* in = (const T*)a.in[w] + b * a.is[w][0] + t * a.is[w][2] + lo * is + c0;
+        T* out = (T*)a.out[w] + b * a.os[w][0] + t * a.os[w][2] + lo * os + c0;
+        auto fetch = [&](Heads& v, int h) {
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const long long phase = (long long)((unsigned long long)at * a.turns[slot * P + i]);  // in 2^-64 turns
-            sincospif((float)phase * 1.0842021724855044e-19f, &sn[i], &cs[i]);                    // 2^-63: half turns
-            cs[i] *= a.gain;
-            sn[i] *= a.back ? -a.gain : a.gain;
-        }
-    }
-    const int h1 = min(a.H + a.Hkv, ((int)blockIdx.y + 1) * a.heads);
-    for (int h0 = blockIdx.y * a.heads; h0 < h1; h0 += kHeads) {
-        E x[kHeads], y[kOne ? 1 : kHeads];
-        T* out[kHeads];
-#pragma unroll
-        for (int i = 0; i < kHeads; ++i) {
-            const int w = h0 + i >= a.H, h = w ? h0 + i - a.H : h0 + i;
-            out[i] = nullptr;
-            if (h0 + i >= h1 || (!turn && a.same[w])) continue;
-            const T* in = (const T*)a.in[w] + b * a.is[w][0] + h * a.is[w][1] + t * a.is[w][2];
-            out[i] = (T*)a.out[w] + b * a.os[w][0] + h * a.os[w][1] + t * a.os[w][2];
-            x[i] = *reinterpret_cast<const E*>(in + c0);
-            if (!kOne && turn) y[i % (kOne ? 1 : kHeads)] = *reinterpret_cast<const E*>(in + c1);
-        }
-#pragma unroll
-        for (int i = 0; i < kHeads; ++i) {
-            if (!out[i]) continue;
-            if (turn) {
-#pragma unroll
-                for (int j = 0; j < P; ++j) {
-                    T& e0 = kOne ? x[i].x[(2 * j) % V] : x[i].x[j % V];
-                    T& e1 = kOne ? x[i].x[(2 * j + 1) % V] : y[i % (kOne ? 1 : kHeads)].x[j % V];
-                    const float x0 = to_f(e0), x1 = to_f(e1);
-                    e0 = from_f<T>(x0 * cs[j] - x1 * sn[j]);
-                    e1 = from_f<T>(x0 * sn[j] + x1 * cs[j]);
-                }
-                if (!kOne) *reinterpret_cast<E*>(out[i] + c1) = y[i % (kOne ? 1 : kHeads)];
+            for (int i = 0; i < kHeads; ++i) {
+                if (h + i >= n) continue;
+                const T* p = in + (h + i) * is;
+                v.x[i][0].load(p);
+                if (!kOne && turn) v.x[i][N - 1].load(p + (c1 - c0));
             }
-            *reinterpret_cast<E*>(out[i] + c0) = x[i];
+        };
+        auto finish = [&](Heads& v, int h) {
+#pragma unroll
+            for (int i = 0; i < kHeads; ++i) {
+                if (h + i >= n) continue;
+                T* p = out + (h + i) * os;
+                if (turn) {
+#pragma unroll
+                    for (int j = 0; j < P; ++j) {
+                        T& e0 = kOne ? v.x[i][0].x[(2 * j) % V] : v.x[i][0].x[j % V];
+                        T& e1 = kOne ? v.x[i][0].x[(2 * j + 1) % V] : v.x[i][N - 1].x[j % V];
+                        const float x0 = to_f(e0), x1 = to_f(e1);
+                        e0 = from_f<T>(x0 * cs[j] - x1 * sn[j]);
+                        e1 = from_f<T>(x0 * sn[j] + x1 * cs[j]);
+                    }
+                    if (!kOne) v.x[i][N - 1].store(p + (c1 - c0));
+                }
+                v.x[i][0].store(p);
+            }
+        };
+        fetch(v[0], 0);
+        if (turn && !known) {
+            const long long at = a.pos ? a.pos[b * a.pos_stride + t] : t;
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const long long phase = (long long)((unsigned long long)at * a.turns[slot * P + i]);  // in 2^-64 turns
+                sincospif((float)phase * 1.0842021724855044e-19f, &sn[i], &cs[i]);                    // 2^-63: half turns
+                cs[i] *= a.gain;
+                sn[i] *= a.back ? -a.gain : a.gain;
+            }
+            known = true;
+        }
+        // the next heads are on their way while these are turned
+        for (int h = 0; h < n; h += 2 * kHeads) {
+            fetch(v[1], h + kHeads);
+            finish(v[0], h);
+            fetch(v[0], h + 2 * kHeads);
+            finish(v[1], h + kHeads);
         }
     }
 }
@@ -108,8 +156,12 @@ template <typename T, bool IL, int V> static cudaError_t rope_v(RopeArgs& a, cud
 }
 
 template <typename T, bool IL> static cudaError_t rope_t(RopeArgs& a, cudaStream_t st) {
-    constexpr int kWide = 16 / sizeof(T);
-    if (rope_fits(a, IL, sizeof(T), kWide)) return rope_v<T, IL, kWide>(a, st);
+    constexpr int kWide = 32 / sizeof(T);
+    // Units of 16 pairs leave a small call's threads with 16 angles each (64 tokens, 40 heads, d = 128: 4.2 us,
+    // with 8 pairs 3.3; 200 tokens 5.5 and 4.0; 256 tokens 5.5 both; 65536 tokens 167 and 235).
+    const bool few = !IL && sizeof(T) == 2 && (long long)a.B * a.T * (a.H + a.Hkv) * a.d < (1 << 20);
+    if (!few && rope_fits(a, IL, sizeof(T), kWide)) return rope_v<T, IL, kWide>(a, st);
+    if (rope_fits(a, IL, sizeof(T), kWide / 2)) return rope_v<T, IL, kWide / 2>(a, st);
     if (rope_fits(a, IL, sizeof(T), 2)) return rope_v<T, IL, 2>(a, st);
     return rope_v<T, IL, 1>(a, st);
 }
