@@ -8,7 +8,7 @@
 // d/2 + d/16 + 4 bytes per token and cache head, writes 4, and does 2 d flops and an exponential
 // per row.
 //
-// Work split. The groups of 16 tokens of all (sequence, cache head) form one line, cut into equal
+// Work split. The steps of 32 tokens of all (sequence, cache head) form one line, cut into equal
 // parts, one per warp; warps share nothing but the search for their place. A token's sum is
 // added in an order of its own, whatever the cut, so the same call gives the same bits.
 #include <algorithm>
@@ -20,7 +20,9 @@ namespace mita {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;  // of a block
-constexpr int kAhead = 4;                              // groups that a warp's loads are ahead
+constexpr int kTok = 2 * kGroup;                       // tokens of a warp's step
+constexpr int kAhead = 2;                              // steps that a warp's loads are ahead
+constexpr int kBlocks = 2;                             // of an SM
 
 struct WeighArgs {
     const float* lse;
@@ -35,14 +37,14 @@ struct LineStart {
     unsigned long long before[kThreads], warps[kWarps];
 };
 struct Place {
-    int b, h, g, groups, n, count;  // sequence, cache head, group of it; the sequence's
-    long long left;                 // groups of the warp's part from here on
+    int b, h, at, steps, n, count;  // sequence, cache head, step of it; the sequence's
+    long long left;                 // steps of the warp's part from here on
 
     __device__ __forceinline__ void enter(const CacheArgs& a, int seq) {
         b = seq;
         n = cache_len(a, b);
         count = cache_count(a, b);
-        groups = (n + kGroup - 1) / kGroup;
+        steps = (n + kTok - 1) / kTok;
     }
     // The part of warp `me` of `all`. A thread sums up its share of the sequences.
     __device__ __forceinline__ void begin(const CacheArgs& a, LineStart& s, long long me, long long all) {
@@ -52,7 +54,7 @@ struct Place {
 #pragma unroll 4
         for (int i = 0; i < per; ++i) {
             const int q = threadIdx.x * per + i;
-            if (q < a.B) mine += (unsigned long long)((cache_len(a, q) + kGroup - 1) / kGroup) * a.Hkv;
+            if (q < a.B) mine += (unsigned long long)((cache_len(a, q) + kTok - 1) / kTok) * a.Hkv;
         }
         unsigned long long x = mine;
 #pragma unroll
@@ -78,35 +80,35 @@ struct Place {
         int slices = 0;  // threads whose share begins at or before w0
 #pragma unroll
         for (int i = 0; i < kThreads; i += 32) slices += __popc(__ballot_sync(0xffffffffu, s.before[i + lane] <= w0));
-        unsigned long long at = w0 - s.before[slices - 1];
+        unsigned long long off = w0 - s.before[slices - 1];
         // (shares of threads without sequences begin at the total, which is above w0; a sequence without
         // tokens shares its beginning with the next)
         bool found = false;
         for (int seq = (slices - 1) * per; seq < a.B && !found; ++seq) {
             enter(a, seq);
-            const unsigned long long units = (unsigned long long)groups * a.Hkv;
-            found = at < units;
-            if (!found) at -= units;
+            const unsigned long long units = (unsigned long long)steps * a.Hkv;
+            found = off < units;
+            if (!found) off -= units;
         }
         if (!found) {  // lengths that changed under the call
             left = 0;
             return;
         }
-        h = (int)(at / groups);
-        g = (int)(at - (unsigned long long)h * groups);
+        h = (int)(off / steps);
+        at = (int)(off - (unsigned long long)h * steps);
     }
-    // Behind `step` groups of the same head.
-    __device__ __forceinline__ bool next(const CacheArgs& a, int step) {
-        left -= step;
-        g += step;
+    // Behind `done` steps of the same head.
+    __device__ __forceinline__ bool next(const CacheArgs& a, int done) {
+        left -= done;
+        at += done;
         if (left <= 0) return false;
-        if (g < groups) return true;
-        g = 0;
+        if (at < steps) return true;
+        at = 0;
         if (++h < a.Hkv) return true;
         h = 0;
         for (int seq = b + 1; seq < a.B; ++seq) {
             enter(a, seq);
-            if (groups) return true;
+            if (steps) return true;
         }
         return false;
     }
@@ -119,6 +121,33 @@ __device__ __forceinline__ float weight(float dot, float f, float lse) {
     float t = fmaf(dot, f, -lse);
     asm("min.NaN.f32 %0, %0, %1;" : "+f"(t) : "f"(0.0f));
     return tc::ex2(t * kLog2e);
+}
+
+// Two at a time (the packed forms take one issue slot).
+__device__ __forceinline__ uint64_t pack2(float2 x) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x.x), "f"(x.y));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(x)), "l"(pack2(y)));
+    return unpack2(r);
+}
+__device__ __forceinline__ float2 weight2(float2 dot, float2 f, float2 minus_lse) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pack2(dot)), "l"(pack2(f)), "l"(pack2(minus_lse)));
+    float2 t = unpack2(r);
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(t.x) : "f"(0.0f));
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(t.y) : "f"(0.0f));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(t)), "l"(pack2(make_float2(kLog2e, kLog2e))));
+    t = unpack2(r);
+    return make_float2(tc::ex2(t.x), tc::ex2(t.y));
 }
 
 }  // namespace
@@ -148,58 +177,60 @@ k_cache_weigh_simt(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint
     at.begin(a, start, (long long)(blockIdx.x - 1) * kWarps + (threadIdx.x >> 5), (long long)(gridDim.x - 1) * kWarps);
     if (at.left == 0) return;
     do {
-        const int group = cache_group(a, at.b, at.h, at.g);
-        if (group < 0) continue;
-        const uint8_t* gr = cache + (long long)group * L::kBytes;
-        const float f = a.scale * pow2(cache_exp(a, 0, at.h));
-        float k[4][E], sum[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int tok = 4 * u + sub;
-            sum[u] = 0.0f;
-            const uint32_t sb = gr[L::k_scale(tok, blk)], s2 = e4m3x2_to_half2(sb | sb << 8);
-#pragma unroll
-            for (int i = 0; i < E / 8; ++i) {
-                uint32_t r[4];
-                e2m1x8_to_half2(reinterpret_cast<const uint32_t*>(gr + tok * L::kRow)[ch * (E / 8) + i], r);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 x = half2_to_float2(hmul2(r[j], s2));
-                    k[u][8 * i + 2 * j] = x.x;
-                    k[u][8 * i + 2 * j + 1] = x.y;
-                }
-            }
-        }
-        const int rows = at.count * a.G;
-        for (int r = 0; r < rows; ++r) {
-            int t;
-            const long long row = row_offset(a, at.b, at.h, r, &t);
-            const int lim = row_limit(a, at.n, at.count, t);
-            if (lim <= at.g * kGroup) continue;
-            float q[E];
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const float x = to_f(Q[row * D + ch * E + i]);
-                q[i] = isfinite(x) ? x : __int_as_float(0x7fc00000);  // the row becomes NaN, as its softmax is
-            }
-            const float lse = w.lse[row];
+        for (int gi = 2 * at.at; gi < 2 * at.at + 2 && gi * kGroup < at.n; ++gi) {
+            const int group = cache_group(a, at.b, at.h, gi);
+            if (group < 0) continue;
+            const uint8_t* gr = cache + (long long)group * L::kBytes;
+            const float f = a.scale * pow2(cache_exp(a, 0, at.h));
+            float k[4][E], sum[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                float z = 0.0f;
+                const int tok = 4 * u + sub;
+                sum[u] = 0.0f;
+                const uint32_t sb = gr[L::k_scale(tok, blk)], s2 = e4m3x2_to_half2(sb | sb << 8);
 #pragma unroll
-                for (int i = 0; i < E; ++i) z = fmaf(q[i], k[u][i], z);
+                for (int i = 0; i < E / 8; ++i) {
+                    uint32_t r[4];
+                    e2m1x8_to_half2(reinterpret_cast<const uint32_t*>(gr + tok * L::kRow)[ch * (E / 8) + i], r);
 #pragma unroll
-                for (int x = 4; x; x >>= 1) z += __shfl_xor_sync(0xffffffffu, z, x);
-                if (at.g * kGroup + 4 * u + sub < lim) sum[u] += weight(z, f, lse);
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 x = half2_to_float2(hmul2(r[j], s2));
+                        k[u][8 * i + 2 * j] = x.x;
+                        k[u][8 * i + 2 * j + 1] = x.y;
+                    }
+                }
             }
-        }
-        const long long base = ((long long)at.b * a.Hkv + at.h) * w.cap;
+            const int rows = at.count * a.G;
+            for (int r = 0; r < rows; ++r) {
+                int t;
+                const long long row = row_offset(a, at.b, at.h, r, &t);
+                const int lim = row_limit(a, at.n, at.count, t);
+                if (lim <= gi * kGroup) continue;
+                float q[E];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int j = at.g * kGroup + 4 * u + sub;
-            if (ch || j >= at.n) continue;
-            if (w.decay != 0.0f && j < at.n - at.count) sum[u] = fmaf(w.decay, w.acc[base + j], sum[u]);
-            w.acc_out[base + j] = sum[u];
+                for (int i = 0; i < E; ++i) {
+                    const float x = to_f(Q[row * D + ch * E + i]);
+                    q[i] = isfinite(x) ? x : __int_as_float(0x7fc00000);  // the row becomes NaN, as its softmax is
+                }
+                const float lse = w.lse[row];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    float z = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < E; ++i) z = fmaf(q[i], k[u][i], z);
+#pragma unroll
+                    for (int x = 4; x; x >>= 1) z += __shfl_xor_sync(0xffffffffu, z, x);
+                    if (gi * kGroup + 4 * u + sub < lim) sum[u] += weight(z, f, lse);
+                }
+            }
+            const long long base = ((long long)at.b * a.Hkv + at.h) * w.cap;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int j = gi * kGroup + 4 * u + sub;
+                if (ch || j >= at.n) continue;
+                if (w.decay != 0.0f && j < at.n - at.count) sum[u] = fmaf(w.decay, w.acc[base + j], sum[u]);
+                w.acc_out[base + j] = sum[u];
+            }
         }
     } while (at.next(a, 1));
 }
@@ -215,12 +246,12 @@ template <typename T, int D, int NR> constexpr int q_bytes() {
 //
 // The lanes of a warp load the codes of a group in the order in which they feed the steps, 16
 // bytes each for d = 128 and neighbours next to each other, so codes go from memory to registers
-// and nothing passes through shared memory; kAhead groups are on their way. Widening is exact
+// and nothing passes through shared memory; kAhead steps, two groups each, are on their way. Widening is exact
 // (cache.cuh). Rows are scaled by a power of two that puts the largest entry in [2^14, 2^15): bf16 rows are exact
 // as halves down to 2^-31 of it; float32 rows are two halves, hi + lo, both in one sum.
-// A lane ends with two tokens and two rows for each eight; four lanes share a token.
+// A lane ends with two tokens of each group and two rows for each eight; four lanes share a token.
 template <typename T, int D, int NR>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kBlocks)
 k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* __restrict__ cache) {
     using L = Grp<D>;
     constexpr bool F = sizeof(T) == 4;  // float rows
@@ -238,45 +269,54 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
     at.begin(a, start, (long long)(blockIdx.x - 1) * kWarps + warp, (long long)(gridDim.x - 1) * kWarps);
     if (at.left == 0) return;
     for (bool more = true; more;) {
-        const int cnt = (int)min(at.left, (long long)(at.groups - at.g)), n = at.n, g0 = at.g;
+        const int cnt = (int)min(at.left, (long long)(at.steps - at.at)), n = at.n, step0 = at.at;
         const int rows = at.count * a.G;
-        const long long sums = ((long long)at.b * a.Hkv + at.h) * w.cap;
-        auto groups = [&](int i) { return i + lane < cnt ? cache_group(a, at.b, at.h, g0 + i + lane) : -1; };
+        // the lane's token of step 0
+        const long long sums = ((long long)at.b * a.Hkv + at.h) * w.cap + (long long)step0 * kTok + 8 * t4 + g;
+        const uint8_t* codes = cache + g * L::kRow + t4 * (D / 8);
+        const uint8_t* scales = cache + L::kKs + g * (D / 8) + t4 * (D / 32);
+        // lane l: group l % 2 of step i + l / 2
+        auto groups = [&](int i) {
+            const int gi = 2 * (step0 + i) + lane;
+            return i + (lane >> 1) < cnt && gi * kGroup < n ? cache_group(a, at.b, at.h, gi) : -1;
+        };
         // Rows in tiles: the first starts from what the tokens had, the others add to what is there
         // (a lane reads what it wrote itself).
         for (int row0 = 0; row0 < max(rows, 1); row0 += RT) {
-            const float* had = row0 ? w.acc_out : w.acc;
+            const float* had = (row0 ? w.acc_out : w.acc) + sums;
             const float decay = row0 ? 1.0f : w.decay;
-            const int olds = row0 ? n : w.decay != 0.0f ? n - at.count : 0;  // places with a sum
-            int gcur = groups(0), gnxt = groups(32);
-            uint2 kc[kAhead][2][KW];
-            uint32_t sc[kAhead], ok = 0;
+            // steps' tokens of the lane with a sum: those before step `olds`
+            const int olds = (row0 ? n : w.decay != 0.0f ? n - at.count : 0) - (step0 * kTok + 8 * t4 + g);
+            int gcur = groups(0), gnxt = groups(16);
+            uint2 kc[kAhead][2][2][KW];  // [step][group][token g, g + 8]
+            uint32_t sc[kAhead][2], ok = 0;
             float base[kAhead];
             auto load = [&](int u, int i) {  // called for every i in turn
-                const int grp = __shfl_sync(0xffffffffu, gcur, i & 31);
-                const int place = (g0 + i) * kGroup + g + 8 * t4;
-                ok = grp >= 0 ? ok | 1u << u : ok & ~(1u << u);
-                base[u] = 0.0f;
-                if (grp >= 0) {
-                    const uint8_t* p = cache + (long long)grp * L::kBytes;
+                ok &= ~(3u << 2 * u);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int grp = __shfl_sync(0xffffffffu, gcur, 2 * (i & 15) + y);
+                    if (grp < 0) continue;
+                    ok |= 1u << (2 * u + y);
+                    const unsigned long long at_group = (unsigned long long)(unsigned)grp * L::kBytes;
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const uint8_t* r = p + (8 * x + g) * L::kRow + t4 * (D / 8);
+                        const uint8_t* r = codes + at_group + 8 * x * L::kRow;
                         if (D == 128) {
                             const uint4 v = *reinterpret_cast<const uint4*>(r);
-                            kc[u][x][0] = make_uint2(v.x, v.y);
-                            kc[u][x][KW - 1] = make_uint2(v.z, v.w);
+                            kc[u][y][x][0] = make_uint2(v.x, v.y);
+                            kc[u][y][x][KW - 1] = make_uint2(v.z, v.w);
                         } else {
-                            kc[u][x][0] = *reinterpret_cast<const uint2*>(r);
+                            kc[u][y][x][0] = *reinterpret_cast<const uint2*>(r);
                         }
                     }
-                    sc[u] = D == 128 ? *reinterpret_cast<const uint32_t*>(p + L::kKs + g * 16 + t4 * 4)
-                                     : *reinterpret_cast<const uint16_t*>(p + L::kKs + g * 8 + t4 * 2);
-                    if (t4 < 2 && place < olds) base[u] = had[sums + place];
+                    sc[u][y] = D == 128 ? *reinterpret_cast<const uint32_t*>(scales + at_group)
+                                        : *reinterpret_cast<const uint16_t*>(scales + at_group);
                 }
-                if ((i & 31) == 31) {
+                base[u] = i < cnt && i * kTok < olds ? had[(long long)i * kTok] : 0.0f;
+                if ((i & 15) == 15) {
                     gcur = gnxt;
-                    gnxt = groups(i + 33);
+                    gnxt = groups(i + 17);
                 }
             };
 #pragma unroll
@@ -285,8 +325,9 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
             // Q: lane (g, t4) has channels [t4 d/4, (t4 + 1) d/4) of rows g, and what it needs of
             // rows 2 t4 and the next: factor of the scores, lse, keys that they see
             uint2 qf[kQRegs ? KS : 1];
-            float zf[NR][2], lse[NR][2];
-            int lim[NR][2], low = 0, top = 0;
+            float2 zf[NR], lse[NR];  // (lse negated)
+            int2 lim[NR];
+            int low = 0, top = 0;
             __syncwarp();  // all have read the tile before
 #pragma unroll
             for (int j = 0; j < NR; ++j) {
@@ -329,13 +370,10 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
                         qs[(ks * NR + j) * 32 + lane] = make_uint2(hi[0], hi[1]);
                     if (F) qs[((KS + ks) * NR + j) * 32 + lane] = make_uint2(lo[0], lo[1]);
                 }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int from = (2 * t4 + e) * 4;
-                    zf[j][e] = __shfl_sync(0xffffffffu, f, from);
-                    lse[j][e] = __shfl_sync(0xffffffffu, l, from);
-                    lim[j][e] = __shfl_sync(0xffffffffu, m, from);
-                }
+                const int r0 = 8 * t4, r1 = r0 + 4;  // lanes with rows 2 t4 and the next
+                zf[j] = make_float2(__shfl_sync(0xffffffffu, f, r0), __shfl_sync(0xffffffffu, f, r1));
+                lse[j] = make_float2(-__shfl_sync(0xffffffffu, l, r0), -__shfl_sync(0xffffffffu, l, r1));
+                lim[j] = make_int2(__shfl_sync(0xffffffffu, m, r0), __shfl_sync(0xffffffffu, m, r1));
             }
             if (rows) {  // keys that the tile's first and last row see: later tokens see more
                 low = row_limit(a, n, at.count, row0 / a.G);
@@ -346,65 +384,79 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
             for (int i0 = 0; i0 < cnt; i0 += kAhead) {
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
-                    const int i = i0 + u, tok = (g0 + i) * kGroup;
+                    const int i = i0 + u, tok = (step0 + i) * kTok;
                     float sum = 0.0f;
                     if (i < cnt && tok < top) {
-                        uint32_t s2[2][KW];  // [token g, g + 8]: scales, each in both halves
-                        if (D == 128) {
-                            const uint32_t a0 = e4m3x2_to_half2(sc[u] & 0xffff), a1 = e4m3x2_to_half2(sc[u] >> 16);
-                            s2[0][0] = __byte_perm(a0, a0, 0x1010);
-                            s2[0][KW - 1] = __byte_perm(a0, a0, 0x3232);
-                            s2[1][0] = __byte_perm(a1, a1, 0x1010);
-                            s2[1][KW - 1] = __byte_perm(a1, a1, 0x3232);
-                        } else {
-                            const uint32_t a0 = e4m3x2_to_half2(sc[u]);
-                            s2[0][0] = __byte_perm(a0, a0, 0x1010);
-                            s2[1][0] = __byte_perm(a0, a0, 0x3232);
-                        }
-                        float z[NR][4];
+                        const bool edge = tok + kTok > low;  // some row does not see all of these tokens
+                        float2 s2t[2][2];                    // [group][token g, g + 8], two rows each
 #pragma unroll
-                        for (int wi = 0; wi < W; ++wi) {
-                            uint32_t k8[2][4];
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                e2m1x8_to_half2(wi & 1 ? kc[u][x][wi / 2].y : kc[u][x][wi / 2].x, k8[x]);
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) k8[x][j] = hmul2(k8[x][j], s2[x][wi / 2]);
+                        for (int y = 0; y < 2; ++y) {
+                            uint32_t s2[2][KW];  // [token g, g + 8]: scales, each in both halves
+                            if (D == 128) {
+                                const uint32_t a0 = e4m3x2_to_half2(sc[u][y] & 0xffff), a1 = e4m3x2_to_half2(sc[u][y] >> 16);
+                                s2[0][0] = __byte_perm(a0, a0, 0x1010);
+                                s2[0][KW - 1] = __byte_perm(a0, a0, 0x3232);
+                                s2[1][0] = __byte_perm(a1, a1, 0x1010);
+                                s2[1][KW - 1] = __byte_perm(a1, a1, 0x3232);
+                            } else {
+                                const uint32_t a0 = e4m3x2_to_half2(sc[u][y]);
+                                s2[0][0] = __byte_perm(a0, a0, 0x1010);
+                                s2[1][0] = __byte_perm(a0, a0, 0x3232);
                             }
+                            float z[NR][4];
 #pragma unroll
-                            for (int k2 = 0; k2 < 2; ++k2)
+                            for (int wi = 0; wi < W; ++wi) {
+                                uint32_t k8[2][4];
 #pragma unroll
-                                for (int j = 0; j < NR; ++j) {
-                                    const int ks = 2 * wi + k2;
-                                    const uint2 q = kQRegs ? qf[ks % (kQRegs ? KS : 1)] : qs[(ks * NR + j) * 32 + lane];
-                                    if (ks == 0)
-                                        mma_f16_first(z[j], k8[0][0], k8[1][0], k8[0][1], k8[1][1], q.x, q.y);
-                                    else
-                                        mma_f16(z[j], k8[0][2 * k2], k8[1][2 * k2], k8[0][2 * k2 + 1], k8[1][2 * k2 + 1], q.x, q.y);
-                                    if (F) {
-                                        const uint2 ql = qs[((KS + ks) * NR + j) * 32 + lane];
-                                        mma_f16(z[j], k8[0][2 * k2], k8[1][2 * k2], k8[0][2 * k2 + 1], k8[1][2 * k2 + 1], ql.x, ql.y);
-                                    }
+                                for (int x = 0; x < 2; ++x) {
+                                    e2m1x8_to_half2(wi & 1 ? kc[u][y][x][wi / 2].y : kc[u][y][x][wi / 2].x, k8[x]);
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j) k8[x][j] = hmul2(k8[x][j], s2[x][wi / 2]);
                                 }
-                        }
-                        const bool edge = tok + kGroup > low;  // some row does not see all of these tokens
-                        float s0 = 0.0f, s1 = 0.0f;  // tokens g and g + 8
 #pragma unroll
-                        for (int j = 0; j < NR; ++j)
+                                for (int k2 = 0; k2 < 2; ++k2)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                float p = weight(z[j][e], zf[j][e & 1], lse[j][e & 1]);
-                                if (edge && tok + g + 8 * (e >> 1) >= lim[j][e & 1]) p = 0.0f;
-                                (e < 2 ? s0 : s1) += p;
+                                    for (int j = 0; j < NR; ++j) {
+                                        const int ks = 2 * wi + k2;
+                                        const uint2 q = kQRegs ? qf[ks % (kQRegs ? KS : 1)] : qs[(ks * NR + j) * 32 + lane];
+                                        if (ks == 0)
+                                            mma_f16_first(z[j], k8[0][0], k8[1][0], k8[0][1], k8[1][1], q.x, q.y);
+                                        else
+                                            mma_f16(z[j], k8[0][2 * k2], k8[1][2 * k2], k8[0][2 * k2 + 1], k8[1][2 * k2 + 1],
+                                                    q.x, q.y);
+                                        if (F) {
+                                            const uint2 ql = qs[((KS + ks) * NR + j) * 32 + lane];
+                                            mma_f16(z[j], k8[0][2 * k2], k8[1][2 * k2], k8[0][2 * k2 + 1], k8[1][2 * k2 + 1],
+                                                    ql.x, ql.y);
+                                        }
+                                    }
                             }
-                        // over the four lanes of a token: even lanes end with token g, odd ones with g + 8
-                        const float give = t4 & 1 ? s0 : s1;
-                        sum = t4 & 1 ? s1 : s0;
-                        sum += __shfl_xor_sync(0xffffffffu, give, 1);
-                        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                            s2t[y][0] = s2t[y][1] = make_float2(0.0f, 0.0f);
+#pragma unroll
+                            for (int j = 0; j < NR; ++j) {
+                                float2 p0 = weight2(make_float2(z[j][0], z[j][1]), zf[j], lse[j]);
+                                float2 p1 = weight2(make_float2(z[j][2], z[j][3]), zf[j], lse[j]);
+                                if (edge) {
+                                    const int t0 = tok + kGroup * y + g;
+                                    if (t0 >= lim[j].x) p0.x = 0.0f;
+                                    if (t0 >= lim[j].y) p0.y = 0.0f;
+                                    if (t0 + 8 >= lim[j].x) p1.x = 0.0f;
+                                    if (t0 + 8 >= lim[j].y) p1.y = 0.0f;
+                                }
+                                s2t[y][0] = j ? add2(s2t[y][0], p0) : p0;
+                                s2t[y][1] = j ? add2(s2t[y][1], p1) : p1;
+                            }
+                        }
+                        // over the four lanes of a token: lane t4 ends with token 8 t4 + g of the step
+                        const bool up = t4 & 2, odd = t4 & 1;
+                        float2 k0 = up ? s2t[1][0] : s2t[0][0], k1 = up ? s2t[1][1] : s2t[0][1];
+                        const float2 g0 = up ? s2t[0][0] : s2t[1][0], g1 = up ? s2t[0][1] : s2t[1][1];
+                        float x0 = k0.x + k0.y + __shfl_xor_sync(0xffffffffu, g0.x + g0.y, 2);
+                        float x1 = k1.x + k1.y + __shfl_xor_sync(0xffffffffu, g1.x + g1.y, 2);
+                        sum = (odd ? x1 : x0) + __shfl_xor_sync(0xffffffffu, odd ? x0 : x1, 1);
                     }
-                    const int place = tok + g + 8 * t4;
-                    if (i < cnt && t4 < 2 && place < n && (ok >> u & 1)) w.acc_out[sums + place] = fmaf(decay, base[u], sum);
+                    if (i < cnt && tok + 8 * t4 + g < n && (ok >> (2 * u + (t4 >> 1)) & 1))
+                        w.acc_out[sums + (long long)i * kTok] = fmaf(decay, base[u], sum);
                     load(u, i + kAhead);
                 }
             }
@@ -415,10 +467,10 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
 
 // ------------------------------------------------------------------ launch
 
-// Parts of the line for `blocks` blocks on each SM, and the block that checks.
+// The block that checks, and those with parts of the line: `blocks` on each SM in all.
 static unsigned weigh_grid(const CacheArgs& a, const WeighArgs& w, int blocks) {
-    const long long groups = (long long)a.B * a.Hkv * ((w.cap + kGroup - 1) / kGroup);
-    return (unsigned)std::min<long long>((groups + kWarps - 1) / kWarps, (long long)blocks * num_sms()) + 1;
+    const long long steps = (long long)a.B * a.Hkv * ((w.cap + kTok - 1) / kTok);
+    return (unsigned)std::min<long long>((steps + kWarps - 1) / kWarps + 1, (long long)blocks * num_sms());
 }
 
 template <typename T, int D, int NR>
@@ -429,7 +481,7 @@ static cudaError_t mma_t(const CacheArgs& a, const WeighArgs& w, const void* Q, 
         const cudaError_t e = set_smem_once((const void*)k_cache_weigh<T, D, NR>, smem, &done);
         if (e != cudaSuccess) return e;
     }
-    k_cache_weigh<T, D, NR><<<weigh_grid(a, w, 2), kThreads, smem, st>>>(a, w, (const T*)Q, cache);
+    k_cache_weigh<T, D, NR><<<weigh_grid(a, w, kBlocks), kThreads, smem, st>>>(a, w, (const T*)Q, cache);
     count_launch();
     return cudaGetLastError();
 }
