@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmita.so")
 SOURCES = ["api.cu", "simt.cu", "select.cu", "tc.cu", "static_ws.cu", "backward.cu", "cache.cu", "cache_attn.cu",
-           "cache_tile.cu", "cache_weigh.cu", "cache_evict.cu", "rope.cu"]
+           "cache_tile.cu", "cache_weigh.cu", "cache_weigh_tile.cu", "cache_evict.cu", "rope.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC,-O2",
          "-I" + os.path.join(ROOT, "include")]

@@ -40,7 +40,7 @@
 // fewer and longer copies (each takes 180 clocks to issue).
 #include <atomic>
 
-#include "cache_walk.cuh"
+#include "cache_tc.cuh"
 
 namespace mita {
 
@@ -59,38 +59,6 @@ struct TileSmem {
     static constexpr int kQ = 0, kPo = kQ + 64 * kD * 2, kRawO = kPo + kSoftStages * kP,
                          kBytes = kRawO + kRawStages * kRaw + 1024;
 };
-
-// Instruction descriptor of kind::f16 with half A and B and fp32 accumulate.
-constexpr uint32_t idesc_half(int M, int N, int a_mn, int b_mn) {
-    return (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
-           ((uint32_t)(M >> 4) << 24);
-}
-
-struct Abort {
-    int flag;   // a role has given up
-    int limit;  // what a wait takes at most, in kSpinTest (from shared memory: as the kernel's
-                // parameter it took operands out of the uniform registers, 263.8 us against 261.4)
-};
-// Bounded wait that also ends when another role has given up.
-__device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t parity, volatile Abort* abort) {
-    if (tc::mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (!tc::mbar_try_wait(bar, parity)) {
-        if (abort->flag) return false;
-        if (clock64() - t0 > abort->limit * tc::kSpinTest) {
-            abort->flag = 1;
-            return false;
-        }
-    }
-    return true;
-}
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile Abort* abort) {
-    return __all_sync(0xffffffffu, tile_wait(bar, parity, abort));
-}
-// For what this block has issued to the asynchronous units, whatever the abort flag says.
-__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, int* status, long long lim) {
-    (void)tc::mbar_wait(bar, parity, status, lim);
-}
 
 // The four softmax warps with the same rows meet here (barrier 1 + wg), all of them the
 // same number of times whatever happened to the waits before.
@@ -112,11 +80,6 @@ __device__ __forceinline__ bool softmax_any(int wg, bool x) {
     return r != 0;
 }
 
-// (No memory clobber: loads may move across. fence_proxy_async() orders it.)
-__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d));
-}
-
 // Joins v[0..16) over the 32 lanes: each step a lane keeps half of the values and
 // gives the other half away. Lane l ends with value l / 2, in v[0].
 template <typename Op> __device__ __forceinline__ void reduce_lanes(float* v, int lane, Op op) {
@@ -136,15 +99,6 @@ template <typename Op> __device__ __forceinline__ void reduce_lanes(float* v, in
     }
 }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
-    uint32_t* r = reinterpret_cast<uint32_t*>(v);
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
     const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
     asm volatile(
@@ -153,12 +107,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
         "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
-}
-// Registers {a0, a1, a2, a3} of an m16n8k16 step's A, twice (two steps): 16 lanes, 16 columns.
-__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t* r) {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
 }
 __device__ __forceinline__ void load_cols(uint32_t taddr, float* v) {  // HN columns
     tmem_ld16(taddr, v);
@@ -176,18 +124,6 @@ __device__ __noinline__ float seen_nan(float v, const uint8_t* nanv, int low, in
         if (nanv[x - low] >> blk & 1) v = __int_as_float(0x7fc00000);
     return v;
 }
-// One lane of a whole warp. (Behind a branch on this the compiler keeps the products'
-// operands in uniform registers; behind one on the lane's number it moves each there.)
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r));
-    return r != 0;
-}
-
 struct TileBars {
     uint64_t raw_full[kRawStages], raw_empty[kRawStages], k_full[2], v_full[2], v_empty[2];
     uint64_t s_full[kSoftStages], p_full[kSoftStages], q_full, o_full, drain;

@@ -13,7 +13,7 @@
 // added in an order of its own, whatever the cut, so the same call gives the same bits.
 #include <algorithm>
 
-#include "cache_walk.cuh"
+#include "cache_weigh.cuh"
 
 namespace mita {
 
@@ -23,132 +23,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;  // of a block
 constexpr int kTok = 2 * kGroup;                       // tokens of a warp's step
 constexpr int kAhead = 2;                              // steps that a warp's loads are ahead
 constexpr int kBlocks = 2;                             // of an SM
-
-struct WeighArgs {
-    const float* lse;
-    const float* acc;
-    float* acc_out;
-    float decay;
-    long long cap;  // places of a sequence
-};
-
-// Where a warp is on the line. begin() is called by the whole block.
-struct LineStart {
-    unsigned long long before[kThreads], warps[kWarps];
-};
-struct Place {
-    int b, h, at, steps, n, count;  // sequence, cache head, step of it; the sequence's
-    long long left;                 // steps of the warp's part from here on
-
-    __device__ __forceinline__ void enter(const CacheArgs& a, int seq) {
-        b = seq;
-        n = cache_len(a, b);
-        count = cache_count(a, b);
-        steps = (n + kTok - 1) / kTok;
-    }
-    // The part of warp `me` of `all`. A thread sums up its share of the sequences.
-    __device__ __forceinline__ void begin(const CacheArgs& a, LineStart& s, long long me, long long all) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        const int per = (a.B + kThreads - 1) / kThreads;
-        unsigned long long mine = 0;
-#pragma unroll 4
-        for (int i = 0; i < per; ++i) {
-            const int q = threadIdx.x * per + i;
-            if (q < a.B) mine += (unsigned long long)((cache_len(a, q) + kTok - 1) / kTok) * a.Hkv;
-        }
-        unsigned long long x = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        if (lane == 31) s.warps[warp] = x;
-        __syncthreads();
-        unsigned long long total = 0, base = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w == warp) base = total;
-            total += s.warps[w];
-        }
-        s.before[threadIdx.x] = base + x - mine;
-        __syncthreads();
-        const unsigned long long q = total / all, r = total - q * all;
-        const unsigned long long w0 = me * q + min((unsigned long long)me, r);
-        left = (long long)(q + ((unsigned long long)me < r));
-        b = a.B;
-        if (left == 0) return;
-        int slices = 0;  // threads whose share begins at or before w0
-#pragma unroll
-        for (int i = 0; i < kThreads; i += 32) slices += __popc(__ballot_sync(0xffffffffu, s.before[i + lane] <= w0));
-        unsigned long long off = w0 - s.before[slices - 1];
-        // (shares of threads without sequences begin at the total, which is above w0; a sequence without
-        // tokens shares its beginning with the next)
-        bool found = false;
-        for (int seq = (slices - 1) * per; seq < a.B && !found; ++seq) {
-            enter(a, seq);
-            const unsigned long long units = (unsigned long long)steps * a.Hkv;
-            found = off < units;
-            if (!found) off -= units;
-        }
-        if (!found) {  // lengths that changed under the call
-            left = 0;
-            return;
-        }
-        h = (int)(off / steps);
-        at = (int)(off - (unsigned long long)h * steps);
-    }
-    // Behind `done` steps of the same head.
-    __device__ __forceinline__ bool next(const CacheArgs& a, int done) {
-        left -= done;
-        at += done;
-        if (left <= 0) return false;
-        if (at < steps) return true;
-        at = 0;
-        if (++h < a.Hkv) return true;
-        h = 0;
-        for (int seq = b + 1; seq < a.B; ++seq) {
-            enter(a, seq);
-            if (steps) return true;
-        }
-        return false;
-    }
-};
-
-// exp(z - lse), at most 1, for a score z = dot f: one rounding of the difference, so that the weights that
-// matter, whose scores are near lse, keep their bits. (Scores of 2^28 and more are further from
-// a rounded lse than exponents reach; a sum that became infinite would stay so.) NaN stays NaN.
-__device__ __forceinline__ float weight(float dot, float f, float lse) {
-    float t = fmaf(dot, f, -lse);
-    asm("min.NaN.f32 %0, %0, %1;" : "+f"(t) : "f"(0.0f));
-    return tc::ex2(t * kLog2e);
-}
-
-// Two at a time (the packed forms take one issue slot).
-__device__ __forceinline__ uint64_t pack2(float2 x) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x.x), "f"(x.y));
-    return r;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t x) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-    return r;
-}
-__device__ __forceinline__ float2 add2(float2 x, float2 y) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(x)), "l"(pack2(y)));
-    return unpack2(r);
-}
-__device__ __forceinline__ float2 weight2(float2 dot, float2 f, float2 minus_lse) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pack2(dot)), "l"(pack2(f)), "l"(pack2(minus_lse)));
-    float2 t = unpack2(r);
-    asm("min.NaN.f32 %0, %0, %1;" : "+f"(t.x) : "f"(0.0f));
-    asm("min.NaN.f32 %0, %0, %1;" : "+f"(t.y) : "f"(0.0f));
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(t)), "l"(pack2(make_float2(kLog2e, kLog2e))));
-    t = unpack2(r);
-    return make_float2(tc::ex2(t.x), tc::ex2(t.y));
-}
+constexpr int kMmaRows = 16;
 
 }  // namespace
 
@@ -167,13 +42,13 @@ __global__ void __launch_bounds__(kThreads)
 k_cache_weigh_simt(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* __restrict__ cache) {
     using L = Grp<D>;
     constexpr int E = D / 8;  // channels of a lane
-    __shared__ LineStart start;
+    __shared__ LineStart<kThreads> start;
     if (blockIdx.x == 0) {
         check(a);
         return;
     }
     const int lane = threadIdx.x & 31, sub = lane >> 3, ch = lane & 7, blk = D == 128 ? ch : ch >> 1;
-    Place at;
+    Place<kTok, kThreads> at;
     at.begin(a, start, (long long)(blockIdx.x - 1) * kWarps + (threadIdx.x >> 5), (long long)(gridDim.x - 1) * kWarps);
     if (at.left == 0) return;
     do {
@@ -258,14 +133,14 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
     constexpr bool kQRegs = NR == 1 && !F;
     constexpr int KS = D / 16, W = D / 32, RT = 8 * NR, KW = D / 64;  // KW: 8-byte words of a lane's codes of a token
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ LineStart start;
+    __shared__ LineStart<kThreads> start;
     if (blockIdx.x == 0) {
         check(a);
         return;
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
     uint2* qs = reinterpret_cast<uint2*>(smem + warp * q_bytes<T, D, NR>());
-    Place at;
+    Place<kTok, kThreads> at;
     at.begin(a, start, (long long)(blockIdx.x - 1) * kWarps + warp, (long long)(gridDim.x - 1) * kWarps);
     if (at.left == 0) return;
     for (bool more = true; more;) {
@@ -495,6 +370,7 @@ static cudaError_t weigh_t(const CacheArgs& a, const WeighArgs& w, unsigned flag
         return cudaGetLastError();
     }
     const long long rows = (long long)a.G * a.T;
+    if (rows > kMmaRows) return launch_cache_weigh_tile(a, w, D, sizeof(T) == 4 ? 0 : 1, Q, cache, st);
     if (rows <= 8) return mma_t<T, D, 1>(a, w, Q, cache, st);
     if (rows <= 16 || sizeof(T) == 4) return mma_t<T, D, 2>(a, w, Q, cache, st);
     return mma_t<T, D, sizeof(T) == 4 ? 2 : 4>(a, w, Q, cache, st);

@@ -108,6 +108,9 @@ CASES = [
     ("bf16", 128, 48, 33, 1, 2, True, [1, 700], None, True, 0.0),
     ("bf16", 128, 16, 66, 1, 9, True, [600, 8, 9], [9, 9, 0], False, 1.0),   # 594 rows a head
     ("bf16", 64, 32, 32, 2, 17, False, [400, 129], [17, 5], True, 0.0),
+    ("bf16", 128, 64, 64, 1, 4, True, [60000, 40], None, False, 1.0),        # several tiles of rows, for long
+    ("bf16", 64, 32, 90, 1, 6, True, [9, 30001], [6, 5], False, 0.5),        # two passes over the rows
+    ("f32", 128, 64, 50, 1, 6, False, [20000], None, False, 1.0),
     ("f32", 128, 64, 2, 2, 1, False, [1, 127, 700], None, True, 1.0),
     ("f32", 64, 16, 6, 2, 3, True, [500, 2, 33], [3, 3, 1], False, 0.75),
     ("f32", 128, 32, 8, 1, 1, True, [4000, 0], None, False, 1.0),
