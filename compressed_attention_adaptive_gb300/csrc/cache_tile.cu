@@ -112,12 +112,6 @@ __device__ __forceinline__ void load_cols(uint32_t taddr, float* v) {  // HN col
     tmem_ld16(taddr, v);
     tc::tmem_wait_ld();
 }
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
-    uint32_t* r = reinterpret_cast<uint32_t*>(v);
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
-}
 // v, or NaN if a token from `low` on that the row sees (up to `end`) has NaN in this block of its values
 __device__ __noinline__ float seen_nan(float v, const uint8_t* nanv, int low, int end, int blk) {
     for (int x = low; x < end; ++x)

@@ -6,7 +6,7 @@
 //                shared memory, fp32 in tensor memory
 //
 // A lane of tensor memory is a token, so a thread has a token's scores with all rows: it adds up their weights
-// by itself, and nothing is exchanged between threads. What a token costs is then one exponential per row
+// by itself. What a token costs is then one exponential per row
 // and the four or so instructions around it; keys are widened once for all rows of a pass.
 //
 // Keys go from memory to registers in the order of m16n8k16's A (the cache's own order: neighbouring lanes
@@ -14,8 +14,9 @@
 // channels of a token in the order {t d/4 + 2 m, t d/4 + 2 m + 1 : t = 0 .. 3} for m = 0, 1, ...; Q's rows are stored in
 // the same order.
 //
-// Warps: three warpgroups for the weights, each with a stage of scores and every third chunk of 128 tokens; eight
-// warps widen keys, four at a time a chunk, each the quarter of the lanes that it can reach; one issues the products.
+// Warps: four warpgroups for the weights, each with a quarter of a tile's rows; they take turns at joining the four parts of
+// a chunk's sums. Eight warps widen keys, four at a time a chunk, each the quarter of the lanes that it can
+// reach; one issues the products.
 // Every wait is bounded; a block that gives up raises its abort flag, lets its products land, frees its
 // tensor memory and says so in the status word.
 #include <algorithm>
@@ -28,24 +29,39 @@ namespace mita {
 
 namespace {
 
-constexpr int kTok = 128, kCols = 128;           // tokens of a chunk; rows of a tile
-constexpr int kSoft = 3;                         // warpgroups for the weights, and stages of scores
+constexpr int kTok = 128;                        // tokens of a chunk
+constexpr int kScores = 256, kKeys = 4;          // columns of scores; stages of keys
+constexpr int kSoft = 4;                         // warpgroups for the weights
 constexpr int kWiden = 4 * kSoft, kIssue = kWiden + 8;  // first warps of the other roles
 constexpr int kThreads = 32 * (kIssue + 1);
-constexpr int kAhead = 2;                        // chunks of its own that a widening warp's loads are ahead
-constexpr uint32_t kK = kSoft * kCols;           // column of the first of two stages of keys
+constexpr int kRaw = 3;                          // stages of codes of a widening warp: copies are kRaw - 1 chunks ahead
+constexpr uint32_t kK = kScores;                 // column of the first stage of keys
 
-// Scores are announced to the warpgroup that waits for them, not by stage: a warpgroup does not use every stage in
-// turn, and a barrier that it had not looked at for two phases would look done. It has at
-// most kSoft tiles to come, so that of kReady barriers in turn each is at most one phase ahead.
-constexpr int kReady = 4;
-static_assert(kReady > kSoft, "a barrier would be two phases ahead");
-struct WeighBars {
-    uint64_t k_full[2], k_empty[2], s_full[kSoft][kReady], s_empty[kSoft], drain;
+// SPLIT: warpgroups that share a tile, with a part of its rows each. Without a split (up to 64 rows, one tile) each has
+// every fourth chunk to itself.
+template <int SPLIT> struct Tiles {
+    static constexpr int kCols = SPLIT == 1 ? 64 : 128;    // rows of a tile
+    static constexpr int kStages = kScores / kCols;        // of scores
 };
 
-// Bytes of a tile's rows: as halves (two for float rows), factors and log sums, limits.
-template <typename T, int D> constexpr int tile_bytes() { return kCols * (D * 2 * (sizeof(T) == 4 ? 2 : 1) + 8 + 4); }
+// Parts of a chunk's sums, for the warpgroup whose number the chunk's is modulo kSoft; it joins them behind its own part
+// of the next chunk. A buffer is used again eight chunks later: a warpgroup comes there only after all have
+// released the scores of a chunk kStages before it, which the joining one does after its join.
+constexpr int kParts = 8;
+static_assert(kParts % kSoft == 0 && kParts > Tiles<kSoft>::kStages + 1, "parts would be overwritten");
+struct WeighBars {
+    uint64_t k_full[kKeys], k_empty[kKeys], s_full[kSoft], s_empty[kSoft], p_full[kParts], drain;
+};
+
+// Bytes of a tile's rows: as halves (two for float rows); log sums, factors, limits.
+template <typename T, int D, int COLS> constexpr int tile_bytes() { return COLS * (D * 2 * (sizeof(T) == 4 ? 2 : 1) + 12); }
+
+// Rows whose largest entry is in [2^-4, 2^7) (or 0) are all scaled by 2^8, others each as in cache_weigh.cu. Where all rows
+// of a pass are of the first kind, which queries are, they share a factor of the scores, and a weight
+// takes one number of its row from shared memory instead of two. Entries of 2^-24 and more are exact as halves then, the others
+// within 2^-33.
+constexpr int kUsual = 8;
+__device__ __forceinline__ bool usual_row(uint32_t amax) { return amax == 0 || (amax >> 23 >= 123 && amax >> 23 < 134); }
 
 // Groups of a role's own chunks, `every` apart: lane l looks up group 2 quarter + l % 2 of chunk i + l / 2.
 struct Groups {
@@ -66,11 +82,38 @@ struct Groups {
     }
 };
 
+// Bytes of the widening warps' codes and scales: two groups' keys of each stage.
+template <int D> constexpr int raw_bytes() { return 8 * kRaw * 2 * 9 * D; }
+
+template <int N> __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+    if (N == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
+
+// Whether any thread but the widening ones has x; they all meet here.
+__device__ __forceinline__ bool any_but_widening(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.red.or.pred q, 1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x), "n"(32 * (kWiden + 1))
+        : "memory");
+    return r != 0;
+}
+
 // The loads into v have arrived.
 __device__ __forceinline__ void wait_cols(float* v) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
-                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                   "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]),
+                   "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
+                   "+f"(v[30]), "+f"(v[31])
                  :
                  : "memory");
 }
@@ -84,20 +127,23 @@ __global__ void __launch_bounds__(256) k_cache_weigh_begin(CacheArgs a) {
     if (threadIdx.x == 0) *a.status = bad ? kStBounds : kStOk;
 }
 
-template <typename T, int D>
+template <typename T, int D, int SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 k_cache_weigh_tile(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* __restrict__ cache, int tiles) {
     using L = Grp<D>;
     constexpr bool F = sizeof(T) == 4;  // float rows: two halves, hi + lo
-    constexpr int KS = D / 16, W = D / 32, KW = D / 64, kHalf = kCols * D * 2, kTile = (F ? 2 : 1) * kHalf;
+    constexpr int kCols = Tiles<SPLIT>::kCols, kStages = Tiles<SPLIT>::kStages;
+    constexpr int KS = D / 16, W = D / 32, kHalf = kCols * D * 2, kTile = (F ? 2 : 1) * kHalf;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t sm = (tc::smem_u32(smem_raw) + 1023) & ~1023u;
     uint8_t* smp = smem_raw + (sm - tc::smem_u32(smem_raw));
-    // of two rows each: factors of the scores, log sums negated
-    float4* ref = reinterpret_cast<float4*>(smp + tiles * kTile);
-    int* lim = reinterpret_cast<int*>(ref + tiles * (kCols / 2));  // keys that a row sees
+    float* mlse = reinterpret_cast<float*>(smp + tiles * kTile);  // of a row: its log sum, negated;
+    float* fac = mlse + tiles * kCols;                            // the factor of its scores;
+    int* lim = reinterpret_cast<int*>(fac + tiles * kCols);       // the keys that it sees
+    const uint32_t raw = tc::smem_u32(lim + tiles * kCols);
     __shared__ LineStart<kThreads> start;
     __shared__ WeighBars bar;
+    __shared__ float parts[SPLIT == 1 ? 1 : kParts][kSoft][kTok];  // [chunk][warpgroup]
     __shared__ uint32_t tmem_slot;
     __shared__ Abort abort;
     volatile Abort* abort_v = &abort;
@@ -105,15 +151,16 @@ k_cache_weigh_tile(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint
     // (waits for another kernel's blocks on this SM, which end whatever this one does)
     if (warp == kIssue) tc::tmem_alloc(&tmem_slot, 512);
     if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kKeys; ++i) {
             // (fault test: one more signal for one block's keys than comes)
             tc::mbar_init(&bar.k_full[i], a.stall && blockIdx.x == 0 ? 5 : 4);
             tc::mbar_init(&bar.k_empty[i], 1);
         }
-        for (int i = 0; i < kSoft; ++i) {
-            for (int j = 0; j < kReady; ++j) tc::mbar_init(&bar.s_full[i][j], 1);
-            tc::mbar_init(&bar.s_empty[i], 4);
+        for (int i = 0; i < kStages; ++i) {
+            tc::mbar_init(&bar.s_full[i], 1);
+            tc::mbar_init(&bar.s_empty[i], 4 * SPLIT);
         }
+        for (int i = 0; i < kParts; ++i) tc::mbar_init(&bar.p_full[i], 4 * kSoft);
         tc::mbar_init(&bar.drain, 1);
         tc::fence_mbar_init();
         abort.flag = 0;
@@ -126,7 +173,6 @@ k_cache_weigh_tile(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
 
     int done = 0, units = 0;  // chunks and tiles before this pass: the stages and their phases go on
-    uint32_t turn = 0;        // tiles that a warpgroup has had; of the issuing warp: a byte for each warpgroup
     for (bool more = at.left > 0; more;) {
         const int cnt = (int)min(at.left, (long long)(at.steps - at.at)), n = at.n, c0 = at.at;
         const int rows = at.count * a.G;
@@ -134,10 +180,12 @@ k_cache_weigh_tile(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint
         bool stop = false;
         for (int row0 = 0; row0 < max(rows, 1) && !stop; row0 += tiles * kCols) {
             const int here = max(0, min(rows - row0, tiles * kCols));     // rows of the pass
-            const int padded = max(16, (here + 15) & ~15), nt = (padded + kCols - 1) / kCols;
-            // Q: a thread has channels 4 x .. 4 x + 3 of each quarter of a row's
+            const int padded = max(32, (here + 31) & ~31), nt = (padded + kCols - 1) / kCols;
             constexpr int PER = D / 16;
-            for (int r = tid / PER; r < padded; r += kThreads / PER) {  // (a warp's rows: all or none)
+            auto factor = [&](int qe) { return fminf(a.scale * pow2(cache_exp(a, 0, at.h)) * pow2(-qe), 3.4028235e38f); };
+            bool unusual = false;
+            // Q, by the weights' warps: a thread has channels 4 x .. 4 x + 3 of each quarter of a row's
+            for (int r = tid / PER; r < padded && warp < kWiden; r += 32 * kWiden / PER) {  // (a warp's rows: all or none)
                 const int x = tid % PER;
                 int t = 0;
                 const bool in = r < here;
@@ -163,12 +211,15 @@ k_cache_weigh_tile(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint
                                            : max(v[i][j] << 16 & 0x7fff0000u, v[i][j] & 0x7fff0000u));
 #pragma unroll
                 for (int i = 1; i < PER; i <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, i));
-                float up;
-                const int qe = query_exp(amax >> 23, &up);
+                float up = pow2(kUsual);
+                int qe = kUsual;
+                if (!usual_row(amax)) {
+                    qe = query_exp(amax >> 23, &up);
+                    unusual = true;
+                }
                 if (x == 0) {
-                    float* f = reinterpret_cast<float*>(ref + (r >> 1)) + (r & 1);
-                    f[0] = fminf(a.scale * pow2(cache_exp(a, 0, at.h)) * pow2(-qe), 3.4028235e38f);
-                    f[2] = in ? -w.lse[row] : -INFINITY;  // (a row that is not there: weights of 0)
+                    fac[r] = factor(qe);
+                    mlse[r] = in ? -w.lse[row] : -INFINITY;  // (a row that is not there: weights of 0)
                     lim[r] = in ? row_limit(a, n, at.count, t) : 0;
                 }
                 const uint32_t to = sm + (r / kCols) * kTile;
@@ -188,188 +239,235 @@ k_cache_weigh_tile(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint
                     if (F) st_shared16(to + kHalf + off, lo[0], lo[1], lo[2], lo[3]);
                 }
             }
-            tc::fence_proxy_async();
-            __syncthreads();
+            if (warp < kWiden || warp == kIssue) {
+                tc::fence_proxy_async();
+                unusual = any_but_widening(unusual);
+            }
 
             if (warp < kWiden) {
                 // ------------------------------------------------ weights
-                const int wg = warp >> 2, first = ((wg - done) % kSoft + kSoft) % kSoft, tl = 32 * quarter + lane;
+                const int wg = warp >> 2, tl = 32 * quarter + lane;
+                const int own0 = (wg - done) & (kSoft - 1);  // chunks whose sums the warpgroup stores: from here on, each kSoft-th
                 const int low = here ? row_limit(a, n, at.count, row0 / a.G) : 0;  // keys that all rows of the pass see
                 const long long sums = ((long long)at.b * a.Hkv + at.h) * w.cap + (long long)c0 * kTok + tl;
                 const float* had = (row0 ? w.acc_out : w.acc) + sums;
                 const float decay = row0 ? 1.0f : w.decay;
                 // the thread's tokens with a sum, from the first chunk's on
                 const int olds = (row0 ? n : w.decay != 0.0f ? n - at.count : 0) - (c0 * kTok + tl);
-                auto base_of = [&](int c) { return c < cnt && c * kTok < olds ? had[(long long)c * kTok] : 0.0f; };
                 auto look = [&](int i) {
-                    const int c = first + kSoft * (i + (lane >> 1)), gi = 8 * (c0 + c) + 2 * quarter + (lane & 1);
+                    const int c = own0 + kSoft * (i + (lane >> 1)), gi = 8 * (c0 + c) + 2 * quarter + (lane & 1);
                     return c < cnt && gi * kGroup < n ? cache_group(a, at.b, at.h, gi) : -1;
                 };
-                const uint32_t cols = tmem + ((uint32_t)quarter << 21);
                 Groups groups;
                 groups.start(look);
-                float base = base_of(first);
-                for (int c = first, i = 0; c < cnt; c += kSoft, ++i) {
-                    const float next = base_of(c + kSoft);
-                    const int group = groups.get(i, lane >> 4, look);
-                    groups.step(i, look);
-                    const int tok = (c0 + c) * kTok + tl;
-                    const bool edge = (c0 + c + 1) * kTok > low;  // some row does not see all of the chunk
-                    float2 sum = make_float2(0.0f, 0.0f);
-                    bool ok = true;
-                    for (int ti = 0; ti < nt; ++ti) {
-                        const int ss = (units + c * nt + ti) % kSoft;
-                        if (!(ok = warp_wait(&bar.s_full[wg][turn % kReady], turn / kReady & 1, abort_v))) break;
-                        ++turn;
-                        tc::fence_after_sync();
-                        const int nb = min(kCols, padded - ti * kCols) / 16;  // blocks of 16 columns
-                        const float4* rf = ref + ti * (kCols / 2);
-                        float y[2][16];
-                        tmem_ld16(cols + ss * kCols, y[0]);
-                        auto block = [&](auto masked, int bi, float* now, float* then) {
-                            wait_cols(now);
-                            if (bi + 1 < nb) {
-                                tmem_ld16(cols + ss * kCols + 16 * (bi + 1), then);
-                            } else {  // all of the stage is in registers
-                                tc::fence_before_sync();
-                                __syncwarp();
-                                if (lane == 0) tc::mbar_arrive(&bar.s_empty[ss]);
-                            }
-                            float2 p[8];
+                const float same = factor(kUsual);
+                // Adds to `sum` the weights of the thread's token tok from `share` rows, from r0 on, whose scores are in the
+                // columns from `from` on of stage ss.
+                auto weigh = [&](float2& sum, int ss, uint32_t from, int r0, int share, int tok, bool each) {
+                    const uint32_t cols = tmem + ((uint32_t)quarter << 21) + ss * kCols + from;
+#pragma unroll 1
+                    for (int b0 = 0; b0 < share; b0 += 32, r0 += 32) {
+                        const int here = min(32, share - b0);
+                        float y[32];
+                        if (here == 32) {
+                            tc::tmem_ld32(cols + b0, y);
+                        } else {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const float4 r = rf[8 * bi + j];
-                                p[j] = weight2(make_float2(now[2 * j], now[2 * j + 1]), make_float2(r.x, r.y),
-                                               make_float2(r.z, r.w));
-                            }
-                            if (decltype(masked)::value) {
+                            for (int i = 0; i < 32; i += 8)
+                                if (i < here) tmem_ld8(cols + b0 + i, y + i);
+                        }
+                        wait_cols(y);
+                        if (b0 + 32 >= share) {  // all are in registers
+                            tc::fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) tc::mbar_arrive(&bar.s_empty[ss]);
+                        }
+                        auto some = [&](auto by_row, int i0, auto count) {
+                            constexpr int kRows = decltype(count)::value;
+                            float2 p[kRows / 2];
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) {
-                                    const int2 m = reinterpret_cast<const int2*>(lim)[ti * (kCols / 2) + 8 * bi + j];
-                                    if (tok >= m.x) p[j].x = 0.0f;
-                                    if (tok >= m.y) p[j].y = 0.0f;
+                            for (int j = 0; j < kRows; j += 4) {
+                                const float4 l = *reinterpret_cast<const float4*>(mlse + r0 + i0 + j);
+                                float4 f = make_float4(same, same, same, same);
+                                if (decltype(by_row)::value) f = *reinterpret_cast<const float4*>(fac + r0 + i0 + j);
+                                const float* z = y + i0 + j;
+                                p[j / 2] = weight2(make_float2(z[0], z[1]), make_float2(f.x, f.y), make_float2(l.x, l.y));
+                                p[j / 2 + 1] = weight2(make_float2(z[2], z[3]), make_float2(f.z, f.w), make_float2(l.z, l.w));
+                                if (decltype(by_row)::value) {
+                                    const int4 m = *reinterpret_cast<const int4*>(lim + r0 + i0 + j);
+                                    if (tok >= m.x) p[j / 2].x = 0.0f;
+                                    if (tok >= m.y) p[j / 2].y = 0.0f;
+                                    if (tok >= m.z) p[j / 2 + 1].x = 0.0f;
+                                    if (tok >= m.w) p[j / 2 + 1].y = 0.0f;
                                 }
                             }
 #pragma unroll
-                            for (int o = 4; o; o >>= 1)
+                            for (int o = kRows / 4; o; o >>= 1)
 #pragma unroll
                                 for (int j = 0; j < o; ++j) p[j] = add2(p[j], p[j + o]);
                             sum = add2(sum, p[0]);
                         };
-                        auto tile = [&](auto masked) {
-#pragma unroll 1
-                            for (int bi = 0; bi < nb; bi += 2) {
-                                block(masked, bi, y[0], y[1]);
-                                if (bi + 1 < nb) block(masked, bi + 1, y[1], y[0]);
+                        if (here == 32 && !each) {
+                            some(std::false_type(), 0, std::integral_constant<int, 16>());
+                            some(std::false_type(), 16, std::integral_constant<int, 16>());
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 8) {
+                                if (i >= here) continue;
+                                if (each)
+                                    some(std::true_type(), i, std::integral_constant<int, 8>());
+                                else
+                                    some(std::false_type(), i, std::integral_constant<int, 8>());
                             }
-                        };
-                        if (edge)
-                            tile(std::true_type());
-                        else
-                            tile(std::false_type());
+                        }
                     }
-                    if (!ok) break;
-                    if (tok < n && group >= 0) w.acc_out[sums + (long long)c * kTok] = fmaf(decay, base, sum.x + sum.y);
-                    base = next;
+                };
+                auto base_of = [&](int c) { return c < cnt && c * kTok < olds ? had[(long long)c * kTok] : 0.0f; };
+                // some row does not see all of the chunk, or has a factor of its own
+                auto each = [&](int c) { return unusual || (c0 + c + 1) * kTok > low; };
+                auto store = [&](int c, int group, float base, float sum) {
+                    if ((c0 + c) * kTok + tl < n && group >= 0) w.acc_out[sums + (long long)c * kTok] = fmaf(decay, base, sum);
+                };
+                if (SPLIT == 1) {
+                    float base = base_of(own0);
+                    for (int c = own0, i = 0; c < cnt; c += kSoft, ++i) {
+                        const float next = base_of(c + kSoft);
+                        const int group = groups.get(i, lane >> 4, look);
+                        groups.step(i, look);
+                        if (!warp_wait(&bar.s_full[wg], (done + c) / kSoft & 1, abort_v)) break;
+                        tc::fence_after_sync();
+                        float2 sum = make_float2(0.0f, 0.0f);
+                        weigh(sum, wg, 0, 0, padded, (c0 + c) * kTok + tl, each(c));
+                        store(c, group, base, sum.x + sum.y);
+                        base = next;
+                    }
+                } else {
+                    float base = 0.0f;  // of the chunk that the warpgroup will join
+                    int u = units, joined = 0;
+                    bool ok = true;
+                    for (int c = 0; c <= cnt && ok; ++c) {  // (the last one only joins)
+                        const int t = done + c;
+                        if (c < cnt) {
+                            float2 sum = make_float2(0.0f, 0.0f);
+                            for (int ti = 0; ti < nt; ++ti, ++u) {
+                                const int ss = u % kStages;
+                                if (!(ok = warp_wait(&bar.s_full[ss], u / kStages & 1, abort_v))) break;
+                                tc::fence_after_sync();
+                                const int share = min(kCols, padded - ti * kCols) / SPLIT;
+                                weigh(sum, ss, wg * share, ti * kCols + wg * share, share, (c0 + c) * kTok + tl, each(c));
+                            }
+                            if (!ok) break;
+                            parts[t & (kParts - 1)][wg][tl] = sum.x + sum.y;
+                            __syncwarp();
+                            if (lane == 0) tc::mbar_arrive(&bar.p_full[t & (kParts - 1)]);
+                        }
+                        if (c > 0 && ((t - 1) & (kSoft - 1)) == wg) {
+                            const int pb = (t - 1) & (kParts - 1), group = groups.get(joined, lane >> 4, look);
+                            groups.step(joined++, look);
+                            if (!(ok = warp_wait(&bar.p_full[pb], (t - 1) / kParts & 1, abort_v))) break;
+                            const float* x = &parts[pb][0][tl];
+                            store(c - 1, group, base, (x[0] + x[kTok]) + (x[2 * kTok] + x[3 * kTok]));
+                        }
+                        if ((t & (kSoft - 1)) == wg) base = base_of(c);
+                    }
                 }
             } else if (warp < kIssue) {
                 // ----------------------------------------------- widening
-                const int st = (warp - kWiden) >> 2, first = (st - done) & 1, g = lane >> 2, t4 = lane & 3;
-                const uint8_t* codes = cache + g * L::kRow + t4 * (D / 8);
-                const uint8_t* scales = cache + L::kKs + g * (D / 8) + t4 * (D / 32);
+                const int first = (((warp - kWiden) >> 2) - done) & 1, g = lane >> 2, t4 = lane & 3;
+                const int codes = g * L::kRow + t4 * (D / 8), scales = L::kKs + g * (D / 8) + t4 * (D / 32);
+                const uint32_t ring = raw + (warp - kWiden) * (kRaw * 18 * D);
                 auto look = [&](int i) {
                     const int c = first + 2 * (i + (lane >> 1)), gi = 8 * (c0 + c) + 2 * quarter + (lane & 1);
                     return c < cnt && gi * kGroup < n ? cache_group(a, at.b, at.h, gi) : -1;
                 };
                 Groups groups;
                 groups.start(look);
-                uint2 kc[kAhead][2][2][KW];  // [chunk][group][token g, g + 8]
-                uint32_t sc[kAhead][2];
-                auto load = [&](int u, int i) {  // called for every i in turn
+                // A lane copies what it will read itself (of d = 64 scales, what it and its neighbour will).
+                auto copy = [&](int i) {  // called for every i in turn
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         const int grp = groups.get(i, y, look);
-                        sc[u][y] = 0;  // (tokens that are not there: zeros)
                         if (grp < 0) continue;
-                        const unsigned long long to = (unsigned long long)(unsigned)grp * L::kBytes;
+                        const uint8_t* src = cache + (unsigned long long)(unsigned)grp * L::kBytes;
+                        const uint32_t dst = ring + (i % kRaw) * (18 * D) + y * (9 * D);
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const uint8_t* r = codes + to + 8 * x * L::kRow;
-                            if (D == 128) {
-                                const uint4 v = *reinterpret_cast<const uint4*>(r);
-                                kc[u][y][x][0] = make_uint2(v.x, v.y);
-                                kc[u][y][x][KW - 1] = make_uint2(v.z, v.w);
-                            } else {
-                                kc[u][y][x][0] = *reinterpret_cast<const uint2*>(r);
-                            }
-                        }
-                        sc[u][y] = D == 128 ? *reinterpret_cast<const uint32_t*>(scales + to)
-                                            : *reinterpret_cast<const uint16_t*>(scales + to);
+                        for (int x = 0; x < 2; ++x) copy_async<D / 8>(dst + codes + 8 * x * L::kRow, src + codes + 8 * x * L::kRow);
+                        if (D == 128 || (t4 & 1) == 0) copy_async<4>(dst + scales, src + scales);
                     }
                     groups.step(i, look);
+                    asm volatile("cp.async.commit_group;" ::: "memory");
                 };
 #pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
+                for (int i = 0; i < kRaw - 1; ++i) copy(i);
+                for (int c = first, i = 0; c < cnt; c += 2, ++i) {
+                    const int t = done + c, st = t % kKeys;
+                    asm volatile("cp.async.wait_group %0;" ::"n"(kRaw - 2) : "memory");
+                    __syncwarp();
+                    uint32_t code[2][2][W], sc[2];  // [group][token g, g + 8]
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
+                    for (int y = 0; y < 2; ++y) {
+                        const uint32_t src = ring + (i % kRaw) * (18 * D) + y * (9 * D);
 #pragma unroll
-                        for (int x = 0; x < 2; ++x)
-#pragma unroll
-                            for (int k = 0; k < KW; ++k) kc[u][y][x][k] = make_uint2(0, 0);
-                    load(u, u);
-                }
-                bool ok = true;
-                for (int c = first, i = 0; c < cnt && ok; i += kAhead) {
-#pragma unroll
-                    for (int u = 0; u < kAhead; ++u, c += 2) {
-                        if (c >= cnt || !ok) continue;
-                        const int t = done + c;
-                        if (!(ok = warp_wait(&bar.k_empty[st], ((t >> 1) & 1) ^ 1, abort_v))) continue;
-                        tc::fence_after_sync();
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            uint32_t s2[2][KW];  // [token g, g + 8]: scales, each in both halves
-                            if (D == 128) {
-                                const uint32_t a0 = e4m3x2_to_half2(sc[u][y] & 0xffff), a1 = e4m3x2_to_half2(sc[u][y] >> 16);
-                                s2[0][0] = __byte_perm(a0, a0, 0x1010);
-                                s2[0][KW - 1] = __byte_perm(a0, a0, 0x3232);
-                                s2[1][0] = __byte_perm(a1, a1, 0x1010);
-                                s2[1][KW - 1] = __byte_perm(a1, a1, 0x3232);
-                            } else {
-                                const uint32_t a0 = e4m3x2_to_half2(sc[u][y]);
-                                s2[0][0] = __byte_perm(a0, a0, 0x1010);
-                                s2[1][0] = __byte_perm(a0, a0, 0x3232);
-                            }
-                            const uint32_t to = tmem + ((uint32_t)quarter << 21) + ((uint32_t)y << 20) + kK + st * 64;
-#pragma unroll
-                            for (int wi = 0; wi < W; ++wi) {
-                                uint32_t h[8];
-#pragma unroll
-                                for (int x = 0; x < 2; ++x) {
-                                    uint32_t k4[4];
-                                    e2m1x8_to_half2(wi & 1 ? kc[u][y][x][wi / 2].y : kc[u][y][x][wi / 2].x, k4);
-#pragma unroll
-                                    for (int j = 0; j < 4; ++j) h[2 * j + x] = hmul2(k4[j], s2[x][wi / 2]);
-                                }
-                                tmem_st_frag(to + 16 * wi, h);
-                            }
+                        for (int x = 0; x < 2; ++x) {
+                            const uint32_t p = src + codes + 8 * x * L::kRow;
+                            if (D == 128)
+                                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                             : "=r"(code[y][x][0]), "=r"(code[y][x][1]), "=r"(code[y][x][W - 2]), "=r"(code[y][x][W - 1])
+                                             : "r"(p));
+                            else
+                                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(code[y][x][0]), "=r"(code[y][x][1]) : "r"(p));
                         }
-                        load(u, i + u + kAhead);
-                        tc::tmem_wait_st();
-                        tc::fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) tc::mbar_arrive(&bar.k_full[st]);
+                        if (D == 128)
+                            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sc[y]) : "r"(src + scales));
+                        else
+                            asm volatile("ld.shared.u16 %0, [%1];" : "=r"(sc[y]) : "r"(src + scales));
                     }
+                    copy(i + kRaw - 1);  // (over the stage that all lanes read before the last barrier)
+                    if (!warp_wait(&bar.k_empty[st], ((t / kKeys) & 1) ^ 1, abort_v)) break;
+                    tc::fence_after_sync();
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        uint32_t s2[2][2];  // [token g, g + 8][16 of the lane's channels]: scales, each in both halves
+                        if (D == 128) {
+                            const uint32_t a0 = e4m3x2_to_half2(sc[y] & 0xffff), a1 = e4m3x2_to_half2(sc[y] >> 16);
+                            s2[0][0] = __byte_perm(a0, a0, 0x1010);
+                            s2[0][1] = __byte_perm(a0, a0, 0x3232);
+                            s2[1][0] = __byte_perm(a1, a1, 0x1010);
+                            s2[1][1] = __byte_perm(a1, a1, 0x3232);
+                        } else {
+                            const uint32_t a0 = e4m3x2_to_half2(sc[y]);
+                            s2[0][0] = __byte_perm(a0, a0, 0x1010);
+                            s2[1][0] = __byte_perm(a0, a0, 0x3232);
+                        }
+                        const uint32_t to = tmem + ((uint32_t)quarter << 21) + ((uint32_t)y << 20) + kK + st * 64;
+#pragma unroll
+                        for (int wi = 0; wi < W; ++wi) {
+                            uint32_t h[8];
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                uint32_t k4[4];
+                                e2m1x8_to_half2(code[y][x][wi], k4);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) h[2 * j + x] = hmul2(k4[j], s2[x][wi / 2]);
+                            }
+                            tmem_st_frag(to + 16 * wi, h);
+                        }
+                    }
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&bar.k_full[st]);
                 }
+                tc::cp_async_wait_all();
             } else {
                 // ----------------------------------------------- products
                 bool ok = true;
                 for (int c = 0; c < cnt && ok; ++c) {
-                    const int t = done + c, st = t & 1;
-                    if (!(ok = warp_wait(&bar.k_full[st], (t >> 1) & 1, abort_v))) break;
+                    const int t = done + c, st = t % kKeys;
+                    if (!(ok = warp_wait(&bar.k_full[st], (t / kKeys) & 1, abort_v))) break;
                     for (int ti = 0; ti < nt; ++ti) {
-                        const int u = units + c * nt + ti, ss = u % kSoft;
-                        if (!(ok = warp_wait(&bar.s_empty[ss], u / kSoft & 1 ^ 1, abort_v))) break;
+                        const int u = units + c * nt + ti, ss = u % kStages;
+                        if (!(ok = warp_wait(&bar.s_empty[ss], u / kStages & 1 ^ 1, abort_v))) break;
                         tc::fence_after_sync();
                         const uint32_t id = idesc_half(kTok, min(kCols, padded - ti * kCols), 0, 0);
                         if (elect_one()) {
@@ -380,11 +478,10 @@ k_cache_weigh_tile(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint
                                                               (k & 3) * 32,
                                                           16, 1024),
                                                 id, k > 0);
-                            tc::mma_commit(&bar.s_full[t % kSoft][turn >> 8 * (t % kSoft) & (kReady - 1)]);
+                            tc::mma_commit(&bar.s_full[ss]);
                             if (ti == nt - 1) tc::mma_commit(&bar.k_empty[st]);
                         }
                         __syncwarp();
-                        turn = __vadd4(turn, 1u << 8 * (t % kSoft));
                     }
                 }
             }
@@ -413,14 +510,15 @@ k_cache_weigh_tile(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint
 
 // ------------------------------------------------------------------ launch
 
-template <typename T, int D>
-static cudaError_t tile_t(const CacheArgs& a, const WeighArgs& w, const void* Q, const uint8_t* cache, cudaStream_t st) {
-    // rows of a pass: as many as there are, within 150 KB
-    constexpr int kMost = 150 * 1024 / tile_bytes<T, D>();
+template <typename T, int D, int SPLIT>
+static cudaError_t split_t(const CacheArgs& a, const WeighArgs& w, const void* Q, const uint8_t* cache, cudaStream_t st) {
+    // rows of a pass: as many as there are, as far as they fit (24 KB are static)
+    constexpr int kCols = Tiles<SPLIT>::kCols, kBytes = tile_bytes<T, D, kCols>();
+    constexpr int kMost = SPLIT == 1 ? 1 : ((227 - 24) * 1024 - 1024 - raw_bytes<D>()) / kBytes;
     const long long rows = (long long)a.G * a.T;
     const int tiles = (int)std::min<long long>(kMost, (rows + kCols - 1) / kCols);
     static std::atomic<unsigned long long> done{0};
-    cudaError_t e = set_smem_once((const void*)k_cache_weigh_tile<T, D>, kMost * tile_bytes<T, D>() + 1024, &done);
+    cudaError_t e = set_smem_once((const void*)k_cache_weigh_tile<T, D, SPLIT>, kMost * kBytes + raw_bytes<D>() + 1024, &done);
     if (e != cudaSuccess) return e;
     k_cache_weigh_begin<<<1, 256, 0, st>>>(a);
     count_launch();
@@ -434,13 +532,18 @@ static cudaError_t tile_t(const CacheArgs& a, const WeighArgs& w, const void* Q,
     // (one SM has the kernel before it)
     c.gridDim = dim3((unsigned)std::min<long long>(chunks, num_sms() - 1));
     c.blockDim = dim3(kThreads);
-    c.dynamicSmemBytes = tiles * tile_bytes<T, D>() + 1024;
+    c.dynamicSmemBytes = tiles * kBytes + raw_bytes<D>() + 1024;
     c.stream = st;
     c.attrs = &at;
     c.numAttrs = 1;
-    e = cudaLaunchKernelEx(&c, k_cache_weigh_tile<T, D>, a, w, (const T*)Q, cache, tiles);
+    e = cudaLaunchKernelEx(&c, k_cache_weigh_tile<T, D, SPLIT>, a, w, (const T*)Q, cache, tiles);
     if (e == cudaSuccess) count_launch();
     return e;
+}
+
+template <typename T, int D>
+static cudaError_t tile_t(const CacheArgs& a, const WeighArgs& w, const void* Q, const uint8_t* cache, cudaStream_t st) {
+    return (long long)a.G * a.T <= Tiles<1>::kCols ? split_t<T, D, 1>(a, w, Q, cache, st) : split_t<T, D, kSoft>(a, w, Q, cache, st);
 }
 
 cudaError_t launch_cache_weigh_tile(const CacheArgs& a, const WeighArgs& w, int d, int dtype, const void* Q,
