@@ -15,8 +15,7 @@
 // the same order.
 //
 // Warps: four warpgroups for the weights, each with a quarter of a tile's rows; they take turns at joining the four parts of
-// a chunk's sums. Eight warps widen keys, four at a time a chunk, each the quarter of the lanes that it can
-// reach; one issues the products.
+// a chunk's sums. Four warps widen keys, each the quarter of the lanes that it can reach; one issues the products.
 // Every wait is bounded; a block that gives up raises its abort flag, lets its products land, frees its
 // tensor memory and says so in the status word.
 #include <algorithm>
@@ -32,7 +31,7 @@ namespace {
 constexpr int kTok = 128;                        // tokens of a chunk
 constexpr int kScores = 256, kKeys = 4;          // columns of scores; stages of keys
 constexpr int kSoft = 4;                         // warpgroups for the weights
-constexpr int kWiden = 4 * kSoft, kIssue = kWiden + 8;  // first warps of the other roles
+constexpr int kWiden = 4 * kSoft, kIssue = kWiden + 4;  // first warps of the other roles
 constexpr int kThreads = 32 * (kIssue + 1);
 constexpr int kRaw = 3;                          // stages of codes of a widening warp: copies are kRaw - 1 chunks ahead
 constexpr uint32_t kK = kScores;                 // column of the first stage of keys
@@ -63,7 +62,7 @@ template <typename T, int D, int COLS> constexpr int tile_bytes() { return COLS 
 constexpr int kUsual = 8;
 __device__ __forceinline__ bool usual_row(uint32_t amax) { return amax == 0 || (amax >> 23 >= 123 && amax >> 23 < 134); }
 
-// Groups of a role's own chunks, `every` apart: lane l looks up group 2 quarter + l % 2 of chunk i + l / 2.
+// Groups of a role's own chunks: lane l looks up group 2 quarter + l % 2 of its own chunk i + l / 2.
 struct Groups {
     int cur, nxt;
     template <typename Look> __device__ __forceinline__ void start(Look look) {
@@ -83,7 +82,7 @@ struct Groups {
 };
 
 // Bytes of the widening warps' codes and scales: two groups' keys of each stage.
-template <int D> constexpr int raw_bytes() { return 8 * kRaw * 2 * 9 * D; }
+template <int D> constexpr int raw_bytes() { return 4 * kRaw * 2 * 9 * D; }
 
 template <int N> __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
     if (N == 16)
@@ -373,11 +372,11 @@ k_cache_weigh_tile(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint
                 }
             } else if (warp < kIssue) {
                 // ----------------------------------------------- widening
-                const int first = (((warp - kWiden) >> 2) - done) & 1, g = lane >> 2, t4 = lane & 3;
+                const int g = lane >> 2, t4 = lane & 3;
                 const int codes = g * L::kRow + t4 * (D / 8), scales = L::kKs + g * (D / 8) + t4 * (D / 32);
                 const uint32_t ring = raw + (warp - kWiden) * (kRaw * 18 * D);
                 auto look = [&](int i) {
-                    const int c = first + 2 * (i + (lane >> 1)), gi = 8 * (c0 + c) + 2 * quarter + (lane & 1);
+                    const int c = i + (lane >> 1), gi = 8 * (c0 + c) + 2 * quarter + (lane & 1);
                     return c < cnt && gi * kGroup < n ? cache_group(a, at.b, at.h, gi) : -1;
                 };
                 Groups groups;
@@ -399,8 +398,8 @@ k_cache_weigh_tile(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint
                 };
 #pragma unroll
                 for (int i = 0; i < kRaw - 1; ++i) copy(i);
-                for (int c = first, i = 0; c < cnt; c += 2, ++i) {
-                    const int t = done + c, st = t % kKeys;
+                for (int i = 0; i < cnt; ++i) {
+                    const int t = done + i, st = t % kKeys;
                     asm volatile("cp.async.wait_group %0;" ::"n"(kRaw - 2) : "memory");
                     __syncwarp();
                     uint32_t code[2][2][W], sc[2];  // [group][token g, g + 8]
