@@ -295,77 +295,60 @@ __global__ void __launch_bounds__(kThreads, 2) k_cache_evict(CacheArgs a, EvictA
     const int moves = min(min(ah, am), cap_list);
     cluster_sync<C>();  // the lists are there, acc has been read, and no block reads another's memory any more
 
-    // A thread moves 16 channels of keys and values, as they are held, of two rows at a time. The next
-    // rows are looked up while these are on their way.
-    constexpr int NB = L::kBlocks, kAtOnce = 2, kStride = C * kThreads;  // (kStride is a multiple of NB)
-    const long long all = (long long)moves * NB;
-    const int blk = threadIdx.x % NB;
-    struct Move {
-        int to[kAtOnce], from[kAtOnce], gt[kAtOnce], gf[kAtOnce];  // places; their groups, -1: nothing to move
-    };
-    auto places_of = [&](Move& m, long long i0) {
-#pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
-            const long long i = i0 + u * kStride;
-            m.to[u] = i < all ? holes[i / NB] : -1;
-            m.from[u] = i < all ? movers[i / NB] : -1;
+    // A warp takes up to 32 moves: a lane looks up one of them, then NB lanes share each, with 16 channels of
+    // keys and values as they are held. Few moves are spread over all warps.
+    constexpr int NB = L::kBlocks, kTeams = 32 / NB, kAtOnce = 4, kAll = C * kWarps;
+    const int per = min(32, ((moves + kAll - 1) / kAll + kTeams - 1) / kTeams * kTeams);
+    const int blk = lane % NB, team = lane / NB;
+    for (long long first = (long long)(rank * kWarps + warp) * per; first < moves; first += (long long)kAll * per) {
+        int to = 0, from = 0, gt = -1, gf = -1;  // places, their groups (-1: nothing to move)
+        if (lane < per && first + lane < moves) {
+            to = holes[first + lane];
+            from = movers[first + lane];
+            gt = cache_group(a, b, h, to / kGroup);
+            gf = cache_group(a, b, h, from / kGroup);
+            e.acc_out[row + to] = acc[from];
+            if (e.src) e.src[row + to] = from;
         }
-    };
-    auto groups_of = [&](Move& m) {
+        if (gt < 0 || gf < 0) gt = -1;
+        for (int i0 = 0; i0 < per; i0 += kAtOnce * kTeams) {
+            uint2 k[kAtOnce], v[kAtOnce];
+            uint8_t ks[kAtOnce], vs[kAtOnce];
 #pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
-            m.gt[u] = m.gf[u] = -1;
-            if (m.to[u] < 0) continue;
-            m.gt[u] = cache_group(a, b, h, m.to[u] / kGroup);
-            m.gf[u] = cache_group(a, b, h, m.from[u] / kGroup);
-        }
-    };
-    Move m, next;
-    const long long first = rank * kThreads + threadIdx.x;
-    places_of(m, first);
-    groups_of(m);
-    for (long long i0 = first; i0 < all; i0 += kAtOnce * kStride) {
-        uint2 k[kAtOnce], v[kAtOnce];
-        uint8_t ks[kAtOnce], vs[kAtOnce];
-        float sum[kAtOnce];
-#pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
-            if (blk == 0 && m.to[u] >= 0) sum[u] = acc[m.from[u]];
-            if (m.gt[u] < 0 || m.gf[u] < 0) continue;
-            const uint8_t* src = cache + (long long)m.gf[u] * L::kBytes;
-            const int tok = m.from[u] % kGroup, vr = L::v_row(tok);
-            k[u] = *reinterpret_cast<const uint2*>(src + L::k_code(tok, blk));
-            ks[u] = src[L::k_scale(tok, blk)];
-            if (D == 128) {  // a block is one chunk
-                v[u] = *reinterpret_cast<const uint2*>(src + L::v_chunk(vr, blk));
-            } else {  // or two
-                v[u].x = *reinterpret_cast<const uint32_t*>(src + L::v_chunk(vr, 2 * blk));
-                v[u].y = *reinterpret_cast<const uint32_t*>(src + L::v_chunk(vr, 2 * blk + 1));
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int i = i0 + u * kTeams + team;  // (below 32; those from per on have no groups)
+                const int at = __shfl_sync(0xffffffffu, from, i) % kGroup, group = __shfl_sync(0xffffffffu, gf, i);
+                if (__shfl_sync(0xffffffffu, gt, i) < 0) continue;
+                const uint8_t* src = cache + (long long)group * L::kBytes;
+                const int vr = L::v_row(at);
+                k[u] = *reinterpret_cast<const uint2*>(src + L::k_code(at, blk));
+                ks[u] = src[L::k_scale(at, blk)];
+                if (D == 128) {  // a block is one chunk
+                    v[u] = *reinterpret_cast<const uint2*>(src + L::v_chunk(vr, blk));
+                } else {  // or two
+                    v[u].x = *reinterpret_cast<const uint32_t*>(src + L::v_chunk(vr, 2 * blk));
+                    v[u].y = *reinterpret_cast<const uint32_t*>(src + L::v_chunk(vr, 2 * blk + 1));
+                }
+                vs[u] = src[L::v_scale(at, blk)];
             }
-            vs[u] = src[L::v_scale(tok, blk)];
-        }
-        places_of(next, i0 + kAtOnce * kStride);
-        groups_of(next);
 #pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
-            if (blk == 0 && m.to[u] >= 0) {
-                e.acc_out[row + m.to[u]] = sum[u];
-                if (e.src) e.src[row + m.to[u]] = m.from[u];
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int i = i0 + u * kTeams + team;
+                const int at = __shfl_sync(0xffffffffu, to, i) % kGroup, group = __shfl_sync(0xffffffffu, gt, i);
+                if (group < 0) continue;
+                uint8_t* dst = cache + (long long)group * L::kBytes;
+                const int vr = L::v_row(at);
+                *reinterpret_cast<uint2*>(dst + L::k_code(at, blk)) = k[u];
+                dst[L::k_scale(at, blk)] = ks[u];
+                if (D == 128) {
+                    *reinterpret_cast<uint2*>(dst + L::v_chunk(vr, blk)) = v[u];
+                } else {
+                    *reinterpret_cast<uint32_t*>(dst + L::v_chunk(vr, 2 * blk)) = v[u].x;
+                    *reinterpret_cast<uint32_t*>(dst + L::v_chunk(vr, 2 * blk + 1)) = v[u].y;
+                }
+                dst[L::v_scale(at, blk)] = vs[u];
             }
-            if (m.gt[u] < 0 || m.gf[u] < 0) continue;
-            uint8_t* dst = cache + (long long)m.gt[u] * L::kBytes;
-            const int tok = m.to[u] % kGroup, vr = L::v_row(tok);
-            *reinterpret_cast<uint2*>(dst + L::k_code(tok, blk)) = k[u];
-            dst[L::k_scale(tok, blk)] = ks[u];
-            if (D == 128) {
-                *reinterpret_cast<uint2*>(dst + L::v_chunk(vr, blk)) = v[u];
-            } else {
-                *reinterpret_cast<uint32_t*>(dst + L::v_chunk(vr, 2 * blk)) = v[u].x;
-                *reinterpret_cast<uint32_t*>(dst + L::v_chunk(vr, 2 * blk + 1)) = v[u].y;
-            }
-            dst[L::v_scale(tok, blk)] = vs[u];
         }
-        m = next;
     }
 }
 
