@@ -22,6 +22,7 @@ import ctypes
 import dataclasses
 import functools
 import os
+import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmita.so")
@@ -147,6 +148,13 @@ class RopeParams:
     @functools.cached_property
     def ref(self):
         return ctypes.byref(self._c)
+
+    @functools.cached_property
+    def _checks(self):
+        """What a call's tensors are held to: dtype and shapes of Q, K and pos."""
+        import torch
+        return (torch, torch.bfloat16 if self.dtype == BF16 else torch.float32, (self.B, self.H, self.T, self.d),
+                (self.B, self.H_kv, self.T, self.d), (self.B, self.T))
 
     def c(self):
         return self._c
@@ -394,7 +402,7 @@ def _cache_index(p: CacheParams, X, Y, heads, cache, table, lens, ws, counts, ex
     s = (p.B, heads, p.T, p.d)
     if X.dtype is not dt or X.get_device() != dev or X.shape != s or not X.is_contiguous():
         _refuse(X, s, dt, dev)
-    if Y.dtype is not dt or Y.get_device() != dev or Y.shape != s or not Y.is_contiguous():
+    if Y is not X and (Y.dtype is not dt or Y.get_device() != dev or Y.shape != s or not Y.is_contiguous()):
         _refuse(Y, s, dt, dev)
     s = (p.B, p.max_pages)
     if table.dtype is not i32 or table.get_device() != dev or table.shape != s or not table.is_contiguous():
@@ -437,7 +445,7 @@ def _on_device(t, fn, args):
     """The C call with t's device current."""
     import torch
     dev = t.get_device()
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         rc = fn(*args)
     else:
         with torch.cuda.device(dev):
@@ -567,12 +575,12 @@ def mita_rope_frequencies(rot, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, ori
 
 def _rope(p, fn, Q, K, Qo, Ko, pos, stream):
     """Written out, like _cache_index. The rows are [B, heads, T, d] with any strides but the last."""
-    import torch
-    dt, dev = torch.bfloat16 if p.dtype == BF16 else torch.float32, Q.get_device()
-    s = (p.B, p.H, p.T, p.d)
-    for t in (Q, Qo):
-        if t.dtype is not dt or t.get_device() != dev or t.shape != s:
-            _refuse_rows(t, s, dt, dev)
+    torch, dt, sq, sk, sp = p._checks
+    dev = Q.get_device()
+    if Q.dtype is not dt or Q.shape != sq:
+        _refuse_rows(Q, sq, dt, dev)
+    if Qo.dtype is not dt or Qo.shape != sq or Qo.get_device() != dev:
+        _refuse_rows(Qo, sq, dt, dev)
     q0, q1, q2, q3 = Q.stride()
     o0, o1, o2, o3 = Qo.stride()
     if K is None and Ko is None:
@@ -581,33 +589,40 @@ def _rope(p, fn, Q, K, Qo, Ko, pos, stream):
     elif K is None or Ko is None:
         raise ValueError("K and its output come together")
     else:
-        s = (p.B, p.H_kv, p.T, p.d)
-        for t in (K, Ko):
-            if t.dtype is not dt or t.get_device() != dev or t.shape != s:
-                _refuse_rows(t, s, dt, dev)
+        if K.dtype is not dt or K.shape != sk or K.get_device() != dev:
+            _refuse_rows(K, sk, dt, dev)
+        if Ko.dtype is not dt or Ko.shape != sk or Ko.get_device() != dev:
+            _refuse_rows(Ko, sk, dt, dev)
         k0, k1, k2, k3 = K.stride()
         r0, r1, r2, r3 = Ko.stride()
-        q3, o3, kp, kop = max(q3, k3), max(o3, r3), K.data_ptr(), Ko.data_ptr()
+        if k3 != 1 or r3 != 1:
+            raise ValueError("the channels of a row must be contiguous")
+        kp, kop = K.data_ptr(), Ko.data_ptr()
     if q3 != 1 or o3 != 1:
         raise ValueError("the channels of a row must be contiguous")
     if dev < 0:
         raise ValueError("the tensors must be on a CUDA device")
     pp, ps = None, 0
     if pos is not None:
-        if pos.dtype is not torch.int32 or pos.get_device() != dev or pos.shape not in ((p.T,), (p.B, p.T)):
-            _refuse_rows(pos, (p.B, p.T), torch.int32, dev)
-        if p.T > 1 and pos.stride(-1) != 1:
+        shape = pos.shape
+        if pos.dtype is not torch.int32 or pos.get_device() != dev or shape != sp and shape != sp[1:]:
+            _refuse_rows(pos, sp, torch.int32, dev)
+        st = pos.stride()
+        if st[-1] != 1 and p.T > 1:
             raise ValueError("a sequence's positions must be contiguous")
-        pp, ps = pos.data_ptr(), pos.stride(0) if pos.dim() == 2 else 0
+        pp = pos.data_ptr()
+        if len(st) == 2:
+            ps = st[0]
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(dev)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
+    # (packed: a ctypes array of twelve numbers takes a microsecond to make)
     _on_device(Q, fn, (p.ref, Q.data_ptr(), kp, Qo.data_ptr(), kop,
-                       _Strides(q0, q1, q2, k0, k1, k2, o0, o1, o2, r0, r1, r2), pp, ps, stream))
+                       _pack_strides(q0, q1, q2, k0, k1, k2, o0, o1, o2, r0, r1, r2), pp, ps, stream))
 
 
-_Strides = ctypes.c_int64 * 12
+_pack_strides = struct.Struct("12q").pack
 
 
 def _refuse_rows(t, shape, dtype, dev):
