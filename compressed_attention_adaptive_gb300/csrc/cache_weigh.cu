@@ -23,7 +23,6 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;  // of a block
 constexpr int kTok = 2 * kGroup;                       // tokens of a warp's step
 constexpr int kAhead = 2;                              // steps that a warp's loads are ahead
 constexpr int kBlocks = 2;                             // of an SM
-constexpr int kMmaRows = 16;
 
 }  // namespace
 
@@ -370,10 +369,13 @@ static cudaError_t weigh_t(const CacheArgs& a, const WeighArgs& w, unsigned flag
         return cudaGetLastError();
     }
     const long long rows = (long long)a.G * a.T;
-    if (rows > kMmaRows) return launch_cache_weigh_tile(a, w, D, sizeof(T) == 4 ? 0 : 1, Q, cache, st);
+    // Tiles on tcgen05 for more than 16 rows of 128 channels, or 32 of 64. Microseconds here and there, bf16, 8 heads of
+    // 1000 tokens, 2 x 8 of 32768, 64 x 8 of 300: d = 128, 16 rows 6.1/8.2, 20.9/26.0, 11.2/22.8; 32 rows 9.1/8.1,
+    // 34.7/26.8, 20.1/22.8; d = 64, 32 rows 6.7/8.6, 18.8/23.6, 12.0/22.7; 64 rows 10.1/9.3, 33.9/25.9, 20.3/26.4.
+    if (rows > (D == 64 ? 32 : 16)) return launch_cache_weigh_tile(a, w, D, sizeof(T) == 4 ? 0 : 1, Q, cache, st);
     if (rows <= 8) return mma_t<T, D, 1>(a, w, Q, cache, st);
-    if (rows <= 16 || sizeof(T) == 4) return mma_t<T, D, 2>(a, w, Q, cache, st);
-    return mma_t<T, D, sizeof(T) == 4 ? 2 : 4>(a, w, Q, cache, st);
+    constexpr int kMost = D == 64 && sizeof(T) == 2 ? 4 : 2;  // (32 float rows in two tiles of 16)
+    return rows <= 16 ? mma_t<T, D, 2>(a, w, Q, cache, st) : mma_t<T, D, kMost>(a, w, Q, cache, st);
 }
 
 cudaError_t launch_cache_weigh(const CacheArgs& a, int d, int dtype, unsigned flags, const void* Q, const void* cache,

@@ -272,9 +272,10 @@ typedef struct {
     int n_pages;     /* pages in the pool                                       */
     int max_pages;   /* columns of the page table                               */
     float scale;     /* softmax scale; 0 means 1/sqrt(d)                        */
-    unsigned flags;  /* mita_cache_attention: MITA_FLAG_CAUSAL, MITA_FLAG_SIMT,
-                        MITA_TESTFLAG_STALL_PRODUCER (see there; one block of
-                        the attention waits for a signal that does not come)   */
+    unsigned flags;  /* mita_cache_attention, mita_cache_weights: MITA_FLAG_CAUSAL,
+                        MITA_FLAG_SIMT, MITA_TESTFLAG_STALL_PRODUCER (see there; one
+                        block of the attention, or of the weights where they run in
+                        tiles, waits for a signal that does not come)          */
     int dtype;       /* mita_dtype of K, V, Q and O                             */
 } mita_cache_params;
 
