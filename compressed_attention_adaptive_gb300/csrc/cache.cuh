@@ -99,7 +99,7 @@ struct EvictArgs {
     const float* acc;
     float* acc_out;  // may be acc
     int *src, *len_out;
-    int* moves;     // [B * Hkv][2][half]: places that are freed, places that move there
+    int* moves;     // [B * Hkv][2 half]: places that are freed, then places that move there
     long long cap;  // places of a sequence
 };
 cudaError_t launch_cache_evict(const CacheArgs& a, const EvictArgs& e, int d, void* cache, cudaStream_t st);

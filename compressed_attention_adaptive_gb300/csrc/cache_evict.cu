@@ -4,7 +4,7 @@
 // and, of the others, the K with the largest sums. The K-th largest is found by radix: counts of the
 // sums' leading digits, then of the next digit among those that share the leading ones, and so on
 // through 32 bits (sums as ordered integers); what is equal to the K-th is
-// told apart by place, in the same way. Kept rows behind the new length then go to the freed places before
+// told apart by place, in the same way. Once few share the digits so far they are compared with each other. Kept rows behind the new length then go to the freed places before
 // it, i-th to i-th: what is read is behind the new length and what is written before it, so rows
 // move in any order and at once.
 //
@@ -29,7 +29,15 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kDigit = 11, kBins = 1 << kDigit;  // 32 bits in digits of 11, 11 and 10
 constexpr int kCoarse = kBins / 32;              // runs of 32 counts
 constexpr int kMaxKeys = 48 * 1024;              // keys that a block holds
-constexpr int kList = 512;                       // moves whose lists are in shared memory
+constexpr int kList = 1024;                      // freed places and rows that move whose list is in shared memory
+constexpr int kCompared = 256;                        // keys that are compared with each other
+// The first digit is not the leading bits, which hold a sign and exponents that weights do not come near: 32 steps for each power of
+// two from 2^-40 to 2^24, and one for all that is below or above. (If it is one of those, leading bits after all.)
+constexpr int kFirstShift = 18, kFirstLow = (int)((0x80000000u | 87u << 23) >> kFirstShift);
+
+__device__ __forceinline__ uint32_t first_digit(uint32_t key) {
+    return (uint32_t)min(max((int)(key >> kFirstShift) - kFirstLow, 0), kBins - 1);
+}
 
 // Larger sums have larger keys; NaN the largest.
 __device__ __forceinline__ uint32_t sum_key(float x) { return x != x ? 0xffffffffu : order_key(x); }
@@ -37,11 +45,12 @@ __device__ __forceinline__ uint32_t sum_key(float x) { return x != x ? 0xfffffff
 struct Select {
     alignas(16) int hist[2][kBins];
     int coarse[2][kCoarse];
-    int holes[kWarps], movers[kWarps];
-    int list[2][kList];
-    int2 all;  // the block's freed places and rows that move
+    int events[kWarps], all;  // freed places and rows that move: of a warp's run, of the block's
+    int list[kList];
+    unsigned long long few[kCompared], all_few[kCompared];  // ranks of the block's, and of all
+    int found;
     unsigned long long bound;
-    int left, bin;
+    int digit, left, bin;
 };
 
 template <int C> __device__ __forceinline__ void cluster_sync() {
@@ -109,6 +118,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_cache_evict(CacheArgs a, EvictA
     const int m0 = e.first, m1 = n - e.recent, K = keep - e.first - e.recent;
     const bool held = run <= room;
     for (int i = threadIdx.x; i < kBins; i += kThreads) s.hist[0][i] = 0;
+    if (threadIdx.x == 0) s.found = 0;
     __syncthreads();
     const int places = p1 - p0;
     const bool wide = ((uintptr_t)(acc + p0) & 15) == 0;
@@ -135,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_cache_evict(CacheArgs a, EvictA
             const uint32_t four[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (p0 + x + i >= m0 && p0 + x + i < min(m1, p1)) count.add(four[i] >> (32 - kDigit));
+                if (p0 + x + i >= m0 && p0 + x + i < min(m1, p1)) count.add(first_digit(four[i]));
         }
         count.end();
     }
@@ -143,26 +153,62 @@ __global__ void __launch_bounds__(kThreads, 2) k_cache_evict(CacheArgs a, EvictA
     auto rank_of = [](int j, uint32_t key) { return (unsigned long long)key << 32 | ~(uint32_t)j; };
 
     unsigned long long bound = 0;
-    for (int left = K, bin = m1 - m0, shift = 64, at = 0; K > 0 && left < bin && shift > 0; at ^= 1) {
-        const int top = shift;  // bits known
-        shift = shift == 42 || shift == 10 ? shift - 10 : shift - 11;
-        if (top < 64) {
-            Counter count(s.hist[at]);
-            const uint32_t high = (uint32_t)(bound >> 32), low = (uint32_t)bound, mask = (1u << (top - shift)) - 1;
-            for (int x = 4 * threadIdx.x; x < places; x += 4 * kThreads) {
-                const uint4 k = keys4(x);
-                const uint32_t four[4] = {k.x, k.y, k.z, k.w};
+    int left = K, bin = m1 - m0, top = 64;  // of the `bin` places with the bits of bound from `top` on, `left` stay
+    // Calls f(place, key) for those of the block's.
+    auto sharing = [&](auto f) {
+        const uint32_t high = (uint32_t)(bound >> 32), low = (uint32_t)bound;
+        for (int x = 4 * threadIdx.x; x < places; x += 4 * kThreads) {
+            const uint4 k = keys4(x);
+            const uint32_t four[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int j = p0 + x + i;
-                    if (j < m0 || j >= min(m1, p1)) continue;
-                    if (top > 32) {  // digits of the sum
-                        if ((four[i] ^ high) >> (top - 32) == 0) count.add(four[i] >> (shift - 32) & mask);
-                    } else if (four[i] == high && (top == 32 || (~(uint32_t)j ^ low) >> top == 0)) {
-                        count.add(~(uint32_t)j >> shift & mask);
-                    }
-                }
+            for (int i = 0; i < 4; ++i) {
+                const int j = p0 + x + i;
+                if (j < m0 || j >= min(m1, p1)) continue;
+                const bool in = top > 32 ? top == 64 || (four[i] ^ high) >> (top - 32) == 0
+                                         : four[i] == high && (top == 32 || (~(uint32_t)j ^ low) >> top == 0);
+                if (in) f(j, four[i]);
             }
+        }
+    };
+    bool first = true;
+    for (int at = 0; K > 0 && left < bin && top > 0; at ^= 1) {
+        if (bin <= kCompared) {
+            sharing([&](int j, uint32_t key) {
+                const int i = atomicAdd(&s.found, 1);
+                if (i < kCompared) s.few[i] = rank_of(j, key);
+            });
+            cluster_sync<C>();
+            int total = 0, from = 0, i = threadIdx.x;
+            int of[C];
+#pragma unroll
+            for (int r = 0; r < C; ++r) of[r] = min(*of_rank<C>(&s.found, r), kCompared);
+#pragma unroll
+            for (int r = 0; r < C; ++r) {
+                if (total <= (int)threadIdx.x) {
+                    from = r;
+                    i = (int)threadIdx.x - total;
+                }
+                total += of[r];
+            }
+            total = min(total, kCompared);
+            if ((int)threadIdx.x < total) s.all_few[threadIdx.x] = of_rank<C>(&s.few[0], from)[i];
+            __syncthreads();
+            if ((int)threadIdx.x < total) {
+                const unsigned long long mine = s.all_few[threadIdx.x];
+                int above = 0;
+#pragma unroll 4
+                for (int i = 0; i < total; ++i) above += s.all_few[i] > mine;
+                if (above == left - 1) s.bound = mine;
+            }
+            __syncthreads();
+            bound = s.bound;
+            break;
+        }
+        const int next = first ? 32 + kFirstShift : max(top - kDigit, top > 32 ? 32 : 0);
+        if (!first) {
+            Counter count(s.hist[at]);
+            const uint32_t mask = (1u << (top - next)) - 1;
+            sharing([&](int j, uint32_t key) { count.add((uint32_t)(rank_of(j, key) >> next) & mask); });
             count.end();
         }
         __syncthreads();
@@ -196,89 +242,83 @@ __global__ void __launch_bounds__(kThreads, 2) k_cache_evict(CacheArgs a, EvictA
             l = reach(fine, left - before, lane, &then);
             fine = __shfl_sync(0xffffffffu, fine, l);
             if (lane == 0) {
-                s.bound = bound | (unsigned long long)(32 * run32 + 31 - l) << shift;
+                s.digit = 32 * run32 + 31 - l;
                 s.left = left - before - then;
                 s.bin = fine;
             }
         }
         __syncthreads();
-        bound = s.bound;
-        left = s.left;
-        bin = s.bin;
+        const int digit = s.digit;
+        if (!first || (digit > 0 && digit < kBins - 1)) {
+            bound |= (unsigned long long)(first ? digit + kFirstLow : digit) << next;
+            left = s.left;
+            bin = s.bin;
+            top = next;
+        }
+        first = false;
     }
     if (held) __syncthreads();  // (K = 0: the keys)
-    auto stays = [&](int j, uint32_t key) { return j < m0 || j >= m1 || (K > 0 && rank_of(j, key) >= bound); };
+    const uint32_t bound_key = (uint32_t)(bound >> 32), bound_at = ~(uint32_t)bound;  // the last place with that sum that stays
+    auto stays = [&](int j, uint32_t key) {
+        return j < m0 || j >= m1 || (K > 0 && (key > bound_key || (key == bound_key && (uint32_t)j <= bound_at)));
+    };
 
-    // Freed places before `keep` and kept rows from there on, numbered in order: a warp takes a run of
+    // Freed places before `keep` and kept rows from there on, numbered in order: there are as many of the one as of the
+    // other, so the first half of a list of both has the places and the second the rows. A warp takes a run of
     // places, counts, and writes them behind what the warps and blocks before it have.
     const int wrun = ((places + kWarps - 1) / kWarps + 127) & ~127, x0 = warp * wrun, x1 = min(places, x0 + wrun);
     const long long half = (e.cap + 1) / 2;
-    int* holes = e.moves + 2 * half * rowi;  // (few moves of one block: in shared memory)
-    int* movers = holes + half;
-    int cap_list = (int)min(half, (long long)INT_MAX);
-    int nh = 0, nm = 0, ah = 0, am = 0;  // those before the warp's, and all
-    for (int pass = 0; pass < 2; ++pass) {
-        int ch = nh, cm = nm;  // (pass 1) those before
-        for (int x = x0; x < x1; x += 128) {  // four places a lane
-            const int j = p0 + x + 4 * lane;
-            const uint4 k = x + 4 * lane < places ? keys4(x + 4 * lane) : make_uint4(0, 0, 0, 0);
-            const uint32_t four[4] = {k.x, k.y, k.z, k.w}, below = (1u << lane) - 1;
-            bool hole[4], mover[4];
-            int ih = ch, im = cm;
+    int* list = e.moves + 2 * half * rowi;  // (few moves of one block: in shared memory)
+    int cap_list = (int)min(2 * half, (long long)INT_MAX);
+    // Which of the four places from p0 + x + 4 lane on are such.
+    auto events = [&](int x) {
+        const int at = x + 4 * lane, j = p0 + at;
+        uint32_t bits = 0;
+        if (at < places) {
+            const uint4 k = keys4(at);
+            const uint32_t four[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bool in = j + i < p1, stay = stays(j + i, four[i]);
-                hole[i] = in && j + i < keep && !stay;
-                mover[i] = in && j + i >= keep && stay;
-                const uint32_t hb = __ballot_sync(0xffffffffu, hole[i]), mb = __ballot_sync(0xffffffffu, mover[i]);
-                ih += __popc(hb & below);
-                im += __popc(mb & below);
-                ch += __popc(hb);
-                cm += __popc(mb);
-            }
-            if (!pass) continue;
+            for (int i = 0; i < 4; ++i)
+                if (stays(j + i, four[i]) == (j + i >= keep) && j + i < p1) bits |= 1u << i;
+        }
+        return bits;
+    };
+    int mine = 0;
+    for (int x = x0; x < x1; x += 128) mine += __popc(events(x));
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if (lane == 0) s.events[warp] = mine;
+    __syncthreads();
+    int before = 0, all = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (hole[i] && ih < cap_list) holes[ih] = j + i;
-                if (mover[i] && im < cap_list) movers[im] = j + i;
-                ih += hole[i];
-                im += mover[i];
-            }
-        }
-        if (pass) break;
-        if (lane == 0) {
-            s.holes[warp] = ch;
-            s.movers[warp] = cm;
-        }
-        __syncthreads();
-        nh = nm = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            if (w == warp) {
-                ch = nh;
-                cm = nm;
-            }
-            nh += s.holes[w];
-            nm += s.movers[w];
-        }
-        if (threadIdx.x == 0) s.all = make_int2(nh, nm);
-        if (C == 1 && min(nh, nm) <= kList) {
-            holes = s.list[0];
-            movers = s.list[1];
-            cap_list = kList;
-        }
-        nh = ch;
-        nm = cm;
-        cluster_sync<C>();
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += s.events[w];
+        all += s.events[w];
+    }
+    if (threadIdx.x == 0) s.all = all;
+    if (C == 1 && all <= kList) {
+        list = s.list;
+        cap_list = kList;
+    }
+    cluster_sync<C>();
+    all = 0;
 #pragma unroll
-        for (int r = 0; r < C; ++r) {
-            const int2 x = *of_rank<C>(&s.all, r);
-            ah += x.x;
-            am += x.y;
-            if (r < rank) {
-                nh += x.x;
-                nm += x.y;
+    for (int r = 0; r < C; ++r) {
+        const int x = *of_rank<C>(&s.all, r);
+        all += x;
+        if (r < rank) before += x;
+    }
+    for (int x = x0; x < x1; x += 128) {
+        const uint32_t bits = events(x), below = (1u << lane) - 1, count = __popc(bits);
+        const uint32_t b0 = __ballot_sync(0xffffffffu, count & 1), b1 = __ballot_sync(0xffffffffu, count & 2),
+                       b2 = __ballot_sync(0xffffffffu, count & 4);
+        int at = before + __popc(b0 & below) + 2 * __popc(b1 & below) + 4 * __popc(b2 & below);
+        before += __popc(b0) + 2 * __popc(b1) + 4 * __popc(b2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (bits >> i & 1) {
+                if (at < cap_list) list[at] = p0 + x + 4 * lane + i;
+                ++at;
             }
-        }
     }
     // Rows that stay where they are, by the whole cluster: those places are its first blocks'.
     if (e.src || e.acc_out != e.acc) {
@@ -290,25 +330,27 @@ __global__ void __launch_bounds__(kThreads, 2) k_cache_evict(CacheArgs a, EvictA
             if (e.src) e.src[row + j] = j;
         }
     }
-    // (as many of the one as of the other, and at most half of the places each; sums that change
-    // under the call leave the results undefined, but no list is left)
-    const int moves = min(min(ah, am), cap_list);
+    // (sums that change under the call leave the results undefined, but no list is left)
+    const int moves = min(all, cap_list) / 2;
     cluster_sync<C>();  // the lists are there, acc has been read, and no block reads another's memory any more
 
     // A warp takes up to 32 moves: a lane looks up one of them, then NB lanes share each, with 16 channels of
     // keys and values as they are held. Few moves are spread over all warps.
     constexpr int NB = L::kBlocks, kTeams = 32 / NB, kAtOnce = 4, kAll = C * kWarps;
-    const int per = min(32, ((moves + kAll - 1) / kAll + kTeams - 1) / kTeams * kTeams);
+    const int turns = max(1, (moves + 32 * kAll - 1) / (32 * kAll));
+    const int per = ((moves + turns * kAll - 1) / (turns * kAll) + kTeams - 1) / kTeams * kTeams;  // of a warp's turn, at most 32
     const int blk = lane % NB, team = lane / NB;
-    for (long long first = (long long)(rank * kWarps + warp) * per; first < moves; first += (long long)kAll * per) {
+    for (long long i1 = (long long)(rank * kWarps + warp) * per; i1 < moves; i1 += (long long)kAll * per) {
         int to = 0, from = 0, gt = -1, gf = -1;  // places, their groups (-1: nothing to move)
-        if (lane < per && first + lane < moves) {
-            to = holes[first + lane];
-            from = movers[first + lane];
-            gt = cache_group(a, b, h, to / kGroup);
-            gf = cache_group(a, b, h, from / kGroup);
-            e.acc_out[row + to] = acc[from];
-            if (e.src) e.src[row + to] = from;
+        if (lane < per && i1 + lane < moves) {
+            to = list[i1 + lane];
+            from = list[moves + i1 + lane];
+            if ((unsigned)to < (unsigned)n && (unsigned)from < (unsigned)n) {  // (else sums changed under the call)
+                gt = cache_group(a, b, h, to / kGroup);
+                gf = cache_group(a, b, h, from / kGroup);
+                e.acc_out[row + to] = acc[from];
+                if (e.src) e.src[row + to] = from;
+            }
         }
         if (gt < 0 || gf < 0) gt = -1;
         for (int i0 = 0; i0 < per; i0 += kAtOnce * kTeams) {
