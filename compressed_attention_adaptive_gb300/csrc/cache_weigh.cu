@@ -111,9 +111,10 @@ k_cache_weigh_simt(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint
 
 // --------------------------------------------------------- tensor cores
 
-// Q's halves of a warp in shared memory: float rows are two of them; eight bf16 rows are in registers
-template <typename T, int D, int NR> constexpr int q_bytes() {
-    return NR == 1 && sizeof(T) == 2 ? 0 : (sizeof(T) == 4 ? 2 : 1) * NR * (D / 16) * 256;
+// Q's halves of a warp in shared memory (float rows are two of them), or in registers where they are few
+template <typename T, int D, int NR, bool FEW> constexpr bool q_regs() { return FEW || (NR == 1 && sizeof(T) == 2); }
+template <typename T, int D, int NR, bool FEW> constexpr int q_bytes() {
+    return q_regs<T, D, NR, FEW>() ? 0 : (sizeof(T) == 4 ? 2 : 1) * NR * (D / 16) * 256;
 }
 
 // Scores on m16n8k16 steps (halves in, fp32 out), tokens on the 16 side and 8 NR query rows on the 8 side.
@@ -124,13 +125,19 @@ template <typename T, int D, int NR> constexpr int q_bytes() {
 // (cache.cuh). Rows are scaled by a power of two that puts the largest entry in [2^14, 2^15): bf16 rows are exact
 // as halves down to 2^-31 of it; float32 rows are two halves, hi + lo, both in one sum.
 // A lane ends with two tokens of each group and two rows for each eight; four lanes share a token.
-template <typename T, int D, int NR>
+//
+// FEW: with two rows, of the eight columns of the 8 side a row has four, each with the channels of every fourth block of
+// its own and zeros elsewhere. The sums of the blocks of 16 channels come out apart, so that scales are multiplied into them
+// (4 d/64 products for two tokens) and not into the codes (32 d/128 for them), and of what the step ends with
+// no column is empty: a lane has one score and one exponential for each group.
+template <typename T, int D, int NR, bool FEW>
 __global__ void __launch_bounds__(kThreads, kBlocks)
 k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* __restrict__ cache) {
     using L = Grp<D>;
     constexpr bool F = sizeof(T) == 4;  // float rows
-    constexpr bool kQRegs = NR == 1 && !F;
-    constexpr int KS = D / 16, W = D / 32, RT = 8 * NR, KW = D / 64;  // KW: 8-byte words of a lane's codes of a token
+    constexpr bool kQRegs = q_regs<T, D, NR, FEW>();
+    constexpr int KS = D / 16, W = D / 32, RT = (FEW ? 2 : 8) * NR, KW = D / 64;  // KW: 8-byte words of a lane's codes of a token
+    constexpr int SW = FEW && D == 128 ? 2 : 1;                                   // words of a lane's scales of a group
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ LineStart<kThreads> start;
     if (blockIdx.x == 0) {
@@ -138,7 +145,7 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
         return;
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
-    uint2* qs = reinterpret_cast<uint2*>(smem + warp * q_bytes<T, D, NR>());
+    uint2* qs = reinterpret_cast<uint2*>(smem + warp * q_bytes<T, D, NR, FEW>());
     Place<kTok, kThreads> at;
     at.begin(a, start, (long long)(blockIdx.x - 1) * kWarps + warp, (long long)(gridDim.x - 1) * kWarps);
     if (at.left == 0) return;
@@ -148,7 +155,7 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
         // the lane's token of step 0
         const long long sums = ((long long)at.b * a.Hkv + at.h) * w.cap + (long long)step0 * kTok + 8 * t4 + g;
         const uint8_t* codes = cache + g * L::kRow + t4 * (D / 8);
-        const uint8_t* scales = cache + L::kKs + g * (D / 8) + t4 * (D / 32);
+        const uint8_t* scales = cache + L::kKs + g * (D / 8) + (FEW ? (t4 & 1) * (D / 16) : t4 * (D / 32));
         // lane l: group l % 2 of step i + l / 2
         auto groups = [&](int i) {
             const int gi = 2 * (step0 + i) + lane;
@@ -163,7 +170,7 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
             const int olds = (row0 ? n : w.decay != 0.0f ? n - at.count : 0) - (step0 * kTok + 8 * t4 + g);
             int gcur = groups(0), gnxt = groups(16);
             uint2 kc[kAhead][2][2][KW];  // [step][group][token g, g + 8]
-            uint32_t sc[kAhead][2], ok = 0;
+            uint32_t sc[kAhead][2][SW], ok = 0;
             float base[kAhead];
             auto load = [&](int u, int i) {  // called for every i in turn
                 ok &= ~(3u << 2 * u);
@@ -184,8 +191,14 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
                             kc[u][y][x][0] = *reinterpret_cast<const uint2*>(r);
                         }
                     }
-                    sc[u][y] = D == 128 ? *reinterpret_cast<const uint32_t*>(scales + at_group)
-                                        : *reinterpret_cast<const uint16_t*>(scales + at_group);
+                    if (SW == 2) {
+                        const uint2 v = *reinterpret_cast<const uint2*>(scales + at_group);
+                        sc[u][y][0] = v.x;
+                        sc[u][y][SW - 1] = v.y;
+                    } else {
+                        sc[u][y][0] = D == 128 || FEW ? *reinterpret_cast<const uint32_t*>(scales + at_group)
+                                                      : *reinterpret_cast<const uint16_t*>(scales + at_group);
+                    }
                 }
                 base[u] = i < cnt && i * kTok < olds ? had[(long long)i * kTok] : 0.0f;
                 if ((i & 15) == 15) {
@@ -197,15 +210,18 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
             for (int u = 0; u < kAhead; ++u) load(u, u);
 
             // Q: lane (g, t4) has channels [t4 d/4, (t4 + 1) d/4) of rows g, and what it needs of
-            // rows 2 t4 and the next: factor of the scores, lse, keys that they see
-            uint2 qf[kQRegs ? KS : 1];
+            // rows 2 t4 and the next: factor of the scores, lse, keys that they see. (FEW: of row g / 4, if t4 is g % 4,
+            // and what it needs of row t4 / 2.)
+            constexpr int kParts = F ? 2 : 1;
+            uint2 qf[kQRegs ? kParts * KS * NR : 1];
             float2 zf[NR], lse[NR];  // (lse negated)
             int2 lim[NR];
             int low = 0, top = 0;
             __syncwarp();  // all have read the tile before
 #pragma unroll
             for (int j = 0; j < NR; ++j) {
-                const int r = row0 + 8 * j + g;
+                const int r = row0 + (FEW ? 2 * j + (g >> 2) : 8 * j + g);
+                const bool mine = r < rows && (!FEW || t4 == (g & 3));
                 int t = 0;
                 const long long row = row_offset(a, at.b, at.h, min(r, max(rows - 1, 0)), &t);
                 constexpr int QW = D / 16 * sizeof(T) / 4;  // 16-byte words of a lane's channels
@@ -213,7 +229,7 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
 #pragma unroll
                 for (int i = 0; i < QW; ++i) {
                     uint4 v = make_uint4(0, 0, 0, 0);
-                    if (r < rows) v = reinterpret_cast<const uint4*>(Q + row * D + t4 * (D / 4))[i];
+                    if (mine) v = reinterpret_cast<const uint4*>(Q + row * D + t4 * (D / 4))[i];
                     x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
                 }
                 // (a row that is not there: weights of 0)
@@ -224,6 +240,10 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
                     amax = max(amax, F ? x[i] & 0x7fffffffu : max(x[i] << 16 & 0x7fff0000u, x[i] & 0x7fff0000u));
                 amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                 amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                if (FEW) {
+                    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 4));
+                    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 8));
+                }
                 float up;
                 const int qe = query_exp(amax >> 23, &up);
                 const float f = fminf(a.scale * pow2(cache_exp(a, 0, at.h)) * pow2(-qe), 3.4028235e38f);
@@ -238,13 +258,18 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
                         const float2 h = half2_to_float2(hi[e]);
                         lo[e] = pack_half2(y0 - h.x, y1 - h.y);
                     }
-                    if (kQRegs)
-                        qf[ks % (kQRegs ? KS : 1)] = make_uint2(hi[0], hi[1]);
-                    else
-                        qs[(ks * NR + j) * 32 + lane] = make_uint2(hi[0], hi[1]);
-                    if (F) qs[((KS + ks) * NR + j) * 32 + lane] = make_uint2(lo[0], lo[1]);
+                    if (FEW && t4 != (g & 3)) hi[0] = hi[1] = lo[0] = lo[1] = 0;  // (0 times a NaN would not be)
+#pragma unroll
+                    for (int part = 0; part < kParts; ++part) {
+                        const uint2 q = part ? make_uint2(lo[0], lo[1]) : make_uint2(hi[0], hi[1]);
+                        if (kQRegs)
+                            qf[((part * KS + ks) * NR + j) % (kQRegs ? kParts * KS * NR : 1)] = q;
+                        else
+                            qs[((part * KS + ks) * NR + j) * 32 + lane] = q;
+                    }
                 }
-                const int r0 = 8 * t4, r1 = r0 + 4;  // lanes with rows 2 t4 and the next
+                // lanes with rows 2 t4 and the next (FEW: with row t4 / 2)
+                const int r0 = FEW ? 8 * (t4 & 2) : 8 * t4, r1 = FEW ? r0 : r0 + 4;
                 zf[j] = make_float2(__shfl_sync(0xffffffffu, f, r0), __shfl_sync(0xffffffffu, f, r1));
                 lse[j] = make_float2(-__shfl_sync(0xffffffffu, l, r0), -__shfl_sync(0xffffffffu, l, r1));
                 lim[j] = make_int2(__shfl_sync(0xffffffffu, m, r0), __shfl_sync(0xffffffffu, m, r1));
@@ -262,72 +287,140 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
                     float sum = 0.0f;
                     if (i < cnt && tok < top) {
                         const bool edge = tok + kTok > low;  // some row does not see all of these tokens
-                        float2 s2t[2][2];                    // [group][token g, g + 8], two rows each
+                        auto rows_of = [&](int part, int ks, int j) {
+                            const int at = (part * KS + ks) * NR + j;
+                            return kQRegs ? qf[at % (kQRegs ? kParts * KS * NR : 1)] : qs[at * 32 + lane];
+                        };
+                        const bool odd = t4 & 1, up = t4 & 2;
+                        if constexpr (FEW) {
+                            float w2[2];  // [group]: of the lane's token and rows
 #pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            uint32_t s2[2][KW];  // [token g, g + 8]: scales, each in both halves
-                            if (D == 128) {
-                                const uint32_t a0 = e4m3x2_to_half2(sc[u][y] & 0xffff), a1 = e4m3x2_to_half2(sc[u][y] >> 16);
-                                s2[0][0] = __byte_perm(a0, a0, 0x1010);
-                                s2[0][KW - 1] = __byte_perm(a0, a0, 0x3232);
-                                s2[1][0] = __byte_perm(a1, a1, 0x1010);
-                                s2[1][KW - 1] = __byte_perm(a1, a1, 0x3232);
-                            } else {
-                                const uint32_t a0 = e4m3x2_to_half2(sc[u][y]);
-                                s2[0][0] = __byte_perm(a0, a0, 0x1010);
-                                s2[1][0] = __byte_perm(a0, a0, 0x3232);
-                            }
-                            float z[NR][4];
+                            for (int y = 0; y < 2; ++y) {
+                                constexpr int HF = D / 64;  // blocks of a lane's channels
+                                float z[NR][HF][4];
 #pragma unroll
-                            for (int wi = 0; wi < W; ++wi) {
-                                uint32_t k8[2][4];
+                                for (int wi = 0; wi < W; ++wi) {
+                                    uint32_t k8[2][4];
 #pragma unroll
-                                for (int x = 0; x < 2; ++x) {
-                                    e2m1x8_to_half2(wi & 1 ? kc[u][y][x][wi / 2].y : kc[u][y][x][wi / 2].x, k8[x]);
+                                    for (int x = 0; x < 2; ++x)
+                                        e2m1x8_to_half2(wi & 1 ? kc[u][y][x][wi / 2].y : kc[u][y][x][wi / 2].x, k8[x]);
 #pragma unroll
-                                    for (int j = 0; j < 4; ++j) k8[x][j] = hmul2(k8[x][j], s2[x][wi / 2]);
+                                    for (int k2 = 0; k2 < 2; ++k2)
+#pragma unroll
+                                        for (int part = 0; part < kParts; ++part)
+#pragma unroll
+                                            for (int j = 0; j < NR; ++j) {
+                                                const int ks = 2 * wi + k2;
+                                                const uint2 q = rows_of(part, ks, j);
+                                                float* to = z[j][ks / 4];
+                                                if (ks % 4 == 0 && part == 0)
+                                                    mma_f16_first(to, k8[0][2 * k2], k8[1][2 * k2], k8[0][2 * k2 + 1],
+                                                                  k8[1][2 * k2 + 1], q.x, q.y);
+                                                else
+                                                    mma_f16(to, k8[0][2 * k2], k8[1][2 * k2], k8[0][2 * k2 + 1], k8[1][2 * k2 + 1],
+                                                            q.x, q.y);
+                                            }
                                 }
+                                float s[2][2][HF];  // [token g, g + 8][column][block]
 #pragma unroll
-                                for (int k2 = 0; k2 < 2; ++k2)
-#pragma unroll
-                                    for (int j = 0; j < NR; ++j) {
-                                        const int ks = 2 * wi + k2;
-                                        const uint2 q = kQRegs ? qf[ks % (kQRegs ? KS : 1)] : qs[(ks * NR + j) * 32 + lane];
-                                        if (ks == 0)
-                                            mma_f16_first(z[j], k8[0][0], k8[1][0], k8[0][1], k8[1][1], q.x, q.y);
-                                        else
-                                            mma_f16(z[j], k8[0][2 * k2], k8[1][2 * k2], k8[0][2 * k2 + 1], k8[1][2 * k2 + 1],
-                                                    q.x, q.y);
-                                        if (F) {
-                                            const uint2 ql = qs[((KS + ks) * NR + j) * 32 + lane];
-                                            mma_f16(z[j], k8[0][2 * k2], k8[1][2 * k2], k8[0][2 * k2 + 1], k8[1][2 * k2 + 1],
-                                                    ql.x, ql.y);
-                                        }
+                                for (int c = 0; c < 2; ++c) {
+                                    if (D == 128) {
+                                        const uint32_t two = sc[u][y][c % SW];
+                                        const float2 a0 = half2_to_float2(e4m3x2_to_half2(two & 0xffff));
+                                        const float2 a1 = half2_to_float2(e4m3x2_to_half2(two >> 16));
+                                        s[0][c][0] = a0.x; s[0][c][HF - 1] = a0.y;
+                                        s[1][c][0] = a1.x; s[1][c][HF - 1] = a1.y;
+                                    } else {
+                                        const uint32_t two = sc[u][y][0] >> 16 * c & 0xffff;
+                                        const float2 a0 = half2_to_float2(e4m3x2_to_half2(two));
+                                        s[0][c][0] = a0.x;
+                                        s[1][c][0] = a0.y;
                                     }
-                            }
-                            s2t[y][0] = s2t[y][1] = make_float2(0.0f, 0.0f);
-#pragma unroll
-                            for (int j = 0; j < NR; ++j) {
-                                float2 p0 = weight2(make_float2(z[j][0], z[j][1]), zf[j], lse[j]);
-                                float2 p1 = weight2(make_float2(z[j][2], z[j][3]), zf[j], lse[j]);
-                                if (edge) {
-                                    const int t0 = tok + kGroup * y + g;
-                                    if (t0 >= lim[j].x) p0.x = 0.0f;
-                                    if (t0 >= lim[j].y) p0.y = 0.0f;
-                                    if (t0 + 8 >= lim[j].x) p1.x = 0.0f;
-                                    if (t0 + 8 >= lim[j].y) p1.y = 0.0f;
                                 }
-                                s2t[y][0] = j ? add2(s2t[y][0], p0) : p0;
-                                s2t[y][1] = j ? add2(s2t[y][1], p1) : p1;
+#pragma unroll
+                                for (int j = 0; j < NR; ++j) {
+                                    float v[2];
+#pragma unroll
+                                    for (int x = 0; x < 2; ++x) {
+                                        v[x] = z[j][0][2 * x] * s[x][0][0];
+#pragma unroll
+                                        for (int i = 1; i < 2 * HF; ++i)
+                                            v[x] = fmaf(z[j][i / 2][2 * x + (i & 1)], s[x][i & 1][i / 2], v[x]);
+                                    }
+                                    const float mine = (odd ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, odd ? v[0] : v[1], 1);
+                                    float p = weight(mine, zf[j].x, -lse[j].x);
+                                    if (edge && tok + kGroup * y + 8 * (t4 & 1) + g >= lim[j].x) p = 0.0f;
+                                    w2[y] = j ? w2[y] + p : p;
+                                }
                             }
+                            sum = (up ? w2[1] : w2[0]) + __shfl_xor_sync(0xffffffffu, up ? w2[0] : w2[1], 2);
+                        } else {
+                            float2 s2t[2][2];  // [group][token g, g + 8], two rows each
+    #pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                uint32_t s2[2][KW];  // [token g, g + 8]: scales, each in both halves
+                                if (D == 128) {
+                                    const uint32_t a0 = e4m3x2_to_half2(sc[u][y][0] & 0xffff), a1 = e4m3x2_to_half2(sc[u][y][0] >> 16);
+                                    s2[0][0] = __byte_perm(a0, a0, 0x1010);
+                                    s2[0][KW - 1] = __byte_perm(a0, a0, 0x3232);
+                                    s2[1][0] = __byte_perm(a1, a1, 0x1010);
+                                    s2[1][KW - 1] = __byte_perm(a1, a1, 0x3232);
+                                } else {
+                                    const uint32_t a0 = e4m3x2_to_half2(sc[u][y][0]);
+                                    s2[0][0] = __byte_perm(a0, a0, 0x1010);
+                                    s2[1][0] = __byte_perm(a0, a0, 0x3232);
+                                }
+                                float z[NR][4];
+    #pragma unroll
+                                for (int wi = 0; wi < W; ++wi) {
+                                    uint32_t k8[2][4];
+    #pragma unroll
+                                    for (int x = 0; x < 2; ++x) {
+                                        e2m1x8_to_half2(wi & 1 ? kc[u][y][x][wi / 2].y : kc[u][y][x][wi / 2].x, k8[x]);
+    #pragma unroll
+                                        for (int j = 0; j < 4; ++j) k8[x][j] = hmul2(k8[x][j], s2[x][wi / 2]);
+                                    }
+    #pragma unroll
+                                    for (int k2 = 0; k2 < 2; ++k2)
+    #pragma unroll
+                                        for (int j = 0; j < NR; ++j) {
+                                            const int ks = 2 * wi + k2;
+                                            const uint2 q = rows_of(0, ks, j);
+                                            if (ks == 0)
+                                                mma_f16_first(z[j], k8[0][0], k8[1][0], k8[0][1], k8[1][1], q.x, q.y);
+                                            else
+                                                mma_f16(z[j], k8[0][2 * k2], k8[1][2 * k2], k8[0][2 * k2 + 1], k8[1][2 * k2 + 1],
+                                                        q.x, q.y);
+                                            if (F) {
+                                                const uint2 ql = rows_of(1, ks, j);
+                                                mma_f16(z[j], k8[0][2 * k2], k8[1][2 * k2], k8[0][2 * k2 + 1], k8[1][2 * k2 + 1],
+                                                        ql.x, ql.y);
+                                            }
+                                        }
+                                }
+                                s2t[y][0] = s2t[y][1] = make_float2(0.0f, 0.0f);
+    #pragma unroll
+                                for (int j = 0; j < NR; ++j) {
+                                    float2 p0 = weight2(make_float2(z[j][0], z[j][1]), zf[j], lse[j]);
+                                    float2 p1 = weight2(make_float2(z[j][2], z[j][3]), zf[j], lse[j]);
+                                    if (edge) {
+                                        const int t0 = tok + kGroup * y + g;
+                                        if (t0 >= lim[j].x) p0.x = 0.0f;
+                                        if (t0 >= lim[j].y) p0.y = 0.0f;
+                                        if (t0 + 8 >= lim[j].x) p1.x = 0.0f;
+                                        if (t0 + 8 >= lim[j].y) p1.y = 0.0f;
+                                    }
+                                    s2t[y][0] = j ? add2(s2t[y][0], p0) : p0;
+                                    s2t[y][1] = j ? add2(s2t[y][1], p1) : p1;
+                                }
+                            }
+                            // over the four lanes of a token: lane t4 ends with token 8 t4 + g of the step
+                            float2 k0 = up ? s2t[1][0] : s2t[0][0], k1 = up ? s2t[1][1] : s2t[0][1];
+                            const float2 g0 = up ? s2t[0][0] : s2t[1][0], g1 = up ? s2t[0][1] : s2t[1][1];
+                            float x0 = k0.x + k0.y + __shfl_xor_sync(0xffffffffu, g0.x + g0.y, 2);
+                            float x1 = k1.x + k1.y + __shfl_xor_sync(0xffffffffu, g1.x + g1.y, 2);
+                            sum = (odd ? x1 : x0) + __shfl_xor_sync(0xffffffffu, odd ? x0 : x1, 1);
                         }
-                        // over the four lanes of a token: lane t4 ends with token 8 t4 + g of the step
-                        const bool up = t4 & 2, odd = t4 & 1;
-                        float2 k0 = up ? s2t[1][0] : s2t[0][0], k1 = up ? s2t[1][1] : s2t[0][1];
-                        const float2 g0 = up ? s2t[0][0] : s2t[1][0], g1 = up ? s2t[0][1] : s2t[1][1];
-                        float x0 = k0.x + k0.y + __shfl_xor_sync(0xffffffffu, g0.x + g0.y, 2);
-                        float x1 = k1.x + k1.y + __shfl_xor_sync(0xffffffffu, g1.x + g1.y, 2);
-                        sum = (odd ? x1 : x0) + __shfl_xor_sync(0xffffffffu, odd ? x0 : x1, 1);
                     }
                     if (i < cnt && tok + 8 * t4 + g < n && (ok >> (2 * u + (t4 >> 1)) & 1))
                         w.acc_out[sums + (long long)i * kTok] = fmaf(decay, base[u], sum);
@@ -347,15 +440,15 @@ static unsigned weigh_grid(const CacheArgs& a, const WeighArgs& w, int blocks) {
     return (unsigned)std::min<long long>((steps + kWarps - 1) / kWarps + 1, (long long)blocks * num_sms());
 }
 
-template <typename T, int D, int NR>
+template <typename T, int D, int NR, bool FEW = false>
 static cudaError_t mma_t(const CacheArgs& a, const WeighArgs& w, const void* Q, const uint8_t* cache, cudaStream_t st) {
-    constexpr int smem = kWarps * q_bytes<T, D, NR>();
+    constexpr int smem = kWarps * q_bytes<T, D, NR, FEW>();
     static std::atomic<unsigned long long> done{0};
     if (smem > 40 * 1024) {
-        const cudaError_t e = set_smem_once((const void*)k_cache_weigh<T, D, NR>, smem, &done);
+        const cudaError_t e = set_smem_once((const void*)k_cache_weigh<T, D, NR, FEW>, smem, &done);
         if (e != cudaSuccess) return e;
     }
-    k_cache_weigh<T, D, NR><<<weigh_grid(a, w, kBlocks), kThreads, smem, st>>>(a, w, (const T*)Q, cache);
+    k_cache_weigh<T, D, NR, FEW><<<weigh_grid(a, w, kBlocks), kThreads, smem, st>>>(a, w, (const T*)Q, cache);
     count_launch();
     return cudaGetLastError();
 }
@@ -373,6 +466,9 @@ static cudaError_t weigh_t(const CacheArgs& a, const WeighArgs& w, unsigned flag
     // 1000 tokens, 2 x 8 of 32768, 64 x 8 of 300: d = 128, 16 rows 6.1/8.2, 20.9/26.0, 11.2/22.8; 32 rows 9.1/8.1,
     // 34.7/26.8, 20.1/22.8; d = 64, 32 rows 6.7/8.6, 18.8/23.6, 12.0/22.7; 64 rows 10.1/9.3, 33.9/25.9, 20.3/26.4.
     if (rows > (D == 64 ? 32 : 16)) return launch_cache_weigh_tile(a, w, D, sizeof(T) == 4 ? 0 : 1, Q, cache, st);
+    // (2 x 16 heads of 32768 tokens, one row each: 24.7 us, and 26.1 in the form for eight rows; float32 29.1 and 32.2. Four rows
+    // in two tiles of two are 33, as each further step of the tensor cores takes its 17 clocks.)
+    if (rows <= 2) return mma_t<T, D, 1, true>(a, w, Q, cache, st);
     if (rows <= 8) return mma_t<T, D, 1>(a, w, Q, cache, st);
     constexpr int kMost = D == 64 && sizeof(T) == 2 ? 4 : 2;  // (32 float rows in two tiles of 16)
     return rows <= 16 ? mma_t<T, D, 2>(a, w, Q, cache, st) : mma_t<T, D, kMost>(a, w, Q, cache, st);

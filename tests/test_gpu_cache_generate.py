@@ -108,6 +108,11 @@ CASES = [
     ("bf16", 128, 48, 33, 1, 2, True, [1, 700], None, True, 0.0),
     ("bf16", 128, 16, 66, 1, 9, True, [600, 8, 9], [9, 9, 0], False, 1.0),   # 594 rows a head
     ("bf16", 64, 32, 32, 2, 17, False, [400, 129], [17, 5], True, 0.0),
+    ("bf16", 128, 16, 6, 3, 1, True, [33, 5000, 0, 31], None, True, 0.9),    # two rows
+    ("bf16", 64, 32, 2, 2, 2, True, [1, 2, 700, 65], [1, 2, 2, 0], False, 1.0),
+    ("f32", 128, 48, 2, 1, 1, False, [900, 17], None, True, 1.0),
+    ("f32", 64, 64, 3, 3, 2, True, [2, 3000, 129], [2, 1, 0], False, 0.5),
+    ("bf16", 64, 64, 11, 1, 3, True, [1300, 30], None, False, 1.0),          # 33 rows: tiles of 128 tokens
     ("bf16", 128, 64, 64, 1, 4, True, [60000, 40], None, False, 1.0),        # several tiles of rows, for long
     ("bf16", 64, 32, 90, 1, 6, True, [9, 30001], [6, 5], False, 0.5),        # two passes over the rows
     ("f32", 128, 64, 50, 1, 6, False, [20000], None, False, 1.0),
@@ -145,7 +150,8 @@ def test_weights_sum_to_the_rows(dtype, H, T, simt):
 
 
 @pytest.mark.parametrize("dtype,H,d,T,simt", [("bf16", 4, 128, 3, False), ("bf16", 12, 64, 3, False), ("bf16", 64, 128, 3, False),
-                                              ("f32", 4, 128, 3, False), ("f32", 40, 64, 3, False), ("f32", 4, 128, 3, True)])
+                                              ("f32", 4, 128, 3, False), ("f32", 40, 64, 3, False), ("f32", 4, 128, 3, True),
+                                              ("bf16", 130, 128, 3, False), ("f32", 100, 128, 3, False)])
 def test_unseen_and_bad_rows(dtype, H, d, T, simt):
     """NaN in keys reaches their own tokens' sums alone; rows with NaN or an infinity, or with a NaN
     for their lse, make NaN of the tokens that they see and of no others; a row that sees nothing is harmless."""
@@ -188,10 +194,26 @@ def test_large_scores_stay_weights(dtype, H):
     assert np.all(o >= even * (1 - 64 * 2.0 ** -23)) and np.all(o <= even * (1 + 64 * 2.0 ** -23) + H // 4 * 2)
 
 
+@pytest.mark.parametrize("dtype,H", [("bf16", 2), ("bf16", 8), ("bf16", 64), ("f32", 2), ("f32", 12), ("f32", 64)])
+def test_rows_of_unlike_size(dtype, H):
+    """Rows from a thousandth of the usual size to a thousand times it, side by side, some of zeros: each is as exact as
+    among its like."""
+    import torch
+    pool = Pool([700, 129], 2, 128, 64, dtype, seed=12)
+    gen = torch.Generator().manual_seed(3)
+    Q = torch.randn((2, H, 2, 128), generator=gen) * 2.0 ** torch.randint(-10, 11, (2, H, 2, 1), generator=gen)
+    Q[0, 0, 0] = 0
+    Q[1, H - 1, 1, ::2] *= 2.0 ** -20
+    Q = Q.to(pool.td).cuda()
+    for scale in (0.0, 0.001):
+        Q, lse, acc, out = _weigh(pool, H, 2, True, q=Q, scale=scale)
+        _check_weights(pool, H, 2, True, Q, lse, acc, out, scale=scale, label="%s unlike rows H%d" % (dtype, H))
+
+
 def test_weights_twice_and_any_split():
     """The same call gives the same bits, and a token's sum does not depend on the other sequences."""
     import torch
-    for dtype, H, T in (("bf16", 8, 1), ("bf16", 40, 4), ("f32", 8, 3)):
+    for dtype, H, T in (("bf16", 8, 1), ("bf16", 4, 2), ("bf16", 40, 4), ("bf16", 256, 5), ("f32", 8, 3), ("f32", 40, 4)):
         pool = Pool([700, 33, 4000], 4, 128, 32, dtype, seed=5)
         Q, lse, acc, a = _weigh(pool, H, T, True)
         _, _, _, b = _weigh(pool, H, T, True)
@@ -203,7 +225,8 @@ def test_weights_twice_and_any_split():
 
 
 @pytest.mark.parametrize("simt", [False, True], ids=["", "simt"])
-@pytest.mark.parametrize("dtype,H,T", [("bf16", 2, 1), ("bf16", 40, 2), ("f32", 6, 2)])
+@pytest.mark.parametrize("dtype,H,T", [("bf16", 2, 1), ("bf16", 6, 1), ("bf16", 40, 2), ("bf16", 160, 2), ("f32", 2, 1), ("f32", 6, 2),
+                                       ("f32", 40, 2)])
 def test_weights_out_of_range(dtype, H, T, simt):
     """Bad pages, lengths, counts and exponents are reported, and the other sequences' sums are right."""
     import torch
