@@ -21,8 +21,7 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;  // of a block
 constexpr int kTok = 2 * kGroup;                       // tokens of a warp's step
-constexpr int kAhead = 2;                              // steps that a warp's loads are ahead
-constexpr int kBlocks = 2;                             // of an SM
+constexpr int kRaw = 2;                                // stages of a warp's codes and scales in shared memory
 
 }  // namespace
 
@@ -117,11 +116,17 @@ template <typename T, int D, int NR, bool FEW> constexpr int q_bytes() {
     return q_regs<T, D, NR, FEW>() ? 0 : (sizeof(T) == 4 ? 2 : 1) * NR * (D / 16) * 256;
 }
 
+// Blocks of an SM. (Eight bf16 rows: 64 sequences of 33 to 8191 tokens, 8 cache heads: 47.1 us with two, 41.1 with
+// three, 47.6 with four; 2 x 16 heads of 32768: 21.2, 23.0 and 27.6. Float rows lose from three on.)
+template <typename T, int NR> constexpr int weigh_blocks() { return NR == 1 && sizeof(T) == 2 ? 3 : 2; }
+
 // Scores on m16n8k16 steps (halves in, fp32 out), tokens on the 16 side and 8 NR query rows on the 8 side.
 //
-// The lanes of a warp load the codes of a group in the order in which they feed the steps, 16
-// bytes each for d = 128 and neighbours next to each other, so codes go from memory to registers
-// and nothing passes through shared memory; kAhead steps, two groups each, are on their way. Widening is exact
+// The lanes of a warp copy the codes of a group in the order in which they feed the steps, 16
+// bytes each for d = 128 and neighbours next to each other, into a part of shared memory that is the warp's own, so that
+// the next step, two groups, is on its way without registers, and no warp waits for another. (Loads into registers two
+// steps ahead: 24.7 us for 2 x 16 heads of 32768 tokens, 20.3 so; copies two or three steps ahead 23.0 and more, with
+// fewer blocks 19.7.) Widening is exact
 // (cache.cuh). Rows are scaled by a power of two that puts the largest entry in [2^14, 2^15): bf16 rows are exact
 // as halves down to 2^-31 of it; float32 rows are two halves, hi + lo, both in one sum.
 // A lane ends with two tokens of each group and two rows for each eight; four lanes share a token.
@@ -131,7 +136,7 @@ template <typename T, int D, int NR, bool FEW> constexpr int q_bytes() {
 // (4 d/64 products for two tokens) and not into the codes (32 d/128 for them), and of what the step ends with
 // no column is empty: a lane has one score and one exponential for each group.
 template <typename T, int D, int NR, bool FEW>
-__global__ void __launch_bounds__(kThreads, kBlocks)
+__global__ void __launch_bounds__(kThreads, weigh_blocks<T, NR>())
 k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* __restrict__ cache) {
     using L = Grp<D>;
     constexpr bool F = sizeof(T) == 4;  // float rows
@@ -146,6 +151,7 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
     uint2* qs = reinterpret_cast<uint2*>(smem + warp * q_bytes<T, D, NR, FEW>());
+    const uint32_t ring = tc::smem_u32(smem) + kWarps * q_bytes<T, D, NR, FEW>() + warp * (kRaw * 18 * D);
     Place<kTok, kThreads> at;
     at.begin(a, start, (long long)(blockIdx.x - 1) * kWarps + warp, (long long)(gridDim.x - 1) * kWarps);
     if (at.left == 0) return;
@@ -154,8 +160,8 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
         const int rows = at.count * a.G;
         // the lane's token of step 0
         const long long sums = ((long long)at.b * a.Hkv + at.h) * w.cap + (long long)step0 * kTok + 8 * t4 + g;
-        const uint8_t* codes = cache + g * L::kRow + t4 * (D / 8);
-        const uint8_t* scales = cache + L::kKs + g * (D / 8) + (FEW ? (t4 & 1) * (D / 16) : t4 * (D / 32));
+        const int codes = g * L::kRow + t4 * (D / 8);
+        const int scales = L::kKs + g * (D / 8) + (FEW ? (t4 & 1) * (D / 16) : t4 * (D / 32));
         // lane l: group l % 2 of step i + l / 2
         auto groups = [&](int i) {
             const int gi = 2 * (step0 + i) + lane;
@@ -169,37 +175,24 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
             // steps' tokens of the lane with a sum: those before step `olds`
             const int olds = (row0 ? n : w.decay != 0.0f ? n - at.count : 0) - (step0 * kTok + 8 * t4 + g);
             int gcur = groups(0), gnxt = groups(16);
-            uint2 kc[kAhead][2][2][KW];  // [step][group][token g, g + 8]
-            uint32_t sc[kAhead][2][SW], ok = 0;
-            float base[kAhead];
-            auto load = [&](int u, int i) {  // called for every i in turn
+            uint32_t ok = 0;
+            float base[kRaw];
+            // Step i into stage u (that of i modulo kRaw); called for every i in turn. A lane copies the codes that it will read, and
+            // scales for its neighbours.
+            auto copy = [&](int u, int i) {
                 ok &= ~(3u << 2 * u);
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     const int grp = __shfl_sync(0xffffffffu, gcur, 2 * (i & 15) + y);
                     if (grp < 0) continue;
                     ok |= 1u << (2 * u + y);
-                    const unsigned long long at_group = (unsigned long long)(unsigned)grp * L::kBytes;
+                    const uint8_t* src = cache + (unsigned long long)(unsigned)grp * L::kBytes;
+                    const uint32_t dst = ring + (u * 2 + y) * (9 * D);
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const uint8_t* r = codes + at_group + 8 * x * L::kRow;
-                        if (D == 128) {
-                            const uint4 v = *reinterpret_cast<const uint4*>(r);
-                            kc[u][y][x][0] = make_uint2(v.x, v.y);
-                            kc[u][y][x][KW - 1] = make_uint2(v.z, v.w);
-                        } else {
-                            kc[u][y][x][0] = *reinterpret_cast<const uint2*>(r);
-                        }
-                    }
-                    if (SW == 2) {
-                        const uint2 v = *reinterpret_cast<const uint2*>(scales + at_group);
-                        sc[u][y][0] = v.x;
-                        sc[u][y][SW - 1] = v.y;
-                    } else {
-                        sc[u][y][0] = D == 128 || FEW ? *reinterpret_cast<const uint32_t*>(scales + at_group)
-                                                      : *reinterpret_cast<const uint16_t*>(scales + at_group);
-                    }
+                    for (int x = 0; x < 2; ++x) copy_async<D / 8>(dst + codes + 8 * x * L::kRow, src + codes + 8 * x * L::kRow);
+                    if (D == 128 || lane < 16) copy_async<4>(dst + L::kKs + 4 * lane, src + L::kKs + 4 * lane);
                 }
+                asm volatile("cp.async.commit_group;" ::: "memory");
                 base[u] = i < cnt && i * kTok < olds ? had[(long long)i * kTok] : 0.0f;
                 if ((i & 15) == 15) {
                     gcur = gnxt;
@@ -207,7 +200,7 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
                 }
             };
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) load(u, u);
+            for (int u = 0; u < kRaw - 1; ++u) copy(u, u);
 
             // Q: lane (g, t4) has channels [t4 d/4, (t4 + 1) d/4) of rows g, and what it needs of
             // rows 2 t4 and the next: factor of the scores, lse, keys that they see. (FEW: of row g / 4, if t4 is g % 4,
@@ -280,12 +273,40 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
             }
             __syncwarp();
 
-            for (int i0 = 0; i0 < cnt; i0 += kAhead) {
+            for (int i0 = 0; i0 < cnt; i0 += kRaw) {
 #pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
+                for (int u = 0; u < kRaw; ++u) {
                     const int i = i0 + u, tok = (step0 + i) * kTok;
                     float sum = 0.0f;
+                    const float was = base[u];
+                    const bool in = i < cnt && tok + 8 * t4 + g < n && (ok >> (2 * u + (t4 >> 1)) & 1);
+                    asm volatile("cp.async.wait_group %0;" ::"n"(kRaw - 2) : "memory");
+                    __syncwarp();
+                    copy((u + kRaw - 1) % kRaw, i + kRaw - 1);  // (over what all lanes read before the barrier)
                     if (i < cnt && tok < top) {
+                        uint2 kc[2][2][KW];  // [group][token g, g + 8]
+                        uint32_t sc[2][SW];
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const uint32_t src = ring + (u * 2 + y) * (9 * D);
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const uint32_t p = src + codes + 8 * x * L::kRow;
+                                if (D == 128)
+                                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                                 : "=r"(kc[y][x][0].x), "=r"(kc[y][x][0].y), "=r"(kc[y][x][KW - 1].x),
+                                                   "=r"(kc[y][x][KW - 1].y)
+                                                 : "r"(p));
+                                else
+                                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(kc[y][x][0].x), "=r"(kc[y][x][0].y) : "r"(p));
+                            }
+                            if (SW == 2)
+                                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(sc[y][0]), "=r"(sc[y][SW - 1]) : "r"(src + scales));
+                            else if (D == 128 || FEW)
+                                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sc[y][0]) : "r"(src + scales));
+                            else
+                                asm volatile("ld.shared.u16 %0, [%1];" : "=r"(sc[y][0]) : "r"(src + scales));
+                        }
                         const bool edge = tok + kTok > low;  // some row does not see all of these tokens
                         auto rows_of = [&](int part, int ks, int j) {
                             const int at = (part * KS + ks) * NR + j;
@@ -303,7 +324,7 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
                                     uint32_t k8[2][4];
 #pragma unroll
                                     for (int x = 0; x < 2; ++x)
-                                        e2m1x8_to_half2(wi & 1 ? kc[u][y][x][wi / 2].y : kc[u][y][x][wi / 2].x, k8[x]);
+                                        e2m1x8_to_half2(wi & 1 ? kc[y][x][wi / 2].y : kc[y][x][wi / 2].x, k8[x]);
 #pragma unroll
                                     for (int k2 = 0; k2 < 2; ++k2)
 #pragma unroll
@@ -325,13 +346,13 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
 #pragma unroll
                                 for (int c = 0; c < 2; ++c) {
                                     if (D == 128) {
-                                        const uint32_t two = sc[u][y][c % SW];
+                                        const uint32_t two = sc[y][c % SW];
                                         const float2 a0 = half2_to_float2(e4m3x2_to_half2(two & 0xffff));
                                         const float2 a1 = half2_to_float2(e4m3x2_to_half2(two >> 16));
                                         s[0][c][0] = a0.x; s[0][c][HF - 1] = a0.y;
                                         s[1][c][0] = a1.x; s[1][c][HF - 1] = a1.y;
                                     } else {
-                                        const uint32_t two = sc[u][y][0] >> 16 * c & 0xffff;
+                                        const uint32_t two = sc[y][0] >> 16 * c & 0xffff;
                                         const float2 a0 = half2_to_float2(e4m3x2_to_half2(two));
                                         s[0][c][0] = a0.x;
                                         s[1][c][0] = a0.y;
@@ -356,33 +377,33 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
                             sum = (up ? w2[1] : w2[0]) + __shfl_xor_sync(0xffffffffu, up ? w2[0] : w2[1], 2);
                         } else {
                             float2 s2t[2][2];  // [group][token g, g + 8], two rows each
-    #pragma unroll
+#pragma unroll
                             for (int y = 0; y < 2; ++y) {
                                 uint32_t s2[2][KW];  // [token g, g + 8]: scales, each in both halves
                                 if (D == 128) {
-                                    const uint32_t a0 = e4m3x2_to_half2(sc[u][y][0] & 0xffff), a1 = e4m3x2_to_half2(sc[u][y][0] >> 16);
+                                    const uint32_t a0 = e4m3x2_to_half2(sc[y][0] & 0xffff), a1 = e4m3x2_to_half2(sc[y][0] >> 16);
                                     s2[0][0] = __byte_perm(a0, a0, 0x1010);
                                     s2[0][KW - 1] = __byte_perm(a0, a0, 0x3232);
                                     s2[1][0] = __byte_perm(a1, a1, 0x1010);
                                     s2[1][KW - 1] = __byte_perm(a1, a1, 0x3232);
                                 } else {
-                                    const uint32_t a0 = e4m3x2_to_half2(sc[u][y][0]);
+                                    const uint32_t a0 = e4m3x2_to_half2(sc[y][0]);
                                     s2[0][0] = __byte_perm(a0, a0, 0x1010);
                                     s2[1][0] = __byte_perm(a0, a0, 0x3232);
                                 }
                                 float z[NR][4];
-    #pragma unroll
+#pragma unroll
                                 for (int wi = 0; wi < W; ++wi) {
                                     uint32_t k8[2][4];
-    #pragma unroll
+#pragma unroll
                                     for (int x = 0; x < 2; ++x) {
-                                        e2m1x8_to_half2(wi & 1 ? kc[u][y][x][wi / 2].y : kc[u][y][x][wi / 2].x, k8[x]);
-    #pragma unroll
+                                        e2m1x8_to_half2(wi & 1 ? kc[y][x][wi / 2].y : kc[y][x][wi / 2].x, k8[x]);
+#pragma unroll
                                         for (int j = 0; j < 4; ++j) k8[x][j] = hmul2(k8[x][j], s2[x][wi / 2]);
                                     }
-    #pragma unroll
+#pragma unroll
                                     for (int k2 = 0; k2 < 2; ++k2)
-    #pragma unroll
+#pragma unroll
                                         for (int j = 0; j < NR; ++j) {
                                             const int ks = 2 * wi + k2;
                                             const uint2 q = rows_of(0, ks, j);
@@ -399,7 +420,7 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
                                         }
                                 }
                                 s2t[y][0] = s2t[y][1] = make_float2(0.0f, 0.0f);
-    #pragma unroll
+#pragma unroll
                                 for (int j = 0; j < NR; ++j) {
                                     float2 p0 = weight2(make_float2(z[j][0], z[j][1]), zf[j], lse[j]);
                                     float2 p1 = weight2(make_float2(z[j][2], z[j][3]), zf[j], lse[j]);
@@ -422,11 +443,11 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
                             sum = (odd ? x1 : x0) + __shfl_xor_sync(0xffffffffu, odd ? x0 : x1, 1);
                         }
                     }
-                    if (i < cnt && tok + 8 * t4 + g < n && (ok >> (2 * u + (t4 >> 1)) & 1))
-                        w.acc_out[sums + (long long)i * kTok] = fmaf(decay, base[u], sum);
-                    load(u, i + kAhead);
+                    if (in) w.acc_out[sums + (long long)i * kTok] = fmaf(decay, was, sum);
                 }
             }
+            tc::cp_async_wait_all();
+            __syncwarp();
         }
         more = at.next(a, cnt);
     }
@@ -442,13 +463,13 @@ static unsigned weigh_grid(const CacheArgs& a, const WeighArgs& w, int blocks) {
 
 template <typename T, int D, int NR, bool FEW = false>
 static cudaError_t mma_t(const CacheArgs& a, const WeighArgs& w, const void* Q, const uint8_t* cache, cudaStream_t st) {
-    constexpr int smem = kWarps * q_bytes<T, D, NR, FEW>();
+    constexpr int smem = kWarps * (q_bytes<T, D, NR, FEW>() + kRaw * 18 * D);
     static std::atomic<unsigned long long> done{0};
     if (smem > 40 * 1024) {
         const cudaError_t e = set_smem_once((const void*)k_cache_weigh<T, D, NR, FEW>, smem, &done);
         if (e != cudaSuccess) return e;
     }
-    k_cache_weigh<T, D, NR, FEW><<<weigh_grid(a, w, kBlocks), kThreads, smem, st>>>(a, w, (const T*)Q, cache);
+    k_cache_weigh<T, D, NR, FEW><<<weigh_grid(a, w, weigh_blocks<T, NR>()), kThreads, smem, st>>>(a, w, (const T*)Q, cache);
     count_launch();
     return cudaGetLastError();
 }

@@ -133,6 +133,13 @@ __device__ __forceinline__ float2 weight2(float2 dot, float2 f, float2 minus_lse
     return make_float2(tc::ex2(t.x), tc::ex2(t.y));
 }
 
+template <int N> __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+    if (N == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
+
 // cache_weigh_tile.cu
 cudaError_t launch_cache_weigh_tile(const CacheArgs& a, const WeighArgs& w, int d, int dtype, const void* Q,
                                     const uint8_t* cache, cudaStream_t st);

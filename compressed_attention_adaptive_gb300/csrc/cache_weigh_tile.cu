@@ -84,13 +84,6 @@ struct Groups {
 // Bytes of the widening warps' codes and scales: two groups' keys of each stage.
 template <int D> constexpr int raw_bytes() { return 4 * kRaw * 2 * 9 * D; }
 
-template <int N> __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
-    if (N == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
-}
-
 // Whether any thread but the widening ones has x; they all meet here.
 __device__ __forceinline__ bool any_but_widening(bool x) {
     uint32_t r;
