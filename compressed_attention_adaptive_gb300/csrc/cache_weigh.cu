@@ -484,8 +484,7 @@ static cudaError_t weigh_t(const CacheArgs& a, const WeighArgs& w, unsigned flag
     }
     const long long rows = (long long)a.G * a.T;
     // Tiles on tcgen05 for more than 16 rows of 128 channels, or 32 of 64. Microseconds here and there, bf16, 8 heads of
-    // 1000 tokens, 2 x 8 of 32768, 64 x 8 of 300: d = 128, 16 rows 6.1/8.2, 20.9/26.0, 11.2/22.8; 32 rows 9.1/8.1,
-    // 34.7/26.8, 20.1/22.8; d = 64, 32 rows 6.7/8.6, 18.8/23.6, 12.0/22.7; 64 rows 10.1/9.3, 33.9/25.9, 20.3/26.4.
+    // 1000 tokens, 2 x 8 of 32768, 64 x 8 of 300: TABLE
     if (rows > (D == 64 ? 32 : 16)) return launch_cache_weigh_tile(a, w, D, sizeof(T) == 4 ? 0 : 1, Q, cache, st);
     // (2 x 16 heads of 32768 tokens, one row each: 24.7 us, and 26.1 in the form for eight rows; float32 29.1 and 32.2. Four rows
     // in two tiles of two are 33, as each further step of the tensor cores takes its 17 clocks.)

@@ -29,27 +29,29 @@ namespace mita {
 namespace {
 
 constexpr int kTok = 128;                        // tokens of a chunk
-constexpr int kScores = 256, kKeys = 4;          // columns of scores; stages of keys
-constexpr int kSoft = 4;                         // warpgroups for the weights
-constexpr int kWiden = 4 * kSoft, kIssue = kWiden + 4;  // first warps of the other roles
-constexpr int kThreads = 32 * (kIssue + 1);
 constexpr int kRaw = 3;                          // stages of codes of a widening warp: copies are kRaw - 1 chunks ahead
-constexpr uint32_t kK = kScores;                 // column of the first stage of keys
 
 // SPLIT: warpgroups that share a tile, with a part of its rows each. Without a split (up to 64 rows, one tile) each has
-// every fourth chunk to itself.
+// chunks to itself, and two smaller blocks share an SM: one's items begin and end while the other's go on.
 template <int SPLIT> struct Tiles {
-    static constexpr int kCols = SPLIT == 1 ? 64 : 128;    // rows of a tile
-    static constexpr int kStages = kScores / kCols;        // of scores
+    static constexpr int kBlocks = SPLIT == 1 ? 2 : 1;              // of an SM
+    static constexpr int kCols = SPLIT == 1 ? 64 : 128;             // rows of a tile
+    static constexpr int kStages = 2;                               // of scores
+    static constexpr int kKeys = SPLIT == 1 ? 2 : 4;                // stages of keys
+    static constexpr int kSoft = SPLIT == 1 ? kStages : SPLIT;      // warpgroups for the weights
+    static constexpr int kWiden = 4 * kSoft, kIssue = kWiden + 4;   // first warps of the other roles
+    static constexpr int kThreads = 32 * (kIssue + 1);
+    static constexpr uint32_t kK = kStages * kCols, kTmem = 512 / kBlocks;  // columns: of the first stage of keys, in all
+    static_assert(kK + kKeys * 64 == kTmem, "tensor memory");
 };
 
 // Parts of a chunk's sums, for the warpgroup whose number the chunk's is modulo kSoft; it joins them behind its own part
 // of the next chunk. A buffer is used again eight chunks later: a warpgroup comes there only after all have
 // released the scores of a chunk kStages before it, which the joining one does after its join.
 constexpr int kParts = 8;
-static_assert(kParts % kSoft == 0 && kParts > Tiles<kSoft>::kStages + 1, "parts would be overwritten");
+static_assert(kParts % Tiles<4>::kSoft == 0 && kParts > Tiles<4>::kStages + 1, "parts would be overwritten");
 struct WeighBars {
-    uint64_t k_full[kKeys], k_empty[kKeys], s_full[kSoft], s_empty[kSoft], p_full[kParts], drain;
+    uint64_t k_full[4], k_empty[4], s_full[2], s_empty[2], p_full[kParts], drain;
 };
 
 // Bytes of a tile's rows: as halves (two for float rows); log sums, factors, limits.
@@ -85,7 +87,7 @@ struct Groups {
 template <int D> constexpr int raw_bytes() { return 4 * kRaw * 2 * 9 * D; }
 
 // Whether any thread but the widening ones has x; they all meet here.
-__device__ __forceinline__ bool any_but_widening(bool x) {
+template <int WARPS> __device__ __forceinline__ bool any_but_widening(bool x) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
@@ -93,7 +95,7 @@ __device__ __forceinline__ bool any_but_widening(bool x) {
         "barrier.red.or.pred q, 1, %2, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)x), "n"(32 * (kWiden + 1))
+        : "r"((uint32_t)x), "n"(32 * WARPS)
         : "memory");
     return r != 0;
 }
@@ -120,11 +122,14 @@ __global__ void __launch_bounds__(256) k_cache_weigh_begin(CacheArgs a) {
 }
 
 template <typename T, int D, int SPLIT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Tiles<SPLIT>::kThreads, Tiles<SPLIT>::kBlocks)
 k_cache_weigh_tile(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* __restrict__ cache, int tiles) {
     using L = Grp<D>;
     constexpr bool F = sizeof(T) == 4;  // float rows: two halves, hi + lo
-    constexpr int kCols = Tiles<SPLIT>::kCols, kStages = Tiles<SPLIT>::kStages;
+    using S = Tiles<SPLIT>;
+    constexpr int kCols = S::kCols, kStages = S::kStages, kKeys = S::kKeys, kSoft = S::kSoft, kWiden = S::kWiden,
+                  kIssue = S::kIssue, kThreads = S::kThreads;
+    constexpr uint32_t kK = S::kK;
     constexpr int KS = D / 16, W = D / 32, kHalf = kCols * D * 2, kTile = (F ? 2 : 1) * kHalf;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t sm = (tc::smem_u32(smem_raw) + 1023) & ~1023u;
@@ -141,7 +146,7 @@ k_cache_weigh_tile(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint
     volatile Abort* abort_v = &abort;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quarter = warp & 3;
     // (waits for another kernel's blocks on this SM, which end whatever this one does)
-    if (warp == kIssue) tc::tmem_alloc(&tmem_slot, 512);
+    if (warp == kIssue) tc::tmem_alloc(&tmem_slot, S::kTmem);
     if (tid == 0) {
         for (int i = 0; i < kKeys; ++i) {
             // (fault test: one more signal for one block's keys than comes)
@@ -233,7 +238,7 @@ k_cache_weigh_tile(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint
             }
             if (warp < kWiden || warp == kIssue) {
                 tc::fence_proxy_async();
-                unusual = any_but_widening(unusual);
+                unusual = any_but_widening<kWiden + 1>(unusual);
             }
 
             if (warp < kWiden) {
@@ -497,7 +502,7 @@ k_cache_weigh_tile(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == kIssue) tc::tmem_dealloc(tmem, 512);
+    if (warp == kIssue) tc::tmem_dealloc(tmem, S::kTmem);
 }
 
 // ------------------------------------------------------------------ launch
@@ -505,7 +510,8 @@ k_cache_weigh_tile(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint
 template <typename T, int D, int SPLIT>
 static cudaError_t split_t(const CacheArgs& a, const WeighArgs& w, const void* Q, const uint8_t* cache, cudaStream_t st) {
     // rows of a pass: as many as there are, as far as they fit (24 KB are static)
-    constexpr int kCols = Tiles<SPLIT>::kCols, kBytes = tile_bytes<T, D, kCols>();
+    using S = Tiles<SPLIT>;
+    constexpr int kCols = S::kCols, kBytes = tile_bytes<T, D, kCols>();
     constexpr int kMost = SPLIT == 1 ? 1 : ((227 - 24) * 1024 - 1024 - raw_bytes<D>()) / kBytes;
     const long long rows = (long long)a.G * a.T;
     const int tiles = (int)std::min<long long>(kMost, (rows + kCols - 1) / kCols);
@@ -522,8 +528,8 @@ static cudaError_t split_t(const CacheArgs& a, const WeighArgs& w, const void* Q
     at.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t c{};
     // (one SM has the kernel before it)
-    c.gridDim = dim3((unsigned)std::min<long long>(chunks, num_sms() - 1));
-    c.blockDim = dim3(kThreads);
+    c.gridDim = dim3((unsigned)std::min<long long>(chunks, S::kBlocks * num_sms() - 1));
+    c.blockDim = dim3(S::kThreads);
     c.dynamicSmemBytes = tiles * kBytes + raw_bytes<D>() + 1024;
     c.stream = st;
     c.attrs = &at;
@@ -535,7 +541,7 @@ static cudaError_t split_t(const CacheArgs& a, const WeighArgs& w, const void* Q
 
 template <typename T, int D>
 static cudaError_t tile_t(const CacheArgs& a, const WeighArgs& w, const void* Q, const uint8_t* cache, cudaStream_t st) {
-    return (long long)a.G * a.T <= Tiles<1>::kCols ? split_t<T, D, 1>(a, w, Q, cache, st) : split_t<T, D, kSoft>(a, w, Q, cache, st);
+    return (long long)a.G * a.T <= Tiles<1>::kCols ? split_t<T, D, 1>(a, w, Q, cache, st) : split_t<T, D, 4>(a, w, Q, cache, st);
 }
 
 cudaError_t launch_cache_weigh_tile(const CacheArgs& a, const WeighArgs& w, int d, int dtype, const void* Q,
