@@ -483,15 +483,20 @@ static cudaError_t weigh_t(const CacheArgs& a, const WeighArgs& w, unsigned flag
         return cudaGetLastError();
     }
     const long long rows = (long long)a.G * a.T;
-    // Tiles on tcgen05 for more than 16 rows of 128 channels, or 32 of 64. Microseconds here and there, bf16, 8 heads of
-    // 1000 tokens, 2 x 8 of 32768, 64 x 8 of 300: TABLE
-    if (rows > (D == 64 ? 32 : 16)) return launch_cache_weigh_tile(a, w, D, sizeof(T) == 4 ? 0 : 1, Q, cache, st);
-    // (2 x 16 heads of 32768 tokens, one row each: 24.7 us, and 26.1 in the form for eight rows; float32 29.1 and 32.2. Four rows
-    // in two tiles of two are 33, as each further step of the tensor cores takes its 17 clocks.)
+    // From how many rows on tiles on tcgen05 take less. Microseconds here and there for 8 heads of 1000 tokens, 2 x 8 of
+    // 32768, 64 x 8 of 300: bf16, d = 128, 16 rows 5.8/7.1, 16.2/22.7, 10.3/17.7; 32 rows 9.1/7.1, 31.4/22.7, 18.4/17.7;
+    // float32, 8 rows 6.1/7.3, 16.6/23.1, 11.1/18.2, 16 rows 8.4/7.3, 27.7/23.0, 17.4/18.1; d = 64, bf16, 32 rows 6.5,
+    // 18.2 and 11.6 here, 33 rows 7.8, 22.8 and 18.7 there (two passes here, 64 rows: 10.1, 33.9 and 20.3).
+    constexpr int kMost = D == 64 ? 32 : sizeof(T) == 4 ? 8 : 16;
+    if (rows > kMost) return launch_cache_weigh_tile(a, w, D, sizeof(T) == 4 ? 0 : 1, Q, cache, st);
+    // (2 x 16 heads of 32768 tokens, one row each, with loads into registers: 24.7 us, and 26.1 in the form for eight rows; float32
+    // 29.1 and 32.2. Four rows in two tiles of two were 33, as each further step of the tensor cores takes its 17 clocks.)
     if (rows <= 2) return mma_t<T, D, 1, true>(a, w, Q, cache, st);
-    if (rows <= 8) return mma_t<T, D, 1>(a, w, Q, cache, st);
-    constexpr int kMost = D == 64 && sizeof(T) == 2 ? 4 : 2;  // (32 float rows in two tiles of 16)
-    return rows <= 16 ? mma_t<T, D, 2>(a, w, Q, cache, st) : mma_t<T, D, kMost>(a, w, Q, cache, st);
+    if constexpr (kMost > 8) {
+        if (rows > 16) return mma_t<T, D, kMost == 32 && sizeof(T) == 2 ? 4 : 2>(a, w, Q, cache, st);  // (float: two tiles of 16)
+        if (rows > 8) return mma_t<T, D, 2>(a, w, Q, cache, st);
+    }
+    return mma_t<T, D, 1>(a, w, Q, cache, st);
 }
 
 cudaError_t launch_cache_weigh(const CacheArgs& a, int d, int dtype, unsigned flags, const void* Q, const void* cache,
