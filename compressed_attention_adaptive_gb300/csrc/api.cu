@@ -843,6 +843,14 @@ mita_status mita_cache_weights(const mita_cache_params* p, const void* Q, const 
     if ((acc && acc != acc_out && overlap(acc, n, acc_out, n)) || overlap(Q, cache_bytes(p, p->H), acc_out, n) ||
         overlap(lse, (size_t)p->B * p->H * p->T * sizeof(float), acc_out, n))
         return fail(MITA_ERR_INVALID_ARG, "acc_out must not overlap Q, lse or acc (but may be acc)");
+    const size_t nb = (size_t)p->B * 4;
+    size_t need;
+    carve_cache(p, plan, nullptr, &need);
+    if (overlap(cache, (size_t)p->n_pages * p->H_kv * a.pgroups * (18 * (size_t)p->d), acc_out, n) ||
+        overlap(table, nb * p->max_pages, acc_out, n) || overlap(len, nb, acc_out, n) ||
+        (count && overlap(count, nb, acc_out, n)) || (exps && overlap(exps, 8 * (size_t)p->H_kv, acc_out, n)) ||
+        overlap(ws, need, acc_out, n))
+        return fail(MITA_ERR_INVALID_ARG, "acc_out must not overlap the cache, the index arrays or the workspace");
     MITA_CUDA(launch_cache_weigh(a, p->d, p->dtype, p->flags, Q, cache, lse, decay, acc, acc_out, (cudaStream_t)stream),
               "cache weights");
     prof_mark((cudaStream_t)stream, "");

@@ -3,15 +3,21 @@
 // Each (sequence, cache head) that has more than keep tokens keeps its first, its last
 // and, of the others, the K with the largest sums. The K-th largest is found by radix: counts of the
 // sums' leading digits, then of the next digit among those that share the leading ones, and so on
-// through 32 bits (sums as ordered integers); what is equal to the K-th is
-// told apart by place, in the same way. Once few share the digits so far they are compared with each other. Kept rows behind the new length then go to the freed places before
-// it, i-th to i-th: what is read is behind the new length and what is written before it, so rows
-// move in any order and at once.
+// through 32 bits (sums as ordered integers); what is equal to the K-th is told apart by place, in the
+// same way. Once few share the digits so far they are compared with each other. Kept rows behind the new
+// length then go to the freed places before it, i-th to i-th: what is read is behind the new length and
+// what is written before it, so rows move in any order and at once.
 //
 // Work split. A row of sums is shared by a cluster of C blocks, each with its run of places: it holds their
 // keys in shared memory (they are read from memory once, if they fit), counts digits there, and
 // adds up the cluster's counts through distributed shared memory, one cluster barrier per
 // digit. The same blocks then number the freed places and the rows that move, and move them.
+//
+// What it reads and writes is 4 bytes a sum, and a row that moves 2 x 288 bytes in sectors of 32 (144 held), which for long
+// rows is a fifth of the time; what bounds it is the chain of steps: for 32 rows of 32768, 20,000 of 40,000 clocks
+// are the digits' and the list's barriers (a cluster's takes 1500), 5000 the loads, 12,000 the moves.
+// Measured, in a graph: 128 rows of 2112 cut to 2048 11.0 us, 144 of 700 to 9001 cut to 1500 22.7, 32 of 32768 cut
+// to 4096 25.1. A thread for each block of a row that moves, which looked its places up itself: 13.2, 26.4 and 31.0.
 #include <cooperative_groups.h>
 
 #include <algorithm>

@@ -6,8 +6,8 @@
 //                shared memory, fp32 in tensor memory
 //
 // A lane of tensor memory is a token, so a thread has a token's scores with all rows: it adds up their weights
-// by itself. What a token costs is then one exponential per row
-// and the four or so instructions around it; keys are widened once for all rows of a pass.
+// by itself. What a token costs is then one exponential per row and the four or so instructions around it; keys are
+// widened once for all rows of a pass.
 //
 // Keys go from memory to registers in the order of m16n8k16's A (the cache's own order: neighbouring lanes
 // read neighbouring bytes) and from there to tensor memory by 16 x 128 bit stores, which puts the
@@ -18,6 +18,14 @@
 // a chunk's sums. Four warps widen keys, each the quarter of the lanes that it can reach; one issues the products.
 // Every wait is bounded; a block that gives up raises its abort flag, lets its products land, frees its
 // tensor memory and says so in the status word.
+//
+// Measured, in a graph: 256 rows over 2 x 8 heads of 32768 tokens 55.1 us (598 TFLOP/s; the register form 221), 32 rows 22.7.
+// A tile of 128 x 128 takes about 1400 clocks: the exponentials 512 of them, the products 450, what
+// four warps of each scheduler issue 800; none is full, the steps wait for each other.
+//   - Three warpgroups with a stage of scores and chunks of their own: 72 us; eight widening warps, at whose cost the
+//     weights have 72 registers instead of 80: 59.5.
+//   - Not kept: half a tile's scores loaded while the other half is weighed, across tiles (68.6); two warpgroups for every
+//     second tile (65); two blocks an SM with one stage of 128 rows each (71); warps that only copy (57.8).
 #include <algorithm>
 #include <type_traits>
 

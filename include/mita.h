@@ -343,12 +343,11 @@ mita_status mita_cache_attention(const mita_cache_params* p, const void* Q, cons
  * row that sees no key is harmless; no weight is above 1 (a rounded lse may be below a score);
  * a row with a NaN or an infinity in Q, or whose lse
  * is NaN, makes the sums of the tokens that it sees NaN. Places j >= len[b] are left
- * as they were. acc_out may be acc; otherwise they must not overlap, and Q and lse must not
- * overlap acc_out. decay is finite, >= 0; with 0 acc is not read and may be NULL. The sum
+ * as they were. acc_out may be acc; no other overlap of acc_out with anything is taken. decay is finite, >= 0; with 0 acc is not read and may be NULL. The sum
  * of an own token starts at 0 whatever its place held before, so sums need no initial value.
  * A sequence with count[b] = 0 has its sums decayed. The same call gives the same bits.
  * Scores, weights and sums are fp32; float32 rows enter as two halves (22 bits), bf16
- * rows exactly. With MITA_FLAG_SIMT fp32 throughout, on CUDA cores. The workspace is that of
+ * rows exactly, each down to 2^-29 of the row's largest entry. With MITA_FLAG_SIMT fp32 throughout, on CUDA cores. The workspace is that of
  * mita_cache_workspace_size(). */
 mita_status mita_cache_weights(const mita_cache_params* p, const void* Q, const void* cache, const int32_t* table,
                                const int32_t* len, const int32_t* count, const int32_t* exps, const float* lse,

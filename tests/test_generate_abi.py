@@ -208,7 +208,8 @@ def test_weights_pointers(lib):
                dict(acc=None), dict(Q=A + 8), dict(cache=2 * A + 8), dict(table=3 * A + 2), dict(lens=4 * A + 1),
                dict(counts=A + 2), dict(exps=A + 2), dict(lse=5 * A + 2), dict(acc=6 * A + 1), dict(out=7 * A + 2),
                dict(decay=-1.0), dict(decay=float("nan")), dict(decay=float("inf")), dict(out=A), dict(out=5 * A),
-               dict(out=6 * A + 4), dict(out=6 * A - 4)):
+               dict(out=6 * A + 4), dict(out=6 * A - 4), dict(out=2 * A + 64), dict(out=3 * A + 4), dict(out=4 * A),
+               dict(out=9 * A, counts=9 * A + 4), dict(out=9 * A, exps=9 * A), dict(out=8 * A + 512)):
         assert _weigh(lib, p, **kw) == 1, kw
     for kw in (dict(ws=None), dict(ws=8 * A + 8), dict(n=need - 1)):
         assert _weigh(lib, p, **kw) == 3, kw

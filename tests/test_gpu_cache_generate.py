@@ -513,6 +513,51 @@ def test_eviction_and_weights_captured():
         assert eager.lens.tolist() == [min(n + t + 1, budget) for n in start]
 
 
+@pytest.mark.parametrize("H,T", [(2, 1), (12, 1), (48, 2), (200, 2)])
+def test_weights_captured_and_beside_another_call(H, T):
+    """A captured call reads its lengths when it is replayed; two calls on two streams at once, with a workspace each,
+    give what they give one after the other."""
+    import torch
+    import compressed_attention_adaptive_gb300 as mita
+    pools = [Pool([5000, 300], 2, 128, 64, "bf16", seed=s) for s in (1, 2)]
+    p = mita.CacheParams(2, H, 2, T, 128, 64, pools[0].n_pages, pools[0].cols, flags=mita.FLAG_CAUSAL)
+    gen = torch.Generator().manual_seed(3)
+    Q = torch.randn((2, H, T, 128), generator=gen).to(torch.bfloat16).cuda()
+    lse = torch.full((2, H, T), 8.0, device="cuda")
+    acc = torch.rand((2, 2, pools[0].cols * 64), generator=gen).cuda()
+    wss = [mita.cache_workspace(p) for _ in pools]
+    lens = [torch.tensor(x, dtype=torch.int32).cuda() for x in ([5000, 300], [4097, 1], [0, 129])]
+
+    def call(i, ln, out, **kw):
+        mita.mita_cache_weights(p, Q, pools[i].cache, pools[i].table, ln, lse, acc, wss[i], decay=0.5, acc_out=out, **kw)
+
+    want = [[torch.zeros_like(acc) for _ in lens] for _ in pools]
+    for i in range(2):
+        for ln, out in zip(lens, want[i]):
+            call(i, ln, out)
+            mita.mita_device_status(wss[i])
+    now, got = lens[0].clone(), torch.zeros_like(acc)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(0, now, got)
+    for ln, w in zip(lens, want[0]):
+        now.copy_(ln)
+        got.zero_()
+        graph.replay()
+        mita.mita_device_status(wss[0])
+        assert torch.equal(got, w)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.zeros_like(acc) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for i in range(2):
+            call(i, lens[0], outs[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        mita.mita_device_status(wss[i])
+        assert torch.equal(outs[i], want[i][0])
+
+
 def test_eviction_beside_another_call():
     """Two evictions on two streams at once, with a workspace each, are as one after the other."""
     import torch
