@@ -12,7 +12,7 @@
 //
 // Measured: queries and keys of two prompts of 32768, 16 heads each, d = 128, out of a projection's order
 // (1074 MB) 167 us (6.4 TB/s, 0.95 of the copy rate), 131,072 rows of 10 heads in place of
-// order 99 us (0.99). One token of 64 sequences, 40 heads: 3.2 us, a launch and three memory latencies.
+// order 99 us (0.99). One token of 64 sequences, 40 heads: 3.4 us, a launch and three memory latencies.
 //   - 16-byte accesses, four heads' loads and then their stores: 253 and 155 us; 16 bytes with the next
 //     heads' loads ahead: 235 and 145; 32 bytes with them ahead: 167 and 99.
 #include <math.h>
