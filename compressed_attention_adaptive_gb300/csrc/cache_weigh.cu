@@ -51,7 +51,7 @@ k_cache_weigh_simt(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint
     }
     const int lane = threadIdx.x & 31, sub = lane >> 3, ch = lane & 7, blk = D == 128 ? ch : ch >> 1;
     Place<kTok, kThreads> at;
-    at.begin(a, start, (long long)(blockIdx.x - 1) * kWarps + (threadIdx.x >> 5), (long long)(gridDim.x - 1) * kWarps);
+    at.begin<true>(a, start, (long long)(blockIdx.x - 1) * kWarps + (threadIdx.x >> 5), (long long)(gridDim.x - 1) * kWarps);
     if (at.left == 0) return;
     do {
         for (int gi = 2 * at.at; gi < 2 * at.at + 2 && gi * kGroup < at.n; ++gi) {
@@ -156,7 +156,7 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
     uint2* qs = reinterpret_cast<uint2*>(smem + warp * q_bytes<T, D, NR, FEW>());
     const uint32_t ring = tc::smem_u32(smem) + kWarps * q_bytes<T, D, NR, FEW>() + warp * (kRaw * 18 * D);
     Place<kTok, kThreads> at;
-    at.begin(a, start, (long long)(blockIdx.x - 1) * kWarps + warp, (long long)(gridDim.x - 1) * kWarps);
+    at.begin<true>(a, start, (long long)(blockIdx.x - 1) * kWarps + warp, (long long)(gridDim.x - 1) * kWarps);
     if (at.left == 0) return;
     for (bool more = true; more;) {
         const int cnt = (int)min(at.left, (long long)(at.steps - at.at)), n = at.n, step0 = at.at;

@@ -14,6 +14,11 @@ struct WeighArgs {
     long long cap;  // places of a sequence
 };
 
+// n / d; as 32-bit numbers where n is one.
+__device__ __forceinline__ unsigned long long divide(unsigned long long n, unsigned d) {
+    return n >> 32 ? n / d : (unsigned)n / d;
+}
+
 // Where a worker (a warp, or a block) is on the line of steps of TOK tokens. begin() is called by the whole
 // block, of THREADS.
 template <int THREADS> struct LineStart {
@@ -29,41 +34,58 @@ template <int TOK, int THREADS> struct Place {
         count = cache_count(a, b);
         steps = (n + TOK - 1) / TOK;
     }
-    // The part of worker `me` of `all`. A thread sums up its share of the sequences.
-    __device__ __forceinline__ void begin(const CacheArgs& a, LineStart<THREADS>& s, long long me, long long all) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        const int per = (a.B + THREADS - 1) / THREADS;
-        unsigned long long mine = 0;
+    // Steps of the sequences from `first` on, `per` of them.
+    __device__ __forceinline__ static unsigned long long share(const CacheArgs& a, int first, int per) {
+        unsigned long long sum = 0;
 #pragma unroll 4
-        for (int i = 0; i < per; ++i) {
-            const int q = threadIdx.x * per + i;
-            if (q < a.B) mine += (unsigned long long)((cache_len(a, q) + TOK - 1) / TOK) * a.Hkv;
-        }
-        unsigned long long x = mine;
+        for (int i = 0; i < per; ++i)
+            if (first + i < a.B) sum += (unsigned long long)((cache_len(a, first + i) + TOK - 1) / TOK) * a.Hkv;
+        return sum;
+    }
+    // The part of worker `me` of `all`. A thread sums up its share of the sequences: of a block's, or (WARPS), when they are
+    // few, of each warp's for itself, without barriers (a call for one sequence of 1000 tokens takes 5.0 us with them, 4.7
+    // without; the tiles' registers spill over the second way, and 55 us become 58).
+    template <bool WARPS> __device__ __forceinline__ void begin(const CacheArgs& a, LineStart<THREADS>& s, long long me, long long all) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const bool few = WARPS && a.B <= 128;
+        const int per = few ? (a.B + 31) / 32 : (a.B + THREADS - 1) / THREADS;
+        const unsigned long long mine = share(a, (few ? lane : threadIdx.x) * per, per);
+        unsigned long long x = mine, total;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x += y;
         }
-        if (lane == 31) s.warps[warp] = x;
-        __syncthreads();
-        unsigned long long total = 0, base = 0;
+        if (few) {
+            total = __shfl_sync(0xffffffffu, x, 31);
+        } else {
+            if (lane == 31) s.warps[warp] = x;
+            __syncthreads();
+            unsigned long long base = 0;
+            total = 0;
 #pragma unroll
-        for (int w = 0; w < THREADS / 32; ++w) {
-            if (w == warp) base = total;
-            total += s.warps[w];
+            for (int w = 0; w < THREADS / 32; ++w) {
+                if (w == warp) base = total;
+                total += s.warps[w];
+            }
+            s.before[threadIdx.x] = base + x - mine;
+            __syncthreads();
         }
-        s.before[threadIdx.x] = base + x - mine;
-        __syncthreads();
-        const unsigned long long q = total / all, r = total - q * all;
+        const unsigned long long q = divide(total, (unsigned)all), r = total - q * all;
         const unsigned long long w0 = me * q + min((unsigned long long)me, r);
         left = (long long)(q + ((unsigned long long)me < r));
         b = a.B;
         if (left == 0) return;
         int slices = 0;  // threads whose share begins at or before w0
+        unsigned long long off;
+        if (few) {
+            slices = __popc(__ballot_sync(0xffffffffu, x - mine <= w0));
+            off = w0 - __shfl_sync(0xffffffffu, x - mine, slices - 1);
+        } else {
 #pragma unroll
-        for (int i = 0; i < THREADS; i += 32) slices += __popc(__ballot_sync(0xffffffffu, s.before[i + lane] <= w0));
-        unsigned long long off = w0 - s.before[slices - 1];
+            for (int i = 0; i < THREADS; i += 32) slices += __popc(__ballot_sync(0xffffffffu, s.before[i + lane] <= w0));
+            off = w0 - s.before[slices - 1];
+        }
         // (shares of threads without sequences begin at the total, which is above w0; a sequence without
         // tokens shares its beginning with the next)
         bool found = false;
@@ -77,7 +99,7 @@ template <int TOK, int THREADS> struct Place {
             left = 0;
             return;
         }
-        h = (int)(off / steps);
+        h = (int)divide(off, (unsigned)steps);
         at = (int)(off - (unsigned long long)h * steps);
     }
     // Behind `done` steps of the same head.

@@ -14,8 +14,9 @@
 // channels of a token in the order {t d/4 + 2 m, t d/4 + 2 m + 1 : t = 0 .. 3} for m = 0, 1, ...; Q's rows are stored in
 // the same order.
 //
-// Warps: four warpgroups for the weights, each with a quarter of a tile's rows; they take turns at joining the four parts of
-// a chunk's sums. Four warps widen keys, each the quarter of the lanes that it can reach; one issues the products.
+// Warps: four warpgroups for the weights, each with a quarter of a tile's rows, which take turns at joining the four parts of
+// a chunk's sums (for up to 64 rows two, each with every other chunk to itself). Four warps widen keys, each the quarter of
+// the lanes that it can reach; one issues the products.
 // Every wait is bounded; a block that gives up raises its abort flag, lets its products land, frees its
 // tensor memory and says so in the status word.
 //
@@ -80,10 +81,7 @@ struct Groups {
         nxt = look(16);
     }
     // called for every i in turn
-    template <typename Look> __device__ __forceinline__ int get(int i, int y, Look look) {
-        const int g = __shfl_sync(0xffffffffu, cur, 2 * (i & 15) + y);
-        return g;
-    }
+    __device__ __forceinline__ int get(int i, int y) const { return __shfl_sync(0xffffffffu, cur, 2 * (i & 15) + y); }
     template <typename Look> __device__ __forceinline__ void step(int i, Look look) {
         if ((i & 15) != 15) return;
         cur = nxt;
@@ -173,7 +171,7 @@ k_cache_weigh_tile(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint
     }
     tc::fence_before_sync();
     Place<kTok, kThreads> at;
-    at.begin(a, start, blockIdx.x, gridDim.x);
+    at.begin<false>(a, start, blockIdx.x, gridDim.x);  // (with barriers: the others' start, and the address of the tensor memory)
     tc::fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
 
@@ -337,7 +335,7 @@ k_cache_weigh_tile(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint
                     float base = base_of(own0);
                     for (int c = own0, i = 0; c < cnt; c += kSoft, ++i) {
                         const float next = base_of(c + kSoft);
-                        const int group = groups.get(i, lane >> 4, look);
+                        const int group = groups.get(i, lane >> 4);
                         groups.step(i, look);
                         if (!warp_wait(&bar.s_full[wg], (done + c) / kSoft & 1, abort_v)) break;
                         tc::fence_after_sync();
@@ -367,7 +365,7 @@ k_cache_weigh_tile(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint
                             if (lane == 0) tc::mbar_arrive(&bar.p_full[t & (kParts - 1)]);
                         }
                         if (c > 0 && ((t - 1) & (kSoft - 1)) == wg) {
-                            const int pb = (t - 1) & (kParts - 1), group = groups.get(joined, lane >> 4, look);
+                            const int pb = (t - 1) & (kParts - 1), group = groups.get(joined, lane >> 4);
                             groups.step(joined++, look);
                             if (!(ok = warp_wait(&bar.p_full[pb], (t - 1) / kParts & 1, abort_v))) break;
                             const float* x = &parts[pb][0][tl];
@@ -391,7 +389,7 @@ k_cache_weigh_tile(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint
                 auto copy = [&](int i) {  // called for every i in turn
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const int grp = groups.get(i, y, look);
+                        const int grp = groups.get(i, y);
                         if (grp < 0) continue;
                         const uint8_t* src = cache + (unsigned long long)(unsigned)grp * L::kBytes;
                         const uint32_t dst = ring + (i % kRaw) * (18 * D) + y * (9 * D);

@@ -194,6 +194,19 @@ def test_large_scores_stay_weights(dtype, H):
     assert np.all(o >= even * (1 - 64 * 2.0 ** -23)) and np.all(o <= even * (1 + 64 * 2.0 ** -23) + H // 4 * 2)
 
 
+@pytest.mark.parametrize("B", [31, 32, 33, 128, 129, 700])
+@pytest.mark.parametrize("H,T", [(2, 1), (10, 1), (36, 2)])
+def test_batches_of_many_sequences(B, H, T):
+    """Short sequences, most of them unlike, some without tokens, at the sizes where the search for a warp's place changes."""
+    rng = np.random.default_rng(B)
+    lens = [int(x) for x in rng.integers(0, 90, B)]
+    lens[0], lens[B // 2], lens[-1] = 0, 300, 0
+    pool = Pool(lens, 2, 64, 16, "bf16", seed=4)
+    Q, lse, acc, out = _weigh(pool, H, T, True, decay=0.5)
+    _behind(pool, out, acc, False)
+    _check_weights(pool, H, T, True, Q, lse, acc, out, decay=0.5, label="bf16 d64 B%d H%d T%d" % (B, H, T))
+
+
 @pytest.mark.parametrize("dtype,H", [("bf16", 2), ("bf16", 8), ("bf16", 64), ("f32", 2), ("f32", 12), ("f32", 64)])
 def test_rows_of_unlike_size(dtype, H):
     """Rows from a thousandth of the usual size to a thousand times it, side by side, some of zeros: each is as exact as
