@@ -108,6 +108,16 @@ class CacheParams:
     def pool_bytes(self):  # mita_cache_size
         return self.n_pages * self.H_kv * self.page * 9 * self.d // 8
 
+    @functools.cached_property
+    def _checks(self):
+        """What a call's tensors are held to: dtypes, and shapes of rows (queries', keys'), table, lens, exps, lse
+        and sums."""
+        import torch
+        B, H, Hkv, T, d = self.B, self.H, self.H_kv, self.T, self.d
+        return (torch.bfloat16 if self.dtype == BF16 else torch.float32, torch.int32, torch.uint8, torch.float32,
+                (B, H, T, d), (B, Hkv, T, d), (B, self.max_pages), (B,), (2, Hkv), (B, H, T),
+                (B, Hkv, self.max_pages * self.page), getattr(torch._C, "_cuda_getCurrentRawStream", None))
+
     def c(self):
         return self._c
 
@@ -396,28 +406,24 @@ def _cache_index(p: CacheParams, X, Y, heads, cache, table, lens, ws, counts, ex
     """Holds the tensors of a cache call to ``p`` (the C ABI sees only pointers) and
     returns the pointers of table, lens, counts and exps, and the stream. Written
     out, not in loops: a decoding step makes these calls for every layer."""
-    import torch
-    i32, u8, dev = torch.int32, torch.uint8, cache.get_device()
-    dt = torch.bfloat16 if p.dtype == BF16 else torch.float32
-    s = (p.B, heads, p.T, p.d)
+    dt, i32, u8, _, sq, sk, st, sl, se, _, _, raw_stream = p._checks
+    dev = cache.get_device()
+    s = sq if heads == p.H else sk
     if X.dtype is not dt or X.get_device() != dev or X.shape != s or not X.is_contiguous():
         _refuse(X, s, dt, dev)
     if Y is not X and (Y.dtype is not dt or Y.get_device() != dev or Y.shape != s or not Y.is_contiguous()):
         _refuse(Y, s, dt, dev)
-    s = (p.B, p.max_pages)
-    if table.dtype is not i32 or table.get_device() != dev or table.shape != s or not table.is_contiguous():
-        _refuse(table, s, i32, dev)
-    s = (p.B,)
-    if lens.dtype is not i32 or lens.get_device() != dev or lens.shape != s or not lens.is_contiguous():
-        _refuse(lens, s, i32, dev)
+    if table.dtype is not i32 or table.get_device() != dev or table.shape != st or not table.is_contiguous():
+        _refuse(table, st, i32, dev)
+    if lens.dtype is not i32 or lens.get_device() != dev or lens.shape != sl or not lens.is_contiguous():
+        _refuse(lens, sl, i32, dev)
     if counts is not None:
-        if counts.dtype is not i32 or counts.get_device() != dev or counts.shape != s or not counts.is_contiguous():
-            _refuse(counts, s, i32, dev)
+        if counts.dtype is not i32 or counts.get_device() != dev or counts.shape != sl or not counts.is_contiguous():
+            _refuse(counts, sl, i32, dev)
         counts = counts.data_ptr()
     if exps is not None:
-        s = (2, p.H_kv)
-        if exps.dtype is not i32 or exps.get_device() != dev or exps.shape != s or not exps.is_contiguous():
-            _refuse(exps, s, i32, dev)
+        if exps.dtype is not i32 or exps.get_device() != dev or exps.shape != se or not exps.is_contiguous():
+            _refuse(exps, se, i32, dev)
         exps = exps.data_ptr()
     if cache.dtype is not u8 or not cache.is_contiguous():
         _refuse(cache, cache.shape, u8, dev)
@@ -428,7 +434,7 @@ def _cache_index(p: CacheParams, X, Y, heads, cache, table, lens, ws, counts, ex
     if dev < 0:
         raise ValueError("the tensors must be on a CUDA device")
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)
+        stream = raw_stream(dev)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
     return table.data_ptr(), lens.data_ptr(), counts, exps, stream
@@ -484,28 +490,27 @@ def mita_cache_attention(p: CacheParams, Q, cache, table, lens, O, ws, counts=No
                 st))
 
 
-def _float_sums(p: CacheParams, t, what, dev):
-    import torch
-    s = (p.B, p.H_kv, p.max_pages * p.page)
-    if t.dtype is not torch.float32 or t.get_device() != dev or t.shape != s or not t.is_contiguous():
-        _refuse(t, s, torch.float32, dev, what)
-    return t.data_ptr()
-
-
 def mita_cache_weights(p: CacheParams, Q, cache, table, lens, lse, acc, ws, counts=None, exps=None, decay=1.0,
                        acc_out=None, stream=None):
     """Adds the attention weight that each cached token gets from the rows Q [B, H, T, d],
     whose log sums are lse [B, H, T], to decay times its sum in acc [B, H_kv, max_pages *
     page], into acc_out (acc itself if None). acc may be None with decay = 0."""
-    import torch
     tp, lp, cp, ep, st = _cache_index(p, Q, Q, p.H, cache, table, lens, ws, counts, exps, stream)
-    dev, s = cache.get_device(), (p.B, p.H, p.T)
-    if lse.dtype is not torch.float32 or lse.get_device() != dev or lse.shape != s or not lse.is_contiguous():
-        _refuse(lse, s, torch.float32, dev, "lse: ")
-    ap = None if acc is None else _float_sums(p, acc, "acc: ", dev)
-    if acc_out is None and acc is None:
+    _, _, _, f32, _, _, _, _, _, s, sums, _ = p._checks
+    dev = cache.get_device()
+    if lse.dtype is not f32 or lse.get_device() != dev or lse.shape != s or not lse.is_contiguous():
+        _refuse(lse, s, f32, dev, "lse: ")
+    ap = op = None
+    if acc is not None:
+        if acc.dtype is not f32 or acc.get_device() != dev or acc.shape != sums or not acc.is_contiguous():
+            _refuse(acc, sums, f32, dev, "acc: ")
+        ap = op = acc.data_ptr()
+    if acc_out is not None:
+        if acc_out.dtype is not f32 or acc_out.get_device() != dev or acc_out.shape != sums or not acc_out.is_contiguous():
+            _refuse(acc_out, sums, f32, dev, "acc_out: ")
+        op = acc_out.data_ptr()
+    elif acc is None:
         raise ValueError("without acc the sums need acc_out")
-    op = ap if acc_out is None else _float_sums(p, acc_out, "acc_out: ", dev)
     _on_device(cache, (_lib or lib()).mita_cache_weights,
                (p.ref, Q.data_ptr(), cache.data_ptr(), tp, lp, cp, ep, lse.data_ptr(), decay, ap, op, ws.data_ptr(),
                 ws.numel(), st))
@@ -530,40 +535,40 @@ def mita_cache_evict(p: CacheParams, cache, table, lens, keep, acc, ws, first=0,
     ``first``, the last ``recent`` and those with the largest sums in acc [B, H_kv, max_pages *
     page]. The new lengths go to len_out (lens itself if None), the sums to acc_out (acc
     itself if None), the place that each row had to src_out (int32 like acc, optional)."""
-    import torch
-    i32, u8, dev = torch.int32, torch.uint8, cache.get_device()
+    _, i32, u8, f32, _, _, st, sl, _, _, sums, raw_stream = p._checks
+    dev = cache.get_device()
     if cache.dtype is not u8 or not cache.is_contiguous():
         _refuse(cache, cache.shape, u8, dev)
     if cache.numel() < p.pool_bytes:
         raise ValueError("cache holds %d bytes, the pool needs %d" % (cache.numel(), p.pool_bytes))
     if ws.dtype is not u8 or ws.get_device() != dev or not ws.is_contiguous():
         _refuse(ws, ws.shape, u8, dev)
-    s = (p.B, p.max_pages)
-    if table.dtype is not i32 or table.get_device() != dev or table.shape != s or not table.is_contiguous():
-        _refuse(table, s, i32, dev)
+    if table.dtype is not i32 or table.get_device() != dev or table.shape != st or not table.is_contiguous():
+        _refuse(table, st, i32, dev)
     if len_out is None:
         len_out = lens
-    s = (p.B,)
     for t in (lens, keep, len_out):
-        if t.dtype is not i32 or t.get_device() != dev or t.shape != s or not t.is_contiguous():
-            _refuse(t, s, i32, dev)
+        if t.dtype is not i32 or t.get_device() != dev or t.shape != sl or not t.is_contiguous():
+            _refuse(t, sl, i32, dev)
     if dev < 0:
         raise ValueError("the tensors must be on a CUDA device")
-    ap = _float_sums(p, acc, "acc: ", dev)
-    op = ap if acc_out is None else _float_sums(p, acc_out, "acc_out: ", dev)
+    if acc_out is None:
+        acc_out = acc
+    for t, what in ((acc, "acc: "), (acc_out, "acc_out: ")):
+        if t.dtype is not f32 or t.get_device() != dev or t.shape != sums or not t.is_contiguous():
+            _refuse(t, sums, f32, dev, what)
     sp = None
     if src_out is not None:
-        s = (p.B, p.H_kv, p.max_pages * p.page)
-        if src_out.dtype is not i32 or src_out.get_device() != dev or src_out.shape != s or not src_out.is_contiguous():
-            _refuse(src_out, s, i32, dev, "src_out: ")
+        if src_out.dtype is not i32 or src_out.get_device() != dev or src_out.shape != sums or not src_out.is_contiguous():
+            _refuse(src_out, sums, i32, dev, "src_out: ")
         sp = src_out.data_ptr()
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)
+        stream = raw_stream(dev)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
     _on_device(cache, (_lib or lib()).mita_cache_evict,
-               (p.ref, cache.data_ptr(), table.data_ptr(), lens.data_ptr(), keep.data_ptr(), first, recent, ap,
-                len_out.data_ptr(), op, sp, ws.data_ptr(), ws.numel(), stream))
+               (p.ref, cache.data_ptr(), table.data_ptr(), lens.data_ptr(), keep.data_ptr(), first, recent, acc.data_ptr(),
+                len_out.data_ptr(), acc_out.data_ptr(), sp, ws.data_ptr(), ws.numel(), stream))
 
 
 def mita_rope_frequencies(rot, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, original=0.0, low=1.0, high=4.0) -> tuple:
