@@ -12,7 +12,7 @@
 // parts, one per warp; warps share nothing but the search for their place. A token's sum is
 // added in an order of its own, whatever the cut, so the same call gives the same bits.
 //
-// Measured, in a graph: one row over 2 x 16 heads of 32768 tokens 20.2 us (4.1 TB/s, 0.61 of the copy rate), 64 sequences
+// Measured, in a graph: one row over 2 x 16 heads of 32768 tokens 20.1 us (4.2 TB/s, 0.61 of the copy rate), 64 sequences
 // of 33 to 8191 tokens, four rows over 8 heads 40.7. About 4.5 us are the launch and the ends; further tokens
 // come at 0.75 of the copy rate, as calls do that only read the keys: they are 1152 bytes of each 2304.
 #include <algorithm>
@@ -131,7 +131,8 @@ template <typename T, int NR> constexpr int weigh_blocks() { return NR == 1 && s
 // the next step, two groups, is on its way without registers, and no warp waits for another. (Loads into registers two
 // steps ahead: 24.7 us for 2 x 16 heads of 32768 tokens, 20.2 so; copies two or three steps ahead 23.0 and more, with
 // fewer blocks 19.7.) Widening is exact (cache.cuh). Rows are scaled by a power of two that puts the largest entry in
-// [2^14, 2^15): bf16 rows are exact as halves down to 2^-31 of it; float32 rows are two halves, hi + lo, both in one sum.
+// [2^14, 2^15): bf16 rows are exact as halves down to 2^-31 of it; float32 rows are two halves, hi + lo, in sums of their own
+// (a sum is cut to 24 bits at every step; what the lower halves add should not be cut at the size of the whole).
 // A lane ends with two tokens of each group and two rows for each eight; four lanes share a token.
 //
 // FEW: with two rows, of the eight columns of the 8 side a row has four, each with the channels of every fourth block of
@@ -321,7 +322,7 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
                                 constexpr int HF = D / 64;  // blocks of a lane's channels
-                                float z[NR][HF][4];
+                                float z[NR][HF][4], zl[F ? NR : 1][HF][4];  // (lower halves in a sum of their own: sums are cut to 24 bits)
 #pragma unroll
                                 for (int wi = 0; wi < W; ++wi) {
                                     uint32_t k8[2][4];
@@ -336,14 +337,18 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
                                             for (int j = 0; j < NR; ++j) {
                                                 const int ks = 2 * wi + k2;
                                                 const uint2 q = rows_of(part, ks, j);
-                                                float* to = z[j][ks / 4];
-                                                if (ks % 4 == 0 && part == 0)
+                                                float* to = part ? zl[F ? j : 0][ks / 4] : z[j][ks / 4];
+                                                if (ks % 4 == 0)
                                                     mma_f16_first(to, k8[0][2 * k2], k8[1][2 * k2], k8[0][2 * k2 + 1],
                                                                   k8[1][2 * k2 + 1], q.x, q.y);
                                                 else
                                                     mma_f16(to, k8[0][2 * k2], k8[1][2 * k2], k8[0][2 * k2 + 1], k8[1][2 * k2 + 1],
                                                             q.x, q.y);
                                             }
+                                }
+                                if (F) {
+#pragma unroll
+                                    for (int i = 0; i < NR * HF * 4; ++i) (&z[0][0][0])[i] += (&zl[0][0][0])[F ? i : 0];
                                 }
                                 float s[2][2][HF];  // [token g, g + 8][column][block]
 #pragma unroll
@@ -394,7 +399,7 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
                                     s2[0][0] = __byte_perm(a0, a0, 0x1010);
                                     s2[1][0] = __byte_perm(a0, a0, 0x3232);
                                 }
-                                float z[NR][4];
+                                float z[NR][4], zl[F ? NR : 1][4];
 #pragma unroll
                                 for (int wi = 0; wi < W; ++wi) {
                                     uint32_t k8[2][4];
@@ -417,12 +422,19 @@ k_cache_weigh(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint8_t* 
                                                         q.x, q.y);
                                             if (F) {
                                                 const uint2 ql = rows_of(1, ks, j);
-                                                mma_f16(z[j], k8[0][2 * k2], k8[1][2 * k2], k8[0][2 * k2 + 1], k8[1][2 * k2 + 1],
-                                                        ql.x, ql.y);
+                                                if (ks == 0)
+                                                    mma_f16_first(zl[F ? j : 0], k8[0][0], k8[1][0], k8[0][1], k8[1][1], ql.x, ql.y);
+                                                else
+                                                    mma_f16(zl[F ? j : 0], k8[0][2 * k2], k8[1][2 * k2], k8[0][2 * k2 + 1],
+                                                            k8[1][2 * k2 + 1], ql.x, ql.y);
                                             }
                                         }
                                 }
                                 s2t[y][0] = s2t[y][1] = make_float2(0.0f, 0.0f);
+                                if (F) {
+#pragma unroll
+                                    for (int i = 0; i < NR * 4; ++i) (&z[0][0])[i] += (&zl[0][0])[F ? i : 0];
+                                }
 #pragma unroll
                                 for (int j = 0; j < NR; ++j) {
                                     float2 p0 = weight2(make_float2(z[j][0], z[j][1]), zf[j], lse[j]);
@@ -493,7 +505,8 @@ static cudaError_t weigh_t(const CacheArgs& a, const WeighArgs& w, unsigned flag
     constexpr int kMost = D == 64 ? 32 : sizeof(T) == 4 ? 8 : 16;
     if (rows > kMost) return launch_cache_weigh_tile(a, w, D, sizeof(T) == 4 ? 0 : 1, Q, cache, st);
     // (2 x 16 heads of 32768 tokens, one row each, with loads into registers: 24.7 us, and 26.1 in the form for eight rows; float32
-    // 29.1 and 32.2. Four rows in two tiles of two were 33, as each further step of the tensor cores takes its 17 clocks.)
+    // 29.1 and 32.2. Four rows in two tiles of two were 33, as each further step of the tensor cores takes its 17 clocks; with copies
+    // 23.6 against 22.8, and 64 sequences of 33 to 8191 tokens 56.6 against 40.3.)
     if (rows <= 2) return mma_t<T, D, 1, true>(a, w, Q, cache, st);
     if constexpr (kMost > 8) {
         if (rows > 16) return mma_t<T, D, kMost == 32 && sizeof(T) == 2 ? 4 : 2>(a, w, Q, cache, st);  // (float: two tiles of 16)

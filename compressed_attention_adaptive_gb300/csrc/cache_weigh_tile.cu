@@ -475,9 +475,9 @@ k_cache_weigh_tile(CacheArgs a, WeighArgs w, const T* __restrict__ Q, const uint
                         const uint32_t id = idesc_half(kTok, min(kCols, padded - ti * kCols), 0, 0);
                         if (elect_one()) {
 #pragma unroll
-                            for (int k = 0; k < (F ? 2 : 1) * KS; ++k)  // 16 channels each
+                            for (int k = 0; k < (F ? 2 : 1) * KS; ++k)  // 16 channels each; lower halves first: sums are cut to 24 bits
                                 tc::mma_bf16_ts(tmem + ss * kCols, tmem + kK + st * 64 + (k % KS) * 8,
-                                                tc::sdesc(sm + ti * kTile + (k / KS) * kHalf + (k % KS >> 2) * (kCols * 128) +
+                                                tc::sdesc(sm + ti * kTile + (F && k < KS) * kHalf + (k % KS >> 2) * (kCols * 128) +
                                                               (k & 3) * 32,
                                                           16, 1024),
                                                 id, k > 0);
