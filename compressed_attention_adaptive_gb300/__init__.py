@@ -10,7 +10,7 @@ entry points carry the names of the C ABI in ``include/mita.h``:
 key/value cache ``mita_cache_size``, ``mita_cache_workspace_size``,
 ``mita_cache_write``, ``mita_cache_read``, ``mita_cache_attention``,
 ``mita_cache_weights``, ``mita_cache_evict_workspace_size``,
-``mita_cache_evict``, and for rotary positions ``mita_rope_frequencies``,
+``mita_cache_evict``, ``mita_cache_evict_aged``, and for rotary positions ``mita_rope_frequencies``,
 ``mita_rope``, ``mita_rope_backward``.
 
 The library must be built first (``python -c "import __graft_entry__ as g;
@@ -215,11 +215,12 @@ def lib():
         L.mita_cache_evict_workspace_size.argtypes = [C]
         L.mita_cache_evict_workspace_size.restype = sz
         L.mita_cache_evict.argtypes = [C, vp, ip, ip, ip, ctypes.c_int, ctypes.c_int, fp, ip, fp, ip, vp, sz, vp]
+        L.mita_cache_evict_aged.argtypes = [C, vp, ip, ip, ip, ctypes.c_int, ctypes.c_int, fp, ip, ip, fp, ip, vp, sz, vp]
         R, dbl = ctypes.POINTER(_CRopeParams), ctypes.c_double
         L.mita_rope_frequencies.argtypes = [R, dbl, ctypes.c_int, dbl, dbl, dbl, dbl]
         for f in ("mita_rope", "mita_rope_backward"):
             getattr(L, f).argtypes = [R, vp, vp, vp, vp, vp, ip, ctypes.c_int64, vp]
-        for f in ("mita_cache_weights", "mita_cache_evict", "mita_rope_frequencies", "mita_rope",
+        for f in ("mita_cache_weights", "mita_cache_evict", "mita_cache_evict_aged", "mita_rope_frequencies", "mita_rope",
                   "mita_rope_backward"):
             getattr(L, f).restype = ctypes.c_int
         L.mita_launch_count.argtypes = []
@@ -530,11 +531,14 @@ def cache_evict_workspace(p: CacheParams, device="cuda"):
 
 
 def mita_cache_evict(p: CacheParams, cache, table, lens, keep, acc, ws, first=0, recent=0, len_out=None, acc_out=None,
-                     src_out=None, stream=None):
+                     src_out=None, stream=None, age=None):
     """Keeps keep[b] tokens of each sequence that has more, in each cache head the first
     ``first``, the last ``recent`` and those with the largest sums in acc [B, H_kv, max_pages *
     page]. The new lengths go to len_out (lens itself if None), the sums to acc_out (acc
-    itself if None), the place that each row had to src_out (int32 like acc, optional)."""
+    itself if None), the place that each row had to src_out (int32 like acc, optional).
+    ``recent`` counts places, which are in the order of age only until a sequence is first
+    cut; with age (int32 like acc, zeros when a sequence begins, kept by the calls in place)
+    it counts the newest tokens (``mita_cache_evict_aged``)."""
     _, i32, u8, f32, _, _, st, sl, _, _, sums, raw_stream = p._checks
     dev = cache.get_device()
     if cache.dtype is not u8 or not cache.is_contiguous():
@@ -562,13 +566,18 @@ def mita_cache_evict(p: CacheParams, cache, table, lens, keep, acc, ws, first=0,
         if src_out.dtype is not i32 or src_out.get_device() != dev or src_out.shape != sums or not src_out.is_contiguous():
             _refuse(src_out, sums, i32, dev, "src_out: ")
         sp = src_out.data_ptr()
+    if age is not None and (age.dtype is not i32 or age.get_device() != dev or age.shape != sums or not age.is_contiguous()):
+        _refuse(age, sums, i32, dev, "age: ")
     if stream is None:
         stream = raw_stream(dev)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    _on_device(cache, (_lib or lib()).mita_cache_evict,
-               (p.ref, cache.data_ptr(), table.data_ptr(), lens.data_ptr(), keep.data_ptr(), first, recent, acc.data_ptr(),
-                len_out.data_ptr(), acc_out.data_ptr(), sp, ws.data_ptr(), ws.numel(), stream))
+    args = (p.ref, cache.data_ptr(), table.data_ptr(), lens.data_ptr(), keep.data_ptr(), first, recent, acc.data_ptr())
+    outs = (len_out.data_ptr(), acc_out.data_ptr(), sp, ws.data_ptr(), ws.numel(), stream)
+    if age is None:
+        _on_device(cache, (_lib or lib()).mita_cache_evict, args + outs)
+    else:
+        _on_device(cache, (_lib or lib()).mita_cache_evict_aged, args + (age.data_ptr(),) + outs)
 
 
 def mita_rope_frequencies(rot, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, original=0.0, low=1.0, high=4.0) -> tuple:

@@ -393,6 +393,51 @@ static int* carve_evict(const mita_cache_params* p, void* ws, int** moves, size_
     return status;
 }
 
+// `age` may be null: `recent` is by place then.
+static mita_status run_evict(const mita_cache_params* p, void* cache, const int32_t* table, const int32_t* len,
+                             const int32_t* keep, int first, int recent, const float* acc, int32_t* age,
+                             int32_t* len_out, float* acc_out, int32_t* src_out, void* ws, size_t ws_bytes, void* stream) {
+    CacheArgs a;
+    CachePlan plan;
+    const mita_status st = resolve_cache(p, false, &a, &plan);
+    if (st) return st;
+    if (!cache || !aligned16(cache)) return fail(MITA_ERR_INVALID_ARG, "cache must be a 16-byte aligned device pointer");
+    if (!table || !len || !keep || !acc || !len_out || !acc_out ||
+        ((uintptr_t)table | (uintptr_t)len | (uintptr_t)keep | (uintptr_t)acc | (uintptr_t)len_out | (uintptr_t)acc_out |
+         (uintptr_t)src_out) % 4)
+        return fail(MITA_ERR_INVALID_ARG, "table, len, keep, acc, len_out and acc_out must be 4-byte aligned device pointers");
+    if (first < 0 || recent < 0) return fail(MITA_ERR_INVALID_ARG, "first and recent must be >= 0");
+    const size_t places = (size_t)p->max_pages * p->page, n = (size_t)p->B * p->H_kv * places * 4, nb = (size_t)p->B * 4;
+    const size_t pool = (size_t)p->n_pages * p->H_kv * a.pgroups * (18 * (size_t)p->d);
+    struct Range {
+        const void* p;
+        size_t n;
+    };
+    const Range ins[] = {{table, nb * p->max_pages}, {len, nb}, {keep, nb}, {acc, n}};
+    const Range outs[] = {{len_out, nb}, {acc_out, n}, {src_out, src_out ? n : 0}, {cache, pool}, {age, age ? n : 0}};
+    for (int i = 0; i < 5; ++i) {
+        if (!outs[i].p) continue;
+        for (const Range& x : ins)
+            if (!(i < 2 && x.p == outs[i].p && x.n == outs[i].n && (i == 0 ? x.p == len : x.p == acc)) &&
+                overlap(x.p, x.n, outs[i].p, outs[i].n))
+                return fail(MITA_ERR_INVALID_ARG, "outputs must not overlap inputs (but len_out may be len, and acc_out acc)");
+        for (int j = 0; j < i; ++j)
+            if (outs[j].p && overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n))
+                return fail(MITA_ERR_INVALID_ARG, "outputs must not overlap each other or the cache");
+    }
+    size_t need;
+    EvictArgs e{keep, first, recent, acc, acc_out, src_out, len_out, age, nullptr, (long long)places};
+    carve_evict(p, nullptr, &e.moves, &need);
+    if (!ws) return fail(MITA_ERR_WORKSPACE, "workspace is NULL");
+    if ((uintptr_t)ws % 256) return fail(MITA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    if (ws_bytes < need) return fail(MITA_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+    a.table = table; a.len = len;
+    a.status = carve_evict(p, ws, &e.moves, &need);
+    MITA_CUDA(launch_cache_evict(a, e, p->d, cache, (cudaStream_t)stream), "cache evict");
+    prof_mark((cudaStream_t)stream, "");
+    return MITA_OK;
+}
+
 // ----------------------------------------------------------------- rotation
 
 static mita_status check_rope(const mita_rope_params* p) {
@@ -871,45 +916,16 @@ mita_status mita_cache_evict(const mita_cache_params* p, void* cache, const int3
                              const int32_t* keep, int first, int recent, const float* acc, int32_t* len_out,
                              float* acc_out, int32_t* src_out, void* ws, size_t ws_bytes, void* stream) {
     g_last_error.clear();
-    CacheArgs a;
-    CachePlan plan;
-    const mita_status st = resolve_cache(p, false, &a, &plan);
-    if (st) return st;
-    if (!cache || !aligned16(cache)) return fail(MITA_ERR_INVALID_ARG, "cache must be a 16-byte aligned device pointer");
-    if (!table || !len || !keep || !acc || !len_out || !acc_out ||
-        ((uintptr_t)table | (uintptr_t)len | (uintptr_t)keep | (uintptr_t)acc | (uintptr_t)len_out | (uintptr_t)acc_out |
-         (uintptr_t)src_out) % 4)
-        return fail(MITA_ERR_INVALID_ARG, "table, len, keep, acc, len_out and acc_out must be 4-byte aligned device pointers");
-    if (first < 0 || recent < 0) return fail(MITA_ERR_INVALID_ARG, "first and recent must be >= 0");
-    const size_t places = (size_t)p->max_pages * p->page, n = (size_t)p->B * p->H_kv * places * 4, nb = (size_t)p->B * 4;
-    const size_t pool = (size_t)p->n_pages * p->H_kv * a.pgroups * (18 * (size_t)p->d);
-    struct Range {
-        const void* p;
-        size_t n;
-    };
-    const Range ins[] = {{table, nb * p->max_pages}, {len, nb}, {keep, nb}, {acc, n}};
-    const Range outs[] = {{len_out, nb}, {acc_out, n}, {src_out, src_out ? n : 0}, {cache, pool}};
-    for (int i = 0; i < 4; ++i) {
-        if (!outs[i].p) continue;
-        for (const Range& x : ins)
-            if (!(i < 2 && x.p == outs[i].p && x.n == outs[i].n && (i == 0 ? x.p == len : x.p == acc)) &&
-                overlap(x.p, x.n, outs[i].p, outs[i].n))
-                return fail(MITA_ERR_INVALID_ARG, "outputs must not overlap inputs (but len_out may be len, and acc_out acc)");
-        for (int j = 0; j < i; ++j)
-            if (outs[j].p && overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n))
-                return fail(MITA_ERR_INVALID_ARG, "outputs must not overlap each other or the cache");
-    }
-    size_t need;
-    EvictArgs e{keep, first, recent, acc, acc_out, src_out, len_out, nullptr, (long long)places};
-    carve_evict(p, nullptr, &e.moves, &need);
-    if (!ws) return fail(MITA_ERR_WORKSPACE, "workspace is NULL");
-    if ((uintptr_t)ws % 256) return fail(MITA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
-    if (ws_bytes < need) return fail(MITA_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, need);
-    a.table = table; a.len = len;
-    a.status = carve_evict(p, ws, &e.moves, &need);
-    MITA_CUDA(launch_cache_evict(a, e, p->d, cache, (cudaStream_t)stream), "cache evict");
-    prof_mark((cudaStream_t)stream, "");
-    return MITA_OK;
+    return run_evict(p, cache, table, len, keep, first, recent, acc, nullptr, len_out, acc_out, src_out, ws, ws_bytes, stream);
+}
+
+mita_status mita_cache_evict_aged(const mita_cache_params* p, void* cache, const int32_t* table, const int32_t* len,
+                                  const int32_t* keep, int first, int recent, const float* acc, int32_t* age,
+                                  int32_t* len_out, float* acc_out, int32_t* src_out, void* ws, size_t ws_bytes,
+                                  void* stream) {
+    g_last_error.clear();
+    if (!age || (uintptr_t)age % 4) return fail(MITA_ERR_INVALID_ARG, "age must be a 4-byte aligned device pointer");
+    return run_evict(p, cache, table, len, keep, first, recent, acc, age, len_out, acc_out, src_out, ws, ws_bytes, stream);
 }
 
 mita_status mita_rope_frequencies(mita_rope_params* p, double base, int scaling, double factor, double original,

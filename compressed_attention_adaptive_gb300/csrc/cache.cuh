@@ -99,6 +99,7 @@ struct EvictArgs {
     const float* acc;
     float* acc_out;  // may be acc
     int *src, *len_out;
+    int* age;       // or null: recent tokens are the last places
     int* moves;     // [B * Hkv][2 half]: places that are freed, then places that move there
     long long cap;  // places of a sequence
 };

@@ -8,6 +8,12 @@
 // length then go to the freed places before it, i-th to i-th: what is read is behind the new length and
 // what is written before it, so rows move in any order and at once.
 //
+// Moves put places out of the order of age, so from a sequence's second eviction on its newest tokens are not its last places.
+// AGED: age[j] is how much older the token at place j is than its place says (an unmoved token at place j - age[j]
+// would be as old; negative: younger). The newest have the largest key of all, the rest is the same. A token
+// that stays has come n - keep places nearer to the sequence's beginning; one that moves takes its place's age along; places from
+// keep on hold 0 again, for the tokens that will be appended there.
+//
 // Work split. A row of sums is shared by a cluster of C blocks, each with its run of places: it holds their
 // keys in shared memory (they are read from memory once, if they fit), counts digits there, and
 // adds up the cluster's counts through distributed shared memory, one cluster barrier per
@@ -18,6 +24,8 @@
 // are the digits' and the list's barriers (a cluster's takes 1500), 5000 the loads, 12,000 the moves.
 // Measured, in a graph: 128 rows of 2112 cut to 2048 11.0 us, 144 of 700 to 9001 cut to 1500 22.7, 32 of 32768 cut
 // to 4096 25.1. A thread for each block of a row that moves, which looked its places up itself: 13.2, 26.4 and 31.0.
+// With ages, 4 more bytes read and written a place, calls back to back on warm caches take 11.3, 23.0 and 26.8 us for these where
+// calls without take 8.9, 19.9 and 22.0.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -47,6 +55,10 @@ __device__ __forceinline__ uint32_t first_digit(uint32_t key) {
 
 // Larger sums have larger keys; NaN the largest.
 __device__ __forceinline__ uint32_t sum_key(float x) { return x != x ? 0xffffffffu : order_key(x); }
+// AGED: the newest tokens' key, above all of these (order_key's largest number is infinity's, 0xff800000).
+constexpr uint32_t kNewest = 0xffffffffu;
+// Ages stop here: a token that far back is old for every window, which a sequence of 2^30 places is at most.
+constexpr long long kMaxAge = 1 << 30;
 
 struct Select {
     alignas(16) int hist[2][kBins];
@@ -99,7 +111,7 @@ __device__ __forceinline__ int reach(int count, int left, int lane, int* before)
 
 }  // namespace
 
-template <int D, int C>
+template <int D, int C, bool AGED>
 __global__ void __launch_bounds__(kThreads, 2) k_cache_evict(CacheArgs a, EvictArgs e, uint8_t* __restrict__ cache, int room) {
     using L = Grp<D>;
     extern __shared__ __align__(16) uint32_t keys[];  // [room]
@@ -121,25 +133,44 @@ __global__ void __launch_bounds__(kThreads, 2) k_cache_evict(CacheArgs a, EvictA
         return;
     }
     // those between: places [m0, m1), of which K stay, the ones with a rank of at least `bound`
-    const int m0 = e.first, m1 = n - e.recent, K = keep - e.first - e.recent;
+    const int m0 = e.first, m1 = AGED ? n : n - e.recent, K = keep - e.first - (AGED ? 0 : e.recent);
+    int* age = AGED ? e.age + row : nullptr;
+    // The key of place j, whose token's sum is x.
+    auto key_of = [&](int j, float x, int a) {
+        const uint32_t key = sum_key(x);
+        return !AGED ? key : a <= j - (n - e.recent) ? kNewest : min(key, kNewest - 1);
+    };
+    // A token's age after the call, at place `to`.
+    auto aged = [&](int to, int from, int a) {
+        return (int)min(max((long long)to - from + a + (n - keep), -kMaxAge), kMaxAge);
+    };
     const bool held = run <= room;
     for (int i = threadIdx.x; i < kBins; i += kThreads) s.hist[0][i] = 0;
     if (threadIdx.x == 0) s.found = 0;
     __syncthreads();
     const int places = p1 - p0;
-    const bool wide = ((uintptr_t)(acc + p0) & 15) == 0;
+    const bool wide = (((uintptr_t)(acc + p0) | (uintptr_t)(AGED ? age + p0 : nullptr)) & 15) == 0;
     // the keys of places p0 + x to p0 + x + 3 (x a multiple of four; 0 behind the block's places)
     auto load4 = [&](int x) {
         float4 v = make_float4(0, 0, 0, 0);
+        int4 a = make_int4(0, 0, 0, 0);
         if (wide && x + 3 < places) {
             v = *reinterpret_cast<const float4*>(acc + p0 + x);
+            if (AGED) a = *reinterpret_cast<const int4*>(age + p0 + x);
         } else {
             if (x < places) v.x = acc[p0 + x];
             if (x + 1 < places) v.y = acc[p0 + x + 1];
             if (x + 2 < places) v.z = acc[p0 + x + 2];
             if (x + 3 < places) v.w = acc[p0 + x + 3];
+            if (AGED) {
+                if (x < places) a.x = age[p0 + x];
+                if (x + 1 < places) a.y = age[p0 + x + 1];
+                if (x + 2 < places) a.z = age[p0 + x + 2];
+                if (x + 3 < places) a.w = age[p0 + x + 3];
+            }
         }
-        return make_uint4(sum_key(v.x), sum_key(v.y), sum_key(v.z), sum_key(v.w));
+        const int j = p0 + x;
+        return make_uint4(key_of(j, v.x, a.x), key_of(j + 1, v.y, a.y), key_of(j + 2, v.z, a.z), key_of(j + 3, v.w, a.w));
     };
     auto keys4 = [&](int x) { return held ? *reinterpret_cast<const uint4*>(keys + x) : load4(x); };
     {
@@ -326,8 +357,28 @@ __global__ void __launch_bounds__(kThreads, 2) k_cache_evict(CacheArgs a, EvictA
                 ++at;
             }
     }
-    // Rows that stay where they are, by the whole cluster: those places are its first blocks'.
-    if (e.src || e.acc_out != e.acc) {
+    // Rows that stay where they are, by the whole cluster: those places are its first blocks'. (AGED: each block its own
+    // places, since ages change where they are and another block's keys may come from them.)
+    if (AGED) {
+        __syncthreads();  // the block has its list, and looks at no age again but at the thread's own places
+        for (int x = 4 * threadIdx.x; x < places; x += 4 * kThreads) {
+            const uint4 k = keys4(x);
+            const uint32_t four[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = p0 + x + i;
+                if (j >= p1) continue;
+                const bool st = stays(j, four[i]);
+                if (j >= keep) {
+                    if (!st) age[j] = 0;
+                } else if (st) {
+                    if (e.acc_out != e.acc) e.acc_out[row + j] = acc[j];
+                    if (e.src) e.src[row + j] = j;
+                    age[j] = aged(j, j, age[j]);
+                }
+            }
+        }
+    } else if (e.src || e.acc_out != e.acc) {
 #pragma unroll 4
         for (int j = rank * kThreads + threadIdx.x; j < keep; j += C * kThreads) {
             const float x = acc[j];
@@ -356,6 +407,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_cache_evict(CacheArgs a, EvictA
                 gf = cache_group(a, b, h, from / kGroup);
                 e.acc_out[row + to] = acc[from];
                 if (e.src) e.src[row + to] = from;
+                if (AGED) {
+                    age[to] = aged(to, from, age[from]);
+                    age[from] = 0;
+                }
             }
         }
         if (gt < 0 || gf < 0) gt = -1;
@@ -414,11 +469,11 @@ __global__ void __launch_bounds__(256) k_cache_evict_end(CacheArgs a, EvictArgs 
     if (threadIdx.x == 0) *a.status = bad ? kStBounds : kStOk;
 }
 
-template <int D, int C>
+template <int D, int C, bool AGED>
 static cudaError_t evict_c(const CacheArgs& a, const EvictArgs& e, uint8_t* cache, cudaStream_t st) {
     const int room = (int)std::min<long long>(kMaxKeys, ((e.cap + C - 1) / C + 3) & ~3LL);
     static std::atomic<unsigned long long> done{0};
-    cudaError_t err = set_smem_once((const void*)k_cache_evict<D, C>, kMaxKeys * 4, &done);
+    cudaError_t err = set_smem_once((const void*)k_cache_evict<D, C, AGED>, kMaxKeys * 4, &done);
     if (err != cudaSuccess) return err;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
@@ -431,7 +486,7 @@ static cudaError_t evict_c(const CacheArgs& a, const EvictArgs& e, uint8_t* cach
     c.stream = st;
     c.attrs = &at;
     c.numAttrs = C > 1;
-    err = cudaLaunchKernelEx(&c, k_cache_evict<D, C>, a, e, cache, room);
+    err = cudaLaunchKernelEx(&c, k_cache_evict<D, C, AGED>, a, e, cache, room);
     if (err != cudaSuccess) return err;
     count_launch();
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -445,22 +500,24 @@ static cudaError_t evict_c(const CacheArgs& a, const EvictArgs& e, uint8_t* cach
     return err;
 }
 
-template <int D> static cudaError_t evict_t(const CacheArgs& a, const EvictArgs& e, uint8_t* cache, cudaStream_t st) {
+template <int D, bool AGED> static cudaError_t evict_t(const CacheArgs& a, const EvictArgs& e, uint8_t* cache, cudaStream_t st) {
     // Blocks of a row: more while they have many places each and two of them for each SM hold all
     // rows at once. (32 rows of 32768 places in 2, 4 and 8 blocks: 49, 30 and 26 us; 144 rows of up to 9001 in
     // 1, 2 and 4: 24.1, 24.3 and 31.)
     const long long rows = (long long)a.B * a.Hkv;
     int c = 1;
     while (c < 8 && e.cap > 4096LL * c && rows * c <= num_sms()) c *= 2;
-    return c == 1   ? evict_c<D, 1>(a, e, cache, st)
-           : c == 2 ? evict_c<D, 2>(a, e, cache, st)
-           : c == 4 ? evict_c<D, 4>(a, e, cache, st)
-                    : evict_c<D, 8>(a, e, cache, st);
+    return c == 1   ? evict_c<D, 1, AGED>(a, e, cache, st)
+           : c == 2 ? evict_c<D, 2, AGED>(a, e, cache, st)
+           : c == 4 ? evict_c<D, 4, AGED>(a, e, cache, st)
+                    : evict_c<D, 8, AGED>(a, e, cache, st);
 }
 
 cudaError_t launch_cache_evict(const CacheArgs& a, const EvictArgs& e, int d, void* cache, cudaStream_t st) {
     prof_mark(st, "cache_evict");
-    return d == 64 ? evict_t<64>(a, e, (uint8_t*)cache, st) : evict_t<128>(a, e, (uint8_t*)cache, st);
+    uint8_t* c = (uint8_t*)cache;
+    if (e.age) return d == 64 ? evict_t<64, true>(a, e, c, st) : evict_t<128, true>(a, e, c, st);
+    return d == 64 ? evict_t<64, false>(a, e, c, st) : evict_t<128, false>(a, e, c, st);
 }
 
 }  // namespace mita

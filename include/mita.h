@@ -330,7 +330,8 @@ mita_status mita_cache_attention(const mita_cache_params* p, const void* Q, cons
  * Not part of the method (the summaries have no counterpart): keeps the cache of a
  * long generation within a budget. After a call's rows have attended,
  * mita_cache_weights() adds the attention weight that each cached token got from
- * them to its sum; mita_cache_evict() keeps the tokens of each cache head with the
+ * them to its sum; mita_cache_evict() and, for sequences that are cut again and again,
+ * mita_cache_evict_aged() keep the tokens of each cache head with the
  * largest sums. Sums are float32 [B][H_kv][max_pages * page], by place.
  *
  * Weights. For each token j < len[b] and cache head h
@@ -355,13 +356,15 @@ mita_status mita_cache_weights(const mita_cache_params* p, const void* Q, const 
                                void* stream);
 
 /* Eviction. keep int32 [B] (device): the tokens that sequence b keeps. A sequence with
- * len[b] <= keep[b] stays as it is. Of the others each cache head keeps its first `first` and
- * its last `recent` tokens and, of those between, the keep[b] - first - recent with the largest
+ * len[b] <= keep[b] stays as it is. Of the others each cache head keeps the tokens at its first `first` and
+ * its last `recent` places and, of those between, the keep[b] - first - recent with the largest
  * acc (ties to the lower place; NaN counts as the largest, -0 as 0). The kept rows at places
  * j >= keep[b] move, in ascending order, to the places that were freed below keep[b], in
  * ascending order; the other kept rows stay where they are. Keys and values move as they are
  * held, without another rounding. (Places are not positions, then: a caller that rotates by
- * position counts positions itself. Heads of one sequence keep different tokens.)
+ * position counts positions itself. Heads of one sequence keep different tokens. The last places
+ * have the newest tokens the first time that a sequence is cut, and not from then on: calls that cut
+ * sequences again and again take mita_cache_evict_aged().)
  *   len_out  int32 [B]: min(len[b], keep[b]). May be len.
  *   acc_out  float32 like acc: the sums of the rows now at j < len_out[b]. May be acc.
  *   src_out  int32 [B][H_kv][max_pages * page] or NULL: the place that the row now at
@@ -371,11 +374,26 @@ mita_status mita_cache_weights(const mita_cache_params* p, const void* Q, const 
  * keep[b] of a sequence that is cut) must not be shared with another sequence.
  * Uses B, H_kv, d, page, n_pages and max_pages of p. first, recent >= 0. Out of range: as
  * above, and a budget keep[b] below first + recent; a sequence whose length or budget is out of
- * range is left as it was, with len_out[b] = len[b]. */
+ * range is left as it was, with len_out[b] = len[b].
+ *
+ * mita_cache_evict_aged() does the same with `recent` by age: each cache head keeps the tokens at its
+ * first `first` places (they never move, so these are the sequence's first tokens if no earlier call
+ * had a smaller `first`), of the others the `recent` newest that it still has, and of the rest those with
+ * the largest acc, keep[b] in all. What a head has lost of the newest, to a call with a smaller `recent`,
+ * others with the largest acc replace. age int32 [B][H_kv][max_pages * page], by place, changed in place, tells how
+ * much older a token is than its place says: the token at place j is as old as an unmoved one at place
+ * j - age[b][h][j] would be (at most 2^30 either way). Zeros are a sequence in order. The caller sets a
+ * sequence's numbers to 0 when it begins and otherwise leaves them to the call: rows appended at len_out[b] and
+ * behind find zeros there, and appended rows that are taken back again leave zeros (a len that falls
+ * below what the last eviction left has no meaning here). age must not overlap anything. */
 size_t mita_cache_evict_workspace_size(const mita_cache_params* p);
 mita_status mita_cache_evict(const mita_cache_params* p, void* cache, const int32_t* table, const int32_t* len,
                              const int32_t* keep, int first, int recent, const float* acc, int32_t* len_out,
                              float* acc_out, int32_t* src_out, void* ws, size_t ws_bytes, void* stream);
+mita_status mita_cache_evict_aged(const mita_cache_params* p, void* cache, const int32_t* table, const int32_t* len,
+                                  const int32_t* keep, int first, int recent, const float* acc, int32_t* age,
+                                  int32_t* len_out, float* acc_out, int32_t* src_out, void* ws, size_t ws_bytes,
+                                  void* stream);
 
 /* ---- rotary positions ----------------------------------------------------------
  * Not part of the method (the summaries have no counterpart): turns the rows of Q and K by

@@ -80,3 +80,20 @@ def evict(acc, keep, first, recent):
     src = np.arange(keep)
     src[free] = move
     return src
+
+
+def evict_aged(acc, born, keep, first, recent, newest):
+    """The same with `recent` by age: born[j] is the number that the token at place j had when it
+    came, of `newest` so far. Stay: the places below first, of the others what came last of the
+    `recent` newest of all, then the largest sums."""
+    n = len(acc)
+    if n <= keep:
+        return np.arange(n)
+    stay = set(range(first))
+    late = [j for j in range(first, n) if born[j] >= newest - recent]
+    value = lambda j: np.inf if np.isnan(acc[j]) else float(acc[j]) + 0.0
+    rest = sorted(set(range(first, n)) - set(late), key=lambda j: (not np.isnan(acc[j]), -value(j), j))
+    stay |= set(late) | set(rest[:keep - first - len(late)])
+    src = np.arange(keep)
+    src[[j for j in range(keep) if j not in stay]] = sorted(j for j in stay if j >= keep)
+    return src
