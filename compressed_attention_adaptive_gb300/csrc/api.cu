@@ -431,6 +431,10 @@ static mita_status run_evict(const mita_cache_params* p, void* cache, const int3
     if (!ws) return fail(MITA_ERR_WORKSPACE, "workspace is NULL");
     if ((uintptr_t)ws % 256) return fail(MITA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
     if (ws_bytes < need) return fail(MITA_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+    bool over = false;
+    for (const Range& x : ins) over |= overlap(x.p, x.n, ws, need);
+    for (const Range& x : outs) over |= x.p && overlap(x.p, x.n, ws, need);
+    if (over) return fail(MITA_ERR_INVALID_ARG, "no other array must overlap the workspace");
     a.table = table; a.len = len;
     a.status = carve_evict(p, ws, &e.moves, &need);
     MITA_CUDA(launch_cache_evict(a, e, p->d, cache, (cudaStream_t)stream), "cache evict");

@@ -370,7 +370,7 @@ mita_status mita_cache_weights(const mita_cache_params* p, const void* Q, const 
  *   src_out  int32 [B][H_kv][max_pages * page] or NULL: the place that the row now at
  *            j < len_out[b] had, to carry anything else along.
  * Places from len_out[b] on keep what they held in acc_out and src_out, and in the cache. Other
- * overlaps of outputs with anything are refused. Pages that the call writes (those of places below
+ * overlaps of outputs or of the workspace with anything are refused. Pages that the call writes (those of places below
  * keep[b] of a sequence that is cut) must not be shared with another sequence.
  * Uses B, H_kv, d, page, n_pages and max_pages of p. first, recent >= 0. Out of range: as
  * above, and a budget keep[b] below first + recent; a sequence whose length or budget is out of

@@ -77,3 +77,23 @@ def test_the_newest_stay_over_many_evictions(keep, first, recent, over):
             assert len(set(born.tolist())) == keep and born[:first].tolist() == list(range(first))
         left[by_age] = int((born >= newest - recent).sum())
     assert left[True] == recent and (left[False] < recent or over >= recent)
+
+
+def test_workspace_over_another_array(lib):
+    """The list of moves and the status word are written to the workspace while the arrays are in use."""
+    p = _p()
+    need = mita.mita_cache_evict_workspace_size(p)
+    x = lambda a: None if a is None else ctypes.c_void_p(a)
+
+    def plain(cache=2 * A, table=3 * A, lens=4 * A, keep=5 * A, acc=6 * A, len_out=7 * A, out=8 * A, src=9 * A):
+        return lib.mita_cache_evict(p.ref, *map(x, (cache, table, lens, keep)), 0, 0, *map(x, (acc, len_out, out, src, 10 * A)),
+                                    need, None)
+
+    for name in ("cache", "table", "lens", "keep", "acc", "len_out", "out", "src"):
+        for at in (10 * A, 10 * A + 1024, 10 * A + need - 16):
+            assert plain(**{name: at}) == 1, (name, at)
+            assert b"workspace" in lib.mita_last_error()
+            assert _evict(lib, p, **{name: at}, n=need) == 1, (name, at)
+    for at in (10 * A, 10 * A + need - 16):
+        assert _evict(lib, p, age=at, n=need) == 1
+    assert plain(acc=10 * A + 1024, out=10 * A + 1024) == 1  # in place
