@@ -417,9 +417,9 @@ static mita_status run_evict(const mita_cache_params* p, void* cache, const int3
     const Range outs[] = {{len_out, nb}, {acc_out, n}, {src_out, src_out ? n : 0}, {cache, pool}, {age, age ? n : 0}};
     for (int i = 0; i < 5; ++i) {
         if (!outs[i].p) continue;
-        for (const Range& x : ins)
-            if (!(i < 2 && x.p == outs[i].p && x.n == outs[i].n && (i == 0 ? x.p == len : x.p == acc)) &&
-                overlap(x.p, x.n, outs[i].p, outs[i].n))
+        for (int j = 0; j < 4; ++j)
+            if (!(ins[j].p == outs[i].p && ((i == 0 && j == 1) || (i == 1 && j == 3))) &&
+                overlap(ins[j].p, ins[j].n, outs[i].p, outs[i].n))
                 return fail(MITA_ERR_INVALID_ARG, "outputs must not overlap inputs (but len_out may be len, and acc_out acc)");
         for (int j = 0; j < i; ++j)
             if (outs[j].p && overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n))

@@ -97,3 +97,11 @@ def test_workspace_over_another_array(lib):
     for at in (10 * A, 10 * A + need - 16):
         assert _evict(lib, p, age=at, n=need) == 1
     assert plain(acc=10 * A + 1024, out=10 * A + 1024) == 1  # in place
+
+
+def test_table_that_is_the_lengths(lib):
+    """len_out may be len, which a table of one column that starts there too does not become."""
+    p = _p(max_pages=1)
+    for kw in (dict(table=4 * A, lens=4 * A, len_out=4 * A), dict(keep=4 * A, lens=4 * A, len_out=4 * A)):
+        assert _evict(lib, p, n=0, **kw) == 1, kw
+    assert _evict(lib, p, n=0, lens=4 * A, len_out=4 * A) == 3
