@@ -461,6 +461,18 @@ static mita_status check_rope(const mita_rope_params* p) {
     return MITA_OK;
 }
 
+// f / (2 pi) without its whole turns, in 2^-64 turns: off by at most 2^-63 of a turn and 2^-104 of f / (2 pi). (One
+// double for the quotient would leave 2^-52 of it, which a position multiplies.)
+static unsigned long long turn_fraction(double f) {
+    constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;  // 1 / (2 pi)
+    const double x = fabs(f);
+    volatile double product = x * kHi;  // rounded here, whatever products and sums the compiler joins
+    const double hi = product, lo = fma(x, kHi, -hi) + x * kLo;
+    auto part = [](double t) { return 2 * (unsigned long long)(long long)((t - rint(t)) * 9223372036854775808.0); };
+    const unsigned long long turns = part(hi) + part(lo);
+    return f < 0.0 ? 0 - turns : turns;
+}
+
 // Rows [B, H, T, d] in memory.
 struct Rows {
     const void* p;
@@ -543,11 +555,7 @@ static mita_status run_rope(const mita_rope_params* p, bool back, const void* Q,
             return fail(MITA_ERR_INVALID_ARG, "an output must not overlap pos");
     }
     if (n == 2 && !disjoint(out[0], out[1])) return fail(MITA_ERR_INVALID_ARG, "outputs must not overlap");
-    for (int i = 0; i < p->rot / 2; ++i) {
-        const double turns = p->freqs[i] * 0.15915494309189535;  // 1 / (2 pi)
-        const double part = turns - floor(turns);  // (1 for a tiny negative one)
-        a.turns[i] = part < 1.0 ? (unsigned long long)(part * 18446744073709551616.0) : 0;
-    }
+    for (int i = 0; i < p->rot / 2; ++i) a.turns[i] = turn_fraction(p->freqs[i]);
     MITA_CUDA(launch_rope(a, p->dtype, p->flags & MITA_FLAG_INTERLEAVED, (cudaStream_t)stream), "rope");
     prof_mark((cudaStream_t)stream, "");
     return MITA_OK;

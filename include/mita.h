@@ -403,8 +403,8 @@ mita_status mita_cache_evict_aged(const mita_cache_params* p, void* cache, const
  *   y0 = gain (x0 cos a - x1 sin a),  y1 = gain (x0 sin a + x1 cos a);
  * the other channels are copied. Pair i is channels i and i + rot / 2, or with
  * MITA_FLAG_INTERLEAVED 2 i and 2 i + 1. Angles are reduced exactly in 64-bit integers (a
- * position times a frequency in turns), so far positions lose nothing: cos and sin are off by
- * about 2^-23. Products and sums are fp32, rounded once to `dtype`. */
+ * position times a frequency in turns, which is off by at most 2^-63 of a turn and 2^-104 of itself), so far
+ * positions lose nothing: cos and sin are off by about 2^-23 at every position, for frequencies up to 2^40. Products and sums are fp32, rounded once to `dtype`. */
 #define MITA_ROPE_PAIRS 128
 typedef struct {
     int B, H, H_kv;   /* sequences, query heads, key heads (H_kv = 0: Q alone)     */
