@@ -32,6 +32,7 @@ F32, BF16 = 0, 1
 FLAG_NO_SHARED, FLAG_SIMT, FLAG_CAUSAL, FLAG_INTERLEAVED = 1, 2, 4, 8
 ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_PARTS = 0, 1, 2, 3
 ROPE_PAIRS = 128
+_INT = 1 << 31
 TESTFLAG_STALL_PRODUCER = 1 << 31  # fault test only (see include/mita.h)
 STATUS = {0: "MITA_OK", 1: "MITA_ERR_INVALID_ARG", 2: "MITA_ERR_UNSUPPORTED", 3: "MITA_ERR_WORKSPACE",
           4: "MITA_ERR_CUDA", 5: "MITA_ERR_TIMEOUT", 6: "MITA_ERR_BOUNDS"}
@@ -541,6 +542,8 @@ def mita_cache_evict(p: CacheParams, cache, table, lens, keep, acc, ws, first=0,
     it counts the newest tokens (``mita_cache_evict_aged``)."""
     _, i32, u8, f32, _, _, st, sl, _, _, sums, raw_stream = p._checks
     dev = cache.get_device()
+    if not -_INT <= first < _INT or not -_INT <= recent < _INT:  # (ctypes would take their lower bits)
+        raise ValueError("first and recent must be 32-bit numbers")
     if cache.dtype is not u8 or not cache.is_contiguous():
         _refuse(cache, cache.shape, u8, dev)
     if cache.numel() < p.pool_bytes:
@@ -582,6 +585,8 @@ def mita_cache_evict(p: CacheParams, cache, table, lens, keep, acc, ws, first=0,
 
 def mita_rope_frequencies(rot, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, original=0.0, low=1.0, high=4.0) -> tuple:
     """Radians per position of the rot / 2 pairs (see include/mita.h for the scaled forms)."""
+    if not -_INT <= rot < _INT or not -_INT <= scaling < _INT:  # (ctypes would take their lower bits)
+        raise ValueError("rot and scaling must be numbers of 32 bits")
     c = _CRopeParams(rot=rot)
     _check(lib().mita_rope_frequencies(ctypes.byref(c), base, scaling, factor, original, low, high))
     return tuple(c.freqs[:rot // 2])

@@ -105,3 +105,16 @@ def test_table_that_is_the_lengths(lib):
     for kw in (dict(table=4 * A, lens=4 * A, len_out=4 * A), dict(keep=4 * A, lens=4 * A, len_out=4 * A)):
         assert _evict(lib, p, n=0, **kw) == 1, kw
     assert _evict(lib, p, n=0, lens=4 * A, len_out=4 * A) == 3
+
+
+def test_numbers_beyond_32_bits(lib):
+    """They would arrive as what their lower 32 bits say."""
+    p = _p()
+    cache, lens = torch.zeros(p.pool_bytes, dtype=torch.uint8), torch.zeros(2, dtype=torch.int32)
+    table, acc, ws = torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, 2, 256), torch.zeros(4096, dtype=torch.uint8)
+    for kw in (dict(first=2 ** 32), dict(recent=2 ** 32 + 5), dict(first=2 ** 31), dict(recent=-2 ** 31 - 1)):
+        with pytest.raises(ValueError, match="first and recent"):
+            mita.mita_cache_evict(p, cache, table, lens, lens.clone(), acc, ws, **kw)
+    for args, kw in (((2 ** 32 + 64,), {}), ((64,), dict(scaling=2 ** 32, factor=2.0))):
+        with pytest.raises(ValueError, match="32 bits"):
+            mita.mita_rope_frequencies(*args, **kw)
