@@ -93,6 +93,7 @@ def test_sums_beside_bad_lengths_and_exponents(dtype, H, T, simt):
             with pytest.raises(mita.MitaError) as e:
                 mita.mita_device_status(ws)
             assert e.value.status == status
+            del e  # (holds this frame)
         mita.mita_device_status(ws)
         return out
 
