@@ -20,8 +20,10 @@
 // digit. The same blocks then number the freed places and the rows that move, and move them.
 //
 // What it reads and writes is 4 bytes a sum, and a row that moves 2 x 288 bytes in sectors of 32 (144 held), which for long
-// rows is a fifth of the time; what bounds it is the chain of steps: for 32 rows of 32768, 20,000 of 40,000 clocks
-// are the digits' and the list's barriers (a cluster's takes 1500), 5000 the loads, 12,000 the moves.
+// rows is a fifth of the time; what bounds it is the chain of steps. 32 rows of 32768, of a block's 40,000 to 42,500 clocks: loads
+// and the first digit's counts 4500 to 5600; four cluster barriers, 1200 to 1800 each, the last up to 3600; the digit
+// 1700; the last few gathered and compared 6700; what moves counted 2300 and listed 4500; rows that stay 1500; moves 10,000 to
+// 12,000.
 // Measured, in a graph: 128 rows of 2112 cut to 2048 11.0 us, 144 of 700 to 9001 cut to 1500 22.7, 32 of 32768 cut
 // to 4096 25.1. A thread for each block of a row that moves, which looked its places up itself: 13.2, 26.4 and 31.0.
 // With ages, 4 more bytes read and written a place, calls back to back on warm caches take 11.3, 23.0 and 26.8 us for these where
@@ -503,7 +505,9 @@ static cudaError_t evict_c(const CacheArgs& a, const EvictArgs& e, uint8_t* cach
 template <int D, bool AGED> static cudaError_t evict_t(const CacheArgs& a, const EvictArgs& e, uint8_t* cache, cudaStream_t st) {
     // Blocks of a row: more while they have many places each and two of them for each SM hold all
     // rows at once. (32 rows of 32768 places in 2, 4 and 8 blocks: 49, 30 and 26 us; 144 rows of up to 9001 in
-    // 1, 2 and 4: 24.1, 24.3 and 31.)
+    // 1, 2 and 4: 24.1, 24.3 and 31.) Lengths are on the device, so the blocks and their shared memory go by the table's
+    // width: where it is far above the lengths that costs (128 rows of 2112 with room for 131,072 places 18.4 us instead of
+    // 8.9, 144 of 700 to 9001 with room for 98,304 28.9 instead of 19.9).
     const long long rows = (long long)a.B * a.Hkv;
     int c = 1;
     while (c < 8 && e.cap > 4096LL * c && rows * c <= num_sms()) c *= 2;

@@ -13,8 +13,9 @@
 // added in an order of its own, whatever the cut, so the same call gives the same bits.
 //
 // Measured, in a graph: one row over 2 x 16 heads of 32768 tokens 20.1 us (4.2 TB/s, 0.61 of the copy rate), 64 sequences
-// of 33 to 8191 tokens, four rows over 8 heads 40.7. About 4.5 us are the launch and the ends; further tokens
-// come at 0.75 of the copy rate, as calls do that only read the keys: they are 1152 bytes of each 2304.
+// of 33 to 8191 tokens, four rows over 8 heads 40.7. A kernel that only reads the first's 75 MB of keys takes 17.9 us (events
+// around it), every other 1152 bytes, as here, or in one run; only more of them come faster (600 MB at 0.91 of the copy
+// rate, in one run at 0.95). Float32, one row: 21.4.
 #include <algorithm>
 
 #include "cache_weigh.cuh"
@@ -121,7 +122,9 @@ template <typename T, int D, int NR, bool FEW> constexpr int q_bytes() {
 }
 
 // Blocks of an SM. (Eight bf16 rows: 64 sequences of 33 to 8191 tokens, 8 cache heads: 47.1 us with two, 41.1 with
-// three, 47.6 with four; 2 x 16 heads of 32768: 21.2, 23.0 and 27.6. Float rows lose from three on.)
+// three, 47.6 with four; 2 x 16 heads of 32768: 21.2, 23.0 and 27.6. Float rows lose from three on.) Three leave 80 registers, and
+// d = 128 spills 32 bytes for one and two rows, 64 for up to eight: 0.4 % of the executed instructions with the
+// first shape, 0.7 % with the second, read back from L1.
 template <typename T, int NR> constexpr int weigh_blocks() { return NR == 1 && sizeof(T) == 2 ? 3 : 2; }
 
 // Scores on m16n8k16 steps (halves in, fp32 out), tokens on the 16 side and 8 NR query rows on the 8 side.
@@ -504,9 +507,9 @@ static cudaError_t weigh_t(const CacheArgs& a, const WeighArgs& w, unsigned flag
     // 18.2 and 11.6 here, 33 rows 7.8, 22.8 and 18.7 there (two passes here, 64 rows: 10.1, 33.9 and 20.3).
     constexpr int kMost = D == 64 ? 32 : sizeof(T) == 4 ? 8 : 16;
     if (rows > kMost) return launch_cache_weigh_tile(a, w, D, sizeof(T) == 4 ? 0 : 1, Q, cache, st);
-    // (2 x 16 heads of 32768 tokens, one row each, with loads into registers: 24.7 us, and 26.1 in the form for eight rows; float32
-    // 29.1 and 32.2. Four rows in two tiles of two were 33, as each further step of the tensor cores takes its 17 clocks; with copies
-    // 23.6 against 22.8, and 64 sequences of 33 to 8191 tokens 56.6 against 40.3.)
+    // (2 x 16 heads of 32768 tokens, one row each: 19.7 us, and 21.4 in the form for eight rows; float32 21.4 and 23.2; d = 64 15.3 and
+    // 15.9, 17.2 and 17.7. Four rows in two tiles of two: 23.6 against 22.8, and 64 sequences of 33 to 8191 tokens 56.6 against
+    // 40.3, as each further step of the tensor cores takes its 17 clocks.)
     if (rows <= 2) return mma_t<T, D, 1, true>(a, w, Q, cache, st);
     if constexpr (kMost > 8) {
         if (rows > 16) return mma_t<T, D, kMost == 32 && sizeof(T) == 2 ? 4 : 2>(a, w, Q, cache, st);  // (float: two tiles of 16)

@@ -347,8 +347,8 @@ mita_status mita_cache_attention(const mita_cache_params* p, const void* Q, cons
  * as they were. acc_out may be acc; no other overlap of acc_out with anything is taken. decay is finite, >= 0; with 0 acc is not read and may be NULL. The sum
  * of an own token starts at 0 whatever its place held before, so sums need no initial value.
  * A sequence with count[b] = 0 has its sums decayed. The same call gives the same bits.
- * Scores, weights and sums are fp32; float32 rows enter as two halves (22 bits), bf16
- * rows exactly, each down to 2^-29 of the row's largest entry. With MITA_FLAG_SIMT fp32 throughout, on CUDA cores. The workspace is that of
+ * Scores, weights and sums are fp32; bf16 rows enter exactly, float32 rows as two halves (22 bits), but for
+ * entries far below the row's largest, which are off by at most 2^-29 of it. With MITA_FLAG_SIMT fp32 throughout, on CUDA cores. The workspace is that of
  * mita_cache_workspace_size(). */
 mita_status mita_cache_weights(const mita_cache_params* p, const void* Q, const void* cache, const int32_t* table,
                                const int32_t* len, const int32_t* count, const int32_t* exps, const float* lse,
