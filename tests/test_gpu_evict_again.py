@@ -208,3 +208,33 @@ def test_decoding_loop_keeps_the_newest():
                 born[b][h] = born[b][h][want]
                 assert np.isin(np.arange(newest[b] - recent, newest[b]), born[b][h]).all()
             n[b] = min(n[b], budget)
+
+
+@pytest.mark.parametrize("odd_acc,odd_age", [(False, True), (True, False), (True, True)])
+def test_ages_aligned_to_their_elements(odd_acc, odd_age):
+    """Sums or ages that are aligned to their elements only give what aligned ones give, on another stream too."""
+    import torch
+    import compressed_attention_adaptive_gb300 as mita
+    lens, keep, shape = [4997, 300], [1234, 200], (2, 2, 5008)
+    pool = Pool(lens, 2, 64, 16, "bf16", seed=3)
+    cap = pool.cols * 16
+    assert cap == shape[2]
+    rng = np.random.default_rng(6)
+    sums, start = _sums(rng, shape, "any"), rng.integers(-300, 300, shape).astype(np.int32)
+    for b, n in enumerate(lens):
+        start[b, :, n:] = 0
+
+    def run(odd_acc, odd_age, stream):
+        place = lambda x, odd: torch.cat([torch.zeros(int(odd), dtype=x.dtype), x.flatten()]).cuda()[int(odd):].view(x.shape)
+        acc, age = place(torch.from_numpy(sums), odd_acc), place(torch.from_numpy(start), odd_age)
+        out, src, new = torch.zeros_like(acc), torch.zeros(shape, dtype=torch.int32, device="cuda"), torch.zeros_like(pool.len_t)
+        ws, cache = mita.cache_evict_workspace(pool.p), pool.cache.clone()
+        kp = torch.tensor(keep, dtype=torch.int32).cuda()
+        torch.cuda.synchronize()
+        mita.mita_cache_evict(pool.p, cache, pool.table, pool.len_t, kp, acc, ws, first=1, recent=64, len_out=new, acc_out=out,
+                              src_out=src, age=age, stream=stream)
+        mita.mita_device_status(ws, stream)
+        return out, src, new, cache, age
+
+    for a, b in zip(run(False, False, None), run(odd_acc, odd_age, torch.cuda.Stream())):
+        assert torch.equal(a, b)
